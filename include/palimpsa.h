@@ -556,6 +556,150 @@ palimpsa_status palimpsa_backward_varlen(
     const int* cu_seqlens, int N, int H, int total_T, int max_seqlen,
     int d_k, int d_v, palimpsa_dtype in_dtype, void* cuda_stream);
 
+/*
+ * State-space operators. The pages build their blocks on state-space backbones
+ * (slide 10: Palimpsa-M on a Mamba2-style block; slides 18-19: 8 of 64 such
+ * layers replaced by Palimpsa): a short causal convolution in front of the mixer,
+ * and, in the layers that stay, a selective scan. The two operators below serve
+ * those layers: a prompt, a packed batch, one token, and training. Unlike the
+ * recurrence above they are laid out token by token:
+ *
+ *   rows      one row of D channels per token; D a multiple of 8. Dense: B
+ *             sequences of T rows each. Packed (cu_seqlens not NULL): B sequences
+ *             among T rows in all, sequence n = rows [cu_seqlens[n],
+ *             cu_seqlens[n+1]), with the rules of palimpsa_forward_varlen for
+ *             cu_seqlens (int32, in DEVICE memory, checked there; a sequence that
+ *             breaks them is skipped and latches PALIMPSA_ERR_DOMAIN) and
+ *             max_seqlen (ignored when dense). Output rows outside every sequence
+ *             are not written.
+ *   strides   input rows may lie further apart than their width (a slice of a
+ *             wider projection): the stride is in elements, 0 means dense, at
+ *             least the width otherwise, and a multiple of 16 bytes
+ *             (PALIMPSA_ERR_ALIGN). Outputs are dense.
+ *   types     token arrays (x, dt, B, C, z, y, their gradients, the convolution's
+ *             state) are in in_dtype; parameters, their gradients and the scan's
+ *             state are fp32. Sums and states are fp32; outputs in in_dtype are
+ *             rounded once.
+ *   alignment 16 bytes, except weight, bias, skip, dt_bias, their gradients, dA and
+ *             cu_seqlens (4 bytes).
+ * T = 0, and empty sequences, pass the state (and its gradient) through; with
+ * T = 0 the token arrays may be NULL. Overlap between inputs and outputs is
+ * undefined, except that a final state may be the initial one. Results do not
+ * depend on timing: no atomics, the same bits every time.
+ */
+
+/* Options of the convolution. SILU: y = u sigmoid(u); without it y = u. */
+typedef enum { PALIMPSA_CONV_SILU = 1 } palimpsa_conv_flags;
+
+/*
+ * palimpsa_causal_conv - depthwise causal convolution of W taps (2, 3 or 4) along
+ * the tokens:  u_t = bias + sum_j weight[:, j] x_{t-(W-1)+j},  y_t = silu(u_t).
+ *   x        rows [D], stride x_stride
+ *   weight   [D, W]; bias [D] or NULL (0)
+ *   state0   [B, W-1, D] in_dtype: the W-1 inputs before each sequence, oldest
+ *            first, or NULL for zeros
+ *   y        rows [D]
+ *   state_T  [B, W-1, D] in_dtype: the last W-1 of (state0, x), or NULL when not
+ *            wanted; may be state0
+ */
+palimpsa_status palimpsa_causal_conv(
+    const void* x, long long x_stride, const float* weight, const float* bias,
+    const void* state0, void* y, void* state_T,
+    const int* cu_seqlens, int B, int T, int max_seqlen, int D, int W,
+    unsigned int flags, palimpsa_dtype in_dtype, void* cuda_stream);
+
+/* palimpsa_causal_conv_step - one token: x, y rows of B sequences, state
+ * [B, W-1, D] updated in place (the oldest input leaves, x enters). */
+palimpsa_status palimpsa_causal_conv_step(
+    const void* x, long long x_stride, const float* weight, const float* bias,
+    void* state, void* y, int B, int D, int W,
+    unsigned int flags, palimpsa_dtype in_dtype, void* cuda_stream);
+
+/*
+ * palimpsa_causal_conv_backward - gradients through palimpsa_causal_conv from dy
+ * (rows [D], stride dy_stride) and dstate_T ([B, W-1, D] or NULL):
+ *   dx rows [D]; dweight [D, W]; dbias [D] or NULL; dstate0 [B, W-1, D] or NULL.
+ * The pre-activations are recomputed. Scratch for the parameters' partial sums
+ * comes from the library's pool.
+ */
+palimpsa_status palimpsa_causal_conv_backward(
+    const void* x, long long x_stride, const float* weight, const float* bias,
+    const void* state0, const void* dy, long long dy_stride, const void* dstate_T,
+    void* dx, float* dweight, float* dbias, void* dstate0,
+    const int* cu_seqlens, int B, int T, int max_seqlen, int D, int W,
+    unsigned int flags, palimpsa_dtype in_dtype, void* cuda_stream);
+
+/* Options of the scan. SOFTPLUS: step sizes softplus(dt + dt_bias); without it
+ * dt + dt_bias, which must then be >= 0. */
+typedef enum { PALIMPSA_SCAN_SOFTPLUS = 1 } palimpsa_scan_flags;
+
+/* Row strides of the scan's inputs, in elements (0: dense). */
+typedef struct {
+  long long x, dt, B, C, z, dy;
+} palimpsa_scan_strides;
+
+/*
+ * palimpsa_selective_scan - a linear recurrence with a decay per channel and
+ * state, step sizes and reads that depend on the token. Per channel d, in group
+ * g = d / (D / G), and state n:
+ *
+ *   s_t = softplus(dt_t + dt_bias)                           (step size)
+ *   h_t = exp(-A[d,n] s_t) h_{t-1} + s_t x_t B_t[g,n]
+ *   y_t = (sum_n C_t[g,n] h_t + skip x_t) silu(z_t)
+ *
+ * A > 0, as for the recurrence above (alpha = exp(-A d_t)): a layer that stores
+ * log A passes exp of it.
+ *   x, dt, z  rows [D] (z NULL: no gate); B_t, C_t rows [G, N]
+ *   A         [D, N] > 0; skip, dt_bias [D] or NULL (0)
+ *   h0        [B, D, N] or NULL (0); h_T [B, D, N], may be h0
+ *   y         rows [D]
+ *   ckpt      NULL, or palimpsa_selective_scan_checkpoint_bytes() bytes that
+ *             receive the state of every sequence before its tokens 0, 16, 32, ...,
+ *             [D, N] each, for the backward (packed: sequence n, from row s0, in
+ *             slots s0 / 16 + n, ...; slots that no sequence owns are not written)
+ *   strides   or NULL when every input is dense
+ *   N in {8, 16, 32, 64, 128}; D / G a multiple of 8.
+ * Where the sequences and channels are few, time is cut into segments (summaries,
+ * carry, scan, as in palimpsa_forward_chunked) with scratch from the library's
+ * pool; results then differ by fp32 rounding. A not positive, or a step size that
+ * is negative or not finite, latches PALIMPSA_ERR_DOMAIN.
+ */
+size_t palimpsa_selective_scan_checkpoint_bytes(int B, int T, int packed, int D, int N);
+
+palimpsa_status palimpsa_selective_scan(
+    const void* x, const void* dt, const float* A, const void* B_t, const void* C_t,
+    const float* skip, const void* z, const float* dt_bias, const float* h0,
+    void* y, float* h_T, float* ckpt, const palimpsa_scan_strides* strides,
+    const int* cu_seqlens, int B, int T, int max_seqlen, int D, int G, int N,
+    unsigned int flags, palimpsa_dtype in_dtype, void* cuda_stream);
+
+/* palimpsa_selective_scan_step - one token of B sequences; h [B, D, N] is updated
+ * in place. */
+palimpsa_status palimpsa_selective_scan_step(
+    const void* x, const void* dt, const float* A, const void* B_t, const void* C_t,
+    const float* skip, const void* z, const float* dt_bias, float* h, void* y,
+    const palimpsa_scan_strides* strides, int B, int D, int G, int N,
+    unsigned int flags, palimpsa_dtype in_dtype, void* cuda_stream);
+
+/*
+ * palimpsa_selective_scan_backward - gradients through palimpsa_selective_scan from
+ * dy (rows [D]) and dh_T ([B, D, N] or NULL), with the ckpt of a forward call on
+ * the same inputs (h0 is in it).
+ *   dx, ddt, dz rows [D] (dz required with z; ddt is the gradient of the raw dt);
+ *   dB, dC rows [G, N], summed over the group's channels; dA [D, N]; dskip,
+ *   ddt_bias [D] or NULL; dh0 [B, D, N] or NULL.
+ * Scratch from the library's pool: about 8 N bytes per row and 32 channels, and
+ * 4 N bytes per channel and segment.
+ */
+palimpsa_status palimpsa_selective_scan_backward(
+    const void* x, const void* dt, const float* A, const void* B_t, const void* C_t,
+    const float* skip, const void* z, const float* dt_bias, const float* ckpt,
+    const void* dy, const float* dh_T,
+    void* dx, void* ddt, float* dA, void* dB, void* dC, float* dskip, void* dz,
+    float* ddt_bias, float* dh0, const palimpsa_scan_strides* strides,
+    const int* cu_seqlens, int B, int T, int max_seqlen, int D, int G, int N,
+    unsigned int flags, palimpsa_dtype in_dtype, void* cuda_stream);
+
 /* Static English text for a status code (never NULL). */
 const char* palimpsa_status_string(palimpsa_status s);
 

@@ -47,3 +47,15 @@ from .binding import (  # noqa: F401
     palimpsa_step,
     palimpsa_step_fused,
 )
+from .ssm import (  # noqa: F401
+    PALIMPSA_CONV_SILU,
+    PALIMPSA_SCAN_SOFTPLUS,
+    palimpsa_causal_conv,
+    palimpsa_causal_conv_backward,
+    palimpsa_causal_conv_step,
+    palimpsa_selective_scan,
+    palimpsa_selective_scan_backward,
+    palimpsa_selective_scan_checkpoint_shape,
+    palimpsa_selective_scan_checkpointed,
+    palimpsa_selective_scan_step,
+)

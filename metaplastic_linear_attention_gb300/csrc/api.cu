@@ -210,6 +210,16 @@ palimpsa_status step_sequence_impl(const void* q, const void* k, const void* v, 
   return PALIMPSA_OK;
 }
 
+}  // namespace
+
+palimpsa_status device_status_word(unsigned int** out) { return status_word(out); }
+cudaError_t acquire_scratch(size_t bytes, cudaStream_t s, float** p) {
+  StreamOrderedScratch scratch;
+  return scratch.acquire(bytes, s, p);
+}
+
+namespace {
+
 constexpr unsigned int kKnownFuseFlags = PALIMPSA_FUSE_QK_NORM | PALIMPSA_FUSE_V_STAR;
 
 Prologue fused_prologue(const float* b_scale, unsigned int flags) {

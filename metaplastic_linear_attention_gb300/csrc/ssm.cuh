@@ -1,0 +1,216 @@
+// Internal declarations of the state-space operators: the short causal
+// convolution (conv.cu) and the selective scan (scan_fwd.cu, scan_bwd.cu,
+// scan_step.cu). Their C ABI is ssm_api.cu.
+//
+// Layouts are token-major: a row of D channels per token, rows of one sequence
+// following each other with a stride (`ld`, elements) that may exceed D, so
+// that a slice of a wider projection goes in without a copy. A dense batch is
+// n_seq sequences of T rows; a packed batch is n_seq sequences of rows
+// [cu[n], cu[n+1]) among T rows in all.
+#pragma once
+
+#include "palimpsa_internal.cuh"
+
+namespace palimpsa {
+
+// Rows of sequence n: first row and length. Shared by both operators.
+struct SeqRows {
+  const int* cu = nullptr;  // null: dense
+  int n_seq = 0;
+  int T = 0;        // rows per sequence (dense) or in all (packed)
+  int max_len = 0;  // longest sequence (= T when dense)
+};
+
+struct ConvArgs {
+  const void* x;
+  const float* weight;  // [D, W]
+  const float* bias;    // [D] or null
+  const void* state0;   // [n_seq, W - 1, D] or null
+  void* y;              // forward and step
+  void* state_T;        // may be null; may be state0
+  // backward
+  const void* dy = nullptr;
+  const void* dstate_T = nullptr;
+  void* dx = nullptr;
+  void* dstate0 = nullptr;
+  float* dweight = nullptr;
+  float* dbias = nullptr;
+  long long x_ld, dy_ld = 0;
+  SeqRows rows;
+  int D, W;
+  bool silu, bf16;
+  unsigned int* status;
+};
+cudaError_t launch_conv_forward(const ConvArgs& a, cudaStream_t s);
+cudaError_t launch_conv_step(const ConvArgs& a, cudaStream_t s);
+size_t conv_backward_scratch_bytes(const ConvArgs& a);
+cudaError_t launch_conv_backward(const ConvArgs& a, float* scratch, cudaStream_t s);
+
+struct ScanArgs {
+  const void* x;
+  const void* dt;
+  const float* A;        // [D, N]
+  const void* B;         // rows of [G, N]
+  const void* C;
+  const float* skip;     // [D] or null
+  const void* z;         // or null
+  const float* dt_bias;  // [D] or null
+  const float* h0;       // [n_seq, D, N] or null
+  void* y;
+  float* h_T;            // [n_seq, D, N]; the step's state, in place
+  float* ckpt = nullptr;
+  long long x_ld, dt_ld, B_ld, C_ld, z_ld;
+  SeqRows rows;
+  int D, G, N;
+  bool softplus, bf16;
+  unsigned int* status;
+  // time split (set by the launcher)
+  int nseg = 1, seg_len = 0;
+  float* seg_state = nullptr;  // [n_seq, nseg, D, N]: summaries, then start states
+  float* seg_dt = nullptr;     // [n_seq, nseg, D]: sums of the step sizes
+  // backward
+  const float* ckpt_in = nullptr;
+  const void* dy = nullptr;
+  const float* dh_T = nullptr;
+  void* dx = nullptr;
+  void* ddt = nullptr;
+  void* dz = nullptr;
+  void* dB = nullptr;
+  void* dC = nullptr;
+  float* dA = nullptr;
+  float* dskip = nullptr;
+  float* ddt_bias = nullptr;
+  float* dh0 = nullptr;
+  long long dy_ld = 0;
+};
+
+constexpr int kScanChannels = 32;      // channels of a scan tile
+constexpr int kScanCheckpoint = 16;    // tokens between training checkpoints
+
+// Checkpoint rows of a batch, each [D, N]: sequence n's checkpoint c (the state
+// before its token 16 c) is row scan_ckpt_row0(n) + c. A packed batch keeps
+// T / 16 + n_seq rows, sequence n (from row s0) starting at s0 / 16 + n: the next
+// sequence starts at least ceil(len / 16) rows later, so none are shared.
+__host__ __device__ inline long long scan_ckpt_rows(const SeqRows& r) {
+  if (r.cu) return (long long)r.T / kScanCheckpoint + r.n_seq;
+  return (long long)r.n_seq * ((r.T + kScanCheckpoint - 1) / kScanCheckpoint);
+}
+__host__ __device__ inline long long scan_ckpt_row0(const SeqRows& r, long long n, long long s0) {
+  if (r.cu) return s0 / kScanCheckpoint + n;
+  return n * ((r.T + kScanCheckpoint - 1) / kScanCheckpoint);
+}
+inline long long scan_tiles(const ScanArgs& a) {
+  const int dg = a.D / a.G;
+  return (long long)a.G * ((dg + kScanChannels - 1) / kScanChannels);
+}
+
+// Time split of a scan or of its backward: segments per sequence and their
+// length (a multiple of kScanCheckpoint). Scratch of scan_scratch_floats() holds it.
+cudaError_t plan_scan(const ScanArgs& a, bool backward, int* nseg, int* seg_len);
+inline size_t scan_scratch_floats(const ScanArgs& a, int nseg) {
+  return nseg > 1 ? (size_t)a.rows.n_seq * nseg * a.D * (a.N + 1) : 0;
+}
+cudaError_t launch_scan_forward(const ScanArgs& a, cudaStream_t s);
+cudaError_t launch_scan_step(const ScanArgs& a, cudaStream_t s);
+// Backward: scratch of scan_backward_scratch_floats() holds the per-tile sums of
+// dB and dC and the per-segment sums of the parameters' gradients.
+size_t scan_backward_scratch_floats(const ScanArgs& a);
+cudaError_t launch_scan_backward(const ScanArgs& a, float* scratch, cudaStream_t s);
+// Pass A of the backward's time split: each segment's gradient with respect to the
+// state before it, from a zero gradient after it, and its sum of step sizes.
+cudaError_t launch_scan_reverse_summary(const ScanArgs& a, cudaStream_t s);
+// The carry over segment summaries of a scan: seg_state becomes each segment's
+// start state. Forward: from h0, in segment order. Reverse: from dh_T, from the
+// last segment back.
+cudaError_t launch_scan_carry(const ScanArgs& a, bool reverse, cudaStream_t s);
+
+#if defined(__CUDACC__)
+
+// First row and length of sequence n; false (and nothing may be touched) when
+// packed offsets are out of order, out of range or longer than max_len.
+__device__ __forceinline__ bool seq_rows(const SeqRows& r, long long n, long long* row0, int* len) {
+  if (!r.cu) {
+    *row0 = n * r.T;
+    *len = r.T;
+    return true;
+  }
+  const int s0 = r.cu[n], s1 = r.cu[n + 1];
+  const bool ok = s0 >= 0 && s1 >= s0 && s1 <= r.T && s1 - s0 <= r.max_len;
+  *row0 = ok ? s0 : 0;
+  *len = ok ? s1 - s0 : 0;
+  return ok;
+}
+
+// A 16-byte vector of the input type as fp32 values: 8 bf16 or 4 fp32.
+template <bool BF16>
+struct Vec {
+  static constexpr int n = BF16 ? 8 : 4;
+  static constexpr int bytes = BF16 ? 2 : 4;  // of one value
+  static __device__ __forceinline__ void unpack(const uint4& u, float* f) {
+    if constexpr (BF16) {
+      f[0] = bf16_lo(u.x); f[1] = bf16_hi(u.x); f[2] = bf16_lo(u.y); f[3] = bf16_hi(u.y);
+      f[4] = bf16_lo(u.z); f[5] = bf16_hi(u.z); f[6] = bf16_lo(u.w); f[7] = bf16_hi(u.w);
+    } else {
+      f[0] = __uint_as_float(u.x); f[1] = __uint_as_float(u.y);
+      f[2] = __uint_as_float(u.z); f[3] = __uint_as_float(u.w);
+    }
+  }
+  // Rounds to the input type (to nearest even), once, at the store.
+  static __device__ __forceinline__ uint4 pack(const float* f) {
+    uint4 u;
+    if constexpr (BF16) {
+      u.x = two(f[0], f[1]); u.y = two(f[2], f[3]); u.z = two(f[4], f[5]); u.w = two(f[6], f[7]);
+    } else {
+      u.x = __float_as_uint(f[0]); u.y = __float_as_uint(f[1]);
+      u.z = __float_as_uint(f[2]); u.w = __float_as_uint(f[3]);
+    }
+    return u;
+  }
+  static __device__ __forceinline__ uint32_t two(float lo, float hi) {
+    const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&p);
+  }
+};
+
+__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int PENDING>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory");
+}
+
+__device__ __forceinline__ float ex2_approx(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+constexpr float kLog2e = 1.4426950408889634f;
+
+// u sigmoid(u), and sigmoid(u), with the fast exponential and division (a few
+// ulp). e^-u overflows to infinity for very negative u, where the quotient is 0.
+__device__ __forceinline__ float sigmoid_fast(float u) { return __fdividef(1.f, 1.f + __expf(-u)); }
+__device__ __forceinline__ float silu_fast(float u) { return __fdividef(u, 1.f + __expf(-u)); }
+
+// softplus(u) = max(u, 0) + log(1 + e), e = e^-|u|. The step sizes of a trained scan
+// are small (0.001 to 0.1, u from -7 to -2), where log(1 + e) has to be accurate
+// relative to itself, which the SFU's logarithm near 1 is not. So
+// log(1 + e) = 2 atanh(r), r = e / (2 + e) <= 1/3, by the series of atanh in r^2 up to
+// r^13: what is left out is below 2e-8 of the sum (r^14 / 15 and on at r = 1/3).
+__device__ __forceinline__ float softplus_fast(float u) {
+  const float e = __expf(-fabsf(u));
+  const float r = __fdividef(e, 2.f + e), q = r * r;
+  float p = 1.f / 13.f;
+  p = fmaf(p, q, 1.f / 11.f);
+  p = fmaf(p, q, 1.f / 9.f);
+  p = fmaf(p, q, 1.f / 7.f);
+  p = fmaf(p, q, 1.f / 5.f);
+  p = fmaf(p, q, 1.f / 3.f);
+  p = fmaf(p, q, 1.f);
+  return fmaf(2.f * r, p, fmaxf(u, 0.f));
+}
+
+#endif  // __CUDACC__
+
+}  // namespace palimpsa
