@@ -5,11 +5,13 @@
 // the last W - 1 inputs before its first token, oldest first, in the input
 // type (they are copies of inputs, so a prompt cut in two gives the same bits).
 //
-// A value is read once and written once, against 2 W + 6 operations: the
-// kernels are bound by HBM. A thread owns one 16-byte vector of channels (8 bf16
-// or 4 fp32) and a short run of tokens, with the W - 1 rows before it read again
-// (they hit in L1/L2: the neighbouring run reads them at the same time). All its
-// loads are issued before any arithmetic. Sums are fp32; y is rounded once.
+// A value is read once and written once, against 2 W + 6 operations: the kernels
+// are bound by HBM. A thread owns 4 channels (8 bytes of bf16, 16 of fp32) and a
+// run of tokens, which it walks in batches of 8 with the next batch's loads in
+// flight; the W - 1 rows before a run are read again (they hit in L1/L2: the
+// neighbouring run reads them at the same time). Long runs also spread the loads of
+// the taps, which are far apart in memory for neighbouring threads. Sums are fp32;
+// y is rounded once.
 #include <algorithm>
 
 #include "ssm.cuh"
@@ -17,39 +19,61 @@
 namespace palimpsa {
 namespace {
 
-constexpr int kRun = 8;        // tokens of a thread, forward
-constexpr int kThreads = 256;
+constexpr int kBatch = 8;      // tokens loaded together
+constexpr int kThreads = 128;
+constexpr int kMaxRun = 64, kMinRun = 16;
+constexpr int kCtas = 5;
 
-// Parameters of a thread's channels.
-template <int VN, int W>
-__device__ __forceinline__ void load_taps(const ConvArgs& a, int ch, float (*w)[W], float* b) {
+// Parameters of a thread's 4 channels, as pairs: 4 W neighbouring floats, by 16-byte
+// loads where the array allows it (it only has to be aligned to 4 bytes).
+template <int W>
+__device__ __forceinline__ void load_taps(const ConvArgs& a, int ch, float2 (*w)[2], float2* b) {
+  const float* const k = a.weight + (size_t)ch * W;
+  float f[4 * W];
+  if ((reinterpret_cast<uintptr_t>(a.weight) & 15) == 0) {
 #pragma unroll
-  for (int i = 0; i < VN; ++i) {
+    for (int j = 0; j < W; ++j) {
+      const float4 v = reinterpret_cast<const float4*>(k)[j];
+      f[4 * j] = v.x; f[4 * j + 1] = v.y; f[4 * j + 2] = v.z; f[4 * j + 3] = v.w;
+    }
+  } else {
 #pragma unroll
-    for (int j = 0; j < W; ++j) w[i][j] = a.weight[(size_t)(ch + i) * W + j];
-    b[i] = a.bias ? a.bias[ch + i] : 0.f;
+    for (int j = 0; j < 4 * W; ++j) f[j] = k[j];
+  }
+#pragma unroll
+  for (int p = 0; p < 2; ++p) {
+#pragma unroll
+    for (int j = 0; j < W; ++j) w[j][p] = make_float2(f[2 * p * W + j], f[(2 * p + 1) * W + j]);
+    b[p] = a.bias ? make_float2(a.bias[ch + 2 * p], a.bias[ch + 2 * p + 1]) : make_float2(0.f, 0.f);
   }
 }
 
-// Input row p of a sequence (p may be negative: the state) as a raw vector.
+template <bool BF16>
+__device__ __forceinline__ typename Quad<BF16>::Raw load_quad(const void* p, long long i) {
+  return *reinterpret_cast<const typename Quad<BF16>::Raw*>(static_cast<const char*>(p) + i * Vec<BF16>::bytes);
+}
+template <bool BF16>
+__device__ __forceinline__ void store_quad(void* p, long long i, const typename Quad<BF16>::Raw& v) {
+  *reinterpret_cast<typename Quad<BF16>::Raw*>(static_cast<char*>(p) + i * Vec<BF16>::bytes) = v;
+}
+
+// Input row p of a sequence (p may be negative: the state).
 template <bool BF16, int W>
-__device__ __forceinline__ uint4 input_row(const ConvArgs& a, long long n, long long row0, int p, int ch) {
-  constexpr int ES = Vec<BF16>::bytes;
-  if (p >= 0)
-    return *reinterpret_cast<const uint4*>(static_cast<const char*>(a.x) + ((row0 + p) * a.x_ld + ch) * ES);
-  if (!a.state0) return make_uint4(0, 0, 0, 0);
-  return *reinterpret_cast<const uint4*>(static_cast<const char*>(a.state0) +
-                                         ((n * (W - 1) + (W - 1 + p)) * a.D + ch) * (long long)ES);
+__device__ __forceinline__ typename Quad<BF16>::Raw input_row(const ConvArgs& a, long long n, long long row0, int p,
+                                                              int ch) {
+  if (p >= 0) return load_quad<BF16>(a.x, (row0 + p) * a.x_ld + ch);
+  if (!a.state0) return Quad<BF16>::zero();
+  return load_quad<BF16>(a.state0, (n * (W - 1) + (W - 1 + p)) * a.D + ch);
 }
 
 template <bool BF16, int W>
-__global__ void __launch_bounds__(kThreads) palimpsa_conv_kernel(ConvArgs a, int runs) {
-  using V = Vec<BF16>;
-  constexpr int VN = V::n, ES = V::bytes;
-  const int nvec = a.D / VN;
+__global__ void __launch_bounds__(kThreads, kCtas) palimpsa_conv_kernel(ConvArgs a, int runs, int run_len) {
+  using Q = Quad<BF16>;
+  using Raw = typename Q::Raw;
+  const int nvec = a.D / 4;
   const long long i = (long long)blockIdx.x * kThreads + threadIdx.x;
   if (i >= (long long)nvec * runs * a.rows.n_seq) return;
-  const int ch = (int)(i % nvec) * VN;
+  const int ch = (int)(i % nvec) * 4;
   const long long r = i / nvec;
   const int run = (int)(r % runs);
   const long long n = r / runs;
@@ -59,77 +83,105 @@ __global__ void __launch_bounds__(kThreads) palimpsa_conv_kernel(ConvArgs a, int
     if (run == 0 && ch == 0) latch_status(a.status, kStatusDomain);
     return;
   }
-  const int t0 = run * kRun, nt = min(kRun, len - t0);
-  if (nt <= 0 && run > 0) return;
-  uint4 raw[kRun + W - 1];
+  const int t0 = run * run_len, t1 = min(len, t0 + run_len);
+  if (t0 >= t1 && run > 0) return;
+  Raw next[kBatch];
+  const long long ld = a.x_ld * Vec<BF16>::bytes;
+  const char* px = static_cast<const char*>(a.x) + (row0 + t0) * ld + ch * Vec<BF16>::bytes;
+  auto fetch = [&](int t) {
+    if (t + kBatch <= t1) {
 #pragma unroll
-  for (int k = 0; k < kRun + W - 1; ++k)
-    if (k < nt + W - 1) raw[k] = input_row<BF16, W>(a, n, row0, t0 - (W - 1) + k, ch);
-  // The state after the sequence: the last W - 1 of (state0, inputs). The
-  // thread that holds the first run reads what it needs before it writes, so
-  // state_T may be state0.
+      for (int k = 0; k < kBatch; ++k) next[k] = *reinterpret_cast<const Raw*>(px + k * ld);
+    } else {
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k)
+        if (t + k < t1) next[k] = *reinterpret_cast<const Raw*>(px + k * ld);
+    }
+    px += kBatch * ld;
+  };
+  float2 win[W - 1][2];  // the W - 1 inputs before the next token
+  {
+    Raw old[W - 1];
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) old[j] = input_row<BF16, W>(a, n, row0, t0 - (W - 1) + j, ch);
+    fetch(t0);
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) Q::unpack(old[j], win[j]);
+  }
+  // The state after the sequence: the last W - 1 of (state0, inputs). The thread that
+  // holds the first run has read the state before it writes, so state_T may be state0.
   if (run == 0 && a.state_T) {
-    uint4 last[W - 1];
+    Raw last[W - 1];
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) last[j] = input_row<BF16, W>(a, n, row0, len - (W - 1) + j, ch);
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j)
-      *reinterpret_cast<uint4*>(static_cast<char*>(a.state_T) + ((n * (W - 1) + j) * a.D + ch) * (long long)ES) =
-          last[j];
+    for (int j = 0; j < W - 1; ++j) store_quad<BF16>(a.state_T, (n * (W - 1) + j) * a.D + ch, last[j]);
   }
-  if (nt <= 0) return;
-  float w[VN][W], b[VN];
-  load_taps<VN, W>(a, ch, w, b);
-  float win[W][VN];
+  float2 w[W][2], b[2];
+  load_taps<W>(a, ch, w, b);
+  const long long yd = (long long)a.D * Vec<BF16>::bytes;
+  char* py = static_cast<char*>(a.y) + (row0 + t0) * yd + ch * Vec<BF16>::bytes;
+  for (int t = t0; t < t1; t += kBatch) {
+    Raw cur[kBatch];
 #pragma unroll
-  for (int k = 0; k < W - 1; ++k) V::unpack(raw[k], win[k]);
+    for (int k = 0; k < kBatch; ++k) cur[k] = next[k];
+    fetch(t + kBatch);
+    auto token = [&](int k) {
+      float2 x[2], out[2];
+      Q::unpack(cur[k], x);
 #pragma unroll
-  for (int t = 0; t < kRun; ++t) {
-    if (t >= nt) break;
-    V::unpack(raw[t + W - 1], win[(t + W - 1) % W]);
-    float out[VN];
+      for (int p = 0; p < 2; ++p) {
+        float2 u = __ffma2_rn(w[W - 1][p], x[p], b[p]);
 #pragma unroll
-    for (int c = 0; c < VN; ++c) {
-      float u = b[c];
+        for (int j = 0; j < W - 1; ++j) u = __ffma2_rn(w[j][p], win[j][p], u);
+        out[p] = a.silu ? silu_fast(u) : u;
 #pragma unroll
-      for (int j = 0; j < W; ++j) u = fmaf(w[c][j], win[(t + j) % W][c], u);
-      out[c] = a.silu ? silu_fast(u) : u;
+        for (int j = 0; j < W - 2; ++j) win[j][p] = win[j + 1][p];
+        win[W - 2][p] = x[p];
+      }
+      *reinterpret_cast<Raw*>(py + k * yd) = Q::pack(out);
+    };
+    if (t + kBatch <= t1) {
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) token(k);
+    } else {
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k)
+        if (t + k < t1) token(k);
     }
-    *reinterpret_cast<uint4*>(static_cast<char*>(a.y) + ((row0 + t0 + t) * a.D + ch) * (long long)ES) =
-        V::pack(out);
+    py += kBatch * yd;
   }
 }
 
 // One token: the state's W - 1 rows and the new input give y, and the state
 // moves on by one row.
 template <bool BF16, int W>
-__global__ void __launch_bounds__(128) palimpsa_conv_step_kernel(ConvArgs a) {
-  using V = Vec<BF16>;
-  constexpr int VN = V::n, ES = V::bytes;
-  const int nvec = a.D / VN;
-  const long long i = (long long)blockIdx.x * 128 + threadIdx.x;
+__global__ void __launch_bounds__(kThreads) palimpsa_conv_step_kernel(ConvArgs a) {
+  using Q = Quad<BF16>;
+  const int nvec = a.D / 4;
+  const long long i = (long long)blockIdx.x * kThreads + threadIdx.x;
   if (i >= (long long)nvec * a.rows.n_seq) return;
-  const int ch = (int)(i % nvec) * VN;
-  const long long n = i / nvec;
-  char* st = static_cast<char*>(a.state_T) + (n * (W - 1) * a.D + ch) * (long long)ES;
-  uint4 raw[W];
-  raw[W - 1] = *reinterpret_cast<const uint4*>(static_cast<const char*>(a.x) + (n * a.x_ld + ch) * ES);
+  const int ch = (int)(i % nvec) * 4;
+  const long long n = i / nvec, st = n * (W - 1) * a.D + ch;
+  typename Q::Raw raw[W];
+  raw[W - 1] = load_quad<BF16>(a.x, n * a.x_ld + ch);
 #pragma unroll
-  for (int j = 0; j < W - 1; ++j) raw[j] = *reinterpret_cast<const uint4*>(st + (long long)j * a.D * ES);
-  float w[VN][W], u[VN];
-  load_taps<VN, W>(a, ch, w, u);
+  for (int j = 0; j < W - 1; ++j) raw[j] = load_quad<BF16>(a.state_T, st + (long long)j * a.D);
+  float2 w[W][2], u[2];
+  load_taps<W>(a, ch, w, u);
 #pragma unroll
-  for (int j = 0; j < W; ++j) {
-    float v[VN];
-    V::unpack(raw[j], v);
+  for (int k = 0; k < W; ++k) {  // the newest input first, as a prompt sums
+    const int j = (k + W - 1) % W;
+    float2 x[2];
+    Q::unpack(raw[j], x);
 #pragma unroll
-    for (int c = 0; c < VN; ++c) u[c] = fmaf(w[c][j], v[c], u[c]);
+    for (int p = 0; p < 2; ++p) u[p] = __ffma2_rn(w[j][p], x[p], u[p]);
   }
 #pragma unroll
-  for (int j = 0; j < W - 1; ++j) *reinterpret_cast<uint4*>(st + (long long)j * a.D * ES) = raw[j + 1];
+  for (int j = 0; j < W - 1; ++j) store_quad<BF16>(a.state_T, st + (long long)j * a.D, raw[j + 1]);
 #pragma unroll
-  for (int c = 0; c < VN; ++c) u[c] = a.silu ? silu_fast(u[c]) : u[c];
-  *reinterpret_cast<uint4*>(static_cast<char*>(a.y) + (n * a.D + ch) * (long long)ES) = V::pack(u);
+  for (int p = 0; p < 2; ++p) u[p] = a.silu ? silu_fast(u[p]) : u[p];
+  store_quad<BF16>(a.y, n * a.D + ch, Q::pack(u));
 }
 
 // ------------------------------------------------------------------ backward
@@ -137,24 +189,25 @@ __global__ void __launch_bounds__(128) palimpsa_conv_step_kernel(ConvArgs a) {
 //   du_t = dy_t silu'(u_t),  silu'(u) = p (1 + u (1 - p)),  p = sigmoid(u)
 //   dx_t = sum_j w_j du_{t + (W-1) - j}   (+ dstate_T for the last W - 1 inputs)
 //   dw_j = sum_t du_t x_{t - (W-1) + j},  dbias = sum_t du_t.
-// u is recomputed from x. A CTA owns 16 vectors of channels and 16 runs of
-// tokens, one run to a thread; each thread walks its run with the last W inputs
-// and W du's in registers, and looks W - 1 tokens past its end for the dx of its
-// last ones. The parameter sums go over the CTA's runs in shared memory and then,
-// in a fixed order, over CTAs in a second kernel: no atomics, the same bits
-// every time.
-constexpr int kBwdVecs = 16, kBwdRuns = 16;
+// u is recomputed from x. A CTA owns 16 quads of channels and 16 runs of tokens, one
+// run to a thread; each thread walks its run in batches of 3 or 4 tokens, the next
+// batch's loads in flight, with the last W - 1 inputs and du's in registers, and looks
+// W - 1 tokens past its end for the dx of its last ones. The parameter sums go over
+// the CTA's runs in shared memory and then, in a fixed order, over CTAs in a second
+// kernel: no atomics, the same bits every time.
+constexpr int kBwdVecs = 16, kBwdRuns = 16, kBwdCtas = 2;
 
 template <bool BF16, int W>
-__global__ void __launch_bounds__(kBwdVecs* kBwdRuns)
+__global__ void __launch_bounds__(kBwdVecs* kBwdRuns, BF16 || W < 4 ? kBwdCtas : 1)
 palimpsa_conv_bwd_kernel(ConvArgs a, int run_len, int blocks_per_seq, float* partial) {
-  using V = Vec<BF16>;
-  constexpr int VN = V::n, ES = V::bytes;
-  const int nvec = a.D / VN, vtiles = (nvec + kBwdVecs - 1) / kBwdVecs;
+  using Q = Quad<BF16>;
+  using Raw = typename Q::Raw;
+  constexpr int ES = Vec<BF16>::bytes;
+  const int nvec = a.D / 4, vtiles = (nvec + kBwdVecs - 1) / kBwdVecs;
   const int vx = threadIdx.x % kBwdVecs, ry = threadIdx.x / kBwdVecs;
   const long long blk = blockIdx.x / vtiles;  // token block, over all sequences
   const int vec = (int)(blockIdx.x % vtiles) * kBwdVecs + vx;
-  const int ch = vec * VN;
+  const int ch = vec * 4;
   const long long n = blk / blocks_per_seq;
   const int t0 = ((int)(blk % blocks_per_seq) * kBwdRuns + ry) * run_len;
   long long row0;
@@ -163,110 +216,137 @@ palimpsa_conv_bwd_kernel(ConvArgs a, int run_len, int blocks_per_seq, float* par
   if (!ok && threadIdx.x == 0) latch_status(a.status, kStatusDomain);
   const bool live = ok && vec < nvec;
   const int t1 = min(len, t0 + run_len);  // this run's tokens are [t0, t1)
+  const float2 zero = make_float2(0.f, 0.f);
 
-  float gw[VN][W], gb[VN];
+  float2 gw[W][2], gb[2] = {zero, zero};
 #pragma unroll
-  for (int c = 0; c < VN; ++c) {
-    gb[c] = 0.f;
-#pragma unroll
-    for (int j = 0; j < W; ++j) gw[c][j] = 0.f;
-  }
+  for (int j = 0; j < W; ++j) gw[j][0] = gw[j][1] = zero;
   // The run at the sequence's start also owns the gradient of the state rows
   // (places -(W-1) .. -1); with an empty sequence they pass dstate_T through.
   const bool first = t0 == 0;
   if (live && (t0 < t1 || first)) {
-    float w[VN][W], b[VN];
-    load_taps<VN, W>(a, ch, w, b);
-    const char* gdy = static_cast<const char*>(a.dy);
-    float x[W][VN], du[W][VN];  // rings by place modulo W
+    float2 w[W][2], b[2];
+    load_taps<W>(a, ch, w, b);
+    // The inputs and du's of the last W tokens, by place modulo W (a batch is a whole
+    // number of turns, so a token's slot is known at compile time).
+    constexpr int NB = W == 3 ? 3 : 4;
+    float2 x[W][2], du[W][2];
 #pragma unroll
-    for (int j = 0; j < W; ++j)
+    for (int j = 0; j < W; ++j) du[j][0] = du[j][1] = x[j][0] = x[j][1] = zero;
 #pragma unroll
-      for (int c = 0; c < VN; ++c) du[j][c] = 0.f;
+    for (int k = 0; k < W - 1; ++k) Q::unpack(input_row<BF16, W>(a, n, row0, t0 - (W - 1) + k, ch), x[k + 1]);
+    // Token t0 + s brings in its x and dy and finishes the gradient of place t0 + s -
+    // (W-1), all of whose W du's are then known.
+    const int steps = max(t1 - t0, 0) + W - 1, stop = min(len, t0 + steps);
+    const long long xl = a.x_ld * ES, yl = a.dy_ld * ES, dl = (long long)a.D * ES;
+    const char* px = static_cast<const char*>(a.x) + (row0 + t0) * xl + ch * ES;
+    const char* pg = static_cast<const char*>(a.dy) + (row0 + t0) * yl + ch * ES;
+    char* pd = static_cast<char*>(a.dx) + (row0 + t0 - (W - 1)) * dl + ch * ES;  // of the finished place
+    Raw nx[NB], nd[NB];
+    auto fetch = [&](int t) {
+      if (t + NB <= stop) {
 #pragma unroll
-    for (int k = 0; k < W - 1; ++k) V::unpack(input_row<BF16, W>(a, n, row0, t0 - (W - 1) + k, ch), x[k]);
-    // Step s brings in token t0 + s (its x and dy) and finishes the gradient of
-    // place t0 + s - (W-1): all W of its du's are then known.
-    const int steps = (t1 - t0 > 0 ? t1 - t0 : 0) + W - 1;
-    for (int s0 = 0; s0 < steps; s0 += W) {
-      // Both rows of the next W tokens are loaded before any is used.
-      uint4 rx[W], rd[W];
+        for (int k = 0; k < NB; ++k) {
+          nx[k] = *reinterpret_cast<const Raw*>(px + k * xl);
+          nd[k] = *reinterpret_cast<const Raw*>(pg + k * yl);
+        }
+      } else {
 #pragma unroll
-      for (int k = 0; k < W; ++k) {
-        const int t = t0 + s0 + k;
-        const bool in = s0 + k < steps && t < len;
-        rx[k] = in ? input_row<BF16, W>(a, n, row0, t, ch) : make_uint4(0, 0, 0, 0);
-        rd[k] = in ? *reinterpret_cast<const uint4*>(gdy + ((row0 + t) * a.dy_ld + ch) * ES) : make_uint4(0, 0, 0, 0);
+        for (int k = 0; k < NB; ++k) {
+          nx[k] = nd[k] = Q::zero();
+          if (t + k < stop) {
+            nx[k] = *reinterpret_cast<const Raw*>(px + k * xl);
+            nd[k] = *reinterpret_cast<const Raw*>(pg + k * yl);
+          }
+        }
       }
+      px += NB * xl;
+      pg += NB * yl;
+    };
+    fetch(t0);
+    for (int s0 = 0; s0 < steps; s0 += NB) {
+      Raw rx[NB], rd[NB];
 #pragma unroll
-      for (int k = 0; k < W; ++k) {
-        if (s0 + k >= steps) break;
-        const int t = t0 + s0 + k, p = t - (W - 1);
-        const bool own = t < t1;  // later tokens only finish this run's dx
-        float g[VN];
-        V::unpack(rx[k], x[(k + W - 1) % W]);
-        V::unpack(rd[k], g);
+      for (int k = 0; k < NB; ++k) {
+        rx[k] = nx[k];
+        rd[k] = nd[k];
+      }
+      fetch(t0 + s0 + NB);
+      // Takes in token t (its sums too, if it is the run's own) and forms the gradient of
+      // place t - (W-1): w_j du_{t - j}.
+      auto token = [&](int k, bool inside, bool own, float2* d) {
+        float2 g[2];
+        Q::unpack(rd[k], g);
+        Q::unpack(rx[k], x[k % W]);
 #pragma unroll
-        for (int c = 0; c < VN; ++c) {
-          float u = b[c];
+        for (int q = 0; q < 2; ++q) {
+          float2 u = b[q];
 #pragma unroll
-          for (int j = 0; j < W; ++j) u = fmaf(w[c][j], x[(k + j) % W][c], u);
+          for (int j = 0; j < W; ++j) u = __ffma2_rn(w[j][q], x[(k + 1 + j) % W][q], u);
           if (a.silu) {
-            const float q = sigmoid_fast(u);
-            g[c] *= q * fmaf(u, 1.f - q, 1.f);
+            const float2 sg = make_float2(sigmoid_fast(u.x), sigmoid_fast(u.y));
+            const float2 m = __ffma2_rn(make_float2(-sg.x, -sg.y), u, u);  // u (1 - p)
+            g[q] = __fmul2_rn(g[q], __ffma2_rn(sg, m, sg));
           }
-          if (t >= len) g[c] = 0.f;
-          du[k][c] = g[c];
+          if (!inside) g[q] = zero;
+          du[k % W][q] = g[q];
           if (own) {
-            gb[c] += g[c];
+            gb[q] = __fadd2_rn(gb[q], g[q]);
 #pragma unroll
-            for (int j = 0; j < W; ++j) gw[c][j] = fmaf(g[c], x[(k + j) % W][c], gw[c][j]);
+            for (int j = 0; j < W; ++j) gw[j][q] = __ffma2_rn(g[q], x[(k + 1 + j) % W][q], gw[j][q]);
           }
-        }
-        // place p takes w_j du_{p + (W-1) - j} = w_j du_{t - j}
-        if (p < t0 && !first) continue;
-        float d[VN];
+          d[q] = __fmul2_rn(w[0][q], g[q]);
 #pragma unroll
-        for (int c = 0; c < VN; ++c) {
-          d[c] = 0.f;
-#pragma unroll
-          for (int j = 0; j < W; ++j) d[c] = fmaf(w[c][j], du[(k - j + W) % W][c], d[c]);
+          for (int j = 1; j < W; ++j) d[q] = __ffma2_rn(w[j][q], du[(k + W - j) % W][q], d[q]);
         }
-        const int back = p - (len - (W - 1));  // place in state_T, if >= 0
-        if (a.dstate_T && back >= 0) {
-          float e[VN];
-          V::unpack(*reinterpret_cast<const uint4*>(static_cast<const char*>(a.dstate_T) +
-                                                    ((n * (W - 1) + back) * a.D + ch) * (long long)ES), e);
+      };
+      const int t = t0 + s0, p = t - (W - 1);
+      // All four tokens the run's own, and their places inside the run and before the
+      // part of it that dstate_T reaches.
+      if (t + NB <= t1 && p >= t0 && (!a.dstate_T || p + NB <= len - (W - 1))) {
 #pragma unroll
-          for (int c = 0; c < VN; ++c) d[c] += e[c];
+        for (int k = 0; k < NB; ++k) {
+          float2 d[2];
+          token(k, true, true, d);
+          *reinterpret_cast<Raw*>(pd + k * dl) = Q::pack(d);
         }
-        if (p >= 0)
-          *reinterpret_cast<uint4*>(static_cast<char*>(a.dx) + ((row0 + p) * a.D + ch) * (long long)ES) = V::pack(d);
-        else if (a.dstate0)
-          *reinterpret_cast<uint4*>(static_cast<char*>(a.dstate0) +
-                                    ((n * (W - 1) + (W - 1 + p)) * a.D + ch) * (long long)ES) = V::pack(d);
+      } else {
+#pragma unroll
+        for (int k = 0; k < NB; ++k) {
+          if (s0 + k >= steps) continue;
+          float2 d[2];
+          token(k, t + k < len, t + k < t1, d);  // tokens past the run only finish its dx
+          if (p + k < t0 && !first) continue;
+          const int back = p + k - (len - (W - 1));  // place in state_T, if >= 0
+          if (a.dstate_T && back >= 0) {
+            float2 e[2];
+            Q::unpack(load_quad<BF16>(a.dstate_T, (n * (W - 1) + back) * a.D + ch), e);
+            d[0] = __fadd2_rn(d[0], e[0]);
+            d[1] = __fadd2_rn(d[1], e[1]);
+          }
+          if (p + k >= 0) *reinterpret_cast<Raw*>(pd + k * dl) = Q::pack(d);
+          else if (a.dstate0) store_quad<BF16>(a.dstate0, (n * (W - 1) + (W - 1 + p + k)) * a.D + ch, Q::pack(d));
+        }
       }
+      pd += NB * dl;
     }
   }
   // Parameter sums over the CTA's runs, value by value.
-  __shared__ float red[kBwdRuns][kBwdVecs * VN + 1];
+  __shared__ float4 red[kBwdRuns][kBwdVecs];
+#pragma unroll
   for (int v = 0; v <= W; ++v) {
     __syncthreads();
-#pragma unroll
-    for (int c = 0; c < VN; ++c) {
-      float g = gb[c];
-#pragma unroll
-      for (int j = 0; j < W; ++j) g = v == j ? gw[c][j] : g;
-      red[ry][vx * VN + c] = g;
-    }
+    const float2 *const g = v == W ? gb : gw[v < W ? v : 0];
+    red[ry][vx] = make_float4(g[0].x, g[0].y, g[1].x, g[1].y);
     __syncthreads();
-    for (int c = threadIdx.x; c < kBwdVecs * VN; c += kBwdVecs * kBwdRuns) {
-      const int cc = (int)(blockIdx.x % vtiles) * kBwdVecs * VN + c;
-      if (cc >= a.D) continue;
-      float s = 0.f;
+    if (ry == v % kBwdRuns && vec < nvec) {
+      float4 s = red[0][vx];
 #pragma unroll
-      for (int r = 0; r < kBwdRuns; ++r) s += red[r][c];
-      partial[(blk * (W + 1) + v) * a.D + cc] = s;
+      for (int r = 1; r < kBwdRuns; ++r) {
+        const float4 e = red[r][vx];
+        s.x += e.x; s.y += e.y; s.z += e.z; s.w += e.w;
+      }
+      *reinterpret_cast<float4*>(partial + (blk * (W + 1) + v) * a.D + ch) = s;
     }
   }
 }
@@ -289,15 +369,15 @@ __global__ void __launch_bounds__(256) palimpsa_conv_bwd_sum_kernel(const float*
   }
 }
 
-// Run length of the backward: long runs waste less on the W - 1 tokens past the
-// end and on partials, short ones make enough threads. From 64 down to 8 until
-// there are 512 threads for each of 152 SMs.
-int bwd_run_len(const ConvArgs& a) {
-  const long long vecs = a.D / (a.bf16 ? 8 : 4);
-  int r = 64;
-  while (r > 8 && (long long)a.rows.n_seq * ((a.rows.max_len + r - 1) / r) * vecs < 152ll * 512) r /= 2;
+// Tokens of a run: long runs read fewer rows twice, short ones make enough threads.
+// From 64 (forward; backward 32) down to 8 until there are 1024 threads (512) for each
+// of 152 SMs.
+int run_len_of(const ConvArgs& a, int longest, long long threads) {
+  int r = longest;
+  while (r > kMinRun && (long long)a.rows.n_seq * ((a.rows.max_len + r - 1) / r) * (a.D / 4) < 152 * threads) r /= 2;
   return r;
 }
+int bwd_run_len(const ConvArgs& a) { return run_len_of(a, 64, 256); }
 int bwd_blocks_per_seq(const ConvArgs& a, int run) {
   const int per = run * kBwdRuns;
   return std::max(1, (a.rows.max_len + per - 1) / per);
@@ -306,7 +386,7 @@ int bwd_blocks_per_seq(const ConvArgs& a, int run) {
 template <bool BF16, int W>
 cudaError_t backward(const ConvArgs& a, float* scratch, cudaStream_t s) {
   const int run = bwd_run_len(a), bps = bwd_blocks_per_seq(a, run);
-  const int nvec = a.D / Vec<BF16>::n, vtiles = (nvec + kBwdVecs - 1) / kBwdVecs;
+  const int nvec = a.D / 4, vtiles = (nvec + kBwdVecs - 1) / kBwdVecs;
   const long long blocks = (long long)bps * a.rows.n_seq;
   if (blocks * vtiles > 0x7fffffffll) return cudaErrorInvalidConfiguration;
   palimpsa_conv_bwd_kernel<BF16, W>
@@ -318,18 +398,18 @@ cudaError_t backward(const ConvArgs& a, float* scratch, cudaStream_t s) {
 
 template <bool BF16, int W>
 cudaError_t forward(const ConvArgs& a, cudaStream_t s) {
-  const int runs = std::max(1, (a.rows.max_len + kRun - 1) / kRun);
-  const long long n = (long long)(a.D / Vec<BF16>::n) * runs * a.rows.n_seq, blocks = (n + kThreads - 1) / kThreads;
+  const int run = run_len_of(a, kMaxRun, 1024), runs = std::max(1, (a.rows.max_len + run - 1) / run);
+  const long long n = (long long)(a.D / 4) * runs * a.rows.n_seq, blocks = (n + kThreads - 1) / kThreads;
   if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
-  palimpsa_conv_kernel<BF16, W><<<(unsigned)blocks, kThreads, 0, s>>>(a, runs);
+  palimpsa_conv_kernel<BF16, W><<<(unsigned)blocks, kThreads, 0, s>>>(a, runs, run);
   return cudaGetLastError();
 }
 
 template <bool BF16, int W>
 cudaError_t step(const ConvArgs& a, cudaStream_t s) {
-  const long long n = (long long)(a.D / Vec<BF16>::n) * a.rows.n_seq, blocks = (n + 127) / 128;
+  const long long n = (long long)(a.D / 4) * a.rows.n_seq, blocks = (n + kThreads - 1) / kThreads;
   if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
-  palimpsa_conv_step_kernel<BF16, W><<<(unsigned)blocks, 128, 0, s>>>(a);
+  palimpsa_conv_step_kernel<BF16, W><<<(unsigned)blocks, kThreads, 0, s>>>(a);
   return cudaGetLastError();
 }
 

@@ -274,7 +274,7 @@ __global__ void __launch_bounds__(256) palimpsa_scan_bwd_kernel(ScanArgs a, Part
           const float2 b = *reinterpret_cast<const float2*>(fB + t * N + n0 + 2 * p);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const float2 u = __fmul2_rn(make_float2(sv[k], sv[k]), A2[k][p]);
+            const float2 u = decay_exponent(make_float2(sv[k], sv[k]), A2[k][p]);
             h[k][p] = __ffma2_rn(make_float2(xv[k], xv[k]), b,
                                  __fmul2_rn(make_float2(ex2_approx(u.x), ex2_approx(u.y)), h[k][p]));
           }
@@ -309,7 +309,7 @@ __global__ void __launch_bounds__(256) palimpsa_scan_bwd_kernel(ScanArgs a, Part
           const float2 b = *reinterpret_cast<const float2*>(fB + t * N + n0 + 2 * p);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const float2 u = __fmul2_rn(make_float2(sv[k], sv[k]), A2[k][p]);
+            const float2 u = decay_exponent(make_float2(sv[k], sv[k]), A2[k][p]);
             al[i][k][p] = make_float2(ex2_approx(u.x), ex2_approx(u.y));
             ah[i][k][p] = __fmul2_rn(al[i][k][p], h[k][p]);
             h[k][p] = __ffma2_rn(make_float2(xv[k], xv[k]), b, ah[i][k][p]);

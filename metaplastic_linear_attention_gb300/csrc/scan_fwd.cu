@@ -32,74 +32,100 @@
 // type once. 2^x is the SFU's (measured bias about -2e-8 a token for decays near
 // 1, so a state with a window of w tokens is off by about 2e-8 w).
 #include <algorithm>
-#include <mutex>
 
 #include "ssm.cuh"
 
 namespace palimpsa {
 namespace {
 
-constexpr int kChunk = 16;   // tokens staged together
-constexpr int kStages = 3;   // chunks in the ring
+constexpr int kChunk = 8;    // tokens staged together
+constexpr int kStages = 2;   // chunks in the ring of raw inputs
 constexpr int CH = kScanChannels;
-
-// Shared memory of a CTA, bytes (all parts 16-byte aligned).
-struct Smem {
-  int rx, rdt, rz, rB, rC, raw;  // one stage
-  int s, sx, B, C, y, par, total;
-  __host__ __device__ Smem(int N, int W, int es, int mode) {
-    const bool summary = mode != 0;
-    rx = 0;
-    rdt = rx + kChunk * CH * es;
-    rz = rdt + kChunk * CH * es;
-    rB = mode == 1 ? rz : rz + kChunk * CH * es;
-    rC = rB + kChunk * N * es;
-    raw = summary ? rC : rC + kChunk * N * es;
-    s = kStages * raw;
-    sx = s + kChunk * CH * 4;
-    B = sx + kChunk * CH * 4;
-    C = B + kChunk * N * 4;
-    y = summary ? C : C + kChunk * N * 4;
-    par = summary ? y : y + W * kChunk * CH * 4;
-    total = par + 2 * CH * 4;
-  }
-};
+constexpr int kGroup = 8;    // tokens whose y is stored together
+constexpr int kWarpsPerSM = 16;
 
 // What a launch computes: the scan; pass A of its time split; or pass A of the
 // backward's, which runs from the last token to the first with dy silu(z) in the
 // place of s x and C in the place of B: g <- exp(-A s_t) (g + C_t dpre_t).
 enum Mode { kForward, kSummary, kReverseSummary };
 
+// Shared memory of a CTA, bytes (all parts 16-byte aligned).
+struct Smem {
+  int rx, rdt, rz, rB, rC, raw;  // one stage of raw inputs
+  int s, sx, par, y, total;      // step sizes, s x, dt_bias and skip, the lane groups' parts of y
+  __host__ __device__ constexpr Smem(int N, int groups, int es, int mode)
+      : rx(0),
+        rdt(kChunk * CH * es),
+        rz(2 * kChunk * CH * es),
+        rB(mode == kSummary ? rz : rz + kChunk * CH * es),
+        rC(rB + kChunk * N * es),
+        raw(mode == kForward ? rC + kChunk * N * es : rC),
+        s(kStages * raw),
+        sx(s + kChunk * CH * 4),
+        par(sx + kChunk * CH * 4),
+        y(par + 2 * CH * 4),
+        total(mode == kForward ? y + groups * kChunk * CH * 4 : y) {}
+};
+
+// 4 values of the input type.
+template <bool BF16>
+__device__ __forceinline__ void load4(float* f, const unsigned char* p) {
+  if constexpr (BF16) {
+    const uint2 u = *reinterpret_cast<const uint2*>(p);
+    f[0] = bf16_lo(u.x); f[1] = bf16_hi(u.x); f[2] = bf16_lo(u.y); f[3] = bf16_hi(u.y);
+  } else {
+    const float4 u = *reinterpret_cast<const float4*>(p);
+    f[0] = u.x; f[1] = u.y; f[2] = u.z; f[3] = u.w;
+  }
+}
+// NS values of a row of B or C as they came, each twice (for two channels).
+template <bool BF16, int NS>
+__device__ __forceinline__ void load_states(float2* f, const unsigned char* p) {
+  float v[NS];
+  if constexpr (NS == 4) {
+    load4<BF16>(v, p);
+  } else if constexpr (BF16) {
+    const uint32_t u = *reinterpret_cast<const uint32_t*>(p);
+    v[0] = bf16_lo(u); v[1] = bf16_hi(u);
+  } else {
+    const float2 u = *reinterpret_cast<const float2*>(p);
+    v[0] = u.x; v[1] = u.y;
+  }
+#pragma unroll
+  for (int j = 0; j < NS; ++j) f[j] = make_float2(v[j], v[j]);
+}
+
+template <int W>
+__device__ __forceinline__ void cta_sync() {
+  if constexpr (W == 1) __syncwarp();
+  else __syncthreads();
+}
+
 // NS states per lane (2 or 4), W warps: N = 4 NS W.
 template <bool BF16, int NS, int W, int MODE>
-__global__ void __launch_bounds__(32 * W) palimpsa_scan_kernel(ScanArgs a, int tiles) {
+__global__ void __launch_bounds__(32 * W, kWarpsPerSM / W) palimpsa_scan_kernel(ScanArgs a, int tiles) {
   using V = Vec<BF16>;
-  constexpr int VN = V::n, ES = V::bytes, N = 4 * NS * W, NP = NS / 2;
-  constexpr int VPR = CH / VN;        // vectors in a row of the tile
-  constexpr int BPR = (N + VN - 1) / VN;  // vectors in a row of B or C
-  constexpr int NT = 32 * W;
-  constexpr bool SUMMARY = MODE != kForward, REV = MODE == kReverseSummary;
+  constexpr int VN = V::n, ES = V::bytes, N = 4 * NS * W, NT = 32 * W;
+  constexpr int VPR = CH / VN;  // vectors in a row of the tile
+  constexpr int BPR = N / VN;   // vectors in a row of B or C
+  constexpr bool FWD = MODE == kForward, REV = MODE == kReverseSummary;
+  constexpr Smem L(N, 4 * W, ES, MODE);
   extern __shared__ __align__(128) unsigned char smem[];
-  const Smem L(N, W, ES, MODE);
   float* const fs = reinterpret_cast<float*>(smem + L.s);
   float* const fsx = reinterpret_cast<float*>(smem + L.sx);
-  float* const fB = reinterpret_cast<float*>(smem + L.B);
-  float* const fC = reinterpret_cast<float*>(smem + L.C);
   float* const fy = reinterpret_cast<float*>(smem + L.y);
-  float* const fbias = reinterpret_cast<float*>(smem + L.par);
-  float* const fskip = fbias + CH;
+  float* const fpar = reinterpret_cast<float*>(smem + L.par);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int tile = (int)(blockIdx.x % tiles);
   const long long rest = blockIdx.x / tiles;
   // Pass A leaves out the segment that no other follows.
-  const int nseg = SUMMARY ? a.nseg - 1 : a.nseg;
+  const int nseg = FWD ? a.nseg : a.nseg - 1;
   const int seg = (int)(rest % nseg) + (REV ? 1 : 0);
   const long long n = rest / nseg;
   const int per_group = a.D / a.G, tpg = (per_group + CH - 1) / CH;
   const int g = tile / tpg, ch0 = g * per_group + (tile % tpg) * CH;
   const int nch = min(CH, (g + 1) * per_group - ch0);  // a multiple of 8
-  const int nv = nch / VN;
   long long row0;
   int len;
   if (!seq_rows(a.rows, n, &row0, &len)) {
@@ -110,95 +136,160 @@ __global__ void __launch_bounds__(32 * W) palimpsa_scan_kernel(ScanArgs a, int t
   const bool last = te >= len;
   // Segments past the end have nothing to do, nor has the forward's pass A on the last.
   if ((tb >= len && seg > 0) || (MODE == kSummary && last)) return;
+  // (A chunk's tokens past the end have steps of size 0 and B = C = 0: they change nothing.)
   const int tn = te - tb, nchunk = (tn + kChunk - 1) / kChunk;
+  auto first_token = [&](int c) { return (REV ? nchunk - 1 - c : c) * kChunk; };
 
-  // A lane's channels 4 cl .. 4 cl + 3 of the tile, and states n0 .. n0 + NS - 1.
-  const int cl = lane & 7, sl = lane >> 3;
-  const int n0 = warp * 4 * NS + sl * NS;
-  bool bad = false;
-  float2 A2[4][NP], h[4][NP];  // A scaled by -log2(e): exp(-A s) = 2^(A2 s)
-  float2 dsum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    const int d = 4 * cl + c;
-    const bool in = d < nch;
-    const size_t an = ((size_t)(ch0 + d)) * N + n0;
-    const float* h0 = nullptr;
-    if (!SUMMARY && in) {
-      if (a.nseg > 1) h0 = a.seg_state + ((size_t)(n * a.nseg + seg) * a.D + ch0 + d) * N + n0;
-      else if (a.h0) h0 = a.h0 + ((size_t)n * a.D + ch0 + d) * N + n0;
-    }
-#pragma unroll
-    for (int p = 0; p < NP; ++p) {
-      const float2 v = in ? *reinterpret_cast<const float2*>(a.A + an + 2 * p) : make_float2(1.f, 1.f);
-      bad |= !(pos_finite(v.x) && pos_finite(v.y));
-      A2[c][p] = make_float2(-kLog2e * v.x, -kLog2e * v.y);
-      h[c][p] = h0 ? *reinterpret_cast<const float2*>(h0 + 2 * p) : make_float2(0.f, 0.f);
-    }
-  }
-  for (int c = tid; c < CH; c += NT) {
-    fbias[c] = c < nch && a.dt_bias ? a.dt_bias[ch0 + c] : 0.f;
-    fskip[c] = c < nch && a.skip ? a.skip[ch0 + c] : 0.f;
-  }
-
-  const long long x_ld = REV ? a.dy_ld : a.x_ld, B_ld = REV ? a.C_ld : a.B_ld;
-  const char* const gx = static_cast<const char*>(REV ? a.dy : a.x) + ((row0 + tb) * x_ld + ch0) * ES;
-  const char* const gdt = static_cast<const char*>(a.dt) + ((row0 + tb) * a.dt_ld + ch0) * ES;
-  const char* const gz = a.z ? static_cast<const char*>(a.z) + ((row0 + tb) * a.z_ld + ch0) * ES : nullptr;
-  const char* const gB = static_cast<const char*>(REV ? a.C : a.B) + ((row0 + tb) * B_ld + g * N) * ES;
-  const char* const gC = SUMMARY ? nullptr : static_cast<const char*>(a.C) + ((row0 + tb) * a.C_ld + g * N) * ES;
-  auto stage = [&](int c) {  // copies of chunk c, as one group
+  // A thread copies in, converts and finishes the same vectors of x, dt and z; their
+  // place v in a row is the same for all of them. The copies' addresses move on by a
+  // chunk each time.
+  constexpr int VPT = (kChunk * VPR + NT - 1) / NT, BPT = (kChunk * BPR + NT - 1) / NT;
+  const int v = tid % VPR, vt = tid / VPR, bv = tid % BPR, bt = tid / BPR;
+  const bool vin = v * VN < nch, gated = a.z && MODE != kSummary;
+  const long long x_ld = (REV ? a.dy_ld : a.x_ld) * ES, dt_ld = a.dt_ld * ES, z_ld = a.z_ld * ES;
+  const long long B_ld = (REV ? a.C_ld : a.B_ld) * ES, C_ld = a.C_ld * ES;
+  const long long rb = row0 + tb;
+  const int t_first = first_token(0);
+  const char* gx = static_cast<const char*>(REV ? a.dy : a.x) + (rb + t_first + vt) * x_ld + ch0 * ES + v * 16;
+  const char* gdt = static_cast<const char*>(a.dt) + (rb + t_first + vt) * dt_ld + ch0 * ES + v * 16;
+  const char* gz = gated ? static_cast<const char*>(a.z) + (rb + t_first + vt) * z_ld + ch0 * ES + v * 16 : nullptr;
+  const char* gB = static_cast<const char*>(REV ? a.C : a.B) + (rb + t_first + bt) * B_ld + g * N * ES + bv * 16;
+  const char* gC = FWD ? static_cast<const char*>(a.C) + (rb + t_first + bt) * C_ld + g * N * ES + bv * 16 : nullptr;
+  auto stage = [&](int c) {  // copies of chunk c (the next in order), as one group
     if (c < nchunk) {
       unsigned char* const st = smem + (c % kStages) * L.raw;
-      const int t0 = (REV ? nchunk - 1 - c : c) * kChunk, nt = min(kChunk, tn - t0);
-      for (int i = tid; i < kChunk * VPR; i += NT) {
-        const int t = i / VPR, v = i % VPR;
-        if (t >= nt || v >= nv) continue;
-        const int o = (t * CH + v * VN) * ES;
-        const long long r = t0 + t, b = (long long)v * 16;
-        cp_async16(st + L.rx + o, gx + r * x_ld * ES + b);
-        cp_async16(st + L.rdt + o, gdt + r * a.dt_ld * ES + b);
-        if (MODE != kSummary && gz) cp_async16(st + L.rz + o, gz + r * a.z_ld * ES + b);
+      const int nt = min(kChunk, tn - first_token(c));
+#pragma unroll
+      for (int k = 0; k < VPT; ++k) {
+        const int i = tid + k * NT;
+        if (k * (NT / VPR) + vt >= nt || !vin) continue;
+        cp_async16(st + L.rx + 16 * i, gx + k * (NT / VPR) * x_ld);
+        cp_async16(st + L.rdt + 16 * i, gdt + k * (NT / VPR) * dt_ld);
+        if (gated) cp_async16(st + L.rz + 16 * i, gz + k * (NT / VPR) * z_ld);
       }
-      for (int i = tid; i < kChunk * BPR; i += NT) {
-        const int t = i / BPR, v = i % BPR;
-        if (t >= nt) continue;
-        const int o = (t * N + v * VN) * ES;
-        const long long r = t0 + t, b = (long long)v * 16;
-        cp_async16(st + L.rB + o, gB + r * B_ld * ES + b);
-        if (!SUMMARY) cp_async16(st + L.rC + o, gC + r * a.C_ld * ES + b);
+#pragma unroll
+      for (int k = 0; k < BPT; ++k) {
+        const int i = tid + k * NT;
+        if (i >= kChunk * BPR) continue;
+        const bool in = k * NT / BPR + bt < nt;  // rows past the end are filled with zeros
+        cp_async16(st + L.rB + 16 * i, in ? gB + k * (NT / BPR) * B_ld : gB - bt * B_ld, in);
+        if (FWD) cp_async16(st + L.rC + 16 * i, in ? gC + k * (NT / BPR) * C_ld : gC - bt * C_ld, in);
       }
+      constexpr int step = REV ? -kChunk : kChunk;
+      gx += step * x_ld;
+      gdt += step * dt_ld;
+      gB += step * B_ld;
+      if (FWD) gC += step * C_ld;
+      if (gated) gz += step * z_ld;
     }
     cp_async_commit();
   };
 #pragma unroll
   for (int c = 0; c < kStages - 1; ++c) stage(c);
 
+  for (int c = tid; c < CH; c += NT) {
+    fpar[c] = c < nch && a.dt_bias ? a.dt_bias[ch0 + c] : 0.f;
+    fpar[CH + c] = FWD && c < nch && a.skip ? a.skip[ch0 + c] : 0.f;
+  }
+  // A lane's channels 4 cl .. 4 cl + 3 of the tile, as two pairs, and its states from n0 on.
+  // In rows of fp32 values per channel (s, s x, y parts) the quads of 4 channels of odd
+  // tokens change places in pairs, so that the threads that hold 8 channels each (two
+  // quads) and those that hold one reach all banks alike.
+  const int cl = lane & 7, ng = warp * 4 + (lane >> 3), n0 = ng * NS;
+  const int cq0 = 4 * cl, cq1 = 4 * (cl ^ 1);
+  float2 A2[2][NS], h[2][NS];  // A scaled by -log2(e): exp(-A s) = 2^(A2 s)
+  float2 dsum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+  const size_t at = (size_t)(ch0 + 4 * cl) * N + n0;  // of the first channel in [D, N]
+  const float* h0 = nullptr;
+  if (FWD && a.nseg > 1) h0 = a.seg_state + (size_t)(n * a.nseg + seg) * a.D * N;
+  else if (FWD && a.h0) h0 = a.h0 + (size_t)n * a.D * N;
+  bool bad = false;
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    const bool in = 4 * cl + c < nch;
+#pragma unroll
+    for (int j = 0; j < NS; ++j) {
+      const float A = in ? a.A[at + c * N + j] : 1.f;
+      bad |= !pos_finite(A);
+      (c & 1 ? A2[c / 2][j].y : A2[c / 2][j].x) = -kLog2e * A;
+      (c & 1 ? h[c / 2][j].y : h[c / 2][j].x) = in && h0 ? h0[at + c * N + j] : 0.f;
+    }
+  }
+  // The lane's part of a [D, N] array, stored.
+  auto store_state = [&](float* out) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      if (4 * cl + c < nch)
+#pragma unroll
+        for (int j = 0; j < NS; j += 2)
+          *reinterpret_cast<float2*>(out + at + c * N + j) =
+              c & 1 ? make_float2(h[c / 2][j].y, h[c / 2][j + 1].y) : make_float2(h[c / 2][j].x, h[c / 2][j + 1].x);
+  };
+  // One token; y gets this lane's part of its channels' y.
+  auto token = [&](const unsigned char* st, int t, float2* y) {
+    const float4 s4 = *reinterpret_cast<const float4*>(fs + t * CH + (t & 1 ? cq1 : cq0));
+    const float4 x4 = *reinterpret_cast<const float4*>(fsx + t * CH + (t & 1 ? cq1 : cq0));
+    const float2 s[2] = {make_float2(s4.x, s4.y), make_float2(s4.z, s4.w)};
+    const float2 x[2] = {make_float2(x4.x, x4.y), make_float2(x4.z, x4.w)};
+    float2 b[NS], cc[NS];
+    load_states<BF16, NS>(b, st + L.rB + (t * N + n0) * ES);
+    if (FWD) load_states<BF16, NS>(cc, st + L.rC + (t * N + n0) * ES);
+#pragma unroll
+    for (int p = 0; p < 2; ++p)
+#pragma unroll
+      for (int j = 0; j < NS; ++j) {
+        float2& hh = h[p][j];
+        const float2 u = decay_exponent(s[p], A2[p][j]);
+        const float2 e = make_float2(ex2_approx(u.x), ex2_approx(u.y));
+        if (REV) hh = __fmul2_rn(e, __ffma2_rn(x[p], b[j], hh));
+        else hh = __ffma2_rn(e, hh, __fmul2_rn(x[p], b[j]));
+        if (FWD) y[p] = j == 0 ? __fmul2_rn(hh, cc[j]) : __ffma2_rn(hh, cc[j], y[p]);
+      }
+    if (!FWD)
+#pragma unroll
+      for (int p = 0; p < 2; ++p) dsum[p] = __fadd2_rn(dsum[p], s[p]);
+  };
+
+  float least = 0.f, most = 0.f;  // of the step sizes
   for (int c = 0; c < nchunk; ++c) {
-    const int t0 = (REV ? nchunk - 1 - c : c) * kChunk, nt = min(kChunk, tn - t0);
+    const int t0 = first_token(c), nt = min(kChunk, tn - t0);
+    unsigned char* const st = smem + (c % kStages) * L.raw;
     cp_async_wait<kStages - 2>();
-    __syncthreads();  // chunk c is here; the last chunk's stage and y are free
+    cta_sync<W>();  // chunk c is here, and the last one's stage, operands and y are free
     stage(c + kStages - 1);
-    const unsigned char* const st = smem + (c % kStages) * L.raw;
+#pragma unroll
     for (int i = tid; i < kChunk * VPR; i += NT) {
-      const int t = i / VPR, v = i % VPR;
-      if (t >= nt) continue;
       float s[VN], x[VN];
-      if (v < nv) {
-        V::unpack(*reinterpret_cast<const uint4*>(st + L.rdt + (t * CH + v * VN) * ES), s);
-        V::unpack(*reinterpret_cast<const uint4*>(st + L.rx + (t * CH + v * VN) * ES), x);
+      if (vin && i / VPR < nt) {
+        float bias[VN];
 #pragma unroll
-        for (int k = 0; k < VN; ++k) {
-          s[k] += fbias[v * VN + k];
-          if (a.softplus) s[k] = softplus_fast(s[k]);
-          bad |= !nonneg_finite(s[k]);
-          if (!REV) x[k] *= s[k];
-        }
-        if (REV && gz) {
+        for (int k = 0; k < VN; k += 4)
+          *reinterpret_cast<float4*>(bias + k) = *reinterpret_cast<const float4*>(fpar + v * VN + k);
+        V::unpack(*reinterpret_cast<const uint4*>(st + L.rdt + 16 * i), s);
+        V::unpack(*reinterpret_cast<const uint4*>(st + L.rx + 16 * i), x);
+        if (REV && gated) {
           float z[VN];
-          V::unpack(*reinterpret_cast<const uint4*>(st + L.rz + (t * CH + v * VN) * ES), z);
+          V::unpack(*reinterpret_cast<const uint4*>(st + L.rz + 16 * i), z);
 #pragma unroll
-          for (int k = 0; k < VN; ++k) x[k] *= silu_fast(z[k]);
+          for (int k = 0; k < VN; k += 2) {
+            const float2 d = __fmul2_rn(make_float2(x[k], x[k + 1]), silu_fast(make_float2(z[k], z[k + 1])));
+            x[k] = d.x;
+            x[k + 1] = d.y;
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < VN; k += 2) {
+          float2 u = __fadd2_rn(make_float2(s[k], s[k + 1]), make_float2(bias[k], bias[k + 1]));
+          if (a.softplus) u = softplus_fast(u);
+          else least = fminf(least, fminf(u.x, u.y));
+          most = fmax_nan(most, fmax_nan(u.x, u.y));
+          s[k] = u.x;
+          s[k + 1] = u.y;
+          if (!REV) {
+            const float2 sx = __fmul2_rn(u, make_float2(x[k], x[k + 1]));
+            x[k] = sx.x;
+            x[k + 1] = sx.y;
+          }
         }
       } else {
 #pragma unroll
@@ -206,121 +297,72 @@ __global__ void __launch_bounds__(32 * W) palimpsa_scan_kernel(ScanArgs a, int t
       }
 #pragma unroll
       for (int k = 0; k < VN; k += 4) {
-        *reinterpret_cast<float4*>(fs + t * CH + v * VN + k) = make_float4(s[k], s[k + 1], s[k + 2], s[k + 3]);
-        *reinterpret_cast<float4*>(fsx + t * CH + v * VN + k) = make_float4(x[k], x[k + 1], x[k + 2], x[k + 3]);
+        const int o = i / VPR * CH + ((v * VN + k) ^ 4 * (i / VPR & 1));
+        *reinterpret_cast<float4*>(fs + o) = make_float4(s[k], s[k + 1], s[k + 2], s[k + 3]);
+        *reinterpret_cast<float4*>(fsx + o) = make_float4(x[k], x[k + 1], x[k + 2], x[k + 3]);
       }
     }
-    for (int i = tid; i < kChunk * BPR; i += NT) {
-      const int t = i / BPR;
-      if (t >= nt) continue;
-      float f[VN];
-      V::unpack(reinterpret_cast<const uint4*>(st + L.rB)[i], f);
-#pragma unroll
-      for (int k = 0; k < VN; k += 4)
-        *reinterpret_cast<float4*>(fB + i * VN + k) = make_float4(f[k], f[k + 1], f[k + 2], f[k + 3]);
-      if (!SUMMARY) {
-        V::unpack(reinterpret_cast<const uint4*>(st + L.rC)[i], f);
-#pragma unroll
-        for (int k = 0; k < VN; k += 4)
-          *reinterpret_cast<float4*>(fC + i * VN + k) = make_float4(f[k], f[k + 1], f[k + 2], f[k + 3]);
-      }
-    }
-    __syncthreads();
+    cta_sync<W>();
 
-    if (!SUMMARY && a.ckpt && (tb + t0) % kScanCheckpoint == 0) {
-      float* const ck = a.ckpt + (scan_ckpt_row0(a.rows, n, row0) + (tb + t0) / kScanCheckpoint) * a.D * N;
+    if (FWD && a.ckpt && (tb + t0) % kScanCheckpoint == 0)
+      store_state(a.ckpt + (scan_ckpt_row0(a.rows, n, row0) + (tb + t0) / kScanCheckpoint) * a.D * N);
+    // y is stored after a group of tokens: a store between two tokens would hold back
+    // the loads of the second, which the compiler cannot tell from it.
+#pragma unroll 1
+    for (int tg = 0; tg < kChunk; tg += kGroup) {
+      float2 y[kGroup][2];
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (4 * cl + k < nch)
+      for (int i = 0; i < kGroup; ++i) token(st, REV ? kChunk - 1 - tg - i : tg + i, y[i]);
+      if (FWD)
 #pragma unroll
-          for (int p = 0; p < NP; ++p)
-            *reinterpret_cast<float2*>(ck + (size_t)(ch0 + 4 * cl + k) * N + n0 + 2 * p) = h[k][p];
+        for (int i = 0; i < kGroup; ++i)
+          *reinterpret_cast<float4*>(fy + (ng * kChunk + tg + i) * CH + ((tg + i) & 1 ? cq1 : cq0)) =
+              make_float4(y[i][0].x, y[i][0].y, y[i][1].x, y[i][1].y);
     }
 
-    auto token = [&](int t) {
-      const float4 s4 = *reinterpret_cast<const float4*>(fs + t * CH + 4 * cl);
-      const float4 x4 = *reinterpret_cast<const float4*>(fsx + t * CH + 4 * cl);
-      const float sv[4] = {s4.x, s4.y, s4.z, s4.w}, xv[4] = {x4.x, x4.y, x4.z, x4.w};
-      float2 b[NP], cc[NP];
+    if (FWD) {
+      cta_sync<W>();
 #pragma unroll
-      for (int p = 0; p < NP; ++p) b[p] = *reinterpret_cast<const float2*>(fB + t * N + n0 + 2 * p);
-      if (!SUMMARY)
-#pragma unroll
-        for (int p = 0; p < NP; ++p) cc[p] = *reinterpret_cast<const float2*>(fC + t * N + n0 + 2 * p);
-      float y[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        float2 acc = make_float2(0.f, 0.f);
-#pragma unroll
-        for (int p = 0; p < NP; ++p) {
-          const float2 u = __fmul2_rn(make_float2(sv[k], sv[k]), A2[k][p]);
-          const float2 e = make_float2(ex2_approx(u.x), ex2_approx(u.y));
-          if (REV) h[k][p] = __fmul2_rn(e, __ffma2_rn(make_float2(xv[k], xv[k]), b[p], h[k][p]));
-          else h[k][p] = __ffma2_rn(e, h[k][p], __fmul2_rn(make_float2(xv[k], xv[k]), b[p]));
-          if (!SUMMARY) acc = p == 0 ? __fmul2_rn(h[k][p], cc[p]) : __ffma2_rn(h[k][p], cc[p], acc);
-        }
-        y[k] = acc.x + acc.y;
-      }
-      if (SUMMARY) {
-        dsum[0] = __fadd2_rn(dsum[0], make_float2(sv[0], sv[1]));
-        dsum[1] = __fadd2_rn(dsum[1], make_float2(sv[2], sv[3]));
-      } else {
-        // Reduce-scatter over the 4 lane groups: lane (cl, sl) ends with channel 4 cl + sl.
-        const bool hi = sl & 2, odd = sl & 1;
-        const float k0 = hi ? y[2] : y[0], k1 = hi ? y[3] : y[1];
-        const float r0 = k0 + __shfl_xor_sync(0xffffffffu, hi ? y[0] : y[2], 16);
-        const float r1 = k1 + __shfl_xor_sync(0xffffffffu, hi ? y[1] : y[3], 16);
-        const float r = (odd ? r1 : r0) + __shfl_xor_sync(0xffffffffu, odd ? r0 : r1, 8);
-        fy[(warp * kChunk + t) * CH + 4 * cl + sl] = r;
-      }
-    };
-    if (nt == kChunk) {
-#pragma unroll 4
-      for (int t = 0; t < kChunk; ++t) token(REV ? kChunk - 1 - t : t);
-    } else {
-      for (int t = 0; t < nt; ++t) token(REV ? nt - 1 - t : t);
-    }
-
-    if (!SUMMARY) {
-      __syncthreads();
       for (int i = tid; i < kChunk * VPR; i += NT) {
-        const int t = i / VPR, v = i % VPR;
-        if (t >= nt || v >= nv) continue;
-        float o[VN], x[VN];
-        V::unpack(*reinterpret_cast<const uint4*>(st + L.rx + (t * CH + v * VN) * ES), x);
+        const int t = i / VPR;
+        if (t >= nt || !vin) continue;
+        float o[VN], x[VN], skip[VN];
+        V::unpack(*reinterpret_cast<const uint4*>(st + L.rx + 16 * i), x);
 #pragma unroll
-        for (int k = 0; k < VN; ++k) {
-          o[k] = fskip[v * VN + k] * x[k];
+        for (int k = 0; k < VN; k += 4) {
+          *reinterpret_cast<float4*>(skip + k) = *reinterpret_cast<const float4*>(fpar + CH + v * VN + k);
+          float2 y0 = __fmul2_rn(make_float2(skip[k], skip[k + 1]), make_float2(x[k], x[k + 1]));
+          float2 y1 = __fmul2_rn(make_float2(skip[k + 2], skip[k + 3]), make_float2(x[k + 2], x[k + 3]));
 #pragma unroll
-          for (int w = 0; w < W; ++w) o[k] += fy[(w * kChunk + t) * CH + v * VN + k];
+          for (int w = 0; w < 4 * W; ++w) {
+            const float4 p =
+                *reinterpret_cast<const float4*>(fy + (w * kChunk + t) * CH + ((v * VN + k) ^ 4 * (t & 1)));
+            y0 = __fadd2_rn(y0, make_float2(p.x, p.y));
+            y1 = __fadd2_rn(y1, make_float2(p.z, p.w));
+          }
+          o[k] = y0.x; o[k + 1] = y0.y; o[k + 2] = y1.x; o[k + 3] = y1.y;
         }
-        if (gz) {
-          V::unpack(*reinterpret_cast<const uint4*>(st + L.rz + (t * CH + v * VN) * ES), x);
+        if (gated) {
+          V::unpack(*reinterpret_cast<const uint4*>(st + L.rz + 16 * i), x);
 #pragma unroll
-          for (int k = 0; k < VN; ++k) o[k] *= silu_fast(x[k]);
+          for (int k = 0; k < VN; k += 2) {
+            const float2 y = __fmul2_rn(make_float2(o[k], o[k + 1]), silu_fast(make_float2(x[k], x[k + 1])));
+            o[k] = y.x;
+            o[k + 1] = y.y;
+          }
         }
-        *reinterpret_cast<uint4*>(static_cast<char*>(a.y) + ((row0 + tb + t0 + t) * a.D + ch0 + v * VN) * ES) =
-            V::pack(o);
+        *reinterpret_cast<uint4*>(static_cast<char*>(a.y) + ((rb + t0 + t) * a.D + ch0 + v * VN) * ES) = V::pack(o);
       }
     }
   }
-  if (bad) latch_status(a.status, kStatusDomain);
-#pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    if (4 * cl + c >= nch) continue;
-    float* out = nullptr;
-    if (SUMMARY) out = a.seg_state + ((size_t)(n * a.nseg + seg) * a.D + ch0 + 4 * cl + c) * N + n0;
-    else if (last && a.h_T) out = a.h_T + ((size_t)n * a.D + ch0 + 4 * cl + c) * N + n0;
-    if (out)
-#pragma unroll
-      for (int p = 0; p < NP; ++p) *reinterpret_cast<float2*>(out + 2 * p) = h[c][p];
-  }
-  if (SUMMARY && warp == 0 && sl == 0) {
-    const float v[4] = {dsum[0].x, dsum[0].y, dsum[1].x, dsum[1].y};
+  if (bad || !(nonneg_finite(least) && nonneg_finite(most))) latch_status(a.status, kStatusDomain);
+  if (!FWD) store_state(a.seg_state + (size_t)(n * a.nseg + seg) * a.D * N);
+  else if (last) store_state(a.h_T + (size_t)n * a.D * N);
+  if (!FWD && ng == 0)
 #pragma unroll
     for (int c = 0; c < 4; ++c)
-      if (4 * cl + c < nch) a.seg_dt[(size_t)(n * a.nseg + seg) * a.D + ch0 + 4 * cl + c] = v[c];
-  }
+      if (4 * cl + c < nch)
+        a.seg_dt[(size_t)(n * a.nseg + seg) * a.D + ch0 + 4 * cl + c] = c & 1 ? dsum[c / 2].y : dsum[c / 2].x;
 }
 
 // Start states of the segments, in place over their summaries: one thread per
@@ -350,7 +392,7 @@ __global__ void __launch_bounds__(256) palimpsa_scan_carry_kernel(ScanArgs a, bo
 
 template <bool BF16, int NS, int W, int MODE>
 cudaError_t run(const ScanArgs& a, cudaStream_t s) {
-  const Smem L(4 * NS * W, W, Vec<BF16>::bytes, MODE);
+  constexpr Smem L(4 * NS * W, 4 * W, Vec<BF16>::bytes, MODE);
   const long long tiles = scan_tiles(a), blocks = tiles * a.rows.n_seq * (MODE != kForward ? a.nseg - 1 : a.nseg);
   if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
   if (L.total > 48 * 1024) {
@@ -375,28 +417,25 @@ cudaError_t dispatch(const ScanArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t plan_scan(const ScanArgs& a, bool backward, int* nseg, int* seg_len) {
+cudaError_t plan_scan(ScanArgs* a, bool backward) {
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  const long long warps = scan_tiles(a) * a.rows.n_seq * std::max(1, a.N / 16);
-  const long long slots = 4ll * sms;  // one warp per scheduler
-  const int len = a.rows.max_len;
-  *nseg = 1;
-  *seg_len = std::max(len, 1);
-  // Forward: the split does about twice the work, so it pays below half a warp
-  // per scheduler; it then aims at three. Backward: pass A is a small part of the
-  // work, so the split pays below the two warps that a scheduler's registers hold.
-  if (backward ? warps < 2 * slots : 2 * warps <= slots) {
-    const int shortest = backward ? 64 : 128;  // tokens of a segment, at least
-    long long want = backward ? 2 * slots / warps : (3 * slots + warps - 1) / warps;
-    want = std::min<long long>(want, len / shortest);
-    if (want >= (backward ? 2 : 3)) {
-      const int per = (int)((len + want - 1) / want);
-      *seg_len = (per + kScanCheckpoint - 1) / kScanCheckpoint * kScanCheckpoint;
-      *nseg = (len + *seg_len - 1) / *seg_len;
-    }
+  const long long warps = scan_tiles(*a) * a->rows.n_seq * std::max(1, a->N / 16);
+  const int len = a->rows.max_len;
+  a->nseg = 1;
+  a->seg_len = std::max(len, 1);
+  // Segments for one wave of CTAs: the warps that an SM holds, in every SM.
+  long long want = (long long)(backward ? 8 : kWarpsPerSM) * sms / warps;
+  // The forward's split does nearly twice the work: it pays from 3 segments on. Pass A
+  // is a small part of a backward.
+  if (!backward && want < 3) want = 1;
+  want = std::min<long long>(want, len / 64);
+  if (want >= 2) {
+    const int per = (int)((len + want - 1) / want);
+    a->seg_len = (per + kScanCheckpoint - 1) / kScanCheckpoint * kScanCheckpoint;
+    a->nseg = (len + a->seg_len - 1) / a->seg_len;
   }
   return cudaSuccess;
 }

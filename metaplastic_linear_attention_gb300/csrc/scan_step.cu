@@ -64,10 +64,10 @@ __global__ void __launch_bounds__(128) palimpsa_scan_step_kernel(ScanArgs a) {
       bad |= !(nonneg_finite(s[k]) && pos_finite(A[k].x) && pos_finite(A[k].y) && pos_finite(A[k].z) &&
                pos_finite(A[k].w));
       const float m = -kLog2e * s[k], w = s[k] * x[k];
-      h[k].x = fmaf(ex2_approx(m * A[k].x), h[k].x, w * B[k].x);
-      h[k].y = fmaf(ex2_approx(m * A[k].y), h[k].y, w * B[k].y);
-      h[k].z = fmaf(ex2_approx(m * A[k].z), h[k].z, w * B[k].z);
-      h[k].w = fmaf(ex2_approx(m * A[k].w), h[k].w, w * B[k].w);
+      h[k].x = fmaf(ex2_approx(fmaf(m, A[k].x, kDecayShift)), h[k].x, w * B[k].x);
+      h[k].y = fmaf(ex2_approx(fmaf(m, A[k].y, kDecayShift)), h[k].y, w * B[k].y);
+      h[k].z = fmaf(ex2_approx(fmaf(m, A[k].z, kDecayShift)), h[k].z, w * B[k].z);
+      h[k].w = fmaf(ex2_approx(fmaf(m, A[k].w, kDecayShift)), h[k].w, w * B[k].w);
       *reinterpret_cast<float4*>(a.h_T + i * N + n0) = h[k];
       y = fmaf(h[k].x, C[k].x, fmaf(h[k].y, C[k].y, fmaf(h[k].z, C[k].z, h[k].w * C[k].w)));
     }

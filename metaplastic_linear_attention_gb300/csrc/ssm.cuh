@@ -104,9 +104,9 @@ inline long long scan_tiles(const ScanArgs& a) {
   return (long long)a.G * ((dg + kScanChannels - 1) / kScanChannels);
 }
 
-// Time split of a scan or of its backward: segments per sequence and their
-// length (a multiple of kScanCheckpoint). Scratch of scan_scratch_floats() holds it.
-cudaError_t plan_scan(const ScanArgs& a, bool backward, int* nseg, int* seg_len);
+// Plans a scan or its backward: sets a->nseg and a->seg_len (a multiple of
+// kScanCheckpoint). Scratch of scan_scratch_floats() holds a time split.
+cudaError_t plan_scan(ScanArgs* a, bool backward);
 inline size_t scan_scratch_floats(const ScanArgs& a, int nseg) {
   return nseg > 1 ? (size_t)a.rows.n_seq * nseg * a.D * (a.N + 1) : 0;
 }
@@ -172,8 +172,39 @@ struct Vec {
   }
 };
 
+// 4 values of the input type: 8 bytes of bf16 or 16 of fp32, as two fp32 pairs.
+template <bool BF16>
+struct Quad {
+  using Raw = uint4;
+  static __device__ __forceinline__ void unpack(const Raw& u, float2* f) {
+    f[0] = make_float2(__uint_as_float(u.x), __uint_as_float(u.y));
+    f[1] = make_float2(__uint_as_float(u.z), __uint_as_float(u.w));
+  }
+  static __device__ __forceinline__ Raw pack(const float2* f) {
+    return make_uint4(__float_as_uint(f[0].x), __float_as_uint(f[0].y), __float_as_uint(f[1].x), __float_as_uint(f[1].y));
+  }
+  static __device__ __forceinline__ Raw zero() { return make_uint4(0, 0, 0, 0); }
+};
+template <>
+struct Quad<true> {
+  using Raw = uint2;
+  static __device__ __forceinline__ void unpack(const Raw& u, float2* f) {
+    f[0] = make_float2(bf16_lo(u.x), bf16_hi(u.x));
+    f[1] = make_float2(bf16_lo(u.y), bf16_hi(u.y));
+  }
+  static __device__ __forceinline__ Raw pack(const float2* f) {
+    return make_uint2(Vec<true>::two(f[0].x, f[0].y), Vec<true>::two(f[1].x, f[1].y));
+  }
+  static __device__ __forceinline__ Raw zero() { return make_uint2(0, 0); }
+};
+
 __device__ __forceinline__ void cp_async16(void* dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+// The same, or 16 bytes of zeros where `in` is false (src is then not read).
+__device__ __forceinline__ void cp_async16(void* dst, const void* src, bool in) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(in ? 16 : 0)
+               : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int PENDING>
@@ -188,28 +219,55 @@ __device__ __forceinline__ float ex2_approx(float x) {
 }
 constexpr float kLog2e = 1.4426950408889634f;
 
-// u sigmoid(u), and sigmoid(u), with the fast exponential and division (a few
-// ulp). e^-u overflows to infinity for very negative u, where the quotient is 0.
-__device__ __forceinline__ float sigmoid_fast(float u) { return __fdividef(1.f, 1.f + __expf(-u)); }
-__device__ __forceinline__ float silu_fast(float u) { return __fdividef(u, 1.f + __expf(-u)); }
+// Exponents A2 s of two decays 2^(A2 s). The SFU's 2^x comes out low, by 1.9e-8
+// relative on average over [-0.1, -0.001] (measured; its largest error there is
+// 1.2e-7), and a state of a long memory would gather that mean over every token it
+// remembers: 2e-6 over 100 tokens. The addend takes the mean out; what is left is
+// random and grows with the root of the tokens. The decay of a step of size 0 stays
+// exactly 1 (2^2.7e-8 rounds to it).
+constexpr float kDecayShift = 2.7e-8f;
+__device__ __forceinline__ float2 decay_exponent(float2 s, float2 A2) {
+  return __ffma2_rn(s, A2, make_float2(kDecayShift, kDecayShift));
+}
+// The larger value, or NaN when one is (fmaxf drops it).
+__device__ __forceinline__ float fmax_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// sigmoid(u) and u sigmoid(u) with the SFU's 2^x and reciprocal (a few ulp). Their
+// flushes to zero do no harm: e^-u below 1e-38 next to 1, and 1 / (1 + e^-u) below it.
+// e^-u overflows to infinity for very negative u, where the reciprocal is 0.
+__device__ __forceinline__ float sigmoid_fast(float u) { return rcp_approx(1.f + ex2_approx(-kLog2e * u)); }
+__device__ __forceinline__ float silu_fast(float u) { return u * sigmoid_fast(u); }
+__device__ __forceinline__ float2 silu_fast(float2 u) {
+  const float2 x = __fmul2_rn(u, make_float2(-kLog2e, -kLog2e));
+  const float2 w = __fadd2_rn(make_float2(ex2_approx(x.x), ex2_approx(x.y)), make_float2(1.f, 1.f));
+  return __fmul2_rn(u, make_float2(rcp_approx(w.x), rcp_approx(w.y)));
+}
 
 // softplus(u) = max(u, 0) + log(1 + e), e = e^-|u|. The step sizes of a trained scan
 // are small (0.001 to 0.1, u from -7 to -2), where log(1 + e) has to be accurate
 // relative to itself, which the SFU's logarithm near 1 is not. So
 // log(1 + e) = 2 atanh(r), r = e / (2 + e) <= 1/3, by the series of atanh in r^2 up to
-// r^13: what is left out is below 2e-8 of the sum (r^14 / 15 and on at r = 1/3).
-__device__ __forceinline__ float softplus_fast(float u) {
-  const float e = __expf(-fabsf(u));
-  const float r = __fdividef(e, 2.f + e), q = r * r;
-  float p = 1.f / 13.f;
-  p = fmaf(p, q, 1.f / 11.f);
-  p = fmaf(p, q, 1.f / 9.f);
-  p = fmaf(p, q, 1.f / 7.f);
-  p = fmaf(p, q, 1.f / 5.f);
-  p = fmaf(p, q, 1.f / 3.f);
-  p = fmaf(p, q, 1.f);
-  return fmaf(2.f * r, p, fmaxf(u, 0.f));
+// r^13: what is left out is below 2e-8 of the sum (r^14 / 15 and on at r = 1/3). e is
+// formed as 2^(x + 64) 2^-64, since the SFU's 2^x flushes results below 1e-38 to zero.
+__device__ __forceinline__ float2 softplus_fast(float2 u) {
+  const float2 x = __ffma2_rn(make_float2(fabsf(u.x), fabsf(u.y)), make_float2(-kLog2e, -kLog2e), make_float2(64.f, 64.f));
+  const float2 e = __fmul2_rn(make_float2(ex2_approx(x.x), ex2_approx(x.y)), make_float2(0x1p-64f, 0x1p-64f));
+  const float2 w = __fadd2_rn(e, make_float2(2.f, 2.f));
+  const float2 r = __fmul2_rn(e, make_float2(rcp_approx(w.x), rcp_approx(w.y))), q = __fmul2_rn(r, r);
+  float2 p = make_float2(1.f / 13.f, 1.f / 13.f);
+  p = __ffma2_rn(p, q, make_float2(1.f / 11.f, 1.f / 11.f));
+  p = __ffma2_rn(p, q, make_float2(1.f / 9.f, 1.f / 9.f));
+  p = __ffma2_rn(p, q, make_float2(1.f / 7.f, 1.f / 7.f));
+  p = __ffma2_rn(p, q, make_float2(1.f / 5.f, 1.f / 5.f));
+  p = __ffma2_rn(p, q, make_float2(1.f / 3.f, 1.f / 3.f));
+  p = __ffma2_rn(p, q, make_float2(1.f, 1.f));
+  return __ffma2_rn(__fadd2_rn(r, r), p, make_float2(fmaxf(u.x, 0.f), fmaxf(u.y, 0.f)));
 }
+__device__ __forceinline__ float softplus_fast(float u) { return softplus_fast(make_float2(u, u)).x; }
 
 #endif  // __CUDACC__
 

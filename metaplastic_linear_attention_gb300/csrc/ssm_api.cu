@@ -229,7 +229,7 @@ palimpsa_status palimpsa_selective_scan(const void* x, const void* dt, const flo
   if (palimpsa_status s = scan_checks(a, in_dtype, flags)) return s;
   if (palimpsa_status s = scan_strides(&a, strides, in_dtype)) return s;
   if (palimpsa_status s = device_status_word(&a.status)) return s;
-  if (plan_scan(a, false, &a.nseg, &a.seg_len) != cudaSuccess) return PALIMPSA_ERR_CUDA;
+  if (plan_scan(&a, false) != cudaSuccess) return PALIMPSA_ERR_CUDA;
   const cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
   float* scratch = nullptr;
   if (take_scratch(&a, 0, s, &scratch) != cudaSuccess) return PALIMPSA_ERR_CUDA;
@@ -279,7 +279,7 @@ palimpsa_status palimpsa_selective_scan_backward(
   if (palimpsa_status s = scan_checks(a, in_dtype, flags)) return s;
   if (palimpsa_status s = scan_strides(&a, strides, in_dtype)) return s;
   if (palimpsa_status s = device_status_word(&a.status)) return s;
-  if (plan_scan(a, true, &a.nseg, &a.seg_len) != cudaSuccess) return PALIMPSA_ERR_CUDA;
+  if (plan_scan(&a, true) != cudaSuccess) return PALIMPSA_ERR_CUDA;
   const cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
   float* scratch = nullptr;
   const size_t more = (scan_backward_scratch_floats(a) + 3) / 4 * 4;

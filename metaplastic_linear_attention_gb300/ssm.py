@@ -52,40 +52,45 @@ def _library():
     return _lib
 
 
-def _ptr(t):
-    return None if t is None else t.data_ptr()
+# The checks below run on every decode token, so they are written for speed: a tensor that
+# passes costs a few comparisons, and only a refusal looks at what is wrong.
 
-
-def _dtype(x, name):
-    if x.dtype == torch.bfloat16:
+def _dtype(x):
+    if x.dtype is torch.bfloat16:
         return PALIMPSA_BF16
-    if x.dtype == F32:
+    if x.dtype is F32:
         return PALIMPSA_F32
-    raise TypeError(f"{name} must be bfloat16 or float32, got {x.dtype}")
+    raise TypeError(f"token arrays must be bfloat16 or float32, got {x.dtype}")
+
+
+def _dense(t, name, shape, dtype, dev):
+    """The address of a contiguous tensor of that shape and dtype on CUDA device `dev`, or None of None."""
+    if t is None:
+        return None
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    _check(t, name, shape, dtype, torch.device("cuda", dev))
+    raise ValueError(f"{name}: expected a tensor of {shape} on cuda:{dev}")
 
 
 def _rows(t, name, shape, dtype, dev, lead):
-    """Checks a token array whose first `lead` dimensions count rows; returns its row
-    stride in elements (0: dense)."""
-    if t is None:
+    """Checks a token array whose first `lead` dimensions count rows; returns its row stride in
+    elements (0: dense)."""
+    if t is None or (t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous()):
         return 0
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.dtype != dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    if t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, expected {dev}")
-    if t.is_contiguous():
-        return 0
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, expected device {dev}")
     st, width = t.stride(), 1
     for k in range(len(shape) - 1, lead - 1, -1):
         if shape[k] != 1 and st[k] != width:
             raise ValueError(f"{name}: a row must be contiguous, got strides {st}")
         width *= shape[k]
-    if lead == 1:
-        ld = st[0]
-    elif shape[1] == 1:
-        ld = st[0]
+    if lead == 1 or shape[1] == 1:
+        ld = st[0] if shape[0] != 1 else width
     else:
         ld = st[1]
         if shape[0] != 1 and st[0] != shape[1] * ld:
@@ -95,32 +100,37 @@ def _rows(t, name, shape, dtype, dev, lead):
     return ld
 
 
-class _Call:
-    """The device and stream of one call: the tensors' device, the caller's stream or
-    the current one. Tensors used on a stream other than the current one are recorded
-    there, so that the allocator keeps them until that stream is done."""
+def _ptr(t):
+    return None if t is None else t.data_ptr()
 
-    def __init__(self, x, name, stream):
-        if not x.is_cuda:
-            raise ValueError(f"{name} takes device tensors")
-        self.dev, self.stream, self.name = x.device, stream, name
 
-    def __call__(self, fn, tensors, *args):
-        if self.dev.index == torch.cuda.current_device():
-            rc = self._run(fn, tensors, args)
-        else:
-            with torch.cuda.device(self.dev):
-                rc = self._run(fn, tensors, args)
-        if rc != 0:
-            raise PalimpsaError(rc, self.name)
+def _device(x, name):
+    dev = x.get_device()
+    if dev < 0:
+        raise ValueError(f"{name} takes device tensors")
+    return dev
 
-    def _run(self, fn, tensors, args):
-        rc = fn(*args, binding._stream_handle(self.stream))
-        if self.stream is not None:
+
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else (
+    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
+def _call(name, dev, stream, tensors, *args):
+    """The library call on the tensors' device, on the caller's stream or the current one. Tensors
+    used on a caller's stream are recorded there, so that the allocator keeps them until that
+    stream is done."""
+    fn = getattr(_library(), name)
+    if stream is None and dev == torch.cuda.current_device():
+        rc = fn(*args, _raw_stream(dev))
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, binding._stream_handle(stream))
+        if stream is not None:
             for t in tensors:
                 if t is not None:
-                    t.record_stream(self.stream)
-        return rc
+                    t.record_stream(stream)
+    if rc != 0:
+        raise PalimpsaError(rc, name)
 
 
 def _batch(x, cu_seqlens, max_seqlen, dev, stream, name):
@@ -131,15 +141,16 @@ def _batch(x, cu_seqlens, max_seqlen, dev, stream, name):
         return x.shape[0], x.shape[1], x.shape[1], None, 2
     if x.dim() != 2:
         raise ValueError(f"{name}: packed x must be [rows, D], got {tuple(x.shape)}")
-    cu, n, longest = _packed_offsets(cu_seqlens, max_seqlen, dev, stream)
+    cu, n, longest = _packed_offsets(cu_seqlens, max_seqlen, x.device, stream)
     return n, x.shape[0], longest, cu, 1
 
 
-def _new(t, name, shape, dtype, dev, zero=False):
-    """An output: checked when given, else allocated (zeroed where rows may stay unwritten)."""
+def _new(t, name, shape, dtype, x, zero=False):
+    """An output on x's device: checked when given, else allocated (zeroed where rows may stay
+    unwritten)."""
     if t is None:
-        return (torch.zeros if zero else torch.empty)(shape, dtype=dtype, device=dev)
-    _check(t, name, shape, dtype, dev)
+        return (torch.zeros if zero else torch.empty)(shape, dtype=dtype, device=x.device)
+    _dense(t, name, shape, dtype, x.get_device())
     return t
 
 
@@ -147,9 +158,7 @@ def _new(t, name, shape, dtype, dev, zero=False):
 
 def _conv_params(x, weight, bias, dev):
     D, W = x.shape[-1], weight.shape[-1]
-    _check(weight, "weight", (D, W), F32, dev)
-    _check(bias, "bias", (D,), F32, dev)
-    return D, W
+    return D, W, _dense(weight, "weight", (D, W), F32, dev), _dense(bias, "bias", (D,), F32, dev)
 
 
 def palimpsa_causal_conv(x, weight, bias=None, state0=None, *, silu=True, cu_seqlens=None, max_seqlen=None, y=None,
@@ -161,17 +170,17 @@ def palimpsa_causal_conv(x, weight, bias=None, state0=None, *, silu=True, cu_seq
     bias [D] fp32; state0 [B, W - 1, D]: the inputs before each sequence, or None for
     zeros. Returns (y, state_T), both in x's dtype; state_T may be given as state0."""
     name = "palimpsa_causal_conv"
-    call = _Call(x, name, stream)
-    dev = x.device
+    dev = _device(x, name)
     B, T, longest, cu, lead = _batch(x, cu_seqlens, max_seqlen, dev, stream, name)
-    D, W = _conv_params(x, weight, bias, dev)
-    ld = _rows(x, "x", tuple(x.shape), x.dtype, dev, lead)
-    _check(state0, "state0", (B, W - 1, D), x.dtype, dev)
-    y = _new(y, "y", tuple(x.shape), x.dtype, dev, cu is not None)
-    state_T = _new(state_T, "state_T", (B, W - 1, D), x.dtype, dev)
-    call(_library().palimpsa_causal_conv, (x, weight, bias, state0, y, state_T, cu),
-         _ptr(x), ld, _ptr(weight), _ptr(bias), _ptr(state0), _ptr(y), _ptr(state_T), _ptr(cu), B, T, longest, D, W,
-         PALIMPSA_CONV_SILU if silu else 0, _dtype(x, "x"))
+    D, W, pw, pb = _conv_params(x, weight, bias, dev)
+    kind = _dtype(x)
+    ld = _rows(x, "x", x.shape, x.dtype, dev, lead)
+    ps = _dense(state0, "state0", (B, W - 1, D), x.dtype, dev)
+    y = _new(y, "y", x.shape, x.dtype, x, cu is not None)
+    state_T = _new(state_T, "state_T", (B, W - 1, D), x.dtype, x)
+    _call(name, dev, stream, (x, weight, bias, state0, y, state_T, cu),
+          x.data_ptr(), ld, pw, pb, ps, y.data_ptr(), state_T.data_ptr(), _ptr(cu), B, T, longest, D, W,
+          PALIMPSA_CONV_SILU if silu else 0, kind)
     return y, state_T
 
 
@@ -179,18 +188,16 @@ def palimpsa_causal_conv_step(x, weight, bias, state, *, silu=True, y=None, stre
     """One token of the convolution (see palimpsa.h): x [B, D], state [B, W - 1, D] updated in
     place. Returns y [B, D]."""
     name = "palimpsa_causal_conv_step"
-    call = _Call(x, name, stream)
-    dev = x.device
+    dev = _device(x, name)
     if x.dim() != 2:
         raise ValueError(f"{name}: x must be [B, D], got {tuple(x.shape)}")
-    B = x.shape[0]
-    D, W = _conv_params(x, weight, bias, dev)
-    ld = _rows(x, "x", (B, D), x.dtype, dev, 1)
-    _check(state, "state", (B, W - 1, D), x.dtype, dev)
-    y = _new(y, "y", (B, D), x.dtype, dev)
-    call(_library().palimpsa_causal_conv_step, (x, weight, bias, state, y),
-         _ptr(x), ld, _ptr(weight), _ptr(bias), _ptr(state), _ptr(y), B, D, W, PALIMPSA_CONV_SILU if silu else 0,
-         _dtype(x, "x"))
+    D, W, pw, pb = _conv_params(x, weight, bias, dev)
+    B, kind = x.shape[0], _dtype(x)
+    ld = _rows(x, "x", x.shape, x.dtype, dev, 1)
+    ps = _dense(state, "state", (B, W - 1, D), x.dtype, dev)
+    y = _new(y, "y", x.shape, x.dtype, x)
+    _call(name, dev, stream, (x, weight, bias, state, y),
+          x.data_ptr(), ld, pw, pb, ps, y.data_ptr(), B, D, W, PALIMPSA_CONV_SILU if silu else 0, kind)
     return y
 
 
@@ -200,43 +207,43 @@ def palimpsa_causal_conv_backward(x, weight, bias, state0, dy, dstate_T=None, *,
     in rows outside every sequence), dweight [D, W], dbias [D] (fp32), and dstate0
     [B, W - 1, D] (x's dtype) when want_state_grad."""
     name = "palimpsa_causal_conv_backward"
-    call = _Call(x, name, stream)
-    dev = x.device
+    dev = _device(x, name)
     B, T, longest, cu, lead = _batch(x, cu_seqlens, max_seqlen, dev, stream, name)
-    D, W = _conv_params(x, weight, bias, dev)
-    ld = _rows(x, "x", tuple(x.shape), x.dtype, dev, lead)
-    ldy = _rows(dy, "dy", tuple(x.shape), x.dtype, dev, lead)
-    _check(state0, "state0", (B, W - 1, D), x.dtype, dev)
-    _check(dstate_T, "dstate_T", (B, W - 1, D), x.dtype, dev)
-    g = {"dx": _new(None, "dx", tuple(x.shape), x.dtype, dev, cu is not None),
-         "dweight": _new(None, "dweight", (D, W), F32, dev), "dbias": _new(None, "dbias", (D,), F32, dev)}
+    D, W, pw, pb = _conv_params(x, weight, bias, dev)
+    kind, dtype = _dtype(x), x.dtype
+    ld = _rows(x, "x", x.shape, dtype, dev, lead)
+    ldy = _rows(dy, "dy", x.shape, dtype, dev, lead)
+    ps = _dense(state0, "state0", (B, W - 1, D), dtype, dev)
+    pd = _dense(dstate_T, "dstate_T", (B, W - 1, D), dtype, dev)
+    # rows outside every sequence, and a sequence that is skipped for its offsets, stay zero
+    g = {"dx": _new(None, "dx", x.shape, dtype, x, cu is not None),
+         "dweight": _new(None, "dweight", (D, W), F32, x), "dbias": _new(None, "dbias", (D,), F32, x)}
     if want_state_grad:
-        # a sequence that is skipped for its offsets leaves its rows as they are
-        g["dstate0"] = _new(None, "dstate0", (B, W - 1, D), x.dtype, dev, cu is not None)
-    call(_library().palimpsa_causal_conv_backward, (x, weight, bias, state0, dy, dstate_T, cu, *g.values()),
-         _ptr(x), ld, _ptr(weight), _ptr(bias), _ptr(state0), _ptr(dy), ldy, _ptr(dstate_T), _ptr(g["dx"]),
-         _ptr(g["dweight"]), _ptr(g["dbias"]), _ptr(g.get("dstate0")), _ptr(cu), B, T, longest, D, W,
-         PALIMPSA_CONV_SILU if silu else 0, _dtype(x, "x"))
+        g["dstate0"] = _new(None, "dstate0", (B, W - 1, D), dtype, x, cu is not None)
+    _call(name, dev, stream, (x, weight, bias, state0, dy, dstate_T, cu, *g.values()),
+          x.data_ptr(), ld, pw, pb, ps, dy.data_ptr(), ldy, pd, g["dx"].data_ptr(), g["dweight"].data_ptr(),
+          g["dbias"].data_ptr(), _ptr(g.get("dstate0")), _ptr(cu), B, T, longest, D, W,
+          PALIMPSA_CONV_SILU if silu else 0, kind)
     return g
 
 
 # ------------------------------------------------------------------ selective scan
 
-def _scan_inputs(x, dt, A, B, C, D, z, dt_bias, lead, dy=None):
-    """Checks the scan's inputs; returns (channels, groups, states, strides or None)."""
-    dev, kind, shape = x.device, x.dtype, tuple(x.shape)
+def _scan_inputs(x, dt, A, B, C, D, z, dt_bias, dev, lead, dy=None):
+    """Checks the scan's inputs; returns (channels, groups, states, strides or None, the addresses
+    of x, dt, A, B, C, D, z, dt_bias)."""
+    kind, shape = x.dtype, x.shape
     if A.dim() != 2 or B.dim() != lead + 2:
         raise ValueError(f"A must be [D, N] and B [..., G, N], got {tuple(A.shape)} and {tuple(B.shape)}")
     ch, n = A.shape
     groups = B.shape[-2]
     bc = shape[:-1] + (groups, n)
-    ld = [_rows(x, "x", shape[:-1] + (ch,), kind, dev, lead), _rows(dt, "dt", shape, kind, dev, lead),
-          _rows(B, "B", bc, kind, dev, lead), _rows(C, "C", bc, kind, dev, lead), _rows(z, "z", shape, kind, dev, lead),
-          _rows(dy, "dy", shape, kind, dev, lead)]
-    _check(A, "A", (ch, n), F32, dev)
-    _check(D, "D", (ch,), F32, dev)
-    _check(dt_bias, "dt_bias", (ch,), F32, dev)
-    return ch, groups, n, ctypes.byref(_Strides(*ld)) if any(ld) else None
+    ld = (_rows(x, "x", shape[:-1] + (ch,), kind, dev, lead), _rows(dt, "dt", shape, kind, dev, lead),
+          _rows(B, "B", bc, kind, dev, lead), _rows(C, "C", bc, kind, dev, lead),
+          _rows(z, "z", shape, kind, dev, lead), _rows(dy, "dy", shape, kind, dev, lead))
+    ptrs = (x.data_ptr(), dt.data_ptr(), _dense(A, "A", (ch, n), F32, dev), B.data_ptr(), C.data_ptr(),
+            _dense(D, "D", (ch,), F32, dev), _ptr(z), _dense(dt_bias, "dt_bias", (ch,), F32, dev))
+    return ch, groups, n, ctypes.byref(_Strides(*ld)) if any(ld) else None, ptrs
 
 
 def palimpsa_selective_scan_checkpoint_shape(batch, tokens, channels, states, packed=False):
@@ -248,19 +255,18 @@ def palimpsa_selective_scan_checkpoint_shape(batch, tokens, channels, states, pa
 
 
 def _scan(name, x, dt, A, B, C, D, z, dt_bias, h0, softplus, cu_seqlens, max_seqlen, y, h_T, want_ckpt, ckpt, stream):
-    call = _Call(x, name, stream)
-    dev = x.device
+    dev = _device(x, name)
     nb, T, longest, cu, lead = _batch(x, cu_seqlens, max_seqlen, dev, stream, name)
-    ch, groups, n, strides = _scan_inputs(x, dt, A, B, C, D, z, dt_bias, lead)
-    _check(h0, "h0", (nb, ch, n), F32, dev)
-    y = _new(y, "y", tuple(x.shape), x.dtype, dev, cu is not None)
-    h_T = _new(h_T, "h_T", (nb, ch, n), F32, dev)
+    ch, groups, n, strides, ptrs = _scan_inputs(x, dt, A, B, C, D, z, dt_bias, dev, lead)
+    kind = _dtype(x)
+    p0 = _dense(h0, "h0", (nb, ch, n), F32, dev)
+    y = _new(y, "y", x.shape, x.dtype, x, cu is not None)
+    h_T = _new(h_T, "h_T", (nb, ch, n), F32, x)
     if want_ckpt:
-        ckpt = _new(ckpt, "ckpt", palimpsa_selective_scan_checkpoint_shape(nb, T, ch, n, cu is not None), F32, dev)
-    call(_library().palimpsa_selective_scan, (x, dt, A, B, C, D, z, dt_bias, h0, y, h_T, ckpt, cu),
-         _ptr(x), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(z), _ptr(dt_bias), _ptr(h0), _ptr(y), _ptr(h_T),
-         _ptr(ckpt), strides, _ptr(cu), nb, T, longest, ch, groups, n, PALIMPSA_SCAN_SOFTPLUS if softplus else 0,
-         _dtype(x, "x"))
+        ckpt = _new(ckpt, "ckpt", palimpsa_selective_scan_checkpoint_shape(nb, T, ch, n, cu is not None), F32, x)
+    _call(name, dev, stream, (x, dt, A, B, C, D, z, dt_bias, h0, y, h_T, ckpt, cu),
+          *ptrs, p0, y.data_ptr(), h_T.data_ptr(), _ptr(ckpt), strides, _ptr(cu), nb, T, longest, ch, groups, n,
+          PALIMPSA_SCAN_SOFTPLUS if softplus else 0, kind)
     return y, h_T, ckpt
 
 
@@ -292,33 +298,29 @@ def palimpsa_selective_scan_backward(x, dt, A, B, C, D, z, dt_bias, h0, ckpt, dy
     (with D), ddt_bias (with dt_bias) fp32, and dh0 [B, D, N] fp32 when want_state_grad. Rows
     outside every sequence are zero."""
     name = "palimpsa_selective_scan_backward"
-    call = _Call(x, name, stream)
-    dev, kind = x.device, x.dtype
+    dev = _device(x, name)
     nb, T, longest, cu, lead = _batch(x, cu_seqlens, max_seqlen, dev, stream, name)
-    ch, groups, n, strides = _scan_inputs(x, dt, A, B, C, D, z, dt_bias, lead, dy)
-    _check(h0, "h0", (nb, ch, n), F32, dev)
-    _check(dh_T, "dh_T", (nb, ch, n), F32, dev)
-    _check(ckpt, "ckpt", palimpsa_selective_scan_checkpoint_shape(nb, T, ch, n, cu is not None), F32, dev)
-    packed = cu is not None
-    g = {"dx": _new(None, "dx", tuple(x.shape), kind, dev, packed),
-         "ddt": _new(None, "ddt", tuple(x.shape), kind, dev, packed),
-         "dA": _new(None, "dA", (ch, n), F32, dev),
-         "dB": _new(None, "dB", tuple(B.shape), kind, dev, packed),
-         "dC": _new(None, "dC", tuple(B.shape), kind, dev, packed)}
+    ch, groups, n, strides, ptrs = _scan_inputs(x, dt, A, B, C, D, z, dt_bias, dev, lead, dy)
+    kind, dtype, packed = _dtype(x), x.dtype, cu is not None
+    _dense(h0, "h0", (nb, ch, n), F32, dev)
+    pg = _dense(dh_T, "dh_T", (nb, ch, n), F32, dev)
+    pc = _dense(ckpt, "ckpt", palimpsa_selective_scan_checkpoint_shape(nb, T, ch, n, packed), F32, dev)
+    g = {"dx": _new(None, "dx", x.shape, dtype, x, packed), "ddt": _new(None, "ddt", x.shape, dtype, x, packed),
+         "dA": _new(None, "dA", (ch, n), F32, x), "dB": _new(None, "dB", B.shape, dtype, x, packed),
+         "dC": _new(None, "dC", B.shape, dtype, x, packed)}
     if D is not None:
-        g["dD"] = _new(None, "dD", (ch,), F32, dev)
+        g["dD"] = _new(None, "dD", (ch,), F32, x)
     if z is not None:
-        g["dz"] = _new(None, "dz", tuple(x.shape), kind, dev, packed)
+        g["dz"] = _new(None, "dz", x.shape, dtype, x, packed)
     if dt_bias is not None:
-        g["ddt_bias"] = _new(None, "ddt_bias", (ch,), F32, dev)
+        g["ddt_bias"] = _new(None, "ddt_bias", (ch,), F32, x)
     if want_state_grad:
-        g["dh0"] = _new(None, "dh0", (nb, ch, n), F32, dev, packed)
-    call(_library().palimpsa_selective_scan_backward,
-         (x, dt, A, B, C, D, z, dt_bias, ckpt, dy, dh_T, cu, *g.values()),
-         _ptr(x), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(z), _ptr(dt_bias), _ptr(ckpt), _ptr(dy),
-         _ptr(dh_T), _ptr(g["dx"]), _ptr(g["ddt"]), _ptr(g["dA"]), _ptr(g["dB"]), _ptr(g["dC"]), _ptr(g.get("dD")),
-         _ptr(g.get("dz")), _ptr(g.get("ddt_bias")), _ptr(g.get("dh0")), strides, _ptr(cu), nb, T, longest, ch, groups,
-         n, PALIMPSA_SCAN_SOFTPLUS if softplus else 0, _dtype(x, "x"))
+        g["dh0"] = _new(None, "dh0", (nb, ch, n), F32, x, packed)
+    at = {k: v.data_ptr() for k, v in g.items()}
+    _call(name, dev, stream, (x, dt, A, B, C, D, z, dt_bias, ckpt, dy, dh_T, cu, *g.values()),
+          *ptrs, pc, dy.data_ptr(), pg, at["dx"], at["ddt"], at["dA"], at["dB"], at["dC"], at.get("dD"), at.get("dz"),
+          at.get("ddt_bias"), at.get("dh0"), strides, _ptr(cu), nb, T, longest, ch, groups, n,
+          PALIMPSA_SCAN_SOFTPLUS if softplus else 0, kind)
     return g
 
 
@@ -327,15 +329,13 @@ def palimpsa_selective_scan_step(x, dt, A, B, C, h, D=None, z=None, dt_bias=None
     """One token of the selective scan (see palimpsa.h): x, dt, z [B, D], B and C [B, G, N], h
     [B, D, N] fp32 updated in place. Returns y [B, D]."""
     name = "palimpsa_selective_scan_step"
-    call = _Call(x, name, stream)
-    dev = x.device
+    dev = _device(x, name)
     if x.dim() != 2:
         raise ValueError(f"{name}: x must be [B, D], got {tuple(x.shape)}")
-    nb = x.shape[0]
-    ch, groups, n, strides = _scan_inputs(x, dt, A, B, C, D, z, dt_bias, 1)
-    _check(h, "h", (nb, ch, n), F32, dev)
-    y = _new(y, "y", (nb, ch), x.dtype, dev)
-    call(_library().palimpsa_selective_scan_step, (x, dt, A, B, C, D, z, dt_bias, h, y),
-         _ptr(x), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(z), _ptr(dt_bias), _ptr(h), _ptr(y), strides, nb,
-         ch, groups, n, PALIMPSA_SCAN_SOFTPLUS if softplus else 0, _dtype(x, "x"))
+    ch, groups, n, strides, ptrs = _scan_inputs(x, dt, A, B, C, D, z, dt_bias, dev, 1)
+    kind, nb = _dtype(x), x.shape[0]
+    ph = _dense(h, "h", (nb, ch, n), F32, dev)
+    y = _new(y, "y", x.shape, x.dtype, x)
+    _call(name, dev, stream, (x, dt, A, B, C, D, z, dt_bias, h, y),
+          *ptrs, ph, y.data_ptr(), strides, nb, ch, groups, n, PALIMPSA_SCAN_SOFTPLUS if softplus else 0, kind)
     return y
