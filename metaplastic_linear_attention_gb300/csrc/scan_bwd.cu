@@ -29,6 +29,7 @@
 // fixed order: no atomics, the same bits every time. All sums are fp32; gradients
 // of token arrays are rounded to the input type once.
 #include <algorithm>
+#include <atomic>
 
 #include "ssm.cuh"
 
@@ -37,31 +38,35 @@ namespace {
 
 constexpr int kChunk = kScanCheckpoint;
 constexpr int kWin = 4;
+constexpr int kWins = kChunk / kWin;
 constexpr int kStages = 2;
 constexpr int CH = kScanChannels;
 
+// Shared memory of a CTA, bytes (all parts 16-byte aligned).
 struct Smem {
-  int rx, rdt, rz, rdy, rB, rC, rck, raw;
-  int s, sx, dp, B, C, sub, sum, par, total;
-  __host__ __device__ Smem(int N, int W, int es) {
-    const int row = kChunk * CH * es;
-    rx = 0;
-    rdt = rx + row;
-    rz = rdt + row;
-    rdy = rz + row;
-    rB = rdy + row;
-    rC = rB + kChunk * N * es;
-    rck = rC + kChunk * N * es;
-    raw = rck + CH * N * 4;
-    s = kStages * raw;
-    sx = s + kChunk * CH * 4;
-    dp = sx + kChunk * CH * 4;
-    B = dp + kChunk * CH * 4;
-    C = B + kChunk * N * 4;
-    sub = C + kChunk * N * 4;
-    sum = sub + (kChunk / kWin - 1) * CH * N * 4;
-    par = sum + 3 * W * kChunk * CH * 4;
-    total = par + 2 * CH * 4;
+  int rx, rdt, rz, rdy, rB, rC, rck, raw;  // one stage of raw inputs and a checkpoint
+  int s, sx, dp;                           // fp32 operands
+  int win;                                 // per warp and window: a state, then the window's sums
+  int acc, par, total;
+  __host__ __device__ constexpr Smem(int N, int W, int es)
+      : rx(0),
+        rdt(kChunk * CH * es),
+        rz(2 * kChunk * CH * es),
+        rdy(3 * kChunk * CH * es),
+        rB(4 * kChunk * CH * es),
+        rC(rB + kChunk * N * es),
+        rck(rC + kChunk * N * es),
+        raw(rck + CH * N * 4),
+        s(kStages * raw),
+        sx(s + kChunk * CH * 4),
+        dp(sx + kChunk * CH * 4),
+        win(dp + kChunk * CH * 4),
+        acc(win + kWins * W * slot(N, W)),
+        par(acc + 32 * W * 16 * 4),
+        total(par + 2 * CH * 4) {}
+  // Bytes of a warp's slot: 16 or 8 states a lane, or 3 sums of 4 tokens of 32 channels.
+  static __host__ __device__ constexpr int slot(int N, int W) {
+    return CH * N / W * 4 > 3 * kWin * CH * 4 ? CH * N / W * 4 : 3 * kWin * CH * 4;
   }
 };
 
@@ -72,32 +77,51 @@ struct Partials {  // parts of the backward's scratch
   float* par;  // [n_seq, nseg, 2, D]: dskip, ddt_bias
 };
 
-// Sum over the 4 lane groups of 4 channels' values: lane (cl, sl) ends with
-// channel 4 cl + sl.
-__device__ __forceinline__ float scatter_groups(const float* y, int sl) {
-  const bool hi = sl & 2, odd = sl & 1;
-  const float k0 = hi ? y[2] : y[0], k1 = hi ? y[3] : y[1];
-  const float r0 = k0 + __shfl_xor_sync(0xffffffffu, hi ? y[0] : y[2], 16);
-  const float r1 = k1 + __shfl_xor_sync(0xffffffffu, hi ? y[1] : y[3], 16);
-  return (odd ? r1 : r0) + __shfl_xor_sync(0xffffffffu, odd ? r0 : r1, 8);
+// NS values of a row of B or C as they came, each twice (for two channels).
+template <bool BF16, int NS>
+__device__ __forceinline__ void load_states(float2* f, const unsigned char* p) {
+  float v[NS];
+  if constexpr (BF16 && NS == 4) {
+    const uint2 u = *reinterpret_cast<const uint2*>(p);
+    v[0] = bf16_lo(u.x); v[1] = bf16_hi(u.x); v[2] = bf16_lo(u.y); v[3] = bf16_hi(u.y);
+  } else if constexpr (BF16) {
+    const uint32_t u = *reinterpret_cast<const uint32_t*>(p);
+    v[0] = bf16_lo(u); v[1] = bf16_hi(u);
+  } else if constexpr (NS == 4) {
+    const float4 u = *reinterpret_cast<const float4*>(p);
+    v[0] = u.x; v[1] = u.y; v[2] = u.z; v[3] = u.w;
+  } else {
+    const float2 u = *reinterpret_cast<const float2*>(p);
+    v[0] = u.x; v[1] = u.y;
+  }
+#pragma unroll
+  for (int j = 0; j < NS; ++j) f[j] = make_float2(v[j], v[j]);
+}
+__device__ __forceinline__ void load_pairs(float2* f, const float* p) {
+  const float4 v = *reinterpret_cast<const float4*>(p);
+  f[0] = make_float2(v.x, v.y);
+  f[1] = make_float2(v.z, v.w);
+}
+// The kept half of two vectors plus the partner's copy of it (the partner keeps the other).
+template <int M>
+__device__ __forceinline__ void halve(float* out, const float* a, const float* b, bool second, int lane_mask) {
+#pragma unroll
+  for (int k = 0; k < M; ++k)
+    out[k] = (second ? b[k] : a[k]) + __shfl_xor_sync(0xffffffffu, second ? a[k] : b[k], lane_mask);
 }
 
-template <bool BF16, int NS>
-__global__ void __launch_bounds__(256) palimpsa_scan_bwd_kernel(ScanArgs a, Partials part, int tiles, int W) {
+template <bool BF16, int NS, int W>
+__global__ void __launch_bounds__(32 * W) palimpsa_scan_bwd_kernel(ScanArgs a, Partials part, int tiles) {
   using V = Vec<BF16>;
-  constexpr int VN = V::n, ES = V::bytes, NP = NS / 2;
-  constexpr int VPR = CH / VN;
-  const int N = 4 * NS * W, NT = 32 * W, BPR = N / VN;
+  constexpr int VN = V::n, ES = V::bytes, N = 4 * NS * W, NT = 32 * W;
+  constexpr int VPR = CH / VN, BPR = N / VN;
+  constexpr Smem L(N, W, ES);
   extern __shared__ __align__(128) unsigned char smem[];
-  const Smem L(N, W, ES);
   float* const fs = reinterpret_cast<float*>(smem + L.s);
   float* const fsx = reinterpret_cast<float*>(smem + L.sx);
   float* const fdp = reinterpret_cast<float*>(smem + L.dp);
-  float* const fB = reinterpret_cast<float*>(smem + L.B);
-  float* const fC = reinterpret_cast<float*>(smem + L.C);
-  float* const fsum = reinterpret_cast<float*>(smem + L.sum);
-  float* const fbias = reinterpret_cast<float*>(smem + L.par);
-  float* const fskip = fbias + CH;
+  float4* const facc = reinterpret_cast<float4*>(smem + L.acc) + threadIdx.x;
+  float* const fpar = reinterpret_cast<float*>(smem + L.par);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int tile = (int)(blockIdx.x % tiles);
@@ -107,7 +131,6 @@ __global__ void __launch_bounds__(256) palimpsa_scan_bwd_kernel(ScanArgs a, Part
   const int per_group = a.D / a.G, tpg = (per_group + CH - 1) / CH;
   const int g = tile / tpg, ch0 = g * per_group + (tile % tpg) * CH;
   const int nch = min(CH, (g + 1) * per_group - ch0);
-  const int nv = nch / VN;
   long long row0;
   int len;
   if (!seq_rows(a.rows, n, &row0, &len)) {
@@ -118,106 +141,118 @@ __global__ void __launch_bounds__(256) palimpsa_scan_bwd_kernel(ScanArgs a, Part
   if (tb >= len && seg > 0) return;
   const int tn = te - tb, nchunk = (tn + kChunk - 1) / kChunk;
 
-  const int cl = lane & 7, sl = lane >> 3;
-  const int n0 = warp * 4 * NS + sl * NS;
+  // A lane's channels 4 cl .. 4 cl + 3 of the tile, as two pairs, and its states from n0
+  // on. Quads of 4 channels of odd tokens change places in pairs in shared memory, as in
+  // the forward.
+  const int cl = lane & 7, sl = lane >> 3, n0 = (warp * 4 + sl) * NS;
+  const int cq0 = 4 * cl, cq1 = 4 * (cl ^ 1);
+  const size_t at = (size_t)(ch0 + 4 * cl) * N + n0;  // of the first channel in [D, N]
   bool bad = false;
-  float2 A2[4][NP], gh[4][NP], dA[4][NP];
+  float2 A2[2][NS], gh[2][NS], dA[2][NS];
+  const float* g0 = nullptr;
+  if (a.nseg > 1) g0 = a.seg_state + (size_t)(n * a.nseg + seg) * a.D * N;
+  else if (a.dh_T) g0 = a.dh_T + (size_t)n * a.D * N;
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
-    const int d = 4 * cl + c;
-    const bool in = d < nch;
-    const float* g0 = nullptr;
-    if (in) {
-      if (a.nseg > 1) g0 = a.seg_state + ((size_t)(n * a.nseg + seg) * a.D + ch0 + d) * N + n0;
-      else if (a.dh_T) g0 = a.dh_T + ((size_t)n * a.D + ch0 + d) * N + n0;
-    }
+    const bool in = 4 * cl + c < nch;
 #pragma unroll
-    for (int p = 0; p < NP; ++p) {
-      const float2 v = in ? *reinterpret_cast<const float2*>(a.A + (size_t)(ch0 + d) * N + n0 + 2 * p)
-                          : make_float2(1.f, 1.f);
-      bad |= !(pos_finite(v.x) && pos_finite(v.y));
-      A2[c][p] = make_float2(-kLog2e * v.x, -kLog2e * v.y);
-      gh[c][p] = g0 ? *reinterpret_cast<const float2*>(g0 + 2 * p) : make_float2(0.f, 0.f);
-      dA[c][p] = make_float2(0.f, 0.f);
+    for (int j = 0; j < NS; ++j) {
+      const float A = in ? a.A[at + c * N + j] : 1.f;
+      bad |= !pos_finite(A);
+      (c & 1 ? A2[c / 2][j].y : A2[c / 2][j].x) = -kLog2e * A;
+      (c & 1 ? gh[c / 2][j].y : gh[c / 2][j].x) = in && g0 ? g0[at + c * N + j] : 0.f;
+      dA[c / 2][j] = make_float2(0.f, 0.f);
     }
   }
   for (int c = tid; c < CH; c += NT) {
-    fbias[c] = c < nch && a.dt_bias ? a.dt_bias[ch0 + c] : 0.f;
-    fskip[c] = c < nch && a.skip ? a.skip[ch0 + c] : 0.f;
+    fpar[c] = c < nch && a.dt_bias ? a.dt_bias[ch0 + c] : 0.f;
+    fpar[CH + c] = c < nch && a.skip ? a.skip[ch0 + c] : 0.f;
   }
+  // Sums over tokens of dskip and ddt_bias of the channels that a thread stores: 2 VN
+  // floats, each thread's own.
+#pragma unroll
+  for (int k = 0; k < VN / 2; ++k) facc[k * NT] = make_float4(0.f, 0.f, 0.f, 0.f);
 
+  // Copies, from the last chunk to the first. A thread copies in, converts and finishes
+  // the same vectors; their place v in a row is the same for all of them.
   const long long rb = row0 + tb;
-  const char* const gx = static_cast<const char*>(a.x) + (rb * a.x_ld + ch0) * ES;
-  const char* const gdt = static_cast<const char*>(a.dt) + (rb * a.dt_ld + ch0) * ES;
-  const char* const gz = a.z ? static_cast<const char*>(a.z) + (rb * a.z_ld + ch0) * ES : nullptr;
-  const char* const gdy = static_cast<const char*>(a.dy) + (rb * a.dy_ld + ch0) * ES;
+  const int v = tid % VPR;
+  const bool vin = v * VN < nch, gated = a.z != nullptr;
+  const char* const gx = static_cast<const char*>(a.x) + (rb * a.x_ld + ch0) * ES + v * 16;
+  const char* const gdt = static_cast<const char*>(a.dt) + (rb * a.dt_ld + ch0) * ES + v * 16;
+  const char* const gz = gated ? static_cast<const char*>(a.z) + (rb * a.z_ld + ch0) * ES + v * 16 : nullptr;
+  const char* const gdy = static_cast<const char*>(a.dy) + (rb * a.dy_ld + ch0) * ES + v * 16;
   const char* const gB = static_cast<const char*>(a.B) + (rb * a.B_ld + g * N) * ES;
   const char* const gC = static_cast<const char*>(a.C) + (rb * a.C_ld + g * N) * ES;
   const float* const gck =
-      a.ckpt_in + ((scan_ckpt_row0(a.rows, n, row0) + tb / kScanCheckpoint) * a.D + ch0) * N;
+      a.ckpt_in + (scan_ckpt_row0(a.rows, n, row0) + tb / kScanCheckpoint) * a.D * N + at;
   auto stage = [&](int c) {  // copies of the c-th chunk from the end, as one group
     if (c < nchunk) {
       unsigned char* const st = smem + (c % kStages) * L.raw;
       const int ci = nchunk - 1 - c, t0 = ci * kChunk, nt = min(kChunk, tn - t0);
+#pragma unroll
       for (int i = tid; i < kChunk * VPR; i += NT) {
-        const int t = i / VPR, v = i % VPR;
-        if (t >= nt || v >= nv) continue;
-        const int o = (t * CH + v * VN) * ES;
-        const long long r = t0 + t, b = (long long)v * 16;
-        cp_async16(st + L.rx + o, gx + r * a.x_ld * ES + b);
-        cp_async16(st + L.rdt + o, gdt + r * a.dt_ld * ES + b);
-        if (gz) cp_async16(st + L.rz + o, gz + r * a.z_ld * ES + b);
-        cp_async16(st + L.rdy + o, gdy + r * a.dy_ld * ES + b);
+        const int t = i / VPR;
+        if (t >= nt || !vin) continue;
+        const long long r = (long long)(t0 + t) * ES;
+        cp_async16(st + L.rx + 16 * i, gx + r * a.x_ld);
+        cp_async16(st + L.rdt + 16 * i, gdt + r * a.dt_ld);
+        if (gated) cp_async16(st + L.rz + 16 * i, gz + r * a.z_ld);
+        cp_async16(st + L.rdy + 16 * i, gdy + r * a.dy_ld);
       }
+#pragma unroll
       for (int i = tid; i < kChunk * BPR; i += NT) {
-        const int t = i / BPR, v = i % BPR;
-        if (t >= nt) continue;
-        const int o = (t * N + v * VN) * ES;
-        const long long r = t0 + t, b = (long long)v * 16;
-        cp_async16(st + L.rB + o, gB + r * a.B_ld * ES + b);
-        cp_async16(st + L.rC + o, gC + r * a.C_ld * ES + b);
+        const int t = i / BPR, o = i % BPR * 16;
+        const long long r = (long long)(t0 + min(t, nt - 1)) * ES;
+        cp_async16(st + L.rB + 16 * i, gB + r * a.B_ld + o, t < nt);
+        cp_async16(st + L.rC + 16 * i, gC + r * a.C_ld + o, t < nt);
       }
+      // each lane its own part of the checkpoint
       const float* const ck = gck + (long long)ci * a.D * N;
-      for (int i = tid; i < nch * N / 4; i += NT) cp_async16(st + L.rck + 16 * i, ck + 4 * i);
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (4 * cl + k < nch) cp_async_states<NS>(st + L.rck + (k * NT + tid) * NS * 4, ck + k * N);
     }
     cp_async_commit();
   };
   stage(0);
 
-  // Sums over tokens of the channels that a thread stores (its vector's place in
-  // the row never changes: the threads are a multiple of the vectors).
-  float sskip[VN], sbias[VN];
-#pragma unroll
-  for (int k = 0; k < VN; ++k) sskip[k] = sbias[k] = 0.f;
-
   for (int c = 0; c < nchunk; ++c) {
     const int ci = nchunk - 1 - c, t0 = ci * kChunk, nt = min(kChunk, tn - t0);
     cp_async_wait<0>();
-    __syncthreads();  // chunk c is here; the other stage and the sums are free
+    cta_sync<W>();  // chunk c is here; the other stage, the operands and the sums are free
     stage(c + 1);
     const unsigned char* const st = smem + (c % kStages) * L.raw;
-    // Tokens past the end and channels past the tile count as s = s x = dpre = 0: they
-    // change nothing.
+    // Tokens past the end and channels past the tile count as s = s x = dpre = 0 (and B = C
+    // = 0): they change nothing.
+#pragma unroll
     for (int i = tid; i < kChunk * VPR; i += NT) {
-      const int t = i / VPR, v = i % VPR;
+      const int t = i / VPR;
       float s[VN], x[VN], d[VN];
-      if (t < nt && v < nv) {
-        const int o = (t * CH + v * VN) * ES;
-        V::unpack(*reinterpret_cast<const uint4*>(st + L.rdt + o), s);
-        V::unpack(*reinterpret_cast<const uint4*>(st + L.rx + o), x);
-        V::unpack(*reinterpret_cast<const uint4*>(st + L.rdy + o), d);
+      if (t < nt && vin) {
+        V::unpack(*reinterpret_cast<const uint4*>(st + L.rdt + 16 * i), s);
+        V::unpack(*reinterpret_cast<const uint4*>(st + L.rx + 16 * i), x);
+        V::unpack(*reinterpret_cast<const uint4*>(st + L.rdy + 16 * i), d);
 #pragma unroll
-        for (int k = 0; k < VN; ++k) {
-          s[k] += fbias[v * VN + k];
-          if (a.softplus) s[k] = softplus_fast(s[k]);
-          bad |= !nonneg_finite(s[k]);
-          x[k] *= s[k];
+        for (int k = 0; k < VN; k += 2) {
+          float2 u = __fadd2_rn(make_float2(s[k], s[k + 1]), *reinterpret_cast<const float2*>(fpar + v * VN + k));
+          if (a.softplus) u = softplus_fast(u);
+          bad |= !(nonneg_finite(u.x) && nonneg_finite(u.y));
+          const float2 sx = __fmul2_rn(u, make_float2(x[k], x[k + 1]));
+          s[k] = u.x;
+          s[k + 1] = u.y;
+          x[k] = sx.x;
+          x[k + 1] = sx.y;
         }
-        if (gz) {
+        if (gated) {
           float z[VN];
-          V::unpack(*reinterpret_cast<const uint4*>(st + L.rz + o), z);
+          V::unpack(*reinterpret_cast<const uint4*>(st + L.rz + 16 * i), z);
 #pragma unroll
-          for (int k = 0; k < VN; ++k) d[k] *= silu_fast(z[k]);
+          for (int k = 0; k < VN; k += 2) {
+            const float2 e = __fmul2_rn(make_float2(d[k], d[k + 1]), silu_fast(make_float2(z[k], z[k + 1])));
+            d[k] = e.x;
+            d[k + 1] = e.y;
+          }
         }
       } else {
 #pragma unroll
@@ -225,201 +260,203 @@ __global__ void __launch_bounds__(256) palimpsa_scan_bwd_kernel(ScanArgs a, Part
       }
 #pragma unroll
       for (int k = 0; k < VN; k += 4) {
-        const int o = t * CH + v * VN + k;
+        const int o = t * CH + ((v * VN + k) ^ 4 * (t & 1));
         *reinterpret_cast<float4*>(fs + o) = make_float4(s[k], s[k + 1], s[k + 2], s[k + 3]);
         *reinterpret_cast<float4*>(fsx + o) = make_float4(x[k], x[k + 1], x[k + 2], x[k + 3]);
         *reinterpret_cast<float4*>(fdp + o) = make_float4(d[k], d[k + 1], d[k + 2], d[k + 3]);
       }
     }
-    for (int i = tid; i < kChunk * BPR; i += NT) {
-      float fb[VN], fc[VN];
-      if (i / BPR < nt) {
-        V::unpack(reinterpret_cast<const uint4*>(st + L.rB)[i], fb);
-        V::unpack(reinterpret_cast<const uint4*>(st + L.rC)[i], fc);
-      } else {
-#pragma unroll
-        for (int k = 0; k < VN; ++k) fb[k] = fc[k] = 0.f;
-      }
-#pragma unroll
-      for (int k = 0; k < VN; k += 4) {
-        *reinterpret_cast<float4*>(fB + i * VN + k) = make_float4(fb[k], fb[k + 1], fb[k + 2], fb[k + 3]);
-        *reinterpret_cast<float4*>(fC + i * VN + k) = make_float4(fc[k], fc[k + 1], fc[k + 2], fc[k + 3]);
-      }
-    }
-    __syncthreads();
+    cta_sync<W>();
 
-    // First sweep: the states before tokens 4, 8, 12 (each lane keeps its own).
-    float2 h[4][NP];
-    const float* const ck = reinterpret_cast<const float*>(st + L.rck);
-    float2* const sub = reinterpret_cast<float2*>(smem + L.sub) + tid;
-    auto load_ckpt = [&]() {
+    float2 h[2][NS];
+    // A lane's states in its own places of shared memory (4 channels of NS states).
+    auto load_h = [&](const unsigned char* p) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
+      for (int k = 0; k < 4; ++k) {
+        float q[NS];
+        load_own<NS>(q, p + (k * NT + tid) * NS * 4);
 #pragma unroll
-        for (int p = 0; p < NP; ++p)
-          h[k][p] = 4 * cl + k < nch ? *reinterpret_cast<const float2*>(ck + (4 * cl + k) * N + n0 + 2 * p)
-                                     : make_float2(0.f, 0.f);
+        for (int j = 0; j < NS; ++j) (k & 1 ? h[k / 2][j].y : h[k / 2][j].x) = 4 * cl + k < nch ? q[j] : 0.f;
+      }
     };
-    load_ckpt();
+    unsigned char* const slots = smem + L.win + warp * (kWins * L.slot(N, W));
+    auto slot_h = [&](int w) { return slots + w * L.slot(N, W) + lane * NS * 4; };
+    // First sweep: the states before tokens 4, 8, 12.
+    load_h(st + L.rck);
 #pragma unroll 1
-    for (int w = 0; w < kChunk / kWin - 1; ++w) {
+    for (int w = 0; w < kWins - 1; ++w) {
 #pragma unroll
       for (int i = 0; i < kWin; ++i) {
-        const int t = w * kWin + i;
-        const float4 s4 = *reinterpret_cast<const float4*>(fs + t * CH + 4 * cl);
-        const float4 x4 = *reinterpret_cast<const float4*>(fsx + t * CH + 4 * cl);
-        const float sv[4] = {s4.x, s4.y, s4.z, s4.w}, xv[4] = {x4.x, x4.y, x4.z, x4.w};
+        const int t = w * kWin + i, q = i & 1 ? cq1 : cq0;
+        float2 s[2], x[2], b[NS];
+        load_pairs(s, fs + t * CH + q);
+        load_pairs(x, fsx + t * CH + q);
+        load_states<BF16, NS>(b, st + L.rB + (t * N + n0) * ES);
 #pragma unroll
-        for (int p = 0; p < NP; ++p) {
-          const float2 b = *reinterpret_cast<const float2*>(fB + t * N + n0 + 2 * p);
+        for (int p = 0; p < 2; ++p)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float2 u = decay_exponent(make_float2(sv[k], sv[k]), A2[k][p]);
-            h[k][p] = __ffma2_rn(make_float2(xv[k], xv[k]), b,
-                                 __fmul2_rn(make_float2(ex2_approx(u.x), ex2_approx(u.y)), h[k][p]));
+          for (int j = 0; j < NS; ++j) {
+            const float2 u = decay_exponent(s[p], A2[p][j]);
+            const float2 e = make_float2(ex2_approx(u.x), ex2_approx(u.y));
+            h[p][j] = __ffma2_rn(x[p], b[j], __fmul2_rn(e, h[p][j]));
           }
-        }
       }
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
+      for (int k = 0; k < 4; ++k) {
+        float q[NS];
 #pragma unroll
-        for (int p = 0; p < NP; ++p) sub[((w * 4 + k) * NP + p) * NT] = h[k][p];
+        for (int j = 0; j < NS; ++j) q[j] = k & 1 ? h[k / 2][j].y : h[k / 2][j].x;
+        store_own<NS>(slot_h(w + 1) + k * 32 * NS * 4, q);
+      }
     }
 
     // Windows, last to first.
 #pragma unroll 1
-    for (int w = kChunk / kWin - 1; w >= 0; --w) {
+    for (int w = kWins - 1; w >= 0; --w) {
       if (w == 0) {
-        load_ckpt();
+        load_h(st + L.rck);
       } else {
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
+        for (int k = 0; k < 4; ++k) {
+          float q[NS];
+          load_own<NS>(q, slot_h(w) + k * 32 * NS * 4);
 #pragma unroll
-          for (int p = 0; p < NP; ++p) h[k][p] = sub[(((w - 1) * 4 + k) * NP + p) * NT];
+          for (int j = 0; j < NS; ++j) (k & 1 ? h[k / 2][j].y : h[k / 2][j].x) = q[j];
+        }
       }
-      float2 al[kWin][4][NP], ah[kWin][4][NP];  // a_t and a_t h_{t-1}
+      float2 al[kWin][2][NS], ah[kWin][2][NS];  // a_t and a_t h_{t-1}
 #pragma unroll
       for (int i = 0; i < kWin; ++i) {
-        const int t = w * kWin + i;
-        const float4 s4 = *reinterpret_cast<const float4*>(fs + t * CH + 4 * cl);
-        const float4 x4 = *reinterpret_cast<const float4*>(fsx + t * CH + 4 * cl);
-        const float sv[4] = {s4.x, s4.y, s4.z, s4.w}, xv[4] = {x4.x, x4.y, x4.z, x4.w};
+        const int t = w * kWin + i, q = i & 1 ? cq1 : cq0;
+        float2 s[2], x[2], b[NS];
+        load_pairs(s, fs + t * CH + q);
+        load_pairs(x, fsx + t * CH + q);
+        load_states<BF16, NS>(b, st + L.rB + (t * N + n0) * ES);
 #pragma unroll
-        for (int p = 0; p < NP; ++p) {
-          const float2 b = *reinterpret_cast<const float2*>(fB + t * N + n0 + 2 * p);
+        for (int p = 0; p < 2; ++p)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float2 u = decay_exponent(make_float2(sv[k], sv[k]), A2[k][p]);
-            al[i][k][p] = make_float2(ex2_approx(u.x), ex2_approx(u.y));
-            ah[i][k][p] = __fmul2_rn(al[i][k][p], h[k][p]);
-            h[k][p] = __ffma2_rn(make_float2(xv[k], xv[k]), b, ah[i][k][p]);
+          for (int j = 0; j < NS; ++j) {
+            const float2 u = decay_exponent(s[p], A2[p][j]);
+            al[i][p][j] = make_float2(ex2_approx(u.x), ex2_approx(u.y));
+            ah[i][p][j] = __fmul2_rn(al[i][p][j], h[p][j]);
+            h[p][j] = __ffma2_rn(x[p], b[j], ah[i][p][j]);
           }
-        }
       }
+      // Sums of a token over the lane's channels (dB, dC) and states (w, sum p A, sum C h).
+      float db[kWin][NS], dc[kWin][NS], sum[3][kWin][4];
 #pragma unroll
       for (int i = kWin - 1; i >= 0; --i) {
-        const int t = w * kWin + i;
-        const float4 s4 = *reinterpret_cast<const float4*>(fs + t * CH + 4 * cl);
-        const float4 x4 = *reinterpret_cast<const float4*>(fsx + t * CH + 4 * cl);
-        const float4 d4 = *reinterpret_cast<const float4*>(fdp + t * CH + 4 * cl);
-        const float sv[4] = {s4.x, s4.y, s4.z, s4.w}, xv[4] = {x4.x, x4.y, x4.z, x4.w},
-                    dv[4] = {d4.x, d4.y, d4.z, d4.w};
-        float2 db[NP], dc[NP], ws[4], qs[4], ys[4];
+        const int t = w * kWin + i, q = i & 1 ? cq1 : cq0;
+        float2 s[2], x[2], d[2], b[NS], cc[NS];
+        load_pairs(s, fs + t * CH + q);
+        load_pairs(x, fsx + t * CH + q);
+        load_pairs(d, fdp + t * CH + q);
+        load_states<BF16, NS>(b, st + L.rB + (t * N + n0) * ES);
+        load_states<BF16, NS>(cc, st + L.rC + (t * N + n0) * ES);
+        float2 ws[2], qs[2], ys[2];
 #pragma unroll
-        for (int p = 0; p < NP; ++p) {
-          const float2 b = *reinterpret_cast<const float2*>(fB + t * N + n0 + 2 * p);
-          const float2 cc = *reinterpret_cast<const float2*>(fC + t * N + n0 + 2 * p);
+        for (int j = 0; j < NS; ++j) {
+          float2 dcj, dbj;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float2 s2 = make_float2(sv[k], sv[k]), x2 = make_float2(xv[k], xv[k]), d2 = make_float2(dv[k], dv[k]);
-            const float2 ht = __ffma2_rn(x2, b, ah[i][k][p]);
-            const float2 gt = __ffma2_rn(cc, d2, gh[k][p]);
-            const float2 pt = __fmul2_rn(gt, ah[i][k][p]);
-            dc[p] = k == 0 ? __fmul2_rn(ht, d2) : __ffma2_rn(ht, d2, dc[p]);
-            db[p] = k == 0 ? __fmul2_rn(gt, x2) : __ffma2_rn(gt, x2, db[p]);
-            ys[k] = p == 0 ? __fmul2_rn(ht, cc) : __ffma2_rn(ht, cc, ys[k]);
-            ws[k] = p == 0 ? __fmul2_rn(gt, b) : __ffma2_rn(gt, b, ws[k]);
-            qs[k] = p == 0 ? __fmul2_rn(pt, A2[k][p]) : __ffma2_rn(pt, A2[k][p], qs[k]);
-            dA[k][p] = __ffma2_rn(pt, s2, dA[k][p]);
-            gh[k][p] = __fmul2_rn(gt, al[i][k][p]);
+          for (int p = 0; p < 2; ++p) {
+            const float2 carried = ah[i][p][j];
+            const float2 ht = __ffma2_rn(x[p], b[j], carried);
+            const float2 gt = __ffma2_rn(cc[j], d[p], gh[p][j]);
+            const float2 pt = __fmul2_rn(gt, carried);
+            dcj = p == 0 ? __fmul2_rn(ht, d[p]) : __ffma2_rn(ht, d[p], dcj);
+            dbj = p == 0 ? __fmul2_rn(gt, x[p]) : __ffma2_rn(gt, x[p], dbj);
+            ws[p] = j == 0 ? __fmul2_rn(gt, b[j]) : __ffma2_rn(gt, b[j], ws[p]);
+            qs[p] = j == 0 ? __fmul2_rn(pt, A2[p][j]) : __ffma2_rn(pt, A2[p][j], qs[p]);
+            ys[p] = j == 0 ? __fmul2_rn(ht, cc[j]) : __ffma2_rn(ht, cc[j], ys[p]);
+            dA[p][j] = __ffma2_rn(pt, s[p], dA[p][j]);
+            gh[p][j] = __fmul2_rn(gt, al[i][p][j]);
           }
+          dc[i][j] = dcj.x + dcj.y;
+          db[i][j] = dbj.x + dbj.y;
         }
-        float v[4];
-        float* const sm = fsum + (warp * kChunk + t) * CH + 4 * cl + sl;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) v[k] = ws[k].x + ws[k].y;
-        sm[0] = scatter_groups(v, sl);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) v[k] = qs[k].x + qs[k].y;
-        sm[W * kChunk * CH] = scatter_groups(v, sl);
-        if (gz) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k) v[k] = ys[k].x + ys[k].y;
-          sm[2 * W * kChunk * CH] = scatter_groups(v, sl);
+        for (int p = 0; p < 2; ++p) {
+          sum[0][i][2 * p] = ws[p].x; sum[0][i][2 * p + 1] = ws[p].y;
+          sum[1][i][2 * p] = qs[p].x; sum[1][i][2 * p + 1] = qs[p].y;
+          sum[2][i][2 * p] = ys[p].x; sum[2][i][2 * p + 1] = ys[p].y;
         }
-        // dB, dC over the 8 lanes that share states: lane cl ends with one value, of dC
-        // where cl & 4, else of dB.
-        const bool b4 = cl & 4, b2 = cl & 2, b1 = cl & 1;
-        float2 keep[NP];
+      }
+      // Over the 4 lane groups: group sl ends with token sl, 4 channels a lane.
+      __syncwarp();  // every lane has read its states from the slot
+      float* const sm = reinterpret_cast<float*>(slots + w * L.slot(N, W)) + sl * CH + (sl & 1 ? cq1 : cq0);
 #pragma unroll
-        for (int p = 0; p < NP; ++p) {
-          const float2 give = b4 ? db[p] : dc[p];
-          keep[p] = b4 ? dc[p] : db[p];
-          keep[p].x += __shfl_xor_sync(0xffffffffu, give.x, 4);
-          keep[p].y += __shfl_xor_sync(0xffffffffu, give.y, 4);
-        }
-        float* const out = part.bc + ((tile * part.rows + rb + t0 + t) * 2 + (b4 ? 1 : 0)) * N + n0;
-        if constexpr (NS == 4) {
-          float2 k2 = b2 ? keep[1] : keep[0];
-          const float2 give = b2 ? keep[0] : keep[1];
-          k2.x += __shfl_xor_sync(0xffffffffu, give.x, 2);
-          k2.y += __shfl_xor_sync(0xffffffffu, give.y, 2);
-          const float r = (b1 ? k2.y : k2.x) + __shfl_xor_sync(0xffffffffu, b1 ? k2.x : k2.y, 1);
-          if (t < nt) out[(b2 ? 2 : 0) + (b1 ? 1 : 0)] = r;
-        } else {
-          float r = (b2 ? keep[0].y : keep[0].x) + __shfl_xor_sync(0xffffffffu, b2 ? keep[0].x : keep[0].y, 2);
-          r += __shfl_xor_sync(0xffffffffu, r, 1);
-          if (t < nt && !b1) out[b2 ? 1 : 0] = r;
-        }
+      for (int k = 0; k < 3; ++k) {
+        float two[8], one[4];
+        halve<8>(two, &sum[k][0][0], &sum[k][2][0], sl & 2, 16);
+        halve<4>(one, two, two + 4, sl & 1, 8);
+        *reinterpret_cast<float4*>(sm + k * kWin * CH) = make_float4(one[0], one[1], one[2], one[3]);
+      }
+      // Over the 8 lanes that share states: lane cl ends with token cl & 3 of dC (cl & 4)
+      // or dB, NS states.
+      {
+        float four[4 * NS], two[2 * NS], one[NS];
+        halve<4 * NS>(four, &db[0][0], &dc[0][0], cl & 4, 4);
+        halve<2 * NS>(two, four, four + 2 * NS, cl & 2, 2);
+        halve<NS>(one, two, two + NS, cl & 1, 1);
+        const int t = w * kWin + (cl & 3);
+        if (t < nt)
+          store_own<NS>(reinterpret_cast<unsigned char*>(
+                            part.bc + ((tile * part.rows + rb + t0 + t) * 2 + (cl >> 2)) * N + n0),
+                        one);
       }
     }
-    __syncthreads();
+    cta_sync<W>();
 
     // Gradients of the tokens' arrays.
-    for (int i = tid; i < kChunk * VPR; i += NT) {
-      const int t = i / VPR, v = i % VPR;
-      if (t >= nt || v >= nv) continue;
-      const int o = (t * CH + v * VN) * ES;
-      float x[VN], dt[VN], dy[VN], z[VN], dx[VN], ddt[VN];
-      V::unpack(*reinterpret_cast<const uint4*>(st + L.rx + o), x);
-      V::unpack(*reinterpret_cast<const uint4*>(st + L.rdt + o), dt);
-      V::unpack(*reinterpret_cast<const uint4*>(st + L.rdy + o), dy);
-      if (gz) V::unpack(*reinterpret_cast<const uint4*>(st + L.rz + o), z);
 #pragma unroll
-      for (int k = 0; k < VN; ++k) {
-        const int e = t * CH + v * VN + k;
-        float ws = 0.f, qs = 0.f, ys = 0.f;
-        for (int w = 0; w < W; ++w) {
-          ws += fsum[w * kChunk * CH + e];
-          qs += fsum[(W + w) * kChunk * CH + e];
-          if (gz) ys += fsum[(2 * W + w) * kChunk * CH + e];
+    for (int i = tid; i < kChunk * VPR; i += NT) {
+      const int t = i / VPR;
+      if (t >= nt || !vin) continue;
+      float x[VN], dt[VN], dy[VN], z[VN], dx[VN], ddt[VN];
+      V::unpack(*reinterpret_cast<const uint4*>(st + L.rx + 16 * i), x);
+      V::unpack(*reinterpret_cast<const uint4*>(st + L.rdt + 16 * i), dt);
+      V::unpack(*reinterpret_cast<const uint4*>(st + L.rdy + 16 * i), dy);
+      if (gated) V::unpack(*reinterpret_cast<const uint4*>(st + L.rz + 16 * i), z);
+#pragma unroll
+      for (int k0 = 0; k0 < VN; k0 += 4) {
+        const int o = (v * VN + k0) ^ 4 * (t & 1);
+        float sums[3][4] = {};
+#pragma unroll
+        for (int wp = 0; wp < W; ++wp)
+#pragma unroll
+          for (int r = 0; r < 3; ++r) {
+            const float4 q = *reinterpret_cast<const float4*>(
+                smem + L.win + wp * (kWins * L.slot(N, W)) + (t / kWin) * L.slot(N, W) +
+                ((r * kWin + t % kWin) * CH + o) * 4);
+            sums[r][0] += q.x; sums[r][1] += q.y; sums[r][2] += q.z; sums[r][3] += q.w;
+          }
+        const float4 s4 = *reinterpret_cast<const float4*>(fs + t * CH + o);
+        const float4 d4 = *reinterpret_cast<const float4*>(fdp + t * CH + o);
+        const float sv[4] = {s4.x, s4.y, s4.z, s4.w}, dv[4] = {d4.x, d4.y, d4.z, d4.w};
+        float4 a0 = facc[(k0 / 2) * NT], a1 = facc[(k0 / 2 + 1) * NT];  // dskip, ddt_bias
+        float *const s0 = &a0.x, *const s1 = &a1.x;
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+          const int k = k0 + m;
+          const float skip = fpar[CH + v * VN + k];
+          dx[k] = fmaf(sums[0][m], sv[m], dv[m] * skip);
+          // the second sum holds -log2(e) sum p A
+          ddt[k] = fmaf(sums[0][m], x[k], sums[1][m] * 0.6931471805599453f);
+          if (a.softplus) ddt[k] *= sigmoid_fast(dt[k] + fpar[v * VN + k]);
+          s0[m] = fmaf(dv[m], x[k], s0[m]);
+          s1[m] += ddt[k];
+          if (gated) {
+            const float q = sigmoid_fast(z[k]);
+            z[k] = dy[k] * fmaf(skip, x[k], sums[2][m]) * (q * fmaf(z[k], 1.f - q, 1.f));
+          }
         }
-        const float skip = fskip[v * VN + k], dpre = fdp[e];
-        dx[k] = fmaf(ws, fs[e], dpre * skip);
-        // qs holds -log2(e) sum p A
-        ddt[k] = fmaf(ws, x[k], qs * 0.6931471805599453f);
-        if (a.softplus) ddt[k] *= sigmoid_fast(dt[k] + fbias[v * VN + k]);
-        sskip[k] = fmaf(dpre, x[k], sskip[k]);
-        sbias[k] += ddt[k];
-        if (gz) {
-          const float q = sigmoid_fast(z[k]);
-          z[k] = dy[k] * fmaf(skip, x[k], ys) * (q * fmaf(z[k], 1.f - q, 1.f));
-        }
+        facc[(k0 / 2) * NT] = a0;
+        facc[(k0 / 2 + 1) * NT] = a1;
       }
-      const long long at = ((rb + t0 + t) * a.D + ch0 + v * VN) * ES;
-      *reinterpret_cast<uint4*>(static_cast<char*>(a.dx) + at) = V::pack(dx);
-      *reinterpret_cast<uint4*>(static_cast<char*>(a.ddt) + at) = V::pack(ddt);
-      if (gz) *reinterpret_cast<uint4*>(static_cast<char*>(a.dz) + at) = V::pack(z);
+      const long long to = ((rb + t0 + t) * a.D + ch0 + v * VN) * ES;
+      *reinterpret_cast<uint4*>(static_cast<char*>(a.dx) + to) = V::pack(dx);
+      *reinterpret_cast<uint4*>(static_cast<char*>(a.ddt) + to) = V::pack(ddt);
+      if (gated) *reinterpret_cast<uint4*>(static_cast<char*>(a.dz) + to) = V::pack(z);
     }
   }
   if (bad) latch_status(a.status, kStatusDomain);
@@ -428,27 +465,24 @@ __global__ void __launch_bounds__(256) palimpsa_scan_bwd_kernel(ScanArgs a, Part
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
     if (4 * cl + c >= nch) continue;
-    const size_t e = (size_t)(ch0 + 4 * cl + c) * N + n0;
+    float q[NS];
 #pragma unroll
-    for (int p = 0; p < NP; ++p) {
-      *reinterpret_cast<float2*>(part.dA + ns * a.D * N + e + 2 * p) = make_float2(-dA[c][p].x, -dA[c][p].y);
-      if (tb == 0 && a.dh0) *reinterpret_cast<float2*>(a.dh0 + (size_t)n * a.D * N + e + 2 * p) = gh[c][p];
+    for (int j = 0; j < NS; ++j) q[j] = -(c & 1 ? dA[c / 2][j].y : dA[c / 2][j].x);
+    store_own<NS>(reinterpret_cast<unsigned char*>(part.dA + ns * a.D * N + at + c * N), q);
+    if (tb == 0 && a.dh0) {
+#pragma unroll
+      for (int j = 0; j < NS; ++j) q[j] = c & 1 ? gh[c / 2][j].y : gh[c / 2][j].x;
+      store_own<NS>(reinterpret_cast<unsigned char*>(a.dh0 + (size_t)n * a.D * N + at + c * N), q);
     }
   }
   // dskip, ddt_bias of the segment: the threads of a vector, added up in thread order.
   __syncthreads();
-  float* const red = fs;  // 2 x NT x VN values fit the chunk's arrays
-  for (int which = 0; which < 2; ++which) {
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < VN; ++k) red[tid * VN + k] = which ? sbias[k] : sskip[k];
-    __syncthreads();
-    for (int e = tid; e < nch; e += NT) {
-      const int v = e / VN, k = e % VN;
-      float s = 0.f;
-      for (int t = v; t < NT; t += VPR) s += red[t * VN + k];
-      part.par[(ns * 2 + which) * a.D + ch0 + e] = s;
-    }
+  for (int e = tid; e < 2 * nch; e += NT) {
+    const int which = e / nch, ch = e % nch, vv = ch / VN, k = ch % VN;
+    const float* const f = reinterpret_cast<const float*>(smem + L.acc) + (k / 4 * 2 + which) * NT * 4 + k % 4;
+    float s = 0.f;
+    for (int t = vv; t < NT; t += VPR) s += f[t * 4];
+    part.par[(ns * 2 + which) * a.D + ch0 + ch] = s;
   }
 }
 
@@ -509,19 +543,38 @@ __global__ void __launch_bounds__(256) palimpsa_scan_bwd_par_kernel(ScanArgs a, 
 
 long long total_rows(const ScanArgs& a) { return a.rows.cu ? a.rows.T : (long long)a.rows.n_seq * a.rows.T; }
 
-template <bool BF16, int NS>
+template <bool BF16, int NS, int W>
+cudaError_t prepare() {
+  constexpr Smem L(4 * NS * W, W, Vec<BF16>::bytes);
+  if (L.total <= 48 * 1024) return cudaSuccess;
+  return cudaFuncSetAttribute(palimpsa_scan_bwd_kernel<BF16, NS, W>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              L.total);
+}
+
+// CTAs that an SM holds (from the occupancy calculator, once per kernel); 0 on failure.
+template <bool BF16, int NS, int W>
+int resident() {
+  static std::atomic<int> known{0};
+  int r = known.load(std::memory_order_relaxed);
+  if (r > 0) return r;
+  constexpr Smem L(4 * NS * W, W, Vec<BF16>::bytes);
+  if (prepare<BF16, NS, W>() != cudaSuccess ||
+      cudaOccupancyMaxActiveBlocksPerMultiprocessor(&r, palimpsa_scan_bwd_kernel<BF16, NS, W>, 32 * W, L.total) !=
+          cudaSuccess)
+    return 0;
+  known.store(r, std::memory_order_relaxed);
+  return r;
+}
+
+template <bool BF16, int NS, int W>
 cudaError_t run(const ScanArgs& a, const Partials& part, cudaStream_t s) {
-  const int W = a.N / (4 * NS);
-  const Smem L(a.N, W, Vec<BF16>::bytes);
+  constexpr Smem L(4 * NS * W, W, Vec<BF16>::bytes);
   const long long tiles = scan_tiles(a), blocks = tiles * a.rows.n_seq * a.nseg;
   if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
-  if (L.total > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(palimpsa_scan_bwd_kernel<BF16, NS>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, L.total);
-    if (e != cudaSuccess) return e;
-  }
-  palimpsa_scan_bwd_kernel<BF16, NS><<<(unsigned)blocks, 32 * W, L.total, s>>>(a, part, (int)tiles, W);
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e = prepare<BF16, NS, W>();
+  if (e != cudaSuccess) return e;
+  palimpsa_scan_bwd_kernel<BF16, NS, W><<<(unsigned)blocks, 32 * W, L.total, s>>>(a, part, (int)tiles);
+  e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const long long bct = (long long)a.rows.n_seq * a.rows.max_len * a.G * (2 * a.N / 4);
   if (bct > 0) {
@@ -557,8 +610,23 @@ cudaError_t launch_scan_backward(const ScanArgs& a, float* scratch, cudaStream_t
     if (e == cudaSuccess) e = launch_scan_carry(a, true, s);
     if (e != cudaSuccess) return e;
   }
-  if (a.N == 8) return a.bf16 ? run<true, 2>(a, part, s) : run<false, 2>(a, part, s);
-  return a.bf16 ? run<true, 4>(a, part, s) : run<false, 4>(a, part, s);
+  switch (a.N) {
+    case 8: return a.bf16 ? run<true, 2, 1>(a, part, s) : run<false, 2, 1>(a, part, s);
+    case 16: return a.bf16 ? run<true, 4, 1>(a, part, s) : run<false, 4, 1>(a, part, s);
+    case 32: return a.bf16 ? run<true, 4, 2>(a, part, s) : run<false, 4, 2>(a, part, s);
+    case 64: return a.bf16 ? run<true, 4, 4>(a, part, s) : run<false, 4, 4>(a, part, s);
+    default: return a.bf16 ? run<true, 4, 8>(a, part, s) : run<false, 4, 8>(a, part, s);
+  }
+}
+
+int scan_backward_resident(const ScanArgs& a) {
+  switch (a.N) {
+    case 8: return a.bf16 ? resident<true, 2, 1>() : resident<false, 2, 1>();
+    case 16: return a.bf16 ? resident<true, 4, 1>() : resident<false, 4, 1>();
+    case 32: return a.bf16 ? resident<true, 4, 2>() : resident<false, 4, 2>();
+    case 64: return a.bf16 ? resident<true, 4, 4>() : resident<false, 4, 4>();
+    default: return a.bf16 ? resident<true, 4, 8>() : resident<false, 4, 8>();
+  }
 }
 
 }  // namespace palimpsa

@@ -95,12 +95,6 @@ __device__ __forceinline__ void load_states(float2* f, const unsigned char* p) {
   for (int j = 0; j < NS; ++j) f[j] = make_float2(v[j], v[j]);
 }
 
-template <int W>
-__device__ __forceinline__ void cta_sync() {
-  if constexpr (W == 1) __syncwarp();
-  else __syncthreads();
-}
-
 // NS states per lane (2 or 4), W warps: N = 4 NS W.
 template <bool BF16, int NS, int W, int MODE>
 __global__ void __launch_bounds__(32 * W, kWarpsPerSM / W) palimpsa_scan_kernel(ScanArgs a, int tiles) {
@@ -427,7 +421,9 @@ cudaError_t plan_scan(ScanArgs* a, bool backward) {
   a->nseg = 1;
   a->seg_len = std::max(len, 1);
   // Segments for one wave of CTAs: the warps that an SM holds, in every SM.
-  long long want = (long long)(backward ? 8 : kWarpsPerSM) * sms / warps;
+  const int held = backward ? scan_backward_resident(*a) * std::max(1, a->N / 16) : kWarpsPerSM;
+  if (held < 1) return cudaErrorInvalidConfiguration;
+  long long want = (long long)held * sms / warps;
   // The forward's split does nearly twice the work: it pays from 3 segments on. Pass A
   // is a small part of a backward.
   if (!backward && want < 3) want = 1;

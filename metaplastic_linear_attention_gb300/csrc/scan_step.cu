@@ -11,7 +11,8 @@
 namespace palimpsa {
 namespace {
 
-constexpr int kPer = 4;  // channels of a lane, one warp-width apart
+constexpr int kPer = 2;    // channels of a lane
+constexpr int kWarps = 4;
 
 template <bool BF16>
 __device__ __forceinline__ float load1(const void* p, long long i) {
@@ -29,37 +30,40 @@ __device__ __forceinline__ float4 load4(const void* p, long long i) {
 }
 
 template <bool BF16, int N>
-__global__ void __launch_bounds__(128) palimpsa_scan_step_kernel(ScanArgs a) {
+__global__ void __launch_bounds__(32 * kWarps) palimpsa_scan_step_kernel(ScanArgs a, unsigned chunks) {
   constexpr int LPC = N / 4, CPW = 32 / LPC;  // lanes per channel, channels per warp and turn
-  const int lane = threadIdx.x & 31;
-  const long long warp = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
-  const long long total = (long long)a.rows.n_seq * a.D;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const long long n = blockIdx.x / chunks;  // sequence
   const int n0 = 4 * (lane % LPC);
-  const long long first = warp * (kPer * CPW) + lane / LPC;  // (sequence, channel) index
+  const int first = (int)(blockIdx.x % chunks) * (kWarps * kPer * CPW) + warp * (kPer * CPW) + lane / LPC;
+  const int per_group = a.D / a.G;
+  float* const hs = a.h_T + (n * a.D + first) * N + n0;
+  const float* const As = a.A + (long long)first * N + n0;
   float4 h[kPer], A[kPer], B[kPer], C[kPer];
-  float s[kPer], x[kPer], z[kPer], sk[kPer];
+  float s[kPer], x[kPer], z[kPer], sk[kPer], bi[kPer];
   bool bad = false;
 #pragma unroll
   for (int k = 0; k < kPer; ++k) {
-    const long long i = first + k * CPW;
-    if (i >= total) continue;
-    const long long n = i / a.D;
-    const int d = (int)(i - n * a.D), g = d / (a.D / a.G);
-    h[k] = *reinterpret_cast<const float4*>(a.h_T + i * N + n0);
-    A[k] = *reinterpret_cast<const float4*>(a.A + (long long)d * N + n0);
-    B[k] = load4<BF16>(a.B, n * a.B_ld + g * N + n0);
-    C[k] = load4<BF16>(a.C, n * a.C_ld + g * N + n0);
-    s[k] = load1<BF16>(a.dt, n * a.dt_ld + d) + (a.dt_bias ? a.dt_bias[d] : 0.f);
+    const int d = first + k * CPW;
+    if (d >= a.D) continue;
+    h[k] = *reinterpret_cast<const float4*>(hs + k * CPW * N);
+    A[k] = *reinterpret_cast<const float4*>(As + k * CPW * N);
+    s[k] = load1<BF16>(a.dt, n * a.dt_ld + d);
     x[k] = load1<BF16>(a.x, n * a.x_ld + d);
     z[k] = a.z ? load1<BF16>(a.z, n * a.z_ld + d) : 0.f;
+    bi[k] = a.dt_bias ? a.dt_bias[d] : 0.f;
     sk[k] = a.skip ? a.skip[d] : 0.f;
+    const int g = a.G == 1 ? 0 : d / per_group;
+    B[k] = load4<BF16>(a.B, n * a.B_ld + g * N + n0);
+    C[k] = load4<BF16>(a.C, n * a.C_ld + g * N + n0);
   }
 #pragma unroll
   for (int k = 0; k < kPer; ++k) {
-    const long long i = first + k * CPW;
-    const bool in = i < total;
+    const int d = first + k * CPW;
+    const bool in = d < a.D;
     float y = 0.f;
     if (in) {
+      s[k] += bi[k];
       if (a.softplus) s[k] = softplus_fast(s[k]);
       bad |= !(nonneg_finite(s[k]) && pos_finite(A[k].x) && pos_finite(A[k].y) && pos_finite(A[k].z) &&
                pos_finite(A[k].w));
@@ -68,7 +72,7 @@ __global__ void __launch_bounds__(128) palimpsa_scan_step_kernel(ScanArgs a) {
       h[k].y = fmaf(ex2_approx(fmaf(m, A[k].y, kDecayShift)), h[k].y, w * B[k].y);
       h[k].z = fmaf(ex2_approx(fmaf(m, A[k].z, kDecayShift)), h[k].z, w * B[k].z);
       h[k].w = fmaf(ex2_approx(fmaf(m, A[k].w, kDecayShift)), h[k].w, w * B[k].w);
-      *reinterpret_cast<float4*>(a.h_T + i * N + n0) = h[k];
+      *reinterpret_cast<float4*>(hs + k * CPW * N) = h[k];
       y = fmaf(h[k].x, C[k].x, fmaf(h[k].y, C[k].y, fmaf(h[k].z, C[k].z, h[k].w * C[k].w)));
     }
 #pragma unroll
@@ -76,8 +80,8 @@ __global__ void __launch_bounds__(128) palimpsa_scan_step_kernel(ScanArgs a) {
     if (in && lane % LPC == 0) {
       y = fmaf(sk[k], x[k], y);
       if (a.z) y *= silu_fast(z[k]);
-      if constexpr (BF16) static_cast<__nv_bfloat16*>(a.y)[i] = __float2bfloat16_rn(y);
-      else static_cast<float*>(a.y)[i] = y;
+      if constexpr (BF16) static_cast<__nv_bfloat16*>(a.y)[n * a.D + d] = __float2bfloat16_rn(y);
+      else static_cast<float*>(a.y)[n * a.D + d] = y;
     }
   }
   if (bad) latch_status(a.status, kStatusDomain);
@@ -85,11 +89,11 @@ __global__ void __launch_bounds__(128) palimpsa_scan_step_kernel(ScanArgs a) {
 
 template <int N>
 cudaError_t run(const ScanArgs& a, cudaStream_t s) {
-  const long long per_block = 4ll * kPer * (32 / (N / 4));
-  const long long blocks = ((long long)a.rows.n_seq * a.D + per_block - 1) / per_block;
+  const int per_block = kWarps * kPer * (32 / (N / 4));
+  const long long chunks = (a.D + per_block - 1) / per_block, blocks = chunks * a.rows.n_seq;
   if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
-  if (a.bf16) palimpsa_scan_step_kernel<true, N><<<(unsigned)blocks, 128, 0, s>>>(a);
-  else palimpsa_scan_step_kernel<false, N><<<(unsigned)blocks, 128, 0, s>>>(a);
+  if (a.bf16) palimpsa_scan_step_kernel<true, N><<<(unsigned)blocks, 32 * kWarps, 0, s>>>(a, (unsigned)chunks);
+  else palimpsa_scan_step_kernel<false, N><<<(unsigned)blocks, 32 * kWarps, 0, s>>>(a, (unsigned)chunks);
   return cudaGetLastError();
 }
 

@@ -116,6 +116,7 @@ cudaError_t launch_scan_step(const ScanArgs& a, cudaStream_t s);
 // dB and dC and the per-segment sums of the parameters' gradients.
 size_t scan_backward_scratch_floats(const ScanArgs& a);
 cudaError_t launch_scan_backward(const ScanArgs& a, float* scratch, cudaStream_t s);
+int scan_backward_resident(const ScanArgs& a);  // CTAs of it that an SM holds; 0 on failure
 // Pass A of the backward's time split: each segment's gradient with respect to the
 // state before it, from a zero gradient after it, and its sum of step sizes.
 cudaError_t launch_scan_reverse_summary(const ScanArgs& a, cudaStream_t s);
@@ -205,6 +206,33 @@ __device__ __forceinline__ void cp_async16(void* dst, const void* src) {
 __device__ __forceinline__ void cp_async16(void* dst, const void* src, bool in) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(in ? 16 : 0)
                : "memory");
+}
+// NS = 2 or 4 floats: an asynchronous copy of them, and plain loads and stores.
+template <int NS>
+__device__ __forceinline__ void cp_async_states(void* dst, const float* src) {
+  if constexpr (NS == 4) cp_async16(dst, src);
+  else asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+template <int NS>
+__device__ __forceinline__ void load_own(float* f, const unsigned char* p) {
+  if constexpr (NS == 4) {
+    const float4 v = *reinterpret_cast<const float4*>(p);
+    f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
+  } else {
+    const float2 v = *reinterpret_cast<const float2*>(p);
+    f[0] = v.x; f[1] = v.y;
+  }
+}
+template <int NS>
+__device__ __forceinline__ void store_own(unsigned char* p, const float* f) {
+  if constexpr (NS == 4) *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+  else *reinterpret_cast<float2*>(p) = make_float2(f[0], f[1]);
+}
+// A CTA of one warp needs no barrier.
+template <int W>
+__device__ __forceinline__ void cta_sync() {
+  if constexpr (W == 1) __syncwarp();
+  else __syncthreads();
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int PENDING>
