@@ -40,15 +40,23 @@ constexpr int kChunk = kScanCheckpoint;
 constexpr int kWin = 4;
 constexpr int kWins = kChunk / kWin;
 constexpr int kStages = 2;
+constexpr int kWarpsPerSM = 12;
 constexpr int CH = kScanChannels;
+
+// Channel pairs of a lane: 1 (two warps share a tile's channels), or 2 at N = 128, where
+// 16 warps of the former's registers do not fit an SM.
+__host__ __device__ constexpr int pairs(int N) { return N == 128 ? 2 : 1; }
+__host__ __device__ constexpr int parts(int N) { return CH / (16 * pairs(N)); }
+__host__ __device__ constexpr int states(int N) { return N == 8 ? 2 : 4; }  // of a lane
+__host__ __device__ constexpr int warps(int N) { return N / (4 * states(N)) * parts(N); }
 
 // Shared memory of a CTA, bytes (all parts 16-byte aligned).
 struct Smem {
   int rx, rdt, rz, rdy, rB, rC, rck, raw;  // one stage of raw inputs and a checkpoint
   int s, sx, dp;                           // fp32 operands
   int win;                                 // per warp and window: a state, then the window's sums
-  int acc, par, total;
-  __host__ __device__ constexpr Smem(int N, int W, int es)
+  int bc, acc, par, total;
+  __host__ __device__ constexpr Smem(int N, int es)
       : rx(0),
         rdt(kChunk * CH * es),
         rz(2 * kChunk * CH * es),
@@ -61,12 +69,14 @@ struct Smem {
         sx(s + kChunk * CH * 4),
         dp(sx + kChunk * CH * 4),
         win(dp + kChunk * CH * 4),
-        acc(win + kWins * W * slot(N, W)),
-        par(acc + 32 * W * 16 * 4),
+        bc(win + kWins * warps(N) * slot(N)),
+        acc(bc + (parts(N) > 1 ? parts(N) * kChunk * 2 * N * 4 : 0)),
+        par(acc + 32 * warps(N) * 2 * (16 / es) * 4),
         total(par + 2 * CH * 4) {}
-  // Bytes of a warp's slot: 16 or 8 states a lane, or 3 sums of 4 tokens of 32 channels.
-  static __host__ __device__ constexpr int slot(int N, int W) {
-    return CH * N / W * 4 > 3 * kWin * CH * 4 ? CH * N / W * 4 : 3 * kWin * CH * 4;
+  // Bytes of a warp's slot: the states of its lanes, or 3 sums of 4 tokens of its channels.
+  static __host__ __device__ constexpr int slot(int N) {
+    return 32 * 2 * pairs(N) * states(N) * 4 > 3 * kWin * 16 * pairs(N) * 4 ? 32 * 2 * pairs(N) * states(N) * 4
+                                                                          : 3 * kWin * 16 * pairs(N) * 4;
   }
 };
 
@@ -97,10 +107,16 @@ __device__ __forceinline__ void load_states(float2* f, const unsigned char* p) {
 #pragma unroll
   for (int j = 0; j < NS; ++j) f[j] = make_float2(v[j], v[j]);
 }
+// 2 CP values, as pairs.
+template <int CP>
 __device__ __forceinline__ void load_pairs(float2* f, const float* p) {
-  const float4 v = *reinterpret_cast<const float4*>(p);
-  f[0] = make_float2(v.x, v.y);
-  f[1] = make_float2(v.z, v.w);
+  if constexpr (CP == 2) {
+    const float4 v = *reinterpret_cast<const float4*>(p);
+    f[0] = make_float2(v.x, v.y);
+    f[1] = make_float2(v.z, v.w);
+  } else {
+    f[0] = *reinterpret_cast<const float2*>(p);
+  }
 }
 // The kept half of two vectors plus the partner's copy of it (the partner keeps the other).
 template <int M>
@@ -110,12 +126,13 @@ __device__ __forceinline__ void halve(float* out, const float* a, const float* b
     out[k] = (second ? b[k] : a[k]) + __shfl_xor_sync(0xffffffffu, second ? a[k] : b[k], lane_mask);
 }
 
-template <bool BF16, int NS, int W>
-__global__ void __launch_bounds__(32 * W) palimpsa_scan_bwd_kernel(ScanArgs a, Partials part, int tiles) {
+template <bool BF16, int N>
+__global__ void __launch_bounds__(32 * warps(N), N == 128 ? 1 : kWarpsPerSM / warps(N))
+palimpsa_scan_bwd_kernel(ScanArgs a, Partials part, int tiles) {
   using V = Vec<BF16>;
-  constexpr int VN = V::n, ES = V::bytes, N = 4 * NS * W, NT = 32 * W;
-  constexpr int VPR = CH / VN, BPR = N / VN;
-  constexpr Smem L(N, W, ES);
+  constexpr int VN = V::n, ES = V::bytes, NS = states(N), CP = pairs(N), CPC = 2 * CP, W = warps(N), NT = 32 * W;
+  constexpr int VPR = CH / VN, BPR = N / VN, kParts = parts(N);
+  constexpr Smem L(N, ES);
   extern __shared__ __align__(128) unsigned char smem[];
   float* const fs = reinterpret_cast<float*>(smem + L.s);
   float* const fsx = reinterpret_cast<float*>(smem + L.sx);
@@ -141,20 +158,19 @@ __global__ void __launch_bounds__(32 * W) palimpsa_scan_bwd_kernel(ScanArgs a, P
   if (tb >= len && seg > 0) return;
   const int tn = te - tb, nchunk = (tn + kChunk - 1) / kChunk;
 
-  // A lane's channels 4 cl .. 4 cl + 3 of the tile, as two pairs, and its states from n0
-  // on. Quads of 4 channels of odd tokens change places in pairs in shared memory, as in
+  // A lane's CPC channels of the tile from d0 on, as pairs, and its states from n0 on. Quads of 4 channels of odd tokens change places in pairs in shared memory, as in
   // the forward.
-  const int cl = lane & 7, sl = lane >> 3, n0 = (warp * 4 + sl) * NS;
-  const int cq0 = 4 * cl, cq1 = 4 * (cl ^ 1);
-  const size_t at = (size_t)(ch0 + 4 * cl) * N + n0;  // of the first channel in [D, N]
+  const int cl = lane & 7, sl = lane >> 3, wpart = warp % kParts, n0 = (warp / kParts * 4 + sl) * NS;
+  const int d0 = wpart * 16 * CP + CPC * cl, cq0 = d0, cq1 = d0 ^ 4;
+  const size_t at = (size_t)(ch0 + d0) * N + n0;  // of the first channel in [D, N]
   bool bad = false;
-  float2 A2[2][NS], gh[2][NS], dA[2][NS];
+  float2 A2[CP][NS], gh[CP][NS], dA[CP][NS];
   const float* g0 = nullptr;
   if (a.nseg > 1) g0 = a.seg_state + (size_t)(n * a.nseg + seg) * a.D * N;
   else if (a.dh_T) g0 = a.dh_T + (size_t)n * a.D * N;
 #pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    const bool in = 4 * cl + c < nch;
+  for (int c = 0; c < CPC; ++c) {
+    const bool in = d0 + c < nch;
 #pragma unroll
     for (int j = 0; j < NS; ++j) {
       const float A = in ? a.A[at + c * N + j] : 1.f;
@@ -210,8 +226,8 @@ __global__ void __launch_bounds__(32 * W) palimpsa_scan_bwd_kernel(ScanArgs a, P
       // each lane its own part of the checkpoint
       const float* const ck = gck + (long long)ci * a.D * N;
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (4 * cl + k < nch) cp_async_states<NS>(st + L.rck + (k * NT + tid) * NS * 4, ck + k * N);
+      for (int k = 0; k < CPC; ++k)
+        if (d0 + k < nch) cp_async_states<NS>(st + L.rck + (k * NT + tid) * NS * 4, ck + k * N);
     }
     cp_async_commit();
   };
@@ -221,7 +237,7 @@ __global__ void __launch_bounds__(32 * W) palimpsa_scan_bwd_kernel(ScanArgs a, P
     const int ci = nchunk - 1 - c, t0 = ci * kChunk, nt = min(kChunk, tn - t0);
     cp_async_wait<0>();
     cta_sync<W>();  // chunk c is here; the other stage, the operands and the sums are free
-    stage(c + 1);
+    if (kStages == 2) stage(c + 1);
     const unsigned char* const st = smem + (c % kStages) * L.raw;
     // Tokens past the end and channels past the tile count as s = s x = dpre = 0 (and B = C
     // = 0): they change nothing.
@@ -268,19 +284,19 @@ __global__ void __launch_bounds__(32 * W) palimpsa_scan_bwd_kernel(ScanArgs a, P
     }
     cta_sync<W>();
 
-    float2 h[2][NS];
-    // A lane's states in its own places of shared memory (4 channels of NS states).
+    float2 h[CP][NS];
+    // A lane's states in its own places of shared memory (CPC channels of NS states).
     auto load_h = [&](const unsigned char* p) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
+      for (int k = 0; k < CPC; ++k) {
         float q[NS];
         load_own<NS>(q, p + (k * NT + tid) * NS * 4);
 #pragma unroll
-        for (int j = 0; j < NS; ++j) (k & 1 ? h[k / 2][j].y : h[k / 2][j].x) = 4 * cl + k < nch ? q[j] : 0.f;
+        for (int j = 0; j < NS; ++j) (k & 1 ? h[k / 2][j].y : h[k / 2][j].x) = d0 + k < nch ? q[j] : 0.f;
       }
     };
-    unsigned char* const slots = smem + L.win + warp * (kWins * L.slot(N, W));
-    auto slot_h = [&](int w) { return slots + w * L.slot(N, W) + lane * NS * 4; };
+    unsigned char* const slots = smem + L.win + warp * (kWins * L.slot(N));
+    auto slot_h = [&](int w) { return slots + w * L.slot(N) + lane * NS * 4; };
     // First sweep: the states before tokens 4, 8, 12.
     load_h(st + L.rck);
 #pragma unroll 1
@@ -288,12 +304,12 @@ __global__ void __launch_bounds__(32 * W) palimpsa_scan_bwd_kernel(ScanArgs a, P
 #pragma unroll
       for (int i = 0; i < kWin; ++i) {
         const int t = w * kWin + i, q = i & 1 ? cq1 : cq0;
-        float2 s[2], x[2], b[NS];
-        load_pairs(s, fs + t * CH + q);
-        load_pairs(x, fsx + t * CH + q);
+        float2 s[CP], x[CP], b[NS];
+        load_pairs<CP>(s, fs + t * CH + q);
+        load_pairs<CP>(x, fsx + t * CH + q);
         load_states<BF16, NS>(b, st + L.rB + (t * N + n0) * ES);
 #pragma unroll
-        for (int p = 0; p < 2; ++p)
+        for (int p = 0; p < CP; ++p)
 #pragma unroll
           for (int j = 0; j < NS; ++j) {
             const float2 u = decay_exponent(s[p], A2[p][j]);
@@ -302,7 +318,7 @@ __global__ void __launch_bounds__(32 * W) palimpsa_scan_bwd_kernel(ScanArgs a, P
           }
       }
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
+      for (int k = 0; k < CPC; ++k) {
         float q[NS];
 #pragma unroll
         for (int j = 0; j < NS; ++j) q[j] = k & 1 ? h[k / 2][j].y : h[k / 2][j].x;
@@ -317,23 +333,23 @@ __global__ void __launch_bounds__(32 * W) palimpsa_scan_bwd_kernel(ScanArgs a, P
         load_h(st + L.rck);
       } else {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < CPC; ++k) {
           float q[NS];
           load_own<NS>(q, slot_h(w) + k * 32 * NS * 4);
 #pragma unroll
           for (int j = 0; j < NS; ++j) (k & 1 ? h[k / 2][j].y : h[k / 2][j].x) = q[j];
         }
       }
-      float2 al[kWin][2][NS], ah[kWin][2][NS];  // a_t and a_t h_{t-1}
+      float2 al[kWin][CP][NS], ah[kWin][CP][NS];  // a_t and a_t h_{t-1}
 #pragma unroll
       for (int i = 0; i < kWin; ++i) {
         const int t = w * kWin + i, q = i & 1 ? cq1 : cq0;
-        float2 s[2], x[2], b[NS];
-        load_pairs(s, fs + t * CH + q);
-        load_pairs(x, fsx + t * CH + q);
+        float2 s[CP], x[CP], b[NS];
+        load_pairs<CP>(s, fs + t * CH + q);
+        load_pairs<CP>(x, fsx + t * CH + q);
         load_states<BF16, NS>(b, st + L.rB + (t * N + n0) * ES);
 #pragma unroll
-        for (int p = 0; p < 2; ++p)
+        for (int p = 0; p < CP; ++p)
 #pragma unroll
           for (int j = 0; j < NS; ++j) {
             const float2 u = decay_exponent(s[p], A2[p][j]);
@@ -343,22 +359,22 @@ __global__ void __launch_bounds__(32 * W) palimpsa_scan_bwd_kernel(ScanArgs a, P
           }
       }
       // Sums of a token over the lane's channels (dB, dC) and states (w, sum p A, sum C h).
-      float db[kWin][NS], dc[kWin][NS], sum[3][kWin][4];
+      float db[kWin][NS], dc[kWin][NS], sum[3][kWin][CPC];
 #pragma unroll
       for (int i = kWin - 1; i >= 0; --i) {
         const int t = w * kWin + i, q = i & 1 ? cq1 : cq0;
-        float2 s[2], x[2], d[2], b[NS], cc[NS];
-        load_pairs(s, fs + t * CH + q);
-        load_pairs(x, fsx + t * CH + q);
-        load_pairs(d, fdp + t * CH + q);
+        float2 s[CP], x[CP], d[CP], b[NS], cc[NS];
+        load_pairs<CP>(s, fs + t * CH + q);
+        load_pairs<CP>(x, fsx + t * CH + q);
+        load_pairs<CP>(d, fdp + t * CH + q);
         load_states<BF16, NS>(b, st + L.rB + (t * N + n0) * ES);
         load_states<BF16, NS>(cc, st + L.rC + (t * N + n0) * ES);
-        float2 ws[2], qs[2], ys[2];
+        float2 ws[CP], qs[CP], ys[CP];
 #pragma unroll
         for (int j = 0; j < NS; ++j) {
           float2 dcj, dbj;
 #pragma unroll
-          for (int p = 0; p < 2; ++p) {
+          for (int p = 0; p < CP; ++p) {
             const float2 carried = ah[i][p][j];
             const float2 ht = __ffma2_rn(x[p], b[j], carried);
             const float2 gt = __ffma2_rn(cc[j], d[p], gh[p][j]);
@@ -375,21 +391,21 @@ __global__ void __launch_bounds__(32 * W) palimpsa_scan_bwd_kernel(ScanArgs a, P
           db[i][j] = dbj.x + dbj.y;
         }
 #pragma unroll
-        for (int p = 0; p < 2; ++p) {
+        for (int p = 0; p < CP; ++p) {
           sum[0][i][2 * p] = ws[p].x; sum[0][i][2 * p + 1] = ws[p].y;
           sum[1][i][2 * p] = qs[p].x; sum[1][i][2 * p + 1] = qs[p].y;
           sum[2][i][2 * p] = ys[p].x; sum[2][i][2 * p + 1] = ys[p].y;
         }
       }
-      // Over the 4 lane groups: group sl ends with token sl, 4 channels a lane.
+      // Over the 4 lane groups: group sl ends with token sl, CPC channels a lane.
       __syncwarp();  // every lane has read its states from the slot
-      float* const sm = reinterpret_cast<float*>(slots + w * L.slot(N, W)) + sl * CH + (sl & 1 ? cq1 : cq0);
+      float* const sm = reinterpret_cast<float*>(slots + w * L.slot(N)) + sl * 16 * CP + CPC * cl;
 #pragma unroll
       for (int k = 0; k < 3; ++k) {
-        float two[8], one[4];
-        halve<8>(two, &sum[k][0][0], &sum[k][2][0], sl & 2, 16);
-        halve<4>(one, two, two + 4, sl & 1, 8);
-        *reinterpret_cast<float4*>(sm + k * kWin * CH) = make_float4(one[0], one[1], one[2], one[3]);
+        float two[2 * CPC], one[CPC];
+        halve<2 * CPC>(two, &sum[k][0][0], &sum[k][2][0], sl & 2, 16);
+        halve<CPC>(one, two, two + CPC, sl & 1, 8);
+        store_own<CPC>(reinterpret_cast<unsigned char*>(sm + k * kWin * 16 * CP), one);
       }
       // Over the 8 lanes that share states: lane cl ends with token cl & 3 of dC (cl & 4)
       // or dB, NS states.
@@ -399,14 +415,30 @@ __global__ void __launch_bounds__(32 * W) palimpsa_scan_bwd_kernel(ScanArgs a, P
         halve<2 * NS>(two, four, four + 2 * NS, cl & 2, 2);
         halve<NS>(one, two, two + NS, cl & 1, 1);
         const int t = w * kWin + (cl & 3);
-        if (t < nt)
+        if constexpr (kParts > 1) {
+          store_own<NS>(smem + L.bc + (((wpart * kChunk + t) * 2 + (cl >> 2)) * N + n0) * 4, one);
+        } else if (t < nt) {
           store_own<NS>(reinterpret_cast<unsigned char*>(
                             part.bc + ((tile * part.rows + rb + t0 + t) * 2 + (cl >> 2)) * N + n0),
                         one);
+        }
       }
     }
     cta_sync<W>();
 
+    if constexpr (kParts > 1) {  // dB, dC of the tile: the parts' rows lie as the scratch's do
+      float4* const out = reinterpret_cast<float4*>(part.bc + (tile * part.rows + rb + t0) * 2 * N);
+      const float4* const in = reinterpret_cast<const float4*>(smem + L.bc);
+      for (int i = tid; i < nt * 2 * N / 4; i += NT) {
+        float4 q = in[i];
+#pragma unroll
+        for (int k = 1; k < kParts; ++k) {
+          const float4 e = in[k * kChunk * 2 * N / 4 + i];
+          q.x += e.x; q.y += e.y; q.z += e.z; q.w += e.w;
+        }
+        out[i] = q;
+      }
+    }
     // Gradients of the tokens' arrays.
 #pragma unroll
     for (int i = tid; i < kChunk * VPR; i += NT) {
@@ -422,12 +454,13 @@ __global__ void __launch_bounds__(32 * W) palimpsa_scan_bwd_kernel(ScanArgs a, P
         const int o = (v * VN + k0) ^ 4 * (t & 1);
         float sums[3][4] = {};
 #pragma unroll
-        for (int wp = 0; wp < W; ++wp)
+        for (int wp = 0; wp < W / kParts; ++wp)  // the warps of the channels' part
 #pragma unroll
           for (int r = 0; r < 3; ++r) {
+            const int dd = v * VN + k0;
             const float4 q = *reinterpret_cast<const float4*>(
-                smem + L.win + wp * (kWins * L.slot(N, W)) + (t / kWin) * L.slot(N, W) +
-                ((r * kWin + t % kWin) * CH + o) * 4);
+                smem + L.win + ((wp * kParts + dd / (16 * CP)) * kWins + t / kWin) * L.slot(N) +
+                ((r * kWin + t % kWin) * 16 * CP + dd % (16 * CP)) * 4);
             sums[r][0] += q.x; sums[r][1] += q.y; sums[r][2] += q.z; sums[r][3] += q.w;
           }
         const float4 s4 = *reinterpret_cast<const float4*>(fs + t * CH + o);
@@ -458,13 +491,17 @@ __global__ void __launch_bounds__(32 * W) palimpsa_scan_bwd_kernel(ScanArgs a, P
       *reinterpret_cast<uint4*>(static_cast<char*>(a.ddt) + to) = V::pack(ddt);
       if (gated) *reinterpret_cast<uint4*>(static_cast<char*>(a.dz) + to) = V::pack(z);
     }
+    if (kStages == 1) {
+      cta_sync<W>();
+      stage(c + 1);
+    }
   }
   if (bad) latch_status(a.status, kStatusDomain);
 
   const size_t ns = (size_t)(n * a.nseg + seg);
 #pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    if (4 * cl + c >= nch) continue;
+  for (int c = 0; c < CPC; ++c) {
+    if (d0 + c >= nch) continue;
     float q[NS];
 #pragma unroll
     for (int j = 0; j < NS; ++j) q[j] = -(c & 1 ? dA[c / 2][j].y : dA[c / 2][j].x);
@@ -543,37 +580,37 @@ __global__ void __launch_bounds__(256) palimpsa_scan_bwd_par_kernel(ScanArgs a, 
 
 long long total_rows(const ScanArgs& a) { return a.rows.cu ? a.rows.T : (long long)a.rows.n_seq * a.rows.T; }
 
-template <bool BF16, int NS, int W>
+template <bool BF16, int N>
 cudaError_t prepare() {
-  constexpr Smem L(4 * NS * W, W, Vec<BF16>::bytes);
+  constexpr Smem L(N, Vec<BF16>::bytes);
   if (L.total <= 48 * 1024) return cudaSuccess;
-  return cudaFuncSetAttribute(palimpsa_scan_bwd_kernel<BF16, NS, W>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  return cudaFuncSetAttribute(palimpsa_scan_bwd_kernel<BF16, N>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               L.total);
 }
 
 // CTAs that an SM holds (from the occupancy calculator, once per kernel); 0 on failure.
-template <bool BF16, int NS, int W>
+template <bool BF16, int N>
 int resident() {
   static std::atomic<int> known{0};
   int r = known.load(std::memory_order_relaxed);
   if (r > 0) return r;
-  constexpr Smem L(4 * NS * W, W, Vec<BF16>::bytes);
-  if (prepare<BF16, NS, W>() != cudaSuccess ||
-      cudaOccupancyMaxActiveBlocksPerMultiprocessor(&r, palimpsa_scan_bwd_kernel<BF16, NS, W>, 32 * W, L.total) !=
+  constexpr Smem L(N, Vec<BF16>::bytes);
+  if (prepare<BF16, N>() != cudaSuccess ||
+      cudaOccupancyMaxActiveBlocksPerMultiprocessor(&r, palimpsa_scan_bwd_kernel<BF16, N>, 32 * warps(N), L.total) !=
           cudaSuccess)
     return 0;
   known.store(r, std::memory_order_relaxed);
   return r;
 }
 
-template <bool BF16, int NS, int W>
+template <bool BF16, int N>
 cudaError_t run(const ScanArgs& a, const Partials& part, cudaStream_t s) {
-  constexpr Smem L(4 * NS * W, W, Vec<BF16>::bytes);
+  constexpr Smem L(N, Vec<BF16>::bytes);
   const long long tiles = scan_tiles(a), blocks = tiles * a.rows.n_seq * a.nseg;
   if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
-  cudaError_t e = prepare<BF16, NS, W>();
+  cudaError_t e = prepare<BF16, N>();
   if (e != cudaSuccess) return e;
-  palimpsa_scan_bwd_kernel<BF16, NS, W><<<(unsigned)blocks, 32 * W, L.total, s>>>(a, part, (int)tiles);
+  palimpsa_scan_bwd_kernel<BF16, N><<<(unsigned)blocks, 32 * warps(N), L.total, s>>>(a, part, (int)tiles);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const long long bct = (long long)a.rows.n_seq * a.rows.max_len * a.G * (2 * a.N / 4);
@@ -611,21 +648,21 @@ cudaError_t launch_scan_backward(const ScanArgs& a, float* scratch, cudaStream_t
     if (e != cudaSuccess) return e;
   }
   switch (a.N) {
-    case 8: return a.bf16 ? run<true, 2, 1>(a, part, s) : run<false, 2, 1>(a, part, s);
-    case 16: return a.bf16 ? run<true, 4, 1>(a, part, s) : run<false, 4, 1>(a, part, s);
-    case 32: return a.bf16 ? run<true, 4, 2>(a, part, s) : run<false, 4, 2>(a, part, s);
-    case 64: return a.bf16 ? run<true, 4, 4>(a, part, s) : run<false, 4, 4>(a, part, s);
-    default: return a.bf16 ? run<true, 4, 8>(a, part, s) : run<false, 4, 8>(a, part, s);
+    case 8: return a.bf16 ? run<true, 8>(a, part, s) : run<false, 8>(a, part, s);
+    case 16: return a.bf16 ? run<true, 16>(a, part, s) : run<false, 16>(a, part, s);
+    case 32: return a.bf16 ? run<true, 32>(a, part, s) : run<false, 32>(a, part, s);
+    case 64: return a.bf16 ? run<true, 64>(a, part, s) : run<false, 64>(a, part, s);
+    default: return a.bf16 ? run<true, 128>(a, part, s) : run<false, 128>(a, part, s);
   }
 }
 
 int scan_backward_resident(const ScanArgs& a) {
   switch (a.N) {
-    case 8: return a.bf16 ? resident<true, 2, 1>() : resident<false, 2, 1>();
-    case 16: return a.bf16 ? resident<true, 4, 1>() : resident<false, 4, 1>();
-    case 32: return a.bf16 ? resident<true, 4, 2>() : resident<false, 4, 2>();
-    case 64: return a.bf16 ? resident<true, 4, 4>() : resident<false, 4, 4>();
-    default: return a.bf16 ? resident<true, 4, 8>() : resident<false, 4, 8>();
+    case 8: return a.bf16 ? resident<true, 8>() : resident<false, 8>();
+    case 16: return a.bf16 ? resident<true, 16>() : resident<false, 16>();
+    case 32: return a.bf16 ? resident<true, 32>() : resident<false, 32>();
+    case 64: return a.bf16 ? resident<true, 64>() : resident<false, 64>();
+    default: return a.bf16 ? resident<true, 128>() : resident<false, 128>();
   }
 }
 

@@ -416,14 +416,14 @@ cudaError_t plan_scan(ScanArgs* a, bool backward) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  const long long warps = scan_tiles(*a) * a->rows.n_seq * std::max(1, a->N / 16);
+  const long long ctas = scan_tiles(*a) * a->rows.n_seq;
   const int len = a->rows.max_len;
   a->nseg = 1;
   a->seg_len = std::max(len, 1);
-  // Segments for one wave of CTAs: the warps that an SM holds, in every SM.
-  const int held = backward ? scan_backward_resident(*a) * std::max(1, a->N / 16) : kWarpsPerSM;
+  // Segments for one wave of CTAs, as many as every SM holds.
+  const int held = backward ? scan_backward_resident(*a) : kWarpsPerSM / std::max(1, a->N / 16);
   if (held < 1) return cudaErrorInvalidConfiguration;
-  long long want = (long long)held * sms / warps;
+  long long want = (long long)held * sms / ctas;
   // The forward's split does nearly twice the work: it pays from 3 segments on. Pass A
   // is a small part of a backward.
   if (!backward && want < 3) want = 1;

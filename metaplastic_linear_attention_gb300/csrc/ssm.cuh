@@ -116,7 +116,7 @@ cudaError_t launch_scan_step(const ScanArgs& a, cudaStream_t s);
 // dB and dC and the per-segment sums of the parameters' gradients.
 size_t scan_backward_scratch_floats(const ScanArgs& a);
 cudaError_t launch_scan_backward(const ScanArgs& a, float* scratch, cudaStream_t s);
-int scan_backward_resident(const ScanArgs& a);  // CTAs of it that an SM holds; 0 on failure
+int scan_backward_resident(const ScanArgs& a);  // CTAs that an SM holds; 0 on failure
 // Pass A of the backward's time split: each segment's gradient with respect to the
 // state before it, from a zero gradient after it, and its sum of step sizes.
 cudaError_t launch_scan_reverse_summary(const ScanArgs& a, cudaStream_t s);
