@@ -523,12 +523,12 @@ palimpsa_scan_bwd_kernel(ScanArgs a, Partials part, int tiles) {
   }
 }
 
-// dB, dC: sum over the tiles of a group, in the input type. One thread per 4
-// values of a row's [2][N].
+// The sums that the tiles and segments left, in one launch: CTAs 0 .. bc_ctas - 1 add
+// up dB and dC over the tiles of a group (one thread per 4 values of a row's [2][N]),
+// the next dA_ctas add up dA over sequences and segments, the rest dskip and ddt_bias.
 template <bool BF16>
-__global__ void __launch_bounds__(256) palimpsa_scan_bwd_bc_kernel(ScanArgs a, Partials part, int tpg) {
+__device__ __forceinline__ void sum_bc(const ScanArgs& a, const Partials& part, int tpg, long long i) {
   const int per = 2 * a.N / 4;  // threads of a row and group
-  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
   const int q = (int)(i % per), g = (int)(i / per % a.G);
   const long long r = i / per / a.G;
   if (r >= (long long)a.rows.n_seq * a.rows.max_len) return;
@@ -538,9 +538,12 @@ __global__ void __launch_bounds__(256) palimpsa_scan_bwd_bc_kernel(ScanArgs a, P
   int len;
   if (!seq_rows(a.rows, n, &row0, &len) || t >= len) return;
   const long long row = row0 + t;
+  const float* const p = part.bc + ((long long)g * tpg * part.rows + row) * 2 * a.N + 4 * q;
+  const long long stride = part.rows * 2 * a.N;
   float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
   for (int k = 0; k < tpg; ++k) {
-    const float4 v = *reinterpret_cast<const float4*>(part.bc + ((g * tpg + k) * part.rows + row) * 2 * a.N + 4 * q);
+    const float4 v = *reinterpret_cast<const float4*>(p + k * stride);
     s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
   }
   const int half = q >= per / 2;
@@ -553,14 +556,14 @@ __global__ void __launch_bounds__(256) palimpsa_scan_bwd_bc_kernel(ScanArgs a, P
     *reinterpret_cast<float4*>(static_cast<float*>(out) + at) = s;
 }
 
-// dA, or dskip and ddt_bias: sum over sequences and segments. The `per` values of
-// one (sequence, segment) lie together in `p`, the first `split` of them for out and
-// the others for out2 (either may be null). 32 values by 8 slices of the sum to a CTA.
-__global__ void __launch_bounds__(256) palimpsa_scan_bwd_par_kernel(ScanArgs a, const float* p, long long per,
-                                                                    long long split, float* out, float* out2) {
+// The `per` values of one (sequence, segment) lie together in p, the first `split` of
+// them for out and the others for out2 (either may be null). 32 values by 8 slices of the
+// sum to a CTA.
+__device__ __forceinline__ void sum_segments(const ScanArgs& a, long long block, const float* p, long long per,
+                                             long long split, float* out, float* out2) {
   __shared__ float red[8][33];
   const int cx = threadIdx.x % 32, sy = threadIdx.x / 32;
-  const long long e = (long long)blockIdx.x * 32 + cx;
+  const long long e = block * 32 + cx;
   float s = 0.f;
   for (long long n = sy; n < a.rows.n_seq; n += 8) {
     long long row0;
@@ -568,6 +571,7 @@ __global__ void __launch_bounds__(256) palimpsa_scan_bwd_par_kernel(ScanArgs a, 
     if (!seq_rows(a.rows, n, &row0, &len)) continue;
     const int ns = max(1, (len + a.seg_len - 1) / a.seg_len);
     if (e < per)
+#pragma unroll 4
       for (int k = 0; k < ns; ++k) s += p[(n * a.nseg + k) * per + e];
   }
   red[sy][cx] = s;
@@ -576,6 +580,16 @@ __global__ void __launch_bounds__(256) palimpsa_scan_bwd_par_kernel(ScanArgs a, 
   for (int k = 1; k < 8; ++k) s += red[k][cx];
   if (e >= split) out = out2 ? out2 - split : nullptr;
   if (out) out[e] = s;
+}
+
+template <bool BF16>
+__global__ void __launch_bounds__(256) palimpsa_scan_bwd_sum_kernel(ScanArgs a, Partials part, int tpg, unsigned bc_ctas,
+                                                                    unsigned dA_ctas) {
+  const unsigned b = blockIdx.x;
+  const long long dn = (long long)a.D * a.N;
+  if (b < bc_ctas) sum_bc<BF16>(a, part, tpg, (long long)b * 256 + threadIdx.x);
+  else if (b < bc_ctas + dA_ctas) sum_segments(a, b - bc_ctas, part.dA, dn, dn, a.dA, nullptr);
+  else sum_segments(a, b - bc_ctas - dA_ctas, part.par, 2ll * a.D, a.D, a.dskip, a.ddt_bias);
 }
 
 long long total_rows(const ScanArgs& a) { return a.rows.cu ? a.rows.T : (long long)a.rows.n_seq * a.rows.T; }
@@ -613,17 +627,11 @@ cudaError_t run(const ScanArgs& a, const Partials& part, cudaStream_t s) {
   palimpsa_scan_bwd_kernel<BF16, N><<<(unsigned)blocks, 32 * warps(N), L.total, s>>>(a, part, (int)tiles);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  const long long bct = (long long)a.rows.n_seq * a.rows.max_len * a.G * (2 * a.N / 4);
-  if (bct > 0) {
-    const long long bb = (bct + 255) / 256;
-    if (bb > 0x7fffffffll) return cudaErrorInvalidConfiguration;
-    palimpsa_scan_bwd_bc_kernel<BF16>
-        <<<(unsigned)bb, 256, 0, s>>>(a, part, (int)(tiles / a.G));
-  }
-  const long long dn = (long long)a.D * a.N;
-  palimpsa_scan_bwd_par_kernel<<<(unsigned)((dn + 31) / 32), 256, 0, s>>>(a, part.dA, dn, dn, a.dA, nullptr);
-  palimpsa_scan_bwd_par_kernel<<<(unsigned)((2 * a.D + 31) / 32), 256, 0, s>>>(a, part.par, 2ll * a.D, a.D,
-                                                                             a.dskip, a.ddt_bias);
+  const long long bc_ctas = ((long long)a.rows.n_seq * a.rows.max_len * a.G * (2 * a.N / 4) + 255) / 256;
+  const long long dA_ctas = ((long long)a.D * a.N + 31) / 32, par_ctas = (2 * a.D + 31) / 32;
+  if (bc_ctas + dA_ctas + par_ctas > 0x7fffffffll) return cudaErrorInvalidConfiguration;
+  palimpsa_scan_bwd_sum_kernel<BF16><<<(unsigned)(bc_ctas + dA_ctas + par_ctas), 256, 0, s>>>(
+      a, part, (int)(tiles / a.G), (unsigned)bc_ctas, (unsigned)dA_ctas);
   return cudaGetLastError();
 }
 

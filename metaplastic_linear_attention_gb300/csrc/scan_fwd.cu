@@ -43,6 +43,7 @@ constexpr int kStages = 2;   // chunks in the ring of raw inputs
 constexpr int CH = kScanChannels;
 constexpr int kGroup = 8;    // tokens whose y is stored together
 constexpr int kWarpsPerSM = 16;
+constexpr int BWAVES = 1;
 
 // What a launch computes: the scan; pass A of its time split; or pass A of the
 // backward's, which runs from the last token to the first with dy silu(z) in the
@@ -373,14 +374,26 @@ __global__ void __launch_bounds__(256) palimpsa_scan_carry_kernel(ScanArgs a, bo
   const float A = -kLog2e * a.A[e];
   const float* const init = reverse ? a.dh_T : a.h0;
   float h = init ? init[n * per + e] : 0.f;
-  float* const st = a.seg_state + n * a.nseg * per + e;
-  const float* const sd = a.seg_dt + n * a.nseg * a.D + d;
-  for (int k = 0; k < ns; ++k) {
-    const int s = reverse ? ns - 1 - k : k;
-    const float add = k + 1 < ns ? st[s * per] : 0.f;
-    const float dec = k + 1 < ns ? ex2_approx(A * sd[(long long)s * a.D]) : 0.f;
-    st[s * per] = h;
-    h = fmaf(dec, h, add);
+  // 8 segments at a time, their loads first: a store would hold back the next segment's.
+  const long long step = reverse ? -1 : 1;
+  float* st = a.seg_state + (n * a.nseg + (reverse ? ns - 1 : 0)) * per + e;
+  const float* sd = a.seg_dt + (n * a.nseg + (reverse ? ns - 1 : 0)) * a.D + d;
+  for (int k0 = 0; k0 < ns; k0 += 8) {
+    float add[8], sum[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const bool more = k0 + k + 1 < ns;  // the last one's summary is not needed (nor there)
+      add[k] = more ? st[k * step * per] : 0.f;
+      sum[k] = more ? sd[k * step * a.D] : 0.f;
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      if (k0 + k >= ns) break;
+      st[k * step * per] = h;
+      h = fmaf(ex2_approx(A * sum[k]), h, add[k]);
+    }
+    st += 8 * step * per;
+    sd += 8 * step * a.D;
   }
 }
 
@@ -423,7 +436,8 @@ cudaError_t plan_scan(ScanArgs* a, bool backward) {
   // Segments for one wave of CTAs, as many as every SM holds.
   const int held = backward ? scan_backward_resident(*a) : kWarpsPerSM / std::max(1, a->N / 16);
   if (held < 1) return cudaErrorInvalidConfiguration;
-  long long want = (long long)held * sms / ctas;
+  const int waves = backward ? BWAVES : 1;
+  long long want = (long long)held * sms * waves / ctas;
   // The forward's split does nearly twice the work: it pays from 3 segments on. Pass A
   // is a small part of a backward.
   if (!backward && want < 3) want = 1;
