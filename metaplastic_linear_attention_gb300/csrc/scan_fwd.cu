@@ -13,14 +13,19 @@
 //   Lanes that share 4 states are neighbours (8 lanes, 32 channels), so a B or C
 //   load is one broadcast per quarter warp, shared by 4 channels; a step size
 //   serves 4 states;
-// * step sizes, s x and B, C become fp32 in shared memory once per chunk of 16
-//   tokens, each value by one lane;
-// * y's sum over a warp's 16 states is a reduce-scatter over its 4 lane groups (3
-//   shuffles for 4 channels); more than 16 states are shared out over warps and
-//   summed with the gate and the skip term when the chunk is stored;
-// * inputs arrive through a ring of asynchronous 16-byte copies, two chunks ahead.
+// * inputs arrive in chunks of 8 tokens by asynchronous 16-byte copies, a chunk ahead;
+//   step sizes and s x become fp32 in shared memory once, each by one lane (B and C stay
+//   as they came: a lane unpacks its 4);
+// * the lane groups' parts of y (4 states each, of all warps) are stored after the chunk's
+//   tokens and summed, with the skip term and the gate, when y is written. (Shuffles in
+//   place of these stores took twice the time: their latency stood in every token.)
 // A tile is 32 channels of one group, all states, one sequence (or a segment of
-// one), by one CTA of N / 16 warps.
+// one), by one CTA of N / 16 warps; a single warp needs no barriers. 16 warps of 128
+// registers fill an SM. Tried and slower: 8 channels a lane (11 warps), the next
+// chunk's conversion among this one's tokens, warps of their own for the conversions.
+// Measured (GB300, bf16, N = 16, gate): 1.3 clocks per channel-token and SM for the
+// scan itself and 0.9 for pass A, two thirds of the issue slots busy: 298 and 204 us at
+// 1 x 32768 x 2048, where half a clock would be 113.
 //
 // Time split. Where the tiles are too few for the GPU, each sequence is cut into
 // segments: pass A runs the recurrence of every segment but the last from zero
@@ -28,9 +33,7 @@
 // exp(-A sum)); the carry kernel folds them into start states; pass C runs every
 // segment from its own.
 //
-// Rounding: states, sums and step sizes are fp32; y is rounded to the input
-// type once. 2^x is the SFU's (measured bias about -2e-8 a token for decays near
-// 1, so a state with a window of w tokens is off by about 2e-8 w).
+// Rounding: states, sums and step sizes are fp32; y is rounded to the input type once.
 #include <algorithm>
 
 #include "ssm.cuh"
@@ -43,7 +46,6 @@ constexpr int kStages = 2;   // chunks in the ring of raw inputs
 constexpr int CH = kScanChannels;
 constexpr int kGroup = 8;    // tokens whose y is stored together
 constexpr int kWarpsPerSM = 16;
-constexpr int BWAVES = 1;
 
 // What a launch computes: the scan; pass A of its time split; or pass A of the
 // backward's, which runs from the last token to the first with dy silu(z) in the
@@ -214,11 +216,12 @@ __global__ void __launch_bounds__(32 * W, kWarpsPerSM / W) palimpsa_scan_kernel(
   auto store_state = [&](float* out) {
 #pragma unroll
     for (int c = 0; c < 4; ++c)
-      if (4 * cl + c < nch)
+      if (4 * cl + c < nch) {
+        float q[NS];
 #pragma unroll
-        for (int j = 0; j < NS; j += 2)
-          *reinterpret_cast<float2*>(out + at + c * N + j) =
-              c & 1 ? make_float2(h[c / 2][j].y, h[c / 2][j + 1].y) : make_float2(h[c / 2][j].x, h[c / 2][j + 1].x);
+        for (int j = 0; j < NS; ++j) q[j] = c & 1 ? h[c / 2][j].y : h[c / 2][j].x;
+        store_own<NS>(reinterpret_cast<unsigned char*>(out + at + c * N), q);
+      }
   };
   // One token; y gets this lane's part of its channels' y.
   auto token = [&](const unsigned char* st, int t, float2* y) {
@@ -429,18 +432,24 @@ cudaError_t plan_scan(ScanArgs* a, bool backward) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  const long long ctas = scan_tiles(*a) * a->rows.n_seq;
   const int len = a->rows.max_len;
   a->nseg = 1;
   a->seg_len = std::max(len, 1);
-  // Segments for one wave of CTAs, as many as every SM holds.
+  // CTAs that an SM holds, and CTAs with work: of a packed batch, as many sequences of the
+  // longest's length as its rows make.
   const int held = backward ? scan_backward_resident(*a) : kWarpsPerSM / std::max(1, a->N / 16);
   if (held < 1) return cudaErrorInvalidConfiguration;
-  const int waves = backward ? BWAVES : 1;
-  long long want = (long long)held * sms * waves / ctas;
-  // The forward's split does nearly twice the work: it pays from 3 segments on. Pass A
-  // is a small part of a backward.
+  const long long slots = (long long)held * sms, tiles = scan_tiles(*a);
+  const long long seqs = a->rows.cu ? std::max(1, (int)(((long long)a->rows.T + len - 1) / std::max(len, 1))) : a->rows.n_seq;
+  // Segments for one wave of CTAs; the backward for two, whose pass A then has CTAs
+  // enough (35 us against 45 at 4 x 2048 x 1024, the rest alike). The forward's split does
+  // nearly twice the work and pays from 3 segments on (N = 16, 1 x 32768 x 2048: 0.52 ms
+  // against 6.4; 8 x 4096 x 1536: 0.41 against 0.97). Pass A is a small part of a backward.
+  long long want = (backward ? 2 : 1) * slots / (tiles * seqs);
   if (!backward && want < 3) want = 1;
+  // CTAs of segments past their sequence's end only look and leave, but they and their
+  // scratch are kept to 16 waves.
+  want = std::min(want, std::max(1ll, 16 * slots / (tiles * a->rows.n_seq)));
   want = std::min<long long>(want, len / 64);
   if (want >= 2) {
     const int per = (int)((len + want - 1) / want);
