@@ -369,6 +369,16 @@ __global__ void __launch_bounds__(256) palimpsa_conv_bwd_sum_kernel(const float*
   }
 }
 
+__global__ void __launch_bounds__(256) palimpsa_zero_outside_kernel(ZeroArgs a) {
+  const long long T = a.rows.T, w = a.width[blockIdx.y] / 16;
+  const long long lo = min(max((long long)a.rows.cu[0], 0ll), T);
+  const long long hi = min(max((long long)a.rows.cu[a.rows.n_seq], lo), T);
+  uint4* const p = static_cast<uint4*>(a.p[blockIdx.y]);
+  const long long step = (long long)gridDim.x * 256, i0 = (long long)blockIdx.x * 256 + threadIdx.x;
+  for (long long i = i0; i < lo * w; i += step) p[i] = make_uint4(0, 0, 0, 0);
+  for (long long i = hi * w + i0; i < T * w; i += step) p[i] = make_uint4(0, 0, 0, 0);
+}
+
 // Tokens of a run: long runs read fewer rows twice, short ones make enough threads.
 // From 64 (forward; backward 32) down to 8 until there are 1024 threads (512) for each
 // of 152 SMs.
@@ -422,6 +432,11 @@ cudaError_t step(const ConvArgs& a, cudaStream_t s) {
     default: return a.bf16 ? f<true, 4>(__VA_ARGS__) : f<false, 4>(__VA_ARGS__); \
   }
 
+cudaError_t launch_zero_outside(const ZeroArgs& a, int n, cudaStream_t s) {
+  if (n == 0 || a.rows.T == 0) return cudaSuccess;
+  palimpsa_zero_outside_kernel<<<dim3(152, n), 256, 0, s>>>(a);
+  return cudaGetLastError();
+}
 cudaError_t launch_conv_forward(const ConvArgs& a, cudaStream_t s) { PALIMPSA_CONV_DISPATCH(forward, a, s) }
 cudaError_t launch_conv_step(const ConvArgs& a, cudaStream_t s) { PALIMPSA_CONV_DISPATCH(step, a, s) }
 size_t conv_backward_scratch_bytes(const ConvArgs& a) {

@@ -175,7 +175,7 @@ palimpsa_scan_bwd_kernel(ScanArgs a, Partials part, int tiles) {
     for (int j = 0; j < NS; ++j) {
       const float A = in ? a.A[at + c * N + j] : 1.f;
       bad |= !pos_finite(A);
-      (c & 1 ? A2[c / 2][j].y : A2[c / 2][j].x) = -kLog2e * A;
+      (c & 1 ? A2[c / 2][j].y : A2[c / 2][j].x) = decay_rate(A);
       (c & 1 ? gh[c / 2][j].y : gh[c / 2][j].x) = in && g0 ? g0[at + c * N + j] : 0.f;
       dA[c / 2][j] = make_float2(0.f, 0.f);
     }
@@ -396,6 +396,12 @@ palimpsa_scan_bwd_kernel(ScanArgs a, Partials part, int tiles) {
           sum[1][i][2 * p] = qs[p].x; sum[1][i][2 * p + 1] = qs[p].y;
           sum[2][i][2 * p] = ys[p].x; sum[2][i][2 * p + 1] = ys[p].y;
         }
+      }
+      if (nch < CH && d0 >= nch) {  // lanes past the tile's channels: 0, whatever B and C hold
+#pragma unroll
+        for (int i = 0; i < kWin; ++i)
+#pragma unroll
+          for (int j = 0; j < NS; ++j) db[i][j] = dc[i][j] = 0.f;
       }
       // Over the 4 lane groups: group sl ends with token sl, CPC channels a lane.
       __syncwarp();  // every lane has read its states from the slot

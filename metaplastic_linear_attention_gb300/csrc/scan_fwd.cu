@@ -208,7 +208,7 @@ __global__ void __launch_bounds__(32 * W, kWarpsPerSM / W) palimpsa_scan_kernel(
     for (int j = 0; j < NS; ++j) {
       const float A = in ? a.A[at + c * N + j] : 1.f;
       bad |= !pos_finite(A);
-      (c & 1 ? A2[c / 2][j].y : A2[c / 2][j].x) = -kLog2e * A;
+      (c & 1 ? A2[c / 2][j].y : A2[c / 2][j].x) = decay_rate(A);
       (c & 1 ? h[c / 2][j].y : h[c / 2][j].x) = in && h0 ? h0[at + c * N + j] : 0.f;
     }
   }
@@ -374,7 +374,7 @@ __global__ void __launch_bounds__(256) palimpsa_scan_carry_kernel(ScanArgs a, bo
   int len;
   if (!seq_rows(a.rows, n, &row0, &len)) return;
   const int ns = max(1, (len + a.seg_len - 1) / a.seg_len);
-  const float A = -kLog2e * a.A[e];
+  const float A = decay_rate(a.A[e]);
   const float* const init = reverse ? a.dh_T : a.h0;
   float h = init ? init[n * per + e] : 0.f;
   // 8 segments at a time, their loads first: a store would hold back the next segment's.
@@ -450,7 +450,7 @@ cudaError_t plan_scan(ScanArgs* a, bool backward) {
   // CTAs of segments past their sequence's end only look and leave, but they and their
   // scratch are kept to 16 waves.
   want = std::min(want, std::max(1ll, 16 * slots / (tiles * a->rows.n_seq)));
-  want = std::min<long long>(want, len / 64);
+  want = std::min<long long>(want, len / 32);
   if (want >= 2) {
     const int per = (int)((len + want - 1) / want);
     a->seg_len = (per + kScanCheckpoint - 1) / kScanCheckpoint * kScanCheckpoint;

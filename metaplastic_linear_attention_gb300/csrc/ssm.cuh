@@ -46,6 +46,16 @@ cudaError_t launch_conv_step(const ConvArgs& a, cudaStream_t s);
 size_t conv_backward_scratch_bytes(const ConvArgs& a);
 cudaError_t launch_conv_backward(const ConvArgs& a, float* scratch, cudaStream_t s);
 
+// Zeros in the rows before the first and behind the last sequence of a packed batch, of
+// up to kZeroArrays dense arrays (row widths in bytes, multiples of 16).
+constexpr int kZeroArrays = 8;
+struct ZeroArgs {
+  void* p[kZeroArrays];
+  long long width[kZeroArrays];
+  SeqRows rows;
+};
+cudaError_t launch_zero_outside(const ZeroArgs& a, int n, cudaStream_t s);
+
 struct ScanArgs {
   const void* x;
   const void* dt;
@@ -257,6 +267,9 @@ constexpr float kDecayShift = 2.7e-8f;
 __device__ __forceinline__ float2 decay_exponent(float2 s, float2 A2) {
   return __ffma2_rn(s, A2, make_float2(kDecayShift, kDecayShift));
 }
+// A as the decay exponents take it. (A above 2.3e38 would overflow, and a step of size 0
+// would make a NaN of it.)
+__device__ __forceinline__ float decay_rate(float A) { return fmaxf(-kLog2e * A, -3.0e38f); }
 // The larger value, or NaN when one is (fmaxf drops it).
 __device__ __forceinline__ float fmax_nan(float a, float b) {
   float r;

@@ -17,7 +17,8 @@ bool dtype_ok(palimpsa_dtype t) { return t == PALIMPSA_F32 || t == PALIMPSA_BF16
 
 // Sizes of a batch: rows of D channels in n_seq sequences, dense or packed.
 bool rows_ok(const SeqRows& r, int D) {
-  if (r.n_seq < 1 || r.T < 0 || D < 1) return false;
+  // (T leaves room for the rounding up to whole runs and segments in int)
+  if (r.n_seq < 1 || r.T < 0 || r.T > 0x7fff0000 || D < 1) return false;
   if (r.cu && (r.max_len < 0 || r.max_len > r.T)) return false;
   const long long rows = r.cu ? r.T : (long long)r.n_seq * r.T;
   const long long lim = 1LL << 40;
@@ -152,6 +153,24 @@ palimpsa_status palimpsa_causal_conv(const void* x, long long x_stride, const fl
   if (palimpsa_status s = device_status_word(&a.status)) return s;
   return launch_conv_forward(a, static_cast<cudaStream_t>(cuda_stream)) == cudaSuccess ? PALIMPSA_OK
                                                                                      : PALIMPSA_ERR_CUDA;
+}
+
+palimpsa_status palimpsa_zero_rows_outside(void* const* arrays, const long long* row_bytes, int n,
+                                           const int* cu_seqlens, int B, int T, void* cuda_stream) {
+  if (!cu_seqlens || (n > 0 && (!arrays || !row_bytes))) return PALIMPSA_ERR_NULL;
+  if (n < 0 || n > kZeroArrays || B < 1 || T < 0) return PALIMPSA_ERR_SHAPE;
+  if (!aligned(cu_seqlens, 4)) return PALIMPSA_ERR_ALIGN;
+  ZeroArgs a{};
+  a.rows = rows_of(cu_seqlens, B, T, T);
+  for (int i = 0; i < n; ++i) {
+    if (!arrays[i] && T != 0) return PALIMPSA_ERR_NULL;
+    if (row_bytes[i] < 0 || row_bytes[i] > (1LL << 40) / (T > 0 ? T : 1)) return PALIMPSA_ERR_SHAPE;
+    if (!aligned(arrays[i], 16) || row_bytes[i] % 16) return PALIMPSA_ERR_ALIGN;
+    a.p[i] = arrays[i];
+    a.width[i] = row_bytes[i];
+  }
+  return launch_zero_outside(a, n, static_cast<cudaStream_t>(cuda_stream)) == cudaSuccess ? PALIMPSA_OK
+                                                                                        : PALIMPSA_ERR_CUDA;
 }
 
 palimpsa_status palimpsa_causal_conv_step(const void* x, long long x_stride, const float* weight, const float* bias,

@@ -39,6 +39,7 @@ def _library():
             "palimpsa_causal_conv": [p, ll, p, p, p, p, p, p, i, i, i, i, i, u, i, p],
             "palimpsa_causal_conv_step": [p, ll, p, p, p, p, i, i, i, u, i, p],
             "palimpsa_causal_conv_backward": [p, ll, p, p, p, p, ll, p, p, p, p, p, p, i, i, i, i, i, u, i, p],
+            "palimpsa_zero_rows_outside": [p, p, i, p, i, i, p],
             "palimpsa_selective_scan": [p] * 12 + [st, p, i, i, i, i, i, i, u, i, p],
             "palimpsa_selective_scan_step": [p] * 10 + [st, i, i, i, i, u, i, p],
             "palimpsa_selective_scan_backward": [p] * 20 + [st, p, i, i, i, i, i, i, u, i, p],
@@ -50,6 +51,14 @@ def _library():
         lib.palimpsa_selective_scan_checkpoint_bytes.argtypes = [i, i, i, i, i]
         _lib = lib
     return _lib
+
+
+_functions = {}
+
+
+def _function(name):
+    _functions[name] = getattr(_library(), name)
+    return _functions[name]
 
 
 # The checks below run on every decode token, so they are written for speed: a tensor that
@@ -119,7 +128,7 @@ def _call(name, dev, stream, tensors, *args):
     """The library call on the tensors' device, on the caller's stream or the current one. Tensors
     used on a caller's stream are recorded there, so that the allocator keeps them until that
     stream is done."""
-    fn = getattr(_library(), name)
+    fn = _functions.get(name) or _function(name)
     if stream is None and dev == torch.cuda.current_device():
         rc = fn(*args, _raw_stream(dev))
     else:
@@ -145,13 +154,20 @@ def _batch(x, cu_seqlens, max_seqlen, dev, stream, name):
     return n, x.shape[0], longest, cu, 1
 
 
-def _new(t, name, shape, dtype, x, zero=False):
-    """An output on x's device: checked when given, else allocated (zeroed where rows may stay
-    unwritten)."""
+def _new(t, name, shape, dtype, x):
+    """An output on x's device: checked when given, else allocated."""
     if t is None:
-        return (torch.zeros if zero else torch.empty)(shape, dtype=dtype, device=x.device)
+        return torch.empty(shape, dtype=dtype, device=x.device)
     _dense(t, name, shape, dtype, x.get_device())
     return t
+
+
+def _zero_outside(outs, cu, nb, rows, dev, stream):
+    """Zeros in the rows of freshly allocated outputs that no sequence of a packed batch covers."""
+    if cu is not None and outs and rows:
+        p = (ctypes.c_void_p * len(outs))(*(t.data_ptr() for t in outs))
+        w = (ctypes.c_longlong * len(outs))(*(t.numel() // rows * t.element_size() for t in outs))
+        _call("palimpsa_zero_rows_outside", dev, stream, (), p, w, len(outs), cu.data_ptr(), nb, rows)
 
 
 # ------------------------------------------------------------------ causal convolution
@@ -176,8 +192,11 @@ def palimpsa_causal_conv(x, weight, bias=None, state0=None, *, silu=True, cu_seq
     kind = _dtype(x)
     ld = _rows(x, "x", x.shape, x.dtype, dev, lead)
     ps = _dense(state0, "state0", (B, W - 1, D), x.dtype, dev)
-    y = _new(y, "y", x.shape, x.dtype, x, cu is not None)
+    fresh = y is None
+    y = _new(y, "y", x.shape, x.dtype, x)
     state_T = _new(state_T, "state_T", (B, W - 1, D), x.dtype, x)
+    if fresh:
+        _zero_outside((y,), cu, B, T, dev, stream)
     _call(name, dev, stream, (x, weight, bias, state0, y, state_T, cu),
           x.data_ptr(), ld, pw, pb, ps, y.data_ptr(), state_T.data_ptr(), _ptr(cu), B, T, longest, D, W,
           PALIMPSA_CONV_SILU if silu else 0, kind)
@@ -215,11 +234,12 @@ def palimpsa_causal_conv_backward(x, weight, bias, state0, dy, dstate_T=None, *,
     ldy = _rows(dy, "dy", x.shape, dtype, dev, lead)
     ps = _dense(state0, "state0", (B, W - 1, D), dtype, dev)
     pd = _dense(dstate_T, "dstate_T", (B, W - 1, D), dtype, dev)
-    # rows outside every sequence, and a sequence that is skipped for its offsets, stay zero
-    g = {"dx": _new(None, "dx", x.shape, dtype, x, cu is not None),
+    g = {"dx": _new(None, "dx", x.shape, dtype, x),
          "dweight": _new(None, "dweight", (D, W), F32, x), "dbias": _new(None, "dbias", (D,), F32, x)}
     if want_state_grad:
-        g["dstate0"] = _new(None, "dstate0", (B, W - 1, D), dtype, x, cu is not None)
+        # a sequence that is skipped for its offsets leaves its part as it is: zeros
+        g["dstate0"] = (torch.empty if cu is None else torch.zeros)((B, W - 1, D), dtype=dtype, device=x.device)
+    _zero_outside((g["dx"],), cu, B, T, dev, stream)
     _call(name, dev, stream, (x, weight, bias, state0, dy, dstate_T, cu, *g.values()),
           x.data_ptr(), ld, pw, pb, ps, dy.data_ptr(), ldy, pd, g["dx"].data_ptr(), g["dweight"].data_ptr(),
           g["dbias"].data_ptr(), _ptr(g.get("dstate0")), _ptr(cu), B, T, longest, D, W,
@@ -238,12 +258,21 @@ def _scan_inputs(x, dt, A, B, C, D, z, dt_bias, dev, lead, dy=None):
     ch, n = A.shape
     groups = B.shape[-2]
     bc = shape[:-1] + (groups, n)
-    ld = (_rows(x, "x", shape[:-1] + (ch,), kind, dev, lead), _rows(dt, "dt", shape, kind, dev, lead),
-          _rows(B, "B", bc, kind, dev, lead), _rows(C, "C", bc, kind, dev, lead),
-          _rows(z, "z", shape, kind, dev, lead), _rows(dy, "dy", shape, kind, dev, lead))
+    if (shape[-1] == ch and x.is_contiguous()
+            and dt.dtype is kind and dt.shape == shape and dt.get_device() == dev and dt.is_contiguous()
+            and B.dtype is kind and B.shape == bc and B.get_device() == dev and B.is_contiguous()
+            and C.dtype is kind and C.shape == bc and C.get_device() == dev and C.is_contiguous()
+            and (z is None or (z.dtype is kind and z.shape == shape and z.get_device() == dev and z.is_contiguous()))
+            and (dy is None or (dy.dtype is kind and dy.shape == shape and dy.get_device() == dev
+                                and dy.is_contiguous()))):
+        ld = None
+    else:
+        ld = (_rows(x, "x", shape[:-1] + (ch,), kind, dev, lead), _rows(dt, "dt", shape, kind, dev, lead),
+              _rows(B, "B", bc, kind, dev, lead), _rows(C, "C", bc, kind, dev, lead),
+              _rows(z, "z", shape, kind, dev, lead), _rows(dy, "dy", shape, kind, dev, lead))
     ptrs = (x.data_ptr(), dt.data_ptr(), _dense(A, "A", (ch, n), F32, dev), B.data_ptr(), C.data_ptr(),
             _dense(D, "D", (ch,), F32, dev), _ptr(z), _dense(dt_bias, "dt_bias", (ch,), F32, dev))
-    return ch, groups, n, ctypes.byref(_Strides(*ld)) if any(ld) else None, ptrs
+    return ch, groups, n, None if ld is None else ctypes.byref(_Strides(*ld)), ptrs
 
 
 def palimpsa_selective_scan_checkpoint_shape(batch, tokens, channels, states, packed=False):
@@ -260,7 +289,10 @@ def _scan(name, x, dt, A, B, C, D, z, dt_bias, h0, softplus, cu_seqlens, max_seq
     ch, groups, n, strides, ptrs = _scan_inputs(x, dt, A, B, C, D, z, dt_bias, dev, lead)
     kind = _dtype(x)
     p0 = _dense(h0, "h0", (nb, ch, n), F32, dev)
-    y = _new(y, "y", x.shape, x.dtype, x, cu is not None)
+    fresh = y is None
+    y = _new(y, "y", x.shape, x.dtype, x)
+    if fresh:
+        _zero_outside((y,), cu, nb, T, dev, stream)
     h_T = _new(h_T, "h_T", (nb, ch, n), F32, x)
     if want_ckpt:
         ckpt = _new(ckpt, "ckpt", palimpsa_selective_scan_checkpoint_shape(nb, T, ch, n, cu is not None), F32, x)
@@ -305,17 +337,20 @@ def palimpsa_selective_scan_backward(x, dt, A, B, C, D, z, dt_bias, h0, ckpt, dy
     _dense(h0, "h0", (nb, ch, n), F32, dev)
     pg = _dense(dh_T, "dh_T", (nb, ch, n), F32, dev)
     pc = _dense(ckpt, "ckpt", palimpsa_selective_scan_checkpoint_shape(nb, T, ch, n, packed), F32, dev)
-    g = {"dx": _new(None, "dx", x.shape, dtype, x, packed), "ddt": _new(None, "ddt", x.shape, dtype, x, packed),
-         "dA": _new(None, "dA", (ch, n), F32, x), "dB": _new(None, "dB", B.shape, dtype, x, packed),
-         "dC": _new(None, "dC", B.shape, dtype, x, packed)}
+    at = x.device
+    e = lambda shape, t: torch.empty(shape, dtype=t, device=at)  # noqa: E731
+    g = {"dx": e(x.shape, dtype), "ddt": e(x.shape, dtype), "dA": e((ch, n), F32), "dB": e(B.shape, dtype),
+         "dC": e(B.shape, dtype)}
     if D is not None:
-        g["dD"] = _new(None, "dD", (ch,), F32, x)
+        g["dD"] = e((ch,), F32)
     if z is not None:
-        g["dz"] = _new(None, "dz", x.shape, dtype, x, packed)
+        g["dz"] = e(x.shape, dtype)
     if dt_bias is not None:
-        g["ddt_bias"] = _new(None, "ddt_bias", (ch,), F32, x)
+        g["ddt_bias"] = e((ch,), F32)
     if want_state_grad:
-        g["dh0"] = _new(None, "dh0", (nb, ch, n), F32, x, packed)
+        # a sequence that is skipped for its offsets leaves its part as it is: zeros
+        g["dh0"] = torch.zeros((nb, ch, n), dtype=F32, device=at) if packed else e((nb, ch, n), F32)
+    _zero_outside([g[k] for k in ("dx", "ddt", "dz", "dB", "dC") if k in g], cu, nb, T, dev, stream)
     at = {k: v.data_ptr() for k, v in g.items()}
     _call(name, dev, stream, (x, dt, A, B, C, D, z, dt_bias, ckpt, dy, dh_T, cu, *g.values()),
           *ptrs, pc, dy.data_ptr(), pg, at["dx"], at["ddt"], at["dA"], at["dB"], at["dC"], at.get("dD"), at.get("dz"),

@@ -68,7 +68,7 @@ def test_common_refusals(lib, name, over, code):
 
 @pytest.mark.parametrize("name", PACKED)
 @pytest.mark.parametrize("over,code", [
-    (dict(T=-1), ERR_SHAPE), (dict(cu=P, max_seqlen=17), ERR_SHAPE), (dict(cu=P, max_seqlen=-1), ERR_SHAPE),
+    (dict(T=-1), ERR_SHAPE), (dict(T=0x7fffffff, B=1, D=8), ERR_SHAPE), (dict(cu=P, max_seqlen=17), ERR_SHAPE), (dict(cu=P, max_seqlen=-1), ERR_SHAPE),
     (dict(cu=P + 2), ERR_ALIGN),
 ])
 def test_batch_refusals(lib, name, over, code):
@@ -101,6 +101,18 @@ def test_scan_refusals(lib, name, over, code):
 def test_scan_stride_refusals(lib, name, field, given, code):
     st = ssm._Strides(**{field: given})
     assert _call(lib, name, strides=ctypes.byref(st)) == code
+
+
+@pytest.mark.parametrize("over,code", [
+    (dict(cu=None), ERR_NULL), (dict(arrays=None), ERR_NULL), (dict(p=[P, 0]), ERR_NULL), (dict(n=9), ERR_SHAPE),
+    (dict(n=-1), ERR_SHAPE), (dict(B=0), ERR_SHAPE), (dict(T=-1), ERR_SHAPE), (dict(p=[P, P + 8]), ERR_ALIGN),
+    (dict(w=[16, 24]), ERR_ALIGN), (dict(w=[16, -16]), ERR_SHAPE), (dict(cu=P + 1), ERR_ALIGN),
+])
+def test_zero_rows_outside_refusals(lib, over, code):
+    a = dict(p=[P, P], w=[16, 32], n=2, cu=P, B=3, T=100, arrays=True) | over
+    p = (ctypes.c_void_p * 2)(*a["p"]) if a["arrays"] else None
+    w = (ctypes.c_longlong * 2)(*a["w"])
+    assert lib.palimpsa_zero_rows_outside(p, w, a["n"], a["cu"], a["B"], a["T"], None) == code
 
 
 def test_checkpoint_bytes(lib):

@@ -282,6 +282,24 @@ def test_rows_of_a_wider_projection():
     _status()
 
 
+@pytest.mark.parametrize("cu", [[0, 5, 20], [3, 9, 17], [4, 4, 4], [0, 0, 0], [20, 20, 20]])
+def test_fresh_packed_outputs_are_zero_outside_the_sequences(cu):
+    rows, D, N = 20, 16, 16
+    junk = torch.full((1 << 20,), float("nan"), device=DEV)       # what the allocator hands out again
+    del junk
+    i = _dev(_scan_inputs(2, rows, 2, D, 1, N, BF))
+    kw = dict(cu_seqlens=torch.tensor(cu, dtype=torch.int32, device=DEV), max_seqlen=20)
+    y, _, ck = pal.palimpsa_selective_scan_checkpointed(*i.values(), **kw)
+    g = pal.palimpsa_selective_scan_backward(*i.values(), ck, i["x"], **kw)
+    w = torch.randn(D, 4, device=DEV)
+    u, _ = pal.palimpsa_causal_conv(i["x"], w, **kw)
+    c = pal.palimpsa_causal_conv_backward(i["x"], w, None, None, i["x"], **kw)
+    for t in (y, u, g["dx"], g["ddt"], g["dz"], g["dB"], g["dC"], c["dx"]):
+        assert not t[:cu[0]].any() and not t[cu[-1]:].any()
+        assert torch.isfinite(t).all()
+    _status()
+
+
 def test_empty_prompt_passes_the_state_through():
     h = torch.randn(2, 16, 16, device=DEV)
     e = torch.empty(2, 0, 16, device=DEV)
@@ -378,6 +396,34 @@ def test_extreme_step_sizes_stay_finite():
         _, got = pal.palimpsa_selective_scan(*_dev(_dense(step, 1)).values())
         # expf of 90 is off by 90 x 2^-23 relative; four more roundings
         _near(got, want, 2e-5, f"softplus({raw[t]})")
+
+
+def test_a_step_of_size_zero_leaves_the_state_as_it_is():
+    """softplus(-200) is 0 in fp32: the decay is exactly 1, for the largest A too."""
+    T, D, N = 37, 40, 16
+    i = _scan_inputs(12, T, 1, D, 1, N, F32)
+    i["dt"], i["dt_bias"] = torch.full((T, D), -200.0), None
+    i["A"][0], i["A"][1] = 3e38, 1e-38
+    d = _dev(_dense(i, 1))
+    _, h = pal.palimpsa_selective_scan(*d.values())
+    assert torch.equal(h, d["h0"])
+    tok = {k: (v[:, 0] if k in ("x", "dt", "z", "B", "C") else v) for k, v in d.items()}
+    h = d["h0"].clone()
+    pal.palimpsa_selective_scan_step(tok["x"], tok["dt"], d["A"], tok["B"], tok["C"], h, d["D"], tok["z"])
+    assert torch.equal(h, d["h0"])
+    _status()
+
+
+def test_channels_past_a_tile_add_nothing_to_the_shared_gradients():
+    """40 channels fill a tile and a quarter: infinite reads of a silent token must not turn into NaN there."""
+    T, D, N = 20, 40, 16
+    i = _dev(_dense(_scan_inputs(13, T, 1, D, 1, N, F32, gate=False), 1))
+    i["B"][0, 7, 0, 3] = float("inf")
+    _, _, ck = pal.palimpsa_selective_scan_checkpointed(*i.values())
+    dy = torch.ones(1, T, D, device=DEV)
+    g = pal.palimpsa_selective_scan_backward(*i.values(), ck, dy)
+    want = (ck[:, :1, :, 3] * 0).sum()                     # (the states before it are finite)
+    assert torch.isfinite(want) and torch.isfinite(g["dC"][0, :7]).all() and torch.isfinite(g["dB"]).all()
 
 
 @pytest.mark.parametrize("side", [False, True])
