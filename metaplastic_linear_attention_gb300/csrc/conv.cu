@@ -21,8 +21,8 @@ namespace {
 
 constexpr int kBatch = 8;      // tokens loaded together
 constexpr int kThreads = 128;
-constexpr int kMaxRun = 64, kMinRun = 16;
-constexpr int kCtas = 5;
+constexpr int kMinRun = 16;   // tokens of a run, at least
+constexpr int kCtas = 5;      // of an SM
 
 // Parameters of a thread's 4 channels, as pairs: 4 W neighbouring floats, by 16-byte
 // loads where the array allows it (it only has to be aligned to 4 bytes).
@@ -379,15 +379,35 @@ __global__ void __launch_bounds__(256) palimpsa_zero_outside_kernel(ZeroArgs a) 
   for (long long i = hi * w + i0; i < T * w; i += step) p[i] = make_uint4(0, 0, 0, 0);
 }
 
-// Tokens of a run: long runs read fewer rows twice, short ones make enough threads.
-// From 64 (forward; backward 32) down to 8 until there are 1024 threads (512) for each
-// of 152 SMs.
-int run_len_of(const ConvArgs& a, int longest, long long threads) {
-  int r = longest;
-  while (r > kMinRun && (long long)a.rows.n_seq * ((a.rows.max_len + r - 1) / r) * (a.D / 4) < 152 * threads) r /= 2;
-  return r;
+// Tokens of a run, a multiple of 8: long runs read fewer rows twice and load the taps
+// less often (together about 8 tokens' worth), short ones make CTAs enough, and the CTAs
+// should fill whole waves of the SMs' slots: the cheapest of waves x (run + 8). (With
+// runs of 64, 8 x 4096 x 1536 took 1536 CTAs on 760 slots, a third wave for the last 16.)
+// `threads` of a CTA take a run of 4 channels each.
+int run_len_of(const ConvArgs& a, long long threads, int slots, int shortest) {
+  // Runs with work: of a packed batch, its rows' and one cut short for every sequence.
+  const long long rows = a.rows.cu ? a.rows.T : a.rows.max_len, seqs = a.rows.cu ? 1 : a.rows.n_seq;
+  long long best = 0;
+  int run = shortest;
+  for (int r = shortest; r <= 128; r += 8) {
+    const long long runs = seqs * ((rows + r - 1) / r) + (a.rows.cu ? a.rows.n_seq : 0);
+    const long long ctas = (runs * (a.D / 4) + threads - 1) / threads;
+    const long long cost = (ctas + slots - 1) / slots * (r + 8);
+    if (r == shortest || cost < best) {
+      best = cost;
+      run = r;
+    }
+  }
+  return run;
 }
-int bwd_run_len(const ConvArgs& a) { return run_len_of(a, 64, 256); }
+int sm_count() {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return 152;
+  return sms;
+}
+int bwd_run_len(const ConvArgs& a) { return run_len_of(a, kBwdVecs * kBwdRuns, kBwdCtas * sm_count(), 8); }
 int bwd_blocks_per_seq(const ConvArgs& a, int run) {
   const int per = run * kBwdRuns;
   return std::max(1, (a.rows.max_len + per - 1) / per);
@@ -408,7 +428,7 @@ cudaError_t backward(const ConvArgs& a, float* scratch, cudaStream_t s) {
 
 template <bool BF16, int W>
 cudaError_t forward(const ConvArgs& a, cudaStream_t s) {
-  const int run = run_len_of(a, kMaxRun, 1024), runs = std::max(1, (a.rows.max_len + run - 1) / run);
+  const int run = run_len_of(a, kThreads, kCtas * sm_count(), kMinRun), runs = std::max(1, (a.rows.max_len + run - 1) / run);
   const long long n = (long long)(a.D / 4) * runs * a.rows.n_seq, blocks = (n + kThreads - 1) / kThreads;
   if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
   palimpsa_conv_kernel<BF16, W><<<(unsigned)blocks, kThreads, 0, s>>>(a, runs, run);
