@@ -217,11 +217,14 @@ __device__ __forceinline__ void cp_async16(void* dst, const void* src, bool in) 
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(in ? 16 : 0)
                : "memory");
 }
+__device__ __forceinline__ void cp_async8(void* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
 // NS = 2 or 4 floats: an asynchronous copy of them, and plain loads and stores.
 template <int NS>
 __device__ __forceinline__ void cp_async_states(void* dst, const float* src) {
   if constexpr (NS == 4) cp_async16(dst, src);
-  else asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+  else cp_async8(dst, src);
 }
 template <int NS>
 __device__ __forceinline__ void load_own(float* f, const unsigned char* p) {
