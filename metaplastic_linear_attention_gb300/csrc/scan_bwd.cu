@@ -166,7 +166,7 @@ palimpsa_scan_bwd_kernel(ScanArgs a, Partials part, int tiles) {
   bool bad = false;
   float2 A2[CP][NS], gh[CP][NS], dA[CP][NS];
   const float* g0 = nullptr;
-  if (a.nseg > 1) g0 = a.seg_state + (size_t)(n * a.nseg + seg) * a.D * N;
+  if (a.carried) g0 = a.seg_state + (size_t)(n * a.nseg + seg) * a.D * N;
   else if (a.dh_T) g0 = a.dh_T + (size_t)n * a.D * N;
 #pragma unroll
   for (int c = 0; c < CPC; ++c) {
@@ -180,6 +180,10 @@ palimpsa_scan_bwd_kernel(ScanArgs a, Partials part, int tiles) {
       dA[c / 2][j] = make_float2(0.f, 0.f);
     }
   }
+  const int nsegs = (len + a.seg_len - 1) / a.seg_len;  // the sequence's; the ones after this one's summaries
+  if (seg + 1 < nsegs && !a.carried && d0 < nch)
+    fold_segments<CPC, NS>(gh, A2, a.seg_state + (size_t)(n * a.nseg + nsegs - 1) * a.D * N + at,
+                           a.seg_dt + (size_t)(n * a.nseg + nsegs - 1) * a.D + ch0 + d0, nsegs - 1 - seg, -1, a.D, N);
   for (int c = tid; c < CH; c += NT) {
     fpar[c] = c < nch && a.dt_bias ? a.dt_bias[ch0 + c] : 0.f;
     fpar[CH + c] = c < nch && a.skip ? a.skip[ch0 + c] : 0.f;
@@ -658,7 +662,7 @@ cudaError_t launch_scan_backward(const ScanArgs& a, float* scratch, cudaStream_t
   part.par = part.dA + (size_t)a.rows.n_seq * a.nseg * a.D * a.N;
   if (a.nseg > 1) {
     cudaError_t e = launch_scan_reverse_summary(a, s);
-    if (e == cudaSuccess) e = launch_scan_carry(a, true, s);
+    if (e == cudaSuccess && a.carried) e = launch_scan_carry(a, true, s);
     if (e != cudaSuccess) return e;
   }
   switch (a.N) {

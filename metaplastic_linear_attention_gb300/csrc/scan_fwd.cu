@@ -30,8 +30,8 @@
 // Time split. Where the tiles are too few for the GPU, each sequence is cut into
 // segments: pass A runs the recurrence of every segment but the last from zero
 // and keeps its end state and the sum of its step sizes (the segment's decay is
-// exp(-A sum)); the carry kernel folds them into start states; pass C runs every
-// segment from its own.
+// exp(-A sum)); pass C runs every segment, from the state that it folds from the
+// summaries before it (or a kernel between them, where the segments are many).
 //
 // Rounding: states, sums and step sizes are fp32; y is rounded to the input type once.
 #include <algorithm>
@@ -197,9 +197,13 @@ __global__ void __launch_bounds__(32 * W, kWarpsPerSM / W) palimpsa_scan_kernel(
   float2 A2[2][NS], h[2][NS];  // A scaled by -log2(e): exp(-A s) = 2^(A2 s)
   float2 dsum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
   const size_t at = (size_t)(ch0 + 4 * cl) * N + n0;  // of the first channel in [D, N]
+  // The start state. With a time split, segment 0's pass A has put h0 into the slot of the
+  // last segment, which no summary takes: h_T may be h0, and another CTA may have written it.
+  float* const slots = a.nseg > 1 ? a.seg_state + (size_t)n * a.nseg * a.D * N : nullptr;  // of the sequence
+  float* const spare = a.nseg > 1 ? slots + (size_t)(a.nseg - 1) * a.D * N : nullptr;
   const float* h0 = nullptr;
-  if (FWD && a.nseg > 1) h0 = a.seg_state + (size_t)(n * a.nseg + seg) * a.D * N;
-  else if (FWD && a.h0) h0 = a.h0 + (size_t)n * a.D * N;
+  if (FWD && a.carried) h0 = slots + (size_t)seg * a.D * N;
+  else if (FWD && a.h0) h0 = last && seg == 0 ? a.h0 + (size_t)n * a.D * N : spare;
   bool bad = false;
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
@@ -210,6 +214,16 @@ __global__ void __launch_bounds__(32 * W, kWarpsPerSM / W) palimpsa_scan_kernel(
       bad |= !pos_finite(A);
       (c & 1 ? A2[c / 2][j].y : A2[c / 2][j].x) = decay_rate(A);
       (c & 1 ? h[c / 2][j].y : h[c / 2][j].x) = in && h0 ? h0[at + c * N + j] : 0.f;
+    }
+  }
+  if (FWD && seg > 0 && !a.carried && 4 * cl < nch)
+    fold_segments<4, NS>(h, A2, slots + at, a.seg_dt + (size_t)n * a.nseg * a.D + ch0 + 4 * cl, seg, 1, a.D, N);
+  if (MODE == kSummary && seg == 0 && a.h0 && !a.carried && 4 * cl < nch) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      float q[NS];
+      load_own<NS>(q, reinterpret_cast<const unsigned char*>(a.h0 + (size_t)n * a.D * N + at + c * N));
+      store_own<NS>(reinterpret_cast<unsigned char*>(spare + at + c * N), q);
     }
   }
   // The lane's part of a [D, N] array, stored.
@@ -455,6 +469,7 @@ cudaError_t plan_scan(ScanArgs* a, bool backward) {
     const int per = (int)((len + want - 1) / want);
     a->seg_len = (per + kScanCheckpoint - 1) / kScanCheckpoint * kScanCheckpoint;
     a->nseg = (len + a->seg_len - 1) / a->seg_len;
+    a->carried = a->nseg > kFoldSegments;
   }
   return cudaSuccess;
 }
@@ -469,7 +484,7 @@ cudaError_t launch_scan_carry(const ScanArgs& a, bool reverse, cudaStream_t s) {
 cudaError_t launch_scan_forward(const ScanArgs& a, cudaStream_t s) {
   if (a.nseg > 1) {
     cudaError_t e = dispatch<kSummary>(a, s);
-    if (e == cudaSuccess) e = launch_scan_carry(a, false, s);
+    if (e == cudaSuccess && a.carried) e = launch_scan_carry(a, false, s);
     if (e != cudaSuccess) return e;
   }
   return dispatch<kForward>(a, s);

@@ -76,7 +76,8 @@ struct ScanArgs {
   unsigned int* status;
   // time split (set by the launcher)
   int nseg = 1, seg_len = 0;
-  float* seg_state = nullptr;  // [n_seq, nseg, D, N]: summaries, then start states
+  float* seg_state = nullptr;  // [n_seq, nseg, D, N]: summaries, then (if carried) start states
+  bool carried = false;        // many segments: a kernel of its own folds the summaries
   float* seg_dt = nullptr;     // [n_seq, nseg, D]: sums of the step sizes
   // backward
   const float* ckpt_in = nullptr;
@@ -130,9 +131,11 @@ int scan_backward_resident(const ScanArgs& a);  // CTAs that an SM holds; 0 on f
 // Pass A of the backward's time split: each segment's gradient with respect to the
 // state before it, from a zero gradient after it, and its sum of step sizes.
 cudaError_t launch_scan_reverse_summary(const ScanArgs& a, cudaStream_t s);
-// The carry over segment summaries of a scan: seg_state becomes each segment's
-// start state. Forward: from h0, in segment order. Reverse: from dh_T, from the
-// last segment back.
+// Above this many segments the folds get a kernel of their own: 11 us at 38 segments of 1
+// x 32768 x 2048, where a fold in every CTA cost 22; 5 us less in all at 19 of 4 x 2048 x
+// 1024, but 15 us more, mostly for its launch, at 17 of 2 x 777 x 520 (N = 8, training).
+constexpr int kFoldSegments = 18;
+// Turns the summaries into start states, in place: forward from h0, or in reverse from dh_T.
 cudaError_t launch_scan_carry(const ScanArgs& a, bool reverse, cudaStream_t s);
 
 #if defined(__CUDACC__)
@@ -209,6 +212,11 @@ struct Quad<true> {
   static __device__ __forceinline__ Raw zero() { return make_uint2(0, 0); }
 };
 
+__device__ __forceinline__ float ex2_approx(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
 __device__ __forceinline__ void cp_async16(void* dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
@@ -241,6 +249,37 @@ __device__ __forceinline__ void store_own(unsigned char* p, const float* f) {
   if constexpr (NS == 4) *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
   else *reinterpret_cast<float2*>(p) = make_float2(f[0], f[1]);
 }
+// A lane's states after `count` segments: h <- exp(-A dt) h + state, over the segments'
+// summaries from `state` (its first channel; N apart per channel) and `dt` on, `step`
+// segments apart (1 or -1). C channels, NS states. 4 segments' loads go out together.
+template <int C, int NS>
+__device__ __forceinline__ void fold_segments(float2 (*h)[NS], const float2 (*A2)[NS], const float* state,
+                                              const float* dt, int count, int step, int D, int N) {
+  const long long ss = (long long)step * D * N, sd = (long long)step * D;
+  for (int k0 = 0; k0 < count; k0 += 4) {
+    float q[4][C][NS], d[4][C];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (k0 + k < count) {
+        load_own<C>(d[k], reinterpret_cast<const unsigned char*>(dt + k * sd));
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+          load_own<NS>(q[k][c], reinterpret_cast<const unsigned char*>(state + k * ss + c * N));
+      }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (k0 + k < count)
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+          for (int j = 0; j < NS; ++j) {
+            float& x = c & 1 ? h[c / 2][j].y : h[c / 2][j].x;
+            x = fmaf(ex2_approx(d[k][c] * (c & 1 ? A2[c / 2][j].y : A2[c / 2][j].x)), x, q[k][c][j]);
+          }
+    state += 4 * ss;
+    dt += 4 * sd;
+  }
+}
 // A CTA of one warp needs no barrier.
 template <int W>
 __device__ __forceinline__ void cta_sync() {
@@ -253,11 +292,6 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory");
 }
 
-__device__ __forceinline__ float ex2_approx(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
 constexpr float kLog2e = 1.4426950408889634f;
 
 // Exponents A2 s of two decays 2^(A2 s). The SFU's 2^x comes out low, by 1.9e-8

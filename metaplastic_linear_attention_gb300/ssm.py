@@ -162,6 +162,11 @@ def _new(t, name, shape, dtype, x):
     return t
 
 
+def _like(t):
+    """An uninitialised contiguous tensor of t's shape, dtype and device."""
+    return torch.empty_like(t) if t.is_contiguous() else torch.empty(t.shape, dtype=t.dtype, device=t.device)
+
+
 def _zero_outside(outs, cu, nb, rows, dev, stream):
     """Zeros in the rows of freshly allocated outputs that no sequence of a packed batch covers."""
     if cu is not None and outs and rows:
@@ -193,7 +198,10 @@ def palimpsa_causal_conv(x, weight, bias=None, state0=None, *, silu=True, cu_seq
     ld = _rows(x, "x", x.shape, x.dtype, dev, lead)
     ps = _dense(state0, "state0", (B, W - 1, D), x.dtype, dev)
     fresh = y is None
-    y = _new(y, "y", x.shape, x.dtype, x)
+    if y is None:
+        y = _like(x)
+    else:
+        _dense(y, "y", x.shape, x.dtype, dev)
     state_T = _new(state_T, "state_T", (B, W - 1, D), x.dtype, x)
     if fresh:
         _zero_outside((y,), cu, B, T, dev, stream)
@@ -214,7 +222,10 @@ def palimpsa_causal_conv_step(x, weight, bias, state, *, silu=True, y=None, stre
     B, kind = x.shape[0], _dtype(x)
     ld = _rows(x, "x", x.shape, x.dtype, dev, 1)
     ps = _dense(state, "state", (B, W - 1, D), x.dtype, dev)
-    y = _new(y, "y", x.shape, x.dtype, x)
+    if y is None:
+        y = _like(x)
+    else:
+        _dense(y, "y", x.shape, x.dtype, dev)
     _call(name, dev, stream, (x, weight, bias, state, y),
           x.data_ptr(), ld, pw, pb, ps, y.data_ptr(), B, D, W, PALIMPSA_CONV_SILU if silu else 0, kind)
     return y
@@ -234,8 +245,7 @@ def palimpsa_causal_conv_backward(x, weight, bias, state0, dy, dstate_T=None, *,
     ldy = _rows(dy, "dy", x.shape, dtype, dev, lead)
     ps = _dense(state0, "state0", (B, W - 1, D), dtype, dev)
     pd = _dense(dstate_T, "dstate_T", (B, W - 1, D), dtype, dev)
-    g = {"dx": _new(None, "dx", x.shape, dtype, x),
-         "dweight": _new(None, "dweight", (D, W), F32, x), "dbias": _new(None, "dbias", (D,), F32, x)}
+    g = {"dx": _like(x), "dweight": _like(weight), "dbias": torch.empty(D, dtype=F32, device=x.device)}
     if want_state_grad:
         # a sequence that is skipped for its offsets leaves its part as it is: zeros
         g["dstate0"] = (torch.empty if cu is None else torch.zeros)((B, W - 1, D), dtype=dtype, device=x.device)
@@ -290,7 +300,10 @@ def _scan(name, x, dt, A, B, C, D, z, dt_bias, h0, softplus, cu_seqlens, max_seq
     kind = _dtype(x)
     p0 = _dense(h0, "h0", (nb, ch, n), F32, dev)
     fresh = y is None
-    y = _new(y, "y", x.shape, x.dtype, x)
+    if y is None:
+        y = _like(x)
+    else:
+        _dense(y, "y", x.shape, x.dtype, dev)
     if fresh:
         _zero_outside((y,), cu, nb, T, dev, stream)
     h_T = _new(h_T, "h_T", (nb, ch, n), F32, x)
@@ -339,14 +352,13 @@ def palimpsa_selective_scan_backward(x, dt, A, B, C, D, z, dt_bias, h0, ckpt, dy
     pc = _dense(ckpt, "ckpt", palimpsa_selective_scan_checkpoint_shape(nb, T, ch, n, packed), F32, dev)
     at = x.device
     e = lambda shape, t: torch.empty(shape, dtype=t, device=at)  # noqa: E731
-    g = {"dx": e(x.shape, dtype), "ddt": e(x.shape, dtype), "dA": e((ch, n), F32), "dB": e(B.shape, dtype),
-         "dC": e(B.shape, dtype)}
+    g = {"dx": _like(x), "ddt": _like(x), "dA": _like(A), "dB": _like(B), "dC": _like(B)}
     if D is not None:
-        g["dD"] = e((ch,), F32)
+        g["dD"] = _like(D)
     if z is not None:
-        g["dz"] = e(x.shape, dtype)
+        g["dz"] = _like(x)
     if dt_bias is not None:
-        g["ddt_bias"] = e((ch,), F32)
+        g["ddt_bias"] = _like(dt_bias)
     if want_state_grad:
         # a sequence that is skipped for its offsets leaves its part as it is: zeros
         g["dh0"] = torch.zeros((nb, ch, n), dtype=F32, device=at) if packed else e((nb, ch, n), F32)
@@ -370,7 +382,10 @@ def palimpsa_selective_scan_step(x, dt, A, B, C, h, D=None, z=None, dt_bias=None
     ch, groups, n, strides, ptrs = _scan_inputs(x, dt, A, B, C, D, z, dt_bias, dev, 1)
     kind, nb = _dtype(x), x.shape[0]
     ph = _dense(h, "h", (nb, ch, n), F32, dev)
-    y = _new(y, "y", x.shape, x.dtype, x)
+    if y is None:
+        y = _like(x)
+    else:
+        _dense(y, "y", x.shape, x.dtype, dev)
     _call(name, dev, stream, (x, dt, A, B, C, D, z, dt_bias, h, y),
           *ptrs, ph, y.data_ptr(), strides, nb, ch, groups, n, PALIMPSA_SCAN_SOFTPLUS if softplus else 0, kind)
     return y
