@@ -551,7 +551,7 @@ __device__ __forceinline__ void sum_bc(const ScanArgs& a, const Partials& part, 
   const float* const p = part.bc + ((long long)g * tpg * part.rows + row) * 2 * a.N + 4 * q;
   const long long stride = part.rows * 2 * a.N;
   float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
+#pragma unroll 16
   for (int k = 0; k < tpg; ++k) {
     const float4 v = *reinterpret_cast<const float4*>(p + k * stride);
     s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
@@ -575,15 +575,16 @@ __device__ __forceinline__ void sum_segments(const ScanArgs& a, long long block,
   const int cx = threadIdx.x % 32, sy = threadIdx.x / 32;
   const long long e = block * 32 + cx;
   float s = 0.f;
-  for (long long n = sy; n < a.rows.n_seq; n += 8) {
-    long long row0;
-    int len;
-    if (!seq_rows(a.rows, n, &row0, &len)) continue;
-    const int ns = max(1, (len + a.seg_len - 1) / a.seg_len);
-    if (e < per)
+  if (e < per)
 #pragma unroll 4
-      for (int k = 0; k < ns; ++k) s += p[(n * a.nseg + k) * per + e];
-  }
+    for (long long i = sy; i < (long long)a.rows.n_seq * a.nseg; i += 8) {
+      long long row0;
+      int len;
+      // (an empty sequence has its first segment's zeros; a skipped one has nothing)
+      if (!seq_rows(a.rows, i / a.nseg, &row0, &len)) continue;
+      const long long k = i % a.nseg;
+      if (k == 0 || k * a.seg_len < len) s += p[i * per + e];
+    }
   red[sy][cx] = s;
   __syncthreads();
   if (sy || e >= per) return;
