@@ -9,25 +9,25 @@
 //   dx_t  = w_t s_t + dpre_t skip,  dskip = sum_t dpre_t x_t
 //   dz_t  = dy_t (sum_n C_t h_t + skip x_t) silu'(z_t),  ddt_bias = sum_t ddt_t.
 //
-// The states come from the forward's checkpoints, one every 16 tokens. A CTA has
-// the forward's tile (32 channels, all states, N / 16 warps; a lane 4 channels x
-// 4 states) and walks its tokens from the last chunk of 16 to the first. In a
-// chunk, a first sweep from the checkpoint leaves the state before tokens 4, 8
-// and 12 in shared memory; then, from the last window of 4 tokens to the first, a
-// second sweep fills the window's a_t and a_t h_{t-1} into registers (128 of them)
-// and the tokens are taken in reverse. The windows hold 4 tokens because two
-// values x 16 states x 4 tokens are half of a lane's registers: two CTA warps per
-// scheduler stay resident.
-// What bounds it: about 16 FP32 operations and 2 exponentials per state-token,
-// 2 clocks per channel-token and SM at N = 16, and as much of the shared-memory
-// and shuffle pipe.
+// The states come from the forward's checkpoints, one every 16 tokens. A CTA has a tile
+// of 32 channels with all states and walks its tokens from the last chunk of 16 to the
+// first; a lane holds a pair of channels x 4 states (two pairs at N = 128), a warp 16
+// channels x 16 states. In a chunk, a first sweep from the checkpoint leaves the states
+// before tokens 4, 8 and 12 in shared memory; then, from the last window of 4 tokens to
+// the first, a second sweep fills the window's a_t and a_t h_{t-1} into registers (64 of
+// them), the tokens are taken in reverse, and their sums are reduced together.
+// What bounds it: about 16 FP32 operations and 2 exponentials per state-token (2 clocks
+// per channel-token and SM at N = 16), and as much again for operands, reductions and the
+// token arrays: issue slots, 61 % busy. Measured (GB300, bf16, N = 16, gate, 4 x 2048 x
+// 1024): 159 us, 5.6 clocks. Before: two pairs a lane (255 registers, 7 warps an SM) 231,
+// reductions token by token 393; with 14 warps of 128 registers it spills (202).
 //
-// Sums. w, sum p A and sum C h go over the 4 lane groups by reduce-scatter and over
-// warps in shared memory; dB_t and dC_t over the 32 channels by reduce-scatter, then
-// to a row of scratch per tile; dA, dskip, ddt_bias stay in registers until the
-// segment's end and go to scratch. Small kernels add tiles and segments up in a
-// fixed order: no atomics, the same bits every time. All sums are fp32; gradients
-// of token arrays are rounded to the input type once.
+// Sums. w, sum p A and sum C h go over the 4 lane groups by halves and over warps in
+// shared memory; dB_t and dC_t over 8 lanes by halves and over the tile's two halves in
+// shared memory, then to a row of scratch per tile; dA stays in registers, dskip and
+// ddt_bias in shared memory until the segment's end, and go to scratch. One more kernel
+// adds tiles and segments up in a fixed order: no atomics, the same bits every time. All
+// sums are fp32; gradients of token arrays are rounded to the input type once.
 #include <algorithm>
 #include <atomic>
 

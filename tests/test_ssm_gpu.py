@@ -300,6 +300,101 @@ def test_fresh_packed_outputs_are_zero_outside_the_sequences(cu):
     _status()
 
 
+def test_offsets_beyond_32_bits():
+    """Rows 2^20 elements apart: the last ones lie beyond 2^31 elements (and 2^32 bytes)."""
+    T, D, N, ld = 2200, 64, 16, 1 << 20
+    wide = torch.empty(T, ld, dtype=BF, device=DEV)
+    g = torch.Generator(device=DEV).manual_seed(5)
+    parts = [torch.randn((T, D), generator=g, device=DEV).to(BF) for _ in range(4)]
+    bc = [torch.randn((T, N), generator=g, device=DEV).to(BF) for _ in range(2)]
+    views = []
+    for k, t in enumerate(parts + bc):
+        v = wide[:, 64 * k:64 * k + t.shape[1]]
+        v.copy_(t)
+        views.append(v)
+    w, A = torch.randn(D, 4, device=DEV), 0.3 + torch.rand(D, N, device=DEV)
+    out = []
+    for x, dt, z, dy, b, c in (views, parts + bc):
+        bm, cm = b.unflatten(-1, (1, N)), c.unflatten(-1, (1, N))
+        one = lambda t: t[None]  # noqa: E731
+        y, st = pal.palimpsa_causal_conv(one(x), w)
+        gc = pal.palimpsa_causal_conv_backward(one(x), w, None, None, one(dy))
+        a = (one(x), one(dt), A, one(bm), one(cm), None, one(z))
+        ys, h, ck = pal.palimpsa_selective_scan_checkpointed(*a)
+        gs = pal.palimpsa_selective_scan_backward(*a, None, None, ck, one(dy))
+        cs, hs = torch.zeros(T, 3, D, dtype=BF, device=DEV), torch.zeros(T, D, N, device=DEV)
+        y1 = pal.palimpsa_causal_conv_step(x, w, None, cs)
+        y2 = pal.palimpsa_selective_scan_step(x, dt, A, bm, cm, hs, None, z)
+        out.append([y, st, ys, h, y1, y2, cs, hs, *gc.values(), *gs.values()])
+    assert all(torch.equal(p, q) for p, q in zip(*out))
+    _status()
+
+
+@pytest.mark.parametrize("gate", [True, False])
+def test_gradients_equal_differences_of_the_kernels(gate):
+    """Along a random direction, (L(p + e m) - L(p - e m)) / 2e of the fp32 kernels against <grad, m>. With e = 2^-6 the
+    differences are off by e^2 / 6 = 4e-5 of the third derivative along m, and by the roundings of L, at most
+    1e-6 |y| |dy| / e; both are held against |grad| |m|."""
+    T, D, N, e = 150, 40, 16, 2.0 ** -6
+    i = _dev(_dense(_scan_inputs(17, T, 1, D, 1, N, F32, gate=gate), 1))
+    g = torch.Generator(device=DEV).manual_seed(3)
+    rnd = lambda t: torch.randn(t.shape, generator=g, device=DEV)  # noqa: E731
+    dy, dh = rnd(i["x"]), rnd(i["h0"])
+
+    def loss(v):
+        y, h = pal.palimpsa_selective_scan(*v.values())
+        return float((y.double() * dy).sum() + (h.double() * dh).sum()), float(y.double().norm() * dy.norm())
+
+    _, _, ck = pal.palimpsa_selective_scan_checkpointed(*i.values())
+    got = pal.palimpsa_selective_scan_backward(*i.values(), ck, dy, dh)
+    names = dict(x="dx", dt="ddt", A="dA", B="dB", C="dC", D="dD", z="dz", dt_bias="ddt_bias", h0="dh0")
+    for k, v in i.items():
+        if v is None:
+            continue
+        m = rnd(v)
+        m = m / m.norm() * min(1.0, 0.25 * float(v.norm()) if k == "A" else 1.0)
+        (up, scale), (down, _) = loss(dict(i, **{k: v + e * m})), loss(dict(i, **{k: v - e * m}))
+        grad = got[names[k]].double()
+        diff = (up - down) / (2 * e)
+        bar = 1e-3 * float(grad.norm() * m.norm()) + 1e-6 * scale / e
+        assert abs(diff - float((grad * m).sum())) <= bar, k
+    x, w, b = i["x"], rnd(torch.empty(D, 4)), rnd(torch.empty(D))
+    st = rnd(torch.empty(1, 3, D))
+    gc = pal.palimpsa_causal_conv_backward(x, w, b, st, dy)
+    for k, name in ((0, "dx"), (1, "dweight"), (2, "dbias"), (3, "dstate0")):
+        args = [x, w, b, st]
+        m = rnd(args[k])
+        m = m / m.norm()
+        y = []
+        for s in (1, -1):
+            moved = list(args)
+            moved[k] = args[k] + s * e * m
+            y.append(pal.palimpsa_causal_conv(*moved)[0].double())
+        diff = float(((y[0] - y[1]) * dy).sum()) / (2 * e)
+        bar = 1e-3 * float(gc[name].norm()) + 1e-6 * float(y[0].norm() * dy.norm()) / e
+        assert abs(diff - float((gc[name].double() * m).sum())) <= bar, name
+    _status()
+
+
+def test_calls_on_two_streams_at_once():
+    """Split scans and their backward, running side by side, do not share scratch."""
+    cases = [_dev(_dense(_scan_inputs(40 + k, 3000, 1, 64, 1, 16, BF), 1)) for k in range(2)]
+
+    def work(i, stream=None):
+        y, h, ck = pal.palimpsa_selective_scan_checkpointed(*i.values(), stream=stream)
+        return [y, h, *pal.palimpsa_selective_scan_backward(*i.values(), ck, i["x"], stream=stream).values()]
+
+    want = [[t.clone() for t in work(i)] for i in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    for _ in range(5):
+        got = [work(i, s) for i, s in zip(cases, streams)]
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert all(torch.equal(p, q) for p, q in zip(a, b))
+    _status()
+
+
 def test_empty_prompt_passes_the_state_through():
     h = torch.randn(2, 16, 16, device=DEV)
     e = torch.empty(2, 0, 16, device=DEV)
