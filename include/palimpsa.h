@@ -610,14 +610,15 @@ palimpsa_status palimpsa_causal_conv(
 
 /*
  * palimpsa_zero_rows_outside - zeros in the rows of up to 8 dense arrays that lie
- * before the first and behind the last sequence of a packed batch (T rows of
- * row_bytes[i] bytes each, a multiple of 16; arrays and row_bytes are HOST arrays
- * of n entries). For outputs that the calls here leave unwritten there; it costs
- * next to nothing where the sequences fill the rows.
+ * before the first and behind the last sequence of a packed batch, or in a sequence
+ * that is skipped for its offsets (T rows of row_bytes[i] bytes each, a multiple of
+ * 16; arrays and row_bytes are HOST arrays of n entries). For outputs that the calls
+ * here leave unwritten there, to be called before them; it costs next to nothing
+ * where the sequences fill the rows.
  */
 palimpsa_status palimpsa_zero_rows_outside(
     void* const* arrays, const long long* row_bytes, int n,
-    const int* cu_seqlens, int B, int T, void* cuda_stream);
+    const int* cu_seqlens, int B, int T, int max_seqlen, void* cuda_stream);
 
 /* palimpsa_causal_conv_step - one token: x, y rows of B sequences, state
  * [B, W-1, D] updated in place (the oldest input leaves, x enters). */

@@ -399,6 +399,22 @@ __global__ void __launch_bounds__(256) palimpsa_zero_outside_kernel(ZeroArgs a) 
   const long long step = (long long)gridDim.x * 256, i0 = (long long)blockIdx.x * 256 + threadIdx.x;
   for (long long i = i0; i < lo * w; i += step) p[i] = make_uint4(0, 0, 0, 0);
   for (long long i = hi * w + i0; i < T * w; i += step) p[i] = make_uint4(0, 0, 0, 0);
+  // Sequences that are skipped for their offsets, each by the warp that finds it.
+  const int lane = threadIdx.x & 31;
+  for (long long n0 = i0 - lane; n0 < a.rows.n_seq; n0 += step) {
+    int from = 0, to = 0;
+    if (n0 + lane < a.rows.n_seq) {
+      const long long s0 = a.rows.cu[n0 + lane], s1 = a.rows.cu[n0 + lane + 1];
+      if (s0 < 0 || s1 > T || s1 - s0 > a.rows.max_len) {
+        from = (int)min(max(s0, 0ll), T);
+        to = (int)min(max(s1, 0ll), T);
+      }
+    }
+    for (unsigned left = __ballot_sync(~0u, to > from); left; left &= left - 1) {
+      const long long r0 = __shfl_sync(~0u, from, __ffs(left) - 1), r1 = __shfl_sync(~0u, to, __ffs(left) - 1);
+      for (long long i = r0 * w + lane; i < r1 * w; i += 32) p[i] = make_uint4(0, 0, 0, 0);
+    }
+  }
 }
 
 // Tokens of a run, a multiple of 8: long runs read fewer rows twice and load the taps

@@ -156,12 +156,12 @@ palimpsa_status palimpsa_causal_conv(const void* x, long long x_stride, const fl
 }
 
 palimpsa_status palimpsa_zero_rows_outside(void* const* arrays, const long long* row_bytes, int n,
-                                           const int* cu_seqlens, int B, int T, void* cuda_stream) {
+                                           const int* cu_seqlens, int B, int T, int max_seqlen, void* cuda_stream) {
   if (!cu_seqlens || (n > 0 && (!arrays || !row_bytes))) return PALIMPSA_ERR_NULL;
-  if (n < 0 || n > kZeroArrays || B < 1 || T < 0) return PALIMPSA_ERR_SHAPE;
+  if (n < 0 || n > kZeroArrays || B < 1 || T < 0 || max_seqlen < 0 || max_seqlen > T) return PALIMPSA_ERR_SHAPE;
   if (!aligned(cu_seqlens, 4)) return PALIMPSA_ERR_ALIGN;
   ZeroArgs a{};
-  a.rows = rows_of(cu_seqlens, B, T, T);
+  a.rows = rows_of(cu_seqlens, B, T, max_seqlen);
   for (int i = 0; i < n; ++i) {
     if (!arrays[i] && T != 0) return PALIMPSA_ERR_NULL;
     if (row_bytes[i] < 0 || row_bytes[i] > (1LL << 40) / (T > 0 ? T : 1)) return PALIMPSA_ERR_SHAPE;

@@ -39,7 +39,7 @@ def _library():
             "palimpsa_causal_conv": [p, ll, p, p, p, p, p, p, i, i, i, i, i, u, i, p],
             "palimpsa_causal_conv_step": [p, ll, p, p, p, p, i, i, i, u, i, p],
             "palimpsa_causal_conv_backward": [p, ll, p, p, p, p, ll, p, p, p, p, p, p, i, i, i, i, i, u, i, p],
-            "palimpsa_zero_rows_outside": [p, p, i, p, i, i, p],
+            "palimpsa_zero_rows_outside": [p, p, i, p, i, i, i, p],
             "palimpsa_selective_scan": [p] * 12 + [st, p, i, i, i, i, i, i, u, i, p],
             "palimpsa_selective_scan_step": [p] * 10 + [st, i, i, i, i, u, i, p],
             "palimpsa_selective_scan_backward": [p] * 20 + [st, p, i, i, i, i, i, i, u, i, p],
@@ -167,12 +167,13 @@ def _like(t):
     return torch.empty_like(t) if t.is_contiguous() else torch.empty(t.shape, dtype=t.dtype, device=t.device)
 
 
-def _zero_outside(outs, cu, nb, rows, dev, stream):
-    """Zeros in the rows of freshly allocated outputs that no sequence of a packed batch covers."""
+def _zero_outside(outs, cu, nb, rows, longest, dev, stream):
+    """Zeros in the rows of freshly allocated outputs that no sequence of a packed batch covers, or
+    only one that is skipped for its offsets."""
     if cu is not None and outs and rows:
         p = (ctypes.c_void_p * len(outs))(*(t.data_ptr() for t in outs))
         w = (ctypes.c_longlong * len(outs))(*(t.numel() // rows * t.element_size() for t in outs))
-        _call("palimpsa_zero_rows_outside", dev, stream, (), p, w, len(outs), cu.data_ptr(), nb, rows)
+        _call("palimpsa_zero_rows_outside", dev, stream, (), p, w, len(outs), cu.data_ptr(), nb, rows, longest)
 
 
 # ------------------------------------------------------------------ causal convolution
@@ -204,7 +205,7 @@ def palimpsa_causal_conv(x, weight, bias=None, state0=None, *, silu=True, cu_seq
         _dense(y, "y", x.shape, x.dtype, dev)
     state_T = _new(state_T, "state_T", (B, W - 1, D), x.dtype, x)
     if fresh:
-        _zero_outside((y,), cu, B, T, dev, stream)
+        _zero_outside((y,), cu, B, T, longest, dev, stream)
     _call(name, dev, stream, (x, weight, bias, state0, y, state_T, cu),
           x.data_ptr(), ld, pw, pb, ps, y.data_ptr(), state_T.data_ptr(), _ptr(cu), B, T, longest, D, W,
           PALIMPSA_CONV_SILU if silu else 0, kind)
@@ -249,7 +250,7 @@ def palimpsa_causal_conv_backward(x, weight, bias, state0, dy, dstate_T=None, *,
     if want_state_grad:
         # a sequence that is skipped for its offsets leaves its part as it is: zeros
         g["dstate0"] = (torch.empty if cu is None else torch.zeros)((B, W - 1, D), dtype=dtype, device=x.device)
-    _zero_outside((g["dx"],), cu, B, T, dev, stream)
+    _zero_outside((g["dx"],), cu, B, T, longest, dev, stream)
     _call(name, dev, stream, (x, weight, bias, state0, dy, dstate_T, cu, *g.values()),
           x.data_ptr(), ld, pw, pb, ps, dy.data_ptr(), ldy, pd, g["dx"].data_ptr(), g["dweight"].data_ptr(),
           g["dbias"].data_ptr(), _ptr(g.get("dstate0")), _ptr(cu), B, T, longest, D, W,
@@ -305,7 +306,7 @@ def _scan(name, x, dt, A, B, C, D, z, dt_bias, h0, softplus, cu_seqlens, max_seq
     else:
         _dense(y, "y", x.shape, x.dtype, dev)
     if fresh:
-        _zero_outside((y,), cu, nb, T, dev, stream)
+        _zero_outside((y,), cu, nb, T, longest, dev, stream)
     h_T = _new(h_T, "h_T", (nb, ch, n), F32, x)
     if want_ckpt:
         ckpt = _new(ckpt, "ckpt", palimpsa_selective_scan_checkpoint_shape(nb, T, ch, n, cu is not None), F32, x)
@@ -362,7 +363,7 @@ def palimpsa_selective_scan_backward(x, dt, A, B, C, D, z, dt_bias, h0, ckpt, dy
     if want_state_grad:
         # a sequence that is skipped for its offsets leaves its part as it is: zeros
         g["dh0"] = torch.zeros((nb, ch, n), dtype=F32, device=at) if packed else e((nb, ch, n), F32)
-    _zero_outside([g[k] for k in ("dx", "ddt", "dz", "dB", "dC") if k in g], cu, nb, T, dev, stream)
+    _zero_outside([g[k] for k in ("dx", "ddt", "dz", "dB", "dC") if k in g], cu, nb, T, longest, dev, stream)
     at = {k: v.data_ptr() for k, v in g.items()}
     _call(name, dev, stream, (x, dt, A, B, C, D, z, dt_bias, ckpt, dy, dh_T, cu, *g.values()),
           *ptrs, pc, dy.data_ptr(), pg, at["dx"], at["ddt"], at["dA"], at["dB"], at["dC"], at.get("dD"), at.get("dz"),

@@ -106,13 +106,14 @@ def test_scan_stride_refusals(lib, name, field, given, code):
 @pytest.mark.parametrize("over,code", [
     (dict(cu=None), ERR_NULL), (dict(arrays=None), ERR_NULL), (dict(p=[P, 0]), ERR_NULL), (dict(n=9), ERR_SHAPE),
     (dict(n=-1), ERR_SHAPE), (dict(B=0), ERR_SHAPE), (dict(T=-1), ERR_SHAPE), (dict(p=[P, P + 8]), ERR_ALIGN),
-    (dict(w=[16, 24]), ERR_ALIGN), (dict(w=[16, -16]), ERR_SHAPE), (dict(cu=P + 1), ERR_ALIGN),
+    (dict(w=[16, 24]), ERR_ALIGN), (dict(w=[16, -16]), ERR_SHAPE), (dict(cu=P + 1), ERR_ALIGN), (dict(longest=-1), ERR_SHAPE),
+    (dict(longest=101), ERR_SHAPE),
 ])
 def test_zero_rows_outside_refusals(lib, over, code):
-    a = dict(p=[P, P], w=[16, 32], n=2, cu=P, B=3, T=100, arrays=True) | over
+    a = dict(p=[P, P], w=[16, 32], n=2, cu=P, B=3, T=100, longest=50, arrays=True) | over
     p = (ctypes.c_void_p * 2)(*a["p"]) if a["arrays"] else None
     w = (ctypes.c_longlong * 2)(*a["w"])
-    assert lib.palimpsa_zero_rows_outside(p, w, a["n"], a["cu"], a["B"], a["T"], None) == code
+    assert lib.palimpsa_zero_rows_outside(p, w, a["n"], a["cu"], a["B"], a["T"], a["longest"], None) == code
 
 
 def test_checkpoint_bytes(lib):

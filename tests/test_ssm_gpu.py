@@ -443,6 +443,35 @@ def test_bad_offsets_are_reported_and_touch_nothing(cu):
     assert torch.equal((y == 7).all(1).cpu(), ~written)
 
 
+def test_fresh_outputs_are_zero_in_the_rows_of_skipped_sequences():
+    cu, rows, D, N, longest = [0, 18, 19, 40, 44, 50], 40, 16, 16, 12  # too long, whole, too long, out of range twice
+    i = _dev(_scan_inputs(2, rows, 5, D, 1, N, F32))
+    c = _dev(_conv_inputs(2, rows, 5, D, 4, F32))
+    cud = torch.tensor(cu, dtype=torch.int32, device=DEV)
+    kw = dict(cu_seqlens=cud, max_seqlen=longest)
+    dy = torch.ones(rows, D, device=DEV)
+
+    def used(*shape):
+        """Leaves the allocator with blocks that hold NaN."""
+        held = [torch.full(shape, float("nan"), device=DEV) for _ in range(8)]
+        del held
+
+    used(rows, D)
+    outs = [pal.palimpsa_causal_conv(*c.values(), **kw)[0]]
+    used(rows, D)
+    outs.append(pal.palimpsa_causal_conv_backward(*c.values(), dy, **kw)["dx"])
+    used(rows, D)
+    y, _, ckpt = pal.palimpsa_selective_scan_checkpointed(*i.values(), **kw)
+    outs.append(y)
+    used(rows, D)
+    g = pal.palimpsa_selective_scan_backward(*i.values(), ckpt, dy, **kw)
+    outs += [g[k] for k in ("dx", "ddt", "dz", "dB", "dC")]
+    assert pal.palimpsa_get_device_status() == 5
+    for o in outs:
+        o = o.reshape(rows, -1)
+        assert o[18].abs().sum() > 0 and not o[:18].any() and not o[19:].any()
+
+
 @pytest.mark.parametrize("what", ["A", "dt", "bias"])
 def test_domain_violations_are_latched(what):
     i = _dev(_dense(_scan_inputs(3, 40, 2, 16, 1, 16, F32), 2))
