@@ -167,6 +167,16 @@ def _like(t):
     return torch.empty_like(t) if t.is_contiguous() else torch.empty(t.shape, dtype=t.dtype, device=t.device)
 
 
+def _zeros(shape, dtype, device, stream):
+    """Zeros filled in on the stream that the call uses."""
+    if stream is None:
+        return torch.zeros(shape, dtype=dtype, device=device)
+    with torch.cuda.device(device):
+        t = torch.empty(shape, dtype=dtype, device=device)
+        with torch.cuda.stream(stream):
+            return t.zero_()
+
+
 def _zero_outside(outs, cu, nb, rows, longest, dev, stream):
     """Zeros in the rows of freshly allocated outputs that no sequence of a packed batch covers, or
     only one that is skipped for its offsets."""
@@ -249,7 +259,9 @@ def palimpsa_causal_conv_backward(x, weight, bias, state0, dy, dstate_T=None, *,
     g = {"dx": _like(x), "dweight": _like(weight), "dbias": torch.empty(D, dtype=F32, device=x.device)}
     if want_state_grad:
         # a sequence that is skipped for its offsets leaves its part as it is: zeros
-        g["dstate0"] = (torch.empty if cu is None else torch.zeros)((B, W - 1, D), dtype=dtype, device=x.device)
+        shape = (B, W - 1, D)
+        g["dstate0"] = (torch.empty(shape, dtype=dtype, device=x.device) if cu is None
+                        else _zeros(shape, dtype, x.device, stream))
     _zero_outside((g["dx"],), cu, B, T, longest, dev, stream)
     _call(name, dev, stream, (x, weight, bias, state0, dy, dstate_T, cu, *g.values()),
           x.data_ptr(), ld, pw, pb, ps, dy.data_ptr(), ldy, pd, g["dx"].data_ptr(), g["dweight"].data_ptr(),
@@ -362,7 +374,7 @@ def palimpsa_selective_scan_backward(x, dt, A, B, C, D, z, dt_bias, h0, ckpt, dy
         g["ddt_bias"] = _like(dt_bias)
     if want_state_grad:
         # a sequence that is skipped for its offsets leaves its part as it is: zeros
-        g["dh0"] = torch.zeros((nb, ch, n), dtype=F32, device=at) if packed else e((nb, ch, n), F32)
+        g["dh0"] = _zeros((nb, ch, n), F32, at, stream) if packed else e((nb, ch, n), F32)
     _zero_outside([g[k] for k in ("dx", "ddt", "dz", "dB", "dC") if k in g], cu, nb, T, longest, dev, stream)
     at = {k: v.data_ptr() for k, v in g.items()}
     _call(name, dev, stream, (x, dt, A, B, C, D, z, dt_bias, ckpt, dy, dh_T, cu, *g.values()),

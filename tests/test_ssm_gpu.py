@@ -472,6 +472,30 @@ def test_fresh_outputs_are_zero_in_the_rows_of_skipped_sequences():
         assert o[18].abs().sum() > 0 and not o[:18].any() and not o[19:].any()
 
 
+def test_state_gradients_of_a_packed_batch_on_another_stream():
+    """The zeros that a packed batch's state gradients start from are filled in on the call's stream: work that is
+    still queued on the current one does not put them over the results."""
+    rows, D, N = 20, 16, 16
+    i = _dev(_scan_inputs(2, rows, 2, D, 1, N, F32))
+    c = _dev(_conv_inputs(2, rows, 2, D, 4, F32))
+    kw = dict(cu_seqlens=torch.tensor([0, 9, 20], dtype=torch.int32, device=DEV), max_seqlen=11)
+    dy = torch.ones(rows, D, device=DEV)
+    _, _, ckpt = pal.palimpsa_selective_scan_checkpointed(*i.values(), **kw)
+    want = [pal.palimpsa_selective_scan_backward(*i.values(), ckpt, dy, **kw)["dh0"],
+            pal.palimpsa_causal_conv_backward(*c.values(), dy, **kw)["dstate0"]]
+    busy = torch.randn(4096, 4096, device=DEV)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        busy = busy @ busy * 1e-2
+    got = [pal.palimpsa_selective_scan_backward(*i.values(), ckpt, dy, stream=side, **kw)["dh0"],
+           pal.palimpsa_causal_conv_backward(*c.values(), dy, stream=side, **kw)["dstate0"]]
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert a.any() and torch.equal(a, b)
+    _status()
+
+
 @pytest.mark.parametrize("what", ["A", "dt", "bias"])
 def test_domain_violations_are_latched(what):
     i = _dev(_dense(_scan_inputs(3, 40, 2, 16, 1, 16, F32), 2))
