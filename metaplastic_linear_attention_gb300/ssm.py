@@ -10,6 +10,8 @@ contiguous, rows evenly spaced); outputs are dense.
 from __future__ import annotations
 
 import ctypes
+import functools
+import inspect
 
 import torch
 
@@ -124,25 +126,50 @@ _raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_get
     lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
-def _call(name, dev, stream, tensors, *args):
-    """The library call on the tensors' device, on the caller's stream or the current one. Tensors
-    used on a caller's stream are recorded there, so that the allocator keeps them until that
-    stream is done."""
+def _call(name, dev, *args):
+    """The library call on the tensors' device, on its current stream."""
     fn = _functions.get(name) or _function(name)
-    if stream is None and dev == torch.cuda.current_device():
+    if dev == torch.cuda.current_device():
         rc = fn(*args, _raw_stream(dev))
     else:
         with torch.cuda.device(dev):
-            rc = fn(*args, binding._stream_handle(stream))
-        if stream is not None:
-            for t in tensors:
-                if t is not None:
-                    t.record_stream(stream)
+            rc = fn(*args, _raw_stream(dev))
     if rc != 0:
         raise PalimpsaError(rc, name)
 
 
-def _batch(x, cu_seqlens, max_seqlen, dev, stream, name):
+def _on_stream(fn):
+    """Adds the argument `stream` to an operator: the stream to run on, instead of the current one.
+    What the call allocates and fills in belongs to that stream, so that nothing queued on the
+    current one can touch it. The inputs are recorded there and fresh outputs on the current
+    stream, so that the allocator keeps either until both streams are done with it."""
+    @functools.wraps(fn)
+    def call(*args, stream=None, **kw):
+        if stream is None:
+            return fn(*args, **kw)
+        given = [t for t in (*args, *kw.values()) if isinstance(t, torch.Tensor) and t.is_cuda]
+        for t in given:
+            if t.get_device() != stream.device_index:
+                raise ValueError(f"{fn.__name__}: a tensor is on {t.device}, the stream on cuda:{stream.device_index}")
+        home = torch.cuda.current_stream(stream.device)
+        if stream == home:
+            return fn(*args, **kw)
+        with torch.cuda.stream(stream):
+            out = fn(*args, **kw)
+        for t in given:
+            t.record_stream(stream)
+        for t in out.values() if isinstance(out, dict) else out if isinstance(out, tuple) else (out,):
+            if t is not None:
+                t.record_stream(home)
+        return out
+
+    sig = inspect.signature(fn)
+    extra = inspect.Parameter("stream", inspect.Parameter.KEYWORD_ONLY, default=None)
+    call.__signature__ = sig.replace(parameters=(*sig.parameters.values(), extra))
+    return call
+
+
+def _batch(x, cu_seqlens, max_seqlen, dev, name):
     """(B, T, max_seqlen, offsets on the device, row dimensions) of a token array x."""
     if cu_seqlens is None:
         if x.dim() != 3:
@@ -150,7 +177,7 @@ def _batch(x, cu_seqlens, max_seqlen, dev, stream, name):
         return x.shape[0], x.shape[1], x.shape[1], None, 2
     if x.dim() != 2:
         raise ValueError(f"{name}: packed x must be [rows, D], got {tuple(x.shape)}")
-    cu, n, longest = _packed_offsets(cu_seqlens, max_seqlen, x.device, stream)
+    cu, n, longest = _packed_offsets(cu_seqlens, max_seqlen, x.device)
     return n, x.shape[0], longest, cu, 1
 
 
@@ -167,23 +194,13 @@ def _like(t):
     return torch.empty_like(t) if t.is_contiguous() else torch.empty(t.shape, dtype=t.dtype, device=t.device)
 
 
-def _zeros(shape, dtype, device, stream):
-    """Zeros filled in on the stream that the call uses."""
-    if stream is None:
-        return torch.zeros(shape, dtype=dtype, device=device)
-    with torch.cuda.device(device):
-        t = torch.empty(shape, dtype=dtype, device=device)
-        with torch.cuda.stream(stream):
-            return t.zero_()
-
-
-def _zero_outside(outs, cu, nb, rows, longest, dev, stream):
+def _zero_outside(outs, cu, nb, rows, longest, dev):
     """Zeros in the rows of freshly allocated outputs that no sequence of a packed batch covers, or
     only one that is skipped for its offsets."""
     if cu is not None and outs and rows:
         p = (ctypes.c_void_p * len(outs))(*(t.data_ptr() for t in outs))
         w = (ctypes.c_longlong * len(outs))(*(t.numel() // rows * t.element_size() for t in outs))
-        _call("palimpsa_zero_rows_outside", dev, stream, (), p, w, len(outs), cu.data_ptr(), nb, rows, longest)
+        _call("palimpsa_zero_rows_outside", dev, p, w, len(outs), cu.data_ptr(), nb, rows, longest)
 
 
 # ------------------------------------------------------------------ causal convolution
@@ -193,8 +210,9 @@ def _conv_params(x, weight, bias, dev):
     return D, W, _dense(weight, "weight", (D, W), F32, dev), _dense(bias, "bias", (D,), F32, dev)
 
 
+@_on_stream
 def palimpsa_causal_conv(x, weight, bias=None, state0=None, *, silu=True, cu_seqlens=None, max_seqlen=None, y=None,
-                         state_T=None, stream=None):
+                         state_T=None):
     """Depthwise causal convolution along the tokens (see palimpsa.h).
 
     x [B, T, D], or [rows, D] with cu_seqlens [B + 1] int32 (max_seqlen: the longest
@@ -203,7 +221,7 @@ def palimpsa_causal_conv(x, weight, bias=None, state0=None, *, silu=True, cu_seq
     zeros. Returns (y, state_T), both in x's dtype; state_T may be given as state0."""
     name = "palimpsa_causal_conv"
     dev = _device(x, name)
-    B, T, longest, cu, lead = _batch(x, cu_seqlens, max_seqlen, dev, stream, name)
+    B, T, longest, cu, lead = _batch(x, cu_seqlens, max_seqlen, dev, name)
     D, W, pw, pb = _conv_params(x, weight, bias, dev)
     kind = _dtype(x)
     ld = _rows(x, "x", x.shape, x.dtype, dev, lead)
@@ -215,14 +233,14 @@ def palimpsa_causal_conv(x, weight, bias=None, state0=None, *, silu=True, cu_seq
         _dense(y, "y", x.shape, x.dtype, dev)
     state_T = _new(state_T, "state_T", (B, W - 1, D), x.dtype, x)
     if fresh:
-        _zero_outside((y,), cu, B, T, longest, dev, stream)
-    _call(name, dev, stream, (x, weight, bias, state0, y, state_T, cu),
-          x.data_ptr(), ld, pw, pb, ps, y.data_ptr(), state_T.data_ptr(), _ptr(cu), B, T, longest, D, W,
+        _zero_outside((y,), cu, B, T, longest, dev)
+    _call(name, dev, x.data_ptr(), ld, pw, pb, ps, y.data_ptr(), state_T.data_ptr(), _ptr(cu), B, T, longest, D, W,
           PALIMPSA_CONV_SILU if silu else 0, kind)
     return y, state_T
 
 
-def palimpsa_causal_conv_step(x, weight, bias, state, *, silu=True, y=None, stream=None):
+@_on_stream
+def palimpsa_causal_conv_step(x, weight, bias, state, *, silu=True, y=None):
     """One token of the convolution (see palimpsa.h): x [B, D], state [B, W - 1, D] updated in
     place. Returns y [B, D]."""
     name = "palimpsa_causal_conv_step"
@@ -237,19 +255,19 @@ def palimpsa_causal_conv_step(x, weight, bias, state, *, silu=True, y=None, stre
         y = _like(x)
     else:
         _dense(y, "y", x.shape, x.dtype, dev)
-    _call(name, dev, stream, (x, weight, bias, state, y),
-          x.data_ptr(), ld, pw, pb, ps, y.data_ptr(), B, D, W, PALIMPSA_CONV_SILU if silu else 0, kind)
+    _call(name, dev, x.data_ptr(), ld, pw, pb, ps, y.data_ptr(), B, D, W, PALIMPSA_CONV_SILU if silu else 0, kind)
     return y
 
 
+@_on_stream
 def palimpsa_causal_conv_backward(x, weight, bias, state0, dy, dstate_T=None, *, silu=True, cu_seqlens=None,
-                                  max_seqlen=None, want_state_grad=True, stream=None):
+                                  max_seqlen=None, want_state_grad=True):
     """Gradients through palimpsa_causal_conv (see palimpsa.h). Returns a dict: dx (x's dtype; zero
     in rows outside every sequence), dweight [D, W], dbias [D] (fp32), and dstate0
     [B, W - 1, D] (x's dtype) when want_state_grad."""
     name = "palimpsa_causal_conv_backward"
     dev = _device(x, name)
-    B, T, longest, cu, lead = _batch(x, cu_seqlens, max_seqlen, dev, stream, name)
+    B, T, longest, cu, lead = _batch(x, cu_seqlens, max_seqlen, dev, name)
     D, W, pw, pb = _conv_params(x, weight, bias, dev)
     kind, dtype = _dtype(x), x.dtype
     ld = _rows(x, "x", x.shape, dtype, dev, lead)
@@ -259,13 +277,10 @@ def palimpsa_causal_conv_backward(x, weight, bias, state0, dy, dstate_T=None, *,
     g = {"dx": _like(x), "dweight": _like(weight), "dbias": torch.empty(D, dtype=F32, device=x.device)}
     if want_state_grad:
         # a sequence that is skipped for its offsets leaves its part as it is: zeros
-        shape = (B, W - 1, D)
-        g["dstate0"] = (torch.empty(shape, dtype=dtype, device=x.device) if cu is None
-                        else _zeros(shape, dtype, x.device, stream))
-    _zero_outside((g["dx"],), cu, B, T, longest, dev, stream)
-    _call(name, dev, stream, (x, weight, bias, state0, dy, dstate_T, cu, *g.values()),
-          x.data_ptr(), ld, pw, pb, ps, dy.data_ptr(), ldy, pd, g["dx"].data_ptr(), g["dweight"].data_ptr(),
-          g["dbias"].data_ptr(), _ptr(g.get("dstate0")), _ptr(cu), B, T, longest, D, W,
+        g["dstate0"] = (torch.empty if cu is None else torch.zeros)((B, W - 1, D), dtype=dtype, device=x.device)
+    _zero_outside((g["dx"],), cu, B, T, longest, dev)
+    _call(name, dev, x.data_ptr(), ld, pw, pb, ps, dy.data_ptr(), ldy, pd, g["dx"].data_ptr(),
+          g["dweight"].data_ptr(), g["dbias"].data_ptr(), _ptr(g.get("dstate0")), _ptr(cu), B, T, longest, D, W,
           PALIMPSA_CONV_SILU if silu else 0, kind)
     return g
 
@@ -306,9 +321,9 @@ def palimpsa_selective_scan_checkpoint_shape(batch, tokens, channels, states, pa
     return (batch, -(-tokens // CHECKPOINT_TOKENS), channels, states)
 
 
-def _scan(name, x, dt, A, B, C, D, z, dt_bias, h0, softplus, cu_seqlens, max_seqlen, y, h_T, want_ckpt, ckpt, stream):
+def _scan(name, x, dt, A, B, C, D, z, dt_bias, h0, softplus, cu_seqlens, max_seqlen, y, h_T, want_ckpt, ckpt):
     dev = _device(x, name)
-    nb, T, longest, cu, lead = _batch(x, cu_seqlens, max_seqlen, dev, stream, name)
+    nb, T, longest, cu, lead = _batch(x, cu_seqlens, max_seqlen, dev, name)
     ch, groups, n, strides, ptrs = _scan_inputs(x, dt, A, B, C, D, z, dt_bias, dev, lead)
     kind = _dtype(x)
     p0 = _dense(h0, "h0", (nb, ch, n), F32, dev)
@@ -318,18 +333,18 @@ def _scan(name, x, dt, A, B, C, D, z, dt_bias, h0, softplus, cu_seqlens, max_seq
     else:
         _dense(y, "y", x.shape, x.dtype, dev)
     if fresh:
-        _zero_outside((y,), cu, nb, T, longest, dev, stream)
+        _zero_outside((y,), cu, nb, T, longest, dev)
     h_T = _new(h_T, "h_T", (nb, ch, n), F32, x)
     if want_ckpt:
         ckpt = _new(ckpt, "ckpt", palimpsa_selective_scan_checkpoint_shape(nb, T, ch, n, cu is not None), F32, x)
-    _call(name, dev, stream, (x, dt, A, B, C, D, z, dt_bias, h0, y, h_T, ckpt, cu),
-          *ptrs, p0, y.data_ptr(), h_T.data_ptr(), _ptr(ckpt), strides, _ptr(cu), nb, T, longest, ch, groups, n,
-          PALIMPSA_SCAN_SOFTPLUS if softplus else 0, kind)
+    _call(name, dev, *ptrs, p0, y.data_ptr(), h_T.data_ptr(), _ptr(ckpt), strides, _ptr(cu), nb, T, longest, ch,
+          groups, n, PALIMPSA_SCAN_SOFTPLUS if softplus else 0, kind)
     return y, h_T, ckpt
 
 
+@_on_stream
 def palimpsa_selective_scan(x, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None, *, softplus=True, cu_seqlens=None,
-                            max_seqlen=None, y=None, h_T=None, stream=None):
+                            max_seqlen=None, y=None, h_T=None):
     """The selective scan (see palimpsa.h): s = softplus(dt + dt_bias), h = exp(-A s) h + s x B,
     y = (C h + D x) silu(z).
 
@@ -338,26 +353,28 @@ def palimpsa_selective_scan(x, dt, A, B, C, D=None, z=None, dt_bias=None, h0=Non
     [D, N] > 0, D (the skip term), dt_bias [D], h0 [B, D, N] fp32; D, z, dt_bias, h0 may be
     None. Returns (y in x's dtype, h_T [B, D, N] fp32); h_T may be given as h0."""
     return _scan("palimpsa_selective_scan", x, dt, A, B, C, D, z, dt_bias, h0, softplus, cu_seqlens, max_seqlen, y, h_T,
-                 False, None, stream)[:2]
+                 False, None)[:2]
 
 
+@_on_stream
 def palimpsa_selective_scan_checkpointed(x, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None, *, softplus=True,
-                                         cu_seqlens=None, max_seqlen=None, ckpt=None, y=None, h_T=None, stream=None):
+                                         cu_seqlens=None, max_seqlen=None, ckpt=None, y=None, h_T=None):
     """palimpsa_selective_scan for training: also the states that the backward reads. Returns
     (y, h_T, ckpt), ckpt of palimpsa_selective_scan_checkpoint_shape."""
     return _scan("palimpsa_selective_scan", x, dt, A, B, C, D, z, dt_bias, h0, softplus, cu_seqlens, max_seqlen, y, h_T,
-                 True, ckpt, stream)
+                 True, ckpt)
 
 
+@_on_stream
 def palimpsa_selective_scan_backward(x, dt, A, B, C, D, z, dt_bias, h0, ckpt, dy, dh_T=None, *, softplus=True,
-                                     cu_seqlens=None, max_seqlen=None, want_state_grad=True, stream=None):
+                                     cu_seqlens=None, max_seqlen=None, want_state_grad=True):
     """Gradients through palimpsa_selective_scan_checkpointed (see palimpsa.h), with its ckpt on the
     same inputs. Returns a dict: dx, ddt, dz (with z), dB, dC in x's dtype; dA [D, N], dD
     (with D), ddt_bias (with dt_bias) fp32, and dh0 [B, D, N] fp32 when want_state_grad. Rows
     outside every sequence are zero."""
     name = "palimpsa_selective_scan_backward"
     dev = _device(x, name)
-    nb, T, longest, cu, lead = _batch(x, cu_seqlens, max_seqlen, dev, stream, name)
+    nb, T, longest, cu, lead = _batch(x, cu_seqlens, max_seqlen, dev, name)
     ch, groups, n, strides, ptrs = _scan_inputs(x, dt, A, B, C, D, z, dt_bias, dev, lead, dy)
     kind, dtype, packed = _dtype(x), x.dtype, cu is not None
     _dense(h0, "h0", (nb, ch, n), F32, dev)
@@ -374,18 +391,17 @@ def palimpsa_selective_scan_backward(x, dt, A, B, C, D, z, dt_bias, h0, ckpt, dy
         g["ddt_bias"] = _like(dt_bias)
     if want_state_grad:
         # a sequence that is skipped for its offsets leaves its part as it is: zeros
-        g["dh0"] = _zeros((nb, ch, n), F32, at, stream) if packed else e((nb, ch, n), F32)
-    _zero_outside([g[k] for k in ("dx", "ddt", "dz", "dB", "dC") if k in g], cu, nb, T, longest, dev, stream)
+        g["dh0"] = torch.zeros((nb, ch, n), dtype=F32, device=at) if packed else e((nb, ch, n), F32)
+    _zero_outside([g[k] for k in ("dx", "ddt", "dz", "dB", "dC") if k in g], cu, nb, T, longest, dev)
     at = {k: v.data_ptr() for k, v in g.items()}
-    _call(name, dev, stream, (x, dt, A, B, C, D, z, dt_bias, ckpt, dy, dh_T, cu, *g.values()),
-          *ptrs, pc, dy.data_ptr(), pg, at["dx"], at["ddt"], at["dA"], at["dB"], at["dC"], at.get("dD"), at.get("dz"),
-          at.get("ddt_bias"), at.get("dh0"), strides, _ptr(cu), nb, T, longest, ch, groups, n,
+    _call(name, dev, *ptrs, pc, dy.data_ptr(), pg, at["dx"], at["ddt"], at["dA"], at["dB"], at["dC"], at.get("dD"),
+          at.get("dz"), at.get("ddt_bias"), at.get("dh0"), strides, _ptr(cu), nb, T, longest, ch, groups, n,
           PALIMPSA_SCAN_SOFTPLUS if softplus else 0, kind)
     return g
 
 
-def palimpsa_selective_scan_step(x, dt, A, B, C, h, D=None, z=None, dt_bias=None, *, softplus=True, y=None,
-                                 stream=None):
+@_on_stream
+def palimpsa_selective_scan_step(x, dt, A, B, C, h, D=None, z=None, dt_bias=None, *, softplus=True, y=None):
     """One token of the selective scan (see palimpsa.h): x, dt, z [B, D], B and C [B, G, N], h
     [B, D, N] fp32 updated in place. Returns y [B, D]."""
     name = "palimpsa_selective_scan_step"
@@ -399,6 +415,6 @@ def palimpsa_selective_scan_step(x, dt, A, B, C, h, D=None, z=None, dt_bias=None
         y = _like(x)
     else:
         _dense(y, "y", x.shape, x.dtype, dev)
-    _call(name, dev, stream, (x, dt, A, B, C, D, z, dt_bias, h, y),
-          *ptrs, ph, y.data_ptr(), strides, nb, ch, groups, n, PALIMPSA_SCAN_SOFTPLUS if softplus else 0, kind)
+    _call(name, dev, *ptrs, ph, y.data_ptr(), strides, nb, ch, groups, n,
+          PALIMPSA_SCAN_SOFTPLUS if softplus else 0, kind)
     return y

@@ -496,6 +496,38 @@ def test_state_gradients_of_a_packed_batch_on_another_stream():
     _status()
 
 
+def test_fresh_outputs_on_another_stream_are_its_own():
+    """Memory given back on the current stream, with work still queued there that writes it, is not taken for the
+    outputs of a call on another one."""
+    B, T, D, N = 2, 50, 64, 16
+    i = _dev(_dense(_scan_inputs(4, B * T, B, D, 1, N, F32), B))
+    w = torch.randn(D, 4, device=DEV)
+
+    def chain(stream):
+        y, st = pal.palimpsa_causal_conv(i["x"], w, stream=stream)
+        o, h, ck = pal.palimpsa_selective_scan_checkpointed(*i.values(), stream=stream)
+        g = pal.palimpsa_selective_scan_backward(*i.values(), ck, i["x"], stream=stream)
+        c = pal.palimpsa_causal_conv_backward(i["x"], w, None, None, i["x"], stream=stream)
+        return [y, st, o, h, ck, *g.values(), *c.values()]
+
+    want = chain(None)
+    shapes = [t.shape for t in want]
+    busy = torch.randn(4096, 4096, device=DEV)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        busy = busy @ busy * 1e-2
+    old = [torch.full(s, float("nan"), device=DEV) for s in shapes]
+    places = {t.data_ptr() for t in old}
+    del old
+    got = chain(side)
+    assert not places & {t.data_ptr() for t in got}
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    _status()
+
+
 @pytest.mark.parametrize("what", ["A", "dt", "bias"])
 def test_domain_violations_are_latched(what):
     i = _dev(_dense(_scan_inputs(3, 40, 2, 16, 1, 16, F32), 2))
