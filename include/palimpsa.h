@@ -564,12 +564,13 @@ palimpsa_status palimpsa_backward_varlen(
  * those layers: a prompt, a packed batch, one token, and training. Unlike the
  * recurrence above they are laid out token by token:
  *
- *   rows      one row of D channels per token; D a multiple of 8. Dense: B
+ *   rows      one row of D channels per token; D a multiple of 8, at most 2^24. Dense: B
  *             sequences of T rows each. Packed (cu_seqlens not NULL): B sequences
  *             among T rows in all, sequence n = rows [cu_seqlens[n],
  *             cu_seqlens[n+1]), with the rules of palimpsa_forward_varlen for
  *             cu_seqlens (int32, in DEVICE memory, checked there; a sequence that
- *             breaks them is skipped and latches PALIMPSA_ERR_DOMAIN) and
+ *             breaks them is skipped and latches PALIMPSA_ERR_DOMAIN; where
+ *             that makes others overlap, some of them may be skipped too) and
  *             max_seqlen (ignored when dense). Output rows outside every sequence
  *             are not written.
  *   strides   input rows may lie further apart than their width (a slice of a

@@ -76,23 +76,21 @@ __device__ __forceinline__ typename Quad<BF16>::Raw input_row(const ConvArgs& a,
 }
 
 template <bool BF16, int W>
-__global__ void __launch_bounds__(kThreads, kCtas) palimpsa_conv_kernel(ConvArgs a, int runs, int run_len) {
+__global__ void __launch_bounds__(kThreads, kCtas) palimpsa_conv_kernel(ConvArgs a) {
   using Q = Quad<BF16>;
   using Raw = typename Q::Raw;
   const int nvec = a.D / 4;
   const long long i = (long long)blockIdx.x * kThreads + threadIdx.x;
-  if (i >= (long long)nvec * runs * a.rows.n_seq) return;
   const int ch = (int)(i % nvec) * 4;
-  const long long r = i / nvec;
-  const int run = (int)(r % runs);
-  const long long n = r / runs;
   long long row0;
-  int len;
+  int seq, run, len;
+  if (i >= nvec * a.slots.count || !slot_place(a.rows, a.slots, i / nvec, &seq, &run)) return;
+  const long long n = seq;
   if (!seq_rows(a.rows, n, &row0, &len)) {
     if (run == 0 && ch == 0) latch_status(a.status, kStatusDomain);
     return;
   }
-  const int t0 = run * run_len, t1 = min(len, t0 + run_len);
+  const int t0 = run * a.run, t1 = min(len, t0 + a.run);
   if (t0 >= t1 && run > 0) return;
   // A ring of batches in shared memory, each thread its own column: no barriers.
   extern __shared__ __align__(16) unsigned char smem[];
@@ -219,7 +217,7 @@ constexpr int kBwdVecs = 16, kBwdRuns = 16, kBwdCtas = 2, kBwdRing = 3;
 
 template <bool BF16, int W>
 __global__ void __launch_bounds__(kBwdVecs* kBwdRuns, BF16 || W < 4 ? kBwdCtas : 1)
-palimpsa_conv_bwd_kernel(ConvArgs a, int run_len, int blocks_per_seq, float* partial) {
+palimpsa_conv_bwd_kernel(ConvArgs a, float* partial) {
   using Q = Quad<BF16>;
   using Raw = typename Q::Raw;
   constexpr int ES = Vec<BF16>::bytes;
@@ -228,14 +226,17 @@ palimpsa_conv_bwd_kernel(ConvArgs a, int run_len, int blocks_per_seq, float* par
   const long long blk = blockIdx.x / vtiles;  // token block, over all sequences
   const int vec = (int)(blockIdx.x % vtiles) * kBwdVecs + vx;
   const int ch = vec * 4;
-  const long long n = blk / blocks_per_seq;
-  const int t0 = ((int)(blk % blocks_per_seq) * kBwdRuns + ry) * run_len;
-  long long row0;
-  int len;
-  const bool ok = seq_rows(a.rows, n, &row0, &len);
-  if (!ok && threadIdx.x == 0) latch_status(a.status, kStatusDomain);
-  const bool live = ok && vec < nvec;
-  const int t1 = min(len, t0 + run_len);  // this run's tokens are [t0, t1)
+  long long row0 = 0;
+  int seq = 0, place = 0, len = 0;
+  bool live = slot_place(a.rows, a.slots, blk, &seq, &place);
+  const long long n = seq;
+  if (live && !seq_rows(a.rows, n, &row0, &len)) {
+    live = false;
+    if (threadIdx.x == 0) latch_status(a.status, kStatusDomain);
+  }
+  live = live && vec < nvec;
+  const int t0 = (place * kBwdRuns + ry) * a.run;
+  const int t1 = min(len, t0 + a.run);  // this run's tokens are [t0, t1)
   const float2 zero = make_float2(0.f, 0.f);
 
   float2 gw[W][2], gb[2] = {zero, zero};
@@ -417,6 +418,55 @@ __global__ void __launch_bounds__(256) palimpsa_zero_outside_kernel(ZeroArgs a) 
   }
 }
 
+// The slots' starts, by one CTA: sums over the sequences before, 1024 at a time. (In 64 bits:
+// offsets out of order can make valid sequences that overlap, and sums past the bounds.)
+__global__ void __launch_bounds__(1024) palimpsa_slot_starts_kernel(SeqRows r, int piece, int* starts, int* row_starts,
+                                                                    unsigned* status) {
+  __shared__ long long sums[2][32];
+  __shared__ int fit[2];  // ends of the sequences that have slots
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const long long bound = r.T / piece + (long long)r.n_seq;
+  long long before[2] = {0, 0};
+  if (tid < 2) fit[tid] = 0;
+  for (int base = 0; base < r.n_seq; base += 1024) {
+    const bool in = tid < r.n_seq - base;
+    long long row0;
+    int len = 0;
+    const bool ok = in && seq_rows(r, base + tid, &row0, &len);
+    const long long own[2] = {ok ? max(1, (len + piece - 1) / piece) : 0, ok ? len : 0};
+    long long upto[2] = {own[0], own[1]};
+    for (int d = 1; d < 32; d *= 2)
+      for (int q = 0; q < 2; ++q) {
+        const long long o = __shfl_up_sync(~0u, upto[q], d);
+        if (lane >= d) upto[q] += o;
+      }
+    __syncthreads();  // the last round's sums are read
+    if (lane == 31)
+      for (int q = 0; q < 2; ++q) sums[q][warp] = upto[q];
+    __syncthreads();
+    long long all[2] = {0, 0};
+    for (int q = 0; q < 2; ++q)
+      for (int w = 0; w < 32; ++w) {
+        if (w == warp) upto[q] += before[q] + all[q];
+        all[q] += sums[q][w];
+      }
+    const bool fits = upto[0] <= bound && upto[1] <= r.T;
+    if (in && fits)
+      for (int q = 0; q < 2; ++q) atomicMax(&fit[q], (int)upto[q]);
+    __syncthreads();
+    if (in) {
+      starts[base + tid] = fits ? (int)(upto[0] - own[0]) : fit[0];
+      if (row_starts) row_starts[base + tid] = fits ? (int)(upto[1] - own[1]) : fit[1];
+      if (!ok || !fits) latch_status(status, kStatusDomain);
+    }
+    for (int q = 0; q < 2; ++q) before[q] += all[q];
+  }
+  if (tid == 0) {
+    starts[r.n_seq] = fit[0];
+    if (row_starts) row_starts[r.n_seq] = fit[1];
+  }
+}
+
 // Tokens of a run, a multiple of 8: long runs read fewer rows twice and load the taps
 // less often (together about 8 tokens' worth), short ones make CTAs enough, and the CTAs
 // should fill whole waves of the SMs' slots: the cheapest of waves x (run + 8). (With
@@ -445,24 +495,18 @@ int sm_count() {
     return 152;
   return sms;
 }
-int bwd_run_len(const ConvArgs& a) { return run_len_of(a, kBwdVecs * kBwdRuns, kBwdCtas * sm_count(), 8); }
-int bwd_blocks_per_seq(const ConvArgs& a, int run) {
-  const int per = run * kBwdRuns;
-  return std::max(1, (a.rows.max_len + per - 1) / per);
-}
+int bwd_vtiles(const ConvArgs& a) { return (a.D / 4 + kBwdVecs - 1) / kBwdVecs; }
+size_t partial_floats(const ConvArgs& a) { return (size_t)a.slots.count * (a.W + 1) * a.D; }
 
 template <bool BF16, int W>
 cudaError_t backward(const ConvArgs& a, float* scratch, cudaStream_t s) {
-  const int run = bwd_run_len(a), bps = bwd_blocks_per_seq(a, run);
-  const int nvec = a.D / 4, vtiles = (nvec + kBwdVecs - 1) / kBwdVecs;
-  const long long blocks = (long long)bps * a.rows.n_seq;
-  if (blocks * vtiles > 0x7fffffffll) return cudaErrorInvalidConfiguration;
+  const long long blocks = a.slots.count, ctas = blocks * bwd_vtiles(a);
+  if (ctas > 0x7fffffffll) return cudaErrorInvalidConfiguration;
   constexpr int bytes = kBwdRing * 2 * (W == 3 ? 3 : 4) * kBwdVecs * kBwdRuns * (int)sizeof(typename Quad<BF16>::Raw);
   const cudaError_t e = cudaFuncSetAttribute(palimpsa_conv_bwd_kernel<BF16, W>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
-  palimpsa_conv_bwd_kernel<BF16, W>
-      <<<(unsigned)(blocks * vtiles), kBwdVecs * kBwdRuns, bytes, s>>>(a, run, bps, scratch);
+  palimpsa_conv_bwd_kernel<BF16, W><<<(unsigned)ctas, kBwdVecs * kBwdRuns, bytes, s>>>(a, scratch);
   palimpsa_conv_bwd_sum_kernel<<<dim3((a.D + 31) / 32, W + 1), 256, 0, s>>>(scratch, blocks, W, a.D, a.dweight,
                                                                             a.dbias);
   return cudaGetLastError();
@@ -470,12 +514,19 @@ cudaError_t backward(const ConvArgs& a, float* scratch, cudaStream_t s) {
 
 template <bool BF16, int W>
 cudaError_t forward(const ConvArgs& a, cudaStream_t s) {
-  const int run = run_len_of(a, kThreads, kCtas * sm_count(), kMinRun), runs = std::max(1, (a.rows.max_len + run - 1) / run);
-  const long long n = (long long)(a.D / 4) * runs * a.rows.n_seq, blocks = (n + kThreads - 1) / kThreads;
+  const long long blocks = (a.D / 4 * a.slots.count + kThreads - 1) / kThreads;
   if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
   constexpr int bytes = kRing * kBatch * kThreads * (int)sizeof(typename Quad<BF16>::Raw);
-  palimpsa_conv_kernel<BF16, W><<<(unsigned)blocks, kThreads, bytes, s>>>(a, runs, run);
+  palimpsa_conv_kernel<BF16, W><<<(unsigned)blocks, kThreads, bytes, s>>>(a);
   return cudaGetLastError();
+}
+
+// The slots' starts, if they lie close, in scratch behind `floats` floats.
+cudaError_t place_slots(ConvArgs* a, int piece, float* scratch, size_t floats, cudaStream_t s) {
+  if (!a->slots.starts) return cudaSuccess;
+  int* const starts = reinterpret_cast<int*>(scratch + floats);
+  a->slots.starts = starts;
+  return launch_slot_starts(a->rows, piece, starts, nullptr, a->status, s);
 }
 
 template <bool BF16, int W>
@@ -495,17 +546,41 @@ cudaError_t step(const ConvArgs& a, cudaStream_t s) {
     default: return a.bf16 ? f<true, 4>(__VA_ARGS__) : f<false, 4>(__VA_ARGS__); \
   }
 
+cudaError_t launch_slot_starts(const SeqRows& r, int piece, int* starts, int* row_starts, unsigned* status,
+                               cudaStream_t s) {
+  palimpsa_slot_starts_kernel<<<1, 1024, 0, s>>>(r, piece, starts, row_starts, status);
+  return cudaGetLastError();
+}
 cudaError_t launch_zero_outside(const ZeroArgs& a, int n, cudaStream_t s) {
   if (n == 0 || a.rows.T == 0) return cudaSuccess;
   palimpsa_zero_outside_kernel<<<dim3(152, n), 256, 0, s>>>(a);
   return cudaGetLastError();
 }
-cudaError_t launch_conv_forward(const ConvArgs& a, cudaStream_t s) { PALIMPSA_CONV_DISPATCH(forward, a, s) }
-cudaError_t launch_conv_step(const ConvArgs& a, cudaStream_t s) { PALIMPSA_CONV_DISPATCH(step, a, s) }
-size_t conv_backward_scratch_bytes(const ConvArgs& a) {
-  return (size_t)bwd_blocks_per_seq(a, bwd_run_len(a)) * a.rows.n_seq * (a.W + 1) * a.D * sizeof(float);
+size_t plan_conv(ConvArgs* a, bool backward) {
+  const int sms = sm_count();
+  a->run = backward ? run_len_of(*a, kBwdVecs * kBwdRuns, kBwdCtas * sms, 8)
+                    : run_len_of(*a, kThreads, kCtas * sms, kMinRun);
+  const int piece = backward ? a->run * kBwdRuns : a->run;
+  a->slots = slots_of(a->rows, piece);
+  const long long close = close_slots(a->rows, piece), idle = a->slots.count - close;
+  const bool lie_close = close_pays(a->rows, backward ? idle * bwd_vtiles(*a) : idle * (a->D / 4) / kThreads);
+  if (lie_close) {
+    a->slots.count = close;
+    a->slots.starts = a->rows.cu;  // until the launch has a place for them
+  }
+  return (backward ? partial_floats(*a) * sizeof(float) : 0) + (lie_close ? (a->rows.n_seq + 1ull) * sizeof(int) : 0);
 }
-cudaError_t launch_conv_backward(const ConvArgs& a, float* scratch, cudaStream_t s) {
+cudaError_t launch_conv_forward(const ConvArgs& given, float* scratch, cudaStream_t s) {
+  ConvArgs a = given;
+  const cudaError_t e = place_slots(&a, a.run, scratch, 0, s);
+  if (e != cudaSuccess) return e;
+  PALIMPSA_CONV_DISPATCH(forward, a, s)
+}
+cudaError_t launch_conv_step(const ConvArgs& a, cudaStream_t s) { PALIMPSA_CONV_DISPATCH(step, a, s) }
+cudaError_t launch_conv_backward(const ConvArgs& given, float* scratch, cudaStream_t s) {
+  ConvArgs a = given;
+  const cudaError_t e = place_slots(&a, a.run * kBwdRuns, scratch, partial_floats(a), s);
+  if (e != cudaSuccess) return e;
   PALIMPSA_CONV_DISPATCH(backward, a, scratch, s)
 }
 

@@ -83,8 +83,8 @@ struct Smem {
 struct Partials {  // parts of the backward's scratch
   float* bc;   // [tiles][rows][2][N]: dB, dC
   long long rows;
-  float* dA;   // [n_seq, nseg, D, N]
-  float* par;  // [n_seq, nseg, 2, D]: dskip, ddt_bias
+  float* dA;   // [slots, D, N]
+  float* par;  // [slots, 2, D]: dskip, ddt_bias
 };
 
 // NS values of a row of B or C as they came, each twice (for two channels).
@@ -143,8 +143,8 @@ palimpsa_scan_bwd_kernel(ScanArgs a, Partials part, int tiles) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int tile = (int)(blockIdx.x % tiles);
   const long long rest = blockIdx.x / tiles;
-  const int seg = (int)(rest % a.nseg);
-  const long long n = rest / a.nseg;
+  int n, seg;
+  if (!slot_place(a.rows, a.slots, rest, &n, &seg)) return;
   const int per_group = a.D / a.G, tpg = (per_group + CH - 1) / CH;
   const int g = tile / tpg, ch0 = g * per_group + (tile % tpg) * CH;
   const int nch = min(CH, (g + 1) * per_group - ch0);
@@ -158,15 +158,16 @@ palimpsa_scan_bwd_kernel(ScanArgs a, Partials part, int tiles) {
   if (tb >= len && seg > 0) return;
   const int tn = te - tb, nchunk = (tn + kChunk - 1) / kChunk;
 
-  // A lane's CPC channels of the tile from d0 on, as pairs, and its states from n0 on. Quads of 4 channels of odd tokens change places in pairs in shared memory, as in
-  // the forward.
+  // A lane's CPC channels of the tile from d0 on, as pairs, and its states from n0 on. Quads
+  // of 4 channels of odd tokens change places in pairs in shared memory, as in the forward.
   const int cl = lane & 7, sl = lane >> 3, wpart = warp % kParts, n0 = (warp / kParts * 4 + sl) * NS;
   const int d0 = wpart * 16 * CP + CPC * cl, cq0 = d0, cq1 = d0 ^ 4;
   const size_t at = (size_t)(ch0 + d0) * N + n0;  // of the first channel in [D, N]
   bool bad = false;
   float2 A2[CP][NS], gh[CP][NS], dA[CP][NS];
   const float* g0 = nullptr;
-  if (a.carried) g0 = a.seg_state + (size_t)(n * a.nseg + seg) * a.D * N;
+  const long long slot0 = rest - seg;  // of the sequence
+  if (a.carried) g0 = a.seg_state + (size_t)rest * a.D * N;
   else if (a.dh_T) g0 = a.dh_T + (size_t)n * a.D * N;
 #pragma unroll
   for (int c = 0; c < CPC; ++c) {
@@ -182,8 +183,8 @@ palimpsa_scan_bwd_kernel(ScanArgs a, Partials part, int tiles) {
   }
   const int nsegs = (len + a.seg_len - 1) / a.seg_len;  // the sequence's; the ones after this one's summaries
   if (seg + 1 < nsegs && !a.carried && d0 < nch)
-    fold_segments<CPC, NS>(gh, A2, a.seg_state + (size_t)(n * a.nseg + nsegs - 1) * a.D * N + at,
-                           a.seg_dt + (size_t)(n * a.nseg + nsegs - 1) * a.D + ch0 + d0, nsegs - 1 - seg, -1, a.D, N);
+    fold_segments<CPC, NS>(gh, A2, a.seg_state + (size_t)(slot0 + nsegs - 1) * a.D * N + at,
+                           a.seg_dt + (size_t)(slot0 + nsegs - 1) * a.D + ch0 + d0, nsegs - 1 - seg, -1, a.D, N);
   for (int c = tid; c < CH; c += NT) {
     fpar[c] = c < nch && a.dt_bias ? a.dt_bias[ch0 + c] : 0.f;
     fpar[CH + c] = c < nch && a.skip ? a.skip[ch0 + c] : 0.f;
@@ -508,7 +509,7 @@ palimpsa_scan_bwd_kernel(ScanArgs a, Partials part, int tiles) {
   }
   if (bad) latch_status(a.status, kStatusDomain);
 
-  const size_t ns = (size_t)(n * a.nseg + seg);
+  const size_t ns = (size_t)rest;
 #pragma unroll
   for (int c = 0; c < CPC; ++c) {
     if (d0 + c >= nch) continue;
@@ -541,11 +542,9 @@ __device__ __forceinline__ void sum_bc(const ScanArgs& a, const Partials& part, 
   const int per = 2 * a.N / 4;  // threads of a row and group
   const int q = (int)(i % per), g = (int)(i / per % a.G);
   const long long r = i / per / a.G;
-  if (r >= (long long)a.rows.n_seq * a.rows.max_len) return;
-  const long long n = r / a.rows.max_len;
-  const int t = (int)(r % a.rows.max_len);
   long long row0;
-  int len;
+  int n, t, len;
+  if (r >= a.row_slots.count || !slot_place(a.rows, a.row_slots, r, &n, &t)) return;
   if (!seq_rows(a.rows, n, &row0, &len) || t >= len) return;
   const long long row = row0 + t;
   const float* const p = part.bc + ((long long)g * tpg * part.rows + row) * 2 * a.N + 4 * q;
@@ -575,9 +574,13 @@ __device__ __forceinline__ void sum_segments(const ScanArgs& a, long long block,
   const int cx = threadIdx.x % 32, sy = threadIdx.x / 32;
   const long long e = block * 32 + cx;
   float s = 0.f;
-  if (e < per)
+  if (e < per && a.slots.starts) {
+    const int count = a.slots.starts[a.rows.n_seq];
 #pragma unroll 4
-    for (long long i = sy; i < (long long)a.rows.n_seq * a.nseg; i += 8) {
+    for (int i = sy; i < count; i += 8) s += p[i * per + e];
+  } else if (e < per) {
+#pragma unroll 4
+    for (long long i = sy; i < a.slots.count; i += 8) {
       long long row0;
       int len;
       // (an empty sequence has its first segment's zeros; a skipped one has nothing)
@@ -585,6 +588,7 @@ __device__ __forceinline__ void sum_segments(const ScanArgs& a, long long block,
       const long long k = i % a.nseg;
       if (k == 0 || k * a.seg_len < len) s += p[i * per + e];
     }
+  }
   red[sy][cx] = s;
   __syncthreads();
   if (sy || e >= per) return;
@@ -631,14 +635,14 @@ int resident() {
 template <bool BF16, int N>
 cudaError_t run(const ScanArgs& a, const Partials& part, cudaStream_t s) {
   constexpr Smem L(N, Vec<BF16>::bytes);
-  const long long tiles = scan_tiles(a), blocks = tiles * a.rows.n_seq * a.nseg;
+  const long long tiles = scan_tiles(a), blocks = tiles * a.slots.count;
   if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
   cudaError_t e = prepare<BF16, N>();
   if (e != cudaSuccess) return e;
   palimpsa_scan_bwd_kernel<BF16, N><<<(unsigned)blocks, 32 * warps(N), L.total, s>>>(a, part, (int)tiles);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  const long long bc_ctas = ((long long)a.rows.n_seq * a.rows.max_len * a.G * (2 * a.N / 4) + 255) / 256;
+  const long long bc_ctas = (a.row_slots.count * a.G * (2 * a.N / 4) + 255) / 256;
   const long long dA_ctas = ((long long)a.D * a.N + 31) / 32, par_ctas = (2 * a.D + 31) / 32;
   if (bc_ctas + dA_ctas + par_ctas > 0x7fffffffll) return cudaErrorInvalidConfiguration;
   palimpsa_scan_bwd_sum_kernel<BF16><<<(unsigned)(bc_ctas + dA_ctas + par_ctas), 256, 0, s>>>(
@@ -651,7 +655,7 @@ size_t bc_floats(const ScanArgs& a) { return (size_t)scan_tiles(a) * total_rows(
 }  // namespace
 
 size_t scan_backward_scratch_floats(const ScanArgs& a) {
-  const size_t ns = (size_t)a.rows.n_seq * a.nseg;
+  const size_t ns = (size_t)a.slots.count;
   return bc_floats(a) + ns * a.D * a.N + ns * 2 * a.D;
 }
 
@@ -660,7 +664,7 @@ cudaError_t launch_scan_backward(const ScanArgs& a, float* scratch, cudaStream_t
   part.bc = scratch;
   part.rows = total_rows(a);
   part.dA = part.bc + bc_floats(a);
-  part.par = part.dA + (size_t)a.rows.n_seq * a.nseg * a.D * a.N;
+  part.par = part.dA + (size_t)a.slots.count * a.D * a.N;
   if (a.nseg > 1) {
     cudaError_t e = launch_scan_reverse_summary(a, s);
     if (e == cudaSuccess && a.carried) e = launch_scan_carry(a, true, s);

@@ -117,9 +117,13 @@ __global__ void __launch_bounds__(32 * W, kWarpsPerSM / W) palimpsa_scan_kernel(
   const int tile = (int)(blockIdx.x % tiles);
   const long long rest = blockIdx.x / tiles;
   // Pass A leaves out the segment that no other follows.
-  const int nseg = FWD ? a.nseg : a.nseg - 1;
-  const int seg = (int)(rest % nseg) + (REV ? 1 : 0);
-  const long long n = rest / nseg;
+  int n, seg;
+  if (FWD || a.slots.starts) {
+    if (!slot_place(a.rows, a.slots, rest, &n, &seg) || (REV && seg == 0)) return;
+  } else {
+    seg = (int)(rest % (a.nseg - 1)) + (REV ? 1 : 0);
+    n = (int)(rest / (a.nseg - 1));
+  }
   const int per_group = a.D / a.G, tpg = (per_group + CH - 1) / CH;
   const int g = tile / tpg, ch0 = g * per_group + (tile % tpg) * CH;
   const int nch = min(CH, (g + 1) * per_group - ch0);  // a multiple of 8
@@ -198,9 +202,13 @@ __global__ void __launch_bounds__(32 * W, kWarpsPerSM / W) palimpsa_scan_kernel(
   float2 dsum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
   const size_t at = (size_t)(ch0 + 4 * cl) * N + n0;  // of the first channel in [D, N]
   // The start state. With a time split, segment 0's pass A has put h0 into the slot of the
-  // last segment, which no summary takes: h_T may be h0, and another CTA may have written it.
-  float* const slots = a.nseg > 1 ? a.seg_state + (size_t)n * a.nseg * a.D * N : nullptr;  // of the sequence
-  float* const spare = a.nseg > 1 ? slots + (size_t)(a.nseg - 1) * a.D * N : nullptr;
+  // sequence's last segment, which no summary takes: h_T may be h0, and another CTA may have
+  // written it.
+  int slot0 = FWD || a.slots.starts ? (int)rest - seg : n * a.nseg;  // of the sequence
+  asm("" : "+r"(slot0));  // (left to form it anew from the grid's indices, the compiler spills: 2 % of the time)
+  const int nsegs = len > a.seg_len ? (len + a.seg_len - 1) / a.seg_len : 1;
+  float* const slots = a.nseg > 1 ? a.seg_state + (size_t)slot0 * a.D * N : nullptr;
+  float* const spare = a.nseg > 1 ? slots + (size_t)(nsegs - 1) * a.D * N : nullptr;
   const float* h0 = nullptr;
   if (FWD && a.carried) h0 = slots + (size_t)seg * a.D * N;
   else if (FWD && a.h0) h0 = last && seg == 0 ? a.h0 + (size_t)n * a.D * N : spare;
@@ -217,7 +225,7 @@ __global__ void __launch_bounds__(32 * W, kWarpsPerSM / W) palimpsa_scan_kernel(
     }
   }
   if (FWD && seg > 0 && !a.carried && 4 * cl < nch)
-    fold_segments<4, NS>(h, A2, slots + at, a.seg_dt + (size_t)n * a.nseg * a.D + ch0 + 4 * cl, seg, 1, a.D, N);
+    fold_segments<4, NS>(h, A2, slots + at, a.seg_dt + (size_t)slot0 * a.D + ch0 + 4 * cl, seg, 1, a.D, N);
   if (MODE == kSummary && seg == 0 && a.h0 && !a.carried && 4 * cl < nch) {
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
@@ -368,13 +376,13 @@ __global__ void __launch_bounds__(32 * W, kWarpsPerSM / W) palimpsa_scan_kernel(
     }
   }
   if (bad || !(nonneg_finite(least) && nonneg_finite(most))) latch_status(a.status, kStatusDomain);
-  if (!FWD) store_state(a.seg_state + (size_t)(n * a.nseg + seg) * a.D * N);
+  if (!FWD) store_state(a.seg_state + (size_t)(slot0 + seg) * a.D * N);
   else if (last) store_state(a.h_T + (size_t)n * a.D * N);
   if (!FWD && ng == 0)
 #pragma unroll
     for (int c = 0; c < 4; ++c)
       if (4 * cl + c < nch)
-        a.seg_dt[(size_t)(n * a.nseg + seg) * a.D + ch0 + 4 * cl + c] = c & 1 ? dsum[c / 2].y : dsum[c / 2].x;
+        a.seg_dt[(size_t)(slot0 + seg) * a.D + ch0 + 4 * cl + c] = c & 1 ? dsum[c / 2].y : dsum[c / 2].x;
 }
 
 // Start states of the segments, in place over their summaries: one thread per
@@ -388,13 +396,15 @@ __global__ void __launch_bounds__(256) palimpsa_scan_carry_kernel(ScanArgs a, bo
   int len;
   if (!seq_rows(a.rows, n, &row0, &len)) return;
   const int ns = max(1, (len + a.seg_len - 1) / a.seg_len);
+  const long long slot0 = first_slot(a.slots, n) + (reverse ? ns - 1 : 0);
+  if (a.slots.starts && a.slots.starts[n + 1] - a.slots.starts[n] != ns) return;  // it has none
   const float A = decay_rate(a.A[e]);
   const float* const init = reverse ? a.dh_T : a.h0;
   float h = init ? init[n * per + e] : 0.f;
   // 8 segments at a time, their loads first: a store would hold back the next segment's.
   const long long step = reverse ? -1 : 1;
-  float* st = a.seg_state + (n * a.nseg + (reverse ? ns - 1 : 0)) * per + e;
-  const float* sd = a.seg_dt + (n * a.nseg + (reverse ? ns - 1 : 0)) * a.D + d;
+  float* st = a.seg_state + slot0 * per + e;
+  const float* sd = a.seg_dt + slot0 * a.D + d;
   for (int k0 = 0; k0 < ns; k0 += 8) {
     float add[8], sum[8];
 #pragma unroll
@@ -417,7 +427,8 @@ __global__ void __launch_bounds__(256) palimpsa_scan_carry_kernel(ScanArgs a, bo
 template <bool BF16, int NS, int W, int MODE>
 cudaError_t run(const ScanArgs& a, cudaStream_t s) {
   constexpr Smem L(4 * NS * W, 4 * W, Vec<BF16>::bytes, MODE);
-  const long long tiles = scan_tiles(a), blocks = tiles * a.rows.n_seq * (MODE != kForward ? a.nseg - 1 : a.nseg);
+  const bool all = MODE == kForward || a.slots.starts;
+  const long long tiles = scan_tiles(a), blocks = tiles * (all ? a.slots.count : a.rows.n_seq * (a.nseg - 1ll));
   if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
   if (L.total > 48 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(palimpsa_scan_kernel<BF16, NS, W, MODE>,
@@ -441,7 +452,7 @@ cudaError_t dispatch(const ScanArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t plan_scan(ScanArgs* a, bool backward) {
+cudaError_t plan_scan(ScanArgs* a, bool backward, bool* close) {
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
@@ -461,9 +472,6 @@ cudaError_t plan_scan(ScanArgs* a, bool backward) {
   // against 6.4; 8 x 4096 x 1536: 0.41 against 0.97). Pass A is a small part of a backward.
   long long want = (backward ? 2 : 1) * slots / (tiles * seqs);
   if (!backward && want < 3) want = 1;
-  // CTAs of segments past their sequence's end only look and leave, but they and their
-  // scratch are kept to 16 waves.
-  want = std::min(want, std::max(1ll, 16 * slots / (tiles * a->rows.n_seq)));
   want = std::min<long long>(want, len / 32);
   if (want >= 2) {
     const int per = (int)((len + want - 1) / want);
@@ -471,6 +479,12 @@ cudaError_t plan_scan(ScanArgs* a, bool backward) {
     a->nseg = (len + a->seg_len - 1) / a->seg_len;
     a->carried = a->nseg > kFoldSegments;
   }
+  a->slots = slots_of(a->rows, a->seg_len);
+  const long long least = close_slots(a->rows, a->seg_len);
+  long long idle = (a->slots.count - least) * tiles;
+  if (backward) idle += ((long long)a->rows.n_seq * len - a->rows.T) * a->G / 256 * (2 * a->N / 4);  // of the sums
+  *close = close_pays(a->rows, idle);
+  if (*close) a->slots.count = least;
   return cudaSuccess;
 }
 

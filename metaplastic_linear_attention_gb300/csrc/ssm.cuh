@@ -21,6 +21,33 @@ struct SeqRows {
   int max_len = 0;  // longest sequence (= T when dense)
 };
 
+// Pieces of equal length (runs, segments, single rows) that a batch is cut into, one
+// slot each: sequence n has slots n per_seq, ... With `starts`, of a packed batch, they
+// lie close instead, and sequence n has slots starts[n] .. starts[n + 1] - 1.
+struct Slots {
+  const int* starts = nullptr;
+  int per_seq = 1;      // of the longest sequence
+  long long count = 0;  // slots in all; with `starts` their bound, ceil included
+};
+// Slots of pieces of `piece` tokens of every sequence, an empty one having one piece.
+inline Slots slots_of(const SeqRows& r, long long piece) {
+  Slots s;
+  s.per_seq = r.max_len > piece ? (int)((r.max_len + piece - 1) / piece) : 1;
+  s.count = (long long)r.n_seq * s.per_seq;
+  return s;
+}
+inline long long close_slots(const SeqRows& r, long long piece) { return r.T / piece + r.n_seq; }
+// Whether a packed batch's slots should lie close, when the usual ones come to `idle` CTAs
+// without work. Those cost about 1.3 ns each (256 sequences, one of 32768 tokens and the
+// rest of 100, D = 1536: convolution 518 us, where 53 go for its bytes); the kernel that
+// lays the slots close and the searches for a slot's sequence cost 5 to 10 us.
+inline bool close_pays(const SeqRows& r, long long idle) { return r.cu && idle > 16384; }
+// starts[n_seq + 1] for pieces of `piece` tokens and, if not null, row_starts[n_seq + 1] for
+// rows. A sequence that is skipped for its offsets has no slots; nor has one that would
+// pass the bounds, which offsets in order never do.
+cudaError_t launch_slot_starts(const SeqRows& r, int piece, int* starts, int* row_starts, unsigned* status,
+                               cudaStream_t s);
+
 struct ConvArgs {
   const void* x;
   const float* weight;  // [D, W]
@@ -37,13 +64,16 @@ struct ConvArgs {
   float* dbias = nullptr;
   long long x_ld, dy_ld = 0;
   SeqRows rows;
+  Slots slots;  // runs (backward: a CTA's runs), set by plan_conv
+  int run = 0;  // tokens of a run
   int D, W;
   bool silu, bf16;
   unsigned int* status;
 };
-cudaError_t launch_conv_forward(const ConvArgs& a, cudaStream_t s);
+// Sets a->run and a->slots; returns the bytes of scratch that the launch takes.
+size_t plan_conv(ConvArgs* a, bool backward);
+cudaError_t launch_conv_forward(const ConvArgs& a, float* scratch, cudaStream_t s);
 cudaError_t launch_conv_step(const ConvArgs& a, cudaStream_t s);
-size_t conv_backward_scratch_bytes(const ConvArgs& a);
 cudaError_t launch_conv_backward(const ConvArgs& a, float* scratch, cudaStream_t s);
 
 // Zeros in the rows before the first and behind the last sequence of a packed batch, of
@@ -75,10 +105,12 @@ struct ScanArgs {
   bool softplus, bf16;
   unsigned int* status;
   // time split (set by the launcher)
-  int nseg = 1, seg_len = 0;
-  float* seg_state = nullptr;  // [n_seq, nseg, D, N]: summaries, then (if carried) start states
+  int nseg = 1, seg_len = 0;   // of the longest sequence
+  Slots slots;                 // segments
+  Slots row_slots;             // backward, if close: rows
+  float* seg_state = nullptr;  // [slots, D, N]: summaries, then (if carried) start states
   bool carried = false;        // many segments: a kernel of its own folds the summaries
-  float* seg_dt = nullptr;     // [n_seq, nseg, D]: sums of the step sizes
+  float* seg_dt = nullptr;     // [slots, D]: sums of the step sizes
   // backward
   const float* ckpt_in = nullptr;
   const void* dy = nullptr;
@@ -115,11 +147,12 @@ inline long long scan_tiles(const ScanArgs& a) {
   return (long long)a.G * ((dg + kScanChannels - 1) / kScanChannels);
 }
 
-// Plans a scan or its backward: sets a->nseg and a->seg_len (a multiple of
-// kScanCheckpoint). Scratch of scan_scratch_floats() holds a time split.
-cudaError_t plan_scan(ScanArgs* a, bool backward);
-inline size_t scan_scratch_floats(const ScanArgs& a, int nseg) {
-  return nseg > 1 ? (size_t)a.rows.n_seq * nseg * a.D * (a.N + 1) : 0;
+// Plans a scan or its backward: sets a->nseg, a->seg_len (a multiple of kScanCheckpoint)
+// and a->slots, and *close if the slots are to lie close.
+cudaError_t plan_scan(ScanArgs* a, bool backward, bool* close);
+// Scratch of a time split.
+inline size_t scan_scratch_floats(const ScanArgs& a) {
+  return a.nseg > 1 ? (size_t)a.slots.count * a.D * (a.N + 1) : 0;
 }
 cudaError_t launch_scan_forward(const ScanArgs& a, cudaStream_t s);
 cudaError_t launch_scan_step(const ScanArgs& a, cudaStream_t s);
@@ -153,6 +186,28 @@ __device__ __forceinline__ bool seq_rows(const SeqRows& r, long long n, long lon
   *row0 = ok ? s0 : 0;
   *len = ok ? s1 - s0 : 0;
   return ok;
+}
+
+// The sequence n and the place k in it of a slot; false for a slot that no sequence has.
+__device__ __forceinline__ bool slot_place(const SeqRows& r, const Slots& s, long long slot, int* n, int* k) {
+  if (!s.starts) {
+    *n = (int)(slot / s.per_seq);
+    *k = (int)(slot % s.per_seq);
+    return true;
+  }
+  if (slot >= s.starts[r.n_seq]) return false;
+  int lo = 0, hi = r.n_seq;  // starts[lo] <= slot < starts[hi]
+  while (hi - lo > 1) {
+    const int mid = lo + (hi - lo) / 2;
+    if (s.starts[mid] <= slot) lo = mid;
+    else hi = mid;
+  }
+  *n = lo;
+  *k = (int)(slot - s.starts[lo]);
+  return true;
+}
+__device__ __forceinline__ long long first_slot(const Slots& s, int n) {
+  return s.starts ? s.starts[n] : (long long)n * s.per_seq;
 }
 
 // A 16-byte vector of the input type as fp32 values: 8 bf16 or 4 fp32.

@@ -16,9 +16,10 @@ bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 bool dtype_ok(palimpsa_dtype t) { return t == PALIMPSA_F32 || t == PALIMPSA_BF16; }
 
 // Sizes of a batch: rows of D channels in n_seq sequences, dense or packed.
+// (D up to 2^24 keeps a row's offsets in int, its groups' states among them.)
 bool rows_ok(const SeqRows& r, int D) {
   // (T leaves room for the rounding up to whole runs and segments in int)
-  if (r.n_seq < 1 || r.T < 0 || r.T > 0x7fff0000 || D < 1) return false;
+  if (r.n_seq < 1 || r.T < 0 || r.T > 0x7fff0000 || D < 1 || D > 1 << 24) return false;
   if (r.cu && (r.max_len < 0 || r.max_len > r.T)) return false;
   const long long rows = r.cu ? r.T : (long long)r.n_seq * r.T;
   const long long lim = 1LL << 40;
@@ -105,16 +106,29 @@ ScanArgs scan_args(const void* x, const void* dt, const float* A, const void* B,
   return a;
 }
 
-// Scratch of a split scan, its segment states and step sums; null when not split.
-cudaError_t take_scratch(ScanArgs* a, size_t more, cudaStream_t s, float** scratch) {
+// Scratch for a scan, `more` floats of it for the caller: the segments' states and step
+// sums, and, if the slots are to lie close, the slots' starts, which are filled in here.
+cudaError_t take_scratch(ScanArgs* a, size_t more, bool backward, bool close, cudaStream_t s, float** scratch) {
   *scratch = nullptr;
-  const size_t split = (scan_scratch_floats(*a, a->nseg) + 3) / 4 * 4;
-  if (split + more == 0) return cudaSuccess;
-  const cudaError_t e = acquire_scratch((split + more) * sizeof(float), s, scratch);
-  if (e != cudaSuccess) return e;
+  const size_t split = (scan_scratch_floats(*a) + 3) / 4 * 4, n = a->rows.n_seq + 1ull;
+  const size_t ints = close ? (backward ? 2 * n : n) : 0;
+  if (split + more + ints == 0) return cudaSuccess;
+  cudaError_t e = acquire_scratch((split + more + ints) * sizeof(float), s, scratch);
+  if (e != cudaSuccess) {
+    *scratch = nullptr;
+    return e;
+  }
   if (a->nseg > 1) {
     a->seg_state = *scratch + more;
-    a->seg_dt = a->seg_state + (size_t)a->rows.n_seq * a->nseg * a->D * a->N;
+    a->seg_dt = a->seg_state + (size_t)a->slots.count * a->D * a->N;
+  }
+  if (close) {
+    int* const starts = reinterpret_cast<int*>(*scratch + more + split);
+    int* const row_starts = backward ? starts + n : nullptr;
+    a->slots.starts = starts;
+    a->row_slots.starts = row_starts;
+    a->row_slots.count = a->rows.T;
+    return launch_slot_starts(a->rows, a->seg_len, starts, row_starts, a->status, s);
   }
   return cudaSuccess;
 }
@@ -151,8 +165,11 @@ palimpsa_status palimpsa_causal_conv(const void* x, long long x_stride, const fl
   if (palimpsa_status s = conv_checks(a, in_dtype, flags)) return s;
   if (palimpsa_status s = stride_of(x_stride, D, in_dtype, &a.x_ld)) return s;
   if (palimpsa_status s = device_status_word(&a.status)) return s;
-  return launch_conv_forward(a, static_cast<cudaStream_t>(cuda_stream)) == cudaSuccess ? PALIMPSA_OK
-                                                                                     : PALIMPSA_ERR_CUDA;
+  const cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
+  float* scratch = nullptr;
+  const size_t bytes = plan_conv(&a, false);
+  if (bytes && acquire_scratch(bytes, s, &scratch) != cudaSuccess) return PALIMPSA_ERR_CUDA;
+  return release(launch_conv_forward(a, scratch, s), scratch, s);
 }
 
 palimpsa_status palimpsa_zero_rows_outside(void* const* arrays, const long long* row_bytes, int n,
@@ -223,7 +240,7 @@ palimpsa_status palimpsa_causal_conv_backward(const void* x, long long x_stride,
   if (palimpsa_status s = device_status_word(&a.status)) return s;
   const cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
   float* scratch = nullptr;
-  if (acquire_scratch(conv_backward_scratch_bytes(a), s, &scratch) != cudaSuccess) return PALIMPSA_ERR_CUDA;
+  if (acquire_scratch(plan_conv(&a, true), s, &scratch) != cudaSuccess) return PALIMPSA_ERR_CUDA;
   return release(launch_conv_backward(a, scratch, s), scratch, s);
 }
 
@@ -248,11 +265,13 @@ palimpsa_status palimpsa_selective_scan(const void* x, const void* dt, const flo
   if (palimpsa_status s = scan_checks(a, in_dtype, flags)) return s;
   if (palimpsa_status s = scan_strides(&a, strides, in_dtype)) return s;
   if (palimpsa_status s = device_status_word(&a.status)) return s;
-  if (plan_scan(&a, false) != cudaSuccess) return PALIMPSA_ERR_CUDA;
+  bool close;
+  if (plan_scan(&a, false, &close) != cudaSuccess) return PALIMPSA_ERR_CUDA;
   const cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
   float* scratch = nullptr;
-  if (take_scratch(&a, 0, s, &scratch) != cudaSuccess) return PALIMPSA_ERR_CUDA;
-  return release(launch_scan_forward(a, s), scratch, s);
+  cudaError_t e = take_scratch(&a, 0, false, close, s, &scratch);
+  if (e == cudaSuccess) e = launch_scan_forward(a, s);
+  return release(e, scratch, s);
 }
 
 palimpsa_status palimpsa_selective_scan_step(const void* x, const void* dt, const float* A, const void* B_t,
@@ -298,12 +317,15 @@ palimpsa_status palimpsa_selective_scan_backward(
   if (palimpsa_status s = scan_checks(a, in_dtype, flags)) return s;
   if (palimpsa_status s = scan_strides(&a, strides, in_dtype)) return s;
   if (palimpsa_status s = device_status_word(&a.status)) return s;
-  if (plan_scan(&a, true) != cudaSuccess) return PALIMPSA_ERR_CUDA;
+  bool close;
+  if (plan_scan(&a, true, &close) != cudaSuccess) return PALIMPSA_ERR_CUDA;
+  a.row_slots = slots_of(a.rows, 1);
   const cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
   float* scratch = nullptr;
   const size_t more = (scan_backward_scratch_floats(a) + 3) / 4 * 4;
-  if (take_scratch(&a, more, s, &scratch) != cudaSuccess) return PALIMPSA_ERR_CUDA;
-  return release(launch_scan_backward(a, scratch, s), scratch, s);
+  cudaError_t e = take_scratch(&a, more, true, close, s, &scratch);
+  if (e == cudaSuccess) e = launch_scan_backward(a, scratch, s);
+  return release(e, scratch, s);
 }
 
 }  // extern "C"

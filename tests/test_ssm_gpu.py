@@ -204,6 +204,72 @@ def test_scan_packed(dtype, lens, D, G, N):
     _scan_case(dtype, lens, False, D, G, N, True, True, True, tail=2)
 
 
+# One long sequence among hundreds of short ones: the grids cover the batch's rows, not the
+# longest sequence's length times the number of sequences (which would be over 16384 CTAs more).
+def _one_long(count, long, at):
+    return [long if k == at else (0, 1, 3, 2)[k % 4] for k in range(count)]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("at", [0, 333, 599])
+@pytest.mark.parametrize("W", [3, 4])
+def test_conv_packed_one_long(dtype, at, W):
+    test_conv_packed(dtype, _one_long(600, 2000, at), W)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("count,long,at,D,G,N", [
+    (600, 900, 599, 40, 1, 16), (1200, 500, 700, 40, 1, 16), (600, 900, 1, 48, 2, 32), (1100, 900, 0, 16, 1, 128),
+    (1100, 500, 1030, 64, 1, 8)])
+def test_scan_packed_one_long(dtype, count, long, at, D, G, N):
+    _scan_case(dtype, _one_long(count, long, at), False, D, G, N, True, True, True, tail=2)
+
+
+def test_packed_one_long_with_bad_offsets():
+    """As above with a sequence over max_seqlen in the middle and one past the rows at the end: both are skipped."""
+    lens = _one_long(700, 900, 20)
+    lens[400], lens[-1] = 901, 50
+    D, N, cu = 136, 16, _cu(lens)
+    rows, ok = cu[-1] - 5, [k not in (400, 699) for k in range(700)]
+    i, c = _scan_inputs(3, rows, 700, D, 1, N, F32), _conv_inputs(3, rows, 700, D, 4, F32)
+    dy = torch.ones(rows, D)
+    keep = torch.zeros(rows, dtype=torch.bool)
+    for n in range(700):
+        if ok[n]:
+            keep[cu[n]:cu[n + 1]] = True
+    cug = _cu([n for n, fine in zip(lens, ok) if fine])
+    okt = torch.tensor(ok)
+    pick = lambda v: (v[keep] if v.shape[0] == rows else v[okt] if v.shape[0] == 700 else v).to(F64)  # noqa: E731
+    sub = lambda d: {k: pick(v) for k, v in d.items()}  # noqa: E731
+    kw = dict(cu_seqlens=torch.tensor(cu, dtype=torch.int32, device=DEV), max_seqlen=900)
+    zero = torch.zeros(int(okt.sum()), D, N, dtype=F64)
+    y, last, want = ssm.gradients(ssm.scan, sub(i), dy[keep].to(F64), zero, cug)
+    h = torch.full((700, D, N), 7.0, device=DEV)
+    gy, _, ckpt = pal.palimpsa_selective_scan_checkpointed(*_dev(i).values(), h_T=h, **kw)
+    assert pal.palimpsa_get_device_status() == 5
+    g = pal.palimpsa_selective_scan_backward(*_dev(i).values(), ckpt, dy.to(DEV), **kw)
+    assert pal.palimpsa_get_device_status() == 5
+    _near(gy[keep], y, 1e-4, "y")
+    _near(h[okt], last, 1e-4, "h_T")
+    assert (h[~okt] == 7).all() and not gy[~keep].any()
+    for k, name in (("dx", "x"), ("ddt", "dt"), ("dB", "B"), ("dC", "C"), ("dz", "z")):
+        _near(g[k][keep], want[name], 1e-4, k)
+        assert not g[k][~keep].any()
+    for k, name in (("dA", "A"), ("dD", "D"), ("ddt_bias", "dt_bias")):
+        _near(g[k], want[name], 1e-4, k)
+    _near(g["dh0"][okt], want["h0"], 1e-4, "dh0")
+    y, last, want = ssm.gradients(ssm.conv, sub(c), dy[keep].to(F64), torch.zeros(int(okt.sum()), 3, D, dtype=F64), cug)
+    gy, gs = pal.palimpsa_causal_conv(*_dev(c).values(), **kw)
+    assert pal.palimpsa_get_device_status() == 5
+    g = pal.palimpsa_causal_conv_backward(*_dev(c).values(), dy.to(DEV), **kw)
+    assert pal.palimpsa_get_device_status() == 5
+    _near(gy[keep], y, 2e-6, "y")
+    assert torch.equal(gs[okt].cpu().to(F64), last) and not gy[~keep].any()
+    _near(g["dx"][keep], want["x"], 2e-6, "dx")
+    _near(g["dweight"], want["weight"], 1e-5, "dweight")
+    _near(g["dbias"], want["bias"], 1e-5, "dbias")
+
+
 def test_scan_leaves_rows_behind_the_last_sequence():
     lens, D, N = [5, 300], 32, 16
     cu = torch.tensor(_cu(lens), dtype=torch.int32, device=DEV)
