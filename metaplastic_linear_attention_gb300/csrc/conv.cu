@@ -207,8 +207,8 @@ __global__ void __launch_bounds__(kThreads) palimpsa_conv_step_kernel(ConvArgs a
 //   du_t = dy_t silu'(u_t),  silu'(u) = p (1 + u (1 - p)),  p = sigmoid(u)
 //   dx_t = sum_j w_j du_{t + (W-1) - j}   (+ dstate_T for the last W - 1 inputs)
 //   dw_j = sum_t du_t x_{t - (W-1) + j},  dbias = sum_t du_t.
-// u is recomputed from x. A CTA owns 16 quads of channels and 16 runs of tokens, one
-// run to a thread; each thread walks its run in batches of 3 or 4 tokens through a ring
+// u is recomputed from x. A CTA owns 16 quads of channels and 16 runs of tokens (of any
+// sequences), one run to a thread; each thread walks its run in batches of 3 or 4 tokens through a ring
 // like the forward's, with the last W inputs and du's in registers, and looks W - 1
 // tokens past its end for the dx of its last ones. The parameter sums go over
 // the CTA's runs in shared memory and then, in a fixed order, over CTAs in a second
@@ -223,19 +223,19 @@ palimpsa_conv_bwd_kernel(ConvArgs a, float* partial) {
   constexpr int ES = Vec<BF16>::bytes;
   const int nvec = a.D / 4, vtiles = (nvec + kBwdVecs - 1) / kBwdVecs;
   const int vx = threadIdx.x % kBwdVecs, ry = threadIdx.x / kBwdVecs;
-  const long long blk = blockIdx.x / vtiles;  // token block, over all sequences
+  const long long blk = blockIdx.x / vtiles;  // of kBwdRuns slots, over all sequences
   const int vec = (int)(blockIdx.x % vtiles) * kBwdVecs + vx;
   const int ch = vec * 4;
   long long row0 = 0;
   int seq = 0, place = 0, len = 0;
-  bool live = slot_place(a.rows, a.slots, blk, &seq, &place);
+  const long long slot = blk * kBwdRuns + ry;
+  bool live = vec < nvec && slot < a.slots.count && slot_place(a.rows, a.slots, slot, &seq, &place);
   const long long n = seq;
   if (live && !seq_rows(a.rows, n, &row0, &len)) {
     live = false;
-    if (threadIdx.x == 0) latch_status(a.status, kStatusDomain);
+    latch_status(a.status, kStatusDomain);
   }
-  live = live && vec < nvec;
-  const int t0 = (place * kBwdRuns + ry) * a.run;
+  const int t0 = place * a.run;
   const int t1 = min(len, t0 + a.run);  // this run's tokens are [t0, t1)
   const float2 zero = make_float2(0.f, 0.f);
 
@@ -496,11 +496,12 @@ int sm_count() {
   return sms;
 }
 int bwd_vtiles(const ConvArgs& a) { return (a.D / 4 + kBwdVecs - 1) / kBwdVecs; }
-size_t partial_floats(const ConvArgs& a) { return (size_t)a.slots.count * (a.W + 1) * a.D; }
+long long bwd_blocks(const ConvArgs& a) { return (a.slots.count + kBwdRuns - 1) / kBwdRuns; }
+size_t partial_floats(const ConvArgs& a) { return (size_t)bwd_blocks(a) * (a.W + 1) * a.D; }
 
 template <bool BF16, int W>
 cudaError_t backward(const ConvArgs& a, float* scratch, cudaStream_t s) {
-  const long long blocks = a.slots.count, ctas = blocks * bwd_vtiles(a);
+  const long long blocks = bwd_blocks(a), ctas = blocks * bwd_vtiles(a);
   if (ctas > 0x7fffffffll) return cudaErrorInvalidConfiguration;
   constexpr int bytes = kBwdRing * 2 * (W == 3 ? 3 : 4) * kBwdVecs * kBwdRuns * (int)sizeof(typename Quad<BF16>::Raw);
   const cudaError_t e = cudaFuncSetAttribute(palimpsa_conv_bwd_kernel<BF16, W>,
@@ -522,11 +523,11 @@ cudaError_t forward(const ConvArgs& a, cudaStream_t s) {
 }
 
 // The slots' starts, if they lie close, in scratch behind `floats` floats.
-cudaError_t place_slots(ConvArgs* a, int piece, float* scratch, size_t floats, cudaStream_t s) {
+cudaError_t place_slots(ConvArgs* a, float* scratch, size_t floats, cudaStream_t s) {
   if (!a->slots.starts) return cudaSuccess;
   int* const starts = reinterpret_cast<int*>(scratch + floats);
   a->slots.starts = starts;
-  return launch_slot_starts(a->rows, piece, starts, nullptr, a->status, s);
+  return launch_slot_starts(a->rows, a->run, starts, nullptr, a->status, s);
 }
 
 template <bool BF16, int W>
@@ -560,10 +561,9 @@ size_t plan_conv(ConvArgs* a, bool backward) {
   const int sms = sm_count();
   a->run = backward ? run_len_of(*a, kBwdVecs * kBwdRuns, kBwdCtas * sms, 8)
                     : run_len_of(*a, kThreads, kCtas * sms, kMinRun);
-  const int piece = backward ? a->run * kBwdRuns : a->run;
-  a->slots = slots_of(a->rows, piece);
-  const long long close = close_slots(a->rows, piece), idle = a->slots.count - close;
-  const bool lie_close = close_pays(a->rows, backward ? idle * bwd_vtiles(*a) : idle * (a->D / 4) / kThreads);
+  a->slots = slots_of(a->rows, a->run);
+  const long long close = close_slots(a->rows, a->run), idle = a->slots.count - close;
+  const bool lie_close = close_pays(a->rows, idle * (a->D / 4) / (backward ? kBwdRuns * kBwdVecs : kThreads));
   if (lie_close) {
     a->slots.count = close;
     a->slots.starts = a->rows.cu;  // until the launch has a place for them
@@ -572,14 +572,14 @@ size_t plan_conv(ConvArgs* a, bool backward) {
 }
 cudaError_t launch_conv_forward(const ConvArgs& given, float* scratch, cudaStream_t s) {
   ConvArgs a = given;
-  const cudaError_t e = place_slots(&a, a.run, scratch, 0, s);
+  const cudaError_t e = place_slots(&a, scratch, 0, s);
   if (e != cudaSuccess) return e;
   PALIMPSA_CONV_DISPATCH(forward, a, s)
 }
 cudaError_t launch_conv_step(const ConvArgs& a, cudaStream_t s) { PALIMPSA_CONV_DISPATCH(step, a, s) }
 cudaError_t launch_conv_backward(const ConvArgs& given, float* scratch, cudaStream_t s) {
   ConvArgs a = given;
-  const cudaError_t e = place_slots(&a, a.run * kBwdRuns, scratch, partial_floats(a), s);
+  const cudaError_t e = place_slots(&a, scratch, partial_floats(a), s);
   if (e != cudaSuccess) return e;
   PALIMPSA_CONV_DISPATCH(backward, a, scratch, s)
 }

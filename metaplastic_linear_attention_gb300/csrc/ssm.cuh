@@ -64,7 +64,7 @@ struct ConvArgs {
   float* dbias = nullptr;
   long long x_ld, dy_ld = 0;
   SeqRows rows;
-  Slots slots;  // runs (backward: a CTA's runs), set by plan_conv
+  Slots slots;  // runs, set by plan_conv
   int run = 0;  // tokens of a run
   int D, W;
   bool silu, bf16;
