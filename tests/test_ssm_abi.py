@@ -61,6 +61,7 @@ def test_gate_needs_its_gradient(lib):
     (dict(dtype=2), ERR_DTYPE), (dict(dtype=-1), ERR_DTYPE), (dict(flags=2), ERR_UNSUPPORTED), (dict(B=0), ERR_SHAPE),
     (dict(B=-1), ERR_SHAPE), (dict(D=0), ERR_SHAPE), (dict(D=-8), ERR_SHAPE), (dict(D=12), ERR_UNSUPPORTED),
     (dict(x=P + 8), ERR_ALIGN), (dict(B=1 << 30, D=1 << 20), ERR_SHAPE),
+    (dict(D=(1 << 24) + 8), ERR_SHAPE),
 ])
 def test_common_refusals(lib, name, over, code):
     assert _call(lib, name, **over) == code

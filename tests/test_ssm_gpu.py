@@ -714,6 +714,39 @@ def test_on_a_side_stream_and_in_a_graph(side):
     _status()
 
 
+def test_graph_of_a_packed_batch_takes_new_offsets():
+    """A captured run of the packed operators replays on offsets, and rows, that were written after its capture."""
+    D, N, count = 136, 16, 700
+    batches = [_cu(_one_long(count, 900, at)) for at in (4, 640)]
+    rows = max(cu[-1] for cu in batches) + 2
+    w = torch.randn(D, 4, device=DEV)
+    ins = [_dev(_scan_inputs(k, rows, count, D, 1, N, F32)) for k in (1, 2)]
+    cud = torch.tensor(batches[0], dtype=torch.int32, device=DEV)
+    i = {k: v.clone() for k, v in ins[0].items()}
+    kw = dict(cu_seqlens=cud, max_seqlen=900)
+
+    def chain():
+        u, st = pal.palimpsa_causal_conv(i["x"], w, **kw)
+        y, h, ck = pal.palimpsa_selective_scan_checkpointed(*dict(i, x=u).values(), **kw)
+        g = pal.palimpsa_selective_scan_backward(*dict(i, x=u).values(), ck, i["x"], **kw)
+        c = pal.palimpsa_causal_conv_backward(i["x"], w, None, None, g["dx"], **kw)
+        return [u, st, y, h, *g.values(), *c.values()]
+
+    chain()
+    torch.cuda.synchronize()
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        out = chain()
+    for cu, src in zip(batches[::-1], ins[::-1]):
+        cud.copy_(torch.tensor(cu, dtype=torch.int32))
+        for k, v in i.items():
+            v.copy_(src[k])
+        gr.replay()
+        got = [t.clone() for t in out]
+        assert all(torch.equal(p, q) for p, q in zip(got, chain()))
+    _status()
+
+
 def test_layer_prompt_then_tokens_and_training():
     """A state-space layer's middle as it is used: projection slices -> convolution -> scan over a packed prompt,
     then tokens from the states it left, against one dense pass of the oracle; and its gradients chained."""
