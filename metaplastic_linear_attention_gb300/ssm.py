@@ -139,9 +139,11 @@ def _call(name, dev, *args):
 
 
 def _on_stream(fn):
-    """Adds the argument `stream` to an operator: the stream to run on, instead of the current one.
-    What the call allocates and fills in belongs to that stream, so that nothing queued on the
-    current one can touch it. The inputs are recorded there and fresh outputs on the current
+    """Adds the argument `stream` to an operator: the stream to run on, instead of the current one,
+    whose queued work it first waits for (as every call of this package does: the inputs are
+    usually made there). The caller waits for it before using the results elsewhere.
+    What the call allocates and fills in belongs to that stream, so that nothing queued later on
+    the current one can touch it. The inputs are recorded there and fresh outputs on the current
     stream, so that the allocator keeps either until both streams are done with it."""
     @functools.wraps(fn)
     def call(*args, stream=None, **kw):
@@ -154,6 +156,7 @@ def _on_stream(fn):
         home = torch.cuda.current_stream(stream.device)
         if stream == home:
             return fn(*args, **kw)
+        binding._stream_handle(stream)  # waits for the current stream
         with torch.cuda.stream(stream):
             out = fn(*args, **kw)
         for t in given:
