@@ -79,6 +79,9 @@ struct StreamOrderedScratch final : ScratchProvider {
     void* v = nullptr;
     e = cudaMallocFromPoolAsync(&v, bytes, pool, s);
     *p = static_cast<float*>(v);
+    // The caller gets the error; left as the thread's last one, the next launch's check (this
+    // library's or PyTorch's) would take it for its own.
+    if (e != cudaSuccess) cudaGetLastError();
     return e;
   }
   cudaError_t release(float* p, cudaStream_t s) override { return cudaFreeAsync(p, s); }
