@@ -612,13 +612,24 @@ palimpsa_status palimpsa_causal_conv(
 /*
  * palimpsa_zero_rows_outside - zeros in the rows of up to 8 dense arrays that lie
  * before the first and behind the last sequence of a packed batch, or in a sequence
- * that is skipped for its offsets (T rows of row_bytes[i] bytes each, a multiple of
- * 16; arrays and row_bytes are HOST arrays of n entries). For outputs that the calls
- * here leave unwritten there, to be called before them; it costs next to nothing
- * where the sequences fill the rows.
+ * that is skipped for its offsets, and in all rows where an offset is below the one
+ * before it (T rows of row_bytes[i] bytes each, a multiple of 16; arrays and row_bytes
+ * are HOST arrays of n entries). For outputs that the calls here leave unwritten there,
+ * to be called before them; it costs next to nothing where the sequences fill the rows.
  */
 palimpsa_status palimpsa_zero_rows_outside(
     void* const* arrays, const long long* row_bytes, int n,
+    const int* cu_seqlens, int B, int T, int max_seqlen, void* cuda_stream);
+
+/*
+ * palimpsa_zero_unwritten - the same in one call with arrays of one entry per sequence
+ * (states and their gradients: B entries of state_bytes[i] bytes each, a multiple of 16),
+ * where the entries of skipped sequences are zeroed, and all of them where an offset is
+ * below the one before it. At most 8 arrays in all.
+ */
+palimpsa_status palimpsa_zero_unwritten(
+    void* const* arrays, const long long* row_bytes, int n,
+    void* const* states, const long long* state_bytes, int n_states,
     const int* cu_seqlens, int B, int T, int max_seqlen, void* cuda_stream);
 
 /* palimpsa_causal_conv_step - one token: x, y rows of B sequences, state

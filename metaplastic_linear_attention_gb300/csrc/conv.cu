@@ -16,6 +16,7 @@
 // copy of as many bytes; backward 18 us at 4 x 2048 x 1024
 // (7 for its bytes; its window of W inputs and W gradients holds it to 16 warps an SM).
 #include <algorithm>
+#include <cooperative_groups.h>
 
 #include "ssm.cuh"
 
@@ -392,28 +393,65 @@ __global__ void __launch_bounds__(256) palimpsa_conv_bwd_sum_kernel(const float*
   }
 }
 
-__global__ void __launch_bounds__(256) palimpsa_zero_outside_kernel(ZeroArgs a) {
-  const long long T = a.rows.T, w = a.width[blockIdx.y] / 16;
-  const long long lo = min(max((long long)a.rows.cu[0], 0ll), T);
-  const long long hi = min(max((long long)a.rows.cu[a.rows.n_seq], lo), T);
-  uint4* const p = static_cast<uint4*>(a.p[blockIdx.y]);
-  const long long step = (long long)gridDim.x * 256, i0 = (long long)blockIdx.x * 256 + threadIdx.x;
-  for (long long i = i0; i < lo * w; i += step) p[i] = make_uint4(0, 0, 0, 0);
-  for (long long i = hi * w + i0; i < T * w; i += step) p[i] = make_uint4(0, 0, 0, 0);
-  // Sequences that are skipped for their offsets, each by the warp that finds it.
+// Where an offset is below the one before it, sequences may overlap, and those that do not
+// fit the close slots are skipped, which only the kernel that lays the slots knows:
+// everything is zeroed then. Every CTA looks all offsets over; with many sequences the 8 CTAs
+// of a cluster do so together (SHARED): 28 us against 390 for 2^20 sequences, the same for
+// 4096, and for 24, where the whole takes 4 us, 1.7 more.
+constexpr int kZeroCtas = 152, kZeroCluster = 8, kZeroAlone = 4096;
+template <bool SHARED>
+__global__ void __launch_bounds__(SHARED ? 512 : 256) palimpsa_zero_outside_kernel(ZeroArgs a, int arrays) {
+  namespace cg = cooperative_groups;
+  constexpr int kZeroThreads = SHARED ? 512 : 256;
+  const int* const cu = a.rows.cu;
+  const long long T = a.rows.T, n_seq = a.rows.n_seq;
+  const long long first = min(max((long long)cu[0], 0ll), T), last = min(max((long long)cu[n_seq], first), T);
+  bool down = false;
+  const int part = SHARED ? blockIdx.x % kZeroCluster : 0, parts = SHARED ? kZeroCluster : 1;
+#pragma unroll 8
+  for (long long n = part * kZeroThreads + threadIdx.x; n < n_seq; n += parts * kZeroThreads) down |= cu[n + 1] < cu[n];
+  down = __syncthreads_or(down);
+  if constexpr (SHARED) {
+    __shared__ int seen;  // by any CTA of the cluster
+    const cg::cluster_group cluster = cg::this_cluster();
+    if (threadIdx.x == 0) seen = 0;
+    cluster.sync();  // every CTA of the cluster is there, its flag clear
+    if (down && threadIdx.x < kZeroCluster) *cluster.map_shared_rank(&seen, threadIdx.x) = 1;
+    cluster.sync();
+    down = seen;
+  }
+
+  const long long step = (long long)gridDim.x * kZeroThreads, i0 = (long long)blockIdx.x * kZeroThreads + threadIdx.x;
   const int lane = threadIdx.x & 31;
-  for (long long n0 = i0 - lane; n0 < a.rows.n_seq; n0 += step) {
-    int from = 0, to = 0;
-    if (n0 + lane < a.rows.n_seq) {
-      const long long s0 = a.rows.cu[n0 + lane], s1 = a.rows.cu[n0 + lane + 1];
-      if (s0 < 0 || s1 > T || s1 - s0 > a.rows.max_len) {
-        from = (int)min(max(s0, 0ll), T);
-        to = (int)min(max(s1, 0ll), T);
-      }
+  for (int k = 0; k < arrays; ++k) {
+    const bool per_token = k < a.row_arrays;
+    const long long rows = per_token ? T : n_seq, w = a.width[k] / 16;
+    long long lo = 0, hi = rows;  // rows [lo, hi) are left to the sequences
+    if (down) {
+      lo = rows;
+    } else if (per_token) {
+      lo = first;
+      hi = last;
     }
-    for (unsigned left = __ballot_sync(~0u, to > from); left; left &= left - 1) {
-      const long long r0 = __shfl_sync(~0u, from, __ffs(left) - 1), r1 = __shfl_sync(~0u, to, __ffs(left) - 1);
-      for (long long i = r0 * w + lane; i < r1 * w; i += 32) p[i] = make_uint4(0, 0, 0, 0);
+    uint4* const p = static_cast<uint4*>(a.p[k]);
+    for (long long i = i0; i < lo * w; i += step) p[i] = make_uint4(0, 0, 0, 0);
+    for (long long i = hi * w + i0; i < rows * w; i += step) p[i] = make_uint4(0, 0, 0, 0);
+    if (down) continue;
+    // Sequences that are skipped for their offsets, each by the warp that finds it.
+    for (long long n0 = i0 - lane; n0 < n_seq; n0 += step) {
+      const long long n = n0 + lane;
+      int from = 0, to = 0;
+      if (n < n_seq) {
+        const long long s0 = cu[n], s1 = cu[n + 1];
+        if (s0 < 0 || s1 > T || s1 - s0 > a.rows.max_len) {
+          from = per_token ? (int)min(max(s0, 0ll), T) : (int)n;
+          to = per_token ? (int)min(max(s1, 0ll), T) : (int)n + 1;
+        }
+      }
+      for (unsigned left = __ballot_sync(~0u, to > from); left; left &= left - 1) {
+        const long long r0 = __shfl_sync(~0u, from, __ffs(left) - 1), r1 = __shfl_sync(~0u, to, __ffs(left) - 1);
+        for (long long i = r0 * w + lane; i < r1 * w; i += 32) p[i] = make_uint4(0, 0, 0, 0);
+      }
     }
   }
 }
@@ -552,10 +590,23 @@ cudaError_t launch_slot_starts(const SeqRows& r, int piece, int* starts, int* ro
   palimpsa_slot_starts_kernel<<<1, 1024, 0, s>>>(r, piece, starts, row_starts, status);
   return cudaGetLastError();
 }
-cudaError_t launch_zero_outside(const ZeroArgs& a, int n, cudaStream_t s) {
-  if (n == 0 || a.rows.T == 0) return cudaSuccess;
-  palimpsa_zero_outside_kernel<<<dim3(152, n), 256, 0, s>>>(a);
-  return cudaGetLastError();
+cudaError_t launch_zero_outside(const ZeroArgs& a, int arrays, cudaStream_t s) {
+  if (arrays == 0) return cudaSuccess;
+  if (a.rows.n_seq <= kZeroAlone) {
+    palimpsa_zero_outside_kernel<false><<<kZeroCtas, 256, 0, s>>>(a, arrays);
+    return cudaGetLastError();
+  }
+  cudaLaunchAttribute cluster = {};
+  cluster.id = cudaLaunchAttributeClusterDimension;
+  cluster.val.clusterDim.x = kZeroCluster;
+  cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
+  cudaLaunchConfig_t c = {};
+  c.gridDim = dim3(kZeroCtas);
+  c.blockDim = dim3(512);
+  c.stream = s;
+  c.attrs = &cluster;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, palimpsa_zero_outside_kernel<true>, a, arrays);
 }
 size_t plan_conv(ConvArgs* a, bool backward) {
   const int sms = sm_count();

@@ -76,15 +76,18 @@ cudaError_t launch_conv_forward(const ConvArgs& a, float* scratch, cudaStream_t 
 cudaError_t launch_conv_step(const ConvArgs& a, cudaStream_t s);
 cudaError_t launch_conv_backward(const ConvArgs& a, float* scratch, cudaStream_t s);
 
-// Zeros in the rows before the first and behind the last sequence of a packed batch, of
-// up to kZeroArrays dense arrays (row widths in bytes, multiples of 16).
+// Zeros in what the kernels leave unwritten of a packed batch's outputs: rows that no
+// sequence covers, and the rows and states of skipped sequences, of up to kZeroArrays dense
+// arrays (widths in bytes, multiples of 16), the first row_arrays of them with a row per
+// token, the others with an entry per sequence.
 constexpr int kZeroArrays = 8;
 struct ZeroArgs {
   void* p[kZeroArrays];
   long long width[kZeroArrays];
+  int row_arrays;
   SeqRows rows;
 };
-cudaError_t launch_zero_outside(const ZeroArgs& a, int n, cudaStream_t s);
+cudaError_t launch_zero_outside(const ZeroArgs& a, int arrays, cudaStream_t s);
 
 struct ScanArgs {
   const void* x;

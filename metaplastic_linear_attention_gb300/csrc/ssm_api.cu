@@ -174,19 +174,36 @@ palimpsa_status palimpsa_causal_conv(const void* x, long long x_stride, const fl
 
 palimpsa_status palimpsa_zero_rows_outside(void* const* arrays, const long long* row_bytes, int n,
                                            const int* cu_seqlens, int B, int T, int max_seqlen, void* cuda_stream) {
-  if (!cu_seqlens || (n > 0 && (!arrays || !row_bytes))) return PALIMPSA_ERR_NULL;
-  if (n < 0 || n > kZeroArrays || B < 1 || T < 0 || max_seqlen < 0 || max_seqlen > T) return PALIMPSA_ERR_SHAPE;
+  return palimpsa_zero_unwritten(arrays, row_bytes, n, nullptr, nullptr, 0, cu_seqlens, B, T, max_seqlen, cuda_stream);
+}
+
+palimpsa_status palimpsa_zero_unwritten(void* const* arrays, const long long* row_bytes, int n, void* const* states,
+                                        const long long* state_bytes, int n_states, const int* cu_seqlens, int B, int T,
+                                        int max_seqlen, void* cuda_stream) {
+  if (!cu_seqlens || (n > 0 && (!arrays || !row_bytes)) || (n_states > 0 && (!states || !state_bytes)))
+    return PALIMPSA_ERR_NULL;
+  if (n < 0 || n_states < 0 || n > kZeroArrays || n_states > kZeroArrays - n) return PALIMPSA_ERR_SHAPE;
+  if (B < 1 || T < 0 || max_seqlen < 0 || max_seqlen > T) return PALIMPSA_ERR_SHAPE;
   if (!aligned(cu_seqlens, 4)) return PALIMPSA_ERR_ALIGN;
   ZeroArgs a{};
   a.rows = rows_of(cu_seqlens, B, T, max_seqlen);
-  for (int i = 0; i < n; ++i) {
-    if (!arrays[i] && T != 0) return PALIMPSA_ERR_NULL;
-    if (row_bytes[i] < 0 || row_bytes[i] > (1LL << 40) / (T > 0 ? T : 1)) return PALIMPSA_ERR_SHAPE;
-    if (!aligned(arrays[i], 16) || row_bytes[i] % 16) return PALIMPSA_ERR_ALIGN;
-    a.p[i] = arrays[i];
-    a.width[i] = row_bytes[i];
-  }
-  return launch_zero_outside(a, n, static_cast<cudaStream_t>(cuda_stream)) == cudaSuccess ? PALIMPSA_OK
+  a.row_arrays = T > 0 ? n : 0;
+  int k = 0;
+  auto add = [&](void* p, long long bytes, int entries) {
+    if (!p && entries != 0) return PALIMPSA_ERR_NULL;
+    if (bytes < 0 || bytes > (1LL << 40) / (entries > 0 ? entries : 1)) return PALIMPSA_ERR_SHAPE;
+    if (!aligned(p, 16) || bytes % 16) return PALIMPSA_ERR_ALIGN;
+    if (entries > 0) {
+      a.p[k] = p;
+      a.width[k++] = bytes;
+    }
+    return PALIMPSA_OK;
+  };
+  for (int i = 0; i < n; ++i)
+    if (const palimpsa_status s = add(arrays[i], row_bytes[i], T)) return s;
+  for (int i = 0; i < n_states; ++i)
+    if (const palimpsa_status s = add(states[i], state_bytes[i], B)) return s;
+  return launch_zero_outside(a, k, static_cast<cudaStream_t>(cuda_stream)) == cudaSuccess ? PALIMPSA_OK
                                                                                         : PALIMPSA_ERR_CUDA;
 }
 

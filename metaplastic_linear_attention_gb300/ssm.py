@@ -42,6 +42,7 @@ def _library():
             "palimpsa_causal_conv_step": [p, ll, p, p, p, p, i, i, i, u, i, p],
             "palimpsa_causal_conv_backward": [p, ll, p, p, p, p, ll, p, p, p, p, p, p, i, i, i, i, i, u, i, p],
             "palimpsa_zero_rows_outside": [p, p, i, p, i, i, i, p],
+            "palimpsa_zero_unwritten": [p, p, i, p, p, i, p, i, i, i, p],
             "palimpsa_selective_scan": [p] * 12 + [st, p, i, i, i, i, i, i, u, i, p],
             "palimpsa_selective_scan_step": [p] * 10 + [st, i, i, i, i, u, i, p],
             "palimpsa_selective_scan_backward": [p] * 20 + [st, p, i, i, i, i, i, i, u, i, p],
@@ -197,13 +198,23 @@ def _like(t):
     return torch.empty_like(t) if t.is_contiguous() else torch.empty(t.shape, dtype=t.dtype, device=t.device)
 
 
-def _zero_outside(outs, cu, nb, rows, longest, dev):
-    """Zeros in the rows of freshly allocated outputs that no sequence of a packed batch covers, or
-    only one that is skipped for its offsets."""
-    if cu is not None and outs and rows:
-        p = (ctypes.c_void_p * len(outs))(*(t.data_ptr() for t in outs))
-        w = (ctypes.c_longlong * len(outs))(*(t.numel() // rows * t.element_size() for t in outs))
-        _call("palimpsa_zero_rows_outside", dev, p, w, len(outs), cu.data_ptr(), nb, rows, longest)
+def _zero_unwritten(outs, states, cu, nb, rows, longest, dev):
+    """Zeros in what a packed call leaves as it is of its freshly allocated outputs: the rows (of
+    `outs`) that no sequence covers, and the rows and `states` of sequences that are skipped for their
+    offsets. (Where offsets are out of order, everything.)"""
+    if cu is None:
+        return
+    outs = outs if rows else ()
+    arrays = lambda ts: (ctypes.c_void_p * len(ts))(*(t.data_ptr() for t in ts))  # noqa: E731
+    widths = lambda ts, n: (ctypes.c_longlong * len(ts))(*(t.numel() // n * t.element_size() for t in ts))  # noqa: E731
+    _call("palimpsa_zero_unwritten", dev, arrays(outs), widths(outs, rows), len(outs), arrays(states), widths(states, nb),
+          len(states), cu.data_ptr(), nb, rows, longest)
+
+
+def _zero_fresh(given, outs, cu, nb, rows, longest, dev):
+    """_zero_unwritten for a forward's (y, state) of which only those that the caller did not give are fresh."""
+    if cu is not None and (given[0] is None or given[1] is None):
+        _zero_unwritten(outs[:1] if given[0] is None else (), outs[1:] if given[1] is None else (), cu, nb, rows, longest, dev)
 
 
 # ------------------------------------------------------------------ causal convolution
@@ -219,9 +230,9 @@ def palimpsa_causal_conv(x, weight, bias=None, state0=None, *, silu=True, cu_seq
     """Depthwise causal convolution along the tokens (see palimpsa.h).
 
     x [B, T, D], or [rows, D] with cu_seqlens [B + 1] int32 (max_seqlen: the longest
-    sequence, read from cu_seqlens when not given, which synchronises); weight [D, W],
-    bias [D] fp32; state0 [B, W - 1, D]: the inputs before each sequence, or None for
-    zeros. Returns (y, state_T), both in x's dtype; state_T may be given as state0."""
+    sequence, read from cu_seqlens when not given, which synchronises; what no sequence
+    writes of outputs that are not given is zero); weight [D, W], bias [D] fp32; state0
+    [B, W - 1, D]: the inputs before each sequence, or None for zeros. Returns (y, state_T), both in x's dtype; state_T may be given as state0."""
     name = "palimpsa_causal_conv"
     dev = _device(x, name)
     B, T, longest, cu, lead = _batch(x, cu_seqlens, max_seqlen, dev, name)
@@ -229,14 +240,13 @@ def palimpsa_causal_conv(x, weight, bias=None, state0=None, *, silu=True, cu_seq
     kind = _dtype(x)
     ld = _rows(x, "x", x.shape, x.dtype, dev, lead)
     ps = _dense(state0, "state0", (B, W - 1, D), x.dtype, dev)
-    fresh = y is None
+    given = y, state_T
     if y is None:
         y = _like(x)
     else:
         _dense(y, "y", x.shape, x.dtype, dev)
     state_T = _new(state_T, "state_T", (B, W - 1, D), x.dtype, x)
-    if fresh:
-        _zero_outside((y,), cu, B, T, longest, dev)
+    _zero_fresh(given, (y, state_T), cu, B, T, longest, dev)
     _call(name, dev, x.data_ptr(), ld, pw, pb, ps, y.data_ptr(), state_T.data_ptr(), _ptr(cu), B, T, longest, D, W,
           PALIMPSA_CONV_SILU if silu else 0, kind)
     return y, state_T
@@ -279,9 +289,8 @@ def palimpsa_causal_conv_backward(x, weight, bias, state0, dy, dstate_T=None, *,
     pd = _dense(dstate_T, "dstate_T", (B, W - 1, D), dtype, dev)
     g = {"dx": _like(x), "dweight": _like(weight), "dbias": torch.empty(D, dtype=F32, device=x.device)}
     if want_state_grad:
-        # a sequence that is skipped for its offsets leaves its part as it is: zeros
-        g["dstate0"] = (torch.empty if cu is None else torch.zeros)((B, W - 1, D), dtype=dtype, device=x.device)
-    _zero_outside((g["dx"],), cu, B, T, longest, dev)
+        g["dstate0"] = torch.empty((B, W - 1, D), dtype=dtype, device=x.device)
+    _zero_unwritten((g["dx"],), (g["dstate0"],) if want_state_grad else (), cu, B, T, longest, dev)
     _call(name, dev, x.data_ptr(), ld, pw, pb, ps, dy.data_ptr(), ldy, pd, g["dx"].data_ptr(),
           g["dweight"].data_ptr(), g["dbias"].data_ptr(), _ptr(g.get("dstate0")), _ptr(cu), B, T, longest, D, W,
           PALIMPSA_CONV_SILU if silu else 0, kind)
@@ -330,14 +339,13 @@ def _scan(name, x, dt, A, B, C, D, z, dt_bias, h0, softplus, cu_seqlens, max_seq
     ch, groups, n, strides, ptrs = _scan_inputs(x, dt, A, B, C, D, z, dt_bias, dev, lead)
     kind = _dtype(x)
     p0 = _dense(h0, "h0", (nb, ch, n), F32, dev)
-    fresh = y is None
+    given = y, h_T
     if y is None:
         y = _like(x)
     else:
         _dense(y, "y", x.shape, x.dtype, dev)
-    if fresh:
-        _zero_outside((y,), cu, nb, T, longest, dev)
     h_T = _new(h_T, "h_T", (nb, ch, n), F32, x)
+    _zero_fresh(given, (y, h_T), cu, nb, T, longest, dev)
     if want_ckpt:
         ckpt = _new(ckpt, "ckpt", palimpsa_selective_scan_checkpoint_shape(nb, T, ch, n, cu is not None), F32, x)
     _call(name, dev, *ptrs, p0, y.data_ptr(), h_T.data_ptr(), _ptr(ckpt), strides, _ptr(cu), nb, T, longest, ch,
@@ -383,8 +391,6 @@ def palimpsa_selective_scan_backward(x, dt, A, B, C, D, z, dt_bias, h0, ckpt, dy
     _dense(h0, "h0", (nb, ch, n), F32, dev)
     pg = _dense(dh_T, "dh_T", (nb, ch, n), F32, dev)
     pc = _dense(ckpt, "ckpt", palimpsa_selective_scan_checkpoint_shape(nb, T, ch, n, packed), F32, dev)
-    at = x.device
-    e = lambda shape, t: torch.empty(shape, dtype=t, device=at)  # noqa: E731
     g = {"dx": _like(x), "ddt": _like(x), "dA": _like(A), "dB": _like(B), "dC": _like(B)}
     if D is not None:
         g["dD"] = _like(D)
@@ -393,9 +399,9 @@ def palimpsa_selective_scan_backward(x, dt, A, B, C, D, z, dt_bias, h0, ckpt, dy
     if dt_bias is not None:
         g["ddt_bias"] = _like(dt_bias)
     if want_state_grad:
-        # a sequence that is skipped for its offsets leaves its part as it is: zeros
-        g["dh0"] = torch.zeros((nb, ch, n), dtype=F32, device=at) if packed else e((nb, ch, n), F32)
-    _zero_outside([g[k] for k in ("dx", "ddt", "dz", "dB", "dC") if k in g], cu, nb, T, longest, dev)
+        g["dh0"] = torch.empty((nb, ch, n), dtype=F32, device=x.device)
+    _zero_unwritten([g[k] for k in ("dx", "ddt", "dz", "dB", "dC") if k in g], (g["dh0"],) if want_state_grad else (), cu,
+                    nb, T, longest, dev)
     at = {k: v.data_ptr() for k, v in g.items()}
     _call(name, dev, *ptrs, pc, dy.data_ptr(), pg, at["dx"], at["ddt"], at["dA"], at["dB"], at["dC"], at.get("dD"),
           at.get("dz"), at.get("ddt_bias"), at.get("dh0"), strides, _ptr(cu), nb, T, longest, ch, groups, n,
