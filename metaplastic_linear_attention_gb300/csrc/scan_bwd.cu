@@ -242,7 +242,7 @@ palimpsa_scan_bwd_kernel(ScanArgs a, Partials part, int tiles) {
     const int ci = nchunk - 1 - c, t0 = ci * kChunk, nt = min(kChunk, tn - t0);
     cp_async_wait<0>();
     cta_sync<W>();  // chunk c is here; the other stage, the operands and the sums are free
-    if (kStages == 2) stage(c + 1);
+    stage(c + 1);
     const unsigned char* const st = smem + (c % kStages) * L.raw;
     // Tokens past the end and channels past the tile count as s = s x = dpre = 0 (and B = C
     // = 0): they change nothing.
@@ -501,10 +501,6 @@ palimpsa_scan_bwd_kernel(ScanArgs a, Partials part, int tiles) {
       *reinterpret_cast<uint4*>(static_cast<char*>(a.dx) + to) = V::pack(dx);
       *reinterpret_cast<uint4*>(static_cast<char*>(a.ddt) + to) = V::pack(ddt);
       if (gated) *reinterpret_cast<uint4*>(static_cast<char*>(a.dz) + to) = V::pack(z);
-    }
-    if (kStages == 1) {
-      cta_sync<W>();
-      stage(c + 1);
     }
   }
   if (bad) latch_status(a.status, kStatusDomain);
