@@ -13,8 +13,9 @@
 // W - 1 rows before a run are read again. Long runs also spread the loads of the taps,
 // which are far apart in memory for neighbouring threads. Sums are fp32; y is rounded
 // once. Measured (GB300, bf16, W = 4, SiLU): 30 us at 8 x 4096 x 1536, the time of a
-// copy of as many bytes; backward 18 us at 4 x 2048 x 1024
-// (7 for its bytes; its window of W inputs and W gradients holds it to 16 warps an SM).
+// copy of as many bytes; backward 17 to 19 us at 4 x 2048 x 1024 and 67 at 8 x 4096 x 1536
+// (7 and 44 for their bytes; its window of W inputs and W gradients holds it to 16 warps an
+// SM), and 3 to 4 for the sums over CTAs.
 #include <algorithm>
 #include <cooperative_groups.h>
 
@@ -27,7 +28,7 @@ constexpr int kBatch = 8;      // tokens loaded together
 constexpr int kRing = 3;       // batches in the ring
 constexpr int kThreads = 128;
 constexpr int kMinRun = 16;   // tokens of a run, at least
-constexpr int kCtas = 5;      // of an SM
+constexpr int kCtas = 5;      // of an SM, in bf16; of fp32's rings (48 KB) 4 fit, and the waves are planned with 5 all the same
 
 // Parameters of a thread's 4 channels, as pairs: 4 W neighbouring floats, by 16-byte
 // loads where the array allows it (it only has to be aligned to 4 bytes).
@@ -213,7 +214,8 @@ __global__ void __launch_bounds__(kThreads) palimpsa_conv_step_kernel(ConvArgs a
 // like the forward's, with the last W inputs and du's in registers, and looks W - 1
 // tokens past its end for the dx of its last ones. The parameter sums go over
 // the CTA's runs in shared memory and then, in a fixed order, over CTAs in a second
-// kernel: no atomics, the same bits every time.
+// kernel: no atomics, the same bits every time. An SM holds two CTAs (one in fp32 with W = 4,
+// 184 registers; the waves are planned with two).
 constexpr int kBwdVecs = 16, kBwdRuns = 16, kBwdCtas = 2, kBwdRing = 3;
 
 template <bool BF16, int W>

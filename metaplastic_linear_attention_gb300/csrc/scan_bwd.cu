@@ -19,7 +19,9 @@
 // What bounds it: about 16 FP32 operations and 2 exponentials per state-token (2 clocks
 // per channel-token and SM at N = 16), and as much again for operands, reductions and the
 // token arrays: issue slots, 61 % busy. Measured (GB300, bf16, N = 16, gate, 4 x 2048 x
-// 1024): 159 us, 5.6 clocks. Before: two pairs a lane (255 registers, 7 warps an SM) 231,
+// 1024): 169 us, 6 clocks, in the two waves of segments that are planned (158 in one, whose
+// pass A takes 10 more). At N = 64 and 128, where an SM holds one CTA of 8 warps (230 to 255
+// registers, spills at 128), 743 and 1415 us. Before: two pairs a lane (255 registers, 7 warps an SM) 231,
 // reductions token by token 393; with 14 warps of 128 registers it spills (202).
 //
 // Sums. w, sum p A and sum C h go over the 4 lane groups by halves and over warps in
@@ -40,7 +42,7 @@ constexpr int kChunk = kScanCheckpoint;
 constexpr int kWin = 4;
 constexpr int kWins = kChunk / kWin;
 constexpr int kStages = 2;
-constexpr int kWarpsPerSM = 12;
+constexpr int kWarpsPerSM = 12;  // up to N = 32
 constexpr int CH = kScanChannels;
 
 // Channel pairs of a lane: 1 (two warps share a tile's channels), or 2 at N = 128, where
