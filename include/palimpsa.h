@@ -560,9 +560,10 @@ palimpsa_status palimpsa_backward_varlen(
  * State-space operators. The pages build their blocks on state-space backbones
  * (slide 10: Palimpsa-M on a Mamba2-style block; slides 18-19: 8 of 64 such
  * layers replaced by Palimpsa): a short causal convolution in front of the mixer,
- * and, in the layers that stay, a selective scan. The two operators below serve
- * those layers: a prompt, a packed batch, one token, and training. Unlike the
- * recurrence above they are laid out token by token:
+ * and, in the layers that stay, a selective scan. The operators below serve
+ * those layers: a prompt, a packed batch, one token, and training; the gated scan
+ * is the form with one state per channel, and the layer norm stands between layers.
+ * Unlike the recurrence above they are laid out token by token:
  *
  *   rows      one row of D channels per token; D a multiple of 8, at most 2^24. Dense: B
  *             sequences of T rows each. Packed (cu_seqlens not NULL): B sequences
@@ -577,12 +578,12 @@ palimpsa_status palimpsa_backward_varlen(
  *             wider projection): the stride is in elements, 0 means dense, at
  *             least the width otherwise, and a multiple of 16 bytes
  *             (PALIMPSA_ERR_ALIGN). Outputs are dense.
- *   types     token arrays (x, dt, B, C, z, y, their gradients, the convolution's
- *             state) are in in_dtype; parameters, their gradients and the scan's
- *             state are fp32. Sums and states are fp32; outputs in in_dtype are
+ *   types     token arrays (x, dt, B, C, z, r, i, y, their gradients, the convolution's
+ *             state) are in in_dtype; parameters, their gradients and the scans'
+ *             states are fp32. Sums and states are fp32; outputs in in_dtype are
  *             rounded once.
- *   alignment 16 bytes, except weight, bias, skip, dt_bias, their gradients, dA and
- *             cu_seqlens (4 bytes).
+ *   alignment 16 bytes, except weight, bias, skip, dt_bias, r_bias, i_bias, the gated
+ *             scan's A, their gradients, dA and cu_seqlens (4 bytes), and stats (8).
  * T = 0, and empty sequences, pass the state (and its gradient) through; with
  * T = 0 the token arrays may be NULL. Overlap between inputs and outputs is
  * undefined, except that a final state may be the initial one. Results do not
@@ -723,6 +724,98 @@ palimpsa_status palimpsa_selective_scan_backward(
     float* ddt_bias, float* dh0, const palimpsa_scan_strides* strides,
     const int* cu_seqlens, int B, int T, int max_seqlen, int D, int G, int N,
     unsigned int flags, palimpsa_dtype in_dtype, void* cuda_stream);
+
+/* Row strides of the gated scan's inputs, in elements (0: dense). */
+typedef struct {
+  long long x, r, i, z, dy;
+} palimpsa_gate_strides;
+
+/*
+ * palimpsa_gated_scan - a linear recurrence with one state per channel, whose decay and
+ * input are gated by the token:
+ *
+ *   a_t = exp(-A sigmoid(r_t + r_bias))
+ *   h_t = a_t h_{t-1} + sqrt(1 - a_t^2) sigmoid(i_t + i_bias) x_t
+ *   y_t = h_t silu(z_t)
+ *
+ * A > 0, as above: the largest rate of forgetting. The factor of the input keeps the
+ * state's variance at the input's, whatever the decay.
+ *   x, r     rows [D]; i rows [D] or NULL (no input gate: a factor of 1); z rows [D] or
+ *            NULL (no output gate)
+ *   A        [D] > 0; r_bias, i_bias [D] or NULL (0); i_bias only with i
+ *   h0       [B, D] or NULL (0); h_T [B, D], may be h0
+ *   y        rows [D]
+ *   ckpt     NULL, or palimpsa_gated_scan_checkpoint_bytes() bytes that receive the
+ *            state of every sequence before its tokens 0, 8, 16, ..., [D] each, for the
+ *            backward (packed: sequence n, from row s0, in slots s0 / 8 + n, ...; slots
+ *            that no sequence owns are not written)
+ *   strides  or NULL when every input is dense
+ * No scratch. A not positive latches PALIMPSA_ERR_DOMAIN.
+ */
+size_t palimpsa_gated_scan_checkpoint_bytes(int B, int T, int packed, int D);
+
+palimpsa_status palimpsa_gated_scan(
+    const void* x, const void* r, const float* A, const void* i, const void* z,
+    const float* r_bias, const float* i_bias, const float* h0,
+    void* y, float* h_T, float* ckpt, const palimpsa_gate_strides* strides,
+    const int* cu_seqlens, int B, int T, int max_seqlen, int D,
+    palimpsa_dtype in_dtype, void* cuda_stream);
+
+/* palimpsa_gated_scan_step - one token of B sequences; h [B, D] is updated in place. */
+palimpsa_status palimpsa_gated_scan_step(
+    const void* x, const void* r, const float* A, const void* i, const void* z,
+    const float* r_bias, const float* i_bias, float* h, void* y,
+    const palimpsa_gate_strides* strides, int B, int D,
+    palimpsa_dtype in_dtype, void* cuda_stream);
+
+/*
+ * palimpsa_gated_scan_backward - gradients through palimpsa_gated_scan from dy (rows [D])
+ * and dh_T ([B, D] or NULL), with the ckpt of a forward call on the same inputs (h0 is in
+ * it).
+ *   dx, dr rows [D]; di, dz rows [D], required with i and z (dr and di are the gradients of
+ *   the raw gates); dA [D]; dr_bias, di_bias [D] or NULL; dh0 [B, D] or NULL.
+ * Scratch from the library's pool: 12 bytes per channel and CTA.
+ */
+palimpsa_status palimpsa_gated_scan_backward(
+    const void* x, const void* r, const float* A, const void* i, const void* z,
+    const float* r_bias, const float* i_bias, const float* ckpt,
+    const void* dy, const float* dh_T,
+    void* dx, void* dr, float* dA, void* di, void* dz,
+    float* dr_bias, float* di_bias, float* dh0, const palimpsa_gate_strides* strides,
+    const int* cu_seqlens, int B, int T, int max_seqlen, int D,
+    palimpsa_dtype in_dtype, void* cuda_stream);
+
+/*
+ * palimpsa_layer_norm - the layer norm of rows of D values, after an addition:
+ *
+ *   s = x + residual,   y = (s - mean(s)) / sqrt(mean((s - mean(s))^2) + eps) weight + bias
+ *
+ * s is rounded to in_dtype before it is normalised: what is normalised is what is kept.
+ *   x, residual  rows [D], strides as above; residual NULL: s is x
+ *   weight, bias [D] fp32, or NULL (1 and 0)
+ *   y            rows [D]; sum: rows [D], required with residual, receives s, and may be x
+ *                or residual where that is dense
+ *   stats        NULL, or [rows, 2] fp32 (8-byte aligned): mean and 1 / sqrt(variance + eps)
+ *                of every row, for the backward
+ *   rows >= 0 (with 0 the row arrays may be NULL); D a multiple of 8, at most 8192; eps > 0.
+ */
+palimpsa_status palimpsa_layer_norm(
+    const void* x, long long x_stride, const void* residual, long long residual_stride,
+    const float* weight, const float* bias, void* y, void* sum, float* stats,
+    long long rows, int D, float eps, palimpsa_dtype in_dtype, void* cuda_stream);
+
+/*
+ * palimpsa_layer_norm_backward - gradients through palimpsa_layer_norm from dy and, where s
+ * is used past the norm, ds (rows [D] or NULL), with s and the stats of the forward call:
+ *   dx             rows [D], the gradient of s, and so of x and of residual (ds included)
+ *   dweight, dbias [D] fp32, or NULL
+ * Scratch for the parameters' partial sums comes from the library's pool.
+ */
+palimpsa_status palimpsa_layer_norm_backward(
+    const void* s, long long s_stride, const float* weight, const float* stats,
+    const void* dy, long long dy_stride, const void* ds, long long ds_stride,
+    void* dx, float* dweight, float* dbias, long long rows, int D,
+    palimpsa_dtype in_dtype, void* cuda_stream);
 
 /* Static English text for a status code (never NULL). */
 const char* palimpsa_status_string(palimpsa_status s);

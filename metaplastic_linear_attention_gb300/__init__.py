@@ -59,3 +59,11 @@ from .ssm import (  # noqa: F401
     palimpsa_selective_scan_checkpointed,
     palimpsa_selective_scan_step,
 )
+from .gated import (  # noqa: F401
+    palimpsa_gated_scan,
+    palimpsa_gated_scan_backward,
+    palimpsa_gated_scan_checkpoint_shape,
+    palimpsa_gated_scan_checkpointed,
+    palimpsa_gated_scan_step,
+)
+from .norm import palimpsa_layer_norm, palimpsa_layer_norm_backward  # noqa: F401

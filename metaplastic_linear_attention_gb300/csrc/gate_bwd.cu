@@ -1,0 +1,305 @@
+// Gated scan, backward. With g_t the gradient with respect to h_t and u_t = p_t x_t, p the
+// input gate, n_t = sqrt(1 - a_t^2) (formulas of the forward in gate_fwd.cu):
+//   g_t = dy_t silu(z_t) + a_{t+1} g_{t+1}        (dh_T comes in behind the last token)
+//   dx = g n p,  di = g n x p (1 - p),  dz = dy h silu'(z),  dh0 = a_0 g_0
+//   dw = g (u a^2 / n - a h_{t-1}),  dr = dw A s (1 - s),  dA = sum_t dw s
+// and the biases' gradients are the sums of dr and di over the tokens.
+//
+// As in the forward, one pass over the data: HBM bounds it, 18 bytes a channel-token in
+// bf16 with both gates (0.84 clocks of an SM's share) and half a byte of checkpoints. The
+// forward leaves the state before every 8th token, so a thread recomputes the states of its
+// piece by itself, with the factors of g_t in dx, di, dr and dA; a first run over the
+// piece from the back, from a gradient of 0, gives its summary, and with the gradient behind
+// the piece known, a second run gives the results. The rounds go from the back to the front.
+// The parameters' sums stay in registers over all rounds; they are added up over
+// the CTA's pieces in shared memory and over CTAs by a second kernel, in a fixed order: no
+// atomics, the same bits every time.
+#include <algorithm>
+
+#include "gate.cuh"
+
+namespace palimpsa {
+namespace {
+
+namespace cg = cooperative_groups;
+
+constexpr int kResident = 2;  // CTAs of an SM
+
+// Shared memory: the ring of raw inputs (and the states before the pieces), then summaries.
+template <bool BF16>
+__host__ __device__ constexpr int stage_bytes(int arrays) {
+  return arrays * GateTile<BF16>::bytes + GateTile<BF16>::warps * kGateChannels * 4;
+}
+template <bool BF16>
+constexpr int bwd_smem(int arrays, bool cluster) {
+  return 2 * stage_bytes<BF16>(arrays) + GateTile<BF16>::warps * 32 * 16 + (cluster ? 2 * kGateCluster * 32 * 16 : 0);
+}
+
+// sums: [n_seq, cluster, 3, D], the CTAs' parts of dA, dr_bias and di_bias.
+template <bool BF16, bool IN, bool GATE, bool CLUSTER>
+__global__ void __launch_bounds__(GateTile<BF16>::threads, BF16 ? kResident : 2 * kResident)
+palimpsa_gate_bwd_kernel(GateArgs a, int tiles, float* sums) {
+  using G = GateTile<BF16>;
+  constexpr int ES = G::ES, NA = 3 + IN + GATE, RT = G::tokens, kStage = stage_bytes<BF16>(NA);
+  constexpr int kI = 3, kZ = 3 + IN;  // places of the arrays x, r, dy, i, z
+  extern __shared__ __align__(128) unsigned char smem[];
+  float4* const agg = reinterpret_cast<float4*>(smem + 2 * kStage);
+  float4* const xagg = agg + G::warps * 32;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int cs = CLUSTER ? a.cluster : 1;
+  const int rank = CLUSTER ? (int)(blockIdx.x % cs) : 0;
+  const long long rest = CLUSTER ? blockIdx.x / cs : blockIdx.x;
+  const int ch0 = (int)(rest % tiles) * kGateChannels, ch = ch0 + 2 * lane;
+  const bool in = ch < a.D;
+  const long long n = rest / tiles;
+  const float2 zero = make_float2(0.f, 0.f);
+  float* const part = sums + (n * cs + rank) * 3 * a.D + ch;
+  long long row0;
+  int len;
+  if (!seq_rows(a.rows, n, &row0, &len)) {
+    if (tid == 0) latch_status(a.status, kStatusDomain);
+    if (warp < 3 && in) *reinterpret_cast<float2*>(part + (long long)warp * a.D) = zero;
+    return;  // (the whole cluster)
+  }
+  const int step = cs * RT, rounds = (len + step - 1) / step;
+  const float* const ckpt = a.ckpt_in + gate_ckpt_row0(a.rows, n, row0) * a.D + ch0;
+
+  const int vec = tid % G::vecs, vrow = tid / G::vecs;
+  const bool vin = ch0 * ES + vec * 16 < a.D * ES;
+  auto stage = [&](int k) {  // copies of round k's tile, as one group
+    const int t0 = k * step + rank * RT, nt = min(RT, len - t0);
+    if (k >= 0) {
+      unsigned char* const to = smem + (k & 1) * kStage;
+      const long long first = row0 + t0 + vrow, col = (long long)ch0 * ES + vec * 16;
+      auto copy = [&](const void* from, long long ld, int slot) {
+        const char* p = static_cast<const char*>(from) + first * ld * ES + col;
+#pragma unroll
+        for (int j = 0; j < RT / G::rows_at_once; ++j)
+          if (j * G::rows_at_once + vrow < nt)
+            cp_async16(to + slot * G::bytes + tid * 16 + j * G::threads * 16, p + j * G::rows_at_once * ld * ES);
+      };
+      if (vin) {
+        copy(a.x, a.x_ld, 0);
+        copy(a.r, a.r_ld, 1);
+        copy(a.dy, a.dy_ld, 2);
+        if (IN) copy(a.i, a.i_ld, kI);
+        if (GATE) copy(a.z, a.z_ld, kZ);
+      }
+      // The states before the pieces: 16 vectors of 4 channels each.
+      if (tid < G::warps * 16 && (tid >> 4) * kPiece < nt && ch0 + (tid & 15) * 4 < a.D)
+        cp_async16(to + NA * G::bytes + tid * 16, ckpt + (long long)(t0 / kPiece + (tid >> 4)) * a.D + (tid & 15) * 4);
+    }
+    cp_async_commit();
+  };
+  stage(rounds - 1);
+
+  const float2 A = pair_or(a.A, ch, in, 1.f);
+  const float2 rb = pair_or(a.r_bias, ch, in, 0.f), ib = pair_or(a.i_bias, ch, in, 0.f);
+  if (!pos_finite(A.x) || !pos_finite(A.y)) latch_status(a.status, kStatusDomain);
+  float2 carry = zero;  // a g of the token behind the round
+  if (a.dh_T && in) carry = *reinterpret_cast<const float2*>(a.dh_T + n * a.D + ch);
+  float2 sA = zero, sr = zero, si = zero;
+  if (CLUSTER) cg::this_cluster().sync();  // every CTA has started: its shared memory may be written
+
+  for (int k = rounds - 1; k >= 0; --k) {
+    const int tp = k * step + rank * RT + warp * kPiece;
+    const int np = min(kPiece, len - tp);
+    unsigned char* const raw = smem + (k & 1) * kStage + warp * kPiece * G::row + lane * 2 * ES;
+    cp_async_wait<0>();
+    __syncthreads();  // the round's inputs are here; the other stage and the summaries are free
+    stage(k - 1);
+
+    // The factors of g_t in dx, di, dr and dA, the decays, and dy silu(z).
+    float2 da[kPiece], fx[kPiece], fi[IN ? kPiece : 1], fr[kPiece], fA[kPiece], gy[kPiece];
+    const long long at = (row0 + tp) * a.D + ch;
+    float2 h = np > 0 ? *reinterpret_cast<const float2*>(smem + (k & 1) * kStage + NA * G::bytes +
+                                                         (warp * kGateChannels + 2 * lane) * 4)
+                      : zero;
+#pragma unroll
+    for (int t = 0; t < kPiece; ++t) {
+      if (t < np) {
+        const float2 x = load_pair<BF16>(raw + t * G::row);
+        const Sigmoid s(__fadd2_rn(load_pair<BF16>(raw + G::bytes + t * G::row), rb));
+        gy[t] = load_pair<BF16>(raw + 2 * G::bytes + t * G::row);
+        const float2 w = __fmul2_rn(A, s.p);
+        float2 q;  // 1 - a^2
+        decay_of(w, &da[t], &q);
+        // (A rate of 0 has q = 0, and no gradient: the factor w of dr, or s of dA, is 0 too.)
+        const float2 ni = make_float2(rsqrt_approx(fmaxf(q.x, 1e-36f)), rsqrt_approx(fmaxf(q.y, 1e-36f)));
+        fx[t] = __fmul2_rn(q, ni);
+        float2 u = x;
+        if (IN) {
+          const Sigmoid p(__fadd2_rn(load_pair<BF16>(raw + kI * G::bytes + t * G::row), ib));
+          fx[t] = __fmul2_rn(fx[t], p.p);
+          fi[t] = __fmul2_rn(__fmul2_rn(fx[t], x), p.rest());
+          u = __fmul2_rn(x, p.p);
+        }
+        const float2 old = __fmul2_rn(da[t], h);
+        // dw / g = u a^2 / n - a h
+        const float2 aa = __fmul2_rn(__fmul2_rn(da[t], da[t]), ni);
+        const float2 dw = ffma2(u, aa, make_float2(-old.x, -old.y));
+        fA[t] = __fmul2_rn(dw, s.p);
+        fr[t] = __fmul2_rn(__fmul2_rn(dw, w), s.rest());
+        h = ffma2(fx[t], x, old);
+        if (GATE) {
+          const float2 z = load_pair<BF16>(raw + kZ * G::bytes + t * G::row);
+          const Sigmoid c(z);
+          const float2 m = ffma2(z, c.rest(), make_float2(1.f, 1.f));  // silu' = c (1 + z (1 - c))
+          const float2 dz = __fmul2_rn(__fmul2_rn(gy[t], h), __fmul2_rn(c.p, m));
+          if (in) store_pair<BF16>(static_cast<char*>(a.dz) + (at + (long long)t * a.D) * ES, dz);
+          gy[t] = __fmul2_rn(gy[t], __fmul2_rn(z, c.p));
+        }
+      } else {
+        da[t] = make_float2(1.f, 1.f);
+        fx[t] = fr[t] = fA[t] = gy[t] = zero;
+        if (IN) fi[t] = zero;
+      }
+    }
+    float2 P = make_float2(1.f, 1.f), C = zero;
+#pragma unroll
+    for (int t = kPiece - 1; t >= 0; --t) {
+      C = __fmul2_rn(da[t], __fadd2_rn(gy[t], C));
+      P = __fmul2_rn(P, da[t]);
+    }
+    agg[warp * 32 + lane] = make_float4(P.x, P.y, C.x, C.y);
+    __syncthreads();
+
+    // The gradient that comes in from behind the piece, and the one before the round.
+    float2 c = carry;
+    if (!CLUSTER) {
+#pragma unroll
+      for (int q = G::warps - 1; q >= 0; --q) {
+        const float4 e = agg[q * 32 + lane];
+        if (q == warp) c = carry;
+        carry = ffma2(make_float2(e.x, e.y), carry, make_float2(e.z, e.w));
+      }
+    } else {
+      float4* const slots = xagg + (k & 1) * kGateCluster * 32;
+      cg::cluster_group cluster = cg::this_cluster();
+      for (int q = warp; q < cs; q += G::warps) {
+        float2 Pc = make_float2(1.f, 1.f), Cc = zero;
+#pragma unroll
+        for (int w = G::warps - 1; w >= 0; --w) {
+          const float4 e = agg[w * 32 + lane];
+          Cc = ffma2(make_float2(e.x, e.y), Cc, make_float2(e.z, e.w));
+          Pc = __fmul2_rn(Pc, make_float2(e.x, e.y));
+        }
+        *cluster.map_shared_rank(slots + rank * 32 + lane, q) = make_float4(Pc.x, Pc.y, Cc.x, Cc.y);
+      }
+      cluster.sync();
+      for (int q = cs - 1; q >= 0; --q) {
+        const float4 e = slots[q * 32 + lane];
+        if (q == rank) c = carry;
+        carry = ffma2(make_float2(e.x, e.y), carry, make_float2(e.z, e.w));
+      }
+      for (int w = G::warps - 1; w > warp; --w) {
+        const float4 e = agg[w * 32 + lane];
+        c = ffma2(make_float2(e.x, e.y), c, make_float2(e.z, e.w));
+      }
+    }
+    if (in && np > 0) {
+      float2 pA = zero, pr = zero, pi = zero;  // the piece's sums
+#pragma unroll
+      for (int t = kPiece - 1; t >= 0; --t)
+        if (t < np) {
+          const float2 g = __fadd2_rn(gy[t], c);
+          c = __fmul2_rn(da[t], g);
+          const long long o = (at + (long long)t * a.D) * ES;
+          store_pair<BF16>(static_cast<char*>(a.dx) + o, __fmul2_rn(g, fx[t]));
+          const float2 dr = __fmul2_rn(g, fr[t]);
+          store_pair<BF16>(static_cast<char*>(a.dr) + o, dr);
+          pr = __fadd2_rn(pr, dr);
+          pA = ffma2(g, fA[t], pA);
+          if (IN) {
+            const float2 di = __fmul2_rn(g, fi[t]);
+            store_pair<BF16>(static_cast<char*>(a.di) + o, di);
+            pi = __fadd2_rn(pi, di);
+          }
+        }
+      sA = __fadd2_rn(sA, pA);
+      sr = __fadd2_rn(sr, pr);
+      si = __fadd2_rn(si, pi);
+    }
+    __syncwarp();
+  }
+  if (rank == 0 && warp == 0 && in && a.dh0) *reinterpret_cast<float2*>(a.dh0 + n * a.D + ch) = carry;
+  // The CTA's sums over its pieces.
+  float2* const red = reinterpret_cast<float2*>(agg);
+  const float2 own[3] = {sA, sr, si};
+#pragma unroll
+  for (int v = 0; v < 3; ++v) {
+    __syncthreads();
+    red[warp * 32 + lane] = own[v];
+    __syncthreads();
+    if (warp == v && in) {
+      float2 t = red[lane];
+#pragma unroll
+      for (int w = 1; w < G::warps; ++w) t = __fadd2_rn(t, red[w * 32 + lane]);
+      *reinterpret_cast<float2*>(part + (long long)v * a.D) = t;
+    }
+  }
+}
+
+// Sums the CTAs' parts [rows, 3, D]; block y = v, 32 channels by 8 slices of the rows.
+__global__ void __launch_bounds__(256) palimpsa_gate_bwd_sum_kernel(const float* sums, long long rows, int D, float* dA,
+                                                                    float* dr_bias, float* di_bias) {
+  __shared__ float red[8][33];
+  const int cx = threadIdx.x % 32, sy = threadIdx.x / 32, ch = blockIdx.x * 32 + cx, v = blockIdx.y;
+  float* const out = v == 0 ? dA : v == 1 ? dr_bias : di_bias;
+  if (!out) return;
+  float s = 0.f;
+  if (ch < D)
+    for (long long b = sy; b < rows; b += 8) s += sums[(b * 3 + v) * D + ch];
+  red[sy][cx] = s;
+  __syncthreads();
+  if (sy == 0 && ch < D) {
+    for (int k = 1; k < 8; ++k) s += red[k][cx];
+    out[ch] = s;
+  }
+}
+
+template <bool BF16, bool IN, bool GATE, bool CLUSTER>
+cudaError_t run(const GateArgs& a, float* sums, cudaStream_t s) {
+  using G = GateTile<BF16>;
+  const long long tiles = gate_tiles(a.D), blocks = tiles * a.rows.n_seq * a.cluster;
+  if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
+  constexpr int bytes = bwd_smem<BF16>(3 + IN + GATE, CLUSTER);
+  const auto kernel = palimpsa_gate_bwd_kernel<BF16, IN, GATE, CLUSTER>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute cluster = {};
+  cluster.id = cudaLaunchAttributeClusterDimension;
+  cluster.val.clusterDim.x = a.cluster;
+  cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
+  cudaLaunchConfig_t c = {};
+  c.gridDim = dim3((unsigned)blocks);
+  c.blockDim = dim3(G::threads);
+  c.dynamicSmemBytes = bytes;
+  c.stream = s;
+  c.attrs = &cluster;
+  c.numAttrs = CLUSTER ? 1 : 0;
+  e = cudaLaunchKernelEx(&c, kernel, a, (int)tiles, sums);
+  if (e != cudaSuccess) return e;
+  palimpsa_gate_bwd_sum_kernel<<<dim3((a.D + 31) / 32, 3), 256, 0, s>>>(sums, (long long)a.rows.n_seq * a.cluster, a.D,
+                                                                        a.dA, a.dr_bias, a.di_bias);
+  return cudaGetLastError();
+}
+
+template <bool BF16, bool IN, bool GATE>
+cudaError_t backward(const GateArgs& a, float* sums, cudaStream_t s) {
+  return a.cluster > 1 ? run<BF16, IN, GATE, true>(a, sums, s) : run<BF16, IN, GATE, false>(a, sums, s);
+}
+
+}  // namespace
+
+size_t plan_gate_backward(GateArgs* a) {
+  a->cluster = a->bf16 ? gate_cluster(a->rows, a->D, GateTile<true>::tokens, kResident)
+                       : gate_cluster(a->rows, a->D, GateTile<false>::tokens, 2 * kResident);
+  return (size_t)a->rows.n_seq * a->cluster * 3 * a->D;
+}
+
+cudaError_t launch_gate_backward(const GateArgs& a, float* scratch, cudaStream_t s) {
+  PALIMPSA_GATE_DISPATCH(backward, a, scratch, s)
+}
+
+}  // namespace palimpsa

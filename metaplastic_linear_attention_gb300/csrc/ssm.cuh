@@ -1,6 +1,7 @@
 // Internal declarations of the state-space operators: the short causal
-// convolution (conv.cu) and the selective scan (scan_fwd.cu, scan_bwd.cu,
-// scan_step.cu). Their C ABI is ssm_api.cu.
+// convolution (conv.cu), the selective scan (scan_fwd.cu, scan_bwd.cu,
+// scan_step.cu) and the gated scan (gate_fwd.cu, gate_bwd.cu), and of the
+// layer norm between such layers (norm.cu). Their C ABI is ssm_api.cu.
 //
 // Layouts are token-major: a row of D channels per token, rows of one sequence
 // following each other with a stride (`ld`, elements) that may exceed D, so
@@ -173,6 +174,85 @@ cudaError_t launch_scan_reverse_summary(const ScanArgs& a, cudaStream_t s);
 constexpr int kFoldSegments = 18;
 // Turns the summaries into start states, in place: forward from h0, or in reverse from dh_T.
 cudaError_t launch_scan_carry(const ScanArgs& a, bool reverse, cudaStream_t s);
+
+// The gated scan: one state per channel, gates from the token (formulas in gate_fwd.cu).
+struct GateArgs {
+  const void* x;
+  const void* r;
+  const void* i;        // or null: the input gate is 1
+  const void* z;        // or null
+  const float* A;       // [D]
+  const float* r_bias;  // [D] or null
+  const float* i_bias;  // [D] or null
+  const float* h0;      // [n_seq, D] or null
+  void* y;
+  float* h_T;           // [n_seq, D]; the step's state, in place
+  float* ckpt = nullptr;
+  long long x_ld, r_ld, i_ld, z_ld;
+  SeqRows rows;
+  int D;
+  bool bf16;
+  unsigned int* status;
+  int cluster = 1;      // CTAs that share a sequence's time, set by plan_gate
+  // backward
+  const float* ckpt_in = nullptr;
+  const void* dy = nullptr;
+  const float* dh_T = nullptr;
+  void* dx = nullptr;
+  void* dr = nullptr;
+  void* di = nullptr;
+  void* dz = nullptr;
+  float* dA = nullptr;
+  float* dr_bias = nullptr;
+  float* di_bias = nullptr;
+  float* dh0 = nullptr;
+  long long dy_ld = 0;
+};
+
+constexpr int kGateCheckpoint = 8;  // tokens between the gated scan's checkpoints
+
+// Checkpoint rows, each [D]: as scan_ckpt_rows, with 8 tokens between two.
+__host__ __device__ inline long long gate_ckpt_rows(const SeqRows& r) {
+  if (r.cu) return (long long)r.T / kGateCheckpoint + r.n_seq;
+  return (long long)r.n_seq * ((r.T + kGateCheckpoint - 1) / kGateCheckpoint);
+}
+__host__ __device__ inline long long gate_ckpt_row0(const SeqRows& r, long long n, long long s0) {
+  if (r.cu) return s0 / kGateCheckpoint + n;
+  return n * ((r.T + kGateCheckpoint - 1) / kGateCheckpoint);
+}
+cudaError_t launch_gate_forward(const GateArgs& a, cudaStream_t s);
+cudaError_t launch_gate_step(const GateArgs& a, cudaStream_t s);
+// Backward: sets a->cluster; scratch of as many floats holds the parameters' sums of every CTA.
+size_t plan_gate_backward(GateArgs* a);
+cudaError_t launch_gate_backward(const GateArgs& a, float* scratch, cudaStream_t s);
+
+// The layer norm of rows of D values, and the addition in front of it (norm.cu).
+constexpr int kNormWidth = 8192;  // the widest row
+struct NormArgs {
+  const void* x;            // forward: the rows; backward: the rows that were normalised
+  const void* residual;     // forward: or null
+  const float* weight;      // [D] or null (1)
+  const float* bias;        // [D] or null (0)
+  void* y;
+  void* sum = nullptr;      // x + residual, with residual
+  float* stats;             // [rows, 2]: mean and 1 / deviation; forward: or null
+  long long x_ld, residual_ld = 0;
+  long long rows;
+  int D;
+  float eps;
+  bool bf16;
+  // backward
+  const void* dy = nullptr;
+  const void* ds = nullptr;  // or null
+  void* dx = nullptr;
+  float* dweight = nullptr;
+  float* dbias = nullptr;
+  long long dy_ld = 0, ds_ld = 0;
+};
+cudaError_t launch_norm_forward(const NormArgs& a, cudaStream_t s);
+// Backward: scratch of norm_backward_scratch_floats() holds every CTA's sums of the parameters' gradients.
+size_t norm_backward_scratch_floats(const NormArgs& a);
+cudaError_t launch_norm_backward(const NormArgs& a, float* scratch, cudaStream_t s);
 
 #if defined(__CUDACC__)
 

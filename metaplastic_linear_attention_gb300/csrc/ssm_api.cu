@@ -1,5 +1,5 @@
-// C ABI of the causal convolution and the selective scan: argument validation and
-// dispatch to their launchers. Declared in palimpsa.h.
+// C ABI of the causal convolution, the selective scan, the gated scan and the layer
+// norm: argument validation and dispatch to their launchers. Declared in palimpsa.h.
 #include "palimpsa.h"
 #include "ssm.cuh"
 
@@ -83,6 +83,47 @@ palimpsa_status scan_strides(ScanArgs* a, const palimpsa_scan_strides* st, palim
   if (!s) s = stride_of(st->z, a->D, t, &a->z_ld);
   if (!s) s = stride_of(st->dy, a->D, t, &a->dy_ld);
   return s;
+}
+
+palimpsa_status gate_checks(const GateArgs& a, palimpsa_dtype t) {
+  if (!dtype_ok(t)) return PALIMPSA_ERR_DTYPE;
+  if (!rows_ok(a.rows, a.D)) return PALIMPSA_ERR_SHAPE;
+  if (a.D % 8) return PALIMPSA_ERR_UNSUPPORTED;
+  return aligned_all({a.x, a.r, a.i, a.z, a.h0, a.y, a.h_T, a.ckpt, a.ckpt_in, a.dy, a.dh_T, a.dx, a.dr, a.di, a.dz, a.dh0},
+                     {a.A, a.r_bias, a.i_bias, a.rows.cu, a.dA, a.dr_bias, a.di_bias});
+}
+
+palimpsa_status gate_strides(GateArgs* a, const palimpsa_gate_strides* st, palimpsa_dtype t) {
+  const palimpsa_gate_strides dense = {};
+  if (!st) st = &dense;
+  palimpsa_status s = stride_of(st->x, a->D, t, &a->x_ld);
+  if (!s) s = stride_of(st->r, a->D, t, &a->r_ld);
+  if (!s) s = stride_of(st->i, a->D, t, &a->i_ld);
+  if (!s) s = stride_of(st->z, a->D, t, &a->z_ld);
+  if (!s) s = stride_of(st->dy, a->D, t, &a->dy_ld);
+  return s;
+}
+
+GateArgs gate_args(const void* x, const void* r, const float* A, const void* i, const void* z, const float* r_bias,
+                   const float* i_bias, int D, palimpsa_dtype t) {
+  GateArgs a{};
+  a.x = x;
+  a.r = r;
+  a.A = A;
+  a.i = i;
+  a.z = z;
+  a.r_bias = r_bias;
+  a.i_bias = i_bias;
+  a.D = D;
+  a.bf16 = t == PALIMPSA_BF16;
+  return a;
+}
+
+palimpsa_status norm_checks(const NormArgs& a, palimpsa_dtype t) {
+  if (!dtype_ok(t)) return PALIMPSA_ERR_DTYPE;
+  if (a.rows < 0 || a.D < 1 || a.rows > (1LL << 40) / a.D) return PALIMPSA_ERR_SHAPE;
+  if (a.D % 8 || a.D > kNormWidth) return PALIMPSA_ERR_UNSUPPORTED;
+  return aligned_all({a.x, a.residual, a.y, a.sum, a.dy, a.ds, a.dx}, {a.weight, a.bias, a.dweight, a.dbias});
 }
 
 ScanArgs scan_args(const void* x, const void* dt, const float* A, const void* B, const void* C, const float* skip,
@@ -343,6 +384,129 @@ palimpsa_status palimpsa_selective_scan_backward(
   cudaError_t e = take_scratch(&a, more, true, close, s, &scratch);
   if (e == cudaSuccess) e = launch_scan_backward(a, scratch, s);
   return release(e, scratch, s);
+}
+
+size_t palimpsa_gated_scan_checkpoint_bytes(int B, int T, int packed, int D) {
+  if (B < 1 || T < 0 || D < 1) return 0;
+  static const int some = 0;
+  return (size_t)gate_ckpt_rows(rows_of(packed ? &some : nullptr, B, T, T)) * D * sizeof(float);
+}
+
+palimpsa_status palimpsa_gated_scan(const void* x, const void* r, const float* A, const void* i, const void* z,
+                                    const float* r_bias, const float* i_bias, const float* h0, void* y, float* h_T,
+                                    float* ckpt, const palimpsa_gate_strides* strides, const int* cu_seqlens, int B, int T,
+                                    int max_seqlen, int D, palimpsa_dtype in_dtype, void* cuda_stream) {
+  if (!A || !h_T || (T != 0 && (!x || !r || !y || (i_bias && !i)))) return PALIMPSA_ERR_NULL;
+  GateArgs a = gate_args(x, r, A, i, z, r_bias, i_bias, D, in_dtype);
+  a.h0 = h0;
+  a.y = y;
+  a.h_T = h_T;
+  a.ckpt = ckpt;
+  a.rows = rows_of(cu_seqlens, B, T, max_seqlen);
+  if (palimpsa_status s = gate_checks(a, in_dtype)) return s;
+  if (palimpsa_status s = gate_strides(&a, strides, in_dtype)) return s;
+  if (palimpsa_status s = device_status_word(&a.status)) return s;
+  return launch_gate_forward(a, static_cast<cudaStream_t>(cuda_stream)) == cudaSuccess ? PALIMPSA_OK
+                                                                                     : PALIMPSA_ERR_CUDA;
+}
+
+palimpsa_status palimpsa_gated_scan_step(const void* x, const void* r, const float* A, const void* i, const void* z,
+                                         const float* r_bias, const float* i_bias, float* h, void* y,
+                                         const palimpsa_gate_strides* strides, int B, int D, palimpsa_dtype in_dtype,
+                                         void* cuda_stream) {
+  if (!x || !r || !A || !h || !y || (i_bias && !i)) return PALIMPSA_ERR_NULL;
+  GateArgs a = gate_args(x, r, A, i, z, r_bias, i_bias, D, in_dtype);
+  a.y = y;
+  a.h_T = h;
+  a.rows = rows_of(nullptr, B, 1, 1);
+  if (palimpsa_status s = gate_checks(a, in_dtype)) return s;
+  if (palimpsa_status s = gate_strides(&a, strides, in_dtype)) return s;
+  if (palimpsa_status s = device_status_word(&a.status)) return s;
+  return launch_gate_step(a, static_cast<cudaStream_t>(cuda_stream)) == cudaSuccess ? PALIMPSA_OK
+                                                                                  : PALIMPSA_ERR_CUDA;
+}
+
+palimpsa_status palimpsa_gated_scan_backward(const void* x, const void* r, const float* A, const void* i, const void* z,
+                                             const float* r_bias, const float* i_bias, const float* ckpt, const void* dy,
+                                             const float* dh_T, void* dx, void* dr, float* dA, void* di, void* dz,
+                                             float* dr_bias, float* di_bias, float* dh0,
+                                             const palimpsa_gate_strides* strides, const int* cu_seqlens, int B, int T,
+                                             int max_seqlen, int D, palimpsa_dtype in_dtype, void* cuda_stream) {
+  if (!A || !dA || (T != 0 && (!x || !r || !ckpt || !dy || !dx || !dr || (i && !di) || (z && !dz) || (i_bias && !i))))
+    return PALIMPSA_ERR_NULL;
+  GateArgs a = gate_args(x, r, A, i, z, r_bias, i_bias, D, in_dtype);
+  a.ckpt_in = ckpt;
+  a.dy = dy;
+  a.dh_T = dh_T;
+  a.dx = dx;
+  a.dr = dr;
+  a.di = di;
+  a.dz = dz;
+  a.dA = dA;
+  a.dr_bias = dr_bias;
+  a.di_bias = di_bias;
+  a.dh0 = dh0;
+  a.rows = rows_of(cu_seqlens, B, T, max_seqlen);
+  if (palimpsa_status s = gate_checks(a, in_dtype)) return s;
+  if (palimpsa_status s = gate_strides(&a, strides, in_dtype)) return s;
+  if (palimpsa_status s = device_status_word(&a.status)) return s;
+  const cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
+  float* scratch = nullptr;
+  if (acquire_scratch(plan_gate_backward(&a) * sizeof(float), s, &scratch) != cudaSuccess) return PALIMPSA_ERR_CUDA;
+  return release(launch_gate_backward(a, scratch, s), scratch, s);
+}
+
+palimpsa_status palimpsa_layer_norm(const void* x, long long x_stride, const void* residual, long long residual_stride,
+                                    const float* weight, const float* bias, void* y, void* sum, float* stats,
+                                    long long rows, int D, float eps, palimpsa_dtype in_dtype, void* cuda_stream) {
+  if (rows != 0 && (!x || !y || (residual && !sum))) return PALIMPSA_ERR_NULL;
+  NormArgs a{};
+  a.x = x;
+  a.residual = residual;
+  a.weight = weight;
+  a.bias = bias;
+  a.y = y;
+  a.sum = sum;
+  a.stats = stats;
+  a.rows = rows;
+  a.D = D;
+  a.eps = eps;
+  a.bf16 = in_dtype == PALIMPSA_BF16;
+  if (palimpsa_status s = norm_checks(a, in_dtype)) return s;
+  if (!(eps > 0.f && eps <= 3.0e38f)) return PALIMPSA_ERR_UNSUPPORTED;
+  if (stats && !aligned(stats, 8)) return PALIMPSA_ERR_ALIGN;
+  if (palimpsa_status s = stride_of(x_stride, D, in_dtype, &a.x_ld)) return s;
+  if (palimpsa_status s = stride_of(residual_stride, D, in_dtype, &a.residual_ld)) return s;
+  return launch_norm_forward(a, static_cast<cudaStream_t>(cuda_stream)) == cudaSuccess ? PALIMPSA_OK : PALIMPSA_ERR_CUDA;
+}
+
+palimpsa_status palimpsa_layer_norm_backward(const void* s, long long s_stride, const float* weight, const float* stats,
+                                             const void* dy, long long dy_stride, const void* ds, long long ds_stride,
+                                             void* dx, float* dweight, float* dbias, long long rows, int D,
+                                             palimpsa_dtype in_dtype, void* cuda_stream) {
+  if (rows != 0 && (!s || !stats || !dy || !dx)) return PALIMPSA_ERR_NULL;
+  NormArgs a{};
+  a.x = s;
+  a.weight = weight;
+  a.stats = const_cast<float*>(stats);
+  a.dy = dy;
+  a.ds = ds;
+  a.dx = dx;
+  a.dweight = dweight;
+  a.dbias = dbias;
+  a.rows = rows;
+  a.D = D;
+  a.bf16 = in_dtype == PALIMPSA_BF16;
+  if (palimpsa_status e = norm_checks(a, in_dtype)) return e;
+  if (stats && !aligned(stats, 8)) return PALIMPSA_ERR_ALIGN;
+  if (palimpsa_status e = stride_of(s_stride, D, in_dtype, &a.x_ld)) return e;
+  if (palimpsa_status e = stride_of(dy_stride, D, in_dtype, &a.dy_ld)) return e;
+  if (palimpsa_status e = stride_of(ds_stride, D, in_dtype, &a.ds_ld)) return e;
+  const cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
+  float* scratch = nullptr;
+  const size_t bytes = norm_backward_scratch_floats(a) * sizeof(float);
+  if (bytes && acquire_scratch(bytes, stream, &scratch) != cudaSuccess) return PALIMPSA_ERR_CUDA;
+  return release(launch_norm_backward(a, scratch, stream), scratch, stream);
 }
 
 }  // extern "C"

@@ -46,12 +46,20 @@ def _library():
             "palimpsa_selective_scan": [p] * 12 + [st, p, i, i, i, i, i, i, u, i, p],
             "palimpsa_selective_scan_step": [p] * 10 + [st, i, i, i, i, u, i, p],
             "palimpsa_selective_scan_backward": [p] * 20 + [st, p, i, i, i, i, i, i, u, i, p],
+            # gated.py and norm.py
+            "palimpsa_gated_scan": [p] * 13 + [i] * 5 + [p],
+            "palimpsa_gated_scan_step": [p] * 10 + [i] * 3 + [p],
+            "palimpsa_gated_scan_backward": [p] * 20 + [i] * 5 + [p],
+            "palimpsa_layer_norm": [p, ll, p, ll, p, p, p, p, p, ll, i, ctypes.c_float, i, p],
+            "palimpsa_layer_norm_backward": [p, ll, p, p, p, ll, p, ll, p, p, p, ll, i, i, p],
         }
         for name, args in sig.items():
             fn = getattr(lib, name)
             fn.restype, fn.argtypes = i, args
         lib.palimpsa_selective_scan_checkpoint_bytes.restype = ctypes.c_size_t
         lib.palimpsa_selective_scan_checkpoint_bytes.argtypes = [i, i, i, i, i]
+        lib.palimpsa_gated_scan_checkpoint_bytes.restype = ctypes.c_size_t
+        lib.palimpsa_gated_scan_checkpoint_bytes.argtypes = [i, i, i, i]
         _lib = lib
     return _lib
 

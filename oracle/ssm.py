@@ -1,6 +1,6 @@
 """ORACLE — test infrastructure only (see ``oracle/__init__``).
 
-Plain fp64 statements of the two state-space operators, one sequence and one token at a
+Plain fp64 statements of the state-space operators and the layer norm, one sequence and one token at a
 time, in torch so that torch.autograd (a library routine) differentiates them exactly. They
 share no code with the CUDA library.
 
@@ -9,6 +9,9 @@ share no code with the CUDA library.
 * ``scan``: s = softplus(dt + dt_bias) (or dt + dt_bias), h_t = exp(-A s_t) h_{t-1} +
   s_t x_t B_t, y_t = (C_t h_t + D x_t) silu(z_t), every channel reading the B and C of its
   group.
+* ``gate``: a_t = exp(-A sigmoid(r_t + r_bias)), h_t = a_t h_{t-1} + sqrt(1 - a_t^2)
+  sigmoid(i_t + i_bias) x_t, y_t = h_t silu(z_t).
+* ``layer_norm``: s = x + residual as it is stored, y = (s - mean) / sqrt(variance + eps) weight + bias.
 
 Token arrays are [rows, ...]; ``cu`` gives the sequences' row ranges. Rows outside every
 sequence come back as zeros.
@@ -67,6 +70,41 @@ def scan(x, dt, A, B, C, D, z, dt_bias, h0, cu, softplus=True):
         lasts.append(h)
     ys.append(torch.zeros(x.shape[0] - at, ch, dtype=F64))
     return torch.cat(ys), torch.stack(lasts)
+
+
+def gate(x, r, A, i, z, r_bias, i_bias, h0, cu):
+    """x, r, i, z [rows, D], A, r_bias, i_bias [D], h0 [n, D] (i, z, r_bias, i_bias, h0 may be None)
+    -> (y [rows, D], h_T [n, D])."""
+    D = x.shape[1]
+    ys, lasts, at = [], [], 0
+    for n in range(len(cu) - 1):
+        s0, s1 = int(cu[n]), int(cu[n + 1])
+        ys.append(torch.zeros(s0 - at, D, dtype=F64))
+        at = s1
+        h = torch.zeros(D, dtype=F64) if h0 is None else h0[n]
+        rows = []
+        for t in range(s0, s1):
+            rate = A * torch.sigmoid(r[t] if r_bias is None else r[t] + r_bias)
+            u = torch.sqrt(-torch.expm1(-2 * rate)) * x[t]
+            if i is not None:
+                u = u * torch.sigmoid(i[t] if i_bias is None else i[t] + i_bias)
+            h = torch.exp(-rate) * h + u
+            rows.append(h if z is None else h * z[t] * torch.sigmoid(z[t]))
+        ys.append(torch.stack(rows) if rows else torch.zeros(0, D, dtype=F64))
+        lasts.append(h)
+    ys.append(torch.zeros(x.shape[0] - at, D, dtype=F64))
+    return torch.cat(ys), torch.stack(lasts)
+
+
+def layer_norm(s, weight, bias, eps):
+    """s [rows, D] (the sum as it is stored), weight, bias [D] or None -> y [rows, D]."""
+    rows = []
+    for v in s:
+        mean = v.sum() / v.numel()
+        t = (v - mean) / torch.sqrt(((v - mean) ** 2).sum() / v.numel() + eps)
+        t = t if weight is None else t * weight
+        rows.append(t if bias is None else t + bias)
+    return torch.stack(rows) if rows else torch.zeros_like(s)
 
 
 def gradients(fn, inputs, dy, dlast, cu, **kw):
