@@ -216,6 +216,7 @@ palimpsa_status step_sequence_impl(const void* q, const void* k, const void* v, 
 }  // namespace
 
 palimpsa_status device_status_word(unsigned int** out) { return status_word(out); }
+unsigned long long wait_timeout_ns() { return g_wait_timeout_ns.load(); }
 cudaError_t acquire_scratch(size_t bytes, cudaStream_t s, float** p) {
   StreamOrderedScratch scratch;
   return scratch.acquire(bytes, s, p);

@@ -8,32 +8,36 @@
 
 namespace palimpsa {
 
-// A tile is 64 channels (a lane holds two, a warp a row of them) by 8 tokens for each of
-// the CTA's warps; the 8 tokens of a warp are a piece. 8 warps in bf16, 4 in fp32, whose
-// rows are twice as long.
+// A tile is 64 channels by a piece of 8 tokens for each of the CTA's groups of threads: half
+// warps in the forward (a lane holds 4 channels), warps in the backward (2).
 constexpr int kPiece = kGateCheckpoint;
 constexpr int kGateChannels = 64;
 constexpr int kGateCluster = 8;  // CTAs of a cluster, at most (the portable limit)
 
-template <bool BF16>
+template <bool BF16, int PIECES, int THREADS>
 struct GateTile {
   static constexpr int ES = BF16 ? 2 : 4;
-  static constexpr int warps = BF16 ? 8 : 4;
-  static constexpr int threads = 32 * warps;
-  static constexpr int tokens = kPiece * warps;
+  static constexpr int pieces = PIECES, threads = THREADS;
+  static constexpr int tokens = kPiece * PIECES;
   static constexpr int row = kGateChannels * ES;      // bytes of a row
   static constexpr int bytes = tokens * row;          // of an array
   static constexpr int vecs = row / 16;               // 16-byte vectors of a row
   static constexpr int rows_at_once = threads / vecs; // rows that the CTA's threads copy in turn
+  static_assert(tokens % rows_at_once == 0, "whole turns");
 };
 
-// A CTA's place: its sequence, rank in the cluster and channels.
 inline long long gate_tiles(int D) { return (D + kGateChannels - 1) / kGateChannels; }
 
 // CTAs of a cluster for tiles of `tokens` tokens, `slots` CTAs at once on the GPU.
 int gate_cluster(const SeqRows& r, int D, int tokens, long long slots);
 
 #if defined(__CUDACC__)
+
+__device__ __forceinline__ float fmin_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
 
 // Two neighbouring channels of the input type.
 template <bool BF16>
@@ -51,59 +55,100 @@ __device__ __forceinline__ void store_pair(void* p, float2 v) {
   else *static_cast<float2*>(p) = v;
 }
 
-// sigmoid(u) = 1 / (1 + e), e = e^-u, and 1 - sigmoid(u) = e sigmoid(u), which does not
-// cancel. e is kept below 2^126, so that both stay finite (and sigmoid above 2^-127).
-struct Sigmoid {
-  float2 p, e;
-  __device__ __forceinline__ explicit Sigmoid(float2 u) {
-    const float2 x = __fmul2_rn(u, make_float2(-kLog2e, -kLog2e));
-    e = make_float2(ex2_approx(fmin_nan(x.x)), ex2_approx(fmin_nan(x.y)));
-    const float2 w = __fadd2_rn(e, make_float2(1.f, 1.f));
-    p = make_float2(rcp_approx(w.x), rcp_approx(w.y));
-  }
-  __device__ __forceinline__ float2 rest() const { return __fmul2_rn(e, p); }  // 1 - p
-  static __device__ __forceinline__ float fmin_nan(float x) {
-    float r;
-    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(126.f));
-    return r;
-  }
-};
-
-// The decay a = e^-w of a rate w >= 0 and 1 - a^2. Slow channels have w of 1e-3 and
-// below, where 1 - a^2 from a rounded a has lost its digits, and a state of a long memory
-// gathers a's own error over the tokens it remembers. So below 0.35 both come from
-// m = 1 - e^-w by its series (up to w^7; what is left out is below 2e-8 of it): a = 1 - m,
-// 1 - a^2 = m (2 - m). Above, a is the SFU's 2^x, and 1 - a^2 > 0.5 does not cancel.
-__device__ __forceinline__ void decay_of(float2 w, float2* a, float2* rest) {
-  float2 m = make_float2(1.f / 5040.f, 1.f / 5040.f);
-  m = __ffma2_rn(m, w, make_float2(-1.f / 720.f, -1.f / 720.f));
-  m = __ffma2_rn(m, w, make_float2(1.f / 120.f, 1.f / 120.f));
-  m = __ffma2_rn(m, w, make_float2(-1.f / 24.f, -1.f / 24.f));
-  m = __ffma2_rn(m, w, make_float2(1.f / 6.f, 1.f / 6.f));
-  m = __ffma2_rn(m, w, make_float2(-0.5f, -0.5f));
-  m = __ffma2_rn(m, w, make_float2(1.f, 1.f));
-  m = __fmul2_rn(m, w);
-  const float2 u = __fmul2_rn(w, make_float2(-kLog2e, -kLog2e));
-  const bool lx = w.x < 0.35f, ly = w.y < 0.35f;
-  a->x = lx ? 1.f - m.x : ex2_approx(u.x);
-  a->y = ly ? 1.f - m.y : ex2_approx(u.y);
-  rest->x = lx ? fmaf(-m.x, m.x, 2.f * m.x) : fmaf(-a->x, a->x, 1.f);
-  rest->y = ly ? fmaf(-m.y, m.y, 2.f * m.y) : fmaf(-a->y, a->y, 1.f);
-}
-__device__ __forceinline__ float sqrt_approx(float x) {
-  float r;
-  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
 __device__ __forceinline__ float rsqrt_approx(float x) {
   float r;
   asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
 
+// 1 + e^-u and sigmoid(u) = 1 / (1 + e^-u), from x = -log2(e) u.
+__device__ __forceinline__ float2 one_plus(float2 x) {
+  return __fadd2_rn(make_float2(ex2_approx(x.x), ex2_approx(x.y)), make_float2(1.f, 1.f));
+}
+__device__ __forceinline__ float2 sigmoid_of(float2 x) {
+  const float2 w = one_plus(x);
+  return make_float2(rcp_approx(w.x), rcp_approx(w.y));
+}
+// The same with 1 - sigmoid(u) = e sigmoid(u), e = e^-u, which does not cancel. e is kept below
+// 2^126, so that both stay finite (and sigmoid above 2^-127).
+__device__ __forceinline__ float2 sigmoid_of(float2 x, float2* rest) {
+  x = make_float2(fmin_nan(x.x, 126.f), fmin_nan(x.y, 126.f));
+  const float2 e = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+  const float2 w = __fadd2_rn(e, make_float2(1.f, 1.f));
+  const float2 p = make_float2(rcp_approx(w.x), rcp_approx(w.y));
+  *rest = __fmul2_rn(e, p);
+  return p;
+}
+
+// The decay a = e^-w of a rate w >= 0 and 1 - a^2 = (1 - a)(1 + a). Slow channels have w of
+// 1e-3 and below, where 1 - a from a rounded a has lost its digits, and a state of a long
+// memory gathers a's own error over the tokens it remembers. So below 0.3 both come from
+// m = 1 - a = w phi(w), with phi = (1 - e^-w) / w by the polynomial of degree 4 that is
+// closest to it over [0, 0.3] (found by an exchange of its extrema; 6e-9 off at most). Above,
+// a is the SFU's 2^x and 1 - a > 0.25 does not cancel. (1 - a^2 is at least 1e-35, so that
+// its root has a reciprocal.)
+__device__ __forceinline__ void decay_of(float2 w, float2* a, float2* rest) {
+  float2 m = make_float2(0.00735594891f, 0.00735594891f);
+  m = __ffma2_rn(m, w, make_float2(-0.0414141268f, -0.0414141268f));
+  m = __ffma2_rn(m, w, make_float2(0.166639641f, 0.166639641f));
+  m = __ffma2_rn(m, w, make_float2(-0.499998987f, -0.499998987f));
+  m = __ffma2_rn(m, w, make_float2(1.f, 1.f));
+  m = __ffma2_rn(m, w, make_float2(1e-35f, 1e-35f));
+  const float2 u = __fmul2_rn(w, make_float2(-kLog2e, -kLog2e));
+  const float2 e = make_float2(ex2_approx(u.x), ex2_approx(u.y));
+  const float2 far = __ffma2_rn(e, make_float2(-1.f, -1.f), make_float2(1.f, 1.f));
+  const float2 near = __ffma2_rn(m, make_float2(-1.f, -1.f), make_float2(1.f, 1.f));
+  const bool lx = w.x < 0.3f, ly = w.y < 0.3f;
+  m = make_float2(lx ? m.x : far.x, ly ? m.y : far.y);
+  *a = make_float2(lx ? near.x : e.x, ly ? near.y : e.y);
+  *rest = __ffma2_rn(m, *a, m);
+}
+// sqrt(rest) sigmoid(u) x, from rest = 1 - a^2 and q = 1 + e^-u: one reciprocal root for the
+// root and the quotient. (q^2 beyond fp32's range gives 0, as the quotient would.)
+__device__ __forceinline__ float2 input_of(float2 rest, float2 q, float2 x) {
+  const float2 v = __fmul2_rn(__fmul2_rn(rest, q), q);
+  return __fmul2_rn(__fmul2_rn(rest, x), make_float2(rsqrt_approx(v.x), rsqrt_approx(v.y)));
+}
+__device__ __forceinline__ float2 input_of(float2 rest, float2 x) {
+  return __fmul2_rn(__fmul2_rn(rest, x), make_float2(rsqrt_approx(rest.x), rsqrt_approx(rest.y)));
+}
+// The address of a shared object in another CTA of the cluster, 16 bytes stored there, counted on
+// a barrier of that CTA, and the wait for them.
+__device__ __forceinline__ uint32_t cluster_addr(const void* p, int rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void st_async(uint32_t to, const float4& v, uint32_t bar) {
+  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(to),
+               "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w), "r"(bar)
+               : "memory");
+}
+__device__ __forceinline__ bool cluster_try_wait(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// false where the wait ran out.
+__device__ __forceinline__ bool cluster_wait(uint64_t* bar, uint32_t parity, unsigned long long timeout_ns) {
+  if (cluster_try_wait(bar, parity)) return true;
+  const unsigned long long t0 = global_ns();
+  for (;;) {
+    for (int i = 0; i < 64; ++i)
+      if (cluster_try_wait(bar, parity)) return true;
+    if (global_ns() - t0 >= timeout_ns) return cluster_try_wait(bar, parity);
+  }
+}
+
 __device__ __forceinline__ float2 ffma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
 
-// The rate of a channel, or its refusal.
+// Two neighbouring channels' parameters, or a value in their place.
 __device__ __forceinline__ float2 pair_or(const float* p, int ch, bool in, float otherwise) {
   return p && in ? make_float2(p[ch], p[ch + 1]) : make_float2(otherwise, otherwise);
 }

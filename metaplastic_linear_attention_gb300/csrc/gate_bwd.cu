@@ -25,26 +25,30 @@ namespace cg = cooperative_groups;
 
 constexpr int kResident = 2;  // CTAs of an SM
 
-// Shared memory: the ring of raw inputs (and the states before the pieces), then summaries.
+// Warps a CTA: in fp32 half as many, whose rows are twice as long.
 template <bool BF16>
-__host__ __device__ constexpr int stage_bytes(int arrays) {
-  return arrays * GateTile<BF16>::bytes + GateTile<BF16>::warps * kGateChannels * 4;
-}
-template <bool BF16>
-constexpr int bwd_smem(int arrays, bool cluster) {
-  return 2 * stage_bytes<BF16>(arrays) + GateTile<BF16>::warps * 32 * 16 + (cluster ? 2 * kGateCluster * 32 * 16 : 0);
-}
+using Tile = GateTile<BF16, BF16 ? 8 : 4, BF16 ? 256 : 128>;
+
+// Shared memory: the ring of raw inputs (and the states before the pieces), then the pieces' and
+// the ranks' summaries.
+template <bool BF16, bool IN, bool GATE, bool CLUSTER>
+struct BwdSmem {
+  static constexpr int h = (3 + IN + GATE) * Tile<BF16>::bytes, stage = h + Tile<BF16>::pieces * kGateChannels * 4;
+  static constexpr int agg = 2 * stage, ranks = agg + Tile<BF16>::pieces * 512;
+  static constexpr int total = ranks + CLUSTER * 2 * kGateCluster * 512;
+};
 
 // sums: [n_seq, cluster, 3, D], the CTAs' parts of dA, dr_bias and di_bias.
 template <bool BF16, bool IN, bool GATE, bool CLUSTER>
-__global__ void __launch_bounds__(GateTile<BF16>::threads, BF16 ? kResident : 2 * kResident)
+__global__ void __launch_bounds__(Tile<BF16>::threads, BF16 ? kResident : 2 * kResident)
 palimpsa_gate_bwd_kernel(GateArgs a, int tiles, float* sums) {
-  using G = GateTile<BF16>;
-  constexpr int ES = G::ES, NA = 3 + IN + GATE, RT = G::tokens, kStage = stage_bytes<BF16>(NA);
+  using G = Tile<BF16>;
+  using S = BwdSmem<BF16, IN, GATE, CLUSTER>;
+  constexpr int ES = G::ES, RT = G::tokens, NP = G::pieces;
   constexpr int kI = 3, kZ = 3 + IN;  // places of the arrays x, r, dy, i, z
   extern __shared__ __align__(128) unsigned char smem[];
-  float4* const agg = reinterpret_cast<float4*>(smem + 2 * kStage);
-  float4* const xagg = agg + G::warps * 32;
+  __shared__ uint64_t bars[2];
+  float4* const agg = reinterpret_cast<float4*>(smem + S::agg);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int cs = CLUSTER ? a.cluster : 1;
   const int rank = CLUSTER ? (int)(blockIdx.x % cs) : 0;
@@ -69,7 +73,7 @@ palimpsa_gate_bwd_kernel(GateArgs a, int tiles, float* sums) {
   auto stage = [&](int k) {  // copies of round k's tile, as one group
     const int t0 = k * step + rank * RT, nt = min(RT, len - t0);
     if (k >= 0) {
-      unsigned char* const to = smem + (k & 1) * kStage;
+      unsigned char* const to = smem + (k & 1) * S::stage;
       const long long first = row0 + t0 + vrow, col = (long long)ch0 * ES + vec * 16;
       auto copy = [&](const void* from, long long ld, int slot) {
         const char* p = static_cast<const char*>(from) + first * ld * ES + col;
@@ -86,68 +90,79 @@ palimpsa_gate_bwd_kernel(GateArgs a, int tiles, float* sums) {
         if (GATE) copy(a.z, a.z_ld, kZ);
       }
       // The states before the pieces: 16 vectors of 4 channels each.
-      if (tid < G::warps * 16 && (tid >> 4) * kPiece < nt && ch0 + (tid & 15) * 4 < a.D)
-        cp_async16(to + NA * G::bytes + tid * 16, ckpt + (long long)(t0 / kPiece + (tid >> 4)) * a.D + (tid & 15) * 4);
+      if (tid < NP * 16 && (tid >> 4) * kPiece < nt && ch0 + (tid & 15) * 4 < a.D)
+        cp_async16(to + S::h + tid * 16, ckpt + (long long)(t0 / kPiece + (tid >> 4)) * a.D + (tid & 15) * 4);
     }
     cp_async_commit();
   };
   stage(rounds - 1);
 
+  if (CLUSTER && tid == 0) {
+    mbar_init(&bars[0], 1);
+    mbar_init(&bars[1], 1);
+    fence_mbar_init();
+  }
   const float2 A = pair_or(a.A, ch, in, 1.f);
-  const float2 rb = pair_or(a.r_bias, ch, in, 0.f), ib = pair_or(a.i_bias, ch, in, 0.f);
+  const float2 scale = make_float2(-kLog2e, -kLog2e);
+  const float2 rb = __fmul2_rn(pair_or(a.r_bias, ch, in, 0.f), scale), ib = __fmul2_rn(pair_or(a.i_bias, ch, in, 0.f), scale);
   if (!pos_finite(A.x) || !pos_finite(A.y)) latch_status(a.status, kStatusDomain);
   float2 carry = zero;  // a g of the token behind the round
   if (a.dh_T && in) carry = *reinterpret_cast<const float2*>(a.dh_T + n * a.D + ch);
   float2 sA = zero, sr = zero, si = zero;
-  if (CLUSTER) cg::this_cluster().sync();  // every CTA has started: its shared memory may be written
+  bool waits = true;
+  if (CLUSTER) cg::this_cluster().sync();  // every CTA has started, its barriers set: it may be written to
 
   for (int k = rounds - 1; k >= 0; --k) {
     const int tp = k * step + rank * RT + warp * kPiece;
     const int np = min(kPiece, len - tp);
-    unsigned char* const raw = smem + (k & 1) * kStage + warp * kPiece * G::row + lane * 2 * ES;
+    unsigned char* const raw = smem + (k & 1) * S::stage + warp * kPiece * G::row + lane * 2 * ES;
     cp_async_wait<0>();
+    if (CLUSTER && tid == 0) mbar_arrive_expect_tx(&bars[k & 1], cs * 512);
     __syncthreads();  // the round's inputs are here; the other stage and the summaries are free
     stage(k - 1);
 
     // The factors of g_t in dx, di, dr and dA, the decays, and dy silu(z).
     float2 da[kPiece], fx[kPiece], fi[IN ? kPiece : 1], fr[kPiece], fA[kPiece], gy[kPiece];
     const long long at = (row0 + tp) * a.D + ch;
-    float2 h = np > 0 ? *reinterpret_cast<const float2*>(smem + (k & 1) * kStage + NA * G::bytes +
+    float2 h = np > 0 ? *reinterpret_cast<const float2*>(smem + (k & 1) * S::stage + S::h +
                                                          (warp * kGateChannels + 2 * lane) * 4)
                       : zero;
 #pragma unroll
     for (int t = 0; t < kPiece; ++t) {
       if (t < np) {
         const float2 x = load_pair<BF16>(raw + t * G::row);
-        const Sigmoid s(__fadd2_rn(load_pair<BF16>(raw + G::bytes + t * G::row), rb));
+        float2 closed;  // 1 - s
+        const float2 s = sigmoid_of(ffma2(load_pair<BF16>(raw + G::bytes + t * G::row), scale, rb), &closed);
         gy[t] = load_pair<BF16>(raw + 2 * G::bytes + t * G::row);
-        const float2 w = __fmul2_rn(A, s.p);
+        const float2 w = __fmul2_rn(A, s);
         float2 q;  // 1 - a^2
         decay_of(w, &da[t], &q);
-        // (A rate of 0 has q = 0, and no gradient: the factor w of dr, or s of dA, is 0 too.)
-        const float2 ni = make_float2(rsqrt_approx(fmaxf(q.x, 1e-36f)), rsqrt_approx(fmaxf(q.y, 1e-36f)));
+        // (A rate of 0 has 1 / n of 3e17, and no gradient: the factor w of dr, or s of dA, is 0 too.)
+        const float2 ni = make_float2(rsqrt_approx(q.x), rsqrt_approx(q.y));
         fx[t] = __fmul2_rn(q, ni);
         float2 u = x;
         if (IN) {
-          const Sigmoid p(__fadd2_rn(load_pair<BF16>(raw + kI * G::bytes + t * G::row), ib));
-          fx[t] = __fmul2_rn(fx[t], p.p);
-          fi[t] = __fmul2_rn(__fmul2_rn(fx[t], x), p.rest());
-          u = __fmul2_rn(x, p.p);
+          float2 shut;  // 1 - p
+          const float2 p = sigmoid_of(ffma2(load_pair<BF16>(raw + kI * G::bytes + t * G::row), scale, ib), &shut);
+          fx[t] = __fmul2_rn(fx[t], p);
+          fi[t] = __fmul2_rn(__fmul2_rn(fx[t], x), shut);
+          u = __fmul2_rn(x, p);
         }
         const float2 old = __fmul2_rn(da[t], h);
         // dw / g = u a^2 / n - a h
         const float2 aa = __fmul2_rn(__fmul2_rn(da[t], da[t]), ni);
         const float2 dw = ffma2(u, aa, make_float2(-old.x, -old.y));
-        fA[t] = __fmul2_rn(dw, s.p);
-        fr[t] = __fmul2_rn(__fmul2_rn(dw, w), s.rest());
+        fA[t] = __fmul2_rn(dw, s);
+        fr[t] = __fmul2_rn(__fmul2_rn(dw, w), closed);
         h = ffma2(fx[t], x, old);
         if (GATE) {
           const float2 z = load_pair<BF16>(raw + kZ * G::bytes + t * G::row);
-          const Sigmoid c(z);
-          const float2 m = ffma2(z, c.rest(), make_float2(1.f, 1.f));  // silu' = c (1 + z (1 - c))
-          const float2 dz = __fmul2_rn(__fmul2_rn(gy[t], h), __fmul2_rn(c.p, m));
+          float2 rest;
+          const float2 c = sigmoid_of(__fmul2_rn(z, scale), &rest);
+          const float2 m = ffma2(z, rest, make_float2(1.f, 1.f));  // silu' = c (1 + z (1 - c))
+          const float2 dz = __fmul2_rn(__fmul2_rn(gy[t], h), __fmul2_rn(c, m));
           if (in) store_pair<BF16>(static_cast<char*>(a.dz) + (at + (long long)t * a.D) * ES, dz);
-          gy[t] = __fmul2_rn(gy[t], __fmul2_rn(z, c.p));
+          gy[t] = __fmul2_rn(gy[t], __fmul2_rn(z, c));
         }
       } else {
         da[t] = make_float2(1.f, 1.f);
@@ -168,31 +183,32 @@ palimpsa_gate_bwd_kernel(GateArgs a, int tiles, float* sums) {
     float2 c = carry;
     if (!CLUSTER) {
 #pragma unroll
-      for (int q = G::warps - 1; q >= 0; --q) {
+      for (int q = NP - 1; q >= 0; --q) {
         const float4 e = agg[q * 32 + lane];
         if (q == warp) c = carry;
         carry = ffma2(make_float2(e.x, e.y), carry, make_float2(e.z, e.w));
       }
     } else {
-      float4* const slots = xagg + (k & 1) * kGateCluster * 32;
-      cg::cluster_group cluster = cg::this_cluster();
-      for (int q = warp; q < cs; q += G::warps) {
+      float4* const slots = reinterpret_cast<float4*>(smem + S::ranks + (k & 1) * kGateCluster * 512);
+      for (int q = warp; q < cs; q += NP) {
         float2 Pc = make_float2(1.f, 1.f), Cc = zero;
 #pragma unroll
-        for (int w = G::warps - 1; w >= 0; --w) {
+        for (int w = NP - 1; w >= 0; --w) {
           const float4 e = agg[w * 32 + lane];
           Cc = ffma2(make_float2(e.x, e.y), Cc, make_float2(e.z, e.w));
           Pc = __fmul2_rn(Pc, make_float2(e.x, e.y));
         }
-        *cluster.map_shared_rank(slots + rank * 32 + lane, q) = make_float4(Pc.x, Pc.y, Cc.x, Cc.y);
+        st_async(cluster_addr(slots + rank * 32 + lane, q), make_float4(Pc.x, Pc.y, Cc.x, Cc.y),
+                 cluster_addr(&bars[k & 1], q));
       }
-      cluster.sync();
+      waits = waits && cluster_wait(&bars[k & 1], ((rounds - 1 - k) >> 1) & 1, a.wait_timeout_ns);
+      if (!waits) latch_status(a.status, kStatusTimeout);
       for (int q = cs - 1; q >= 0; --q) {
         const float4 e = slots[q * 32 + lane];
         if (q == rank) c = carry;
         carry = ffma2(make_float2(e.x, e.y), carry, make_float2(e.z, e.w));
       }
-      for (int w = G::warps - 1; w > warp; --w) {
+      for (int w = NP - 1; w > warp; --w) {
         const float4 e = agg[w * 32 + lane];
         c = ffma2(make_float2(e.x, e.y), c, make_float2(e.z, e.w));
       }
@@ -234,10 +250,11 @@ palimpsa_gate_bwd_kernel(GateArgs a, int tiles, float* sums) {
     if (warp == v && in) {
       float2 t = red[lane];
 #pragma unroll
-      for (int w = 1; w < G::warps; ++w) t = __fadd2_rn(t, red[w * 32 + lane]);
+      for (int w = 1; w < NP; ++w) t = __fadd2_rn(t, red[w * 32 + lane]);
       *reinterpret_cast<float2*>(part + (long long)v * a.D) = t;
     }
   }
+  if (CLUSTER) cg::this_cluster().sync();  // nobody sends to a CTA that has left
 }
 
 // Sums the CTAs' parts [rows, 3, D]; block y = v, 32 channels by 8 slices of the rows.
@@ -260,10 +277,10 @@ __global__ void __launch_bounds__(256) palimpsa_gate_bwd_sum_kernel(const float*
 
 template <bool BF16, bool IN, bool GATE, bool CLUSTER>
 cudaError_t run(const GateArgs& a, float* sums, cudaStream_t s) {
-  using G = GateTile<BF16>;
+  using G = Tile<BF16>;
   const long long tiles = gate_tiles(a.D), blocks = tiles * a.rows.n_seq * a.cluster;
   if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
-  constexpr int bytes = bwd_smem<BF16>(3 + IN + GATE, CLUSTER);
+  constexpr int bytes = BwdSmem<BF16, IN, GATE, CLUSTER>::total;
   const auto kernel = palimpsa_gate_bwd_kernel<BF16, IN, GATE, CLUSTER>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
@@ -293,8 +310,8 @@ cudaError_t backward(const GateArgs& a, float* sums, cudaStream_t s) {
 }  // namespace
 
 size_t plan_gate_backward(GateArgs* a) {
-  a->cluster = a->bf16 ? gate_cluster(a->rows, a->D, GateTile<true>::tokens, kResident)
-                       : gate_cluster(a->rows, a->D, GateTile<false>::tokens, 2 * kResident);
+  a->cluster = a->bf16 ? gate_cluster(a->rows, a->D, Tile<true>::tokens, kResident)
+                       : gate_cluster(a->rows, a->D, Tile<false>::tokens, 2 * kResident);
   return (size_t)a->rows.n_seq * a->cluster * 3 * a->D;
 }
 

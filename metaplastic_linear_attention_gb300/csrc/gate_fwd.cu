@@ -7,14 +7,15 @@
 // What bounds it: HBM. A channel-token moves 8 bytes in bf16 (10 with z), 0.37 clocks
 // (0.47) of an SM's share of the measured 6.77 TB/s, against 3 2^x, 2 reciprocals and a
 // root on the SFU (0.28 clocks; a 2^x and a reciprocal more with z) and about 30 FP32
-// operations. So every input is read once: a thread takes 8 tokens of two channels (a piece),
+// operations. So every input is read once: a thread takes 8 tokens of 4 channels (a piece),
 // forms their decays and inputs a, b in registers, and runs them twice, first from 0 for
 // the piece's summary (the product of its a and its end state), then, with the state
 // before the piece known, for the states themselves. The summaries of a CTA's pieces (its
-// warps, along time) pass through shared memory, and those of a cluster's CTAs through
-// distributed shared memory; every thread folds the ones before its own. A CTA walks its
-// sequence in rounds of such tiles, the next round's inputs coming by asynchronous
-// copies meanwhile, and carries the state in registers.
+// half warps, along time) pass through shared memory, and those of a cluster's CTAs
+// through each other's shared memory, as asynchronous stores that a barrier there counts;
+// every thread folds the ones before its own. A CTA walks its sequence in rounds of
+// such tiles, the next round's inputs coming by asynchronous copies meanwhile, and
+// carries the state in registers.
 //
 // Rounding: gates, decays and states are fp32; y is rounded to the input type once.
 #include <algorithm>
@@ -26,27 +27,48 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kResident = 3;  // CTAs of an SM
+constexpr int kResident = 4;  // CTAs of an SM
 
-// Shared memory: the ring of raw inputs, then the pieces' and the ranks' summaries.
+// Half warps a CTA: in fp32 half as many, whose rows are twice as long.
 template <bool BF16>
-constexpr int fwd_smem(int arrays, bool cluster) {
-  return 2 * arrays * GateTile<BF16>::bytes + GateTile<BF16>::warps * 32 * 16 +
-         (cluster ? 2 * kGateCluster * 32 * 16 : 0);
-}
+using Tile = GateTile<BF16, BF16 ? 8 : 4, BF16 ? 128 : 64>;
+
+// Shared memory: two stages of x, r and i, then two sets of the ranks' summaries,
+// [rank][products, states][16 lanes] of 4 channels. A piece's summary takes the place of its
+// first rows of x.
+template <bool BF16, bool IN>
+constexpr int kStageBytes = (2 + IN) * Tile<BF16>::bytes;
+
+// h <- P h + H over 4 channels.
+struct Four {
+  float2 v[2];
+  __device__ __forceinline__ void fold(const float4& P, const float4& H) {
+    v[0] = ffma2(make_float2(P.x, P.y), v[0], make_float2(H.x, H.y));
+    v[1] = ffma2(make_float2(P.z, P.w), v[1], make_float2(H.z, H.w));
+  }
+  __device__ __forceinline__ void times(const float4& P) {
+    v[0] = __fmul2_rn(v[0], make_float2(P.x, P.y));
+    v[1] = __fmul2_rn(v[1], make_float2(P.z, P.w));
+  }
+  __device__ __forceinline__ float4 all() const { return make_float4(v[0].x, v[0].y, v[1].x, v[1].y); }
+};
+__device__ __forceinline__ Four four(float v) { return {make_float2(v, v), make_float2(v, v)}; }
 
 template <bool BF16, bool IN, bool GATE, bool CLUSTER>
-__global__ void __launch_bounds__(GateTile<BF16>::threads, kResident) palimpsa_gate_kernel(GateArgs a, int tiles) {
-  using G = GateTile<BF16>;
-  constexpr int ES = G::ES, NA = 2 + IN + GATE, RT = G::tokens;
+__global__ void __launch_bounds__(Tile<BF16>::threads, kResident)
+palimpsa_gate_kernel(GateArgs a, int tiles) {
+  using G = Tile<BF16>;
+  using Q = Quad<BF16>;
+  using Raw = typename Q::Raw;
+  constexpr int ES = G::ES, RT = G::tokens, NP = G::pieces, kStage = kStageBytes<BF16, IN>;
   extern __shared__ __align__(128) unsigned char smem[];
-  float4* const agg = reinterpret_cast<float4*>(smem + 2 * NA * G::bytes);
-  float4* const xagg = agg + G::warps * 32;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  __shared__ uint64_t bars[2];
+  const int tid = threadIdx.x, piece = tid >> 4, lane = tid & 15;
   const int cs = CLUSTER ? a.cluster : 1;
   const int rank = CLUSTER ? (int)(blockIdx.x % cs) : 0;
   const long long rest = CLUSTER ? blockIdx.x / cs : blockIdx.x;
-  const int ch0 = (int)(rest % tiles) * kGateChannels, ch = ch0 + 2 * lane;
+  const int ch0 = (int)(rest % tiles) * kGateChannels, ch = ch0 + 4 * lane;
+  const bool in = ch < a.D;
   const long long n = rest / tiles;
   long long row0;
   int len;
@@ -56,122 +78,175 @@ __global__ void __launch_bounds__(GateTile<BF16>::threads, kResident) palimpsa_g
   }
   const int step = cs * RT, rounds = (len + step - 1) / step;
 
-  // Copies of a round's tile, as one group: a thread takes the same vector of rows
+  // Copies of a round's x, r and i, as one group: a thread takes the same vector of rows
   // rows_at_once apart. Rows past the end and channels past D are left as they are.
   const int vec = tid % G::vecs, vrow = tid / G::vecs;
   const bool vin = ch0 * ES + vec * 16 < a.D * ES;
   auto stage = [&](int k) {
     const int t0 = k * step + rank * RT, nt = min(RT, len - t0);
     if (k < rounds && vin) {
-      unsigned char* const to = smem + (k & 1) * NA * G::bytes + tid * 16;
+      unsigned char* const to = smem + (k & 1) * kStage + tid * 16;
       const long long first = row0 + t0 + vrow, col = (long long)ch0 * ES + vec * 16;
       auto copy = [&](const void* from, long long ld, int slot) {
         const char* p = static_cast<const char*>(from) + first * ld * ES + col;
+        const long long next = G::rows_at_once * ld * ES;
+        if (nt == RT) {
 #pragma unroll
-        for (int j = 0; j < RT / G::rows_at_once; ++j)
-          if (j * G::rows_at_once + vrow < nt)
-            cp_async16(to + slot * G::bytes + j * G::threads * 16, p + j * G::rows_at_once * ld * ES);
+          for (int j = 0; j < RT / G::rows_at_once; ++j, p += next)
+            cp_async16(to + slot * G::bytes + j * G::threads * 16, p);
+        } else {
+#pragma unroll
+          for (int j = 0; j < RT / G::rows_at_once; ++j, p += next)
+            if (j * G::rows_at_once + vrow < nt) cp_async16(to + slot * G::bytes + j * G::threads * 16, p);
+        }
       };
       copy(a.x, a.x_ld, 0);
       copy(a.r, a.r_ld, 1);
       if (IN) copy(a.i, a.i_ld, 2);
-      if (GATE) copy(a.z, a.z_ld, 2 + IN);
     }
     cp_async_commit();
   };
   stage(0);
 
-  const bool in = ch < a.D;
-  const float2 A = pair_or(a.A, ch, in, 1.f);
-  const float2 rb = pair_or(a.r_bias, ch, in, 0.f), ib = pair_or(a.i_bias, ch, in, 0.f);
-  if (!pos_finite(A.x) || !pos_finite(A.y)) latch_status(a.status, kStatusDomain);
-  float2 carry = make_float2(0.f, 0.f);  // the state before the round
-  if (a.h0 && in) carry = *reinterpret_cast<const float2*>(a.h0 + n * a.D + ch);
-  if (CLUSTER) cg::this_cluster().sync();  // every CTA has started: its shared memory may be written
+  if (CLUSTER && tid == 0) {
+    mbar_init(&bars[0], 1);
+    mbar_init(&bars[1], 1);
+    fence_mbar_init();
+  }
+  // Parameters, the gates' biases as their exponents' addends.
+  float2 A[2], rb[2], ib[2];
+  Four carry = four(0.f);  // the state before the round
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    A[j] = pair_or(a.A, ch + 2 * j, in, 1.f);
+    if (!pos_finite(A[j].x) || !pos_finite(A[j].y)) latch_status(a.status, kStatusDomain);
+    rb[j] = __fmul2_rn(pair_or(a.r_bias, ch + 2 * j, in, 0.f), make_float2(-kLog2e, -kLog2e));
+    if (IN) ib[j] = __fmul2_rn(pair_or(a.i_bias, ch + 2 * j, in, 0.f), make_float2(-kLog2e, -kLog2e));
+    if (a.h0 && in) carry.v[j] = *reinterpret_cast<const float2*>(a.h0 + n * a.D + ch + 2 * j);
+  }
+  bool waits = true;
+  if (CLUSTER) cg::this_cluster().sync();  // every CTA has started, its barriers set: it may be written to
 
+  const long long yd = (long long)a.D * ES;
   for (int k = 0; k < rounds; ++k) {
-    const int tp = k * step + rank * RT + warp * kPiece;  // the piece's first token
-    const int np = min(kPiece, len - tp);                 // its tokens (0 or less: none)
-    const unsigned char* const raw =
-        smem + (k & 1) * NA * G::bytes + warp * kPiece * G::row + lane * 2 * ES;
+    const int tp = k * step + rank * RT + piece * kPiece;  // the piece's first token
+    const int np = min(kPiece, len - tp);                  // its tokens (0 or less: none)
+    unsigned char* const tile = smem + (k & 1) * kStage;
+    const unsigned char* const raw = tile + piece * kPiece * G::row + lane * 4 * ES;
+    // A piece's summary: products and states of the lane's channels.
+    auto sums_of = [&](int p) { return reinterpret_cast<float4*>(tile + p * kPiece * G::row) + lane; };
     cp_async_wait<0>();
+    if (CLUSTER && tid == 0) mbar_arrive_expect_tx(&bars[k & 1], cs * 512);
     __syncthreads();  // the round's inputs are here; the other stage and the summaries are free
     stage(k + 1);
 
-    float2 da[kPiece], b[kPiece];
-    float2 P = make_float2(1.f, 1.f), H = make_float2(0.f, 0.f);
+    float2 da[kPiece][2], b[kPiece][2];
+    auto token = [&](int t) {
+      float2 x[2], r[2], i[2];
+      Q::unpack(*reinterpret_cast<const Raw*>(raw + t * G::row), x);
+      Q::unpack(*reinterpret_cast<const Raw*>(raw + G::bytes + t * G::row), r);
+      if (IN) Q::unpack(*reinterpret_cast<const Raw*>(raw + 2 * G::bytes + t * G::row), i);
 #pragma unroll
-    for (int t = 0; t < kPiece; ++t) {
-      if (t < np) {
-        const float2 x = load_pair<BF16>(raw + t * G::row);
-        const Sigmoid s(__fadd2_rn(load_pair<BF16>(raw + G::bytes + t * G::row), rb));
-        float2 rest2;
-        decay_of(__fmul2_rn(A, s.p), &da[t], &rest2);
-        b[t] = __fmul2_rn(make_float2(sqrt_approx(rest2.x), sqrt_approx(rest2.y)), x);
-        if (IN) {
-          const Sigmoid p(__fadd2_rn(load_pair<BF16>(raw + 2 * G::bytes + t * G::row), ib));
-          b[t] = __fmul2_rn(b[t], p.p);
-        }
-      } else {
-        da[t] = make_float2(1.f, 1.f);
-        b[t] = make_float2(0.f, 0.f);
+      for (int j = 0; j < 2; ++j) {
+        const float2 s = sigmoid_of(ffma2(r[j], make_float2(-kLog2e, -kLog2e), rb[j]));
+        float2 sq;
+        decay_of(__fmul2_rn(A[j], s), &da[t][j], &sq);
+        b[t][j] = IN ? input_of(sq, one_plus(ffma2(i[j], make_float2(-kLog2e, -kLog2e), ib[j])), x[j])
+                     : input_of(sq, x[j]);
       }
-      H = ffma2(da[t], H, b[t]);
-      P = __fmul2_rn(P, da[t]);
+    };
+    if (np == kPiece) {
+#pragma unroll
+      for (int t = 0; t < kPiece; ++t) token(t);
+    } else {
+#pragma unroll
+      for (int t = 0; t < kPiece; ++t) {
+        da[t][0] = da[t][1] = make_float2(1.f, 1.f);
+        b[t][0] = b[t][1] = make_float2(0.f, 0.f);
+        if (t < np) token(t);
+      }
     }
-    agg[warp * 32 + lane] = make_float4(P.x, P.y, H.x, H.y);
+    Four P = four(1.f), H = four(0.f);
+#pragma unroll
+    for (int t = 0; t < kPiece; ++t)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        H.v[j] = ffma2(da[t][j], H.v[j], b[t][j]);
+        P.v[j] = __fmul2_rn(P.v[j], da[t][j]);
+      }
+    __syncwarp();  // the piece's rows of x are read
+    sums_of(piece)[0] = P.all();
+    sums_of(piece)[16] = H.all();
+    Raw z[kPiece];  // on their way during the exchange
+    if (GATE && in) {
+      const char* p = static_cast<const char*>(a.z) + ((row0 + tp) * a.z_ld + ch) * ES;
+#pragma unroll
+      for (int t = 0; t < kPiece; ++t, p += a.z_ld * ES)
+        if (t < np) z[t] = *reinterpret_cast<const Raw*>(p);
+    }
     __syncthreads();
 
     // The state before the piece, and the one before the next round.
-    float2 h = carry;
+    Four h = carry;
     if (!CLUSTER) {
 #pragma unroll
-      for (int q = 0; q < G::warps; ++q) {
-        const float4 e = agg[q * 32 + lane];
-        if (q == warp) h = carry;
-        carry = ffma2(make_float2(e.x, e.y), carry, make_float2(e.z, e.w));
+      for (int q = 0; q < NP; ++q) {
+        if (q == piece) h = carry;
+        carry.fold(sums_of(q)[0], sums_of(q)[16]);
       }
     } else {
-      // Warp q sends the CTA's summary to rank q. (Two sets of slots: a rank may be a round ahead.)
-      float4* const slots = xagg + (k & 1) * kGateCluster * 32;
-      cg::cluster_group cluster = cg::this_cluster();
-      for (int q = warp; q < cs; q += G::warps) {
-        float2 Pc = make_float2(1.f, 1.f), Hc = make_float2(0.f, 0.f);
+      // Group q sends the CTA's summary to rank q. (Two sets of slots: a rank may be a round ahead.)
+      float4* const slots = reinterpret_cast<float4*>(smem + 2 * kStage + (k & 1) * cs * 512) + lane;
+      for (int q = piece; q < cs; q += NP) {
+        Four Pc = four(1.f), Hc = four(0.f);
 #pragma unroll
-        for (int w = 0; w < G::warps; ++w) {
-          const float4 e = agg[w * 32 + lane];
-          Hc = ffma2(make_float2(e.x, e.y), Hc, make_float2(e.z, e.w));
-          Pc = __fmul2_rn(Pc, make_float2(e.x, e.y));
+        for (int w = 0; w < NP; ++w) {
+          Hc.fold(sums_of(w)[0], sums_of(w)[16]);
+          Pc.times(sums_of(w)[0]);
         }
-        *cluster.map_shared_rank(slots + rank * 32 + lane, q) = make_float4(Pc.x, Pc.y, Hc.x, Hc.y);
+        const uint32_t to = cluster_addr(slots + rank * 32, q), bar = cluster_addr(&bars[k & 1], q);
+        st_async(to, Pc.all(), bar);
+        st_async(to + 256, Hc.all(), bar);
       }
-      cluster.sync();
-      for (int q = 0; q < cs; ++q) {
-        const float4 e = slots[q * 32 + lane];
-        if (q == rank) h = carry;
-        carry = ffma2(make_float2(e.x, e.y), carry, make_float2(e.z, e.w));
-      }
-      for (int w = 0; w < warp; ++w) {
-        const float4 e = agg[w * 32 + lane];
-        h = ffma2(make_float2(e.x, e.y), h, make_float2(e.z, e.w));
-      }
+      waits = waits && cluster_wait(&bars[k & 1], (k >> 1) & 1, a.wait_timeout_ns);
+      if (!waits) latch_status(a.status, kStatusTimeout);
+      int q = 0;
+      for (; q < rank; ++q) carry.fold(slots[q * 32], slots[q * 32 + 16]);
+      h = carry;
+      for (; q < cs; ++q) carry.fold(slots[q * 32], slots[q * 32 + 16]);
+      for (int w = 0; w < piece; ++w) h.fold(sums_of(w)[0], sums_of(w)[16]);
     }
     if (in && np > 0) {
       if (a.ckpt)
-        *reinterpret_cast<float2*>(a.ckpt + (gate_ckpt_row0(a.rows, n, row0) + tp / kPiece) * a.D + ch) = h;
-      char* const py = static_cast<char*>(a.y) + ((row0 + tp) * a.D + ch) * ES;
+        *reinterpret_cast<float4*>(a.ckpt + (gate_ckpt_row0(a.rows, n, row0) + tp / kPiece) * a.D + ch) = h.all();
+      char* py = static_cast<char*>(a.y) + (row0 + tp) * yd + ch * ES;
+      auto out = [&](int t) {
+        float2 y[2];
 #pragma unroll
-      for (int t = 0; t < kPiece; ++t)
-        if (t < np) {
-          h = ffma2(da[t], h, b[t]);
-          float2 y = h;
-          if (GATE) y = __fmul2_rn(y, silu_fast(load_pair<BF16>(raw + (2 + IN) * G::bytes + t * G::row)));
-          store_pair<BF16>(py + (long long)t * a.D * ES, y);
+        for (int j = 0; j < 2; ++j) y[j] = h.v[j] = ffma2(da[t][j], h.v[j], b[t][j]);
+        if (GATE) {
+          float2 f[2];
+          Q::unpack(z[t], f);
+#pragma unroll
+          for (int j = 0; j < 2; ++j) y[j] = __fmul2_rn(y[j], silu_fast(f[j]));
         }
+        *reinterpret_cast<Raw*>(py) = Q::pack(y);
+        py += yd;
+      };
+      if (np == kPiece) {
+#pragma unroll
+        for (int t = 0; t < kPiece; ++t) out(t);
+      } else {
+#pragma unroll
+        for (int t = 0; t < kPiece; ++t)
+          if (t < np) out(t);
+      }
     }
     __syncwarp();
   }
-  if (rank == 0 && warp == 0 && in) *reinterpret_cast<float2*>(a.h_T + n * a.D + ch) = carry;
+  if (rank == 0 && piece == 0 && in) *reinterpret_cast<float4*>(a.h_T + n * a.D + ch) = carry.all();
+  __syncwarp();
+  if (CLUSTER) cg::this_cluster().sync();  // nobody sends to a CTA that has left
 }
 
 // One token: a thread takes 4 channels of a sequence. A few bytes each way: latency alone.
@@ -200,11 +275,13 @@ __global__ void __launch_bounds__(128) palimpsa_gate_step_kernel(GateArgs a) {
   for (int j = 0; j < 2; ++j) {
     const float2 A = pair_or(a.A, ch + 2 * j, true, 1.f);
     bad |= !pos_finite(A.x) || !pos_finite(A.y);
-    const Sigmoid s(__fadd2_rn(r[j], pair_or(a.r_bias, ch + 2 * j, true, 0.f)));
-    float2 da, rest;
-    decay_of(__fmul2_rn(A, s.p), &da, &rest);
-    float2 b = __fmul2_rn(make_float2(sqrt_approx(rest.x), sqrt_approx(rest.y)), x[j]);
-    if (IN) b = __fmul2_rn(b, Sigmoid(__fadd2_rn(i[j], pair_or(a.i_bias, ch + 2 * j, true, 0.f))).p);
+    const float2 scale = make_float2(-kLog2e, -kLog2e);
+    const float2 s = sigmoid_of(__fmul2_rn(__fadd2_rn(r[j], pair_or(a.r_bias, ch + 2 * j, true, 0.f)), scale));
+    float2 da, sq;
+    decay_of(__fmul2_rn(A, s), &da, &sq);
+    const float2 b =
+        IN ? input_of(sq, one_plus(__fmul2_rn(__fadd2_rn(i[j], pair_or(a.i_bias, ch + 2 * j, true, 0.f)), scale)), x[j])
+           : input_of(sq, x[j]);
     h[j] = ffma2(da, h[j], b);
     y[j] = GATE ? __fmul2_rn(h[j], silu_fast(z[j])) : h[j];
   }
@@ -215,10 +292,10 @@ __global__ void __launch_bounds__(128) palimpsa_gate_step_kernel(GateArgs a) {
 
 template <bool BF16, bool IN, bool GATE, bool CLUSTER>
 cudaError_t run(const GateArgs& a, cudaStream_t s) {
-  using G = GateTile<BF16>;
+  using G = Tile<BF16>;
   const long long tiles = gate_tiles(a.D), blocks = tiles * a.rows.n_seq * a.cluster;
   if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
-  constexpr int bytes = fwd_smem<BF16>(2 + IN + GATE, CLUSTER);
+  const int bytes = 2 * kStageBytes<BF16, IN> + (CLUSTER ? 2 * a.cluster * 512 : 0);
   const auto kernel = palimpsa_gate_kernel<BF16, IN, GATE, CLUSTER>;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
@@ -239,7 +316,7 @@ cudaError_t run(const GateArgs& a, cudaStream_t s) {
 template <bool BF16, bool IN, bool GATE>
 cudaError_t forward(const GateArgs& given, cudaStream_t s) {
   GateArgs a = given;
-  a.cluster = gate_cluster(a.rows, a.D, GateTile<BF16>::tokens, kResident);
+  a.cluster = gate_cluster(a.rows, a.D, Tile<BF16>::tokens, kResident);
   return a.cluster > 1 ? run<BF16, IN, GATE, true>(a, s) : run<BF16, IN, GATE, false>(a, s);
 }
 

@@ -193,7 +193,8 @@ struct GateArgs {
   int D;
   bool bf16;
   unsigned int* status;
-  int cluster = 1;      // CTAs that share a sequence's time, set by plan_gate
+  int cluster = 1;      // CTAs that share a sequence's time, set by the launcher
+  unsigned long long wait_timeout_ns = 0;
   // backward
   const float* ckpt_in = nullptr;
   const void* dy = nullptr;

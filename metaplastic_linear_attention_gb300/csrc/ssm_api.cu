@@ -5,8 +5,10 @@
 
 namespace palimpsa {
 
-// api.cu: the device's status word, and scratch from the library's pool (freed with cudaFreeAsync).
+// api.cu: the device's status word, the limit of a device wait, and scratch from the library's pool (freed
+// with cudaFreeAsync).
 palimpsa_status device_status_word(unsigned int** out);
+unsigned long long wait_timeout_ns();
 cudaError_t acquire_scratch(size_t bytes, cudaStream_t s, float** p);
 
 namespace {
@@ -116,6 +118,7 @@ GateArgs gate_args(const void* x, const void* r, const float* A, const void* i, 
   a.i_bias = i_bias;
   a.D = D;
   a.bf16 = t == PALIMPSA_BF16;
+  a.wait_timeout_ns = wait_timeout_ns();
   return a;
 }
 
