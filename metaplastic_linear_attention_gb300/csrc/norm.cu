@@ -5,15 +5,17 @@
 // (ds: the gradient that reaches s past the norm; x and residual both receive ds'.)
 //
 // Bound by HBM: 4 bytes a value in bf16 (8 with a residual), backward 6 (8), against some 15 and
-// 20 operations. A thread owns 8 columns (16 for rows of more than 4096) of many rows, so
-// that weights and the parameters' sums stay in registers; a row's team of threads is
-// part of a warp (8 lanes up to 64 columns, a whole one up to 256) or a CTA. A grid of as many
-// CTAs as the GPU holds walks the rows, two at a time in bf16; the next ones come by
-// asynchronous copies into a ring in shared memory, each thread its own columns, so the
-// copies need no barrier. A forward row costs one exchange between warps: each has the
-// mean and the squares about its own mean of its part, and these are joined exactly
-// (the squares about the row's mean are those about the warp's plus count (mean_w - m)^2),
-// so nothing cancels, however far the row is off centre.
+// 20 operations. A row's team of threads, each with 1 to 8 vectors of 8 columns, is a quarter of
+// a warp (up to 64 columns), a warp (forward up to 2048, backward up to 512) or a CTA.
+// A grid of as many CTAs as the GPU holds walks the rows; the next ones come by asynchronous
+// copies into a ring in shared memory, each thread its own columns, so the copies need no barrier.
+// The squares are summed about the row's mean, which is known by then; where a row is a CTA's,
+// each warp sums them about the mean of its own part, and the parts are joined by
+//   sum (s - m)^2 = sum over warps of (sum (s - m_w)^2 + count (m_w - m)^2)
+// with one exchange, so nothing cancels, however far the row is off centre. The backward's teams
+// are wider than the forward's, since a thread keeps the parameters' sums of its columns in
+// registers over all its rows; CTAs leave theirs for a second kernel, which adds them in a fixed
+// order: no atomics, the same bits every time.
 //
 // Rounding: sums and statistics are fp32; outputs are rounded to the input type once.
 #include <algorithm>
@@ -24,21 +26,14 @@ namespace palimpsa {
 namespace {
 
 constexpr int kCols = 8, kPairs = 4;  // columns of a thread's vector
-constexpr int kWarps = 8;            // of a CTA of several teams
 
-// Rows at a time and stages of the ring: at most 192 bytes a thread and vector (and 16 to
-// spread the threads over the banks).
-template <bool BF16>
-constexpr int kRows = BF16 ? 2 : 1;
-template <int ARRAYS>
-constexpr int kRing = ARRAYS == 1 ? 4 : ARRAYS == 2 ? 3 : 2;
-
-// A thread's place: its team, its vectors' columns, the rows it walks, and its part of the
-// ring: [stage][array][row][vector][half] of 16 bytes, an odd number in all.
-template <bool BF16, int LANES, bool MULTI, int V, int ARRAYS>
+// A thread's place: its team, its vectors' columns, the rows it walks (R at a time), and its part
+// of the ring: [stage][array][row][vector][half] of 16 bytes, an odd number in all, which
+// spreads the threads over the banks.
+template <bool BF16, int LANES, bool MULTI, int V, int R_, int ARRAYS>
 struct Walk {
-  static constexpr int R = kRows<BF16>, S = kRing<ARRAYS>, H = BF16 ? 1 : 2, ES = Vec<BF16>::bytes;
-  static constexpr int planes = ARRAYS * R * V * H, units = S * planes | 1;
+  static constexpr int R = R_, H = BF16 ? 1 : 2, ES = Vec<BF16>::bytes;
+  static constexpr int planes = ARRAYS * R * V * H, S = planes <= 4 ? 4 : planes <= 6 ? 3 : 2, units = S * planes | 1;
   int t, team_size, batches, nv;
   long long rows, first, stride;  // the team's first row, and how far apart its rows are
   unsigned char* ring;
@@ -60,12 +55,15 @@ struct Walk {
   }
   __device__ __forceinline__ int col(int v) const { return (v * team_size + t) * kCols; }
   __device__ __forceinline__ bool has(int v) const { return v * team_size + t < nv; }
+  // Bytes from a vector to the thread's next.
+  __device__ __forceinline__ int across(int v) const { return v * team_size * kCols * ES; }
   // The byte offset of the team's first row, and from a row to the next, in an array.
   __device__ __forceinline__ long long start(long long ld) const { return (first * ld + t * kCols) * ES; }
   __device__ __forceinline__ long long apart(long long ld) const { return stride * ld * ES; }
   // A batch's rows of an array, from row on, p their place in the first; rows past the end as
   // zeros.
   __device__ __forceinline__ void fetch(int stage, int array, const char* p, long long next, long long row) const {
+    unsigned char* const to = ring + (stage * planes + array * R * V * H) * 16;
 #pragma unroll
     for (int j = 0; j < R; ++j) {
       const bool in = row + j * stride < rows;
@@ -74,9 +72,7 @@ struct Walk {
       for (int v = 0; v < V; ++v)
         if (has(v))
 #pragma unroll
-          for (int h = 0; h < H; ++h)
-            cp_async16(ring + (stage * planes + ((array * R + j) * V + v) * H + h) * 16,
-                       q + (long long)v * team_size * (kCols * ES) + 16 * h, in);
+          for (int h = 0; h < H; ++h) cp_async16(to + ((j * V + v) * H + h) * 16, q + across(v) + 16 * h, in);
     }
   }
   // 8 values of the ring, as pairs.
@@ -97,7 +93,7 @@ struct Walk {
         u = make_uint4(__float_as_uint(f[2 * h].x), __float_as_uint(f[2 * h].y), __float_as_uint(f[2 * h + 1].x),
                        __float_as_uint(f[2 * h + 1].y));
       }
-      if (in) *reinterpret_cast<uint4*>(p + (long long)v * team_size * (kCols * ES) + 16 * h) = u;
+      if (in) *reinterpret_cast<uint4*>(p + across(v) + 16 * h) = u;
       if (keep && BF16) unpack(u, f);
     }
   }
@@ -112,11 +108,45 @@ struct Walk {
       f[1] = make_float2(__uint_as_float(u.z), __uint_as_float(u.w));
     }
   }
-  // A thread's columns of a parameter.
-  __device__ __forceinline__ void param(const float* p, float otherwise, int v, float2* f) const {
+};
+
+// A thread's columns of a parameter vector: in registers, or, for long rows of one warp (4 vectors
+// and more), in shared memory, where all the CTA's teams read them: [half][vector][lane].
+template <int V, bool SHARED>
+struct Param {
+  float2 f[SHARED ? 1 : V][kPairs];
+  const float4* at;
+  template <class W>
+  __device__ __forceinline__ Param(const W& w, const float* p, float otherwise, float4* shared) {
+    if constexpr (SHARED) {
+      for (int k = threadIdx.x; k < V * 64; k += blockDim.x) {  // vectors' halves
+        const int c = (k >> 1) * kCols + (k & 1) * 4;
+        float4 u = make_float4(otherwise, otherwise, otherwise, otherwise);
+        if (p && c < w.nv * kCols) u = make_float4(p[c], p[c + 1], p[c + 2], p[c + 3]);
+        shared[(k & 1) * V * 32 + (k >> 1)] = u;
+      }
+      at = shared + w.t;
+    } else {
 #pragma unroll
-    for (int c = 0; c < kPairs; ++c)
-      f[c] = p && has(v) ? make_float2(p[col(v) + 2 * c], p[col(v) + 2 * c + 1]) : make_float2(otherwise, otherwise);
+      for (int v = 0; v < V; ++v)
+#pragma unroll
+        for (int c = 0; c < kPairs; ++c)
+          f[v][c] = p && w.has(v) ? make_float2(p[w.col(v) + 2 * c], p[w.col(v) + 2 * c + 1])
+                                  : make_float2(otherwise, otherwise);
+    }
+  }
+  __device__ __forceinline__ void get(int v, float2* out) const {
+    if constexpr (SHARED) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float4 u = at[(h * V + v) * 32];
+        out[2 * h] = make_float2(u.x, u.y);
+        out[2 * h + 1] = make_float2(u.z, u.w);
+      }
+    } else {
+#pragma unroll
+      for (int c = 0; c < kPairs; ++c) out[c] = f[v][c];
+    }
   }
 };
 
@@ -142,14 +172,13 @@ __device__ __forceinline__ float team_sums(float (&v)[N]) {
 // All N sums in every lane, from what team_sums left.
 template <int LANES, int N>
 __device__ __forceinline__ void spread(float mine, float (&v)[N]) {
-  const int first = (threadIdx.x & 31) & ~(LANES - 1);
+  if constexpr (N == 1) {
+    v[0] = mine;
+  } else {
+    const int first = (threadIdx.x & 31) & ~(LANES - 1);
 #pragma unroll
-  for (int k = 0; k < N; ++k) v[k] = __shfl_sync(~0u, mine, first + k * (LANES / N));
-}
-__device__ __forceinline__ float sum16(float x) {
-#pragma unroll
-  for (int d = 8; d > 0; d /= 2) x += __shfl_xor_sync(~0u, x, d);
-  return x;
+    for (int k = 0; k < N; ++k) v[k] = __shfl_sync(~0u, mine, first + k * (LANES / N));
+  }
 }
 __device__ __forceinline__ float2 two(float x) { return make_float2(x, x); }
 // 1 / sqrt(x): the SFU's, with one step of Newton's method.
@@ -158,12 +187,15 @@ __device__ __forceinline__ float rsqrt_of(float x) {
   return y * fmaf(-0.5f * x * y, y, 1.5f);
 }
 
-template <bool BF16, int LANES, bool MULTI, int V, bool RES>
-__global__ void __launch_bounds__(MULTI ? 512 : 32 * kWarps, MULTI ? 3 - V : 4) palimpsa_norm_kernel(NormArgs a) {
-  using W = Walk<BF16, LANES, MULTI, V, 1 + RES>;
-  constexpr int R = W::R;
+template <int V, bool MULTI>
+constexpr bool kSharedParams = !MULTI && V > 2;
+
+template <bool BF16, int LANES, bool MULTI, int V, int R, bool RES>
+__global__ void __launch_bounds__(MULTI ? 512 : V > 2 ? 128 : 256, MULTI ? 1 : V == 2 ? 3 : 4)
+palimpsa_norm_kernel(NormArgs a) {
+  using W = Walk<BF16, LANES, MULTI, V, R, 1 + RES>;
   extern __shared__ __align__(16) unsigned char smem[];
-  __shared__ float2 parts[2][R][16];  // of the warps: sums, and squares about their means
+  __shared__ float2 parts[2][16][R];  // of the warps: sums, and squares about their means
   const W at(a.rows, a.D, smem);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, warps = blockDim.x / 32;
   const long long nx = at.apart(a.x_ld), nr = at.apart(a.residual_ld), ny = at.apart(a.D);
@@ -174,8 +206,10 @@ __global__ void __launch_bounds__(MULTI ? 512 : 32 * kWarps, MULTI ? 3 - V : 4) 
   long long ahead = at.first, row = at.first;  // the next batch's rows to fetch, and at hand
   int to = 0;
   auto stage = [&]() {
-    at.fetch(to, 0, px, nx, ahead);
-    if (RES) at.fetch(to, 1, pr, nr, ahead);
+    if (ahead < at.rows) {
+      at.fetch(to, 0, px, nx, ahead);
+      if (RES) at.fetch(to, 1, pr, nr, ahead);
+    }
     cp_async_commit();
     px += R * nx;
     if (RES) pr += R * nr;
@@ -184,12 +218,10 @@ __global__ void __launch_bounds__(MULTI ? 512 : 32 * kWarps, MULTI ? 3 - V : 4) 
   };
 #pragma unroll
   for (int k = 0; k < W::S - 1; ++k) stage();
-  float2 wt[V][kPairs], bias[V][kPairs];
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    at.param(a.weight, 1.f, v, wt[v]);
-    at.param(a.bias, 0.f, v, bias[v]);
-  }
+  constexpr bool kShared = kSharedParams<V, MULTI>;
+  float4* const shared = reinterpret_cast<float4*>(smem + blockDim.x * W::units * 16);
+  const Param<V, kShared> weight(at, a.weight, 1.f, shared), bias(at, a.bias, 0.f, shared + V * 64);
+  if (kShared) __syncthreads();
   // Values of warp w's part of a row.
   auto count = [&](int w) {
     int n = 0;
@@ -198,8 +230,6 @@ __global__ void __launch_bounds__(MULTI ? 512 : 32 * kWarps, MULTI ? 3 - V : 4) 
     return (float)(n * kCols);
   };
   const float whole = __frcp_rn((float)a.D), own = MULTI ? __frcp_rn(count(warp)) : whole;
-  const int part = lane & 15;  // the warp whose part of a row (the second half warp: of the second row) a lane joins
-  const float parts_n = MULTI && part < warps ? count(part) : 0.f, parts_inv = parts_n ? __frcp_rn(parts_n) : 0.f;
 
   int from = 0;
   for (int b = 0; b < at.batches; ++b) {
@@ -248,30 +278,39 @@ __global__ void __launch_bounds__(MULTI ? 512 : 32 * kWarps, MULTI ? 3 - V : 4) 
     }
     const float squares = team_sums<LANES>(sq);
     if (MULTI) {
-      if (lane % (32 / R) == 0) parts[b & 1][lane / (32 / R)][warp] = make_float2(sums, squares);
+      if (lane % (32 / R) == 0) parts[b & 1][warp][lane / (32 / R)] = make_float2(sums, squares);
       __syncthreads();  // (two sets of parts: the last batch's may still be read)
-      const float2 p = part < warps ? parts[b & 1][R == 2 ? lane / 16 : 0][part] : make_float2(0.f, 0.f);
-      const float m = sum16(p.x) * whole, d = fmaf(p.x, parts_inv, -m);
-      const float q = sum16(fmaf(parts_n * d, d, p.y));
-      const float r = rsqrt_of(fmaf(q, whole, a.eps));
 #pragma unroll
       for (int j = 0; j < R; ++j) {
-        mean[j] = __shfl_sync(~0u, m, 16 * j);
-        rstd[j] = __shfl_sync(~0u, r, 16 * j);
+        float m = 0.f, q = 0.f;
+        for (int w = 0; w < warps; ++w) m += parts[b & 1][w][j].x;
+        m *= whole;
+        for (int w = 0; w < warps; ++w) {
+          const float2 p = parts[b & 1][w][j];
+          const float n = count(w), d = fmaf(p.x, __frcp_rn(n), -m);
+          q += fmaf(n * d, d, p.y);
+        }
+        mean[j] = m;
+        rstd[j] = rsqrt_of(fmaf(q, whole, a.eps));
       }
     } else {
       spread<LANES>(rsqrt_of(fmaf(squares, whole, a.eps)), rstd);
     }
 #pragma unroll
-    for (int j = 0; j < R; ++j) {
+    for (int j = 0; j < R; ++j)
       if (a.stats && live[j] && at.t == 0)
         reinterpret_cast<float2*>(a.stats)[row + j * at.stride] = make_float2(mean[j], rstd[j]);
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
+    for (int v = 0; v < V; ++v) {
+      float2 wt[kPairs], add[kPairs];
+      weight.get(v, wt);
+      bias.get(v, add);
+#pragma unroll
+      for (int j = 0; j < R; ++j) {
 #pragma unroll
         for (int c = 0; c < kPairs; ++c) {
           const float2 t = __fmul2_rn(__fadd2_rn(s[j][v][c], two(-mean[j])), two(rstd[j]));
-          s[j][v][c] = __ffma2_rn(t, wt[v][c], bias[v][c]);
+          s[j][v][c] = __ffma2_rn(t, wt[c], add[c]);
         }
         at.write(py + j * ny, v, s[j][v], live[j] && at.has(v), false);
       }
@@ -284,12 +323,12 @@ __global__ void __launch_bounds__(MULTI ? 512 : 32 * kWarps, MULTI ? 3 - V : 4) 
 }
 
 // sums: [CTAs, 2, D], the CTAs' parts of dweight and dbias, or null.
-template <bool BF16, int LANES, bool MULTI, int V, bool DS>
-__global__ void __launch_bounds__(MULTI ? 512 : 32 * kWarps, MULTI ? 3 - V : 3) palimpsa_norm_bwd_kernel(NormArgs a, float* sums) {
-  using W = Walk<BF16, LANES, MULTI, V, 2 + DS>;
-  constexpr int R = W::R;
+template <bool BF16, int LANES, bool MULTI, int V, int R, bool DS>
+__global__ void __launch_bounds__(MULTI ? 512 : 256, MULTI ? 1 : V == 2 ? 2 : 3)
+palimpsa_norm_bwd_kernel(NormArgs a, float* sums) {
+  using W = Walk<BF16, LANES, MULTI, V, R, 2 + DS>;
   extern __shared__ __align__(16) unsigned char smem[];
-  __shared__ float parts[2][2 * R][16];  // of the warps: mean(u), mean(u t), each for every row
+  __shared__ float parts[2][16][2 * R];  // of the warps: mean(u), mean(u t), each for every row
   const W at(a.rows, a.D, smem);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, warps = blockDim.x / 32;
   const long long nx = at.apart(a.x_ld), ny = at.apart(a.dy_ld), ns = at.apart(a.ds_ld), nd = at.apart(a.D);
@@ -297,13 +336,15 @@ __global__ void __launch_bounds__(MULTI ? 512 : 32 * kWarps, MULTI ? 3 - V : 3) 
   const char* py = static_cast<const char*>(a.dy) + at.start(a.dy_ld);
   const char* ps = static_cast<const char*>(a.ds) + at.start(a.ds_ld);
   char* pd = static_cast<char*>(a.dx) + at.start(a.D);
-  const float2* const stats = reinterpret_cast<const float2*>(a.stats);
+  const float2* stats = reinterpret_cast<const float2*>(a.stats) + at.first;
   long long ahead = at.first, row = at.first;
   int to = 0;
   auto stage = [&]() {
-    at.fetch(to, 0, px, nx, ahead);
-    at.fetch(to, 1, py, ny, ahead);
-    if (DS) at.fetch(to, 2, ps, ns, ahead);
+    if (ahead < at.rows) {
+      at.fetch(to, 0, px, nx, ahead);
+      at.fetch(to, 1, py, ny, ahead);
+      if (DS) at.fetch(to, 2, ps, ns, ahead);
+    }
     cp_async_commit();
     px += R * nx;
     py += R * ny;
@@ -314,22 +355,25 @@ __global__ void __launch_bounds__(MULTI ? 512 : 32 * kWarps, MULTI ? 3 - V : 3) 
   float2 next[R];  // the statistics of the next batch's rows
   auto load_stats = [&](long long r) {
 #pragma unroll
-    for (int j = 0; j < R; ++j) next[j] = r + j * at.stride < at.rows ? stats[r + j * at.stride] : make_float2(0.f, 0.f);
+    for (int j = 0; j < R; ++j) next[j] = r + j * at.stride < at.rows ? stats[j * at.stride] : make_float2(0.f, 0.f);
+    stats += R * at.stride;
   };
   load_stats(row);
 #pragma unroll
   for (int k = 0; k < W::S - 1; ++k) stage();
-  float2 wt[V][kPairs], gw[V][kPairs], gb[V][kPairs];
+  const Param<V, false> weight(at, a.weight, 1.f, nullptr);
+  float2 gw[V][kPairs], gb[V][kPairs];
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    at.param(a.weight, 1.f, v, wt[v]);
+  for (int v = 0; v < V; ++v)
 #pragma unroll
     for (int c = 0; c < kPairs; ++c) gw[v][c] = gb[v][c] = two(0.f);
-  }
   const float inv = __frcp_rn((float)a.D);
 
   int from = 0;
   for (int b = 0; b < at.batches; ++b) {
+    // (A team of a warp may have no row left while others have: it goes on, its ring then
+    // holding anything.)
+    if (MULTI && row >= at.rows) break;
     float2 st[R];
     float tot[2 * R];
     bool live[R];
@@ -342,35 +386,34 @@ __global__ void __launch_bounds__(MULTI ? 512 : 32 * kWarps, MULTI ? 3 - V : 3) 
     for (int j = 0; j < R; ++j) {
       live[j] = row + j * at.stride < at.rows;
       float2 s1 = two(0.f), s2 = two(0.f);
+      if (live[0])
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        float2 x[kPairs], dy[kPairs];
-        at.read(from, 0, j, v, x);
-        at.read(from, 1, j, v, dy);
+        for (int v = 0; v < V; ++v) {
+          float2 x[kPairs], dy[kPairs];
+          at.read(from, 0, j, v, x);
+          at.read(from, 1, j, v, dy);
 #pragma unroll
-        for (int c = 0; c < kPairs; ++c) {
-          const float2 t = __fmul2_rn(__fadd2_rn(x[c], two(-st[j].x)), two(st[j].y)), u = __fmul2_rn(dy[c], wt[v][c]);
-          gw[v][c] = __ffma2_rn(dy[c], t, gw[v][c]);
-          gb[v][c] = __fadd2_rn(gb[v][c], dy[c]);
-          s1 = __fadd2_rn(s1, u);
-          s2 = __ffma2_rn(u, t, s2);
+          for (int c = 0; c < kPairs; ++c) {
+            const float2 t = __fmul2_rn(__fadd2_rn(x[c], two(-st[j].x)), two(st[j].y)), u = __fmul2_rn(dy[c], weight.f[v][c]);
+            gw[v][c] = __ffma2_rn(dy[c], t, gw[v][c]);
+            gb[v][c] = __fadd2_rn(gb[v][c], dy[c]);
+            s1 = __fadd2_rn(s1, u);
+            s2 = __ffma2_rn(u, t, s2);
+          }
         }
-      }
       tot[2 * j] = s1.x + s1.y;
       tot[2 * j + 1] = s2.x + s2.y;
     }
     constexpr int per = LANES / (2 * R);  // lanes that share a sum
-    float mine = team_sums<LANES>(tot) * inv;
+    const float mine = team_sums<LANES>(tot) * inv;
     if (MULTI) {
-      if (lane % per == 0) parts[b & 1][lane / per][warp] = mine;
+      if (lane % per == 0) parts[b & 1][warp][lane / per] = mine;
       __syncthreads();
-      const int half = lane / 16, w = lane & 15;
 #pragma unroll
-      for (int j = 0; j < R; ++j) {  // a half warp adds up each of the row's two sums
-        const float all = sum16(w < warps ? parts[b & 1][2 * j + half][w] : 0.f);
-        tot[2 * j] = __shfl_sync(~0u, all, 0);
-        tot[2 * j + 1] = __shfl_sync(~0u, all, 16);
-      }
+      for (int j = 0; j < 2 * R; ++j) tot[j] = parts[b & 1][0][j];
+      for (int w = 1; w < warps; ++w)
+#pragma unroll
+        for (int j = 0; j < 2 * R; ++j) tot[j] += parts[b & 1][w][j];
     } else {
       spread<LANES>(mine, tot);
     }
@@ -385,7 +428,7 @@ __global__ void __launch_bounds__(MULTI ? 512 : 32 * kWarps, MULTI ? 3 - V : 3) 
 #pragma unroll
         for (int c = 0; c < kPairs; ++c) {
           const float2 t = __fmul2_rn(__fadd2_rn(x[c], two(-st[j].x)), two(st[j].y));
-          const float2 d = __ffma2_rn(t, two(-tot[2 * j + 1]), __ffma2_rn(dy[c], wt[v][c], two(-tot[2 * j])));
+          const float2 d = __ffma2_rn(t, two(-tot[2 * j + 1]), __ffma2_rn(dy[c], weight.f[v][c], two(-tot[2 * j])));
           x[c] = DS ? __ffma2_rn(two(st[j].y), d, ds[c]) : __fmul2_rn(two(st[j].y), d);
         }
         at.write(pd + j * nd, v, x, live[j] && at.has(v), false);
@@ -413,23 +456,26 @@ __global__ void __launch_bounds__(MULTI ? 512 : 32 * kWarps, MULTI ? 3 - V : 3) 
     // The CTA's teams, through the ring's memory (its copies are done: the last groups are empty).
     cp_async_wait<0>();
     float* const red = reinterpret_cast<float*>(smem);
-    const int teams = blockDim.x / LANES, team = threadIdx.x / LANES, cols = LANES * kCols;
+    constexpr int cols = LANES * kCols;
+    const int teams = blockDim.x / LANES, team = threadIdx.x / LANES;
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      __syncthreads();
+    for (int v = 0; v < V; ++v)
 #pragma unroll
-      for (int c = 0; c < kCols; ++c) {
-        const float2 g = q ? gb[0][c / 2] : gw[0][c / 2];
-        red[(team * kCols + c) * LANES + at.t] = c & 1 ? g.y : g.x;
+      for (int q = 0; q < 2; ++q) {
+        __syncthreads();
+#pragma unroll
+        for (int c = 0; c < kCols; ++c) {
+          const float2 g = q ? gb[v][c / 2] : gw[v][c / 2];
+          red[(team * kCols + c) * LANES + at.t] = c & 1 ? g.y : g.x;
+        }
+        __syncthreads();
+        for (int k = threadIdx.x; k < cols; k += blockDim.x) {
+          float s = 0.f;
+          for (int m = 0; m < teams; ++m) s += red[m * cols + k];
+          const int col = v * cols + k % LANES * kCols + k / LANES;
+          if (col < a.D) out[q * a.D + col] = s;
+        }
       }
-      __syncthreads();
-      for (int k = threadIdx.x; k < cols; k += blockDim.x) {
-        float s = 0.f;
-        for (int m = 0; m < teams; ++m) s += red[m * cols + k];
-        const int col = k % LANES * kCols + k / LANES;
-        if (col < a.D) out[q * a.D + col] = s;
-      }
-    }
   }
 }
 
@@ -442,7 +488,7 @@ __global__ void __launch_bounds__(1024) palimpsa_norm_bwd_sum_kernel(const float
   if (!out) return;
   float s = 0.f;
   if (col < D)
-#pragma unroll 4
+#pragma unroll 8
     for (int b = sy; b < rows; b += 32) s += sums[((long long)b * 2 + v) * D + col];
   red[sy][cx] = s;
   __syncthreads();
@@ -452,82 +498,104 @@ __global__ void __launch_bounds__(1024) palimpsa_norm_bwd_sum_kernel(const float
   if (cx == 0 && blockIdx.x * 32 + sy < D) out[blockIdx.x * 32 + sy] = s;
 }
 
-// Threads of a CTA and its teams for rows of D values.
+// A launch: as many CTAs as the rows need and the GPU holds.
 struct Shape {
-  int threads, teams, ctas;  // ctas: as the rows need, and the GPU holds
+  int threads, bytes, ctas;
 };
-Shape shape_of(const NormArgs& a, bool backward) {
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    sms = 152;
-  const int nv = a.D / kCols;
+template <class K>
+cudaError_t shape_of(K kernel, const NormArgs& a, int threads, int teams, int bytes, Shape* p) {
+  int dev = 0, sms = 0, held = 0;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&held, kernel, threads, bytes);
+  if (e != cudaSuccess) return e;
+  if (held < 1) return cudaErrorInvalidConfiguration;
+  *p = {threads, bytes, (int)std::max<long long>(1, std::min((long long)held * sms, (a.rows + teams - 1) / teams))};
+  return cudaSuccess;
+}
+// Threads of a CTA that a row takes for itself, each with V vectors.
+template <int V>
+int row_threads(const NormArgs& a) {
+  return (a.D / kCols + V * 32 - 1) / (V * 32) * 32;
+}
+
+template <bool BF16, int LANES, bool MULTI, int V, int R, bool MORE>
+cudaError_t forward(const NormArgs& a, cudaStream_t s) {
+  using W = Walk<BF16, LANES, MULTI, V, R, 1 + MORE>;
+  constexpr bool kShared = kSharedParams<V, MULTI>;
+  const auto kernel = palimpsa_norm_kernel<BF16, LANES, MULTI, V, R, MORE>;
+  const int threads = MULTI ? row_threads<V>(a) : kShared ? 128 : 256;
   Shape p;
-  if (nv <= 32) {
-    p.threads = 32 * kWarps;
-    p.teams = p.threads / (nv <= 8 ? 8 : 32);
-  } else {
-    const int per = nv <= 512 ? nv : (nv + 1) / 2;
-    p.threads = (per + 31) / 32 * 32;
-    p.teams = 1;
+  const cudaError_t e = shape_of(kernel, a, threads, MULTI ? 1 : threads / LANES,
+                                 threads * 16 * W::units + (kShared ? V * 2048 : 0), &p);
+  if (e != cudaSuccess) return e;
+  kernel<<<p.ctas, p.threads, p.bytes, s>>>(a);
+  return cudaGetLastError();
+}
+
+template <bool BF16, int LANES, bool MULTI, int V, int R, bool MORE>
+cudaError_t backward(const NormArgs& a, float* sums, int* ctas, cudaStream_t s) {
+  using W = Walk<BF16, LANES, MULTI, V, R, 2 + MORE>;
+  const auto kernel = palimpsa_norm_bwd_kernel<BF16, LANES, MULTI, V, R, MORE>;
+  const int threads = MULTI ? row_threads<V>(a) : 256;
+  Shape p;
+  const cudaError_t e = shape_of(kernel, a, threads, MULTI ? 1 : threads / LANES, threads * 16 * W::units, &p);
+  if (e != cudaSuccess) return e;
+  if (ctas) {
+    *ctas = p.ctas;
+    return cudaSuccess;
   }
-  // (The backward of narrow rows needs 80 registers a thread, the others 64.)
-  const int per_sm = backward && p.teams > 1 ? 768 : 1024;
-  const long long held = (long long)std::max(1, per_sm / p.threads) * sms;
-  p.ctas = (int)std::min(held, (a.rows + p.teams - 1) / p.teams);
-  return p;
-}
-
-template <bool BF16, int LANES, bool MULTI, int V, bool MORE>
-cudaError_t run_forward(const NormArgs& a, const Shape& p, cudaStream_t s) {
-  using W = Walk<BF16, LANES, MULTI, V, 1 + MORE>;
-  const int bytes = p.threads * 16 * W::units;
-  const auto kernel = palimpsa_norm_kernel<BF16, LANES, MULTI, V, MORE>;
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e != cudaSuccess) return e;
-  kernel<<<p.ctas, p.threads, bytes, s>>>(a);
+  kernel<<<p.ctas, p.threads, p.bytes, s>>>(a, sums);
   return cudaGetLastError();
 }
 
-template <bool BF16, int LANES, bool MULTI, int V, bool MORE>
-cudaError_t run_backward(const NormArgs& a, const Shape& p, float* sums, cudaStream_t s) {
-  using W = Walk<BF16, LANES, MULTI, V, 2 + MORE>;
-  const int bytes = p.threads * 16 * W::units;
-  const auto kernel = palimpsa_norm_bwd_kernel<BF16, LANES, MULTI, V, MORE>;
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e != cudaSuccess) return e;
-  kernel<<<p.ctas, p.threads, bytes, s>>>(a, sums);
-  return cudaGetLastError();
+template <bool BF16, bool MORE>
+cudaError_t forward_by_width(const NormArgs& a, cudaStream_t s) {
+  if (a.D <= 64) return forward<BF16, 8, false, 1, 2, MORE>(a, s);
+  if (a.D <= 256) return forward<BF16, 32, false, 1, 2, MORE>(a, s);
+  if (a.D <= 512) return forward<BF16, 32, false, 2, 2, MORE>(a, s);
+  if (a.D <= 1024) return forward<BF16, 32, false, 4, 1, MORE>(a, s);
+  if (a.D <= 1536) return forward<BF16, 32, false, 6, 1, MORE>(a, s);
+  if (a.D <= 2048) return forward<BF16, 32, false, 8, 1, MORE>(a, s);
+  return forward<BF16, 32, true, 2, BF16 ? 2 : 1, MORE>(a, s);
+}
+template <bool BF16, bool MORE>
+cudaError_t backward_by_width(const NormArgs& a, float* sums, int* ctas, cudaStream_t s) {
+  if (a.D <= 64) return backward<BF16, 8, false, 1, BF16 ? 2 : 1, MORE>(a, sums, ctas, s);
+  if (a.D <= 256) return backward<BF16, 32, false, 1, BF16 ? 2 : 1, MORE>(a, sums, ctas, s);
+  if (a.D <= 512) return backward<BF16, 32, false, 2, BF16 ? 2 : 1, MORE>(a, sums, ctas, s);
+  return backward<BF16, 32, true, 2, BF16 ? 2 : 1, MORE>(a, sums, ctas, s);
+}
+cudaError_t backward_any(const NormArgs& a, float* sums, int* ctas, cudaStream_t s) {
+  if (a.bf16) return a.ds ? backward_by_width<true, true>(a, sums, ctas, s) : backward_by_width<true, false>(a, sums, ctas, s);
+  return a.ds ? backward_by_width<false, true>(a, sums, ctas, s) : backward_by_width<false, false>(a, sums, ctas, s);
 }
 
 }  // namespace
 
-#define PALIMPSA_NORM_TEAM(f, BF16, MORE, ...)                                                    \
-  (a.D <= 64 ? f<BF16, 8, false, 1, MORE>(__VA_ARGS__)                                            \
-   : a.D <= 256 ? f<BF16, 32, false, 1, MORE>(__VA_ARGS__)                                        \
-   : a.D <= 4096 ? f<BF16, 32, true, 1, MORE>(__VA_ARGS__) : f<BF16, 32, true, 2, MORE>(__VA_ARGS__))
-#define PALIMPSA_NORM_DISPATCH(f, more, ...)                                                      \
-  (a.bf16 ? ((more) ? PALIMPSA_NORM_TEAM(f, true, true, __VA_ARGS__) : PALIMPSA_NORM_TEAM(f, true, false, __VA_ARGS__)) \
-          : ((more) ? PALIMPSA_NORM_TEAM(f, false, true, __VA_ARGS__) : PALIMPSA_NORM_TEAM(f, false, false, __VA_ARGS__)))
-
 cudaError_t launch_norm_forward(const NormArgs& a, cudaStream_t s) {
   if (a.rows == 0) return cudaSuccess;
-  const Shape p = shape_of(a, false);
-  return PALIMPSA_NORM_DISPATCH(run_forward, a.residual, a, p, s);
+  if (a.bf16) return a.residual ? forward_by_width<true, true>(a, s) : forward_by_width<true, false>(a, s);
+  return a.residual ? forward_by_width<false, true>(a, s) : forward_by_width<false, false>(a, s);
 }
 
-size_t norm_backward_scratch_floats(const NormArgs& a) {
-  return a.dweight || a.dbias ? (size_t)shape_of(a, true).ctas * 2 * a.D : 0;
+cudaError_t plan_norm_backward(NormArgs* a, size_t* floats) {
+  *floats = 0;
+  a->ctas = 0;
+  if (a->rows == 0) return cudaSuccess;
+  const cudaError_t e = backward_any(*a, nullptr, &a->ctas, nullptr);
+  if (a->dweight || a->dbias) *floats = (size_t)a->ctas * 2 * a->D;
+  return e;
 }
 
 cudaError_t launch_norm_backward(const NormArgs& a, float* scratch, cudaStream_t s) {
-  const Shape p = shape_of(a, true);
   if (a.rows > 0) {
-    const cudaError_t e = PALIMPSA_NORM_DISPATCH(run_backward, a.ds, a, p, scratch, s);
+    const cudaError_t e = backward_any(a, scratch, nullptr, s);
     if (e != cudaSuccess) return e;
   }
   if (!a.dweight && !a.dbias) return cudaSuccess;
-  palimpsa_norm_bwd_sum_kernel<<<dim3((a.D + 31) / 32, 2), 1024, 0, s>>>(scratch, a.rows > 0 ? p.ctas : 0, a.D,
-                                                                         a.dweight, a.dbias);
+  palimpsa_norm_bwd_sum_kernel<<<dim3((a.D + 31) / 32, 2), 1024, 0, s>>>(scratch, a.ctas, a.D, a.dweight, a.dbias);
   return cudaGetLastError();
 }
 

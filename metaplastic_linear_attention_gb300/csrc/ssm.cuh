@@ -249,10 +249,11 @@ struct NormArgs {
   float* dweight = nullptr;
   float* dbias = nullptr;
   long long dy_ld = 0, ds_ld = 0;
+  int ctas = 0;
 };
 cudaError_t launch_norm_forward(const NormArgs& a, cudaStream_t s);
-// Backward: scratch of norm_backward_scratch_floats() holds every CTA's sums of the parameters' gradients.
-size_t norm_backward_scratch_floats(const NormArgs& a);
+// Backward: sets a->ctas and the scratch that holds every CTA's sums of the parameters' gradients.
+cudaError_t plan_norm_backward(NormArgs* a, size_t* floats);
 cudaError_t launch_norm_backward(const NormArgs& a, float* scratch, cudaStream_t s);
 
 #if defined(__CUDACC__)

@@ -507,8 +507,9 @@ palimpsa_status palimpsa_layer_norm_backward(const void* s, long long s_stride, 
   if (palimpsa_status e = stride_of(ds_stride, D, in_dtype, &a.ds_ld)) return e;
   const cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
   float* scratch = nullptr;
-  const size_t bytes = norm_backward_scratch_floats(a) * sizeof(float);
-  if (bytes && acquire_scratch(bytes, stream, &scratch) != cudaSuccess) return PALIMPSA_ERR_CUDA;
+  size_t floats = 0;
+  if (plan_norm_backward(&a, &floats) != cudaSuccess) return PALIMPSA_ERR_CUDA;
+  if (floats && acquire_scratch(floats * sizeof(float), stream, &scratch) != cudaSuccess) return PALIMPSA_ERR_CUDA;
   return release(launch_norm_backward(a, scratch, stream), scratch, stream);
 }
 
