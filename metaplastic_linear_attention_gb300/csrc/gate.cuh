@@ -8,28 +8,29 @@
 
 namespace palimpsa {
 
-// A tile is 64 channels by a piece of 8 tokens for each of the CTA's groups of threads: half
-// warps in the forward (a lane holds 4 channels), warps in the backward (2).
-constexpr int kPiece = kGateCheckpoint;
-constexpr int kGateChannels = 64;
-constexpr int kGateCluster = 8;  // CTAs of a cluster, at most (the portable limit)
+constexpr int kPiece = kGateCheckpoint;  // tokens that a group of threads holds
+constexpr int kGateCluster = 8;          // CTAs of a cluster, at most (the portable limit)
 
-template <bool BF16, int PIECES, int THREADS>
+// A tile of CH channels by a piece of tokens for each of the CTA's groups of threads, CPT
+// channels a thread.
+template <bool BF16, int CH_, int CPT, int THREADS>
 struct GateTile {
-  static constexpr int ES = BF16 ? 2 : 4;
-  static constexpr int pieces = PIECES, threads = THREADS;
-  static constexpr int tokens = kPiece * PIECES;
-  static constexpr int row = kGateChannels * ES;      // bytes of a row
+  static constexpr int ES = BF16 ? 2 : 4, CH = CH_;
+  static constexpr int group = CH / CPT, pieces = THREADS / group, threads = THREADS;
+  static constexpr int tokens = kPiece * pieces;
+  static constexpr int row = CH * ES;                 // bytes of a row
   static constexpr int bytes = tokens * row;          // of an array
   static constexpr int vecs = row / 16;               // 16-byte vectors of a row
   static constexpr int rows_at_once = threads / vecs; // rows that the CTA's threads copy in turn
   static_assert(tokens % rows_at_once == 0, "whole turns");
 };
 
-inline long long gate_tiles(int D) { return (D + kGateChannels - 1) / kGateChannels; }
-
-// CTAs of a cluster for tiles of `tokens` tokens, `slots` CTAs at once on the GPU.
-int gate_cluster(const SeqRows& r, int D, int tokens, long long slots);
+// How a batch is shared out: channels of a tile, and CTAs along time (a cluster's).
+struct GatePlan {
+  int channels, cluster;
+};
+// `tokens` of a CTA's tile of 64 channels (twice as many at 32), `resident` CTAs on an SM.
+GatePlan gate_plan(const SeqRows& r, int D, int tokens, int resident);
 
 #if defined(__CUDACC__)
 

@@ -27,15 +27,14 @@ constexpr int kResident = 2;  // CTAs of an SM
 
 // Warps a CTA: in fp32 half as many, whose rows are twice as long.
 template <bool BF16>
-using Tile = GateTile<BF16, BF16 ? 8 : 4, BF16 ? 256 : 128>;
+using Tile = GateTile<BF16, 64, 2, BF16 ? 256 : 128>;
 
 // Shared memory: the ring of raw inputs (and the states before the pieces), then the pieces' and
 // the ranks' summaries.
-template <bool BF16, bool IN, bool GATE, bool CLUSTER>
+template <bool BF16, bool IN, bool GATE>
 struct BwdSmem {
-  static constexpr int h = (3 + IN + GATE) * Tile<BF16>::bytes, stage = h + Tile<BF16>::pieces * kGateChannels * 4;
+  static constexpr int h = (3 + IN + GATE) * Tile<BF16>::bytes, stage = h + Tile<BF16>::pieces * Tile<BF16>::CH * 4;
   static constexpr int agg = 2 * stage, ranks = agg + Tile<BF16>::pieces * 512;
-  static constexpr int total = ranks + CLUSTER * 2 * kGateCluster * 512;
 };
 
 // sums: [n_seq, cluster, 3, D], the CTAs' parts of dA, dr_bias and di_bias.
@@ -43,7 +42,7 @@ template <bool BF16, bool IN, bool GATE, bool CLUSTER>
 __global__ void __launch_bounds__(Tile<BF16>::threads, BF16 ? kResident : 2 * kResident)
 palimpsa_gate_bwd_kernel(GateArgs a, int tiles, float* sums) {
   using G = Tile<BF16>;
-  using S = BwdSmem<BF16, IN, GATE, CLUSTER>;
+  using S = BwdSmem<BF16, IN, GATE>;
   constexpr int ES = G::ES, RT = G::tokens, NP = G::pieces;
   constexpr int kI = 3, kZ = 3 + IN;  // places of the arrays x, r, dy, i, z
   extern __shared__ __align__(128) unsigned char smem[];
@@ -53,7 +52,7 @@ palimpsa_gate_bwd_kernel(GateArgs a, int tiles, float* sums) {
   const int cs = CLUSTER ? a.cluster : 1;
   const int rank = CLUSTER ? (int)(blockIdx.x % cs) : 0;
   const long long rest = CLUSTER ? blockIdx.x / cs : blockIdx.x;
-  const int ch0 = (int)(rest % tiles) * kGateChannels, ch = ch0 + 2 * lane;
+  const int ch0 = (int)(rest % tiles) * Tile<BF16>::CH, ch = ch0 + 2 * lane;
   const bool in = ch < a.D;
   const long long n = rest / tiles;
   const float2 zero = make_float2(0.f, 0.f);
@@ -125,7 +124,7 @@ palimpsa_gate_bwd_kernel(GateArgs a, int tiles, float* sums) {
     float2 da[kPiece], fx[kPiece], fi[IN ? kPiece : 1], fr[kPiece], fA[kPiece], gy[kPiece];
     const long long at = (row0 + tp) * a.D + ch;
     float2 h = np > 0 ? *reinterpret_cast<const float2*>(smem + (k & 1) * S::stage + S::h +
-                                                         (warp * kGateChannels + 2 * lane) * 4)
+                                                         (warp * Tile<BF16>::CH + 2 * lane) * 4)
                       : zero;
 #pragma unroll
     for (int t = 0; t < kPiece; ++t) {
@@ -189,7 +188,7 @@ palimpsa_gate_bwd_kernel(GateArgs a, int tiles, float* sums) {
         carry = ffma2(make_float2(e.x, e.y), carry, make_float2(e.z, e.w));
       }
     } else {
-      float4* const slots = reinterpret_cast<float4*>(smem + S::ranks + (k & 1) * kGateCluster * 512);
+      float4* const slots = reinterpret_cast<float4*>(smem + S::ranks + (k & 1) * cs * 512);
       for (int q = warp; q < cs; q += NP) {
         float2 Pc = make_float2(1.f, 1.f), Cc = zero;
 #pragma unroll
@@ -278,11 +277,12 @@ __global__ void __launch_bounds__(256) palimpsa_gate_bwd_sum_kernel(const float*
 template <bool BF16, bool IN, bool GATE, bool CLUSTER>
 cudaError_t run(const GateArgs& a, float* sums, cudaStream_t s) {
   using G = Tile<BF16>;
-  const long long tiles = gate_tiles(a.D), blocks = tiles * a.rows.n_seq * a.cluster;
+  const long long tiles = (a.D + G::CH - 1) / G::CH, blocks = tiles * a.rows.n_seq * a.cluster;
   if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
-  constexpr int bytes = BwdSmem<BF16, IN, GATE, CLUSTER>::total;
+  const int bytes = BwdSmem<BF16, IN, GATE>::ranks + (CLUSTER ? 2 * a.cluster * 512 : 0);
   const auto kernel = palimpsa_gate_bwd_kernel<BF16, IN, GATE, CLUSTER>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && a.cluster > 8) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute cluster = {};
   cluster.id = cudaLaunchAttributeClusterDimension;
@@ -310,8 +310,8 @@ cudaError_t backward(const GateArgs& a, float* sums, cudaStream_t s) {
 }  // namespace
 
 size_t plan_gate_backward(GateArgs* a) {
-  a->cluster = a->bf16 ? gate_cluster(a->rows, a->D, Tile<true>::tokens, kResident)
-                       : gate_cluster(a->rows, a->D, Tile<false>::tokens, 2 * kResident);
+  a->cluster = a->bf16 ? gate_plan(a->rows, a->D, Tile<true>::tokens, kResident).cluster
+                       : gate_plan(a->rows, a->D, Tile<false>::tokens, 2 * kResident).cluster;
   return (size_t)a->rows.n_seq * a->cluster * 3 * a->D;
 }
 

@@ -10,8 +10,9 @@
 // operations. So every input is read once: a thread takes 8 tokens of 4 channels (a piece),
 // forms their decays and inputs a, b in registers, and runs them twice, first from 0 for
 // the piece's summary (the product of its a and its end state), then, with the state
-// before the piece known, for the states themselves. The summaries of a CTA's pieces (its
-// half warps, along time) pass through shared memory, and those of a cluster's CTAs
+// before the piece known, for the states themselves. (4 tokens and twice the threads took 1.3
+// times as long: what a round costs a thread besides its tokens is a fifth of it.) The
+// summaries of a CTA's pieces (groups of 16 or 8 threads, along time) pass through shared memory, and those of a cluster's CTAs
 // through each other's shared memory, as asynchronous stores that a barrier there counts;
 // every thread folds the ones before its own. A CTA walks its sequence in rounds of
 // such tiles, the next round's inputs coming by asynchronous copies meanwhile, and
@@ -19,6 +20,7 @@
 //
 // Rounding: gates, decays and states are fp32; y is rounded to the input type once.
 #include <algorithm>
+#include <cmath>
 
 #include "gate.cuh"
 
@@ -29,15 +31,17 @@ namespace cg = cooperative_groups;
 
 constexpr int kResident = 4;  // CTAs of an SM
 
-// Half warps a CTA: in fp32 half as many, whose rows are twice as long.
-template <bool BF16>
-using Tile = GateTile<BF16, BF16 ? 8 : 4, BF16 ? 128 : 64>;
+// Tiles of 64 channels, or 32 where those are too few; in fp32 half the threads, since rows are
+// twice as long.
+template <bool BF16, int CH>
+using Tile = GateTile<BF16, CH, 4, BF16 ? 128 : 64>;
 
 // Shared memory: two stages of x, r and i, then two sets of the ranks' summaries,
-// [rank][products, states][16 lanes] of 4 channels. A piece's summary takes the place of its
-// first rows of x.
+// [rank][products, states][lanes of a group] of 4 channels. A piece's summary takes the place of
+// its first rows of x. Where rows are 64 bytes, those of odd pieces change places in pairs, so
+// that the two that a half warp reads at once lie in different banks.
 template <bool BF16, bool IN>
-constexpr int kStageBytes = (2 + IN) * Tile<BF16>::bytes;
+constexpr int kStageBytes = (2 + IN) * Tile<BF16, 64>::bytes;  // the same for 32
 
 // h <- P h + H over 4 channels.
 struct Four {
@@ -54,20 +58,19 @@ struct Four {
 };
 __device__ __forceinline__ Four four(float v) { return {make_float2(v, v), make_float2(v, v)}; }
 
-template <bool BF16, bool IN, bool GATE, bool CLUSTER>
-__global__ void __launch_bounds__(Tile<BF16>::threads, kResident)
-palimpsa_gate_kernel(GateArgs a, int tiles) {
-  using G = Tile<BF16>;
+template <bool BF16, bool IN, bool GATE, bool CLUSTER, int CH>
+__global__ void __launch_bounds__(BF16 ? 128 : 64, kResident) palimpsa_gate_kernel(GateArgs a, int tiles) {
+  using G = Tile<BF16, CH>;
   using Q = Quad<BF16>;
   using Raw = typename Q::Raw;
-  constexpr int ES = G::ES, RT = G::tokens, NP = G::pieces, kStage = kStageBytes<BF16, IN>;
+  constexpr int ES = G::ES, RT = G::tokens, NP = G::pieces, LG = G::group, kStage = kStageBytes<BF16, IN>;
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ uint64_t bars[2];
-  const int tid = threadIdx.x, piece = tid >> 4, lane = tid & 15;
+  const int tid = threadIdx.x, piece = tid / LG, lane = tid % LG;
   const int cs = CLUSTER ? a.cluster : 1;
   const int rank = CLUSTER ? (int)(blockIdx.x % cs) : 0;
   const long long rest = CLUSTER ? blockIdx.x / cs : blockIdx.x;
-  const int ch0 = (int)(rest % tiles) * kGateChannels, ch = ch0 + 4 * lane;
+  const int ch0 = (int)(rest % tiles) * CH, ch = ch0 + 4 * lane;
   const bool in = ch < a.D;
   const long long n = rest / tiles;
   long long row0;
@@ -81,11 +84,14 @@ palimpsa_gate_kernel(GateArgs a, int tiles) {
   // Copies of a round's x, r and i, as one group: a thread takes the same vector of rows
   // rows_at_once apart. Rows past the end and channels past D are left as they are.
   const int vec = tid % G::vecs, vrow = tid / G::vecs;
+  constexpr bool kFlip = G::row == 64;
+  static_assert(!kFlip || G::rows_at_once % (2 * kPiece) == 0, "a thread's rows are all of odd or all of even pieces");
+  const int flip = kFlip ? (vrow / kPiece) & 1 : 0, slot0 = ((vrow ^ flip) * G::vecs + vec) * 16;
   const bool vin = ch0 * ES + vec * 16 < a.D * ES;
   auto stage = [&](int k) {
     const int t0 = k * step + rank * RT, nt = min(RT, len - t0);
     if (k < rounds && vin) {
-      unsigned char* const to = smem + (k & 1) * kStage + tid * 16;
+      unsigned char* const to = smem + (k & 1) * kStage + slot0;
       const long long first = row0 + t0 + vrow, col = (long long)ch0 * ES + vec * 16;
       auto copy = [&](const void* from, long long ld, int slot) {
         const char* p = static_cast<const char*>(from) + first * ld * ES + col;
@@ -133,19 +139,20 @@ palimpsa_gate_kernel(GateArgs a, int tiles) {
     const int np = min(kPiece, len - tp);                  // its tokens (0 or less: none)
     unsigned char* const tile = smem + (k & 1) * kStage;
     const unsigned char* const raw = tile + piece * kPiece * G::row + lane * 4 * ES;
+    const int odd = kFlip ? piece & 1 : 0;
     // A piece's summary: products and states of the lane's channels.
     auto sums_of = [&](int p) { return reinterpret_cast<float4*>(tile + p * kPiece * G::row) + lane; };
     cp_async_wait<0>();
-    if (CLUSTER && tid == 0) mbar_arrive_expect_tx(&bars[k & 1], cs * 512);
+    if (CLUSTER && tid == 0) mbar_arrive_expect_tx(&bars[k & 1], cs * LG * 32);
     __syncthreads();  // the round's inputs are here; the other stage and the summaries are free
     stage(k + 1);
 
     float2 da[kPiece][2], b[kPiece][2];
     auto token = [&](int t) {
       float2 x[2], r[2], i[2];
-      Q::unpack(*reinterpret_cast<const Raw*>(raw + t * G::row), x);
-      Q::unpack(*reinterpret_cast<const Raw*>(raw + G::bytes + t * G::row), r);
-      if (IN) Q::unpack(*reinterpret_cast<const Raw*>(raw + 2 * G::bytes + t * G::row), i);
+      Q::unpack(*reinterpret_cast<const Raw*>(raw + (t ^ odd) * G::row), x);
+      Q::unpack(*reinterpret_cast<const Raw*>(raw + G::bytes + (t ^ odd) * G::row), r);
+      if (IN) Q::unpack(*reinterpret_cast<const Raw*>(raw + 2 * G::bytes + (t ^ odd) * G::row), i);
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const float2 s = sigmoid_of(ffma2(r[j], make_float2(-kLog2e, -kLog2e), rb[j]));
@@ -176,7 +183,7 @@ palimpsa_gate_kernel(GateArgs a, int tiles) {
       }
     __syncwarp();  // the piece's rows of x are read
     sums_of(piece)[0] = P.all();
-    sums_of(piece)[16] = H.all();
+    sums_of(piece)[LG] = H.all();
     Raw z[kPiece];  // on their way during the exchange
     if (GATE && in) {
       const char* p = static_cast<const char*>(a.z) + ((row0 + tp) * a.z_ld + ch) * ES;
@@ -192,29 +199,29 @@ palimpsa_gate_kernel(GateArgs a, int tiles) {
 #pragma unroll
       for (int q = 0; q < NP; ++q) {
         if (q == piece) h = carry;
-        carry.fold(sums_of(q)[0], sums_of(q)[16]);
+        carry.fold(sums_of(q)[0], sums_of(q)[LG]);
       }
     } else {
       // Group q sends the CTA's summary to rank q. (Two sets of slots: a rank may be a round ahead.)
-      float4* const slots = reinterpret_cast<float4*>(smem + 2 * kStage + (k & 1) * cs * 512) + lane;
+      float4* const slots = reinterpret_cast<float4*>(smem + 2 * kStage + (k & 1) * cs * LG * 32) + lane;
       for (int q = piece; q < cs; q += NP) {
         Four Pc = four(1.f), Hc = four(0.f);
 #pragma unroll
         for (int w = 0; w < NP; ++w) {
-          Hc.fold(sums_of(w)[0], sums_of(w)[16]);
+          Hc.fold(sums_of(w)[0], sums_of(w)[LG]);
           Pc.times(sums_of(w)[0]);
         }
-        const uint32_t to = cluster_addr(slots + rank * 32, q), bar = cluster_addr(&bars[k & 1], q);
+        const uint32_t to = cluster_addr(slots + rank * 2 * LG, q), bar = cluster_addr(&bars[k & 1], q);
         st_async(to, Pc.all(), bar);
-        st_async(to + 256, Hc.all(), bar);
+        st_async(to + LG * 16, Hc.all(), bar);
       }
       waits = waits && cluster_wait(&bars[k & 1], (k >> 1) & 1, a.wait_timeout_ns);
       if (!waits) latch_status(a.status, kStatusTimeout);
       int q = 0;
-      for (; q < rank; ++q) carry.fold(slots[q * 32], slots[q * 32 + 16]);
+      for (; q < rank; ++q) carry.fold(slots[q * 2 * LG], slots[(q * 2 + 1) * LG]);
       h = carry;
-      for (; q < cs; ++q) carry.fold(slots[q * 32], slots[q * 32 + 16]);
-      for (int w = 0; w < piece; ++w) h.fold(sums_of(w)[0], sums_of(w)[16]);
+      for (; q < cs; ++q) carry.fold(slots[q * 2 * LG], slots[(q * 2 + 1) * LG]);
+      for (int w = 0; w < piece; ++w) h.fold(sums_of(w)[0], sums_of(w)[LG]);
     }
     if (in && np > 0) {
       if (a.ckpt)
@@ -290,13 +297,13 @@ __global__ void __launch_bounds__(128) palimpsa_gate_step_kernel(GateArgs a) {
   if (bad) latch_status(a.status, kStatusDomain);
 }
 
-template <bool BF16, bool IN, bool GATE, bool CLUSTER>
+template <bool BF16, bool IN, bool GATE, bool CLUSTER, int CH>
 cudaError_t run(const GateArgs& a, cudaStream_t s) {
-  using G = Tile<BF16>;
-  const long long tiles = gate_tiles(a.D), blocks = tiles * a.rows.n_seq * a.cluster;
+  using G = Tile<BF16, CH>;
+  const long long tiles = (a.D + CH - 1) / CH, blocks = tiles * a.rows.n_seq * a.cluster;
   if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
-  const int bytes = 2 * kStageBytes<BF16, IN> + (CLUSTER ? 2 * a.cluster * 512 : 0);
-  const auto kernel = palimpsa_gate_kernel<BF16, IN, GATE, CLUSTER>;
+  const int bytes = 2 * kStageBytes<BF16, IN> + (CLUSTER ? 2 * a.cluster * G::group * 32 : 0);
+  const auto kernel = palimpsa_gate_kernel<BF16, IN, GATE, CLUSTER, CH>;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute cluster = {};
@@ -316,8 +323,11 @@ cudaError_t run(const GateArgs& a, cudaStream_t s) {
 template <bool BF16, bool IN, bool GATE>
 cudaError_t forward(const GateArgs& given, cudaStream_t s) {
   GateArgs a = given;
-  a.cluster = gate_cluster(a.rows, a.D, Tile<BF16>::tokens, kResident);
-  return a.cluster > 1 ? run<BF16, IN, GATE, true>(a, s) : run<BF16, IN, GATE, false>(a, s);
+  const GatePlan p = gate_plan(a.rows, a.D, Tile<BF16, 64>::tokens, kResident);
+  a.cluster = p.cluster;
+  if (p.channels == 32)
+    return a.cluster > 1 ? run<BF16, IN, GATE, true, 32>(a, s) : run<BF16, IN, GATE, false, 32>(a, s);
+  return a.cluster > 1 ? run<BF16, IN, GATE, true, 64>(a, s) : run<BF16, IN, GATE, false, 64>(a, s);
 }
 
 template <bool BF16, bool IN, bool GATE>
@@ -330,24 +340,34 @@ cudaError_t step(const GateArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-// The cheapest of 1, 2, 4 and 8 CTAs a cluster. The GPU's rounds: every tile of every sequence
-// takes its tokens in rounds of cluster x `tokens`, `resident` CTAs an SM at once; and no
-// batch is faster than its longest sequence's rounds, one after the other, each with its
-// exchange. (What is left of a round costs as much as a whole one.)
-int gate_cluster(const SeqRows& r, int D, int tokens, long long resident) {
+// The cheapest of 1 to 8 CTAs a cluster and of 64 or 32 channels a tile. A round of a CTA with
+// c CTAs on its SM took 0.9 + 0.78 c us in bf16 (8 x 4096 x 1536: 108 us with 192 CTAs of 64 rounds,
+// 93 with 384 of 32, 83 with 576 of 22, 96 with 768 of 16, which is a wave of 608 and a rest,
+// 111 with 1536), and a CTA costs some 1.5 rounds besides. The last wave has as many CTAs an SM
+// as are left. A tile of 32 channels has twice the pieces to fold: 6 % more. A packed batch's
+// CTAs have the mean of the rounds (and half of one lost), but none is done before its
+// longest sequence's rounds, one after the other.
+GatePlan gate_plan(const SeqRows& r, int D, int tokens, int resident) {
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     sms = 152;
-  const long long slots = resident * sms, tiles = gate_tiles(D);
-  int best = 1;
-  long long least = 0;
-  for (int cs = 1; cs <= kGateCluster; cs *= 2) {
-    const long long per = (long long)cs * tokens, longest = (r.max_len + per - 1) / per;
-    const long long all = r.cu ? cs * (r.T / per + r.n_seq) : cs * longest * r.n_seq;  // CTA rounds, a tile
-    const long long cost = std::max((all * tiles + slots - 1) / slots, longest);
-    if (cs == 1 || cost < least) {
-      best = cs;
-      least = cost;
+  const double slots = (double)resident * sms;
+  GatePlan best = {64, 1};
+  double least = 0;
+  for (int ch = 64; ch >= 32; ch /= 2) {
+    const double tiles = (D + ch - 1) / ch;
+    for (int cs = 1; cs <= kGateCluster; ++cs) {
+      const long long per = (long long)cs * tokens * (64 / ch);
+      const double longest = (double)((r.max_len + per - 1) / per);
+      const double rounds = r.cu ? std::min(longest, (double)r.T / per / r.n_seq + 0.5) : longest;
+      const double ctas = tiles * r.n_seq * cs, waves = std::floor(ctas / slots), rest = ctas - waves * slots;
+      const double full = 0.9 + 0.78 * resident, some = 0.9 + 0.78 * rest / sms;
+      double cost = (rounds + 1.5) * (waves * full + (rest > 0 ? some : 0));
+      cost = std::max(cost, (longest + 1.5) * (waves >= 1 ? full : some)) * (ch == 64 ? 1 : 1.06);
+      if ((ch == 64 && cs == 1) || cost < least) {
+        best = {ch, cs};
+        least = cost;
+      }
     }
   }
   return best;

@@ -5,7 +5,7 @@
 // (ds: the gradient that reaches s past the norm; x and residual both receive ds'.)
 //
 // Bound by HBM: 4 bytes a value in bf16 (8 with a residual), backward 6 (8), against some 15 and
-// 20 operations. A row's team of threads, each with 1 to 8 vectors of 8 columns, is a quarter of
+// 20 operations. A row's team of threads, each with 8 to 64 columns, is a quarter of
 // a warp (up to 64 columns), a warp (forward up to 2048, backward up to 512) or a CTA.
 // A grid of as many CTAs as the GPU holds walks the rows; the next ones come by asynchronous
 // copies into a ring in shared memory, each thread its own columns, so the copies need no barrier.
@@ -25,77 +25,68 @@
 namespace palimpsa {
 namespace {
 
-constexpr int kCols = 8, kPairs = 4;  // columns of a thread's vector
-
-// A thread's place: its team, its vectors' columns, the rows it walks (R at a time), and its part
-// of the ring: [stage][array][row][vector][half] of 16 bytes, an odd number in all, which
-// spreads the threads over the banks.
-template <bool BF16, int LANES, bool MULTI, int V, int R_, int ARRAYS>
+// A thread's place: its team, the rows it walks (R at a time), its columns (V vectors of 16 bytes,
+// a team's width apart), and its part of the ring, [stage][array][row][vector][thread]: lanes
+// that are neighbours in HBM are so there too (with each thread's vectors next to each other
+// in the ring instead, a copy asks for every sector twice: 88 us against 71 at 32768 x 1536 with a
+// residual).
+template <bool BF16, int LANES, bool MULTI, int COLS, int R_, int ARRAYS>
 struct Walk {
-  static constexpr int R = R_, H = BF16 ? 1 : 2, ES = Vec<BF16>::bytes;
-  static constexpr int planes = ARRAYS * R * V * H, S = planes <= 4 ? 4 : planes <= 6 ? 3 : 2, units = S * planes | 1;
+  static constexpr int R = R_, ES = Vec<BF16>::bytes, N = Vec<BF16>::n, V = COLS / N, P = N / 2;  // P: pairs of a vector
+  static constexpr int planes = ARRAYS * R * V, S = planes <= 4 ? 4 : planes <= 6 ? 3 : 2;
   int t, team_size, batches, nv;
   long long rows, first, stride;  // the team's first row, and how far apart its rows are
   unsigned char* ring;
-  __device__ __forceinline__ Walk(long long rows_, int D, unsigned char* smem) : nv(D / kCols), rows(rows_) {
+  __device__ __forceinline__ Walk(long long rows_, int D, unsigned char* smem) : nv(D / N), rows(rows_) {
     const int tid = threadIdx.x, teams = MULTI ? 1 : blockDim.x / LANES;
     t = MULTI ? tid : tid % LANES;
     team_size = MULTI ? blockDim.x : LANES;
     first = (long long)blockIdx.x * teams + (MULTI ? 0 : tid / LANES);
     stride = (long long)gridDim.x * teams;
     batches = (int)((rows + stride * R - 1) / (stride * R));  // the same for every team
-    ring = smem + tid * units * 16;
+    ring = smem + tid * 16;
     // Columns past D are zeros: no copy goes there.
 #pragma unroll
     for (int v = 0; v < V; ++v)
       if (!has(v))
-        for (int k = 0; k < S * ARRAYS * R; ++k)
-#pragma unroll
-          for (int h = 0; h < H; ++h) *reinterpret_cast<uint4*>(ring + ((k * V + v) * H + h) * 16) = make_uint4(0, 0, 0, 0);
+        for (int k = 0; k < S * ARRAYS * R; ++k) *reinterpret_cast<uint4*>(ring + plane(k * V + v)) = make_uint4(0, 0, 0, 0);
   }
-  __device__ __forceinline__ int col(int v) const { return (v * team_size + t) * kCols; }
+  static __device__ __forceinline__ int plane(int k) { return k * (int)blockDim.x * 16; }
+  __device__ __forceinline__ int col(int v) const { return (v * team_size + t) * N; }
   __device__ __forceinline__ bool has(int v) const { return v * team_size + t < nv; }
-  // Bytes from a vector to the thread's next.
-  __device__ __forceinline__ int across(int v) const { return v * team_size * kCols * ES; }
+  // Bytes from a thread's first vector to another.
+  __device__ __forceinline__ int across(int v) const { return v * team_size * 16; }
   // The byte offset of the team's first row, and from a row to the next, in an array.
-  __device__ __forceinline__ long long start(long long ld) const { return (first * ld + t * kCols) * ES; }
+  __device__ __forceinline__ long long start(long long ld) const { return first * ld * ES + t * 16; }
   __device__ __forceinline__ long long apart(long long ld) const { return stride * ld * ES; }
   // A batch's rows of an array, from row on, p their place in the first; rows past the end as
   // zeros.
   __device__ __forceinline__ void fetch(int stage, int array, const char* p, long long next, long long row) const {
-    unsigned char* const to = ring + (stage * planes + array * R * V * H) * 16;
+    unsigned char* const to = ring + plane(stage * planes + array * R * V);
 #pragma unroll
     for (int j = 0; j < R; ++j) {
       const bool in = row + j * stride < rows;
       const char* const q = in ? p + j * next : p;
 #pragma unroll
       for (int v = 0; v < V; ++v)
-        if (has(v))
-#pragma unroll
-          for (int h = 0; h < H; ++h) cp_async16(to + ((j * V + v) * H + h) * 16, q + across(v) + 16 * h, in);
+        if (has(v)) cp_async16(to + plane(j * V + v), q + across(v), in);
     }
   }
-  // 8 values of the ring, as pairs.
+  // A vector of the ring, as pairs.
   __device__ __forceinline__ void read(int stage, int array, int j, int v, float2* f) const {
-#pragma unroll
-    for (int h = 0; h < H; ++h)
-      unpack(*reinterpret_cast<const uint4*>(ring + (stage * planes + ((array * R + j) * V + v) * H + h) * 16), f + 2 * h);
+    unpack(*reinterpret_cast<const uint4*>(ring + plane(stage * planes + (array * R + j) * V + v)), f);
   }
-  // Rounds 8 values to the type, stores them at p and, if kept, leaves them rounded in f.
+  // Rounds a vector to the type, stores it at p and, if kept, leaves it rounded in f.
   __device__ __forceinline__ void write(char* p, int v, float2* f, bool in, bool keep) const {
-#pragma unroll
-    for (int h = 0; h < H; ++h) {
-      uint4 u;
-      if constexpr (BF16) {
-        u = make_uint4(Vec<true>::two(f[0].x, f[0].y), Vec<true>::two(f[1].x, f[1].y), Vec<true>::two(f[2].x, f[2].y),
-                       Vec<true>::two(f[3].x, f[3].y));
-      } else {
-        u = make_uint4(__float_as_uint(f[2 * h].x), __float_as_uint(f[2 * h].y), __float_as_uint(f[2 * h + 1].x),
-                       __float_as_uint(f[2 * h + 1].y));
-      }
-      if (in) *reinterpret_cast<uint4*>(p + across(v) + 16 * h) = u;
-      if (keep && BF16) unpack(u, f);
+    uint4 u;
+    if constexpr (BF16) {
+      u = make_uint4(Vec<true>::two(f[0].x, f[0].y), Vec<true>::two(f[1].x, f[1].y), Vec<true>::two(f[2].x, f[2].y),
+                     Vec<true>::two(f[3].x, f[3].y));
+    } else {
+      u = make_uint4(__float_as_uint(f[0].x), __float_as_uint(f[0].y), __float_as_uint(f[1].x), __float_as_uint(f[1].y));
     }
+    if (in) *reinterpret_cast<uint4*>(p + across(v)) = u;
+    if (keep && BF16) unpack(u, f);
   }
   static __device__ __forceinline__ void unpack(const uint4& u, float2* f) {
     if constexpr (BF16) {
@@ -110,42 +101,43 @@ struct Walk {
   }
 };
 
-// A thread's columns of a parameter vector: in registers, or, for long rows of one warp (4 vectors
-// and more), in shared memory, where all the CTA's teams read them: [half][vector][lane].
-template <int V, bool SHARED>
+// A thread's columns of a parameter vector: in registers, or, for long rows of one warp, in
+// shared memory, where all the CTA's teams read them: [vector][4 of its columns][lane].
+template <class W, bool SHARED>
 struct Param {
-  float2 f[SHARED ? 1 : V][kPairs];
+  float2 f[SHARED ? 1 : W::V][W::P];
   const float4* at;
-  template <class W>
   __device__ __forceinline__ Param(const W& w, const float* p, float otherwise, float4* shared) {
     if constexpr (SHARED) {
-      for (int k = threadIdx.x; k < V * 64; k += blockDim.x) {  // vectors' halves
-        const int c = (k >> 1) * kCols + (k & 1) * 4;
+      constexpr int Q = W::N / 4;
+      for (int k = threadIdx.x; k < W::V * 32 * Q; k += blockDim.x) {
+        const int c = k * 4;  // of 4 columns: vector (k / Q) of the row, lane (k / Q) % 32 of vector (k / Q) / 32
         float4 u = make_float4(otherwise, otherwise, otherwise, otherwise);
-        if (p && c < w.nv * kCols) u = make_float4(p[c], p[c + 1], p[c + 2], p[c + 3]);
-        shared[(k & 1) * V * 32 + (k >> 1)] = u;
+        if (p && c < w.nv * W::N) u = make_float4(p[c], p[c + 1], p[c + 2], p[c + 3]);
+        shared[(k / Q / 32 * Q + k % Q) * 32 + k / Q % 32] = u;
       }
       at = shared + w.t;
     } else {
 #pragma unroll
-      for (int v = 0; v < V; ++v)
+      for (int v = 0; v < W::V; ++v)
 #pragma unroll
-        for (int c = 0; c < kPairs; ++c)
+        for (int c = 0; c < W::P; ++c)
           f[v][c] = p && w.has(v) ? make_float2(p[w.col(v) + 2 * c], p[w.col(v) + 2 * c + 1])
                                   : make_float2(otherwise, otherwise);
     }
   }
   __device__ __forceinline__ void get(int v, float2* out) const {
     if constexpr (SHARED) {
+      constexpr int Q = W::N / 4;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const float4 u = at[(h * V + v) * 32];
-        out[2 * h] = make_float2(u.x, u.y);
-        out[2 * h + 1] = make_float2(u.z, u.w);
+      for (int q = 0; q < Q; ++q) {
+        const float4 u = at[(v * Q + q) * 32];
+        out[2 * q] = make_float2(u.x, u.y);
+        out[2 * q + 1] = make_float2(u.z, u.w);
       }
     } else {
 #pragma unroll
-      for (int c = 0; c < kPairs; ++c) out[c] = f[v][c];
+      for (int c = 0; c < W::P; ++c) out[c] = f[v][c];
     }
   }
 };
@@ -187,13 +179,14 @@ __device__ __forceinline__ float rsqrt_of(float x) {
   return y * fmaf(-0.5f * x * y, y, 1.5f);
 }
 
-template <int V, bool MULTI>
-constexpr bool kSharedParams = !MULTI && V > 2;
+template <int COLS, bool MULTI>
+constexpr bool kSharedParams = !MULTI && COLS > 16;
 
-template <bool BF16, int LANES, bool MULTI, int V, int R, bool RES>
-__global__ void __launch_bounds__(MULTI ? 512 : V > 2 ? 128 : 256, MULTI ? 1 : V == 2 ? 3 : 4)
+template <bool BF16, int LANES, bool MULTI, int COLS, int R, bool RES>
+__global__ void __launch_bounds__(MULTI ? 512 : COLS > 16 ? 128 : 256, MULTI ? 1 : COLS == 16 ? 3 : 4)
 palimpsa_norm_kernel(NormArgs a) {
-  using W = Walk<BF16, LANES, MULTI, V, R, 1 + RES>;
+  using W = Walk<BF16, LANES, MULTI, COLS, R, 1 + RES>;
+  constexpr int V = W::V, P = W::P;
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ float2 parts[2][16][R];  // of the warps: sums, and squares about their means
   const W at(a.rows, a.D, smem);
@@ -218,23 +211,23 @@ palimpsa_norm_kernel(NormArgs a) {
   };
 #pragma unroll
   for (int k = 0; k < W::S - 1; ++k) stage();
-  constexpr bool kShared = kSharedParams<V, MULTI>;
-  float4* const shared = reinterpret_cast<float4*>(smem + blockDim.x * W::units * 16);
-  const Param<V, kShared> weight(at, a.weight, 1.f, shared), bias(at, a.bias, 0.f, shared + V * 64);
+  constexpr bool kShared = kSharedParams<COLS, MULTI>;
+  float4* const shared = reinterpret_cast<float4*>(smem + W::plane(W::S * W::planes));
+  const Param<W, kShared> weight(at, a.weight, 1.f, shared), bias(at, a.bias, 0.f, shared + COLS * 8);
   if (kShared) __syncthreads();
   // Values of warp w's part of a row.
   auto count = [&](int w) {
     int n = 0;
 #pragma unroll
     for (int v = 0; v < V; ++v) n += min(max(at.nv - (v * (int)blockDim.x + 32 * w), 0), 32);
-    return (float)(n * kCols);
+    return (float)(n * W::N);
   };
   const float whole = __frcp_rn((float)a.D), own = MULTI ? __frcp_rn(count(warp)) : whole;
 
   int from = 0;
   for (int b = 0; b < at.batches; ++b) {
     cp_async_wait<W::S - 2>();
-    float2 s[R][V][kPairs];
+    float2 s[R][V][P];
     float sum[R], sq[R], mean[R], rstd[R];
     bool live[R];
 #pragma unroll
@@ -245,14 +238,14 @@ palimpsa_norm_kernel(NormArgs a) {
       for (int v = 0; v < V; ++v) {
         at.read(from, 0, j, v, s[j][v]);
         if (RES) {
-          float2 r[kPairs];
+          float2 r[P];
           at.read(from, 1, j, v, r);
 #pragma unroll
-          for (int c = 0; c < kPairs; ++c) s[j][v][c] = __fadd2_rn(s[j][v][c], r[c]);
+          for (int c = 0; c < P; ++c) s[j][v][c] = __fadd2_rn(s[j][v][c], r[c]);
           at.write(ps + j * ny, v, s[j][v], live[j] && at.has(v), true);
         }
 #pragma unroll
-        for (int c = 0; c < kPairs; ++c) t = __fadd2_rn(t, s[j][v][c]);
+        for (int c = 0; c < P; ++c) t = __fadd2_rn(t, s[j][v][c]);
       }
       sum[j] = t.x + t.y;
     }
@@ -268,7 +261,7 @@ palimpsa_norm_kernel(NormArgs a) {
       for (int v = 0; v < V; ++v) {
         float2 q = two(0.f);
 #pragma unroll
-        for (int c = 0; c < kPairs; ++c) {
+        for (int c = 0; c < P; ++c) {
           const float2 d = __fadd2_rn(s[j][v][c], two(-mean[j]));
           q = __ffma2_rn(d, d, q);
         }
@@ -302,13 +295,13 @@ palimpsa_norm_kernel(NormArgs a) {
         reinterpret_cast<float2*>(a.stats)[row + j * at.stride] = make_float2(mean[j], rstd[j]);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      float2 wt[kPairs], add[kPairs];
+      float2 wt[P], add[P];
       weight.get(v, wt);
       bias.get(v, add);
 #pragma unroll
       for (int j = 0; j < R; ++j) {
 #pragma unroll
-        for (int c = 0; c < kPairs; ++c) {
+        for (int c = 0; c < P; ++c) {
           const float2 t = __fmul2_rn(__fadd2_rn(s[j][v][c], two(-mean[j])), two(rstd[j]));
           s[j][v][c] = __ffma2_rn(t, wt[c], add[c]);
         }
@@ -323,10 +316,11 @@ palimpsa_norm_kernel(NormArgs a) {
 }
 
 // sums: [CTAs, 2, D], the CTAs' parts of dweight and dbias, or null.
-template <bool BF16, int LANES, bool MULTI, int V, int R, bool DS>
-__global__ void __launch_bounds__(MULTI ? 512 : 256, MULTI ? 1 : V == 2 ? 2 : 3)
+template <bool BF16, int LANES, bool MULTI, int COLS, int R, bool DS>
+__global__ void __launch_bounds__(MULTI ? 512 : 256, MULTI ? 1 : COLS == 16 ? 2 : 3)
 palimpsa_norm_bwd_kernel(NormArgs a, float* sums) {
-  using W = Walk<BF16, LANES, MULTI, V, R, 2 + DS>;
+  using W = Walk<BF16, LANES, MULTI, COLS, R, 2 + DS>;
+  constexpr int V = W::V, P = W::P;
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ float parts[2][16][2 * R];  // of the warps: mean(u), mean(u t), each for every row
   const W at(a.rows, a.D, smem);
@@ -361,12 +355,12 @@ palimpsa_norm_bwd_kernel(NormArgs a, float* sums) {
   load_stats(row);
 #pragma unroll
   for (int k = 0; k < W::S - 1; ++k) stage();
-  const Param<V, false> weight(at, a.weight, 1.f, nullptr);
-  float2 gw[V][kPairs], gb[V][kPairs];
+  const Param<W, false> weight(at, a.weight, 1.f, nullptr);
+  float2 gw[V][P], gb[V][P];
 #pragma unroll
   for (int v = 0; v < V; ++v)
 #pragma unroll
-    for (int c = 0; c < kPairs; ++c) gw[v][c] = gb[v][c] = two(0.f);
+    for (int c = 0; c < P; ++c) gw[v][c] = gb[v][c] = two(0.f);
   const float inv = __frcp_rn((float)a.D);
 
   int from = 0;
@@ -389,11 +383,11 @@ palimpsa_norm_bwd_kernel(NormArgs a, float* sums) {
       if (live[0])
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-          float2 x[kPairs], dy[kPairs];
+          float2 x[P], dy[P];
           at.read(from, 0, j, v, x);
           at.read(from, 1, j, v, dy);
 #pragma unroll
-          for (int c = 0; c < kPairs; ++c) {
+          for (int c = 0; c < P; ++c) {
             const float2 t = __fmul2_rn(__fadd2_rn(x[c], two(-st[j].x)), two(st[j].y)), u = __fmul2_rn(dy[c], weight.f[v][c]);
             gw[v][c] = __ffma2_rn(dy[c], t, gw[v][c]);
             gb[v][c] = __fadd2_rn(gb[v][c], dy[c]);
@@ -421,12 +415,12 @@ palimpsa_norm_bwd_kernel(NormArgs a, float* sums) {
     for (int j = 0; j < R; ++j) {
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        float2 x[kPairs], dy[kPairs], ds[kPairs];
+        float2 x[P], dy[P], ds[P];
         at.read(from, 0, j, v, x);
         at.read(from, 1, j, v, dy);
         if (DS) at.read(from, 2, j, v, ds);
 #pragma unroll
-        for (int c = 0; c < kPairs; ++c) {
+        for (int c = 0; c < P; ++c) {
           const float2 t = __fmul2_rn(__fadd2_rn(x[c], two(-st[j].x)), two(st[j].y));
           const float2 d = __ffma2_rn(t, two(-tot[2 * j + 1]), __ffma2_rn(dy[c], weight.f[v][c], two(-tot[2 * j])));
           x[c] = DS ? __ffma2_rn(two(st[j].y), d, ds[c]) : __fmul2_rn(two(st[j].y), d);
@@ -446,7 +440,7 @@ palimpsa_norm_bwd_kernel(NormArgs a, float* sums) {
     for (int v = 0; v < V; ++v)
       if (at.has(v)) {
 #pragma unroll
-        for (int c = 0; c < kPairs; c += 2) {
+        for (int c = 0; c < P; c += 2) {
           float* const p = out + at.col(v) + 2 * c;
           *reinterpret_cast<float4*>(p) = make_float4(gw[v][c].x, gw[v][c].y, gw[v][c + 1].x, gw[v][c + 1].y);
           *reinterpret_cast<float4*>(p + a.D) = make_float4(gb[v][c].x, gb[v][c].y, gb[v][c + 1].x, gb[v][c + 1].y);
@@ -456,7 +450,7 @@ palimpsa_norm_bwd_kernel(NormArgs a, float* sums) {
     // The CTA's teams, through the ring's memory (its copies are done: the last groups are empty).
     cp_async_wait<0>();
     float* const red = reinterpret_cast<float*>(smem);
-    constexpr int cols = LANES * kCols;
+    constexpr int N = W::N, cols = LANES * N;
     const int teams = blockDim.x / LANES, team = threadIdx.x / LANES;
 #pragma unroll
     for (int v = 0; v < V; ++v)
@@ -464,15 +458,15 @@ palimpsa_norm_bwd_kernel(NormArgs a, float* sums) {
       for (int q = 0; q < 2; ++q) {
         __syncthreads();
 #pragma unroll
-        for (int c = 0; c < kCols; ++c) {
+        for (int c = 0; c < N; ++c) {
           const float2 g = q ? gb[v][c / 2] : gw[v][c / 2];
-          red[(team * kCols + c) * LANES + at.t] = c & 1 ? g.y : g.x;
+          red[(team * N + c) * LANES + at.t] = c & 1 ? g.y : g.x;
         }
         __syncthreads();
         for (int k = threadIdx.x; k < cols; k += blockDim.x) {
           float s = 0.f;
           for (int m = 0; m < teams; ++m) s += red[m * cols + k];
-          const int col = v * cols + k % LANES * kCols + k / LANES;
+          const int col = v * cols + k % LANES * N + k / LANES;
           if (col < a.D) out[q * a.D + col] = s;
         }
       }
@@ -514,33 +508,33 @@ cudaError_t shape_of(K kernel, const NormArgs& a, int threads, int teams, int by
   *p = {threads, bytes, (int)std::max<long long>(1, std::min((long long)held * sms, (a.rows + teams - 1) / teams))};
   return cudaSuccess;
 }
-// Threads of a CTA that a row takes for itself, each with V vectors.
-template <int V>
+// Threads of a CTA that a row takes for itself, each with COLS columns.
+template <int COLS>
 int row_threads(const NormArgs& a) {
-  return (a.D / kCols + V * 32 - 1) / (V * 32) * 32;
+  return (a.D + COLS * 32 - 1) / (COLS * 32) * 32;
 }
 
-template <bool BF16, int LANES, bool MULTI, int V, int R, bool MORE>
+template <bool BF16, int LANES, bool MULTI, int COLS, int R, bool MORE>
 cudaError_t forward(const NormArgs& a, cudaStream_t s) {
-  using W = Walk<BF16, LANES, MULTI, V, R, 1 + MORE>;
-  constexpr bool kShared = kSharedParams<V, MULTI>;
-  const auto kernel = palimpsa_norm_kernel<BF16, LANES, MULTI, V, R, MORE>;
-  const int threads = MULTI ? row_threads<V>(a) : kShared ? 128 : 256;
+  using W = Walk<BF16, LANES, MULTI, COLS, R, 1 + MORE>;
+  constexpr bool kShared = kSharedParams<COLS, MULTI>;
+  const auto kernel = palimpsa_norm_kernel<BF16, LANES, MULTI, COLS, R, MORE>;
+  const int threads = MULTI ? row_threads<COLS>(a) : kShared ? 128 : 256;
   Shape p;
   const cudaError_t e = shape_of(kernel, a, threads, MULTI ? 1 : threads / LANES,
-                                 threads * 16 * W::units + (kShared ? V * 2048 : 0), &p);
+                                 threads * 16 * W::S * W::planes + (kShared ? COLS * 256 : 0), &p);
   if (e != cudaSuccess) return e;
   kernel<<<p.ctas, p.threads, p.bytes, s>>>(a);
   return cudaGetLastError();
 }
 
-template <bool BF16, int LANES, bool MULTI, int V, int R, bool MORE>
+template <bool BF16, int LANES, bool MULTI, int COLS, int R, bool MORE>
 cudaError_t backward(const NormArgs& a, float* sums, int* ctas, cudaStream_t s) {
-  using W = Walk<BF16, LANES, MULTI, V, R, 2 + MORE>;
-  const auto kernel = palimpsa_norm_bwd_kernel<BF16, LANES, MULTI, V, R, MORE>;
-  const int threads = MULTI ? row_threads<V>(a) : 256;
+  using W = Walk<BF16, LANES, MULTI, COLS, R, 2 + MORE>;
+  const auto kernel = palimpsa_norm_bwd_kernel<BF16, LANES, MULTI, COLS, R, MORE>;
+  const int threads = MULTI ? row_threads<COLS>(a) : 256;
   Shape p;
-  const cudaError_t e = shape_of(kernel, a, threads, MULTI ? 1 : threads / LANES, threads * 16 * W::units, &p);
+  const cudaError_t e = shape_of(kernel, a, threads, MULTI ? 1 : threads / LANES, threads * 16 * W::S * W::planes, &p);
   if (e != cudaSuccess) return e;
   if (ctas) {
     *ctas = p.ctas;
@@ -552,20 +546,20 @@ cudaError_t backward(const NormArgs& a, float* sums, int* ctas, cudaStream_t s) 
 
 template <bool BF16, bool MORE>
 cudaError_t forward_by_width(const NormArgs& a, cudaStream_t s) {
-  if (a.D <= 64) return forward<BF16, 8, false, 1, 2, MORE>(a, s);
-  if (a.D <= 256) return forward<BF16, 32, false, 1, 2, MORE>(a, s);
-  if (a.D <= 512) return forward<BF16, 32, false, 2, 2, MORE>(a, s);
-  if (a.D <= 1024) return forward<BF16, 32, false, 4, 1, MORE>(a, s);
-  if (a.D <= 1536) return forward<BF16, 32, false, 6, 1, MORE>(a, s);
-  if (a.D <= 2048) return forward<BF16, 32, false, 8, 1, MORE>(a, s);
-  return forward<BF16, 32, true, 2, BF16 ? 2 : 1, MORE>(a, s);
+  if (a.D <= 64) return forward<BF16, 8, false, 8, 2, MORE>(a, s);
+  if (a.D <= 256) return forward<BF16, 32, false, 8, 2, MORE>(a, s);
+  if (a.D <= 512) return forward<BF16, 32, false, 16, 2, MORE>(a, s);
+  if (a.D <= 1024) return forward<BF16, 32, false, 32, 1, MORE>(a, s);
+  if (a.D <= 1536) return forward<BF16, 32, false, 48, 1, MORE>(a, s);
+  if (a.D <= 2048) return forward<BF16, 32, false, 64, 1, MORE>(a, s);
+  return forward<BF16, 32, true, 16, BF16 ? 2 : 1, MORE>(a, s);
 }
 template <bool BF16, bool MORE>
 cudaError_t backward_by_width(const NormArgs& a, float* sums, int* ctas, cudaStream_t s) {
-  if (a.D <= 64) return backward<BF16, 8, false, 1, BF16 ? 2 : 1, MORE>(a, sums, ctas, s);
-  if (a.D <= 256) return backward<BF16, 32, false, 1, BF16 ? 2 : 1, MORE>(a, sums, ctas, s);
-  if (a.D <= 512) return backward<BF16, 32, false, 2, BF16 ? 2 : 1, MORE>(a, sums, ctas, s);
-  return backward<BF16, 32, true, 2, BF16 ? 2 : 1, MORE>(a, sums, ctas, s);
+  if (a.D <= 64) return backward<BF16, 8, false, 8, BF16 ? 2 : 1, MORE>(a, sums, ctas, s);
+  if (a.D <= 256) return backward<BF16, 32, false, 8, BF16 ? 2 : 1, MORE>(a, sums, ctas, s);
+  if (a.D <= 512) return backward<BF16, 32, false, 16, BF16 ? 2 : 1, MORE>(a, sums, ctas, s);
+  return backward<BF16, 32, true, 16, BF16 ? 2 : 1, MORE>(a, sums, ctas, s);
 }
 cudaError_t backward_any(const NormArgs& a, float* sums, int* ctas, cudaStream_t s) {
   if (a.bf16) return a.ds ? backward_by_width<true, true>(a, sums, ctas, s) : backward_by_width<true, false>(a, sums, ctas, s);
