@@ -29,8 +29,9 @@ struct GateTile {
 struct GatePlan {
   int channels, cluster;
 };
-// `tokens` of a CTA's tile of 64 channels (twice as many at 32), `resident` CTAs on an SM.
-GatePlan gate_plan(const SeqRows& r, int D, int tokens, int resident);
+// `tokens` of a CTA's tile of 64 channels (twice as many at `narrow`, the least channels of a tile),
+// `resident` CTAs on an SM.
+GatePlan gate_plan(const SeqRows& r, int D, int tokens, int resident, int narrow);
 
 #if defined(__CUDACC__)
 
@@ -113,8 +114,8 @@ __device__ __forceinline__ float2 input_of(float2 rest, float2 q, float2 x) {
 __device__ __forceinline__ float2 input_of(float2 rest, float2 x) {
   return __fmul2_rn(__fmul2_rn(rest, x), make_float2(rsqrt_approx(rest.x), rsqrt_approx(rest.y)));
 }
-// The address of a shared object in another CTA of the cluster, 16 bytes stored there, counted on
-// a barrier of that CTA, and the wait for them.
+// The address of a shared object in another CTA of the cluster, 16 or 8 bytes stored there, counted
+// on a barrier of that CTA, and the wait for them.
 __device__ __forceinline__ uint32_t cluster_addr(const void* p, int rank) {
   uint32_t r;
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
@@ -123,6 +124,11 @@ __device__ __forceinline__ uint32_t cluster_addr(const void* p, int rank) {
 __device__ __forceinline__ void st_async(uint32_t to, const float4& v, uint32_t bar) {
   asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(to),
                "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w), "r"(bar)
+               : "memory");
+}
+__device__ __forceinline__ void st_async(uint32_t to, const float2& v, uint32_t bar) {
+  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(to),
+               "f"(v.x), "f"(v.y), "r"(bar)
                : "memory");
 }
 __device__ __forceinline__ bool cluster_try_wait(uint64_t* bar, uint32_t parity) {

@@ -29,12 +29,12 @@ constexpr int kResident = 2;  // CTAs of an SM
 template <bool BF16>
 using Tile = GateTile<BF16, 64, 2, BF16 ? 256 : 128>;
 
-// Shared memory: the ring of raw inputs (and the states before the pieces), then the pieces' and
-// the ranks' summaries.
+// Shared memory: the ring of raw inputs (and the states before the pieces), then the pieces'
+// summaries and two gradients that the CTA behind hands over.
 template <bool BF16, bool IN, bool GATE>
 struct BwdSmem {
   static constexpr int h = (3 + IN + GATE) * Tile<BF16>::bytes, stage = h + Tile<BF16>::pieces * Tile<BF16>::CH * 4;
-  static constexpr int agg = 2 * stage, ranks = agg + Tile<BF16>::pieces * 512;
+  static constexpr int agg = 2 * stage, given = agg + Tile<BF16>::pieces * 512;
 };
 
 // sums: [n_seq, cluster, 3, D], the CTAs' parts of dA, dr_bias and di_bias.
@@ -105,7 +105,7 @@ palimpsa_gate_bwd_kernel(GateArgs a, int tiles, float* sums) {
   const float2 scale = make_float2(-kLog2e, -kLog2e);
   const float2 rb = __fmul2_rn(pair_or(a.r_bias, ch, in, 0.f), scale), ib = __fmul2_rn(pair_or(a.i_bias, ch, in, 0.f), scale);
   if (!pos_finite(A.x) || !pos_finite(A.y)) latch_status(a.status, kStatusDomain);
-  float2 carry = zero;  // a g of the token behind the round
+  float2 carry = zero;  // a g of the token behind the round (in a cluster, behind the sequence)
   if (a.dh_T && in) carry = *reinterpret_cast<const float2*>(a.dh_T + n * a.D + ch);
   float2 sA = zero, sr = zero, si = zero;
   bool waits = true;
@@ -116,7 +116,9 @@ palimpsa_gate_bwd_kernel(GateArgs a, int tiles, float* sums) {
     const int np = min(kPiece, len - tp);
     unsigned char* const raw = smem + (k & 1) * S::stage + warp * kPiece * G::row + lane * 2 * ES;
     cp_async_wait<0>();
-    if (CLUSTER && tid == 0) mbar_arrive_expect_tx(&bars[k & 1], cs * 512);
+    const int turn = rounds - 1 - k;
+    const bool end = turn == 0 && rank == cs - 1;  // nothing comes from behind
+    if (CLUSTER && tid == 0) mbar_arrive_expect_tx(&bars[turn & 1], end ? 0 : 256);
     __syncthreads();  // the round's inputs are here; the other stage and the summaries are free
     stage(k - 1);
 
@@ -178,7 +180,7 @@ palimpsa_gate_bwd_kernel(GateArgs a, int tiles, float* sums) {
     agg[warp * 32 + lane] = make_float4(P.x, P.y, C.x, C.y);
     __syncthreads();
 
-    // The gradient that comes in from behind the piece, and the one before the round.
+    // The gradient that comes in from behind the piece, and the one that the round passes on.
     float2 c = carry;
     if (!CLUSTER) {
 #pragma unroll
@@ -188,24 +190,28 @@ palimpsa_gate_bwd_kernel(GateArgs a, int tiles, float* sums) {
         carry = ffma2(make_float2(e.x, e.y), carry, make_float2(e.z, e.w));
       }
     } else {
-      float4* const slots = reinterpret_cast<float4*>(smem + S::ranks + (k & 1) * cs * 512);
-      for (int q = warp; q < cs; q += NP) {
-        float2 Pc = make_float2(1.f, 1.f), Cc = zero;
+      // The first warp works out the CTA's summary, and hands on what goes back from the tile.
+      float2 Pc = make_float2(1.f, 1.f), Cc = zero;
+      if (warp == 0)
 #pragma unroll
         for (int w = NP - 1; w >= 0; --w) {
           const float4 e = agg[w * 32 + lane];
           Cc = ffma2(make_float2(e.x, e.y), Cc, make_float2(e.z, e.w));
           Pc = __fmul2_rn(Pc, make_float2(e.x, e.y));
         }
-        st_async(cluster_addr(slots + rank * 32 + lane, q), make_float4(Pc.x, Pc.y, Cc.x, Cc.y),
-                 cluster_addr(&bars[k & 1], q));
-      }
-      waits = waits && cluster_wait(&bars[k & 1], ((rounds - 1 - k) >> 1) & 1, a.wait_timeout_ns);
+      float2* const given = reinterpret_cast<float2*>(smem + S::given) + lane;
+      waits = waits && cluster_wait(&bars[turn & 1], (turn >> 1) & 1, a.wait_timeout_ns);
       if (!waits) latch_status(a.status, kStatusTimeout);
-      for (int q = cs - 1; q >= 0; --q) {
-        const float4 e = slots[q * 32 + lane];
-        if (q == rank) c = carry;
-        carry = ffma2(make_float2(e.x, e.y), carry, make_float2(e.z, e.w));
+      if (!end) c = given[(turn & 1) * 32];
+      if (warp == 0) {
+        Cc = ffma2(Pc, c, Cc);
+        const int next = rank == 0 ? turn + 1 : turn;  // the turn of the CTA before
+        if (next < rounds) {
+          const int to = rank == 0 ? cs - 1 : rank - 1;
+          st_async(cluster_addr(given + (next & 1) * 32, to), Cc, cluster_addr(&bars[next & 1], to));
+        } else if (in && a.dh0) {
+          *reinterpret_cast<float2*>(a.dh0 + n * a.D + ch) = Cc;
+        }
       }
       for (int w = NP - 1; w > warp; --w) {
         const float4 e = agg[w * 32 + lane];
@@ -237,7 +243,8 @@ palimpsa_gate_bwd_kernel(GateArgs a, int tiles, float* sums) {
     }
     __syncwarp();
   }
-  if (rank == 0 && warp == 0 && in && a.dh0) *reinterpret_cast<float2*>(a.dh0 + n * a.D + ch) = carry;
+  if ((!CLUSTER || rounds == 0) && rank == 0 && warp == 0 && in && a.dh0)
+    *reinterpret_cast<float2*>(a.dh0 + n * a.D + ch) = carry;
   // The CTA's sums over its pieces.
   float2* const red = reinterpret_cast<float2*>(agg);
   const float2 own[3] = {sA, sr, si};
@@ -253,7 +260,7 @@ palimpsa_gate_bwd_kernel(GateArgs a, int tiles, float* sums) {
       *reinterpret_cast<float2*>(part + (long long)v * a.D) = t;
     }
   }
-  if (CLUSTER) cg::this_cluster().sync();  // nobody sends to a CTA that has left
+  if (CLUSTER) cg::this_cluster().sync();  // nobody hands anything to a CTA that has left
 }
 
 // Sums the CTAs' parts [rows, 3, D]; block y = v, 32 channels by 8 slices of the rows.
@@ -279,7 +286,7 @@ cudaError_t run(const GateArgs& a, float* sums, cudaStream_t s) {
   using G = Tile<BF16>;
   const long long tiles = (a.D + G::CH - 1) / G::CH, blocks = tiles * a.rows.n_seq * a.cluster;
   if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
-  const int bytes = BwdSmem<BF16, IN, GATE>::ranks + (CLUSTER ? 2 * a.cluster * 512 : 0);
+  constexpr int bytes = BwdSmem<BF16, IN, GATE>::given + (CLUSTER ? 512 : 0);
   const auto kernel = palimpsa_gate_bwd_kernel<BF16, IN, GATE, CLUSTER>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e == cudaSuccess && a.cluster > 8) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
@@ -310,8 +317,8 @@ cudaError_t backward(const GateArgs& a, float* sums, cudaStream_t s) {
 }  // namespace
 
 size_t plan_gate_backward(GateArgs* a) {
-  a->cluster = a->bf16 ? gate_plan(a->rows, a->D, Tile<true>::tokens, kResident).cluster
-                       : gate_plan(a->rows, a->D, Tile<false>::tokens, 2 * kResident).cluster;
+  a->cluster = a->bf16 ? gate_plan(a->rows, a->D, Tile<true>::tokens, kResident, 64).cluster
+                       : gate_plan(a->rows, a->D, Tile<false>::tokens, 2 * kResident, 64).cluster;
   return (size_t)a->rows.n_seq * a->cluster * 3 * a->D;
 }
 

@@ -12,11 +12,14 @@
 // the piece's summary (the product of its a and its end state), then, with the state
 // before the piece known, for the states themselves. (4 tokens and twice the threads took 1.3
 // times as long: what a round costs a thread besides its tokens is a fifth of it.) The
-// summaries of a CTA's pieces (groups of 16 or 8 threads, along time) pass through shared memory, and those of a cluster's CTAs
-// through each other's shared memory, as asynchronous stores that a barrier there counts;
-// every thread folds the ones before its own. A CTA walks its sequence in rounds of
-// such tiles, the next round's inputs coming by asynchronous copies meanwhile, and
-// carries the state in registers.
+// summaries of a CTA's pieces (groups of 16 or 8 threads, along time) pass through shared
+// memory, and every thread folds the ones before its own. A CTA walks its sequence in rounds
+// of such tiles, the next round's inputs coming by asynchronous copies meanwhile. Where
+// the CTAs are too few, those of a cluster take turns along time: each gets the state before its
+// tile from the one before it and hands on the state after it, as an asynchronous store into
+// the next one's shared memory that a barrier there counts. (A ring: with all summaries sent
+// to all, the CTAs of a cluster went in step, and 8 x 4096 x 1536 took
+// 83 us, now 78.)
 //
 // Rounding: gates, decays and states are fp32; y is rounded to the input type once.
 #include <algorithm>
@@ -36,8 +39,8 @@ constexpr int kResident = 4;  // CTAs of an SM
 template <bool BF16, int CH>
 using Tile = GateTile<BF16, CH, 4, BF16 ? 128 : 64>;
 
-// Shared memory: two stages of x, r and i, then two sets of the ranks' summaries,
-// [rank][products, states][lanes of a group] of 4 channels. A piece's summary takes the place of
+// Shared memory: two stages of x, r and i, then two states of the tile's channels that the CTA
+// before hands over. A piece's summary takes the place of
 // its first rows of x. Where rows are 64 bytes, those of odd pieces change places in pairs, so
 // that the two that a half warp reads at once lie in different banks.
 template <bool BF16, bool IN>
@@ -53,6 +56,15 @@ struct Four {
   __device__ __forceinline__ void times(const float4& P) {
     v[0] = __fmul2_rn(v[0], make_float2(P.x, P.y));
     v[1] = __fmul2_rn(v[1], make_float2(P.z, P.w));
+  }
+  // v + P h
+  __device__ __forceinline__ void fold_after(const Four& P, const Four& h) {
+    v[0] = ffma2(P.v[0], h.v[0], v[0]);
+    v[1] = ffma2(P.v[1], h.v[1], v[1]);
+  }
+  __device__ __forceinline__ void set(const float4& f) {
+    v[0] = make_float2(f.x, f.y);
+    v[1] = make_float2(f.z, f.w);
   }
   __device__ __forceinline__ float4 all() const { return make_float4(v[0].x, v[0].y, v[1].x, v[1].y); }
 };
@@ -121,7 +133,7 @@ __global__ void __launch_bounds__(BF16 ? 128 : 64, kResident) palimpsa_gate_kern
   }
   // Parameters, the gates' biases as their exponents' addends.
   float2 A[2], rb[2], ib[2];
-  Four carry = four(0.f);  // the state before the round
+  Four carry = four(0.f);  // the state before the round (in a cluster, before the first)
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
     A[j] = pair_or(a.A, ch + 2 * j, in, 1.f);
@@ -143,7 +155,7 @@ __global__ void __launch_bounds__(BF16 ? 128 : 64, kResident) palimpsa_gate_kern
     // A piece's summary: products and states of the lane's channels.
     auto sums_of = [&](int p) { return reinterpret_cast<float4*>(tile + p * kPiece * G::row) + lane; };
     cp_async_wait<0>();
-    if (CLUSTER && tid == 0) mbar_arrive_expect_tx(&bars[k & 1], cs * LG * 32);
+    if (CLUSTER && tid == 0) mbar_arrive_expect_tx(&bars[k & 1], k + rank > 0 ? LG * 16 : 0);
     __syncthreads();  // the round's inputs are here; the other stage and the summaries are free
     stage(k + 1);
 
@@ -202,25 +214,30 @@ __global__ void __launch_bounds__(BF16 ? 128 : 64, kResident) palimpsa_gate_kern
         carry.fold(sums_of(q)[0], sums_of(q)[LG]);
       }
     } else {
-      // Group q sends the CTA's summary to rank q. (Two sets of slots: a rank may be a round ahead.)
-      float4* const slots = reinterpret_cast<float4*>(smem + 2 * kStage + (k & 1) * cs * LG * 32) + lane;
-      for (int q = piece; q < cs; q += NP) {
-        Four Pc = four(1.f), Hc = four(0.f);
+      // The last group works out the CTA's summary, and hands on the state behind the tile. (Two
+      // places for it, each written again only after this CTA's next state has gone round.)
+      const bool last = piece == NP - 1;
+      Four Pc = four(1.f), Hc = four(0.f);
+      if (last)
 #pragma unroll
         for (int w = 0; w < NP; ++w) {
           Hc.fold(sums_of(w)[0], sums_of(w)[LG]);
           Pc.times(sums_of(w)[0]);
         }
-        const uint32_t to = cluster_addr(slots + rank * 2 * LG, q), bar = cluster_addr(&bars[k & 1], q);
-        st_async(to, Pc.all(), bar);
-        st_async(to + LG * 16, Hc.all(), bar);
-      }
+      float4* const states = reinterpret_cast<float4*>(smem + 2 * kStage) + lane;
       waits = waits && cluster_wait(&bars[k & 1], (k >> 1) & 1, a.wait_timeout_ns);
       if (!waits) latch_status(a.status, kStatusTimeout);
-      int q = 0;
-      for (; q < rank; ++q) carry.fold(slots[q * 2 * LG], slots[(q * 2 + 1) * LG]);
-      h = carry;
-      for (; q < cs; ++q) carry.fold(slots[q * 2 * LG], slots[(q * 2 + 1) * LG]);
+      if (k + rank > 0) h.set(states[(k & 1) * LG]);
+      if (last) {
+        Hc.fold_after(Pc, h);
+        const int next = rank + 1 == cs ? k + 1 : k;  // its round
+        if (next < rounds) {
+          const int to = rank + 1 == cs ? 0 : rank + 1;
+          st_async(cluster_addr(states + (next & 1) * LG, to), Hc.all(), cluster_addr(&bars[next & 1], to));
+        } else if (in) {
+          *reinterpret_cast<float4*>(a.h_T + n * a.D + ch) = Hc.all();
+        }
+      }
       for (int w = 0; w < piece; ++w) h.fold(sums_of(w)[0], sums_of(w)[LG]);
     }
     if (in && np > 0) {
@@ -251,9 +268,10 @@ __global__ void __launch_bounds__(BF16 ? 128 : 64, kResident) palimpsa_gate_kern
     }
     __syncwarp();
   }
-  if (rank == 0 && piece == 0 && in) *reinterpret_cast<float4*>(a.h_T + n * a.D + ch) = carry.all();
+  if ((!CLUSTER || rounds == 0) && rank == 0 && piece == 0 && in)
+    *reinterpret_cast<float4*>(a.h_T + n * a.D + ch) = carry.all();
   __syncwarp();
-  if (CLUSTER) cg::this_cluster().sync();  // nobody sends to a CTA that has left
+  if (CLUSTER) cg::this_cluster().sync();  // nobody hands anything to a CTA that has left
 }
 
 // One token: a thread takes 4 channels of a sequence. A few bytes each way: latency alone.
@@ -302,7 +320,7 @@ cudaError_t run(const GateArgs& a, cudaStream_t s) {
   using G = Tile<BF16, CH>;
   const long long tiles = (a.D + CH - 1) / CH, blocks = tiles * a.rows.n_seq * a.cluster;
   if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
-  const int bytes = 2 * kStageBytes<BF16, IN> + (CLUSTER ? 2 * a.cluster * G::group * 32 : 0);
+  constexpr int bytes = 2 * kStageBytes<BF16, IN> + (CLUSTER ? 2 * G::group * 16 : 0);
   const auto kernel = palimpsa_gate_kernel<BF16, IN, GATE, CLUSTER, CH>;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
@@ -323,7 +341,7 @@ cudaError_t run(const GateArgs& a, cudaStream_t s) {
 template <bool BF16, bool IN, bool GATE>
 cudaError_t forward(const GateArgs& given, cudaStream_t s) {
   GateArgs a = given;
-  const GatePlan p = gate_plan(a.rows, a.D, Tile<BF16, 64>::tokens, kResident);
+  const GatePlan p = gate_plan(a.rows, a.D, Tile<BF16, 64>::tokens, kResident, 32);
   a.cluster = p.cluster;
   if (p.channels == 32)
     return a.cluster > 1 ? run<BF16, IN, GATE, true, 32>(a, s) : run<BF16, IN, GATE, false, 32>(a, s);
@@ -347,14 +365,14 @@ cudaError_t step(const GateArgs& a, cudaStream_t s) {
 // as are left. A tile of 32 channels has twice the pieces to fold: 6 % more. A packed batch's
 // CTAs have the mean of the rounds (and half of one lost), but none is done before its
 // longest sequence's rounds, one after the other.
-GatePlan gate_plan(const SeqRows& r, int D, int tokens, int resident) {
+GatePlan gate_plan(const SeqRows& r, int D, int tokens, int resident, int narrow) {
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     sms = 152;
   const double slots = (double)resident * sms;
   GatePlan best = {64, 1};
   double least = 0;
-  for (int ch = 64; ch >= 32; ch /= 2) {
+  for (int ch = 64; ch >= narrow; ch /= 2) {
     const double tiles = (D + ch - 1) / ch;
     for (int cs = 1; cs <= kGateCluster; ++cs) {
       const long long per = (long long)cs * tokens * (64 / ch);
