@@ -76,10 +76,16 @@ palimpsa_gate_bwd_kernel(GateArgs a, int tiles, float* sums) {
       const long long first = row0 + t0 + vrow, col = (long long)ch0 * ES + vec * 16;
       auto copy = [&](const void* from, long long ld, int slot) {
         const char* p = static_cast<const char*>(from) + first * ld * ES + col;
+        unsigned char* const q = to + slot * G::bytes + tid * 16;
+        const long long next = G::rows_at_once * ld * ES;
+        if (nt == RT) {
 #pragma unroll
-        for (int j = 0; j < RT / G::rows_at_once; ++j)
-          if (j * G::rows_at_once + vrow < nt)
-            cp_async16(to + slot * G::bytes + tid * 16 + j * G::threads * 16, p + j * G::rows_at_once * ld * ES);
+          for (int j = 0; j < RT / G::rows_at_once; ++j, p += next) cp_async16(q + j * G::threads * 16, p);
+        } else {
+#pragma unroll
+          for (int j = 0; j < RT / G::rows_at_once; ++j, p += next)
+            if (j * G::rows_at_once + vrow < nt) cp_async16(q + j * G::threads * 16, p);
+        }
       };
       if (vin) {
         copy(a.x, a.x_ld, 0);
@@ -109,6 +115,7 @@ palimpsa_gate_bwd_kernel(GateArgs a, int tiles, float* sums) {
   if (a.dh_T && in) carry = *reinterpret_cast<const float2*>(a.dh_T + n * a.D + ch);
   float2 sA = zero, sr = zero, si = zero;
   bool waits = true;
+  const long long yd = (long long)a.D * ES;
   if (CLUSTER) cg::this_cluster().sync();  // every CTA has started, its barriers set: it may be written to
 
   for (int k = rounds - 1; k >= 0; --k) {
@@ -124,51 +131,58 @@ palimpsa_gate_bwd_kernel(GateArgs a, int tiles, float* sums) {
 
     // The factors of g_t in dx, di, dr and dA, the decays, and dy silu(z).
     float2 da[kPiece], fx[kPiece], fi[IN ? kPiece : 1], fr[kPiece], fA[kPiece], gy[kPiece];
-    const long long at = (row0 + tp) * a.D + ch;
+    const long long at = ((row0 + tp) * a.D + ch) * ES;  // bytes
+    char* pz = static_cast<char*>(a.dz) + at;
     float2 h = np > 0 ? *reinterpret_cast<const float2*>(smem + (k & 1) * S::stage + S::h +
                                                          (warp * Tile<BF16>::CH + 2 * lane) * 4)
                       : zero;
+    auto token = [&](int t) {
+      const float2 x = load_pair<BF16>(raw + t * G::row);
+      float2 closed;  // 1 - s
+      const float2 s = sigmoid_of(ffma2(load_pair<BF16>(raw + G::bytes + t * G::row), scale, rb), &closed);
+      gy[t] = load_pair<BF16>(raw + 2 * G::bytes + t * G::row);
+      const float2 w = __fmul2_rn(A, s);
+      float2 q;  // 1 - a^2
+      decay_of(w, &da[t], &q);
+      // (A rate of 0 has 1 / n of 3e17, and no gradient: the factor w of dr, or s of dA, is 0 too.)
+      const float2 ni = make_float2(rsqrt_approx(q.x), rsqrt_approx(q.y));
+      fx[t] = __fmul2_rn(q, ni);
+      float2 u = x;
+      if (IN) {
+        float2 shut;  // 1 - p
+        const float2 p = sigmoid_of(ffma2(load_pair<BF16>(raw + kI * G::bytes + t * G::row), scale, ib), &shut);
+        fx[t] = __fmul2_rn(fx[t], p);
+        fi[t] = __fmul2_rn(__fmul2_rn(fx[t], x), shut);
+        u = __fmul2_rn(x, p);
+      }
+      const float2 old = __fmul2_rn(da[t], h);
+      // dw / g = u a^2 / n - a h
+      const float2 aa = __fmul2_rn(__fmul2_rn(da[t], da[t]), ni);
+      const float2 dw = ffma2(u, aa, make_float2(-old.x, -old.y));
+      fA[t] = __fmul2_rn(dw, s);
+      fr[t] = __fmul2_rn(__fmul2_rn(dw, w), closed);
+      h = ffma2(fx[t], x, old);
+      if (GATE) {
+        const float2 z = load_pair<BF16>(raw + kZ * G::bytes + t * G::row);
+        float2 rest;
+        const float2 c = sigmoid_of(__fmul2_rn(z, scale), &rest);
+        const float2 m = ffma2(z, rest, make_float2(1.f, 1.f));  // silu' = c (1 + z (1 - c))
+        const float2 dz = __fmul2_rn(__fmul2_rn(gy[t], h), __fmul2_rn(c, m));
+        if (in) store_pair<BF16>(pz, dz);
+        pz += yd;
+        gy[t] = __fmul2_rn(gy[t], __fmul2_rn(z, c));
+      }
+    };
+    if (np == kPiece) {
 #pragma unroll
-    for (int t = 0; t < kPiece; ++t) {
-      if (t < np) {
-        const float2 x = load_pair<BF16>(raw + t * G::row);
-        float2 closed;  // 1 - s
-        const float2 s = sigmoid_of(ffma2(load_pair<BF16>(raw + G::bytes + t * G::row), scale, rb), &closed);
-        gy[t] = load_pair<BF16>(raw + 2 * G::bytes + t * G::row);
-        const float2 w = __fmul2_rn(A, s);
-        float2 q;  // 1 - a^2
-        decay_of(w, &da[t], &q);
-        // (A rate of 0 has 1 / n of 3e17, and no gradient: the factor w of dr, or s of dA, is 0 too.)
-        const float2 ni = make_float2(rsqrt_approx(q.x), rsqrt_approx(q.y));
-        fx[t] = __fmul2_rn(q, ni);
-        float2 u = x;
-        if (IN) {
-          float2 shut;  // 1 - p
-          const float2 p = sigmoid_of(ffma2(load_pair<BF16>(raw + kI * G::bytes + t * G::row), scale, ib), &shut);
-          fx[t] = __fmul2_rn(fx[t], p);
-          fi[t] = __fmul2_rn(__fmul2_rn(fx[t], x), shut);
-          u = __fmul2_rn(x, p);
-        }
-        const float2 old = __fmul2_rn(da[t], h);
-        // dw / g = u a^2 / n - a h
-        const float2 aa = __fmul2_rn(__fmul2_rn(da[t], da[t]), ni);
-        const float2 dw = ffma2(u, aa, make_float2(-old.x, -old.y));
-        fA[t] = __fmul2_rn(dw, s);
-        fr[t] = __fmul2_rn(__fmul2_rn(dw, w), closed);
-        h = ffma2(fx[t], x, old);
-        if (GATE) {
-          const float2 z = load_pair<BF16>(raw + kZ * G::bytes + t * G::row);
-          float2 rest;
-          const float2 c = sigmoid_of(__fmul2_rn(z, scale), &rest);
-          const float2 m = ffma2(z, rest, make_float2(1.f, 1.f));  // silu' = c (1 + z (1 - c))
-          const float2 dz = __fmul2_rn(__fmul2_rn(gy[t], h), __fmul2_rn(c, m));
-          if (in) store_pair<BF16>(static_cast<char*>(a.dz) + (at + (long long)t * a.D) * ES, dz);
-          gy[t] = __fmul2_rn(gy[t], __fmul2_rn(z, c));
-        }
-      } else {
+      for (int t = 0; t < kPiece; ++t) token(t);
+    } else {
+#pragma unroll
+      for (int t = 0; t < kPiece; ++t) {
         da[t] = make_float2(1.f, 1.f);
         fx[t] = fr[t] = fA[t] = gy[t] = zero;
         if (IN) fi[t] = zero;
+        if (t < np) token(t);
       }
     }
     float2 P = make_float2(1.f, 1.f), C = zero;
@@ -220,23 +234,33 @@ palimpsa_gate_bwd_kernel(GateArgs a, int tiles, float* sums) {
     }
     if (in && np > 0) {
       float2 pA = zero, pr = zero, pi = zero;  // the piece's sums
-#pragma unroll
-      for (int t = kPiece - 1; t >= 0; --t)
-        if (t < np) {
-          const float2 g = __fadd2_rn(gy[t], c);
-          c = __fmul2_rn(da[t], g);
-          const long long o = (at + (long long)t * a.D) * ES;
-          store_pair<BF16>(static_cast<char*>(a.dx) + o, __fmul2_rn(g, fx[t]));
-          const float2 dr = __fmul2_rn(g, fr[t]);
-          store_pair<BF16>(static_cast<char*>(a.dr) + o, dr);
-          pr = __fadd2_rn(pr, dr);
-          pA = ffma2(g, fA[t], pA);
-          if (IN) {
-            const float2 di = __fmul2_rn(g, fi[t]);
-            store_pair<BF16>(static_cast<char*>(a.di) + o, di);
-            pi = __fadd2_rn(pi, di);
-          }
+      const long long last = at + (np - 1) * yd;
+      char *px = static_cast<char*>(a.dx) + last, *pg = static_cast<char*>(a.dr) + last, *pp = static_cast<char*>(a.di) + last;
+      auto out = [&](int t) {
+        const float2 g = __fadd2_rn(gy[t], c);
+        c = __fmul2_rn(da[t], g);
+        store_pair<BF16>(px, __fmul2_rn(g, fx[t]));
+        px -= yd;
+        const float2 dr = __fmul2_rn(g, fr[t]);
+        store_pair<BF16>(pg, dr);
+        pg -= yd;
+        pr = __fadd2_rn(pr, dr);
+        pA = ffma2(g, fA[t], pA);
+        if (IN) {
+          const float2 di = __fmul2_rn(g, fi[t]);
+          store_pair<BF16>(pp, di);
+          pp -= yd;
+          pi = __fadd2_rn(pi, di);
         }
+      };
+      if (np == kPiece) {
+#pragma unroll
+        for (int t = kPiece - 1; t >= 0; --t) out(t);
+      } else {
+#pragma unroll
+        for (int t = kPiece - 1; t >= 0; --t)
+          if (t < np) out(t);
+      }
       sA = __fadd2_rn(sA, pA);
       sr = __fadd2_rn(sr, pr);
       si = __fadd2_rn(si, pi);
@@ -317,8 +341,10 @@ cudaError_t backward(const GateArgs& a, float* sums, cudaStream_t s) {
 }  // namespace
 
 size_t plan_gate_backward(GateArgs* a) {
-  a->cluster = a->bf16 ? gate_plan(a->rows, a->D, Tile<true>::tokens, kResident, 64).cluster
-                       : gate_plan(a->rows, a->D, Tile<false>::tokens, 2 * kResident, 64).cluster;
+  // In fp32 an SM's shared memory holds 2 CTAs with both gates, 3 with one and 4 without.
+  const int resident = a->bf16 ? kResident : 4 - (a->i != nullptr) - (a->z != nullptr);
+  const int tokens = a->bf16 ? Tile<true>::tokens : Tile<false>::tokens;
+  a->cluster = gate_plan(a->rows, a->D, tokens, resident, 64).cluster;
   return (size_t)a->rows.n_seq * a->cluster * 3 * a->D;
 }
 
