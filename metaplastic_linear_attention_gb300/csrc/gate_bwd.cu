@@ -287,24 +287,6 @@ palimpsa_gate_bwd_kernel(GateArgs a, int tiles, float* sums) {
   if (CLUSTER) cg::this_cluster().sync();  // nobody hands anything to a CTA that has left
 }
 
-// Sums the CTAs' parts [rows, 3, D]; block y = v, 32 channels by 8 slices of the rows.
-__global__ void __launch_bounds__(256) palimpsa_gate_bwd_sum_kernel(const float* sums, long long rows, int D, float* dA,
-                                                                    float* dr_bias, float* di_bias) {
-  __shared__ float red[8][33];
-  const int cx = threadIdx.x % 32, sy = threadIdx.x / 32, ch = blockIdx.x * 32 + cx, v = blockIdx.y;
-  float* const out = v == 0 ? dA : v == 1 ? dr_bias : di_bias;
-  if (!out) return;
-  float s = 0.f;
-  if (ch < D)
-    for (long long b = sy; b < rows; b += 8) s += sums[(b * 3 + v) * D + ch];
-  red[sy][cx] = s;
-  __syncthreads();
-  if (sy == 0 && ch < D) {
-    for (int k = 1; k < 8; ++k) s += red[k][cx];
-    out[ch] = s;
-  }
-}
-
 template <bool BF16, bool IN, bool GATE, bool CLUSTER>
 cudaError_t run(const GateArgs& a, float* sums, cudaStream_t s) {
   using G = Tile<BF16>;
@@ -328,9 +310,8 @@ cudaError_t run(const GateArgs& a, float* sums, cudaStream_t s) {
   c.numAttrs = CLUSTER ? 1 : 0;
   e = cudaLaunchKernelEx(&c, kernel, a, (int)tiles, sums);
   if (e != cudaSuccess) return e;
-  palimpsa_gate_bwd_sum_kernel<<<dim3((a.D + 31) / 32, 3), 256, 0, s>>>(sums, (long long)a.rows.n_seq * a.cluster, a.D,
-                                                                        a.dA, a.dr_bias, a.di_bias);
-  return cudaGetLastError();
+  float* const out[3] = {a.dA, a.dr_bias, a.di_bias};
+  return launch_row_sums(sums, (long long)a.rows.n_seq * a.cluster, 3, a.D, out, s);
 }
 
 template <bool BF16, bool IN, bool GATE>

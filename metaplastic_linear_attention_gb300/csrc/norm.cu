@@ -473,25 +473,6 @@ palimpsa_norm_bwd_kernel(NormArgs a, float* sums) {
   }
 }
 
-// Sums the CTAs' parts [rows, 2, D]: 32 columns by 32 slices of the rows; block y = 0 dweight, 1 dbias.
-__global__ void __launch_bounds__(1024) palimpsa_norm_bwd_sum_kernel(const float* sums, int rows, int D, float* dweight,
-                                                                     float* dbias) {
-  __shared__ float red[32][33];
-  const int cx = threadIdx.x % 32, sy = threadIdx.x / 32, col = blockIdx.x * 32 + cx, v = blockIdx.y;
-  float* const out = v ? dbias : dweight;
-  if (!out) return;
-  float s = 0.f;
-  if (col < D)
-#pragma unroll 8
-    for (int b = sy; b < rows; b += 32) s += sums[((long long)b * 2 + v) * D + col];
-  red[sy][cx] = s;
-  __syncthreads();
-  s = red[cx][sy];  // column sy
-#pragma unroll
-  for (int d = 16; d > 0; d /= 2) s += __shfl_xor_sync(~0u, s, d);
-  if (cx == 0 && blockIdx.x * 32 + sy < D) out[blockIdx.x * 32 + sy] = s;
-}
-
 // A launch: as many CTAs as the rows need and the GPU holds.
 struct Shape {
   int threads, bytes, ctas;
@@ -589,8 +570,8 @@ cudaError_t launch_norm_backward(const NormArgs& a, float* scratch, cudaStream_t
     if (e != cudaSuccess) return e;
   }
   if (!a.dweight && !a.dbias) return cudaSuccess;
-  palimpsa_norm_bwd_sum_kernel<<<dim3((a.D + 31) / 32, 2), 1024, 0, s>>>(scratch, a.ctas, a.D, a.dweight, a.dbias);
-  return cudaGetLastError();
+  float* const out[2] = {a.dweight, a.dbias};
+  return launch_row_sums(scratch, a.ctas, 2, a.D, out, s);
 }
 
 }  // namespace palimpsa

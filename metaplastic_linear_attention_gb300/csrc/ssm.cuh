@@ -227,6 +227,9 @@ cudaError_t launch_gate_step(const GateArgs& a, cudaStream_t s);
 size_t plan_gate_backward(GateArgs* a);
 cudaError_t launch_gate_backward(const GateArgs& a, float* scratch, cudaStream_t s);
 
+// out[v][d] (null: not wanted) = sum over rows of parts[row, v, d]; V = 2 or 3 (row_sums.cu).
+cudaError_t launch_row_sums(const float* parts, long long rows, int V, int D, float* const* out, cudaStream_t s);
+
 // The layer norm of rows of D values, and the addition in front of it (norm.cu).
 constexpr int kNormWidth = 8192;  // the widest row
 struct NormArgs {
