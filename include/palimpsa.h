@@ -725,6 +725,11 @@ palimpsa_status palimpsa_selective_scan_backward(
     const int* cu_seqlens, int B, int T, int max_seqlen, int D, int G, int N,
     unsigned int flags, palimpsa_dtype in_dtype, void* cuda_stream);
 
+/* Options of a packed gated scan and its backward: zeros, first, in what the call leaves
+ * unwritten of its outputs, as palimpsa_zero_unwritten fills them: of the row arrays, and of
+ * the state. (Nothing in a dense batch.) */
+typedef enum { PALIMPSA_GATE_ZERO_ROWS = 1, PALIMPSA_GATE_ZERO_STATES = 2 } palimpsa_gate_flags;
+
 /* Row strides of the gated scan's inputs, in elements (0: dense). */
 typedef struct {
   long long x, r, i, z, dy;
@@ -759,7 +764,7 @@ palimpsa_status palimpsa_gated_scan(
     const float* r_bias, const float* i_bias, const float* h0,
     void* y, float* h_T, float* ckpt, const palimpsa_gate_strides* strides,
     const int* cu_seqlens, int B, int T, int max_seqlen, int D,
-    palimpsa_dtype in_dtype, void* cuda_stream);
+    unsigned int flags, palimpsa_dtype in_dtype, void* cuda_stream);
 
 /* palimpsa_gated_scan_step - one token of B sequences; h [B, D] is updated in place. */
 palimpsa_status palimpsa_gated_scan_step(
@@ -783,7 +788,7 @@ palimpsa_status palimpsa_gated_scan_backward(
     void* dx, void* dr, float* dA, void* di, void* dz,
     float* dr_bias, float* di_bias, float* dh0, const palimpsa_gate_strides* strides,
     const int* cu_seqlens, int B, int T, int max_seqlen, int D,
-    palimpsa_dtype in_dtype, void* cuda_stream);
+    unsigned int flags, palimpsa_dtype in_dtype, void* cuda_stream);
 
 /*
  * palimpsa_layer_norm - the layer norm of rows of D values, after an addition:

@@ -60,6 +60,8 @@ from .ssm import (  # noqa: F401
     palimpsa_selective_scan_step,
 )
 from .gated import (  # noqa: F401
+    PALIMPSA_GATE_ZERO_ROWS,
+    PALIMPSA_GATE_ZERO_STATES,
     palimpsa_gated_scan,
     palimpsa_gated_scan_backward,
     palimpsa_gated_scan_checkpoint_shape,

@@ -294,7 +294,8 @@ cudaError_t run(const GateArgs& a, float* sums, cudaStream_t s) {
   if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
   constexpr int bytes = BwdSmem<BF16, IN, GATE>::given + (CLUSTER ? 512 : 0);
   const auto kernel = palimpsa_gate_bwd_kernel<BF16, IN, GATE, CLUSTER>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  static SharedBytes allowed;
+  cudaError_t e = allow_shared(kernel, bytes, &allowed);
   if (e == cudaSuccess && a.cluster > 8) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute cluster = {};

@@ -322,7 +322,8 @@ cudaError_t run(const GateArgs& a, cudaStream_t s) {
   if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
   constexpr int bytes = 2 * kStageBytes<BF16, IN> + (CLUSTER ? 2 * G::group * 16 : 0);
   const auto kernel = palimpsa_gate_kernel<BF16, IN, GATE, CLUSTER, CH>;
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  static SharedBytes allowed;
+  const cudaError_t e = allow_shared(kernel, bytes, &allowed);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute cluster = {};
   cluster.id = cudaLaunchAttributeClusterDimension;
@@ -366,9 +367,7 @@ cudaError_t step(const GateArgs& a, cudaStream_t s) {
 // CTAs have the mean of the rounds (and half of one lost), but none is done before its
 // longest sequence's rounds, one after the other.
 GatePlan gate_plan(const SeqRows& r, int D, int tokens, int resident, int narrow) {
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    sms = 152;
+  const int sms = sms_of_device();
   const double slots = (double)resident * sms;
   GatePlan best = {64, 1};
   double least = 0;

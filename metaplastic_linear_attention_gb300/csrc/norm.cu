@@ -477,16 +477,24 @@ palimpsa_norm_bwd_kernel(NormArgs a, float* sums) {
 struct Shape {
   int threads, bytes, ctas;
 };
+// What an SM holds of a kernel, by its threads (a multiple of 32, up to 512); it is asked for once.
+struct Held {
+  std::atomic<int> ctas[17] = {};
+  SharedBytes allowed;
+};
 template <class K>
-cudaError_t shape_of(K kernel, const NormArgs& a, int threads, int teams, int bytes, Shape* p) {
-  int dev = 0, sms = 0, held = 0;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess) e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&held, kernel, threads, bytes);
+cudaError_t shape_of(K kernel, const NormArgs& a, int threads, int teams, int bytes, Held* known, Shape* p) {
+  cudaError_t e = allow_shared(kernel, bytes, &known->allowed);
   if (e != cudaSuccess) return e;
-  if (held < 1) return cudaErrorInvalidConfiguration;
-  *p = {threads, bytes, (int)std::max<long long>(1, std::min((long long)held * sms, (a.rows + teams - 1) / teams))};
+  std::atomic<int>& ctas = known->ctas[threads / 32];
+  int held = ctas.load(std::memory_order_relaxed);
+  if (held == 0) {
+    if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&held, kernel, threads, bytes)) != cudaSuccess) return e;
+    if (held < 1) return cudaErrorInvalidConfiguration;
+    ctas.store(held, std::memory_order_relaxed);
+  }
+  const long long most = (long long)held * sms_of_device();
+  *p = {threads, bytes, (int)std::max<long long>(1, std::min(most, (a.rows + teams - 1) / teams))};
   return cudaSuccess;
 }
 // Threads of a CTA that a row takes for itself, each with COLS columns.
@@ -501,9 +509,10 @@ cudaError_t forward(const NormArgs& a, cudaStream_t s) {
   constexpr bool kShared = kSharedParams<COLS, MULTI>;
   const auto kernel = palimpsa_norm_kernel<BF16, LANES, MULTI, COLS, R, MORE>;
   const int threads = MULTI ? row_threads<COLS>(a) : kShared ? 128 : 256;
+  static Held known;
   Shape p;
   const cudaError_t e = shape_of(kernel, a, threads, MULTI ? 1 : threads / LANES,
-                                 threads * 16 * W::S * W::planes + (kShared ? COLS * 256 : 0), &p);
+                                 threads * 16 * W::S * W::planes + (kShared ? COLS * 256 : 0), &known, &p);
   if (e != cudaSuccess) return e;
   kernel<<<p.ctas, p.threads, p.bytes, s>>>(a);
   return cudaGetLastError();
@@ -514,8 +523,10 @@ cudaError_t backward(const NormArgs& a, float* sums, int* ctas, cudaStream_t s) 
   using W = Walk<BF16, LANES, MULTI, COLS, R, 2 + MORE>;
   const auto kernel = palimpsa_norm_bwd_kernel<BF16, LANES, MULTI, COLS, R, MORE>;
   const int threads = MULTI ? row_threads<COLS>(a) : 256;
+  static Held known;
   Shape p;
-  const cudaError_t e = shape_of(kernel, a, threads, MULTI ? 1 : threads / LANES, threads * 16 * W::S * W::planes, &p);
+  const cudaError_t e = shape_of(kernel, a, threads, MULTI ? 1 : threads / LANES, threads * 16 * W::S * W::planes,
+                                 &known, &p);
   if (e != cudaSuccess) return e;
   if (ctas) {
     *ctas = p.ctas;

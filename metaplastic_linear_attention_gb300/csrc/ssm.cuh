@@ -10,6 +10,9 @@
 // [cu[n], cu[n+1]) among T rows in all.
 #pragma once
 
+#include <atomic>
+#include <mutex>
+
 #include "palimpsa_internal.cuh"
 
 namespace palimpsa {
@@ -174,6 +177,37 @@ cudaError_t launch_scan_reverse_summary(const ScanArgs& a, cudaStream_t s);
 constexpr int kFoldSegments = 18;
 // Turns the summaries into start states, in place: forward from h0, or in reverse from dh_T.
 cudaError_t launch_scan_carry(const ScanArgs& a, bool reverse, cudaStream_t s);
+
+// The current device's SMs (asked for once a device; 152 where that fails).
+inline int sms_of_device() {
+  static std::atomic<int> known[64] = {};
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 152;
+  if (dev >= 0 && dev < 64 && (sms = known[dev].load(std::memory_order_relaxed)) > 0) return sms;
+  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 152;
+  if (dev >= 0 && dev < 64) known[dev].store(sms, std::memory_order_relaxed);
+  return sms;
+}
+// Lets a kernel have `bytes` of dynamic shared memory: a call of the runtime only when this device
+// has not yet allowed it as many. `allowed` is the kernel's own.
+struct SharedBytes {
+  std::atomic<int> on[64] = {};
+  std::mutex raising;  // two calls at once must not leave the smaller of their limits
+};
+template <class K>
+cudaError_t allow_shared(K kernel, int bytes, SharedBytes* allowed) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;  // (as the library's pools)
+  std::atomic<int>& on = allowed->on[dev];
+  if (on.load() >= bytes) return cudaSuccess;
+  std::lock_guard<std::mutex> lock(allowed->raising);
+  if (on.load() >= bytes) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) on.store(bytes);
+  return e;
+}
 
 // The gated scan: one state per channel, gates from the token (formulas in gate_fwd.cu).
 struct GateArgs {

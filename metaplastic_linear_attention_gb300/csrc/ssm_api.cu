@@ -87,8 +87,9 @@ palimpsa_status scan_strides(ScanArgs* a, const palimpsa_scan_strides* st, palim
   return s;
 }
 
-palimpsa_status gate_checks(const GateArgs& a, palimpsa_dtype t) {
+palimpsa_status gate_checks(const GateArgs& a, palimpsa_dtype t, unsigned int flags) {
   if (!dtype_ok(t)) return PALIMPSA_ERR_DTYPE;
+  if (flags & ~(unsigned)(PALIMPSA_GATE_ZERO_ROWS | PALIMPSA_GATE_ZERO_STATES)) return PALIMPSA_ERR_UNSUPPORTED;
   if (!rows_ok(a.rows, a.D)) return PALIMPSA_ERR_SHAPE;
   if (a.D % 8) return PALIMPSA_ERR_UNSUPPORTED;
   return aligned_all({a.x, a.r, a.i, a.z, a.h0, a.y, a.h_T, a.ckpt, a.ckpt_in, a.dy, a.dh_T, a.dx, a.dr, a.di, a.dz, a.dh0},
@@ -104,6 +105,25 @@ palimpsa_status gate_strides(GateArgs* a, const palimpsa_gate_strides* st, palim
   if (!s) s = stride_of(st->z, a->D, t, &a->z_ld);
   if (!s) s = stride_of(st->dy, a->D, t, &a->dy_ld);
   return s;
+}
+
+// Zeros, as the flags ask, in what a packed call leaves as it is of its row arrays and its state array.
+template <int N>
+cudaError_t zero_for_gate(const GateArgs& a, unsigned int flags, void* const (&rows)[N], void* state, cudaStream_t s) {
+  if (!a.rows.cu || !flags) return cudaSuccess;
+  ZeroArgs z{};
+  z.rows = a.rows;
+  int k = 0;
+  auto add = [&](void* p, long long bytes) {
+    if (!p) return;
+    z.p[k] = p;
+    z.width[k++] = bytes;
+  };
+  if ((flags & PALIMPSA_GATE_ZERO_ROWS) && a.rows.T > 0)
+    for (void* p : rows) add(p, (long long)a.D * (a.bf16 ? 2 : 4));
+  z.row_arrays = k;
+  if (flags & PALIMPSA_GATE_ZERO_STATES) add(state, (long long)a.D * 4);
+  return launch_zero_outside(z, k, s);
 }
 
 GateArgs gate_args(const void* x, const void* r, const float* A, const void* i, const void* z, const float* r_bias,
@@ -398,7 +418,8 @@ size_t palimpsa_gated_scan_checkpoint_bytes(int B, int T, int packed, int D) {
 palimpsa_status palimpsa_gated_scan(const void* x, const void* r, const float* A, const void* i, const void* z,
                                     const float* r_bias, const float* i_bias, const float* h0, void* y, float* h_T,
                                     float* ckpt, const palimpsa_gate_strides* strides, const int* cu_seqlens, int B, int T,
-                                    int max_seqlen, int D, palimpsa_dtype in_dtype, void* cuda_stream) {
+                                    int max_seqlen, int D, unsigned int flags, palimpsa_dtype in_dtype,
+                                    void* cuda_stream) {
   if (!A || !h_T || (T != 0 && (!x || !r || !y || (i_bias && !i)))) return PALIMPSA_ERR_NULL;
   GateArgs a = gate_args(x, r, A, i, z, r_bias, i_bias, D, in_dtype);
   a.h0 = h0;
@@ -406,11 +427,12 @@ palimpsa_status palimpsa_gated_scan(const void* x, const void* r, const float* A
   a.h_T = h_T;
   a.ckpt = ckpt;
   a.rows = rows_of(cu_seqlens, B, T, max_seqlen);
-  if (palimpsa_status s = gate_checks(a, in_dtype)) return s;
+  if (palimpsa_status s = gate_checks(a, in_dtype, flags)) return s;
   if (palimpsa_status s = gate_strides(&a, strides, in_dtype)) return s;
   if (palimpsa_status s = device_status_word(&a.status)) return s;
-  return launch_gate_forward(a, static_cast<cudaStream_t>(cuda_stream)) == cudaSuccess ? PALIMPSA_OK
-                                                                                     : PALIMPSA_ERR_CUDA;
+  const cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
+  if (zero_for_gate(a, flags, {y}, h_T, s) != cudaSuccess) return PALIMPSA_ERR_CUDA;
+  return launch_gate_forward(a, s) == cudaSuccess ? PALIMPSA_OK : PALIMPSA_ERR_CUDA;
 }
 
 palimpsa_status palimpsa_gated_scan_step(const void* x, const void* r, const float* A, const void* i, const void* z,
@@ -422,7 +444,7 @@ palimpsa_status palimpsa_gated_scan_step(const void* x, const void* r, const flo
   a.y = y;
   a.h_T = h;
   a.rows = rows_of(nullptr, B, 1, 1);
-  if (palimpsa_status s = gate_checks(a, in_dtype)) return s;
+  if (palimpsa_status s = gate_checks(a, in_dtype, 0)) return s;
   if (palimpsa_status s = gate_strides(&a, strides, in_dtype)) return s;
   if (palimpsa_status s = device_status_word(&a.status)) return s;
   return launch_gate_step(a, static_cast<cudaStream_t>(cuda_stream)) == cudaSuccess ? PALIMPSA_OK
@@ -434,7 +456,8 @@ palimpsa_status palimpsa_gated_scan_backward(const void* x, const void* r, const
                                              const float* dh_T, void* dx, void* dr, float* dA, void* di, void* dz,
                                              float* dr_bias, float* di_bias, float* dh0,
                                              const palimpsa_gate_strides* strides, const int* cu_seqlens, int B, int T,
-                                             int max_seqlen, int D, palimpsa_dtype in_dtype, void* cuda_stream) {
+                                             int max_seqlen, int D, unsigned int flags, palimpsa_dtype in_dtype,
+                                             void* cuda_stream) {
   if (!A || !dA || (T != 0 && (!x || !r || !ckpt || !dy || !dx || !dr || (i && !di) || (z && !dz) || (i_bias && !i))))
     return PALIMPSA_ERR_NULL;
   GateArgs a = gate_args(x, r, A, i, z, r_bias, i_bias, D, in_dtype);
@@ -450,10 +473,11 @@ palimpsa_status palimpsa_gated_scan_backward(const void* x, const void* r, const
   a.di_bias = di_bias;
   a.dh0 = dh0;
   a.rows = rows_of(cu_seqlens, B, T, max_seqlen);
-  if (palimpsa_status s = gate_checks(a, in_dtype)) return s;
+  if (palimpsa_status s = gate_checks(a, in_dtype, flags)) return s;
   if (palimpsa_status s = gate_strides(&a, strides, in_dtype)) return s;
   if (palimpsa_status s = device_status_word(&a.status)) return s;
   const cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
+  if (zero_for_gate(a, flags, {dx, dr, di, dz}, dh0, s) != cudaSuccess) return PALIMPSA_ERR_CUDA;
   float* scratch = nullptr;
   if (acquire_scratch(plan_gate_backward(&a) * sizeof(float), s, &scratch) != cudaSuccess) return PALIMPSA_ERR_CUDA;
   return release(launch_gate_backward(a, scratch, s), scratch, s);

@@ -8,8 +8,9 @@ import ctypes
 
 import torch
 
-from .ssm import F32, _batch, _call, _dense, _device, _dtype, _like, _new, _on_stream, _ptr, _rows, _zero_fresh, _zero_unwritten
+from .ssm import F32, _batch, _call, _dense, _device, _dtype, _like, _new, _on_stream, _ptr, _rows
 
+PALIMPSA_GATE_ZERO_ROWS, PALIMPSA_GATE_ZERO_STATES = 1, 2   # palimpsa_gate_flags
 CHECKPOINT_TOKENS = 8
 
 
@@ -50,16 +51,18 @@ def _scan(name, x, r, A, i, z, r_bias, i_bias, h0, cu_seqlens, max_seqlen, y, h_
     ch, strides, ptrs = _inputs(x, r, A, i, z, r_bias, i_bias, dev, lead)
     kind = _dtype(x)
     p0 = _dense(h0, "h0", (nb, ch), F32, dev)
-    given = y, h_T
+    fill = 0    # of a packed call's fresh outputs, what it leaves unwritten
     if y is None:
-        y = _like(x)
+        y, fill = _like(x), PALIMPSA_GATE_ZERO_ROWS
     else:
         _dense(y, "y", x.shape, x.dtype, dev)
+    if h_T is None:
+        fill |= PALIMPSA_GATE_ZERO_STATES
     h_T = _new(h_T, "h_T", (nb, ch), F32, x)
-    _zero_fresh(given, (y, h_T), cu, nb, T, longest, dev)
     if want_ckpt:
         ckpt = _new(ckpt, "ckpt", palimpsa_gated_scan_checkpoint_shape(nb, T, ch, cu is not None), F32, x)
-    _call(name, dev, *ptrs, p0, y.data_ptr(), h_T.data_ptr(), _ptr(ckpt), strides, _ptr(cu), nb, T, longest, ch, kind)
+    _call(name, dev, *ptrs, p0, y.data_ptr(), h_T.data_ptr(), _ptr(ckpt), strides, _ptr(cu), nb, T, longest, ch, fill,
+          kind)
     return y, h_T, ckpt
 
 
@@ -104,11 +107,10 @@ def palimpsa_gated_scan_backward(x, r, A, i, z, r_bias, i_bias, ckpt, dy, dh_T=N
         g["dz"] = _like(x)
     if want_state_grad:
         g["dh0"] = torch.empty((nb, ch), dtype=F32, device=x.device)
-    _zero_unwritten([g[k] for k in ("dx", "dr", "di", "dz") if k in g], (g["dh0"],) if want_state_grad else (), cu, nb, T,
-                    longest, dev)
     at = {k: v.data_ptr() for k, v in g.items()}
     _call(name, dev, *ptrs, pc, dy.data_ptr(), pg, at["dx"], at["dr"], at["dA"], at.get("di"), at.get("dz"), at["dr_bias"],
-          at.get("di_bias"), at.get("dh0"), strides, _ptr(cu), nb, T, longest, ch, kind)
+          at.get("di_bias"), at.get("dh0"), strides, _ptr(cu), nb, T, longest, ch,
+          PALIMPSA_GATE_ZERO_ROWS | PALIMPSA_GATE_ZERO_STATES, kind)
     return g
 
 

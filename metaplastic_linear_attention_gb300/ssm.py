@@ -47,9 +47,9 @@ def _library():
             "palimpsa_selective_scan_step": [p] * 10 + [st, i, i, i, i, u, i, p],
             "palimpsa_selective_scan_backward": [p] * 20 + [st, p, i, i, i, i, i, i, u, i, p],
             # gated.py and norm.py
-            "palimpsa_gated_scan": [p] * 13 + [i] * 5 + [p],
+            "palimpsa_gated_scan": [p] * 13 + [i] * 4 + [u, i, p],
             "palimpsa_gated_scan_step": [p] * 10 + [i] * 3 + [p],
-            "palimpsa_gated_scan_backward": [p] * 20 + [i] * 5 + [p],
+            "palimpsa_gated_scan_backward": [p] * 20 + [i] * 4 + [u, i, p],
             "palimpsa_layer_norm": [p, ll, p, ll, p, p, p, p, p, ll, i, ctypes.c_float, i, p],
             "palimpsa_layer_norm_backward": [p, ll, p, p, p, ll, p, ll, p, p, p, ll, i, i, p],
         }

@@ -20,10 +20,10 @@ def lib():
 
 
 SCAN = dict(x=P, r=P, A=P, i=None, z=None, r_bias=None, i_bias=None, h0=None, y=P, h_T=P, ckpt=None, strides=None, cu=None,
-            B=2, T=16, max_seqlen=16, D=64, dtype=1)
+            B=2, T=16, max_seqlen=16, D=64, flags=0, dtype=1)
 STEP = dict(x=P, r=P, A=P, i=None, z=None, r_bias=None, i_bias=None, h=P, y=P, strides=None, B=2, D=64, dtype=1)
 BWD = dict(x=P, r=P, A=P, i=None, z=None, r_bias=None, i_bias=None, ckpt=P, dy=P, dh_T=None, dx=P, dr=P, dA=P, di=None, dz=None,
-           dr_bias=None, di_bias=None, dh0=None, strides=None, cu=None, B=2, T=16, max_seqlen=16, D=64, dtype=1)
+           dr_bias=None, di_bias=None, dh0=None, strides=None, cu=None, B=2, T=16, max_seqlen=16, D=64, flags=0, dtype=1)
 NORM = dict(x=P, x_stride=0, residual=None, residual_stride=0, weight=None, bias=None, y=P, sum=None, stats=None, rows=16, D=64,
             eps=1e-5, dtype=1)
 NORM_BWD = dict(s=P, s_stride=0, weight=None, stats=P, dy=P, dy_stride=0, ds=None, ds_stride=0, dx=P, dweight=None, dbias=None,
@@ -78,7 +78,7 @@ def test_scan_refusals(lib, name, over, code):
 @pytest.mark.parametrize("name", PACKED)
 @pytest.mark.parametrize("over,code", [
     (dict(T=-1), ERR_SHAPE), (dict(T=0x7fffffff, B=1, D=8), ERR_SHAPE), (dict(cu=P, max_seqlen=17), ERR_SHAPE),
-    (dict(cu=P, max_seqlen=-1), ERR_SHAPE), (dict(cu=P + 2), ERR_ALIGN), (dict(ckpt=P + 4), ERR_ALIGN),
+    (dict(cu=P, max_seqlen=-1), ERR_SHAPE), (dict(cu=P + 2), ERR_ALIGN), (dict(ckpt=P + 4), ERR_ALIGN), (dict(flags=4), ERR_UNSUPPORTED),
 ])
 def test_batch_refusals(lib, name, over, code):
     assert _call(lib, name, **over) == code
