@@ -5,8 +5,8 @@
 // (ds: the gradient that reaches s past the norm; x and residual both receive ds'.)
 //
 // Bound by HBM: 4 bytes a value in bf16 (8 with a residual), backward 6 (8), against some 15 and
-// 20 operations. A row's team of threads, each with 8 to 64 columns, is a quarter of
-// a warp (up to 64 columns), a warp (forward up to 2048, backward up to 512) or a CTA.
+// 20 operations. A row's team of threads, each with 8 to 64 columns, is 4 to 16
+// lanes (up to 128 columns), a warp (forward up to 2048, backward up to 512) or a CTA.
 // A grid of as many CTAs as the GPU holds walks the rows; the next ones come by asynchronous
 // copies into a ring in shared memory, each thread its own columns, so the copies need no barrier.
 // The squares are summed about the row's mean, which is known by then; where a row is a CTA's,
@@ -101,22 +101,24 @@ struct Walk {
   }
 };
 
-// A thread's columns of a parameter vector: in registers, or, for long rows of one warp, in
-// shared memory, where all the CTA's teams read them: [vector][4 of its columns][lane].
+// A thread's columns of a parameter vector: in registers, or, where a thread has more than 16, in
+// shared memory, where all the CTA's teams read them: [vector][4 of its columns][thread of the team].
 template <class W, bool SHARED>
 struct Param {
   float2 f[SHARED ? 1 : W::V][W::P];
   const float4* at;
+  int size;
   __device__ __forceinline__ Param(const W& w, const float* p, float otherwise, float4* shared) {
     if constexpr (SHARED) {
       constexpr int Q = W::N / 4;
-      for (int k = threadIdx.x; k < W::V * 32 * Q; k += blockDim.x) {
-        const int c = k * 4;  // of 4 columns: vector (k / Q) of the row, lane (k / Q) % 32 of vector (k / Q) / 32
+      for (int k = threadIdx.x; k < W::V * w.team_size * Q; k += blockDim.x) {
+        const int c = k * 4, unit = k / Q;  // 4 columns, of the row's vector `unit`
         float4 u = make_float4(otherwise, otherwise, otherwise, otherwise);
         if (p && c < w.nv * W::N) u = make_float4(p[c], p[c + 1], p[c + 2], p[c + 3]);
-        shared[(k / Q / 32 * Q + k % Q) * 32 + k / Q % 32] = u;
+        shared[(unit / w.team_size * Q + k % Q) * w.team_size + unit % w.team_size] = u;
       }
       at = shared + w.t;
+      size = w.team_size;
     } else {
 #pragma unroll
       for (int v = 0; v < W::V; ++v)
@@ -131,7 +133,7 @@ struct Param {
       constexpr int Q = W::N / 4;
 #pragma unroll
       for (int q = 0; q < Q; ++q) {
-        const float4 u = at[(v * Q + q) * 32];
+        const float4 u = at[(v * Q + q) * size];
         out[2 * q] = make_float2(u.x, u.y);
         out[2 * q + 1] = make_float2(u.z, u.w);
       }
@@ -179,11 +181,11 @@ __device__ __forceinline__ float rsqrt_of(float x) {
   return y * fmaf(-0.5f * x * y, y, 1.5f);
 }
 
-template <int COLS, bool MULTI>
-constexpr bool kSharedParams = !MULTI && COLS > 16;
+template <int COLS>
+constexpr bool kSharedParams = COLS > 16;
 
 template <bool BF16, int LANES, bool MULTI, int COLS, int R, bool RES>
-__global__ void __launch_bounds__(MULTI ? 512 : COLS > 16 ? 128 : 256, MULTI ? 1 : COLS == 16 ? 3 : 4)
+__global__ void __launch_bounds__(COLS > 16 && !MULTI ? 128 : 256, MULTI ? 2 : COLS == 16 ? 3 : 4)
 palimpsa_norm_kernel(NormArgs a) {
   using W = Walk<BF16, LANES, MULTI, COLS, R, 1 + RES>;
   constexpr int V = W::V, P = W::P;
@@ -211,9 +213,9 @@ palimpsa_norm_kernel(NormArgs a) {
   };
 #pragma unroll
   for (int k = 0; k < W::S - 1; ++k) stage();
-  constexpr bool kShared = kSharedParams<COLS, MULTI>;
+  constexpr bool kShared = kSharedParams<COLS>;
   float4* const shared = reinterpret_cast<float4*>(smem + W::plane(W::S * W::planes));
-  const Param<W, kShared> weight(at, a.weight, 1.f, shared), bias(at, a.bias, 0.f, shared + COLS * 8);
+  const Param<W, kShared> weight(at, a.weight, 1.f, shared), bias(at, a.bias, 0.f, shared + COLS / 4 * at.team_size);
   if (kShared) __syncthreads();
   // Values of warp w's part of a row.
   auto count = [&](int w) {
@@ -506,13 +508,13 @@ int row_threads(const NormArgs& a) {
 template <bool BF16, int LANES, bool MULTI, int COLS, int R, bool MORE>
 cudaError_t forward(const NormArgs& a, cudaStream_t s) {
   using W = Walk<BF16, LANES, MULTI, COLS, R, 1 + MORE>;
-  constexpr bool kShared = kSharedParams<COLS, MULTI>;
+  constexpr bool kShared = kSharedParams<COLS>;
   const auto kernel = palimpsa_norm_kernel<BF16, LANES, MULTI, COLS, R, MORE>;
   const int threads = MULTI ? row_threads<COLS>(a) : kShared ? 128 : 256;
   static Held known;
   Shape p;
   const cudaError_t e = shape_of(kernel, a, threads, MULTI ? 1 : threads / LANES,
-                                 threads * 16 * W::S * W::planes + (kShared ? COLS * 256 : 0), &known, &p);
+                                 threads * 16 * W::S * W::planes + (kShared ? 8 * COLS * (MULTI ? threads : LANES) : 0), &known, &p);
   if (e != cudaSuccess) return e;
   kernel<<<p.ctas, p.threads, p.bytes, s>>>(a);
   return cudaGetLastError();
@@ -538,17 +540,21 @@ cudaError_t backward(const NormArgs& a, float* sums, int* ctas, cudaStream_t s) 
 
 template <bool BF16, bool MORE>
 cudaError_t forward_by_width(const NormArgs& a, cudaStream_t s) {
+  if (a.D <= 32) return forward<BF16, 4, false, 8, 2, MORE>(a, s);
   if (a.D <= 64) return forward<BF16, 8, false, 8, 2, MORE>(a, s);
+  if (a.D <= 128) return forward<BF16, 16, false, 8, 2, MORE>(a, s);
   if (a.D <= 256) return forward<BF16, 32, false, 8, 2, MORE>(a, s);
   if (a.D <= 512) return forward<BF16, 32, false, 16, 2, MORE>(a, s);
   if (a.D <= 1024) return forward<BF16, 32, false, 32, 1, MORE>(a, s);
   if (a.D <= 1536) return forward<BF16, 32, false, 48, 1, MORE>(a, s);
   if (a.D <= 2048) return forward<BF16, 32, false, 64, 1, MORE>(a, s);
-  return forward<BF16, 32, true, 16, BF16 ? 2 : 1, MORE>(a, s);
+  return forward<BF16, 32, true, 32, 1, MORE>(a, s);
 }
 template <bool BF16, bool MORE>
 cudaError_t backward_by_width(const NormArgs& a, float* sums, int* ctas, cudaStream_t s) {
+  if (a.D <= 32) return backward<BF16, 4, false, 8, BF16 ? 2 : 1, MORE>(a, sums, ctas, s);
   if (a.D <= 64) return backward<BF16, 8, false, 8, BF16 ? 2 : 1, MORE>(a, sums, ctas, s);
+  if (a.D <= 128) return backward<BF16, 16, false, 8, BF16 ? 2 : 1, MORE>(a, sums, ctas, s);
   if (a.D <= 256) return backward<BF16, 32, false, 8, BF16 ? 2 : 1, MORE>(a, sums, ctas, s);
   if (a.D <= 512) return backward<BF16, 32, false, 16, BF16 ? 2 : 1, MORE>(a, sums, ctas, s);
   return backward<BF16, 32, true, 16, BF16 ? 2 : 1, MORE>(a, sums, ctas, s);
