@@ -841,11 +841,12 @@ int palimpsa_abi_version(void);
 /*
  * Failure-detection controls (process-wide; for tests).
  * palimpsa_set_wait_timeout_ns sets how long a kernel waits for a staged copy
- * before it records PALIMPSA_ERR_TIMEOUT and returns (default 2e9 ns).
+ * (or a neighbour's state) before it records PALIMPSA_ERR_TIMEOUT and returns (default 2e9 ns).
  * palimpsa_debug_withhold_first_copy(1) makes the next chunked launches skip
  * issuing their first staged copy, so that their wait can never be satisfied
- * and must run out; 0 restores normal operation. Neither changes results
- * otherwise.
+ * and must run out; 0 restores normal operation. In the gated scan it makes the
+ * first CTA of a cluster hand no state (or gradient) on in its first round, so that the
+ * others' waits run out. Neither changes results otherwise.
  */
 void palimpsa_set_wait_timeout_ns(uint64_t ns);
 void palimpsa_debug_withhold_first_copy(int on);

@@ -217,6 +217,7 @@ palimpsa_status step_sequence_impl(const void* q, const void* k, const void* v, 
 
 palimpsa_status device_status_word(unsigned int** out) { return status_word(out); }
 unsigned long long wait_timeout_ns() { return g_wait_timeout_ns.load(); }
+int withhold_first() { return g_withhold_first_copy.load(); }
 cudaError_t acquire_scratch(size_t bytes, cudaStream_t s, float** p) {
   StreamOrderedScratch scratch;
   return scratch.acquire(bytes, s, p);

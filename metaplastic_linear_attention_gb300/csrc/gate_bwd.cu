@@ -125,7 +125,7 @@ palimpsa_gate_bwd_kernel(GateArgs a, int tiles, float* sums) {
     cp_async_wait<0>();
     const int turn = rounds - 1 - k;
     const bool end = turn == 0 && rank == cs - 1;  // nothing comes from behind
-    if (CLUSTER && tid == 0) mbar_arrive_expect_tx(&bars[turn & 1], end ? 0 : 256);
+    if (CLUSTER && tid == 0 && waits) mbar_arrive_expect_tx(&bars[turn & 1], end ? 0 : 256);
     __syncthreads();  // the round's inputs are here; the other stage and the summaries are free
     stage(k - 1);
 
@@ -222,7 +222,9 @@ palimpsa_gate_bwd_kernel(GateArgs a, int tiles, float* sums) {
         const int next = rank == 0 ? turn + 1 : turn;  // the turn of the CTA before
         if (next < rounds) {
           const int to = rank == 0 ? cs - 1 : rank - 1;
-          st_async(cluster_addr(given + (next & 1) * 32, to), Cc, cluster_addr(&bars[next & 1], to));
+          // (Where a wait has run out, nothing more is handed on: the others' waits run out too.)
+          if (waits && !(a.withhold && end))
+            st_async(cluster_addr(given + (next & 1) * 32, to), Cc, cluster_addr(&bars[next & 1], to));
         } else if (in && a.dh0) {
           *reinterpret_cast<float2*>(a.dh0 + n * a.D + ch) = Cc;
         }

@@ -155,7 +155,7 @@ __global__ void __launch_bounds__(BF16 ? 128 : 64, kResident) palimpsa_gate_kern
     // A piece's summary: products and states of the lane's channels.
     auto sums_of = [&](int p) { return reinterpret_cast<float4*>(tile + p * kPiece * G::row) + lane; };
     cp_async_wait<0>();
-    if (CLUSTER && tid == 0) mbar_arrive_expect_tx(&bars[k & 1], k + rank > 0 ? LG * 16 : 0);
+    if (CLUSTER && tid == 0 && waits) mbar_arrive_expect_tx(&bars[k & 1], k + rank > 0 ? LG * 16 : 0);
     __syncthreads();  // the round's inputs are here; the other stage and the summaries are free
     stage(k + 1);
 
@@ -233,7 +233,9 @@ __global__ void __launch_bounds__(BF16 ? 128 : 64, kResident) palimpsa_gate_kern
         const int next = rank + 1 == cs ? k + 1 : k;  // its round
         if (next < rounds) {
           const int to = rank + 1 == cs ? 0 : rank + 1;
-          st_async(cluster_addr(states + (next & 1) * LG, to), Hc.all(), cluster_addr(&bars[next & 1], to));
+          // (Where a wait has run out, nothing more is handed on: the others' waits run out too.)
+          if (waits && !(a.withhold && k + rank == 0))
+            st_async(cluster_addr(states + (next & 1) * LG, to), Hc.all(), cluster_addr(&bars[next & 1], to));
         } else if (in) {
           *reinterpret_cast<float4*>(a.h_T + n * a.D + ch) = Hc.all();
         }

@@ -5,10 +5,11 @@
 
 namespace palimpsa {
 
-// api.cu: the device's status word, the limit of a device wait, and scratch from the library's pool (freed
+// api.cu: the device's status word, the limit of a device wait and the test of it, and scratch from the library's pool (freed
 // with cudaFreeAsync).
 palimpsa_status device_status_word(unsigned int** out);
 unsigned long long wait_timeout_ns();
+int withhold_first();
 cudaError_t acquire_scratch(size_t bytes, cudaStream_t s, float** p);
 
 namespace {
@@ -139,6 +140,7 @@ GateArgs gate_args(const void* x, const void* r, const float* A, const void* i, 
   a.D = D;
   a.bf16 = t == PALIMPSA_BF16;
   a.wait_timeout_ns = wait_timeout_ns();
+  a.withhold = withhold_first();
   return a;
 }
 

@@ -411,3 +411,30 @@ def test_two_streams_at_once():
             for p, q in zip(w, g):
                 assert torch.equal(p, q)
     _status()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_a_state_that_is_not_handed_on_times_out(dtype):
+    """One long sequence, shared by a cluster whose first CTA withholds its first state (gradient): the others' bounded
+    waits run out, the kernels latch PALIMPSA_ERR_TIMEOUT and end, and later calls work."""
+    i = _dev(_dense(_inputs(51, 1500, 1, 64, dtype), 1))
+    want = pal.palimpsa_gated_scan_checkpointed(*i.values())
+    args = list(i.values())[:-1]
+    grads = pal.palimpsa_gated_scan_backward(*args, want[2], i["x"])
+    _status()
+    pal.palimpsa_set_wait_timeout_ns(2_000_000)
+    pal.palimpsa_debug_withhold_first_copy(True)
+    try:
+        pal.palimpsa_gated_scan(*i.values())
+        assert pal.palimpsa_get_device_status() == 8
+        pal.palimpsa_gated_scan_backward(*args, want[2], i["x"])
+        assert pal.palimpsa_get_device_status() == 8
+    finally:
+        pal.palimpsa_debug_withhold_first_copy(False)
+        pal.palimpsa_set_wait_timeout_ns(2_000_000_000)
+    for a, b in zip(want, pal.palimpsa_gated_scan_checkpointed(*i.values())):
+        assert torch.equal(a, b)
+    again = pal.palimpsa_gated_scan_backward(*args, want[2], i["x"])
+    for k in grads:
+        assert torch.equal(grads[k], again[k])
+    _status()
