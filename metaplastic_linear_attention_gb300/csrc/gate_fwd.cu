@@ -8,9 +8,9 @@
 // (0.47) of an SM's share of the measured 6.77 TB/s, against 3 2^x, 2 reciprocals and a
 // root on the SFU (0.28 clocks; a 2^x and a reciprocal more with z) and about 30 FP32
 // operations. So every input is read once: a thread takes 8 tokens of 4 channels (a piece),
-// forms their decays and inputs a, b in registers, and runs them twice, first from 0 for
-// the piece's summary (the product of its a and its end state), then, with the state
-// before the piece known, for the states themselves. (4 tokens and twice the threads took 1.3
+// forms their decays and inputs a, b in registers and runs them from 0, keeping for each token
+// the product P of the a's and the state H so far; with the state h before the piece
+// known, the states are P h + H. The last of them are the piece's summary. (4 tokens and twice the threads took 1.3
 // times as long: what a round costs a thread besides its tokens is a fifth of it.) The
 // summaries of a CTA's pieces (groups of 16 or 8 threads, along time) pass through shared
 // memory, and every thread folds the ones before its own. A CTA walks its sequence in rounds
@@ -190,8 +190,9 @@ __global__ void __launch_bounds__(BF16 ? 128 : 64, kResident) palimpsa_gate_kern
     for (int t = 0; t < kPiece; ++t)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        H.v[j] = ffma2(da[t][j], H.v[j], b[t][j]);
-        P.v[j] = __fmul2_rn(P.v[j], da[t][j]);
+        // (In their places: the state after the token is then P h + H, with h the one before the piece.)
+        b[t][j] = H.v[j] = ffma2(da[t][j], H.v[j], b[t][j]);
+        da[t][j] = P.v[j] = __fmul2_rn(P.v[j], da[t][j]);
       }
     __syncwarp();  // the piece's rows of x are read
     sums_of(piece)[0] = P.all();
@@ -249,7 +250,7 @@ __global__ void __launch_bounds__(BF16 ? 128 : 64, kResident) palimpsa_gate_kern
       auto out = [&](int t) {
         float2 y[2];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) y[j] = h.v[j] = ffma2(da[t][j], h.v[j], b[t][j]);
+        for (int j = 0; j < 2; ++j) y[j] = ffma2(da[t][j], h.v[j], b[t][j]);
         if (GATE) {
           float2 f[2];
           Q::unpack(z[t], f);
