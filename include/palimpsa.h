@@ -803,6 +803,8 @@ palimpsa_status palimpsa_gated_scan_backward(
  *   stats        NULL, or [rows, 2] fp32 (8-byte aligned): mean and 1 / sqrt(variance + eps)
  *                of every row, for the backward
  *   rows >= 0 (with 0 the row arrays may be NULL); D a multiple of 8, at most 8192; eps > 0.
+ * A row with infinities or NaN gives NaN, in that row alone. A row whose squared deviations
+ * pass fp32's range (deviations above 1e19) is taken to have an infinite deviation: y = bias.
  */
 palimpsa_status palimpsa_layer_norm(
     const void* x, long long x_stride, const void* residual, long long residual_stride,

@@ -87,15 +87,15 @@ __device__ __forceinline__ float2 sigmoid_of(float2 x, float2* rest) {
 // memory gathers a's own error over the tokens it remembers. So below 0.3 both come from
 // m = 1 - a = w phi(w), with phi = (1 - e^-w) / w by the polynomial of degree 4 that is
 // closest to it over [0, 0.3] (found by an exchange of its extrema; 6e-9 off at most). Above,
-// a is the SFU's 2^x and 1 - a > 0.25 does not cancel. (1 - a^2 is at least 1e-35, so that
-// its root has a reciprocal.)
+// a is the SFU's 2^x and 1 - a > 0.25 does not cancel. (1 - a^2 is kept at 4e-38 and above, a
+// normal number, so that its root has a reciprocal.)
 __device__ __forceinline__ void decay_of(float2 w, float2* a, float2* rest) {
   float2 m = make_float2(0.00735594891f, 0.00735594891f);
   m = __ffma2_rn(m, w, make_float2(-0.0414141268f, -0.0414141268f));
   m = __ffma2_rn(m, w, make_float2(0.166639641f, 0.166639641f));
   m = __ffma2_rn(m, w, make_float2(-0.499998987f, -0.499998987f));
   m = __ffma2_rn(m, w, make_float2(1.f, 1.f));
-  m = __ffma2_rn(m, w, make_float2(1e-35f, 1e-35f));
+  m = __ffma2_rn(m, w, make_float2(2e-38f, 2e-38f));
   const float2 u = __fmul2_rn(w, make_float2(-kLog2e, -kLog2e));
   const float2 e = make_float2(ex2_approx(u.x), ex2_approx(u.y));
   const float2 far = __ffma2_rn(e, make_float2(-1.f, -1.f), make_float2(1.f, 1.f));
@@ -114,6 +114,7 @@ __device__ __forceinline__ float2 input_of(float2 rest, float2 q, float2 x) {
 __device__ __forceinline__ float2 input_of(float2 rest, float2 x) {
   return __fmul2_rn(__fmul2_rn(rest, x), make_float2(rsqrt_approx(rest.x), rsqrt_approx(rest.y)));
 }
+
 // The address of a shared object in another CTA of the cluster, 16 or 8 bytes stored there, counted
 // on a barrier of that CTA, and the wait for them.
 __device__ __forceinline__ uint32_t cluster_addr(const void* p, int rank) {

@@ -9,17 +9,20 @@
 // root on the SFU (0.28 clocks; a 2^x and a reciprocal more with z) and about 30 FP32
 // operations. So every input is read once: a thread takes 8 tokens of 4 channels (a piece),
 // forms their decays and inputs a, b in registers and runs them from 0, keeping for each token
-// the product P of the a's and the state H so far; with the state h before the piece
-// known, the states are P h + H. The last of them are the piece's summary. (4 tokens and twice the threads took 1.3
-// times as long: what a round costs a thread besides its tokens is a fifth of it.) The
+// the product P of the a's and the state H so far; with the state h before the piece known, the
+// states are P h + H. The last P and H are the piece's summary. (4 tokens and twice the threads
+// took 1.3 times as long: what a round costs a thread besides its tokens is a fifth of it.) The
 // summaries of a CTA's pieces (groups of 16 or 8 threads, along time) pass through shared
-// memory, and every thread folds the ones before its own. A CTA walks its sequence in rounds
-// of such tiles, the next round's inputs coming by asynchronous copies meanwhile. Where
-// the CTAs are too few, those of a cluster take turns along time: each gets the state before its
-// tile from the one before it and hands on the state after it, as an asynchronous store into
-// the next one's shared memory that a barrier there counts. (A ring: with all summaries sent
-// to all, the CTAs of a cluster went in step, and 8 x 4096 x 1536 took
-// 83 us, now 78.)
+// memory, and every thread folds the ones before its own. A CTA walks its sequence in rounds of
+// such tiles, the next round's inputs coming by asynchronous copies meanwhile. Where the CTAs are
+// too few, those of a cluster take turns along time: each gets the state before its tile from
+// the one before it and hands on the state after it, as an asynchronous store into the next
+// one's shared memory that a barrier there counts. (A ring: with all summaries sent to all, the
+// CTAs of a cluster went in step, and 8 x 4096 x 1536 took 83 us, now 78.)
+// Measured (GB300, bf16): 78 us at 8 x 4096 x 1536 without z (5.2 TB/s, 59 at the rate of a
+// copy), 164 at 1 x 32768 x 2048 with z (4.1 TB/s, 99), in fp32 at a copy's rate. The warp
+// schedulers issue in 55 to 60 % of their cycles, with the 16 warps an SM that 128 registers and two
+// stages of inputs allow.
 //
 // Rounding: gates, decays and states are fp32; y is rounded to the input type once.
 #include <algorithm>
@@ -40,9 +43,9 @@ template <bool BF16, int CH>
 using Tile = GateTile<BF16, CH, 4, BF16 ? 128 : 64>;
 
 // Shared memory: two stages of x, r and i, then two states of the tile's channels that the CTA
-// before hands over. A piece's summary takes the place of
-// its first rows of x. Where rows are 64 bytes, those of odd pieces change places in pairs, so
-// that the two that a half warp reads at once lie in different banks.
+// before hands over. A piece's summary takes the place of its first rows of x. Where rows are 64
+// bytes, those of odd pieces change places in pairs, so that the two that a half warp reads at
+// once lie in different banks.
 template <bool BF16, bool IN>
 constexpr int kStageBytes = (2 + IN) * Tile<BF16, 64>::bytes;  // the same for 32
 
@@ -362,13 +365,14 @@ cudaError_t step(const GateArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-// The cheapest of 1 to 8 CTAs a cluster and of 64 or 32 channels a tile. A round of a CTA with
-// c CTAs on its SM took 0.9 + 0.78 c us in bf16 (8 x 4096 x 1536: 108 us with 192 CTAs of 64 rounds,
-// 93 with 384 of 32, 83 with 576 of 22, 96 with 768 of 16, which is a wave of 608 and a rest,
-// 111 with 1536), and a CTA costs some 1.5 rounds besides. The last wave has as many CTAs an SM
-// as are left. A tile of 32 channels has twice the pieces to fold: 6 % more. A packed batch's
-// CTAs have the mean of the rounds (and half of one lost), but none is done before its
-// longest sequence's rounds, one after the other.
+// The cheapest of 1 to 8 CTAs a cluster and of 64 or 32 channels a tile, by a model of the time.
+// A round of a CTA with c CTAs on its SM takes some 0.9 + 0.78 c us in bf16, and a CTA costs 1.5
+// rounds besides. The last wave has as many CTAs an SM as are left. A tile of 32 channels has
+// twice the pieces to fold: 6 % more. A packed batch's CTAs have the mean of the rounds (and half
+// of one lost), but none is done before its longest sequence's rounds, one after the other.
+// Measured, 8 x 4096 x 1536 with clusters of 1, 2, 3, 4 and 8: 110, 88, 78, 88 and 87 us (3 is
+// taken: 576 CTAs where 608 fit; 768 are a wave and a rest); 1 x 32768 x 2048 with 64 channels a
+// tile and 8: 174, with 32 channels (taken): 161.
 GatePlan gate_plan(const SeqRows& r, int D, int tokens, int resident, int narrow) {
   const int sms = sms_of_device();
   const double slots = (double)resident * sms;

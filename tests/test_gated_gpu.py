@@ -283,6 +283,16 @@ def test_gates_far_out(dtype):
     _status()
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_channels_that_hardly_forget(dtype):
+    """Rates down to 1e-12: 1 - a^2 is 2 w to the last digit, though a is 1 in fp32. A state's own rounding, 6e-8 a token over 300
+    tokens, stays below 300 x 6e-8 = 1.8e-5 of it."""
+    T, D = 300, 64
+    i = _inputs(61, T, 1, D, dtype, state=False)
+    i["A"] = torch.logspace(-12, -3, D)
+    _case(dtype, [T], True, D, state=False, inputs=i)
+
+
 @pytest.mark.parametrize("bad", [0.0, -1.0, float("nan"), float("inf")])
 def test_rates_out_of_range_are_latched(bad):
     i = _dev(_dense(_inputs(1, 20, 2, 72, F32), 2))

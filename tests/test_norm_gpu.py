@@ -173,6 +173,19 @@ def test_a_row_with_infinity_or_nan_spoils_no_other(dtype, D):
     assert torch.isfinite(g["dx"][ok]).all() and torch.isfinite(g["dbias"]).all()
 
 
+@pytest.mark.parametrize("D", [64, 200, 1536, 4104])
+def test_deviations_past_the_range_of_their_squares(D):
+    """Deviations of 1e30: their squares overflow, and y is the bias; the rows beside it are as ever."""
+    x = _r(_gen(D), 5, D).to(DEV)
+    w, b = torch.rand(D, device=DEV), torch.randn(D, device=DEV)
+    want, _, _ = pal.palimpsa_layer_norm(x, w, b)
+    x[2] *= 1e30
+    y, _, st = pal.palimpsa_layer_norm(x, w, b, want_stats=True)
+    assert torch.equal(y[2], b) and st[2, 1] == 0
+    y[2] = want[2]
+    assert torch.equal(y, want)
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("D", [64, 520])
 def test_rows_of_wider_rows_and_in_place(dtype, D):
