@@ -8,10 +8,10 @@
 // As in the forward, one pass over the data: HBM bounds it, 18 bytes a channel-token in
 // bf16 with both gates (0.84 clocks of an SM's share) and half a byte of checkpoints. The
 // forward leaves the state before every 8th token, so a thread recomputes the states of its
-// piece by itself (8 tokens of 2 channels), with the factors of g_t in dx, di, dr and dA; a run
-// over the piece from the back, from a gradient of 0, gives its summary and each token's part
-// of g_t that is known by then; with the gradient behind the piece known, the results follow.
-// The rounds go from the back to the front, and in a cluster the gradient goes round the other way.
+// piece by itself (8 tokens of 2 channels), with the factors of g_t in dx, di, dr and dA; a first
+// run over the piece from the back, from a gradient of 0, gives its summary, and with the
+// gradient behind the piece known, a second run gives the results. (Kept products and sums instead
+// of the second run, as in the forward: 1 % slower.) The rounds go from the back to the front, and in a cluster the gradient goes round the other way.
 // The parameters' sums stay in registers over all rounds; they are added up over the CTA's
 // pieces in shared memory and over CTAs by a second kernel, in a fixed order: no atomics, the
 // same bits every time.
@@ -192,12 +192,8 @@ palimpsa_gate_bwd_kernel(GateArgs a, int tiles, float* sums) {
     float2 P = make_float2(1.f, 1.f), C = zero;
 #pragma unroll
     for (int t = kPiece - 1; t >= 0; --t) {
-      // (In their places: with c from behind the piece, g_t is P c + C.)
-      const float2 d = da[t];
-      gy[t] = __fadd2_rn(gy[t], C);
-      da[t] = P;
-      C = __fmul2_rn(d, gy[t]);
-      P = __fmul2_rn(P, d);
+      C = __fmul2_rn(da[t], __fadd2_rn(gy[t], C));
+      P = __fmul2_rn(P, da[t]);
     }
     agg[warp * 32 + lane] = make_float4(P.x, P.y, C.x, C.y);
     __syncthreads();
@@ -247,7 +243,8 @@ palimpsa_gate_bwd_kernel(GateArgs a, int tiles, float* sums) {
       const long long last = at + (np - 1) * yd;
       char *px = static_cast<char*>(a.dx) + last, *pg = static_cast<char*>(a.dr) + last, *pp = static_cast<char*>(a.di) + last;
       auto out = [&](int t) {
-        const float2 g = ffma2(da[t], c, gy[t]);
+        const float2 g = __fadd2_rn(gy[t], c);
+        c = __fmul2_rn(da[t], g);
         store_pair<BF16>(px, __fmul2_rn(g, fx[t]));
         px -= yd;
         const float2 dr = __fmul2_rn(g, fr[t]);
