@@ -48,12 +48,16 @@ cudaError_t scratch_pool(cudaMemPool_t* out) {
     props.location.type = cudaMemLocationTypeDevice;
     props.location.id = dev;
     cudaMemPool_t pool = nullptr;
-    if ((e = cudaMemPoolCreate(&pool, &props)) != cudaSuccess) return e;
+    // (The first call may come while a stream is being captured, where this is refused unless the
+    // thread says that it is no part of the capture.)
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    if ((e = cudaThreadExchangeStreamCaptureMode(&mode)) != cudaSuccess) return e;
     unsigned long long keep = g_scratch_keep_bytes.load();
-    if ((e = cudaMemPoolSetAttribute(pool, cudaMemPoolAttrReleaseThreshold, &keep)) != cudaSuccess) {
+    e = cudaMemPoolCreate(&pool, &props);
+    if (e == cudaSuccess && (e = cudaMemPoolSetAttribute(pool, cudaMemPoolAttrReleaseThreshold, &keep)) != cudaSuccess)
       cudaMemPoolDestroy(pool);
-      return e;
-    }
+    const cudaError_t e2 = cudaThreadExchangeStreamCaptureMode(&mode);
+    if (e != cudaSuccess || (e = e2) != cudaSuccess) return e;
     g_pools[dev] = pool;
   }
   *out = g_pools[dev];
