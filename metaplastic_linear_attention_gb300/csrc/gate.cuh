@@ -28,10 +28,14 @@ struct GateTile {
 // How a batch is shared out: channels of a tile, and CTAs along time (a cluster's).
 struct GatePlan {
   int channels, cluster;
+  double us;  // the time that the model gives
 };
 // `tokens` of a CTA's tile of 64 channels (twice as many at `narrow`, the least channels of a tile),
 // `resident` CTAs on an SM.
 GatePlan gate_plan(const SeqRows& r, int D, int tokens, int resident, int narrow);
+// Whether the batch's sequences are better walked by a thread (or a warp) each, `rate` channel-tokens a
+// microsecond, than in tiles with plan p.
+bool gate_short(const SeqRows& r, int D, const GatePlan& p, double rate);
 
 #if defined(__CUDACC__)
 
@@ -49,6 +53,15 @@ __device__ __forceinline__ float2 load_pair(const void* p) {
     return make_float2(bf16_lo(u), bf16_hi(u));
   } else {
     return *static_cast<const float2*>(p);
+  }
+}
+template <bool BF16>
+__device__ __forceinline__ float2 read_pair(const void* p) {  // of what the kernel does not write
+  if constexpr (BF16) {
+    const uint32_t u = __ldg(static_cast<const unsigned int*>(p));
+    return make_float2(bf16_lo(u), bf16_hi(u));
+  } else {
+    return __ldg(static_cast<const float2*>(p));
   }
 }
 template <bool BF16>

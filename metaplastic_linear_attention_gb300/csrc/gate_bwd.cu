@@ -11,7 +11,8 @@
 // piece by itself (8 tokens of 2 channels), with the factors of g_t in dx, di, dr and dA; a first
 // run over the piece from the back, from a gradient of 0, gives its summary, and with the
 // gradient behind the piece known, a second run gives the results. (Kept products and sums instead
-// of the second run, as in the forward: 1 % slower.) The rounds go from the back to the front, and in a cluster the gradient goes round the other way.
+// of the second run, as in the forward: 1 % slower.) The rounds go from the back to the front, and
+// in a cluster the gradient goes round the other way.
 // The parameters' sums stay in registers over all rounds; they are added up over the CTA's
 // pieces in shared memory and over CTAs by a second kernel, in a fixed order: no atomics, the
 // same bits every time.
@@ -39,6 +40,114 @@ template <bool BF16, bool IN, bool GATE>
 struct BwdSmem {
   static constexpr int h = (3 + IN + GATE) * Tile<BF16>::bytes, stage = h + Tile<BF16>::pieces * Tile<BF16>::CH * 4;
   static constexpr int agg = 2 * stage, given = agg + Tile<BF16>::pieces * 512;
+};
+
+// A thread's piece: 8 tokens of two neighbouring channels.
+template <bool BF16, bool IN, bool GATE>
+struct Piece {
+  // The decays, the factors of g_t in dx, di, dr and dA, and dy silu(z).
+  float2 da[kPiece], fx[kPiece], fi[IN ? kPiece : 1], fr[kPiece], fA[kPiece], gy[kPiece];
+
+  __device__ __forceinline__ void no_token(int t) {
+    da[t] = make_float2(1.f, 1.f);
+    fx[t] = fr[t] = fA[t] = gy[t] = make_float2(0.f, 0.f);
+    if (IN) fi[t] = make_float2(0.f, 0.f);
+  }
+  // Takes in token t, with the state before it in h, which moves on; returns dz. (rb, ib: the biases
+  // times -log2(e).)
+  __device__ __forceinline__ float2 token(int t, float2 x, float2 r, float2 dy, float2 i, float2 z, float2 A, float2 rb,
+                                          float2 ib, float2* h) {
+    const float2 scale = make_float2(-kLog2e, -kLog2e);
+    float2 closed;  // 1 - s
+    const float2 s = sigmoid_of(ffma2(r, scale, rb), &closed);
+    gy[t] = dy;
+    const float2 w = __fmul2_rn(A, s);
+    float2 q;  // 1 - a^2
+    decay_of(w, &da[t], &q);
+    // (A rate of 0 has 1 / n of 5e18, and no gradient: the factor w of dr, or s of dA, is 0 too.)
+    const float2 ni = make_float2(rsqrt_approx(q.x), rsqrt_approx(q.y));
+    fx[t] = __fmul2_rn(q, ni);
+    float2 u = x;
+    if (IN) {
+      float2 shut;  // 1 - p
+      const float2 p = sigmoid_of(ffma2(i, scale, ib), &shut);
+      fx[t] = __fmul2_rn(fx[t], p);
+      fi[t] = __fmul2_rn(__fmul2_rn(fx[t], x), shut);
+      u = __fmul2_rn(x, p);
+    }
+    const float2 old = __fmul2_rn(da[t], *h);
+    // dw / g = u a^2 / n - a h
+    const float2 aa = __fmul2_rn(__fmul2_rn(da[t], da[t]), ni);
+    const float2 dw = ffma2(u, aa, make_float2(-old.x, -old.y));
+    fA[t] = __fmul2_rn(dw, s);
+    fr[t] = __fmul2_rn(__fmul2_rn(dw, w), closed);
+    *h = ffma2(fx[t], x, old);
+    if (!GATE) return dy;
+    float2 rest;
+    const float2 c = sigmoid_of(__fmul2_rn(z, scale), &rest);
+    const float2 m = ffma2(z, rest, make_float2(1.f, 1.f));  // silu' = c (1 + z (1 - c))
+    gy[t] = __fmul2_rn(dy, __fmul2_rn(z, c));
+    return __fmul2_rn(__fmul2_rn(dy, *h), __fmul2_rn(c, m));
+  }
+};
+
+// A thread's sums of dA, dr_bias and di_bias, and where its results go, from the back: `last` bytes into
+// each array, `yd` bytes a token.
+template <bool BF16, bool IN, bool GATE>
+struct Results {
+  float2 sA = make_float2(0.f, 0.f), sr = sA, si = sA;
+  // The results of a piece's np tokens; c comes in from behind it, and what goes on to the token before it
+  // comes out.
+  __device__ __forceinline__ float2 finish(const GateArgs& a, const Piece<BF16, IN, GATE>& p, int np, long long last,
+                                           long long yd, float2 c) {
+    float2 pA = make_float2(0.f, 0.f), pr = pA, pi = pA;  // the piece's sums
+    char *px = static_cast<char*>(a.dx) + last, *pg = static_cast<char*>(a.dr) + last, *pp = static_cast<char*>(a.di) + last;
+    auto out = [&](int t) {
+      const float2 g = __fadd2_rn(p.gy[t], c);
+      c = __fmul2_rn(p.da[t], g);
+      store_pair<BF16>(px, __fmul2_rn(g, p.fx[t]));
+      px -= yd;
+      const float2 dr = __fmul2_rn(g, p.fr[t]);
+      store_pair<BF16>(pg, dr);
+      pg -= yd;
+      pr = __fadd2_rn(pr, dr);
+      pA = ffma2(g, p.fA[t], pA);
+      if (IN) {
+        const float2 di = __fmul2_rn(g, p.fi[t]);
+        store_pair<BF16>(pp, di);
+        pp -= yd;
+        pi = __fadd2_rn(pi, di);
+      }
+    };
+    if (np == kPiece) {
+#pragma unroll
+      for (int t = kPiece - 1; t >= 0; --t) out(t);
+    } else {
+#pragma unroll
+      for (int t = kPiece - 1; t >= 0; --t)
+        if (t < np) out(t);
+    }
+    sA = __fadd2_rn(sA, pA);
+    sr = __fadd2_rn(sr, pr);
+    si = __fadd2_rn(si, pi);
+    return c;
+  }
+  // The CTA's sums over its warps, through red ([warps][32]), to part [3, D] (a thread's two channels of it).
+  __device__ __forceinline__ void leave(float2* red, float* part, int D, int warps, bool in) const {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const float2 own[3] = {sA, sr, si};
+#pragma unroll
+    for (int v = 0; v < 3; ++v) {
+      __syncthreads();
+      red[warp * 32 + lane] = own[v];
+      __syncthreads();
+      if (warp == v && in) {
+        float2 t = red[lane];
+        for (int w = 1; w < warps; ++w) t = __fadd2_rn(t, red[w * 32 + lane]);
+        *reinterpret_cast<float2*>(part + (long long)v * D) = t;
+      }
+    }
+  }
 };
 
 // sums: [n_seq, cluster, 3, D], the CTAs' parts of dA, dr_bias and di_bias.
@@ -117,7 +226,7 @@ palimpsa_gate_bwd_kernel(GateArgs a, int tiles, float* sums) {
   if (!pos_finite(A.x) || !pos_finite(A.y)) latch_status(a.status, kStatusDomain);
   float2 carry = zero;  // a g of the token behind the round (in a cluster, behind the sequence)
   if (a.dh_T && in) carry = *reinterpret_cast<const float2*>(a.dh_T + n * a.D + ch);
-  float2 sA = zero, sr = zero, si = zero;
+  Results<BF16, IN, GATE> res;
   bool waits = true;
   const long long yd = (long long)a.D * ES;
   if (CLUSTER) cg::this_cluster().sync();  // every CTA has started, its barriers set: it may be written to
@@ -133,48 +242,18 @@ palimpsa_gate_bwd_kernel(GateArgs a, int tiles, float* sums) {
     __syncthreads();  // the round's inputs are here; the other stage and the summaries are free
     stage(k - 1);
 
-    // The factors of g_t in dx, di, dr and dA, the decays, and dy silu(z).
-    float2 da[kPiece], fx[kPiece], fi[IN ? kPiece : 1], fr[kPiece], fA[kPiece], gy[kPiece];
+    Piece<BF16, IN, GATE> p;
     const long long at = ((row0 + tp) * a.D + ch) * ES;  // bytes
     char* pz = static_cast<char*>(a.dz) + at;
     float2 h = np > 0 ? *reinterpret_cast<const float2*>(smem + (k & 1) * S::stage + S::h +
                                                          (warp * Tile<BF16>::CH + 2 * lane) * 4)
                       : zero;
     auto token = [&](int t) {
-      const float2 x = load_pair<BF16>(raw + t * G::row);
-      float2 closed;  // 1 - s
-      const float2 s = sigmoid_of(ffma2(load_pair<BF16>(raw + G::bytes + t * G::row), scale, rb), &closed);
-      gy[t] = load_pair<BF16>(raw + 2 * G::bytes + t * G::row);
-      const float2 w = __fmul2_rn(A, s);
-      float2 q;  // 1 - a^2
-      decay_of(w, &da[t], &q);
-      // (A rate of 0 has 1 / n of 5e18, and no gradient: the factor w of dr, or s of dA, is 0 too.)
-      const float2 ni = make_float2(rsqrt_approx(q.x), rsqrt_approx(q.y));
-      fx[t] = __fmul2_rn(q, ni);
-      float2 u = x;
-      if (IN) {
-        float2 shut;  // 1 - p
-        const float2 p = sigmoid_of(ffma2(load_pair<BF16>(raw + kI * G::bytes + t * G::row), scale, ib), &shut);
-        fx[t] = __fmul2_rn(fx[t], p);
-        fi[t] = __fmul2_rn(__fmul2_rn(fx[t], x), shut);
-        u = __fmul2_rn(x, p);
-      }
-      const float2 old = __fmul2_rn(da[t], h);
-      // dw / g = u a^2 / n - a h
-      const float2 aa = __fmul2_rn(__fmul2_rn(da[t], da[t]), ni);
-      const float2 dw = ffma2(u, aa, make_float2(-old.x, -old.y));
-      fA[t] = __fmul2_rn(dw, s);
-      fr[t] = __fmul2_rn(__fmul2_rn(dw, w), closed);
-      h = ffma2(fx[t], x, old);
+      auto load = [&](int array) { return load_pair<BF16>(raw + array * G::bytes + t * G::row); };
+      const float2 dz = p.token(t, load(0), load(1), load(2), IN ? load(kI) : zero, GATE ? load(kZ) : zero, A, rb, ib, &h);
       if (GATE) {
-        const float2 z = load_pair<BF16>(raw + kZ * G::bytes + t * G::row);
-        float2 rest;
-        const float2 c = sigmoid_of(__fmul2_rn(z, scale), &rest);
-        const float2 m = ffma2(z, rest, make_float2(1.f, 1.f));  // silu' = c (1 + z (1 - c))
-        const float2 dz = __fmul2_rn(__fmul2_rn(gy[t], h), __fmul2_rn(c, m));
         if (in) store_pair<BF16>(pz, dz);
         pz += yd;
-        gy[t] = __fmul2_rn(gy[t], __fmul2_rn(z, c));
       }
     };
     if (np == kPiece) {
@@ -183,17 +262,15 @@ palimpsa_gate_bwd_kernel(GateArgs a, int tiles, float* sums) {
     } else {
 #pragma unroll
       for (int t = 0; t < kPiece; ++t) {
-        da[t] = make_float2(1.f, 1.f);
-        fx[t] = fr[t] = fA[t] = gy[t] = zero;
-        if (IN) fi[t] = zero;
+        p.no_token(t);
         if (t < np) token(t);
       }
     }
     float2 P = make_float2(1.f, 1.f), C = zero;
 #pragma unroll
     for (int t = kPiece - 1; t >= 0; --t) {
-      C = __fmul2_rn(da[t], __fadd2_rn(gy[t], C));
-      P = __fmul2_rn(P, da[t]);
+      C = __fmul2_rn(p.da[t], __fadd2_rn(p.gy[t], C));
+      P = __fmul2_rn(P, p.da[t]);
     }
     agg[warp * 32 + lane] = make_float4(P.x, P.y, C.x, C.y);
     __syncthreads();
@@ -238,59 +315,73 @@ palimpsa_gate_bwd_kernel(GateArgs a, int tiles, float* sums) {
         c = ffma2(make_float2(e.x, e.y), c, make_float2(e.z, e.w));
       }
     }
-    if (in && np > 0) {
-      float2 pA = zero, pr = zero, pi = zero;  // the piece's sums
-      const long long last = at + (np - 1) * yd;
-      char *px = static_cast<char*>(a.dx) + last, *pg = static_cast<char*>(a.dr) + last, *pp = static_cast<char*>(a.di) + last;
-      auto out = [&](int t) {
-        const float2 g = __fadd2_rn(gy[t], c);
-        c = __fmul2_rn(da[t], g);
-        store_pair<BF16>(px, __fmul2_rn(g, fx[t]));
-        px -= yd;
-        const float2 dr = __fmul2_rn(g, fr[t]);
-        store_pair<BF16>(pg, dr);
-        pg -= yd;
-        pr = __fadd2_rn(pr, dr);
-        pA = ffma2(g, fA[t], pA);
-        if (IN) {
-          const float2 di = __fmul2_rn(g, fi[t]);
-          store_pair<BF16>(pp, di);
-          pp -= yd;
-          pi = __fadd2_rn(pi, di);
-        }
-      };
-      if (np == kPiece) {
-#pragma unroll
-        for (int t = kPiece - 1; t >= 0; --t) out(t);
-      } else {
-#pragma unroll
-        for (int t = kPiece - 1; t >= 0; --t)
-          if (t < np) out(t);
-      }
-      sA = __fadd2_rn(sA, pA);
-      sr = __fadd2_rn(sr, pr);
-      si = __fadd2_rn(si, pi);
-    }
+    if (in && np > 0) res.finish(a, p, np, at + (np - 1) * yd, yd, c);
     __syncwarp();
   }
   if ((!CLUSTER || rounds == 0) && rank == 0 && warp == 0 && in && a.dh0)
     *reinterpret_cast<float2*>(a.dh0 + n * a.D + ch) = carry;
-  // The CTA's sums over its pieces.
-  float2* const red = reinterpret_cast<float2*>(agg);
-  const float2 own[3] = {sA, sr, si};
-#pragma unroll
-  for (int v = 0; v < 3; ++v) {
-    __syncthreads();
-    red[warp * 32 + lane] = own[v];
-    __syncthreads();
-    if (warp == v && in) {
-      float2 t = red[lane];
-#pragma unroll
-      for (int w = 1; w < NP; ++w) t = __fadd2_rn(t, red[w * 32 + lane]);
-      *reinterpret_cast<float2*>(part + (long long)v * a.D) = t;
-    }
-  }
+  res.leave(reinterpret_cast<float2*>(agg), part, a.D, NP, in);
   if (CLUSTER) cg::this_cluster().sync();  // nobody hands anything to a CTA that has left
+}
+
+// Short sequences, many of them (see the forward's): a warp takes 64 channels of one sequence after
+// another, piece by piece from the back, with nothing to exchange; its parameters' sums go over all
+// its sequences. sums: [groups, 3, D]. (Read-only loads: behind stores that they might overlap, the
+// next token's would wait: 308 us against 150 at 256 x 64 x 2048.)
+constexpr int kShortWarps = 4, kShortCtas = 3;  // warps of a CTA, CTAs of an SM
+template <bool BF16, bool IN, bool GATE>
+__global__ void __launch_bounds__(32 * kShortWarps, kShortCtas) palimpsa_gate_short_bwd_kernel(GateArgs a, int tiles, float* sums) {
+  constexpr int ES = BF16 ? 2 : 4;
+  __shared__ float2 red[kShortWarps * 32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int ch = (int)(blockIdx.x % tiles) * 64 + 2 * lane;
+  const long long group = blockIdx.x / tiles, groups = gridDim.x / tiles;
+  const bool in = ch < a.D;
+  const float2 zero = make_float2(0.f, 0.f), scale = make_float2(-kLog2e, -kLog2e);
+  const float2 A = pair_or(a.A, ch, in, 1.f);
+  const float2 rb = __fmul2_rn(pair_or(a.r_bias, ch, in, 0.f), scale), ib = __fmul2_rn(pair_or(a.i_bias, ch, in, 0.f), scale);
+  if (!pos_finite(A.x) || !pos_finite(A.y)) latch_status(a.status, kStatusDomain);
+  const long long yd = (long long)a.D * ES;
+  Results<BF16, IN, GATE> res;
+  for (long long n = group * kShortWarps + warp; n < a.rows.n_seq; n += groups * kShortWarps) {
+    long long row0;
+    int len;
+    if (!seq_rows(a.rows, n, &row0, &len)) {
+      if (ch == 0) latch_status(a.status, kStatusDomain);
+      continue;
+    }
+    if (!in) continue;
+    const float* const ckpt = a.ckpt_in + gate_ckpt_row0(a.rows, n, row0) * a.D + ch;
+    float2 c = a.dh_T ? *reinterpret_cast<const float2*>(a.dh_T + n * a.D + ch) : zero;
+    for (int tp = (len - 1) / kPiece * kPiece; tp >= 0 && len > 0; tp -= kPiece) {
+      const int np = min(kPiece, len - tp);
+      const long long row = row0 + tp, at = (row * a.D + ch) * ES;
+      auto start = [&](const void* p, long long ld) { return static_cast<const char*>(p) + (row * ld + ch) * ES; };
+      const char *px = start(a.x, a.x_ld), *pr = start(a.r, a.r_ld), *py = start(a.dy, a.dy_ld), *pi = start(a.i, a.i_ld),
+                 *pz = start(a.z, a.z_ld);
+      Piece<BF16, IN, GATE> p;
+      float2 h = *reinterpret_cast<const float2*>(ckpt + (long long)(tp / kPiece) * a.D);
+      auto token = [&](int t) {
+        auto load = [&](const char* q, long long ld) { return read_pair<BF16>(q + t * ld * ES); };
+        const float2 dz = p.token(t, load(px, a.x_ld), load(pr, a.r_ld), load(py, a.dy_ld), IN ? load(pi, a.i_ld) : zero,
+                                  GATE ? load(pz, a.z_ld) : zero, A, rb, ib, &h);
+        if (GATE) store_pair<BF16>(static_cast<char*>(a.dz) + at + t * yd, dz);
+      };
+      if (np == kPiece) {
+#pragma unroll
+        for (int t = 0; t < kPiece; ++t) token(t);
+      } else {
+#pragma unroll
+        for (int t = 0; t < kPiece; ++t) {
+          p.no_token(t);
+          if (t < np) token(t);
+        }
+      }
+      c = res.finish(a, p, np, at + (np - 1) * yd, yd, c);
+    }
+    if (a.dh0) *reinterpret_cast<float2*>(a.dh0 + n * a.D + ch) = c;
+  }
+  res.leave(red, sums + group * 3 * a.D + ch, a.D, kShortWarps, in);
 }
 
 template <bool BF16, bool IN, bool GATE, bool CLUSTER>
@@ -302,7 +393,6 @@ cudaError_t run(const GateArgs& a, float* sums, cudaStream_t s) {
   const auto kernel = palimpsa_gate_bwd_kernel<BF16, IN, GATE, CLUSTER>;
   static SharedBytes allowed;
   cudaError_t e = allow_shared(kernel, bytes, &allowed);
-  if (e == cudaSuccess && a.cluster > 8) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute cluster = {};
   cluster.id = cudaLaunchAttributeClusterDimension;
@@ -315,15 +405,22 @@ cudaError_t run(const GateArgs& a, float* sums, cudaStream_t s) {
   c.stream = s;
   c.attrs = &cluster;
   c.numAttrs = CLUSTER ? 1 : 0;
-  e = cudaLaunchKernelEx(&c, kernel, a, (int)tiles, sums);
-  if (e != cudaSuccess) return e;
-  float* const out[3] = {a.dA, a.dr_bias, a.di_bias};
-  return launch_row_sums(sums, (long long)a.rows.n_seq * a.cluster, 3, a.D, out, s);
+  return cudaLaunchKernelEx(&c, kernel, a, (int)tiles, sums);
 }
 
 template <bool BF16, bool IN, bool GATE>
 cudaError_t backward(const GateArgs& a, float* sums, cudaStream_t s) {
-  return a.cluster > 1 ? run<BF16, IN, GATE, true>(a, sums, s) : run<BF16, IN, GATE, false>(a, sums, s);
+  cudaError_t e;
+  if (a.groups > 0) {
+    const int tiles = (a.D + 63) / 64;
+    palimpsa_gate_short_bwd_kernel<BF16, IN, GATE><<<(unsigned)(a.groups * tiles), 32 * kShortWarps, 0, s>>>(a, tiles, sums);
+    e = cudaGetLastError();
+  } else {
+    e = a.cluster > 1 ? run<BF16, IN, GATE, true>(a, sums, s) : run<BF16, IN, GATE, false>(a, sums, s);
+  }
+  if (e != cudaSuccess) return e;
+  float* const out[3] = {a.dA, a.dr_bias, a.di_bias};
+  return launch_row_sums(sums, a.groups > 0 ? a.groups : (long long)a.rows.n_seq * a.cluster, 3, a.D, out, s);
 }
 
 }  // namespace
@@ -332,8 +429,16 @@ size_t plan_gate_backward(GateArgs* a) {
   // In fp32 an SM's shared memory holds 2 CTAs with both gates, 3 with one and 4 without.
   const int resident = a->bf16 ? kResident : 4 - (a->i != nullptr) - (a->z != nullptr);
   const int tokens = a->bf16 ? Tile<true>::tokens : Tile<false>::tokens;
-  a->cluster = gate_plan(a->rows, a->D, tokens, resident, 64).cluster;
-  return (size_t)a->rows.n_seq * a->cluster * 3 * a->D;
+  const GatePlan p = gate_plan(a->rows, a->D, tokens, resident, 64);
+  a->cluster = p.cluster;
+  a->groups = 0;
+  long long rows = (long long)a->rows.n_seq * a->cluster;
+  if (gate_short(a->rows, a->D, p, 330e3)) {
+    // As many groups of warps as the GPU holds at once and the sequences fill.
+    const long long tiles = (a->D + 63) / 64, held = (long long)kShortCtas * sms_of_device() / tiles;
+    rows = a->groups = (int)std::max(1ll, std::min(held, (a->rows.n_seq + kShortWarps - 1ll) / kShortWarps));
+  }
+  return (size_t)rows * 3 * a->D;
 }
 
 cudaError_t launch_gate_backward(const GateArgs& a, float* scratch, cudaStream_t s) {

@@ -280,6 +280,82 @@ __global__ void __launch_bounds__(BF16 ? 128 : 64, kResident) palimpsa_gate_kern
   if (CLUSTER) cg::this_cluster().sync();  // nobody hands anything to a CTA that has left
 }
 
+// Short sequences, many of them: a thread takes 4 channels of a sequence and walks its tokens, with
+// nothing to exchange (in the kernel above a sequence of 8 tokens leaves seven of eight groups of
+// threads idle). kBatch tokens' loads go out together.
+constexpr int kBatch = 4;
+template <bool BF16, bool IN, bool GATE>
+__global__ void __launch_bounds__(128, BF16 ? 5 : 4) palimpsa_gate_short_kernel(GateArgs a) {
+  using Q = Quad<BF16>;
+  using Raw = typename Q::Raw;
+  constexpr int ES = Vec<BF16>::bytes;
+  const int quads = a.D / 4;
+  const long long k = (long long)blockIdx.x * 128 + threadIdx.x;
+  if (k >= quads * (long long)a.rows.n_seq) return;
+  const long long n = k / quads;
+  const int ch = (int)(k % quads) * 4;
+  long long row0;
+  int len;
+  if (!seq_rows(a.rows, n, &row0, &len)) {
+    if (ch == 0) latch_status(a.status, kStatusDomain);
+    return;
+  }
+  const float2 scale = make_float2(-kLog2e, -kLog2e);
+  float2 A[2], rb[2], ib[2];
+  Four h = four(0.f);
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    A[j] = pair_or(a.A, ch + 2 * j, true, 1.f);
+    if (!pos_finite(A[j].x) || !pos_finite(A[j].y)) latch_status(a.status, kStatusDomain);
+    rb[j] = __fmul2_rn(pair_or(a.r_bias, ch + 2 * j, true, 0.f), scale);
+    if (IN) ib[j] = __fmul2_rn(pair_or(a.i_bias, ch + 2 * j, true, 0.f), scale);
+  }
+  if (a.h0) h.set(*reinterpret_cast<const float4*>(a.h0 + n * a.D + ch));
+  float* ckpt = a.ckpt ? a.ckpt + gate_ckpt_row0(a.rows, n, row0) * a.D + ch : nullptr;
+  auto at = [&](const void* p, long long ld) { return static_cast<const char*>(p) + (row0 * ld + ch) * ES; };
+  const char *px = at(a.x, a.x_ld), *pr = at(a.r, a.r_ld), *pi = at(a.i, a.i_ld), *pz = at(a.z, a.z_ld);
+  char* py = static_cast<char*>(a.y) + (row0 * a.D + ch) * ES;
+  for (int t0 = 0; t0 < len; t0 += kBatch) {
+    Raw x[kBatch], r[kBatch], i[kBatch], z[kBatch];
+#pragma unroll
+    for (int t = 0; t < kBatch; ++t)
+      if (t0 + t < len) {
+        x[t] = *reinterpret_cast<const Raw*>(px + t * a.x_ld * ES);
+        r[t] = *reinterpret_cast<const Raw*>(pr + t * a.r_ld * ES);
+        if (IN) i[t] = *reinterpret_cast<const Raw*>(pi + t * a.i_ld * ES);
+        if (GATE) z[t] = *reinterpret_cast<const Raw*>(pz + t * a.z_ld * ES);
+      }
+    if (ckpt && t0 % kPiece == 0) {
+      *reinterpret_cast<float4*>(ckpt) = h.all();
+      ckpt += a.D;
+    }
+#pragma unroll
+    for (int t = 0; t < kBatch; ++t)
+      if (t0 + t < len) {
+        float2 fx[2], fr[2], fi[2], fz[2], y[2];
+        Q::unpack(x[t], fx);
+        Q::unpack(r[t], fr);
+        if (IN) Q::unpack(i[t], fi);
+        if (GATE) Q::unpack(z[t], fz);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          float2 da, sq;
+          decay_of(__fmul2_rn(A[j], sigmoid_of(ffma2(fr[j], scale, rb[j]))), &da, &sq);
+          const float2 b = IN ? input_of(sq, one_plus(ffma2(fi[j], scale, ib[j])), fx[j]) : input_of(sq, fx[j]);
+          h.v[j] = ffma2(da, h.v[j], b);
+          y[j] = GATE ? __fmul2_rn(h.v[j], silu_fast(fz[j])) : h.v[j];
+        }
+        *reinterpret_cast<Raw*>(py + (long long)t * a.D * ES) = Q::pack(y);
+      }
+    px += kBatch * a.x_ld * ES;
+    pr += kBatch * a.r_ld * ES;
+    pi += kBatch * a.i_ld * ES;
+    pz += kBatch * a.z_ld * ES;
+    py += (long long)kBatch * a.D * ES;
+  }
+  *reinterpret_cast<float4*>(a.h_T + n * a.D + ch) = h.all();
+}
+
 // One token: a thread takes 4 channels of a sequence. A few bytes each way: latency alone.
 template <bool BF16, bool IN, bool GATE>
 __global__ void __launch_bounds__(128) palimpsa_gate_step_kernel(GateArgs a) {
@@ -349,6 +425,12 @@ template <bool BF16, bool IN, bool GATE>
 cudaError_t forward(const GateArgs& given, cudaStream_t s) {
   GateArgs a = given;
   const GatePlan p = gate_plan(a.rows, a.D, Tile<BF16, 64>::tokens, kResident, 32);
+  if (gate_short(a.rows, a.D, p, 400e3)) {
+    const long long blocks = ((long long)(a.D / 4) * a.rows.n_seq + 127) / 128;
+    if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
+    palimpsa_gate_short_kernel<BF16, IN, GATE><<<(unsigned)blocks, 128, 0, s>>>(a);
+    return cudaGetLastError();
+  }
   a.cluster = p.cluster;
   if (p.channels == 32)
     return a.cluster > 1 ? run<BF16, IN, GATE, true, 32>(a, s) : run<BF16, IN, GATE, false, 32>(a, s);
@@ -376,7 +458,7 @@ cudaError_t step(const GateArgs& a, cudaStream_t s) {
 GatePlan gate_plan(const SeqRows& r, int D, int tokens, int resident, int narrow) {
   const int sms = sms_of_device();
   const double slots = (double)resident * sms;
-  GatePlan best = {64, 1};
+  GatePlan best = {64, 1, 0};
   double least = 0;
   for (int ch = 64; ch >= narrow; ch /= 2) {
     const double tiles = (D + ch - 1) / ch;
@@ -389,12 +471,23 @@ GatePlan gate_plan(const SeqRows& r, int D, int tokens, int resident, int narrow
       double cost = (rounds + 1.5) * (waves * full + (rest > 0 ? some : 0));
       cost = std::max(cost, (longest + 1.5) * (waves >= 1 ? full : some)) * (ch == 64 ? 1 : 1.06);
       if ((ch == 64 && cs == 1) || cost < least) {
-        best = {ch, cs};
+        best = {ch, cs, cost};
         least = cost;
       }
     }
   }
   return best;
+}
+
+// A token takes a thread 0.35 to 0.45 us at least, and the GPU's threads together come to `rate`. The
+// rates are those that choose right against the model of the tiles, which is too dear for tiles with
+// few rounds. Measured in bf16 with both gates, threads against tiles: 256 x 4 x 2048 8.5 us and 41,
+// 256 x 16 20.7 and 45, 256 x 64 76 and 72 (threads are taken), 256 x 256 274 and 226; backward, warps
+// against tiles, 19 and 84, 45 and 107, 150 and 154 (warps are taken), 575 and 497. In fp32 512 x 32 x
+// 2048 105 and 124, 256 x 256 389 and 391; backward 217 and 236, 829 and 785 (warps are taken).
+bool gate_short(const SeqRows& r, int D, const GatePlan& p, double rate) {
+  const double rows = r.cu ? r.T : (double)r.n_seq * r.T;
+  return std::max(rows * D / rate, 0.45 * r.max_len) < p.us;
 }
 
 cudaError_t launch_gate_forward(const GateArgs& a, cudaStream_t s) { PALIMPSA_GATE_DISPATCH(forward, a, s) }

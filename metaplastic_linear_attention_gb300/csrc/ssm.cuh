@@ -243,6 +243,7 @@ struct GateArgs {
   float* di_bias = nullptr;
   float* dh0 = nullptr;
   long long dy_ld = 0;
+  int groups = 0;       // short sequences: groups of warps that walk them, set by plan_gate_backward
 };
 
 constexpr int kGateCheckpoint = 8;  // tokens between the gated scan's checkpoints
@@ -258,7 +259,7 @@ __host__ __device__ inline long long gate_ckpt_row0(const SeqRows& r, long long 
 }
 cudaError_t launch_gate_forward(const GateArgs& a, cudaStream_t s);
 cudaError_t launch_gate_step(const GateArgs& a, cudaStream_t s);
-// Backward: sets a->cluster; scratch of as many floats holds the parameters' sums of every CTA.
+// Backward: sets a->cluster and a->groups; scratch of as many floats holds the parameters' sums of every CTA.
 size_t plan_gate_backward(GateArgs* a);
 cudaError_t launch_gate_backward(const GateArgs& a, float* scratch, cudaStream_t s);
 

@@ -124,6 +124,54 @@ def test_dense(dtype, B, T, D, gates, bias, state):
     _case(dtype, [T] * B, True, D, gates, bias, state)
 
 
+# Short sequences, many of them: a thread (backward: a warp) walks each.
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("B,T,D", [(700, 1, 72), (300, 3, 8), (300, 8, 264), (200, 9, 520), (500, 20, 136)])
+@pytest.mark.parametrize("gates,bias,state", [("iz", True, True), ("", False, False), ("z", True, True), ("i", False, False)])
+def test_many_short(dtype, B, T, D, gates, bias, state):
+    _case(dtype, [T] * B, True, D, gates, bias, state)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_many_short_packed(dtype):
+    _case(dtype, [(5, 0, 1, 8, 17, 2)[k % 6] for k in range(900)], False, 200, tail=3)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_many_short_with_bad_offsets(dtype):
+    """One sequence among hundreds is longer than max_seqlen, the last ends past the rows: both are skipped."""
+    lens = [(4, 1, 7, 2)[k % 4] for k in range(600)]
+    lens[300] = 9
+    D, cu = 136, _cu(lens)
+    rows, ok = cu[-1] - 1, [k not in (300, 599) for k in range(600)]
+    i = _inputs(3, rows, 600, D, dtype)
+    dy = _r(_gen(5), rows, D, dtype=dtype)
+    keep = torch.zeros(rows, dtype=torch.bool)
+    for n in range(600):
+        if ok[n]:
+            keep[cu[n]:cu[n + 1]] = True
+    okt = torch.tensor(ok)
+    pick = lambda v: (v[keep] if v.shape[0] == rows else v[okt] if v.shape[0] == 600 else v).to(F64)  # noqa: E731
+    cug = _cu([n for n, fine in zip(lens, ok) if fine])
+    y, last, want = ssm.gradients(ssm.gate, {k: pick(v) for k, v in i.items()}, pick(dy), torch.zeros(598, D, dtype=F64), cug)
+    kw = dict(cu_seqlens=torch.tensor(cu, dtype=torch.int32, device=DEV), max_seqlen=8)
+    h = torch.full((600, D), 7.0, device=DEV)
+    gy, _, ckpt = pal.palimpsa_gated_scan_checkpointed(*_dev(i).values(), h_T=h, **kw)
+    assert pal.palimpsa_get_device_status() == 5
+    g = pal.palimpsa_gated_scan_backward(*list(_dev(i).values())[:-1], ckpt, dy.to(DEV), **kw)
+    assert pal.palimpsa_get_device_status() == 5
+    _near(gy[keep], y, HALF[dtype] + FINE, "y")
+    _near(h[okt], last, FINE, "h_T")
+    assert (h[~okt] == 7).all() and not gy[~keep].any()
+    for k, name in NAMES:
+        _near(g[k][keep], want[name], HALF[dtype] + FINE_G, k)
+        assert not g[k][~keep].any()
+    for k, name in PARAMS[:3]:
+        _near(g[k], want[name], FINE_G, k)
+    _near(g["dh0"][okt], want["h0"], FINE_G, "dh0")
+    assert not g["dh0"][~okt].any()
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("gates,bias,state", [("i", True, False), ("z", False, True), ("i", False, True), ("z", True, False)])
 @pytest.mark.parametrize("B,T,D", [(2, 75, 72), (1, 300, 64), (80, 70, 512)])
