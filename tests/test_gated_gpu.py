@@ -424,6 +424,28 @@ def test_long_memory_beyond_32_bits():
     _status()
 
 
+def test_gradients_beyond_32_bits():
+    """The same, backward: rows, checkpoints and gradients past 2^31 elements of an array."""
+    B, T, D = 3, 131072, 8192
+    x, r, dy = (torch.zeros(B, T, D, dtype=BF, device=DEV) for _ in range(3))
+    last = slice(D - 64, D)
+    g = _gen(2)
+    xs, rs, ds = (_r(g, 300, 64, dtype=BF) for _ in range(3))
+    for t, v in ((x, xs), (r, rs), (dy, ds)):
+        t[-1, -300:, last] = v.to(DEV)
+    A = torch.full((D,), 0.5, device=DEV)
+    ckpt = pal.palimpsa_gated_scan_checkpointed(x, r, A)[2]
+    got = pal.palimpsa_gated_scan_backward(x, r, A, None, None, None, None, ckpt, dy)
+    i = dict(x=xs, r=rs, A=torch.full((64,), 0.5), i=None, z=None, r_bias=None, i_bias=None, h0=None)
+    want = ssm.gradients(ssm.gate, _up(i), ds.to(F64), torch.zeros(1, 64, dtype=F64), [0, 300])[2]
+    for k in ("dx", "dr"):
+        _near(got[k][-1, -300:, last], want[k[1:]], HALF[BF] + FINE_G, k)
+        assert not got[k][:-1].any() and not got[k][-1, :, :D - 64].any()
+    _near(got["dA"][last], want["A"], FINE_G, "dA")     # (x and h are 0 in front of the last 300 tokens)
+    assert not got["dA"][:D - 64].any()
+    _status()
+
+
 def test_captured_and_replayed():
     """A training pass in a CUDA graph, replayed on new inputs and new offsets."""
     D, rows = 72, 500

@@ -208,6 +208,26 @@ def test_rows_of_wider_rows_and_in_place(dtype, D):
             assert torch.equal(g[k], h[k])
 
 
+def test_beyond_32_bits():
+    """More than 2^31 elements of an array: the last rows are those of a small call."""
+    D, some = 1024, 5
+    rows = 2 ** 31 // D + some
+    i = _dev(_inputs(7, some, D, BF))
+    big = {}
+    for k in ("x", "residual", "dy"):
+        big[k] = torch.zeros(rows, D, dtype=BF, device=DEV)
+        big[k][-some:] = i[k]
+    y, s, stats = pal.palimpsa_layer_norm(big["x"], i["weight"], i["bias"], big["residual"], want_stats=True)
+    wy, ws, wstats = pal.palimpsa_layer_norm(i["x"], i["weight"], i["bias"], i["residual"], want_stats=True)
+    assert torch.equal(y[-some:], wy) and torch.equal(s[-some:], ws) and torch.equal(stats[-some:], wstats)
+    assert torch.equal(y[0], i["bias"].bfloat16()) and torch.equal(y[-some - 1], y[0])
+    g = pal.palimpsa_layer_norm_backward(s, i["weight"], stats, big["dy"])
+    w = pal.palimpsa_layer_norm_backward(ws, i["weight"], wstats, i["dy"])
+    assert torch.equal(g["dx"][-some:], w["dx"]) and not g["dx"][:-some].any()
+    for k in ("dweight", "dbias"):
+        _near(g[k], w[k].cpu(), FINE_G, k)
+
+
 def test_no_rows():
     x, w = torch.empty(0, 72, device=DEV), torch.ones(72, device=DEV)
     y, s, st = pal.palimpsa_layer_norm(x, w, w, x, want_stats=True)
