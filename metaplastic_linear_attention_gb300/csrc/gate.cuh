@@ -9,7 +9,7 @@
 namespace palimpsa {
 
 constexpr int kPiece = kGateCheckpoint;  // tokens that a group of threads holds
-constexpr int kGateCluster = 8;          // CTAs of a cluster, at most (the portable limit)
+constexpr int kGateCluster = 12;         // CTAs of a cluster, at most
 
 // A tile of CH channels by a piece of tokens for each of the CTA's groups of threads, CPT
 // channels a thread.
@@ -30,9 +30,12 @@ struct GatePlan {
   int channels, cluster;
   double us;  // the time that the model gives
 };
+struct GateCost {
+  double round, cta, ends, hop;  // see gate_plan
+};
 // `tokens` of a CTA's tile of 64 channels (twice as many at `narrow`, the least channels of a tile),
 // `resident` CTAs on an SM.
-GatePlan gate_plan(const SeqRows& r, int D, int tokens, int resident, int narrow);
+GatePlan gate_plan(const SeqRows& r, int D, int tokens, int resident, int narrow, const GateCost& c);
 // Whether the batch's sequences are better walked by a thread (or a warp) each, `rate` channel-tokens a
 // microsecond, than in tiles with plan p.
 bool gate_short(const SeqRows& r, int D, const GatePlan& p, double rate);

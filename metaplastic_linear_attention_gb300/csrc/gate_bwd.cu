@@ -392,7 +392,7 @@ cudaError_t run(const GateArgs& a, float* sums, cudaStream_t s) {
   constexpr int bytes = BwdSmem<BF16, IN, GATE>::given + (CLUSTER ? 512 : 0);
   const auto kernel = palimpsa_gate_bwd_kernel<BF16, IN, GATE, CLUSTER>;
   static SharedBytes allowed;
-  cudaError_t e = allow_shared(kernel, bytes, &allowed);
+  cudaError_t e = allow_shared(kernel, bytes, &allowed, CLUSTER);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute cluster = {};
   cluster.id = cudaLaunchAttributeClusterDimension;
@@ -429,11 +429,11 @@ size_t plan_gate_backward(GateArgs* a) {
   // In fp32 an SM's shared memory holds 2 CTAs with both gates, 3 with one and 4 without.
   const int resident = a->bf16 ? kResident : 4 - (a->i != nullptr) - (a->z != nullptr);
   const int tokens = a->bf16 ? Tile<true>::tokens : Tile<false>::tokens;
-  const GatePlan p = gate_plan(a->rows, a->D, tokens, resident, 64);
+  const GatePlan p = gate_plan(a->rows, a->D, tokens, resident, 64, {1.6, 1.4, 0.25, 0.04});
   a->cluster = p.cluster;
   a->groups = 0;
   long long rows = (long long)a->rows.n_seq * a->cluster;
-  if (gate_short(a->rows, a->D, p, 330e3)) {
+  if (gate_short(a->rows, a->D, p, a->bf16 ? 225e3 : 150e3)) {
     // As many groups of warps as the GPU holds at once and the sequences fill.
     const long long tiles = (a->D + 63) / 64, held = (long long)kShortCtas * sms_of_device() / tiles;
     rows = a->groups = (int)std::max(1ll, std::min(held, (a->rows.n_seq + kShortWarps - 1ll) / kShortWarps));

@@ -405,7 +405,7 @@ cudaError_t run(const GateArgs& a, cudaStream_t s) {
   constexpr int bytes = 2 * kStageBytes<BF16, IN> + (CLUSTER ? 2 * G::group * 16 : 0);
   const auto kernel = palimpsa_gate_kernel<BF16, IN, GATE, CLUSTER, CH>;
   static SharedBytes allowed;
-  const cudaError_t e = allow_shared(kernel, bytes, &allowed);
+  const cudaError_t e = allow_shared(kernel, bytes, &allowed, CLUSTER);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute cluster = {};
   cluster.id = cudaLaunchAttributeClusterDimension;
@@ -424,8 +424,8 @@ cudaError_t run(const GateArgs& a, cudaStream_t s) {
 template <bool BF16, bool IN, bool GATE>
 cudaError_t forward(const GateArgs& given, cudaStream_t s) {
   GateArgs a = given;
-  const GatePlan p = gate_plan(a.rows, a.D, Tile<BF16, 64>::tokens, kResident, 32);
-  if (gate_short(a.rows, a.D, p, 400e3)) {
+  const GatePlan p = gate_plan(a.rows, a.D, Tile<BF16, 64>::tokens, kResident, 32, {1.8, 0.55, 0.5, 0.06});
+  if (gate_short(a.rows, a.D, p, BF16 ? 430e3 : 330e3)) {
     const long long blocks = ((long long)(a.D / 4) * a.rows.n_seq + 127) / 128;
     if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
     palimpsa_gate_short_kernel<BF16, IN, GATE><<<(unsigned)blocks, 128, 0, s>>>(a);
@@ -447,47 +447,52 @@ cudaError_t step(const GateArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-// The cheapest of 1 to 8 CTAs a cluster and of 64 or 32 channels a tile, by a model of the time.
-// A round of a CTA with c CTAs on its SM takes some 0.9 + 0.78 c us in bf16, and a CTA costs 1.5
-// rounds besides. The last wave has as many CTAs an SM as are left. A tile of 32 channels has
-// twice the pieces to fold: 6 % more. A packed batch's CTAs have the mean of the rounds (and half
-// of one lost), but none is done before its longest sequence's rounds, one after the other.
-// Measured, 8 x 4096 x 1536 with clusters of 1, 2, 3, 4 and 8: 110, 88, 78, 88 and 87 us (3 is
-// taken: 576 CTAs where 608 fit; 768 are a wave and a rest); 1 x 32768 x 2048 with 64 channels a
-// tile and 8: 174, with 32 channels (taken): 161.
-GatePlan gate_plan(const SeqRows& r, int D, int tokens, int resident, int narrow) {
+// The cheapest of 1 to 12 CTAs a cluster and of 64 or 32 channels a tile, by a model of the time (its
+// constants fitted to 44 sweeps of both passes, from 2 x 3000 x 520 to 8 x 4096 x 2048; what it takes
+// is within 2 % of the best on average, and within 12). A round of a CTA with c CTAs on its SM takes
+// c `cta` us and a `round` besides, and a CTA `ends` rounds besides its own. Clusters leave some SMs
+// short of CTAs (larger than 12, a quarter of them; powers of two fewer). Where there is one wave, the SMs with the most
+// CTAs set its pace, half the way from the mean; in the last of several less so. Handing the state
+// on takes `hop` a tile. A tile of 32 channels has twice the pieces to fold: 12 % more. A packed
+// batch's CTAs have the mean of the rounds (and half of one lost) and fill the slots as they come free;
+// what the longest sequence has beyond the mean comes behind that, by 0.9 of it (6 ragged batches:
+// within 3 % of the best on average, and within 11).
+// Measured, 8 x 4096 x 1536 with clusters of 1, 2, 3, 4 and 8: 111, 90, 78 (taken: 576 CTAs where 584
+// fit), 90 and 87 us; 8 x 4096 x 2048 166, 139, 147, 127 (taken) and 134; 1 x 32768 x 512 in tiles of
+// 32 channels with 6, 8, 12 and 16: 110, 103, 81 (taken) and 80, backward 240, 171, 136 and 149.
+GatePlan gate_plan(const SeqRows& r, int D, int tokens, int resident, int narrow, const GateCost& c) {
   const int sms = sms_of_device();
-  const double slots = (double)resident * sms;
   GatePlan best = {64, 1, 0};
-  double least = 0;
   for (int ch = 64; ch >= narrow; ch /= 2) {
     const double tiles = (D + ch - 1) / ch;
     for (int cs = 1; cs <= kGateCluster; ++cs) {
       const long long per = (long long)cs * tokens * (64 / ch);
       const double longest = (double)((r.max_len + per - 1) / per);
       const double rounds = r.cu ? std::min(longest, (double)r.T / per / r.n_seq + 0.5) : longest;
+      const double slots = (cs == 1 ? 1 : cs > 8 ? 0.84 : cs & (cs - 1) ? 0.95 : 0.96) * resident * sms;
       const double ctas = tiles * r.n_seq * cs, waves = std::floor(ctas / slots), rest = ctas - waves * slots;
-      const double full = 0.9 + 0.78 * resident, some = 0.9 + 0.78 * rest / sms;
-      double cost = (rounds + 1.5) * (waves * full + (rest > 0 ? some : 0));
-      cost = std::max(cost, (longest + 1.5) * (waves >= 1 ? full : some)) * (ch == 64 ? 1 : 1.06);
-      if ((ch == 64 && cs == 1) || cost < least) {
-        best = {ch, cs, cost};
-        least = cost;
-      }
+      const double mean = rest / sms, load = mean + (waves > 0 ? 0.4 : 0.5) * (std::ceil(mean) - mean);
+      const double full = c.round + c.cta * resident, some = rest > 0 ? c.round + c.cta * load : 0;
+      const double one = waves > 0 ? full : some;
+      double us = (rounds + c.ends) * (waves * full + some);
+      if (r.cu) us = (rounds + c.ends) * (waves > 0 ? ctas / slots * full : some) + 0.9 * (longest - rounds) * one;
+      if (cs > 1) us += longest * cs * c.hop;
+      if (ch < 64) us *= 1.12;
+      if ((ch == 64 && cs == 1) || us < best.us) best = {ch, cs, us};
     }
   }
   return best;
 }
 
-// A token takes a thread 0.35 to 0.45 us at least, and the GPU's threads together come to `rate`. The
-// rates are those that choose right against the model of the tiles, which is too dear for tiles with
-// few rounds. Measured in bf16 with both gates, threads against tiles: 256 x 4 x 2048 8.5 us and 41,
-// 256 x 16 20.7 and 45, 256 x 64 76 and 72 (threads are taken), 256 x 256 274 and 226; backward, warps
-// against tiles, 19 and 84, 45 and 107, 150 and 154 (warps are taken), 575 and 497. In fp32 512 x 32 x
-// 2048 105 and 124, 256 x 256 389 and 391; backward 217 and 236, 829 and 785 (warps are taken).
+// A token takes a thread 0.35 to 0.45 us at least, and the GPU's threads together come to `rate`. Measured
+// in bf16 with both gates, threads against tiles: 256 x 4 x 2048 8.5 us and 41, 256 x 16 20.7 and 45,
+// 256 x 64 76 and 72 (threads are taken), 256 x 256 274 and 226; backward, warps against tiles, 19 and
+// 84, 45 and 107, 150 and 154, 575 and 497. In fp32 512 x 32 x 2048 105 and 124, 256 x 256 389 and 391;
+// backward 217 and 236, 829 and 785. Where the sequences differ, the threads of the longest end last: 300
+// of 1 to 581 tokens, 218 on average, x 1536, backward 774 and 428.
 bool gate_short(const SeqRows& r, int D, const GatePlan& p, double rate) {
-  const double rows = r.cu ? r.T : (double)r.n_seq * r.T;
-  return std::max(rows * D / rate, 0.45 * r.max_len) < p.us;
+  const double rows = r.cu ? r.T : (double)r.n_seq * r.T, uneven = r.max_len - rows / r.n_seq;
+  return std::max(rows * D / rate, 0.45 * r.max_len) + 0.35 * std::max(uneven, 0.0) < p.us;
 }
 
 cudaError_t launch_gate_forward(const GateArgs& a, cudaStream_t s) { PALIMPSA_GATE_DISPATCH(forward, a, s) }

@@ -188,14 +188,14 @@ inline int sms_of_device() {
   if (dev >= 0 && dev < 64) known[dev].store(sms, std::memory_order_relaxed);
   return sms;
 }
-// Lets a kernel have `bytes` of dynamic shared memory: a call of the runtime only when this device
-// has not yet allowed it as many. `allowed` is the kernel's own.
+// Lets a kernel have `bytes` of dynamic shared memory (and, if wide, clusters of more than 8): calls of
+// the runtime only when this device has not yet allowed it as many. `allowed` is the kernel's own.
 struct SharedBytes {
   std::atomic<int> on[64] = {};
   std::mutex raising;  // two calls at once must not leave the smaller of their limits
 };
 template <class K>
-cudaError_t allow_shared(K kernel, int bytes, SharedBytes* allowed) {
+cudaError_t allow_shared(K kernel, int bytes, SharedBytes* allowed, bool wide = false) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -205,6 +205,7 @@ cudaError_t allow_shared(K kernel, int bytes, SharedBytes* allowed) {
   std::lock_guard<std::mutex> lock(allowed->raising);
   if (on.load() >= bytes) return cudaSuccess;
   e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && wide) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e == cudaSuccess) on.store(bytes);
   return e;
 }

@@ -114,7 +114,7 @@ def _case(dtype, lens, dense, D, gates="iz", bias=True, state=True, tail=0, inpu
 # From one token on, around the pieces of 8 tokens and the tiles of 64 (32 in fp32) and 64 channels, and lengths that
 # clusters of every size share.
 SHAPES = [(1, 1, 8), (2, 7, 64), (3, 8, 72), (1, 9, 128), (2, 31, 136), (1, 33, 64), (2, 63, 8), (1, 65, 200), (2, 130, 64),
-          (1, 200, 72), (1, 515, 64), (1, 1500, 40), (64, 70, 512), (200, 33, 320), (3, 300, 1024)]
+          (1, 200, 72), (1, 515, 64), (1, 1500, 40), (1, 2100, 64), (2, 3500, 24), (64, 70, 512), (200, 33, 320), (3, 300, 1024)]
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
