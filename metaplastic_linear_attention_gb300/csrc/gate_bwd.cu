@@ -17,7 +17,7 @@
 // pieces in shared memory and over CTAs by a second kernel, in a fixed order: no atomics, the
 // same bits every time.
 // Measured (GB300, bf16, both gates): 198 us at 8 x 4096 x 1536 (138 for its bytes at the rate of a
-// copy), 40 at 4 x 2048 x 1024 (23); fp32 at 0.81 to 0.84 of that rate. What a token keeps
+// copy), 40 at 4 x 2048 x 1024 (23); fp32 at 0.87 to 0.93 of that rate. What a token keeps
 // (the decay, four factors, its part of g_t) takes 96 of the 128 registers that 16 warps an SM allow.
 #include <algorithm>
 

@@ -20,8 +20,8 @@
 // one's shared memory that a barrier there counts. (A ring: with all summaries sent to all, the
 // CTAs of a cluster went in step, and 8 x 4096 x 1536 took 83 us, now 78.)
 // Measured (GB300, bf16): 78 us at 8 x 4096 x 1536 without z (5.2 TB/s, 59 at the rate of a
-// copy), 164 at 1 x 32768 x 2048 with z (4.1 TB/s, 99), in fp32 at a copy's rate. The warp
-// schedulers issue in 55 to 60 % of their cycles, with the 16 warps an SM that 128 registers and two
+// copy), 164 at 1 x 32768 x 2048 with z (4.1 TB/s, 99), 225 at 256 x 256 x 2048 (6.0 TB/s), where
+// CTAs are many; in fp32 at a copy's rate. The warp schedulers issue in 50 to 60 % of their cycles, with the 16 warps an SM that 128 registers and two
 // stages of inputs allow.
 //
 // Rounding: gates, decays and states are fp32; y is rounded to the input type once.
