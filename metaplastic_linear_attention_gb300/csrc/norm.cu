@@ -6,7 +6,7 @@
 //
 // Bound by HBM: 4 bytes a value in bf16 (8 with a residual), backward 6 (8), against some 15 and
 // 20 operations. A row's team of threads, each with 8 to 64 columns, is 4 to 16
-// lanes (up to 128 columns), a warp (forward up to 2048, backward up to 512) or a CTA.
+// lanes (up to 128 columns), a warp (forward up to 2048, backward up to 512 and in bf16 1024) or a CTA.
 // A grid of as many CTAs as the GPU holds walks the rows; the next ones come by asynchronous
 // copies into a ring in shared memory, each thread its own columns, so the copies need no barrier.
 // The squares are summed about the row's mean, which is known by then; where a row is a CTA's,
@@ -19,8 +19,8 @@
 //
 // Measured (GB300): 71 us at 32768 x 1536 in bf16 with a residual (5.7 TB/s, 59 at the rate of a
 // copy), backward 61; rows of 64 to 4096 columns run at 0.75 to 0.9 of a copy's rate in fp32 and
-// 0.7 to 0.9 in bf16 where most of a team's threads have columns (just above a limit, 72, 264, 520 or
-// 4104, half of them have none: 0.45 to 0.65).
+// 0.6 to 0.9 in bf16 where most of a team's threads have columns (just above a limit, 72, 264, 1032,
+// 2056 or 4104, half of them have none: 0.45 to 0.7).
 //
 // Rounding: sums and statistics are fp32; outputs are rounded to the input type once.
 #include <algorithm>
@@ -324,7 +324,7 @@ palimpsa_norm_kernel(NormArgs a) {
 
 // sums: [CTAs, 2, D], the CTAs' parts of dweight and dbias, or null.
 template <bool BF16, int LANES, bool MULTI, int COLS, int R, bool DS>
-__global__ void __launch_bounds__(MULTI ? 512 : 256, MULTI ? 1 : COLS == 16 ? 2 : 3)
+__global__ void __launch_bounds__(MULTI ? 8192 / COLS : COLS > 16 ? 128 : 256, MULTI ? 1 : COLS == 16 ? 2 : 3)
 palimpsa_norm_bwd_kernel(NormArgs a, float* sums) {
   using W = Walk<BF16, LANES, MULTI, COLS, R, 2 + DS>;
   constexpr int V = W::V, P = W::P;
@@ -529,7 +529,7 @@ template <bool BF16, int LANES, bool MULTI, int COLS, int R, bool MORE>
 cudaError_t backward(const NormArgs& a, float* sums, int* ctas, cudaStream_t s) {
   using W = Walk<BF16, LANES, MULTI, COLS, R, 2 + MORE>;
   const auto kernel = palimpsa_norm_bwd_kernel<BF16, LANES, MULTI, COLS, R, MORE>;
-  const int threads = MULTI ? row_threads<COLS>(a) : 256;
+  const int threads = MULTI ? row_threads<COLS>(a) : COLS > 16 ? 128 : 256;
   static Held known;
   Shape p;
   const cudaError_t e = shape_of(kernel, a, threads, MULTI ? 1 : threads / LANES, threads * 16 * W::S * W::planes,
@@ -543,6 +543,8 @@ cudaError_t backward(const NormArgs& a, float* sums, int* ctas, cudaStream_t s) 
   return cudaGetLastError();
 }
 
+// (Two rows at a time in a CTA halve its barriers: 4096 columns in bf16 without a residual 47 us -> 43 for
+// 96 MB; in fp32, whose rows are twice as long, 38.7 -> 39.9.)
 template <bool BF16, bool MORE>
 cudaError_t forward_by_width(const NormArgs& a, cudaStream_t s) {
   if (a.D <= 32) return forward<BF16, 4, false, 8, 2, MORE>(a, s);
@@ -553,8 +555,11 @@ cudaError_t forward_by_width(const NormArgs& a, cudaStream_t s) {
   if (a.D <= 1024) return forward<BF16, 32, false, 32, 1, MORE>(a, s);
   if (a.D <= 1536) return forward<BF16, 32, false, 48, 1, MORE>(a, s);
   if (a.D <= 2048) return forward<BF16, 32, false, 64, 1, MORE>(a, s);
-  return forward<BF16, 32, true, 32, 1, MORE>(a, s);
+  return forward<BF16, 32, true, 32, BF16 && !MORE ? 2 : 1, MORE>(a, s);
 }
+// (In bf16 a CTA a row with 16 columns a thread has too little to do between its barriers: 520, 768 and
+// 1024 columns 92, 70 and 61 us for 96 MB, with a warp a row 68, 57 and 57; 8192 with 32 columns a
+// thread 77 -> 69. From 1032 to 2048 a warp a row, its weight in shared memory, is no faster.)
 template <bool BF16, bool MORE>
 cudaError_t backward_by_width(const NormArgs& a, float* sums, int* ctas, cudaStream_t s) {
   if (a.D <= 32) return backward<BF16, 4, false, 8, BF16 ? 2 : 1, MORE>(a, sums, ctas, s);
@@ -562,6 +567,11 @@ cudaError_t backward_by_width(const NormArgs& a, float* sums, int* ctas, cudaStr
   if (a.D <= 128) return backward<BF16, 16, false, 8, BF16 ? 2 : 1, MORE>(a, sums, ctas, s);
   if (a.D <= 256) return backward<BF16, 32, false, 8, BF16 ? 2 : 1, MORE>(a, sums, ctas, s);
   if (a.D <= 512) return backward<BF16, 32, false, 16, BF16 ? 2 : 1, MORE>(a, sums, ctas, s);
+  if constexpr (BF16) {
+    if (a.D <= 768) return backward<true, 32, false, 24, 2, MORE>(a, sums, ctas, s);
+    if (a.D <= 1024) return backward<true, 32, false, 32, 2, MORE>(a, sums, ctas, s);
+    if (a.D >= 4096) return backward<true, 32, true, 32, 1, MORE>(a, sums, ctas, s);
+  }
   return backward<BF16, 32, true, 16, BF16 ? 2 : 1, MORE>(a, sums, ctas, s);
 }
 cudaError_t backward_any(const NormArgs& a, float* sums, int* ctas, cudaStream_t s) {

@@ -90,7 +90,7 @@ def _case(rows, D, dtype, residual, affine, with_ds, eps=1e-5, shape=None):
 
 
 # Widths around the teams' limits (8 lanes to 64, a warp to 256, a CTA with one vector a thread to 4096, two to 8192).
-WIDTHS = [8, 16, 56, 64, 72, 128, 248, 256, 264, 520, 1024, 1536, 2048, 4088, 4096, 4104, 6152, 8192]
+WIDTHS = [8, 16, 56, 64, 72, 128, 248, 256, 264, 520, 768, 776, 1024, 1032, 1536, 2048, 4088, 4096, 4104, 6152, 8192]
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
