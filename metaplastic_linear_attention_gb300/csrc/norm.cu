@@ -5,8 +5,8 @@
 // (ds: the gradient that reaches s past the norm; x and residual both receive ds'.)
 //
 // Bound by HBM: 4 bytes a value in bf16 (8 with a residual), backward 6 (8), against some 15 and
-// 20 operations. A row's team of threads, each with 8 to 64 columns, is 4 to 16
-// lanes (up to 128 columns), a warp (forward up to 2048, backward up to 512 and in bf16 1024) or a CTA.
+// 20 operations. A row's team of threads, each with 8 to 64 columns, is 2 to 32 lanes (forward up to 2048
+// columns, backward up to 512 and in bf16 1024) or a CTA.
 // A grid of as many CTAs as the GPU holds walks the rows; the next ones come by asynchronous
 // copies into a ring in shared memory, each thread its own columns, so the copies need no barrier.
 // The squares are summed about the row's mean, which is known by then; where a row is a CTA's,
@@ -18,9 +18,8 @@
 // order: no atomics, the same bits every time.
 //
 // Measured (GB300): 71 us at 32768 x 1536 in bf16 with a residual (5.7 TB/s, 59 at the rate of a
-// copy), backward 61; rows of 64 to 4096 columns run at 0.75 to 0.9 of a copy's rate in fp32 and
-// 0.6 to 0.9 in bf16 where most of a team's threads have columns (just above a limit, 72, 264, 1032,
-// 2056 or 4104, half of them have none: 0.45 to 0.7).
+// copy), backward 61; rows of 16 to 2048 columns run at 0.7 to 0.9 of a copy's rate (the backward in bf16
+// at 0.6 to 0.85), wider ones at 0.7 to 0.9 in fp32 and 0.45 to 0.9 in bf16.
 //
 // Rounding: sums and statistics are fp32; outputs are rounded to the input type once.
 #include <algorithm>
@@ -543,29 +542,42 @@ cudaError_t backward(const NormArgs& a, float* sums, int* ctas, cudaStream_t s) 
   return cudaGetLastError();
 }
 
+// (Few lanes with many columns each: a lane without columns does the same work, and sums over lanes take
+// steps. 136, 264 and 384 columns in bf16 with 8 or 16 lanes of 24: 40, 38 and 37 us for 96 MB; with a warp of
+// 8 or 16 each: 56, 57 and 44. 64 columns with 2 lanes of 32: 41, with 8 of 8: 37.)
 // (Two rows at a time in a CTA halve its barriers: 4096 columns in bf16 without a residual 47 us -> 43 for
 // 96 MB; in fp32, whose rows are twice as long, 38.7 -> 39.9.)
 template <bool BF16, bool MORE>
 cudaError_t forward_by_width(const NormArgs& a, cudaStream_t s) {
+  if (a.D <= (BF16 ? 16 : 8)) return forward<BF16, 2, false, 8, 2, MORE>(a, s);
   if (a.D <= 32) return forward<BF16, 4, false, 8, 2, MORE>(a, s);
   if (a.D <= 64) return forward<BF16, 8, false, 8, 2, MORE>(a, s);
-  if (a.D <= 128) return forward<BF16, 16, false, 8, 2, MORE>(a, s);
-  if (a.D <= 256) return forward<BF16, 32, false, 8, 2, MORE>(a, s);
-  if (a.D <= 512) return forward<BF16, 32, false, 16, 2, MORE>(a, s);
+  if (a.D <= 96) return forward<BF16, 4, false, 24, 2, MORE>(a, s);
+  if (a.D <= 128) return forward<BF16, 4, false, 32, 2, MORE>(a, s);
+  if (a.D <= 192) return forward<BF16, 8, false, 24, 2, MORE>(a, s);
+  if (a.D <= 256) return forward<BF16, 8, false, 32, 2, MORE>(a, s);
+  if (a.D <= 384) return forward<BF16, 16, false, 24, 2, MORE>(a, s);
+  if (a.D <= 512) return forward<BF16, 16, false, 32, 2, MORE>(a, s);
   if (a.D <= 1024) return forward<BF16, 32, false, 32, 1, MORE>(a, s);
   if (a.D <= 1536) return forward<BF16, 32, false, 48, 1, MORE>(a, s);
   if (a.D <= 2048) return forward<BF16, 32, false, 64, 1, MORE>(a, s);
   return forward<BF16, 32, true, 32, BF16 && !MORE ? 2 : 1, MORE>(a, s);
 }
+// (As in the forward: 72, 136, 264 columns in bf16 78, 70 and 68 us; with 16 lanes or a warp of 8 or 16 columns
+// each 97, 99 and 82.)
 // (In bf16 a CTA a row with 16 columns a thread has too little to do between its barriers: 520, 768 and
 // 1024 columns 92, 70 and 61 us for 96 MB, with a warp a row 68, 57 and 57; 8192 with 32 columns a
 // thread 77 -> 69. From 1032 to 2048 a warp a row, its weight in shared memory, is no faster.)
 template <bool BF16, bool MORE>
 cudaError_t backward_by_width(const NormArgs& a, float* sums, int* ctas, cudaStream_t s) {
+  if (a.D <= (BF16 ? 16 : 8)) return backward<BF16, 2, false, 8, 1, MORE>(a, sums, ctas, s);
   if (a.D <= 32) return backward<BF16, 4, false, 8, BF16 ? 2 : 1, MORE>(a, sums, ctas, s);
-  if (a.D <= 64) return backward<BF16, 8, false, 8, BF16 ? 2 : 1, MORE>(a, sums, ctas, s);
-  if (a.D <= 128) return backward<BF16, 16, false, 8, BF16 ? 2 : 1, MORE>(a, sums, ctas, s);
-  if (a.D <= 256) return backward<BF16, 32, false, 8, BF16 ? 2 : 1, MORE>(a, sums, ctas, s);
+  if (a.D <= 64) return backward<BF16, BF16 ? 4 : 8, false, BF16 ? 16 : 8, BF16 ? 2 : 1, MORE>(a, sums, ctas, s);
+  if (a.D <= 96) return backward<BF16, 4, false, 24, BF16 ? 2 : 1, MORE>(a, sums, ctas, s);
+  if (a.D <= 128) return backward<BF16, 8, false, 16, BF16 ? 2 : 1, MORE>(a, sums, ctas, s);
+  if (a.D <= 192) return backward<BF16, 8, false, 24, BF16 ? 2 : 1, MORE>(a, sums, ctas, s);
+  if (a.D <= 256) return backward<BF16, 16, false, 16, BF16 ? 2 : 1, MORE>(a, sums, ctas, s);
+  if (a.D <= 384) return backward<BF16, 16, false, 24, BF16 ? 2 : 1, MORE>(a, sums, ctas, s);
   if (a.D <= 512) return backward<BF16, 32, false, 16, BF16 ? 2 : 1, MORE>(a, sums, ctas, s);
   if constexpr (BF16) {
     if (a.D <= 768) return backward<true, 32, false, 24, 2, MORE>(a, sums, ctas, s);

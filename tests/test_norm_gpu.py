@@ -89,8 +89,9 @@ def _case(rows, D, dtype, residual, affine, with_ds, eps=1e-5, shape=None):
         _near(g["dbias"], i["dy"].to(F64).sum(0), FINE_G, "dbias")
 
 
-# Widths around the teams' limits (8 lanes to 64, a warp to 256, a CTA with one vector a thread to 4096, two to 8192).
-WIDTHS = [8, 16, 56, 64, 72, 128, 248, 256, 264, 520, 768, 776, 1024, 1032, 1536, 2048, 4088, 4096, 4104, 6152, 8192]
+# Widths around the teams' limits.
+WIDTHS = [8, 16, 24, 32, 56, 64, 72, 96, 104, 128, 136, 192, 200, 248, 256, 264, 384, 392, 512, 520, 768, 776, 1024, 1032, 1536,
+          1544, 2048, 2056, 4088, 4096, 4104, 6152, 8192]
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
@@ -116,9 +117,10 @@ def test_leading_dimensions(shape):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
-def test_many_rows(dtype):
+@pytest.mark.parametrize("rows,D", [(60001, 72), (120001, 16), (60001, 64), (30001, 264), (20001, 520), (20001, 1024), (5001, 2056),
+                                    (5001, 4104)])
+def test_many_rows(dtype, rows, D):
     """More rows than the GPU's CTAs hold at once: every CTA walks several batches. Against torch in 64 bits on the GPU."""
-    rows, D = 60001, 72
     g = torch.Generator(device=DEV).manual_seed(1)
     x, dy = (torch.randn(rows, D, generator=g, device=DEV).to(dtype) for _ in range(2))
     w, b = torch.rand(D, generator=g, device=DEV) + 0.5, torch.randn(D, generator=g, device=DEV)
