@@ -19,7 +19,7 @@
 //
 // Measured (GB300): 71 us at 32768 x 1536 in bf16 with a residual (5.7 TB/s, 59 at the rate of a
 // copy), backward 61; rows of 16 to 2048 columns run at 0.7 to 0.9 of a copy's rate (the backward in bf16
-// at 0.6 to 0.85), wider ones at 0.7 to 0.9 in fp32 and 0.45 to 0.9 in bf16.
+// at 0.55 to 0.85), wider ones at 0.65 to 0.9 in fp32 and 0.5 to 0.9 in bf16.
 //
 // Rounding: sums and statistics are fp32; outputs are rounded to the input type once.
 #include <algorithm>
@@ -189,7 +189,7 @@ template <int COLS>
 constexpr bool kSharedParams = COLS > 16;
 
 template <bool BF16, int LANES, bool MULTI, int COLS, int R, bool RES>
-__global__ void __launch_bounds__(COLS > 16 && !MULTI ? 128 : 256, MULTI ? 2 : COLS == 16 ? 3 : 4)
+__global__ void __launch_bounds__(MULTI ? 8192 / COLS : COLS > 16 ? 128 : 256, MULTI ? 2 : COLS == 16 ? 3 : 4)
 palimpsa_norm_kernel(NormArgs a) {
   using W = Walk<BF16, LANES, MULTI, COLS, R, 1 + RES>;
   constexpr int V = W::V, P = W::P;
@@ -546,7 +546,8 @@ cudaError_t backward(const NormArgs& a, float* sums, int* ctas, cudaStream_t s) 
 // steps. 136, 264 and 384 columns in bf16 with 8 or 16 lanes of 24: 40, 38 and 37 us for 96 MB; with a warp of
 // 8 or 16 each: 56, 57 and 44. 64 columns with 2 lanes of 32: 41, with 8 of 8: 37.)
 // (Two rows at a time in a CTA halve its barriers: 4096 columns in bf16 without a residual 47 us -> 43 for
-// 96 MB; in fp32, whose rows are twice as long, 38.7 -> 39.9.)
+// 96 MB; in fp32, whose rows are twice as long, 38.7 -> 39.9. Above 4096, one row with 64 columns a thread:
+// 8192 66 -> 52; with a residual 82 -> 83.)
 template <bool BF16, bool MORE>
 cudaError_t forward_by_width(const NormArgs& a, cudaStream_t s) {
   if (a.D <= (BF16 ? 16 : 8)) return forward<BF16, 2, false, 8, 2, MORE>(a, s);
@@ -561,6 +562,8 @@ cudaError_t forward_by_width(const NormArgs& a, cudaStream_t s) {
   if (a.D <= 1024) return forward<BF16, 32, false, 32, 1, MORE>(a, s);
   if (a.D <= 1536) return forward<BF16, 32, false, 48, 1, MORE>(a, s);
   if (a.D <= 2048) return forward<BF16, 32, false, 64, 1, MORE>(a, s);
+  if constexpr (BF16 && !MORE)
+    if (a.D > 4096) return forward<true, 32, true, 64, 1, false>(a, s);
   return forward<BF16, 32, true, 32, BF16 && !MORE ? 2 : 1, MORE>(a, s);
 }
 // (As in the forward: 72, 136, 264 columns in bf16 78, 70 and 68 us; with 16 lanes or a warp of 8 or 16 columns
