@@ -848,7 +848,7 @@ int palimpsa_abi_version(void);
  * issuing their first staged copy, so that their wait can never be satisfied
  * and must run out; 0 restores normal operation. In the gated scan it makes the
  * first CTA of a cluster hand no state (or gradient) on in its first round, so that the
- * others' waits run out. Neither changes results otherwise.
+ * others' waits run out; with 2, hand it on late, when they have. Neither changes results otherwise.
  */
 void palimpsa_set_wait_timeout_ns(uint64_t ns);
 void palimpsa_debug_withhold_first_copy(int on);

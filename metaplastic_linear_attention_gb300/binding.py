@@ -163,8 +163,8 @@ def palimpsa_set_wait_timeout_ns(ns: int) -> None:
     load_library().palimpsa_set_wait_timeout_ns(int(ns))
 
 
-def palimpsa_debug_withhold_first_copy(on: bool) -> None:
-    load_library().palimpsa_debug_withhold_first_copy(1 if on else 0)
+def palimpsa_debug_withhold_first_copy(on: bool | int) -> None:
+    load_library().palimpsa_debug_withhold_first_copy(int(on))
 
 
 def palimpsa_set_forward_segments(segments: int) -> None:

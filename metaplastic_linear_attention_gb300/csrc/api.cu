@@ -625,7 +625,7 @@ int palimpsa_abi_version(void) { return PALIMPSA_ABI_VERSION; }
 
 void palimpsa_set_wait_timeout_ns(uint64_t ns) { g_wait_timeout_ns.store(ns); }
 
-void palimpsa_debug_withhold_first_copy(int on) { g_withhold_first_copy.store(on ? 1 : 0); }
+void palimpsa_debug_withhold_first_copy(int on) { g_withhold_first_copy.store(on == 2 ? 2 : on ? 1 : 0); }
 
 void palimpsa_set_forward_segments(int segments) { g_forward_segments.store(segments > 0 ? segments : 0); }
 

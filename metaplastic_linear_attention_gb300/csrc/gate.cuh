@@ -168,6 +168,24 @@ __device__ __forceinline__ bool cluster_wait(uint64_t* bar, uint32_t parity, uns
       if (cluster_try_wait(bar, parity)) return true;
     if (global_ns() - t0 >= timeout_ns) return cluster_try_wait(bar, parity);
   }
+}// Tests: until the others' waits have run out.
+__device__ __forceinline__ void pass_the_limit(const GateArgs& a) {
+  const unsigned long long t0 = global_ns(), late = 4 * min(a.wait_timeout_ns, 250000000ull) + 20000000ull;
+  while (global_ns() - t0 < late) __nanosleep(1000);
+}
+// The end of a ring. An asynchronous store is seen to have landed by its barrier alone, not by a
+// barrier of the cluster. A CTA whose waits have all held has seen every one of its states. Where a wait
+// has run out, one that was merely late may still be under way; so each CTA tells the next one for how
+// many rounds it has sent a state, and after the cluster's barrier, when no more are sent, the CTA's
+// first thread waits (2 s at most) for those beyond the `good` rounds that it has seen. (A round's
+// state is sent by all of its threads or none, and none once a wait of one of them has run out: a ring
+// that breaks leaves two such states at most, one of them in a round for whose bytes this thread has
+// not yet arrived.)
+__device__ __forceinline__ void settle(uint64_t* bars, int good, int told, uint32_t bytes) {
+  for (int k = good; k < told; ++k) {
+    if (k > good) mbar_arrive_expect_tx(&bars[k & 1], bytes);
+    if (!cluster_wait(&bars[k & 1], (k >> 1) & 1, 2000000000ull)) return;
+  }
 }
 
 __device__ __forceinline__ float2 ffma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }

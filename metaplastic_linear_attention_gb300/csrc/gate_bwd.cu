@@ -160,6 +160,7 @@ palimpsa_gate_bwd_kernel(GateArgs a, int tiles, float* sums) {
   constexpr int kI = 3, kZ = 3 + IN;  // places of the arrays x, r, dy, i, z
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ uint64_t bars[2];
+  __shared__ int told, good[2];  // see settle; the turns whose wait has held, for the first thread and for all of the first warp
   float4* const agg = reinterpret_cast<float4*>(smem + S::agg);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int cs = CLUSTER ? a.cluster : 1;
@@ -218,6 +219,7 @@ palimpsa_gate_bwd_kernel(GateArgs a, int tiles, float* sums) {
   if (CLUSTER && tid == 0) {
     mbar_init(&bars[0], 1);
     mbar_init(&bars[1], 1);
+    good[0] = good[1] = rounds;
     fence_mbar_init();
   }
   const float2 A = pair_or(a.A, ch, in, 1.f);
@@ -230,6 +232,7 @@ palimpsa_gate_bwd_kernel(GateArgs a, int tiles, float* sums) {
   bool waits = true;
   const long long yd = (long long)a.D * ES;
   if (CLUSTER) cg::this_cluster().sync();  // every CTA has started, its barriers set: it may be written to
+  if (CLUSTER && a.late && rank == cs - 1) pass_the_limit(a);
 
   for (int k = rounds - 1; k >= 0; --k) {
     const int tp = k * step + rank * RT + warp * kPiece;
@@ -295,16 +298,21 @@ palimpsa_gate_bwd_kernel(GateArgs a, int tiles, float* sums) {
           Pc = __fmul2_rn(Pc, make_float2(e.x, e.y));
         }
       float2* const given = reinterpret_cast<float2*>(smem + S::given) + lane;
-      waits = waits && cluster_wait(&bars[turn & 1], (turn >> 1) & 1, a.wait_timeout_ns);
-      if (!waits) latch_status(a.status, kStatusTimeout);
+      if (waits && !cluster_wait(&bars[turn & 1], (turn >> 1) & 1, a.wait_timeout_ns)) {
+        waits = false;
+        if (tid == 0) good[0] = turn;
+        latch_status(a.status, kStatusTimeout);
+      }
       if (!end) c = given[(turn & 1) * 32];
       if (warp == 0) {
+        const bool all = __all_sync(~0u, waits);
+        if (!all) good[1] = min(good[1], turn);
         Cc = ffma2(Pc, c, Cc);
         const int next = rank == 0 ? turn + 1 : turn;  // the turn of the CTA before
         if (next < rounds) {
           const int to = rank == 0 ? cs - 1 : rank - 1;
           // (Where a wait has run out, nothing more is handed on: the others' waits run out too.)
-          if (waits && !(a.withhold && end))
+          if (all && !(a.withhold && end))
             st_async(cluster_addr(given + (next & 1) * 32, to), Cc, cluster_addr(&bars[next & 1], to));
         } else if (in && a.dh0) {
           *reinterpret_cast<float2*>(a.dh0 + n * a.D + ch) = Cc;
@@ -321,7 +329,15 @@ palimpsa_gate_bwd_kernel(GateArgs a, int tiles, float* sums) {
   if ((!CLUSTER || rounds == 0) && rank == 0 && warp == 0 && in && a.dh0)
     *reinterpret_cast<float2*>(a.dh0 + n * a.D + ch) = carry;
   res.leave(reinterpret_cast<float2*>(agg), part, a.D, NP, in);
-  if (CLUSTER) cg::this_cluster().sync();  // nobody hands anything to a CTA that has left
+  if (CLUSTER) {
+    // Nobody hands anything to a CTA that has left.
+    if (tid == 0) {
+      const int sent = a.withhold && rank == cs - 1 ? 0 : rank == 0 ? min(good[1] + 1, rounds) : good[1];
+      *cg::this_cluster().map_shared_rank(&told, rank == 0 ? cs - 1 : rank - 1) = sent;
+    }
+    cg::this_cluster().sync();
+    if (tid == 0) settle(bars, good[0], told, 256);
+  }
 }
 
 // Short sequences, many of them (see the forward's): a warp takes 64 channels of one sequence after

@@ -81,6 +81,7 @@ __global__ void __launch_bounds__(BF16 ? 128 : 64, kResident) palimpsa_gate_kern
   constexpr int ES = G::ES, RT = G::tokens, NP = G::pieces, LG = G::group, kStage = kStageBytes<BF16, IN>;
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ uint64_t bars[2];
+  __shared__ int told, good[2];  // see settle; the rounds whose wait has held, for the first thread and for all of the last group
   const int tid = threadIdx.x, piece = tid / LG, lane = tid % LG;
   const int cs = CLUSTER ? a.cluster : 1;
   const int rank = CLUSTER ? (int)(blockIdx.x % cs) : 0;
@@ -132,6 +133,7 @@ __global__ void __launch_bounds__(BF16 ? 128 : 64, kResident) palimpsa_gate_kern
   if (CLUSTER && tid == 0) {
     mbar_init(&bars[0], 1);
     mbar_init(&bars[1], 1);
+    good[0] = good[1] = rounds;
     fence_mbar_init();
   }
   // Parameters, the gates' biases as their exponents' addends.
@@ -146,7 +148,9 @@ __global__ void __launch_bounds__(BF16 ? 128 : 64, kResident) palimpsa_gate_kern
     if (a.h0 && in) carry.v[j] = *reinterpret_cast<const float2*>(a.h0 + n * a.D + ch + 2 * j);
   }
   bool waits = true;
+  constexpr unsigned kLast = ~0u << (32 - LG);  // the last group's lanes
   if (CLUSTER) cg::this_cluster().sync();  // every CTA has started, its barriers set: it may be written to
+  if (CLUSTER && a.late && rank == 0) pass_the_limit(a);
 
   const long long yd = (long long)a.D * ES;
   for (int k = 0; k < rounds; ++k) {
@@ -229,16 +233,21 @@ __global__ void __launch_bounds__(BF16 ? 128 : 64, kResident) palimpsa_gate_kern
           Pc.times(sums_of(w)[0]);
         }
       float4* const states = reinterpret_cast<float4*>(smem + 2 * kStage) + lane;
-      waits = waits && cluster_wait(&bars[k & 1], (k >> 1) & 1, a.wait_timeout_ns);
-      if (!waits) latch_status(a.status, kStatusTimeout);
+      if (waits && !cluster_wait(&bars[k & 1], (k >> 1) & 1, a.wait_timeout_ns)) {
+        waits = false;
+        if (tid == 0) good[0] = k;
+        latch_status(a.status, kStatusTimeout);
+      }
       if (k + rank > 0) h.set(states[(k & 1) * LG]);
       if (last) {
+        const bool all = __all_sync(kLast, waits);
+        if (!all) good[1] = min(good[1], k);
         Hc.fold_after(Pc, h);
         const int next = rank + 1 == cs ? k + 1 : k;  // its round
         if (next < rounds) {
           const int to = rank + 1 == cs ? 0 : rank + 1;
           // (Where a wait has run out, nothing more is handed on: the others' waits run out too.)
-          if (waits && !(a.withhold && k + rank == 0))
+          if (all && !(a.withhold && k + rank == 0))
             st_async(cluster_addr(states + (next & 1) * LG, to), Hc.all(), cluster_addr(&bars[next & 1], to));
         } else if (in) {
           *reinterpret_cast<float4*>(a.h_T + n * a.D + ch) = Hc.all();
@@ -277,7 +286,15 @@ __global__ void __launch_bounds__(BF16 ? 128 : 64, kResident) palimpsa_gate_kern
   if ((!CLUSTER || rounds == 0) && rank == 0 && piece == 0 && in)
     *reinterpret_cast<float4*>(a.h_T + n * a.D + ch) = carry.all();
   __syncwarp();
-  if (CLUSTER) cg::this_cluster().sync();  // nobody hands anything to a CTA that has left
+  if (CLUSTER) {
+    // Nobody hands anything to a CTA that has left.
+    if (piece == NP - 1 && lane == 0) {
+      const int sent = a.withhold && rank == 0 ? 0 : rank + 1 == cs ? min(good[1] + 1, rounds) : good[1];
+      *cg::this_cluster().map_shared_rank(&told, rank + 1 == cs ? 0 : rank + 1) = sent;
+    }
+    cg::this_cluster().sync();
+    if (tid == 0) settle(bars, good[0], told, LG * 16);
+  }
 }
 
 // Short sequences, many of them: a thread takes 4 channels of a sequence and walks its tokens, with

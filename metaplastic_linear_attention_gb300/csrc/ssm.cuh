@@ -230,7 +230,7 @@ struct GateArgs {
   unsigned int* status;
   int cluster = 1;      // CTAs that share a sequence's time, set by the launcher
   unsigned long long wait_timeout_ns = 0;
-  int withhold = 0;     // tests: the first CTA of a cluster hands nothing on in its first round
+  bool withhold = false, late = false;  // tests: the first CTA of a cluster hands nothing on in its first round, or late
   // backward
   const float* ckpt_in = nullptr;
   const void* dy = nullptr;

@@ -140,7 +140,8 @@ GateArgs gate_args(const void* x, const void* r, const float* A, const void* i, 
   a.D = D;
   a.bf16 = t == PALIMPSA_BF16;
   a.wait_timeout_ns = wait_timeout_ns();
-  a.withhold = withhold_first();
+  a.withhold = withhold_first() == 1;
+  a.late = withhold_first() == 2;
   return a;
 }
 
