@@ -39,7 +39,8 @@ using Tile = GateTile<BF16, 64, 2, BF16 ? 256 : 128>;
 template <bool BF16, bool IN, bool GATE>
 struct BwdSmem {
   static constexpr int h = (3 + IN + GATE) * Tile<BF16>::bytes, stage = h + Tile<BF16>::pieces * Tile<BF16>::CH * 4;
-  static constexpr int agg = 2 * stage, given = agg + Tile<BF16>::pieces * 512;
+  static constexpr int agg = 2 * stage, rates = agg + Tile<BF16>::pieces * 512,
+                       given = rates + Tile<BF16>::pieces * 256;
 };
 
 // A thread's piece: 8 tokens of two neighbouring channels.
@@ -47,6 +48,7 @@ template <bool BF16, bool IN, bool GATE>
 struct Piece {
   // The decays, the factors of g_t in dx, di, dr and dA, and dy silu(z).
   float2 da[kPiece], fx[kPiece], fi[IN ? kPiece : 1], fr[kPiece], fA[kPiece], gy[kPiece];
+  float2 W = make_float2(0.f, 0.f);  // the rates' sum
 
   __device__ __forceinline__ void no_token(int t) {
     da[t] = make_float2(1.f, 1.f);
@@ -64,6 +66,7 @@ struct Piece {
     const float2 w = __fmul2_rn(A, s);
     float2 q;  // 1 - a^2
     decay_of(w, &da[t], &q);
+    W = __fadd2_rn(W, w);
     // (A rate of 0 has 1 / n of 5e18, and no gradient: the factor w of dr, or s of dA, is 0 too.)
     const float2 ni = make_float2(rsqrt_approx(q.x), rsqrt_approx(q.y));
     fx[t] = __fmul2_rn(q, ni);
@@ -162,6 +165,7 @@ palimpsa_gate_bwd_kernel(GateArgs a, int tiles, float* sums) {
   __shared__ uint64_t bars[2];
   __shared__ int told, good[2];  // see settle; the turns whose wait has held, for the first thread and for all of the first warp
   float4* const agg = reinterpret_cast<float4*>(smem + S::agg);
+  float2* const rates = reinterpret_cast<float2*>(smem + S::rates);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int cs = CLUSTER ? a.cluster : 1;
   const int rank = CLUSTER ? (int)(blockIdx.x % cs) : 0;
@@ -226,8 +230,9 @@ palimpsa_gate_bwd_kernel(GateArgs a, int tiles, float* sums) {
   const float2 scale = make_float2(-kLog2e, -kLog2e);
   const float2 rb = __fmul2_rn(pair_or(a.r_bias, ch, in, 0.f), scale), ib = __fmul2_rn(pair_or(a.i_bias, ch, in, 0.f), scale);
   if (!pos_finite(A.x) || !pos_finite(A.y)) latch_status(a.status, kStatusDomain);
-  float2 carry = zero;  // a g of the token behind the round (in a cluster, behind the sequence)
-  if (a.dh_T && in) carry = *reinterpret_cast<const float2*>(a.dh_T + n * a.D + ch);
+  // a g of the token behind this CTA's rounds, two places in turn.
+  float2* const given = reinterpret_cast<float2*>(smem + S::given) + lane;
+  if (rank == cs - 1 && warp == 0) given[0] = a.dh_T && in ? *reinterpret_cast<const float2*>(a.dh_T + n * a.D + ch) : zero;
   Results<BF16, IN, GATE> res;
   bool waits = true;
   const long long yd = (long long)a.D * ES;
@@ -276,58 +281,51 @@ palimpsa_gate_bwd_kernel(GateArgs a, int tiles, float* sums) {
       P = __fmul2_rn(P, p.da[t]);
     }
     agg[warp * 32 + lane] = make_float4(P.x, P.y, C.x, C.y);
+    rates[warp * 32 + lane] = p.W;
     __syncthreads();
 
-    // The gradient that comes in from behind the piece, and the one that the round passes on.
-    float2 c = carry;
-    if (!CLUSTER) {
+    // The first warp works out the CTA's summary, and hands on what goes back from the tile (as in the forward).
+    float2 Cc = zero, Pc, Lc;
+    if (warp == 0) {
+      float2 Wc = zero, rest;
 #pragma unroll
-      for (int q = NP - 1; q >= 0; --q) {
-        const float4 e = agg[q * 32 + lane];
-        if (q == warp) c = carry;
-        carry = ffma2(make_float2(e.x, e.y), carry, make_float2(e.z, e.w));
+      for (int w = NP - 1; w >= 0; --w) {
+        const float4 e = agg[w * 32 + lane];
+        Cc = ffma2(make_float2(e.x, e.y), Cc, make_float2(e.z, e.w));
+        Wc = __fadd2_rn(Wc, rates[w * 32 + lane]);
       }
-    } else {
-      // The first warp works out the CTA's summary, and hands on what goes back from the tile.
-      float2 Pc = make_float2(1.f, 1.f), Cc = zero;
-      if (warp == 0)
-#pragma unroll
-        for (int w = NP - 1; w >= 0; --w) {
-          const float4 e = agg[w * 32 + lane];
-          Cc = ffma2(make_float2(e.x, e.y), Cc, make_float2(e.z, e.w));
-          Pc = __fmul2_rn(Pc, make_float2(e.x, e.y));
-        }
-      float2* const given = reinterpret_cast<float2*>(smem + S::given) + lane;
-      if (waits && !cluster_wait(&bars[turn & 1], (turn >> 1) & 1, a.wait_timeout_ns)) {
-        waits = false;
-        if (tid == 0) good[0] = turn;
-        latch_status(a.status, kStatusTimeout);
-      }
-      if (!end) c = given[(turn & 1) * 32];
-      if (warp == 0) {
+      decay_of(Wc, &Pc, &rest, &Lc);
+    }
+    if (CLUSTER && waits && !cluster_wait(&bars[turn & 1], (turn >> 1) & 1, a.wait_timeout_ns)) {
+      waits = false;
+      if (tid == 0) good[0] = turn;
+      latch_status(a.status, kStatusTimeout);
+    }
+    float2 c = given[(turn & 1) * 32];
+    if (warp == 0) {
+      Cc = ffma2(Pc, c, ffma2(Lc, c, Cc));
+      const int next = rank == 0 ? turn + 1 : turn;  // the turn of the CTA before
+      if (next >= rounds) {
+        if (in && a.dh0) *reinterpret_cast<float2*>(a.dh0 + n * a.D + ch) = Cc;
+      } else if (!CLUSTER) {
+        given[(next & 1) * 32] = Cc;
+      } else {
+        const int to = rank == 0 ? cs - 1 : rank - 1;
+        // (Where a wait has run out, nothing more is handed on: the others' waits run out too.)
         const bool all = __all_sync(~0u, waits);
         if (!all) good[1] = min(good[1], turn);
-        Cc = ffma2(Pc, c, Cc);
-        const int next = rank == 0 ? turn + 1 : turn;  // the turn of the CTA before
-        if (next < rounds) {
-          const int to = rank == 0 ? cs - 1 : rank - 1;
-          // (Where a wait has run out, nothing more is handed on: the others' waits run out too.)
-          if (all && !(a.withhold && end))
-            st_async(cluster_addr(given + (next & 1) * 32, to), Cc, cluster_addr(&bars[next & 1], to));
-        } else if (in && a.dh0) {
-          *reinterpret_cast<float2*>(a.dh0 + n * a.D + ch) = Cc;
-        }
+        else if (!(a.withhold && end))
+          st_async(cluster_addr(given + (next & 1) * 32, to), Cc, cluster_addr(&bars[next & 1], to));
       }
-      for (int w = NP - 1; w > warp; --w) {
-        const float4 e = agg[w * 32 + lane];
-        c = ffma2(make_float2(e.x, e.y), c, make_float2(e.z, e.w));
-      }
+    }
+    for (int w = NP - 1; w > warp; --w) {
+      const float4 e = agg[w * 32 + lane];
+      c = ffma2(make_float2(e.x, e.y), c, make_float2(e.z, e.w));
     }
     if (in && np > 0) res.finish(a, p, np, at + (np - 1) * yd, yd, c);
     __syncwarp();
   }
-  if ((!CLUSTER || rounds == 0) && rank == 0 && warp == 0 && in && a.dh0)
-    *reinterpret_cast<float2*>(a.dh0 + n * a.D + ch) = carry;
+  if (rounds == 0 && rank == cs - 1 && warp == 0 && in && a.dh0) *reinterpret_cast<float2*>(a.dh0 + n * a.D + ch) = given[0];
   res.leave(reinterpret_cast<float2*>(agg), part, a.D, NP, in);
   if (CLUSTER) {
     // Nobody hands anything to a CTA that has left.
@@ -393,7 +391,13 @@ __global__ void __launch_bounds__(32 * kShortWarps, kShortCtas) palimpsa_gate_sh
           if (t < np) token(t);
         }
       }
-      c = res.finish(a, p, np, at + (np - 1) * yd, yd, c);
+      // (What the piece's decays leave out of their product, for the gradient that goes on.)
+      float2 P, q, left, Q = p.da[0];
+      decay_of(p.W, &P, &q, &left);
+#pragma unroll
+      for (int t = 1; t < kPiece; ++t) Q = __fmul2_rn(Q, p.da[t]);
+      left = __fadd2_rn(left, __fadd2_rn(P, make_float2(-Q.x, -Q.y)));
+      c = ffma2(left, c, res.finish(a, p, np, at + (np - 1) * yd, yd, c));
     }
     if (a.dh0) *reinterpret_cast<float2*>(a.dh0 + n * a.D + ch) = c;
   }
@@ -405,7 +409,7 @@ cudaError_t run(const GateArgs& a, float* sums, cudaStream_t s) {
   using G = Tile<BF16>;
   const long long tiles = (a.D + G::CH - 1) / G::CH, blocks = tiles * a.rows.n_seq * a.cluster;
   if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
-  constexpr int bytes = BwdSmem<BF16, IN, GATE>::given + (CLUSTER ? 512 : 0);
+  constexpr int bytes = BwdSmem<BF16, IN, GATE>::given + 512;
   const auto kernel = palimpsa_gate_bwd_kernel<BF16, IN, GATE, CLUSTER>;
   static SharedBytes allowed;
   cudaError_t e = allow_shared(kernel, bytes, &allowed, CLUSTER);

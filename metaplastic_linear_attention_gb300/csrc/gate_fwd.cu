@@ -56,21 +56,18 @@ struct Four {
     v[0] = ffma2(make_float2(P.x, P.y), v[0], make_float2(H.x, H.y));
     v[1] = ffma2(make_float2(P.z, P.w), v[1], make_float2(H.z, H.w));
   }
-  __device__ __forceinline__ void times(const float4& P) {
-    v[0] = __fmul2_rn(v[0], make_float2(P.x, P.y));
-    v[1] = __fmul2_rn(v[1], make_float2(P.z, P.w));
+  __device__ __forceinline__ void add(const float4& f) {
+    v[0] = __fadd2_rn(v[0], make_float2(f.x, f.y));
+    v[1] = __fadd2_rn(v[1], make_float2(f.z, f.w));
   }
-  // v + P h
-  __device__ __forceinline__ void fold_after(const Four& P, const Four& h) {
-    v[0] = ffma2(P.v[0], h.v[0], v[0]);
-    v[1] = ffma2(P.v[1], h.v[1], v[1]);
-  }
-  __device__ __forceinline__ void set(const float4& f) {
-    v[0] = make_float2(f.x, f.y);
-    v[1] = make_float2(f.z, f.w);
+  // v + P h + L h
+  __device__ __forceinline__ void fold_after(const Four& P, const Four& L, const Four& h) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) v[j] = ffma2(P.v[j], h.v[j], ffma2(L.v[j], h.v[j], v[j]));
   }
   __device__ __forceinline__ float4 all() const { return make_float4(v[0].x, v[0].y, v[1].x, v[1].y); }
 };
+__device__ __forceinline__ Four four(const float4& f) { return {make_float2(f.x, f.y), make_float2(f.z, f.w)}; }
 __device__ __forceinline__ Four four(float v) { return {make_float2(v, v), make_float2(v, v)}; }
 
 template <bool BF16, bool IN, bool GATE, bool CLUSTER, int CH>
@@ -138,14 +135,16 @@ __global__ void __launch_bounds__(BF16 ? 128 : 64, kResident) palimpsa_gate_kern
   }
   // Parameters, the gates' biases as their exponents' addends.
   float2 A[2], rb[2], ib[2];
-  Four carry = four(0.f);  // the state before the round (in a cluster, before the first)
+  // The states before this CTA's rounds, two places in turn.
+  float4* const states = reinterpret_cast<float4*>(smem + 2 * kStage) + lane;
+  if (rank == 0 && piece == 0)
+    states[0] = a.h0 && in ? *reinterpret_cast<const float4*>(a.h0 + n * a.D + ch) : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
     A[j] = pair_or(a.A, ch + 2 * j, in, 1.f);
     if (!pos_finite(A[j].x) || !pos_finite(A[j].y)) latch_status(a.status, kStatusDomain);
     rb[j] = __fmul2_rn(pair_or(a.r_bias, ch + 2 * j, in, 0.f), make_float2(-kLog2e, -kLog2e));
     if (IN) ib[j] = __fmul2_rn(pair_or(a.i_bias, ch + 2 * j, in, 0.f), make_float2(-kLog2e, -kLog2e));
-    if (a.h0 && in) carry.v[j] = *reinterpret_cast<const float2*>(a.h0 + n * a.D + ch + 2 * j);
   }
   bool waits = true;
   constexpr unsigned kLast = ~0u << (32 - LG);  // the last group's lanes
@@ -167,6 +166,7 @@ __global__ void __launch_bounds__(BF16 ? 128 : 64, kResident) palimpsa_gate_kern
     stage(k + 1);
 
     float2 da[kPiece][2], b[kPiece][2];
+    Four W = four(0.f);  // the rates' sum
     auto token = [&](int t) {
       float2 x[2], r[2], i[2];
       Q::unpack(*reinterpret_cast<const Raw*>(raw + (t ^ odd) * G::row), x);
@@ -176,7 +176,9 @@ __global__ void __launch_bounds__(BF16 ? 128 : 64, kResident) palimpsa_gate_kern
       for (int j = 0; j < 2; ++j) {
         const float2 s = sigmoid_of(ffma2(r[j], make_float2(-kLog2e, -kLog2e), rb[j]));
         float2 sq;
-        decay_of(__fmul2_rn(A[j], s), &da[t][j], &sq);
+        const float2 w = __fmul2_rn(A[j], s);
+        W.v[j] = __fadd2_rn(W.v[j], w);
+        decay_of(w, &da[t][j], &sq);
         b[t][j] = IN ? input_of(sq, one_plus(ffma2(i[j], make_float2(-kLog2e, -kLog2e), ib[j])), x[j])
                      : input_of(sq, x[j]);
       }
@@ -204,6 +206,7 @@ __global__ void __launch_bounds__(BF16 ? 128 : 64, kResident) palimpsa_gate_kern
     __syncwarp();  // the piece's rows of x are read
     sums_of(piece)[0] = P.all();
     sums_of(piece)[LG] = H.all();
+    sums_of(piece)[2 * LG] = W.all();
     Raw z[kPiece];  // on their way during the exchange
     if (GATE && in) {
       const char* p = static_cast<const char*>(a.z) + ((row0 + tp) * a.z_ld + ch) * ES;
@@ -213,48 +216,47 @@ __global__ void __launch_bounds__(BF16 ? 128 : 64, kResident) palimpsa_gate_kern
     }
     __syncthreads();
 
-    // The state before the piece, and the one before the next round.
-    Four h = carry;
-    if (!CLUSTER) {
-#pragma unroll
-      for (int q = 0; q < NP; ++q) {
-        if (q == piece) h = carry;
-        carry.fold(sums_of(q)[0], sums_of(q)[LG]);
+    // The last group works out the CTA's summary, and hands on the state behind the tile: the decay from the
+    // rates' sum, so that no state gathers the roundings of products. (Two places for it. A cluster's are each
+    // written again only after this CTA's next state has gone round.)
+    const bool last = piece == NP - 1;
+    Four Hc = four(0.f), Pc, Lc;
+    if (last) {
+      Four Wc = four(0.f);
+#pragma unroll 2  // (registers: in full, 1 x 32768 x 2048 takes 182 us, 171 so)
+      for (int w = 0; w < NP; ++w) {
+        Hc.fold(sums_of(w)[0], sums_of(w)[LG]);
+        Wc.add(sums_of(w)[2 * LG]);
       }
-    } else {
-      // The last group works out the CTA's summary, and hands on the state behind the tile. (Two
-      // places for it, each written again only after this CTA's next state has gone round.)
-      const bool last = piece == NP - 1;
-      Four Pc = four(1.f), Hc = four(0.f);
-      if (last)
 #pragma unroll
-        for (int w = 0; w < NP; ++w) {
-          Hc.fold(sums_of(w)[0], sums_of(w)[LG]);
-          Pc.times(sums_of(w)[0]);
-        }
-      float4* const states = reinterpret_cast<float4*>(smem + 2 * kStage) + lane;
-      if (waits && !cluster_wait(&bars[k & 1], (k >> 1) & 1, a.wait_timeout_ns)) {
-        waits = false;
-        if (tid == 0) good[0] = k;
-        latch_status(a.status, kStatusTimeout);
+      for (int j = 0; j < 2; ++j) {
+        float2 rest;
+        decay_of(Wc.v[j], &Pc.v[j], &rest, &Lc.v[j]);
       }
-      if (k + rank > 0) h.set(states[(k & 1) * LG]);
-      if (last) {
+    }
+    if (CLUSTER && waits && !cluster_wait(&bars[k & 1], (k >> 1) & 1, a.wait_timeout_ns)) {
+      waits = false;
+      if (tid == 0) good[0] = k;
+      latch_status(a.status, kStatusTimeout);
+    }
+    Four h = four(states[(k & 1) * LG]);
+    if (last) {
+      Hc.fold_after(Pc, Lc, h);
+      const int next = rank + 1 == cs ? k + 1 : k;  // its round
+      if (next >= rounds) {
+        if (in) *reinterpret_cast<float4*>(a.h_T + n * a.D + ch) = Hc.all();
+      } else if (!CLUSTER) {
+        states[(next & 1) * LG] = Hc.all();
+      } else {
+        const int to = rank + 1 == cs ? 0 : rank + 1;
+        // (Where a wait has run out, nothing more is handed on: the others' waits run out too.)
         const bool all = __all_sync(kLast, waits);
         if (!all) good[1] = min(good[1], k);
-        Hc.fold_after(Pc, h);
-        const int next = rank + 1 == cs ? k + 1 : k;  // its round
-        if (next < rounds) {
-          const int to = rank + 1 == cs ? 0 : rank + 1;
-          // (Where a wait has run out, nothing more is handed on: the others' waits run out too.)
-          if (all && !(a.withhold && k + rank == 0))
-            st_async(cluster_addr(states + (next & 1) * LG, to), Hc.all(), cluster_addr(&bars[next & 1], to));
-        } else if (in) {
-          *reinterpret_cast<float4*>(a.h_T + n * a.D + ch) = Hc.all();
-        }
+        else if (!(a.withhold && k + rank == 0))
+          st_async(cluster_addr(states + (next & 1) * LG, to), Hc.all(), cluster_addr(&bars[next & 1], to));
       }
-      for (int w = 0; w < piece; ++w) h.fold(sums_of(w)[0], sums_of(w)[LG]);
     }
+    for (int w = 0; w < piece; ++w) h.fold(sums_of(w)[0], sums_of(w)[LG]);
     if (in && np > 0) {
       if (a.ckpt)
         *reinterpret_cast<float4*>(a.ckpt + (gate_ckpt_row0(a.rows, n, row0) + tp / kPiece) * a.D + ch) = h.all();
@@ -283,8 +285,7 @@ __global__ void __launch_bounds__(BF16 ? 128 : 64, kResident) palimpsa_gate_kern
     }
     __syncwarp();
   }
-  if ((!CLUSTER || rounds == 0) && rank == 0 && piece == 0 && in)
-    *reinterpret_cast<float4*>(a.h_T + n * a.D + ch) = carry.all();
+  if (rounds == 0 && rank == 0 && piece == 0 && in) *reinterpret_cast<float4*>(a.h_T + n * a.D + ch) = states[0];
   __syncwarp();
   if (CLUSTER) {
     // Nobody hands anything to a CTA that has left.
@@ -327,7 +328,7 @@ __global__ void __launch_bounds__(128, BF16 ? 5 : 4) palimpsa_gate_short_kernel(
     rb[j] = __fmul2_rn(pair_or(a.r_bias, ch + 2 * j, true, 0.f), scale);
     if (IN) ib[j] = __fmul2_rn(pair_or(a.i_bias, ch + 2 * j, true, 0.f), scale);
   }
-  if (a.h0) h.set(*reinterpret_cast<const float4*>(a.h0 + n * a.D + ch));
+  if (a.h0) h = four(*reinterpret_cast<const float4*>(a.h0 + n * a.D + ch));
   float* ckpt = a.ckpt ? a.ckpt + gate_ckpt_row0(a.rows, n, row0) * a.D + ch : nullptr;
   auto at = [&](const void* p, long long ld) { return static_cast<const char*>(p) + (row0 * ld + ch) * ES; };
   const char *px = at(a.x, a.x_ld), *pr = at(a.r, a.r_ld), *pi = at(a.i, a.i_ld), *pz = at(a.z, a.z_ld);
@@ -356,10 +357,10 @@ __global__ void __launch_bounds__(128, BF16 ? 5 : 4) palimpsa_gate_short_kernel(
         if (GATE) Q::unpack(z[t], fz);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          float2 da, sq;
-          decay_of(__fmul2_rn(A[j], sigmoid_of(ffma2(fr[j], scale, rb[j]))), &da, &sq);
+          float2 da, sq, left;
+          decay_of(__fmul2_rn(A[j], sigmoid_of(ffma2(fr[j], scale, rb[j]))), &da, &sq, &left);
           const float2 b = IN ? input_of(sq, one_plus(ffma2(fi[j], scale, ib[j])), fx[j]) : input_of(sq, fx[j]);
-          h.v[j] = ffma2(da, h.v[j], b);
+          h.v[j] = ffma2(da, h.v[j], ffma2(left, h.v[j], b));
           y[j] = GATE ? __fmul2_rn(h.v[j], silu_fast(fz[j])) : h.v[j];
         }
         *reinterpret_cast<Raw*>(py + (long long)t * a.D * ES) = Q::pack(y);
@@ -401,12 +402,12 @@ __global__ void __launch_bounds__(128) palimpsa_gate_step_kernel(GateArgs a) {
     bad |= !pos_finite(A.x) || !pos_finite(A.y);
     const float2 scale = make_float2(-kLog2e, -kLog2e);
     const float2 s = sigmoid_of(__fmul2_rn(__fadd2_rn(r[j], pair_or(a.r_bias, ch + 2 * j, true, 0.f)), scale));
-    float2 da, sq;
-    decay_of(__fmul2_rn(A, s), &da, &sq);
+    float2 da, sq, left;
+    decay_of(__fmul2_rn(A, s), &da, &sq, &left);
     const float2 b =
         IN ? input_of(sq, one_plus(__fmul2_rn(__fadd2_rn(i[j], pair_or(a.i_bias, ch + 2 * j, true, 0.f)), scale)), x[j])
            : input_of(sq, x[j]);
-    h[j] = ffma2(da, h[j], b);
+    h[j] = ffma2(da, h[j], ffma2(left, h[j], b));
     y[j] = GATE ? __fmul2_rn(h[j], silu_fast(z[j])) : h[j];
   }
   *state = make_float4(h[0].x, h[0].y, h[1].x, h[1].y);
@@ -419,7 +420,7 @@ cudaError_t run(const GateArgs& a, cudaStream_t s) {
   using G = Tile<BF16, CH>;
   const long long tiles = (a.D + CH - 1) / CH, blocks = tiles * a.rows.n_seq * a.cluster;
   if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
-  constexpr int bytes = 2 * kStageBytes<BF16, IN> + (CLUSTER ? 2 * G::group * 16 : 0);
+  constexpr int bytes = 2 * kStageBytes<BF16, IN> + 2 * G::group * 16;
   const auto kernel = palimpsa_gate_kernel<BF16, IN, GATE, CLUSTER, CH>;
   static SharedBytes allowed;
   const cudaError_t e = allow_shared(kernel, bytes, &allowed, CLUSTER);
