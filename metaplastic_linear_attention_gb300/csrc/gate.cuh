@@ -185,10 +185,10 @@ __device__ __forceinline__ void pass_the_limit(const GateArgs& a) {
 // barrier of the cluster. A CTA whose waits have all held has seen every one of its states. Where a wait
 // has run out, one that was merely late may still be under way; so each CTA tells the next one for how
 // many rounds it has sent a state, and after the cluster's barrier, when no more are sent, the CTA's
-// first thread waits (2 s at most) for those beyond the `good` rounds that it has seen. (A round's
-// state is sent by all of its threads or none, and none once a wait of one of them has run out: a ring
-// that breaks leaves two such states at most, one of them in a round for whose bytes this thread has
-// not yet arrived.)
+// first thread waits (2 s at most) for those beyond the `good` rounds that it has seen. (Where the waits
+// of some only of the threads that send a state have run out, the others have sent their parts, and these make
+// up for theirs before they tell. A ring that breaks leaves two such states at most, one of them in a
+// round for whose bytes this thread has not yet arrived.)
 __device__ __forceinline__ void settle(uint64_t* bars, int good, int told, uint32_t bytes) {
   for (int k = good; k < told; ++k) {
     if (k > good) mbar_arrive_expect_tx(&bars[k & 1], bytes);

@@ -40,7 +40,8 @@ template <bool BF16, bool IN, bool GATE>
 struct BwdSmem {
   static constexpr int h = (3 + IN + GATE) * Tile<BF16>::bytes, stage = h + Tile<BF16>::pieces * Tile<BF16>::CH * 4;
   static constexpr int agg = 2 * stage, rates = agg + Tile<BF16>::pieces * 512,
-                       given = rates + Tile<BF16>::pieces * 256;
+                       given = rates + Tile<BF16>::pieces * 256, own = given + 512,
+                       bytes = own + Tile<BF16>::threads * 8 * (2 + IN);
 };
 
 // A thread's piece: 8 tokens of two neighbouring channels.
@@ -163,7 +164,7 @@ palimpsa_gate_bwd_kernel(GateArgs a, int tiles, float* sums) {
   constexpr int kI = 3, kZ = 3 + IN;  // places of the arrays x, r, dy, i, z
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ uint64_t bars[2];
-  __shared__ int told, good[2];  // see settle; the turns whose wait has held, for the first thread and for all of the first warp
+  __shared__ int told, held[32];  // see settle; the turns whose wait has held, for the first warp's threads
   float4* const agg = reinterpret_cast<float4*>(smem + S::agg);
   float2* const rates = reinterpret_cast<float2*>(smem + S::rates);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -223,9 +224,9 @@ palimpsa_gate_bwd_kernel(GateArgs a, int tiles, float* sums) {
   if (CLUSTER && tid == 0) {
     mbar_init(&bars[0], 1);
     mbar_init(&bars[1], 1);
-    good[0] = good[1] = rounds;
     fence_mbar_init();
   }
+  if (CLUSTER && warp == 0) held[lane] = rounds;
   const float2 A = pair_or(a.A, ch, in, 1.f);
   const float2 scale = make_float2(-kLog2e, -kLog2e);
   const float2 rb = __fmul2_rn(pair_or(a.r_bias, ch, in, 0.f), scale), ib = __fmul2_rn(pair_or(a.i_bias, ch, in, 0.f), scale);
@@ -233,7 +234,10 @@ palimpsa_gate_bwd_kernel(GateArgs a, int tiles, float* sums) {
   // a g of the token behind this CTA's rounds, two places in turn.
   float2* const given = reinterpret_cast<float2*>(smem + S::given) + lane;
   if (rank == cs - 1 && warp == 0) given[0] = a.dh_T && in ? *reinterpret_cast<const float2*>(a.dh_T + n * a.D + ch) : zero;
-  Results<BF16, IN, GATE> res;
+  // The thread's sums over its rounds (in registers they would spill what the tokens keep).
+  float2* const own = reinterpret_cast<float2*>(smem + S::own) + tid;
+  own[0] = own[G::threads] = zero;
+  if (IN) own[2 * G::threads] = zero;
   bool waits = true;
   const long long yd = (long long)a.D * ES;
   if (CLUSTER) cg::this_cluster().sync();  // every CTA has started, its barriers set: it may be written to
@@ -298,7 +302,7 @@ palimpsa_gate_bwd_kernel(GateArgs a, int tiles, float* sums) {
     }
     if (CLUSTER && waits && !cluster_wait(&bars[turn & 1], (turn >> 1) & 1, a.wait_timeout_ns)) {
       waits = false;
-      if (tid == 0) good[0] = turn;
+      if (warp == 0) held[lane] = turn;
       latch_status(a.status, kStatusTimeout);
     }
     float2 c = given[(turn & 1) * 32];
@@ -312,9 +316,7 @@ palimpsa_gate_bwd_kernel(GateArgs a, int tiles, float* sums) {
       } else {
         const int to = rank == 0 ? cs - 1 : rank - 1;
         // (Where a wait has run out, nothing more is handed on: the others' waits run out too.)
-        const bool all = __all_sync(~0u, waits);
-        if (!all) good[1] = min(good[1], turn);
-        else if (!(a.withhold && end))
+        if (waits && !(a.withhold && end))
           st_async(cluster_addr(given + (next & 1) * 32, to), Cc, cluster_addr(&bars[next & 1], to));
       }
     }
@@ -322,19 +324,32 @@ palimpsa_gate_bwd_kernel(GateArgs a, int tiles, float* sums) {
       const float4 e = agg[w * 32 + lane];
       c = ffma2(make_float2(e.x, e.y), c, make_float2(e.z, e.w));
     }
-    if (in && np > 0) res.finish(a, p, np, at + (np - 1) * yd, yd, c);
+    if (in && np > 0) {
+      Results<BF16, IN, GATE> piece;
+      piece.finish(a, p, np, at + (np - 1) * yd, yd, c);
+      own[0] = __fadd2_rn(own[0], piece.sA);
+      own[G::threads] = __fadd2_rn(own[G::threads], piece.sr);
+      if (IN) own[2 * G::threads] = __fadd2_rn(own[2 * G::threads], piece.si);
+    }
     __syncwarp();
   }
   if (rounds == 0 && rank == cs - 1 && warp == 0 && in && a.dh0) *reinterpret_cast<float2*>(a.dh0 + n * a.D + ch) = given[0];
+  Results<BF16, IN, GATE> res;
+  res.sA = own[0];
+  res.sr = own[G::threads];
+  if (IN) res.si = own[2 * G::threads];
   res.leave(reinterpret_cast<float2*>(agg), part, a.D, NP, in);
   if (CLUSTER) {
     // Nobody hands anything to a CTA that has left.
-    if (tid == 0) {
-      const int sent = a.withhold && rank == cs - 1 ? 0 : rank == 0 ? min(good[1] + 1, rounds) : good[1];
-      *cg::this_cluster().map_shared_rank(&told, rank == 0 ? cs - 1 : rank - 1) = sent;
+    if (warp == 0) {
+      const int to = rank == 0 ? cs - 1 : rank - 1, on = rank == 0;
+      const int mine = a.withhold && rank == cs - 1 ? 0 : held[lane], sent = __reduce_max_sync(~0u, mine);
+      for (int k = mine + on; k < min(sent + on, rounds); ++k)
+        st_async(cluster_addr(given + (k & 1) * 32, to), zero, cluster_addr(&bars[k & 1], to));
+      if (lane == 0) *cg::this_cluster().map_shared_rank(&told, to) = min(sent + on, rounds);
     }
     cg::this_cluster().sync();
-    if (tid == 0) settle(bars, good[0], told, 256);
+    if (tid == 0) settle(bars, held[0], told, 256);
   }
 }
 
@@ -409,7 +424,7 @@ cudaError_t run(const GateArgs& a, float* sums, cudaStream_t s) {
   using G = Tile<BF16>;
   const long long tiles = (a.D + G::CH - 1) / G::CH, blocks = tiles * a.rows.n_seq * a.cluster;
   if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
-  constexpr int bytes = BwdSmem<BF16, IN, GATE>::given + 512;
+  constexpr int bytes = BwdSmem<BF16, IN, GATE>::bytes;
   const auto kernel = palimpsa_gate_bwd_kernel<BF16, IN, GATE, CLUSTER>;
   static SharedBytes allowed;
   cudaError_t e = allow_shared(kernel, bytes, &allowed, CLUSTER);

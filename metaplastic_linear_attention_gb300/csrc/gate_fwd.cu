@@ -78,7 +78,7 @@ __global__ void __launch_bounds__(BF16 ? 128 : 64, kResident) palimpsa_gate_kern
   constexpr int ES = G::ES, RT = G::tokens, NP = G::pieces, LG = G::group, kStage = kStageBytes<BF16, IN>;
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ uint64_t bars[2];
-  __shared__ int told, good[2];  // see settle; the rounds whose wait has held, for the first thread and for all of the last group
+  __shared__ int told, held[G::group + 1];  // see settle; the rounds whose wait has held, for the last group's threads and the first
   const int tid = threadIdx.x, piece = tid / LG, lane = tid % LG;
   const int cs = CLUSTER ? a.cluster : 1;
   const int rank = CLUSTER ? (int)(blockIdx.x % cs) : 0;
@@ -130,9 +130,10 @@ __global__ void __launch_bounds__(BF16 ? 128 : 64, kResident) palimpsa_gate_kern
   if (CLUSTER && tid == 0) {
     mbar_init(&bars[0], 1);
     mbar_init(&bars[1], 1);
-    good[0] = good[1] = rounds;
     fence_mbar_init();
   }
+  if (CLUSTER && piece == NP - 1) held[lane] = rounds;
+  if (CLUSTER && tid == 0) held[LG] = rounds;
   // Parameters, the gates' biases as their exponents' addends.
   float2 A[2], rb[2], ib[2];
   // The states before this CTA's rounds, two places in turn.
@@ -236,7 +237,8 @@ __global__ void __launch_bounds__(BF16 ? 128 : 64, kResident) palimpsa_gate_kern
     }
     if (CLUSTER && waits && !cluster_wait(&bars[k & 1], (k >> 1) & 1, a.wait_timeout_ns)) {
       waits = false;
-      if (tid == 0) good[0] = k;
+      if (tid == 0) held[LG] = k;
+      if (last) held[lane] = k;
       latch_status(a.status, kStatusTimeout);
     }
     Four h = four(states[(k & 1) * LG]);
@@ -250,9 +252,7 @@ __global__ void __launch_bounds__(BF16 ? 128 : 64, kResident) palimpsa_gate_kern
       } else {
         const int to = rank + 1 == cs ? 0 : rank + 1;
         // (Where a wait has run out, nothing more is handed on: the others' waits run out too.)
-        const bool all = __all_sync(kLast, waits);
-        if (!all) good[1] = min(good[1], k);
-        else if (!(a.withhold && k + rank == 0))
+        if (waits && !(a.withhold && k + rank == 0))
           st_async(cluster_addr(states + (next & 1) * LG, to), Hc.all(), cluster_addr(&bars[next & 1], to));
       }
     }
@@ -289,12 +289,15 @@ __global__ void __launch_bounds__(BF16 ? 128 : 64, kResident) palimpsa_gate_kern
   __syncwarp();
   if (CLUSTER) {
     // Nobody hands anything to a CTA that has left.
-    if (piece == NP - 1 && lane == 0) {
-      const int sent = a.withhold && rank == 0 ? 0 : rank + 1 == cs ? min(good[1] + 1, rounds) : good[1];
-      *cg::this_cluster().map_shared_rank(&told, rank + 1 == cs ? 0 : rank + 1) = sent;
+    if (piece == NP - 1) {
+      const int to = rank + 1 == cs ? 0 : rank + 1, on = rank + 1 == cs;
+      const int mine = a.withhold && rank == 0 ? 0 : held[lane], sent = __reduce_max_sync(kLast, mine);
+      for (int k = mine + on; k < min(sent + on, rounds); ++k)
+        st_async(cluster_addr(states + (k & 1) * LG, to), make_float4(0.f, 0.f, 0.f, 0.f), cluster_addr(&bars[k & 1], to));
+      if (lane == 0) *cg::this_cluster().map_shared_rank(&told, to) = min(sent + on, rounds);
     }
     cg::this_cluster().sync();
-    if (tid == 0) settle(bars, good[0], told, LG * 16);
+    if (tid == 0) settle(bars, held[LG], told, LG * 16);
   }
 }
 
