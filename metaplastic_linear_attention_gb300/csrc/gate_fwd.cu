@@ -168,7 +168,7 @@ __global__ void __launch_bounds__(BF16 ? 128 : 64, kResident) palimpsa_gate_kern
 
     float2 da[kPiece][2], b[kPiece][2];
     Four W = four(0.f);  // the rates' sum
-    auto token = [&](int t) {
+    auto token = [&](int t, bool open) {
       float2 x[2], r[2], i[2];
       Q::unpack(*reinterpret_cast<const Raw*>(raw + (t ^ odd) * G::row), x);
       Q::unpack(*reinterpret_cast<const Raw*>(raw + G::bytes + (t ^ odd) * G::row), r);
@@ -180,19 +180,36 @@ __global__ void __launch_bounds__(BF16 ? 128 : 64, kResident) palimpsa_gate_kern
         const float2 w = __fmul2_rn(A[j], s);
         W.v[j] = __fadd2_rn(W.v[j], w);
         decay_of(w, &da[t][j], &sq);
-        b[t][j] = IN ? input_of(sq, one_plus(ffma2(i[j], make_float2(-kLog2e, -kLog2e), ib[j])), x[j])
-                     : input_of(sq, x[j]);
+        const float2 u = IN ? ffma2(i[j], make_float2(-kLog2e, -kLog2e), ib[j]) : make_float2(0.f, 0.f);
+        b[t][j] = !IN ? input_of(sq, x[j]) : open ? open_input_of(sq, one_plus(u), x[j]) : input_of(sq, sigmoid_of(u), x[j]);
       }
     };
-    if (np == kPiece) {
+    // Whole pieces whose input gates are open far enough; others token by token.
+    bool open = true;
+    if (IN && np == kPiece) {
+      float2 low[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-      for (int t = 0; t < kPiece; ++t) token(t);
+      for (int t = 0; t < kPiece; ++t) {
+        float2 i[2];
+        Q::unpack(*reinterpret_cast<const Raw*>(raw + 2 * G::bytes + (t ^ odd) * G::row), i);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) low[j] = make_float2(fminf(low[j].x, i[j].x), fminf(low[j].y, i[j].y));
+      }
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const float2 u = ffma2(low[j], make_float2(-kLog2e, -kLog2e), ib[j]);
+        open = open && u.x <= -kLog2e * kOpenGate && u.y <= -kLog2e * kOpenGate;
+      }
+    }
+    if (np == kPiece && open) {
+#pragma unroll
+      for (int t = 0; t < kPiece; ++t) token(t, true);
     } else {
 #pragma unroll
       for (int t = 0; t < kPiece; ++t) {
         da[t][0] = da[t][1] = make_float2(1.f, 1.f);
         b[t][0] = b[t][1] = make_float2(0.f, 0.f);
-        if (t < np) token(t);
+        if (t < np) token(t, false);
       }
     }
     Four P = four(1.f), H = four(0.f);
@@ -224,7 +241,7 @@ __global__ void __launch_bounds__(BF16 ? 128 : 64, kResident) palimpsa_gate_kern
     Four Hc = four(0.f), Pc, Lc;
     if (last) {
       Four Wc = four(0.f);
-#pragma unroll 2  // (registers: in full, 1 x 32768 x 2048 takes 182 us, 171 so)
+#pragma unroll 4  // (in full it wants more registers than there are: 1 x 32768 x 2048 takes 177 us, 166 so)
       for (int w = 0; w < NP; ++w) {
         Hc.fold(sums_of(w)[0], sums_of(w)[LG]);
         Wc.add(sums_of(w)[2 * LG]);
@@ -362,7 +379,7 @@ __global__ void __launch_bounds__(128, BF16 ? 5 : 4) palimpsa_gate_short_kernel(
         for (int j = 0; j < 2; ++j) {
           float2 da, sq, left;
           decay_of(__fmul2_rn(A[j], sigmoid_of(ffma2(fr[j], scale, rb[j]))), &da, &sq, &left);
-          const float2 b = IN ? input_of(sq, one_plus(ffma2(fi[j], scale, ib[j])), fx[j]) : input_of(sq, fx[j]);
+          const float2 b = IN ? input_of(sq, sigmoid_of(ffma2(fi[j], scale, ib[j])), fx[j]) : input_of(sq, fx[j]);
           h.v[j] = ffma2(da, h.v[j], ffma2(left, h.v[j], b));
           y[j] = GATE ? __fmul2_rn(h.v[j], silu_fast(fz[j])) : h.v[j];
         }
@@ -408,7 +425,7 @@ __global__ void __launch_bounds__(128) palimpsa_gate_step_kernel(GateArgs a) {
     float2 da, sq, left;
     decay_of(__fmul2_rn(A, s), &da, &sq, &left);
     const float2 b =
-        IN ? input_of(sq, one_plus(__fmul2_rn(__fadd2_rn(i[j], pair_or(a.i_bias, ch + 2 * j, true, 0.f)), scale)), x[j])
+        IN ? input_of(sq, sigmoid_of(__fmul2_rn(__fadd2_rn(i[j], pair_or(a.i_bias, ch + 2 * j, true, 0.f)), scale)), x[j])
            : input_of(sq, x[j]);
     h[j] = ffma2(da, h[j], ffma2(left, h[j], b));
     y[j] = GATE ? __fmul2_rn(h[j], silu_fast(z[j])) : h[j];
