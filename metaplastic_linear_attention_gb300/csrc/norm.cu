@@ -179,10 +179,11 @@ __device__ __forceinline__ void spread(float mine, float (&v)[N]) {
   }
 }
 __device__ __forceinline__ float2 two(float x) { return make_float2(x, x); }
-// 1 / sqrt(x): the SFU's, with one step of Newton's method (0 where x has overflowed).
+// 1 / sqrt(x): the SFU's, with one step of Newton's method (0 where x has overflowed). x y is the root, a
+// normal number where x, and half of it, are not.
 __device__ __forceinline__ float rsqrt_of(float x) {
   const float y = rsqrtf(x);
-  return x <= 3.4e38f ? y * fmaf(-0.5f * x * y, y, 1.5f) : y;
+  return x <= 3.4e38f ? y * fmaf(x * y * -0.5f, y, 1.5f) : y;
 }
 
 template <int COLS>
