@@ -195,7 +195,7 @@ palimpsa_norm_kernel(NormArgs a) {
   using W = Walk<BF16, LANES, MULTI, COLS, R, 1 + RES>;
   constexpr int V = W::V, P = W::P;
   extern __shared__ __align__(16) unsigned char smem[];
-  __shared__ float2 parts[2][16][R];  // of the warps: sums, and squares about their means
+  __shared__ float2 parts[2][16][R];  // of the warps: means, and squares about them
   const W at(a.rows, a.D, smem);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, warps = blockDim.x / 32;
   const long long nx = at.apart(a.x_ld), nr = at.apart(a.residual_ld), ny = at.apart(a.D);
@@ -235,7 +235,7 @@ palimpsa_norm_kernel(NormArgs a) {
   for (int b = 0; b < at.batches; ++b) {
     cp_async_wait<W::S - 2>();
     float2 s[R][V][P];
-    float sum[R], sq[R], mean[R], rstd[R];
+    float mean[R], sq[R], rstd[R];
     bool live[R];
 #pragma unroll
     for (int j = 0; j < R; ++j) {
@@ -251,18 +251,18 @@ palimpsa_norm_kernel(NormArgs a) {
           for (int c = 0; c < P; ++c) s[j][v][c] = __fadd2_rn(s[j][v][c], r[c]);
           at.write(ps + j * ny, v, s[j][v], live[j] && at.has(v), true);
         }
+        // (Each value's part of the mean: the sum may pass fp32's range.)
 #pragma unroll
-        for (int c = 0; c < P; ++c) t = __fadd2_rn(t, s[j][v][c]);
+        for (int c = 0; c < P; ++c) t = __ffma2_rn(s[j][v][c], two(own), t);
       }
-      sum[j] = t.x + t.y;
+      mean[j] = t.x + t.y;
     }
     from = from + 1 == W::S ? 0 : from + 1;
     stage();  // into the stage of the batch before
-    const float sums = team_sums<LANES>(sum);
-    spread<LANES>(sums, sum);
+    const float means = team_sums<LANES>(mean);
+    spread<LANES>(means, mean);
 #pragma unroll
     for (int j = 0; j < R; ++j) {
-      mean[j] = sum[j] * own;
       float2 t = two(0.f);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
@@ -278,16 +278,15 @@ palimpsa_norm_kernel(NormArgs a) {
     }
     const float squares = team_sums<LANES>(sq);
     if (MULTI) {
-      if (lane % (32 / R) == 0) parts[b & 1][warp][lane / (32 / R)] = make_float2(sums, squares);
+      if (lane % (32 / R) == 0) parts[b & 1][warp][lane / (32 / R)] = make_float2(means, squares);
       __syncthreads();  // (two sets of parts: the last batch's may still be read)
 #pragma unroll
       for (int j = 0; j < R; ++j) {
         float m = 0.f, q = 0.f;
-        for (int w = 0; w < warps; ++w) m += parts[b & 1][w][j].x;
-        m *= whole;
+        for (int w = 0; w < warps; ++w) m = fmaf(parts[b & 1][w][j].x, count(w) * whole, m);
         for (int w = 0; w < warps; ++w) {
           const float2 p = parts[b & 1][w][j];
-          const float n = count(w), d = fmaf(p.x, __frcp_rn(n), -m);
+          const float n = count(w), d = p.x - m;
           q += fmaf(n * d, d, p.y);
         }
         mean[j] = m;
@@ -393,9 +392,10 @@ palimpsa_norm_bwd_kernel(NormArgs a, float* sums) {
           float2 x[P], dy[P];
           at.read(from, 0, j, v, x);
           at.read(from, 1, j, v, dy);
+          const float scale = at.has(v) ? st[j].y : 0.f;  // (columns past D: a mean may be past fp32's range of it)
 #pragma unroll
           for (int c = 0; c < P; ++c) {
-            const float2 t = __fmul2_rn(__fadd2_rn(x[c], two(-st[j].x)), two(st[j].y)), u = __fmul2_rn(dy[c], weight.f[v][c]);
+            const float2 t = __fmul2_rn(__fadd2_rn(x[c], two(-st[j].x)), two(scale)), u = __fmul2_rn(dy[c], weight.f[v][c]);
             gw[v][c] = __ffma2_rn(dy[c], t, gw[v][c]);
             gb[v][c] = __fadd2_rn(gb[v][c], dy[c]);
             s1 = __fadd2_rn(s1, u);
