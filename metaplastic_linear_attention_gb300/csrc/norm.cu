@@ -9,13 +9,14 @@
 // columns, backward up to 512 and in bf16 1024) or a CTA.
 // A grid of as many CTAs as the GPU holds walks the rows; the next ones come by asynchronous
 // copies into a ring in shared memory, each thread its own columns, so the copies need no barrier.
-// The squares are summed about the row's mean, which is known by then; where a row is a CTA's,
-// each warp sums them about the mean of its own part, and the parts are joined by
-//   sum (s - m)^2 = sum over warps of (sum (s - m_w)^2 + count (m_w - m)^2)
-// with one exchange, so nothing cancels, however far the row is off centre. The backward's teams
-// are wider than the forward's, since a thread keeps the parameters' sums of its columns in
-// registers over all its rows; CTAs leave theirs for a second kernel, which adds them in a fixed
-// order: no atomics, the same bits every time.
+// The squares are summed about the row's mean m, which is known by then to the roundings of a sum; so is what m
+// leaves out, e = mean(s - m), and the variance is mean((s - m)^2) - e^2 and the mean m + e. Where a row is a
+// CTA's, each warp does this about the mean m_w of its own part, and the parts are joined by
+//   n variance = sum over warps of n_w (variance_w + (m_w + e_w - mean)^2)
+// with one exchange, the means taken relative to the first warp's: nothing cancels, however far the row and its parts are
+// off centre. Up to 1024 columns in bf16 (512 in fp32) a row is a team's of a warp in the backward too, else a CTA's: a thread
+// keeps the parameters' sums of its columns in registers over all its rows. CTAs leave theirs for a second
+// kernel, which adds them in a fixed order: no atomics, the same bits every time.
 //
 // Measured (GB300): 71 us at 32768 x 1536 in bf16 with a residual (5.7 TB/s, 59 at the rate of a
 // copy), backward 61; rows of 16 to 2048 columns run at 0.7 to 0.9 of a copy's rate (the backward in bf16
@@ -178,7 +179,26 @@ __device__ __forceinline__ void spread(float mine, float (&v)[N]) {
     for (int k = 0; k < N; ++k) v[k] = __shfl_sync(~0u, mine, first + k * (LANES / N));
   }
 }
+// All sums of both in every lane; in one go where the team has lanes enough.
+template <int LANES, int N>
+__device__ __forceinline__ void all_sums(float (&a)[N], float (&b)[N]) {
+  if constexpr (2 * N <= LANES) {
+    float v[2 * N];
+#pragma unroll
+    for (int k = 0; k < N; ++k) v[k] = a[k], v[N + k] = b[k];
+    spread<LANES>(team_sums<LANES>(v), v);
+#pragma unroll
+    for (int k = 0; k < N; ++k) a[k] = v[k], b[k] = v[N + k];
+  } else {
+    spread<LANES>(team_sums<LANES>(a), a);
+    spread<LANES>(team_sums<LANES>(b), b);
+  }
+}
 __device__ __forceinline__ float2 two(float x) { return make_float2(x, x); }
+// The variance from the mean square about a rounded mean and what that mean leaves out.
+__device__ __forceinline__ float variance(float square, float rest) {
+  return square <= 3.4e38f ? fmaxf(fmaf(-rest, rest, square), 0.f) : square;
+}
 // 1 / sqrt(x): the SFU's, with one step of Newton's method (0 where x has overflowed). x y is the root, a
 // normal number where x, and half of it, are not.
 __device__ __forceinline__ float rsqrt_of(float x) {
@@ -194,8 +214,12 @@ __global__ void __launch_bounds__(MULTI ? 8192 / COLS : COLS > 16 ? 128 : 256, M
 palimpsa_norm_kernel(NormArgs a) {
   using W = Walk<BF16, LANES, MULTI, COLS, R, 1 + RES>;
   constexpr int V = W::V, P = W::P;
+  // Whether what a mean's sum leaves out of it is added up from the deviations and put right. (With 8 columns a
+  // thread the sum has 8 roundings at most, and that takes 131072 x 64 in fp32 from 7.9 us to 9.9.)
+  constexpr bool kCorrected = COLS > 8;
   extern __shared__ __align__(16) unsigned char smem[];
-  __shared__ float2 parts[2][16][R];  // of the warps: means, and squares about them
+  __shared__ float4 parts[2][16][R];  // of the warps: means, what they leave out, squares about them
+  __shared__ float2 shares[16];       // of the warps in a row's values, and one value's in theirs
   const W at(a.rows, a.D, smem);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, warps = blockDim.x / 32;
   const long long nx = at.apart(a.x_ld), nr = at.apart(a.residual_ld), ny = at.apart(a.D);
@@ -230,12 +254,13 @@ palimpsa_norm_kernel(NormArgs a) {
     return (float)(n * W::N);
   };
   const float whole = __frcp_rn((float)a.D), own = MULTI ? __frcp_rn(count(warp)) : whole;
+  if (MULTI && lane == 0) shares[warp] = make_float2(count(warp) * whole, own);  // (read behind the first batch's barrier)
 
   int from = 0;
   for (int b = 0; b < at.batches; ++b) {
     cp_async_wait<W::S - 2>();
     float2 s[R][V][P];
-    float mean[R], sq[R], rstd[R];
+    float mean[R], sq[R], rest[R], rstd[R];
     bool live[R];
 #pragma unroll
     for (int j = 0; j < R; ++j) {
@@ -259,41 +284,66 @@ palimpsa_norm_kernel(NormArgs a) {
     }
     from = from + 1 == W::S ? 0 : from + 1;
     stage();  // into the stage of the batch before
-    const float means = team_sums<LANES>(mean);
-    spread<LANES>(means, mean);
+    spread<LANES>(team_sums<LANES>(mean), mean);
 #pragma unroll
     for (int j = 0; j < R; ++j) {
-      float2 t = two(0.f);
+      float2 t = two(0.f), u = two(0.f);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         float2 q = two(0.f);
+        const float part = at.has(v) ? own : 0.f;
+        if (!kCorrected || v * at.team_size < at.nv) {
 #pragma unroll
-        for (int c = 0; c < P; ++c) {
-          const float2 d = __fadd2_rn(s[j][v][c], two(-mean[j]));
-          q = __ffma2_rn(d, d, q);
+          for (int c = 0; c < P; ++c) {
+            const float2 d = __fadd2_rn(s[j][v][c], two(-mean[j]));
+            q = __ffma2_rn(d, d, q);
+            if (kCorrected) u = __ffma2_rn(d, two(part), u);
+          }
+          if (at.has(v)) t = __fadd2_rn(t, q);
         }
-        if (at.has(v)) t = __fadd2_rn(t, q);
       }
       sq[j] = t.x + t.y;
+      rest[j] = u.x + u.y;
     }
-    const float squares = team_sums<LANES>(sq);
-    if (MULTI) {
-      if (lane % (32 / R) == 0) parts[b & 1][warp][lane / (32 / R)] = make_float2(means, squares);
+    if constexpr (MULTI) {
+      float both[2 * R];
+#pragma unroll
+      for (int j = 0; j < R; ++j) both[j] = rest[j], both[R + j] = sq[j];
+      const float mine = team_sums<LANES>(both);
+      constexpr int per = LANES / (2 * R);
+      float* const p = &parts[b & 1][warp][0].x;
+      if (lane % per == 0) p[lane / per % R * 4 + 1 + lane / per / R] = mine;
+#pragma unroll
+      for (int j = 0; j < R; ++j)
+        if (lane == j) p[j * 4] = mean[j];
       __syncthreads();  // (two sets of parts: the last batch's may still be read)
 #pragma unroll
       for (int j = 0; j < R; ++j) {
+        // Means relative to the first warp's, m the row's.
+        const float first = parts[b & 1][0][j].x;
         float m = 0.f, q = 0.f;
-        for (int w = 0; w < warps; ++w) m = fmaf(parts[b & 1][w][j].x, count(w) * whole, m);
         for (int w = 0; w < warps; ++w) {
-          const float2 p = parts[b & 1][w][j];
-          const float n = count(w), d = p.x - m;
-          q += fmaf(n * d, d, p.y);
+          const float4 p = parts[b & 1][w][j];
+          m = fmaf((p.x - first) + p.y, shares[w].x, m);
         }
-        mean[j] = m;
-        rstd[j] = rsqrt_of(fmaf(q, whole, a.eps));
+        for (int w = 0; w < warps; ++w) {
+          const float4 p = parts[b & 1][w][j];
+          const float2 share = shares[w];
+          const float d = ((p.x - first) + p.y) - m;
+          q = fmaf(fmaf(d, d, variance(p.z * share.y, p.y)), share.x, q);
+        }
+        mean[j] = first + m;
+        rstd[j] = rsqrt_of(q + a.eps);
+      }
+    } else if constexpr (kCorrected) {
+      all_sums<LANES>(sq, rest);
+#pragma unroll
+      for (int j = 0; j < R; ++j) {
+        rstd[j] = rsqrt_of(variance(sq[j] * own, rest[j]) + a.eps);
+        mean[j] += rest[j];
       }
     } else {
-      spread<LANES>(rsqrt_of(fmaf(squares, whole, a.eps)), rstd);
+      spread<LANES>(rsqrt_of(fmaf(team_sums<LANES>(sq), own, a.eps)), rstd);
     }
 #pragma unroll
     for (int j = 0; j < R; ++j)
@@ -545,7 +595,8 @@ cudaError_t backward(const NormArgs& a, float* sums, int* ctas, cudaStream_t s) 
 
 // (Few lanes with many columns each: a lane without columns does the same work, and sums over lanes take
 // steps. 136, 264 and 384 columns in bf16 with 8 or 16 lanes of 24: 40, 38 and 37 us for 96 MB; with a warp of
-// 8 or 16 each: 56, 57 and 44. 64 columns with 2 lanes of 32: 41, with 8 of 8: 37.)
+// 8 or 16 each: 56, 57 and 44. 64 columns with 2 lanes of 32: 41, with 8 of 8: 37. In bf16 without a residual
+// 520 and 640 columns with a warp of 24: 40 and 35, with 32 each 47 and 41; with one 71 and 70, 69 and 64.)
 // (Two rows at a time in a CTA halve its barriers: 4096 columns in bf16 without a residual 47 us -> 43 for
 // 96 MB; in fp32, whose rows are twice as long, 38.7 -> 39.9. Above 4096, one row with 64 columns a thread:
 // 8192 66 -> 52; with a residual 82 -> 83.)
@@ -560,6 +611,8 @@ cudaError_t forward_by_width(const NormArgs& a, cudaStream_t s) {
   if (a.D <= 256) return forward<BF16, 8, false, 32, 2, MORE>(a, s);
   if (a.D <= 384) return forward<BF16, 16, false, 24, 2, MORE>(a, s);
   if (a.D <= 512) return forward<BF16, 16, false, 32, 2, MORE>(a, s);
+  if constexpr (BF16 && !MORE)
+    if (a.D <= 768) return forward<true, 32, false, 24, 1, false>(a, s);
   if (a.D <= 1024) return forward<BF16, 32, false, 32, 1, MORE>(a, s);
   if (a.D <= 1536) return forward<BF16, 32, false, 48, 1, MORE>(a, s);
   if (a.D <= 2048) return forward<BF16, 32, false, 64, 1, MORE>(a, s);
