@@ -534,22 +534,16 @@ palimpsa_norm_bwd_kernel(NormArgs a, float* sums) {
 struct Shape {
   int threads, bytes, ctas;
 };
-// What an SM holds of a kernel, by its threads (a multiple of 32, up to 512); it is asked for once.
 struct Held {
-  std::atomic<int> ctas[17] = {};
+  HeldCtas ctas;
   SharedBytes allowed;
 };
 template <class K>
 cudaError_t shape_of(K kernel, const NormArgs& a, int threads, int teams, int bytes, Held* known, Shape* p) {
   cudaError_t e = allow_shared(kernel, bytes, &known->allowed);
   if (e != cudaSuccess) return e;
-  std::atomic<int>& ctas = known->ctas[threads / 32];
-  int held = ctas.load(std::memory_order_relaxed);
-  if (held == 0) {
-    if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&held, kernel, threads, bytes)) != cudaSuccess) return e;
-    if (held < 1) return cudaErrorInvalidConfiguration;
-    ctas.store(held, std::memory_order_relaxed);
-  }
+  int held;
+  if ((e = held_ctas(kernel, threads, bytes, &known->ctas, &held)) != cudaSuccess) return e;
   const long long most = (long long)held * sms_of_device();
   *p = {threads, bytes, (int)std::max<long long>(1, std::min(most, (a.rows + teams - 1) / teams))};
   return cudaSuccess;

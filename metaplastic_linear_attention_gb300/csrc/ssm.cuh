@@ -209,6 +209,25 @@ cudaError_t allow_shared(K kernel, int bytes, SharedBytes* allowed, bool wide = 
   if (e == cudaSuccess) on.store(bytes);
   return e;
 }
+// What an SM of the current device holds of a kernel's CTAs, by their threads (a multiple of 32, up to 512; `bytes`
+// of dynamic shared memory follow from them); asked for once a device. `known` is the kernel's own.
+struct HeldCtas {
+  std::atomic<int> ctas[64][17] = {};
+};
+template <class K>
+cudaError_t held_ctas(K kernel, int threads, int bytes, HeldCtas* known, int* held) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  std::atomic<int>& ctas = known->ctas[dev][threads / 32];
+  *held = ctas.load(std::memory_order_relaxed);
+  if (*held > 0) return cudaSuccess;
+  if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(held, kernel, threads, bytes)) != cudaSuccess) return e;
+  if (*held < 1) return cudaErrorInvalidConfiguration;
+  ctas.store(*held, std::memory_order_relaxed);
+  return cudaSuccess;
+}
 
 // The gated scan: one state per channel, gates from the token (formulas in gate_fwd.cu).
 struct GateArgs {
