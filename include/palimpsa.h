@@ -586,7 +586,7 @@ palimpsa_status palimpsa_backward_varlen(
  *             scan's A, their gradients, dA and cu_seqlens (4 bytes), and stats (8).
  * T = 0, and empty sequences, pass the state (and its gradient) through; with
  * T = 0 the token arrays may be NULL. Overlap between inputs and outputs is
- * undefined, except that a final state may be the initial one. Results do not
+ * undefined, except that a final state may be the initial one, and where it is allowed below. Results do not
  * depend on timing: no atomics, the same bits every time.
  */
 
@@ -744,7 +744,8 @@ typedef struct {
  *   y_t = h_t silu(z_t)
  *
  * A > 0, as above: the largest rate of forgetting. The factor of the input keeps the
- * state's variance at the input's, whatever the decay.
+ * state's variance at the input's, whatever the decay. States are rounded to fp32 where they are
+ * handed on, token by token or tile by tile; what the rounding of a decay leaves out is kept.
  *   x, r     rows [D]; i rows [D] or NULL (no input gate: a factor of 1); z rows [D] or
  *            NULL (no output gate)
  *   A        [D] > 0; r_bias, i_bias [D] or NULL (0); i_bias only with i
@@ -804,7 +805,8 @@ palimpsa_status palimpsa_gated_scan_backward(
  *                of every row, for the backward
  *   rows >= 0 (with 0 the row arrays may be NULL); D a multiple of 8, at most 8192; eps > 0.
  * A row with infinities or NaN gives NaN, in that row alone. A row whose squared deviations
- * pass fp32's range (deviations above 1e19) is taken to have an infinite deviation: y = bias.
+ * pass fp32's range (deviations above 1e19) is taken to have an infinite deviation: y = bias,
+ * as long as no two of its values differ by more than fp32 can hold.
  */
 palimpsa_status palimpsa_layer_norm(
     const void* x, long long x_stride, const void* residual, long long residual_stride,
@@ -814,7 +816,8 @@ palimpsa_status palimpsa_layer_norm(
 /*
  * palimpsa_layer_norm_backward - gradients through palimpsa_layer_norm from dy and, where s
  * is used past the norm, ds (rows [D] or NULL), with s and the stats of the forward call:
- *   dx             rows [D], the gradient of s, and so of x and of residual (ds included)
+ *   dx             rows [D], the gradient of s, and so of x and of residual (ds included); may be
+ *                  dy or ds where that is dense
  *   dweight, dbias [D] fp32, or NULL
  * Scratch for the parameters' partial sums comes from the library's pool.
  */

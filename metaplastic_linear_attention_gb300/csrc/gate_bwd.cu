@@ -13,11 +13,11 @@
 // gradient behind the piece known, a second run gives the results. (Kept products and sums instead
 // of the second run, as in the forward: 1 % slower.) The rounds go from the back to the front, and
 // in a cluster the gradient goes round the other way.
-// The parameters' sums stay in registers over all rounds; they are added up over the CTA's
-// pieces in shared memory and over CTAs by a second kernel, in a fixed order: no atomics, the
-// same bits every time.
-// Measured (GB300, bf16, both gates): 198 us at 8 x 4096 x 1536 (138 for its bytes at the rate of a
-// copy), 40 at 4 x 2048 x 1024 (23); fp32 at 0.87 to 0.93 of that rate. What a token keeps
+// The parameters' sums wait in shared memory from round to round, each thread's in its own place; they
+// are added up over the CTA's pieces and over CTAs by a second kernel, in a fixed order: no atomics, the
+// same bits every time. (In registers they spilled: 8 x 4096 x 2048 267 us, now 249.)
+// Measured (GB300, bf16, both gates): 191 us at 8 x 4096 x 1536 (138 for its bytes at the rate of a
+// copy), 41 at 4 x 2048 x 1024 with the sums (23); fp32 292 at 8 x 4096 x 1536, 0.95 of that rate. What a token keeps
 // (the decay, four factors, its part of g_t) takes 96 of the 128 registers that 16 warps an SM allow.
 #include <algorithm>
 

@@ -5,24 +5,25 @@
 // The input's factor keeps the state's variance at the input's, whatever the decay.
 //
 // What bounds it: HBM. A channel-token moves 8 bytes in bf16 (10 with z), 0.37 clocks
-// (0.47) of an SM's share of the measured 6.77 TB/s, against 3 2^x, 2 reciprocals and a
-// root on the SFU (0.28 clocks; a 2^x and a reciprocal more with z) and about 30 FP32
+// (0.47) of an SM's share of the measured 6.77 TB/s, against 3 2^x, a reciprocal and a
+// reciprocal root on the SFU (0.22 clocks; a 2^x and a reciprocal more with z) and about 30 FP32
 // operations. So every input is read once: a thread takes 8 tokens of 4 channels (a piece),
 // forms their decays and inputs a, b in registers and runs them from 0, keeping for each token
 // the product P of the a's and the state H so far; with the state h before the piece known, the
-// states are P h + H. The last P and H are the piece's summary. (4 tokens and twice the threads
+// states are P h + H. The last P and H and the sum of the rates are the piece's summary. (4 tokens and twice the threads
 // took 1.3 times as long: what a round costs a thread besides its tokens is a fifth of it.) The
 // summaries of a CTA's pieces (groups of 16 or 8 threads, along time) pass through shared
-// memory, and every thread folds the ones before its own. A CTA walks its sequence in rounds of
+// memory, every thread folds the ones before its own, and the last group works out the state
+// behind the tile, which goes to the next round by shared memory too. A CTA walks its sequence in rounds of
 // such tiles, the next round's inputs coming by asynchronous copies meanwhile. Where the CTAs are
 // too few, those of a cluster take turns along time: each gets the state before its tile from
 // the one before it and hands on the state after it, as an asynchronous store into the next
 // one's shared memory that a barrier there counts. (A ring: with all summaries sent to all, the
-// CTAs of a cluster went in step, and 8 x 4096 x 1536 took 83 us, now 78.)
+// CTAs of a cluster went in step, and 8 x 4096 x 1536 took 83 us, where the ring took 78.)
 // Measured (GB300, bf16): 78 us at 8 x 4096 x 1536 without z (5.2 TB/s, 59 at the rate of a
-// copy), 164 at 1 x 32768 x 2048 with z (4.1 TB/s, 99), 225 at 256 x 256 x 2048 (6.0 TB/s), where
-// CTAs are many; in fp32 at a copy's rate. The warp schedulers issue in 50 to 60 % of their cycles, with the 16 warps an SM that 128 registers and two
-// stages of inputs allow.
+// copy), 166 at 1 x 32768 x 2048 with z (4.0 TB/s, 99), 230 at 256 x 256 x 2048 (5.8 TB/s), where
+// CTAs are many; in fp32 157 at 8 x 4096 x 1536 with z, 0.95 of a copy's rate. The warp schedulers issue in 50 to
+// 60 % of their cycles, with the 16 warps an SM that 128 registers and two stages of inputs allow.
 //
 // Rounding: gates, decays and states are fp32; y is rounded to the input type once.
 #include <algorithm>
@@ -42,8 +43,7 @@ constexpr int kResident = 4;  // CTAs of an SM
 template <bool BF16, int CH>
 using Tile = GateTile<BF16, CH, 4, BF16 ? 128 : 64>;
 
-// Shared memory: two stages of x, r and i, then two states of the tile's channels that the CTA
-// before hands over. A piece's summary takes the place of its first rows of x. Where rows are 64
+// Shared memory: two stages of x, r and i, then two states of the tile's channels before it. A piece's summary takes the place of its first rows of x. Where rows are 64
 // bytes, those of odd pieces change places in pairs, so that the two that a half warp reads at
 // once lie in different banks.
 template <bool BF16, bool IN>
@@ -498,9 +498,11 @@ cudaError_t step(const GateArgs& a, cudaStream_t s) {
 // batch's CTAs have the mean of the rounds (and half of one lost) and fill the slots as they come free;
 // what the longest sequence has beyond the mean comes behind that, by 0.9 of it (6 ragged batches:
 // within 3 % of the best on average, and within 11).
-// Measured, 8 x 4096 x 1536 with clusters of 1, 2, 3, 4 and 8: 111, 90, 78 (taken: 576 CTAs where 584
-// fit), 90 and 87 us; 8 x 4096 x 2048 166, 139, 147, 127 (taken) and 134; 1 x 32768 x 512 in tiles of
-// 32 channels with 6, 8, 12 and 16: 110, 103, 81 (taken) and 80, backward 240, 171, 136 and 149.
+// Measured for the fit, 8 x 4096 x 1536 with clusters of 1, 2, 3, 4 and 8: 111, 90, 78 (taken: 576 CTAs
+// where 584 fit), 90 and 87 us; 8 x 4096 x 2048 166, 139, 147, 127 (taken) and 134; 1 x 32768 x 512 in tiles of
+// 32 channels with 6, 8, 12 and 16: 110, 103, 81 (taken) and 80, backward 240, 171, 136 and 149. For one
+// sequence of 32768 tokens and 1024 or 2048 channels the forward was faster with 16 than with the 12 or 8 that are taken, 94
+// us against 99 (fp32 115 against 128) and 154 against 165, the backward slower: 260 against 189, 406 against 297.
 GatePlan gate_plan(const SeqRows& r, int D, int tokens, int resident, int narrow, const GateCost& c) {
   const int sms = sms_of_device();
   GatePlan best = {64, 1, 0};
@@ -525,7 +527,7 @@ GatePlan gate_plan(const SeqRows& r, int D, int tokens, int resident, int narrow
   return best;
 }
 
-// A token takes a thread 0.35 to 0.45 us at least, and the GPU's threads together come to `rate`. Measured
+// A token takes a thread 0.35 to 0.45 us at least, and the GPU's threads together come to `rate`. Measured for the fit
 // in bf16 with both gates, threads against tiles: 256 x 4 x 2048 8.5 us and 41, 256 x 16 20.7 and 45,
 // 256 x 64 76 and 72 (threads are taken), 256 x 256 274 and 226; backward, warps against tiles, 19 and
 // 84, 45 and 107, 150 and 154, 575 and 497. In fp32 512 x 32 x 2048 105 and 124, 256 x 256 389 and 391;

@@ -14,13 +14,13 @@
 // CTA's, each warp does this about the mean m_w of its own part, and the parts are joined by
 //   n variance = sum over warps of n_w (variance_w + (m_w + e_w - mean)^2)
 // with one exchange, the means taken relative to the first warp's: nothing cancels, however far the row and its parts are
-// off centre. Up to 1024 columns in bf16 (512 in fp32) a row is a team's of a warp in the backward too, else a CTA's: a thread
+// off centre. Above 1024 columns in bf16 (512 in fp32) the backward's rows are a CTA's: a thread
 // keeps the parameters' sums of its columns in registers over all its rows. CTAs leave theirs for a second
 // kernel, which adds them in a fixed order: no atomics, the same bits every time.
 //
-// Measured (GB300): 71 us at 32768 x 1536 in bf16 with a residual (5.7 TB/s, 59 at the rate of a
+// Measured (GB300): 70 us at 32768 x 1536 in bf16 with a residual (5.8 TB/s, 59 at the rate of a
 // copy), backward 61; rows of 16 to 2048 columns run at 0.7 to 0.9 of a copy's rate (the backward in bf16
-// at 0.55 to 0.85), wider ones at 0.65 to 0.9 in fp32 and 0.5 to 0.9 in bf16.
+// at 0.55 to 0.85), wider ones at 0.7 to 0.9 in fp32 and 0.65 to 0.9 in bf16.
 //
 // Rounding: sums and statistics are fp32; outputs are rounded to the input type once.
 #include <algorithm>
@@ -593,7 +593,7 @@ cudaError_t backward(const NormArgs& a, float* sums, int* ctas, cudaStream_t s) 
 // 520 and 640 columns with a warp of 24: 40 and 35, with 32 each 47 and 41; with one 71 and 70, 69 and 64.)
 // (Two rows at a time in a CTA halve its barriers: 4096 columns in bf16 without a residual 47 us -> 43 for
 // 96 MB; in fp32, whose rows are twice as long, 38.7 -> 39.9. Above 4096, one row with 64 columns a thread:
-// 8192 66 -> 52; with a residual 82 -> 83.)
+// 8192 66 -> 52; with a residual 82 -> 83. Since then 4096 columns have come to 38 and 8192 to 44.)
 template <bool BF16, bool MORE>
 cudaError_t forward_by_width(const NormArgs& a, cudaStream_t s) {
   if (a.D <= (BF16 ? 16 : 8)) return forward<BF16, 2, false, 8, 2, MORE>(a, s);

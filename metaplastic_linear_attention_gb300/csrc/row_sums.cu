@@ -3,7 +3,7 @@
 //
 // A thread takes 4 columns of one row in 64 (8 slices of a CTA, up to 8 CTAs of a cluster, which
 // adds up through shared memory), always the same, so the bits are the same every time. It is a few
-// MB at most: 760 rows of 2 x 1536 took 9 us with 96 CTAs of 32 columns, now 4.
+// MB at most: 760 rows of 2 x 1536 add 6 us to the layer norm's backward.
 #include <algorithm>
 #include <cooperative_groups.h>
 
