@@ -129,6 +129,11 @@ __device__ __forceinline__ void decay_of(float2 w, float2* a, float2* rest) {
   float2 left;
   decay_of(w, a, rest, &left);
 }
+// left h + b; b where h is infinite, so that an infinite state stays what a makes of it.
+__device__ __forceinline__ float2 with_left(float2 left, float2 h, float2 b) {
+  const float2 t = __ffma2_rn(left, h, b);
+  return make_float2(fabsf(h.x) <= 3.4028235e38f ? t.x : b.x, fabsf(h.y) <= 3.4028235e38f ? t.y : b.y);
+}
 // sqrt(rest) x, from rest = 1 - a^2, and with the input gate p. In this order no product leaves fp32's
 // range where the result does not.
 __device__ __forceinline__ float2 input_of(float2 rest, float2 x) {
@@ -181,7 +186,8 @@ __device__ __forceinline__ bool cluster_wait(uint64_t* bar, uint32_t parity, uns
       if (cluster_try_wait(bar, parity)) return true;
     if (global_ns() - t0 >= timeout_ns) return cluster_try_wait(bar, parity);
   }
-}// Tests: until the others' waits have run out.
+}
+// Tests: until the others' waits have run out.
 __device__ __forceinline__ void pass_the_limit(const GateArgs& a) {
   const unsigned long long t0 = global_ns(), late = 4 * min(a.wait_timeout_ns, 250000000ull) + 20000000ull;
   while (global_ns() - t0 < late) __nanosleep(1000);

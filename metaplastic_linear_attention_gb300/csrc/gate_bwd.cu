@@ -307,7 +307,7 @@ palimpsa_gate_bwd_kernel(GateArgs a, int tiles, float* sums) {
     }
     float2 c = given[(turn & 1) * 32];
     if (warp == 0) {
-      Cc = ffma2(Pc, c, ffma2(Lc, c, Cc));
+      Cc = ffma2(Pc, c, with_left(Lc, c, Cc));
       const int next = rank == 0 ? turn + 1 : turn;  // the turn of the CTA before
       if (next >= rounds) {
         if (in && a.dh0) *reinterpret_cast<float2*>(a.dh0 + n * a.D + ch) = Cc;
@@ -412,7 +412,7 @@ __global__ void __launch_bounds__(32 * kShortWarps, kShortCtas) palimpsa_gate_sh
 #pragma unroll
       for (int t = 1; t < kPiece; ++t) Q = __fmul2_rn(Q, p.da[t]);
       left = __fadd2_rn(left, __fadd2_rn(P, make_float2(-Q.x, -Q.y)));
-      c = ffma2(left, c, res.finish(a, p, np, at + (np - 1) * yd, yd, c));
+      c = with_left(left, c, res.finish(a, p, np, at + (np - 1) * yd, yd, c));
     }
     if (a.dh0) *reinterpret_cast<float2*>(a.dh0 + n * a.D + ch) = c;
   }

@@ -43,9 +43,10 @@ constexpr int kResident = 4;  // CTAs of an SM
 template <bool BF16, int CH>
 using Tile = GateTile<BF16, CH, 4, BF16 ? 128 : 64>;
 
-// Shared memory: two stages of x, r and i, then two states of the tile's channels before it. A piece's summary takes the place of its first rows of x. Where rows are 64
-// bytes, those of odd pieces change places in pairs, so that the two that a half warp reads at
-// once lie in different banks.
+// Shared memory: two stages of x, r and i, then two states of the tile's channels before it. A
+// piece's summary takes the place of its first rows of x. Where rows are 64 bytes, those of odd
+// pieces change places in pairs, so that the two that a half warp reads at once lie in different
+// banks.
 template <bool BF16, bool IN>
 constexpr int kStageBytes = (2 + IN) * Tile<BF16, 64>::bytes;  // the same for 32
 
@@ -63,7 +64,7 @@ struct Four {
   // v + P h + L h
   __device__ __forceinline__ void fold_after(const Four& P, const Four& L, const Four& h) {
 #pragma unroll
-    for (int j = 0; j < 2; ++j) v[j] = ffma2(P.v[j], h.v[j], ffma2(L.v[j], h.v[j], v[j]));
+    for (int j = 0; j < 2; ++j) v[j] = ffma2(P.v[j], h.v[j], with_left(L.v[j], h.v[j], v[j]));
   }
   __device__ __forceinline__ float4 all() const { return make_float4(v[0].x, v[0].y, v[1].x, v[1].y); }
 };
@@ -383,7 +384,7 @@ __global__ void __launch_bounds__(128, BF16 ? 5 : 4) palimpsa_gate_short_kernel(
           float2 da, sq, left;
           decay_of(__fmul2_rn(A[j], sigmoid_of(ffma2(fr[j], scale, rb[j]))), &da, &sq, &left);
           const float2 b = IN ? input_of(sq, sigmoid_of(ffma2(fi[j], scale, ib[j])), fx[j]) : input_of(sq, fx[j]);
-          h.v[j] = ffma2(da, h.v[j], ffma2(left, h.v[j], b));
+          h.v[j] = ffma2(da, h.v[j], with_left(left, h.v[j], b));
           y[j] = GATE ? __fmul2_rn(h.v[j], silu_fast(fz[j])) : h.v[j];
         }
         *reinterpret_cast<Raw*>(py + (long long)t * a.D * ES) = Q::pack(y);
@@ -430,7 +431,7 @@ __global__ void __launch_bounds__(128) palimpsa_gate_step_kernel(GateArgs a) {
     const float2 b =
         IN ? input_of(sq, sigmoid_of(__fmul2_rn(__fadd2_rn(i[j], pair_or(a.i_bias, ch + 2 * j, true, 0.f)), scale)), x[j])
            : input_of(sq, x[j]);
-    h[j] = ffma2(da, h[j], ffma2(left, h[j], b));
+    h[j] = ffma2(da, h[j], with_left(left, h[j], b));
     y[j] = GATE ? __fmul2_rn(h[j], silu_fast(z[j])) : h[j];
   }
   *state = make_float4(h[0].x, h[0].y, h[1].x, h[1].y);
