@@ -38,3 +38,19 @@ def test_rows_whose_sum_passes_the_range(dtype, D, size):
     assert not got["dx"][2:5].any() and torch.isfinite(got["dx"]).all()
     assert torch.equal(got["dx"][0], wg["dx"][0]) and torch.equal(got["dx"][5], wg["dx"][5])
     assert torch.isfinite(got["dweight"]).all() and torch.isfinite(got["dbias"]).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("D", [16, 1536, 2056, 4096, 8192])
+@pytest.mark.parametrize("col", [0, -1])
+def test_infinities_and_nan_spoil_their_own_row_alone(dtype, D, col):
+    g = torch.Generator(device=DEV).manual_seed(D)
+    x = torch.randn(40, D, generator=g, device=DEV).to(dtype)
+    w, b = torch.rand(D, generator=g, device=DEV) + 0.5, torch.randn(D, generator=g, device=DEV)
+    want, _, _ = pal.palimpsa_layer_norm(x, w, b)
+    x[3, col], x[17, col], x[30, col] = float("inf"), float("-inf"), float("nan")
+    y, _, st = pal.palimpsa_layer_norm(x, w, b, want_stats=True)
+    for k in (3, 17, 30):
+        assert torch.isnan(y[k]).all() and torch.isnan(st[k, 1])
+        y[k] = want[k]
+    assert torch.equal(y, want)
